@@ -59,8 +59,8 @@ typedef enum {
 /* Device error bits reported by moe_get_device_status(). */
 #define MOE_DEVERR_EXPERT_RANGE 0x1u /* an expert id outside [0, E) was skipped */
 #define MOE_DEVERR_TIMEOUT 0x2u      /* a bounded wait inside a kernel gave up */
-#define MOE_DEVERR_SEGMENT 0x4u      /* backward: a segment offset outside the padded rows
-                                      * was skipped */
+#define MOE_DEVERR_SEGMENT 0x4u      /* a segment or group offset outside the rows was
+                                      * skipped */
 
 typedef struct {
     int32_t T;            /* tokens */
@@ -750,6 +750,108 @@ moe_status_t moe_layer_bwd(const moe_config_t *cfg, const moe_weights_t *w,
                            const void *fwd_ws, size_t fwd_ws_bytes, const void *gu_saved,
                            size_t gu_saved_bytes, const moe_grads_t *grads, void *bws,
                            size_t bws_bytes, void *stream);
+
+/* ----------------------------------------- products on ragged row groups -- */
+
+/* Plain matrix products grouped by expert, for expert bodies other than the
+ * layer's SwiGLU pair, for adapters, and for training them: token rows sorted
+ * by group, group e owning rows [offsets[e], offsets[e + 1]) (int32 [E + 1],
+ * device; e.g. the group_offsets of moe_build_offsets_unpadded or the
+ * padded_offsets of moe_build_offsets).  Groups may have any size, none, any
+ * start and gaps between them; rows outside every group are left untouched in
+ * the output.  A group that does not lie in [0, R] or runs backwards counts as
+ * empty and sets MOE_DEVERR_SEGMENT in *status.
+ *
+ * Shared rules: dtype is MOE_DTYPE_BF16 or MOE_DTYPE_F16 (operands and output
+ * alike); R >= 0 rows (at most 2^30), 1 <= E <= 256; matrix dimensions are
+ * multiples of 8; matrices are row-major and 16-byte aligned with row strides
+ * (in elements) that are multiples of 8.  Sums are kept in fp32 and rounded
+ * once.  status: uint32 [1] device error word, or NULL. */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_F16 1
+
+/* y[r] = row_scale[r] * x[r] W[e]^T for every row r of every group e; with
+ * w_transposed, y[r] = row_scale[r] * x[r] W[e].  The second form on the
+ * first's weights is its data gradient (dx = dy W).  R = 0 enqueues nothing.
+ *   x          [R, K], row stride ldx >= K       device, read
+ *   w          [E, N, K], or [E, K, N] (w_transposed)  device, read
+ *   row_scale  fp32 [R] or NULL (1)              device, read
+ *   y          [R, N], row stride ldy >= N       device, written */
+moe_status_t moe_grouped_gemm(int32_t dtype, int64_t R, int32_t N, int32_t K, int32_t E,
+                              const void *x, int64_t ldx, const void *w, int32_t w_transposed,
+                              const int32_t *offsets, const float *row_scale, void *y, int64_t ldy,
+                              uint32_t *status, void *stream);
+
+/* out[e] = sum over the rows r of group e of a[r]^T b[r]: the weight gradient
+ * of moe_grouped_gemm (a = dy, b = x gives [E, N, K]; exchanged, [E, K, N]).
+ * Every element of out is written; an empty group's are zero.
+ *   a    [R, M], row stride lda >= M   device, read
+ *   b    [R, N], row stride ldb >= N   device, read
+ *   out  [E, M, N]                     device, written */
+moe_status_t moe_grouped_wgrad(int32_t dtype, int64_t R, int32_t M, int32_t N, int32_t E,
+                               const void *a, int64_t lda, const void *b, int64_t ldb,
+                               const int32_t *offsets, void *out, uint32_t *status, void *stream);
+
+/* ------------------------------------------------- 4-bit block-scaled rows -- */
+
+/* Rows of 4-bit codes with block scales: e2m1 values (0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6 and their negatives), two to a byte, the even element in the low
+ * nibble, and one scale byte for each block of consecutive elements of a row:
+ *   MOE_FP4_MX  blocks of 32, scale 2^(byte - 127) (OCP MX: e2m1 with e8m0;
+ *               byte 255 is NaN)
+ *   MOE_FP4_NV  blocks of 16, scale an e4m3 value (byte 127 is NaN) times one
+ *               fp32 scale for the whole tensor
+ * codes uint8 [rows, K / 2]; scales uint8 [rows, moe_fp4_scale_stride(fmt, K)]:
+ * a row's K / 32 or K / 16 bytes, padded to a multiple of 16.  K is a multiple
+ * of 32; codes and scales are 16-byte aligned. */
+#define MOE_FP4_MX 0
+#define MOE_FP4_NV 1
+
+/* Bytes of one row of scales; 0 if fmt or K is invalid. */
+size_t moe_fp4_scale_stride(int32_t fmt, int32_t K);
+
+/* Quantises rows: output row r holds x[src[r] / src_div] (src int32 [rows];
+ * negative entries and those past x's rows give a row of zeros), or x[r] when
+ * src is NULL.  With the row_src and k of moe_build_offsets(_unpadded) that is
+ * the permute into expert order.  With swiglu, x has 2 K columns, gate and up
+ * interleaved per 128 (the column order of the packed W13; K a multiple of
+ * 128), and the element quantised is silu(gate) * up rounded to x's type.
+ *   MX: scale = the smallest power of two with max|block| <= 6 * scale (1 for
+ *       a block of zeros);
+ *   NV: scale = e4m3(min(448, max|block| / (6 g))) * g with g = *tensor_scale
+ *       (1 if NULL; MX ignores it), nearest, ties to even;
+ * code = the e2m1 value nearest to x / scale, ties to even, saturating at 6
+ * (0 where the scale is 0).  A NaN or infinity makes its block's scale NaN.
+ * The padding of a scale row is written as zeros.
+ *   x       dtype [x_rows, K or 2 K], row stride ldx   device, read
+ *   codes   uint8 [rows, K / 2], scales uint8 [rows, stride]  device, written */
+moe_status_t moe_quantize_fp4(int32_t fmt, int32_t dtype, int64_t rows, int32_t K, const void *x,
+                              int64_t x_rows, int64_t ldx, const int32_t *src, int32_t src_div,
+                              int32_t swiglu, const float *tensor_scale, void *codes, void *scales,
+                              void *stream);
+
+/* out[r] = the values of row r (dtype, row stride ldo): e2m1 * scale, times
+ * *tensor_scale for NV, in fp32, rounded once. */
+moe_status_t moe_dequantize_fp4(int32_t fmt, int32_t dtype, int64_t rows, int32_t K,
+                                const void *codes, const void *scales, const float *tensor_scale,
+                                void *out, int64_t ldo, void *stream);
+
+/* The grouped product on 4-bit rows and weights, both in format fmt:
+ *   y[r] = row_scale[r] * x_scale * w_scale[e] * x[r] W[e]^T
+ * on the groups of moe_grouped_gemm (same rules; K a multiple of 32, N of 8).
+ * The products of codes and block scales are exact, the sum is kept in fp32.
+ *   x_codes, x_scales  rows [R, K]         device, read
+ *   w_codes, w_scales  rows [E * N, K]     device, read
+ *   x_scale  fp32 [1] or NULL (1), w_scale  fp32 [E] or NULL (1): the tensor
+ *            scales of the operands, e.g. of MOE_FP4_NV  device, read
+ *   row_scale  fp32 [R] or NULL (1)        device, read
+ *   y  bf16 [R, N], row stride ldy >= N    device, written */
+moe_status_t moe_grouped_gemm_fp4(int32_t fmt, int64_t R, int32_t N, int32_t K, int32_t E,
+                                  const void *x_codes, const void *x_scales, const void *w_codes,
+                                  const void *w_scales, const int32_t *offsets,
+                                  const float *x_scale, const float *w_scale,
+                                  const float *row_scale, void *y, int64_t ldy, uint32_t *status,
+                                  void *stream);
 
 /* ---------------------------------------------------------- diagnostics -- */
 

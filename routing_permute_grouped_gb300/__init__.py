@@ -39,11 +39,17 @@ __all__ = [
     "moe_widen_e4m3", "moe_grouped_gemm_swiglu_scaled", "moe_shared_expert_scaled",
     "moe_gather_rows", "moe_build_blocks_from_counts", "moe_copy_pieces",
     "moe_build_offsets_unpadded", "moe_grouped_gemm_swiglu_unpadded",
+    "moe_grouped_gemm", "moe_grouped_wgrad", "FP4_MX", "FP4_NV", "FP4_FORMATS",
+    "moe_fp4_scale_stride", "moe_quantize_fp4", "moe_dequantize_fp4", "moe_grouped_gemm_fp4",
 ]
 
 MOE_OK = 0
 DEVERR_EXPERT_RANGE = 0x1
 DEVERR_TIMEOUT = 0x2
+DEVERR_SEGMENT = 0x4
+FP4_MX, FP4_NV = 0, 1
+FP4_FORMATS = {"mx": FP4_MX, "nv": FP4_NV}
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 
 class MoeError(RuntimeError):
@@ -105,7 +111,7 @@ def load():
         raise ImportError(f"CUDA library not built: {path} is missing "
                           "(run routing_permute_grouped_gb300.build.build())")
     lib = ctypes.CDLL(path)
-    P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     CP = ctypes.POINTER(MoeConfig)
     sigs = {
         "moe_check_config": (ctypes.c_int, [CP]),
@@ -159,6 +165,14 @@ def load():
         "moe_layer_bwd": (ctypes.c_int, [CP, ctypes.POINTER(MoeWeights),
                                          ctypes.POINTER(MoeWeightsBwd), P, P, P, SZ, P, SZ,
                                          ctypes.POINTER(MoeGrads), P, SZ, P]),
+        "moe_grouped_gemm": (ctypes.c_int, [I32, I64, I32, I32, I32, P, I64, P, I32, P, P, P, I64, P,
+                                            P]),
+        "moe_grouped_wgrad": (ctypes.c_int, [I32, I64, I32, I32, I32, P, I64, P, I64, P, P, P, P]),
+        "moe_fp4_scale_stride": (SZ, [I32, I32]),
+        "moe_quantize_fp4": (ctypes.c_int, [I32, I32, I64, I32, P, I64, I64, P, I32, I32, P, P, P,
+                                            P]),
+        "moe_dequantize_fp4": (ctypes.c_int, [I32, I32, I64, I32, P, P, P, P, I64, P]),
+        "moe_grouped_gemm_fp4": (ctypes.c_int, [I32, I64, I32, I32, I32] + [P] * 9 + [I64, P, P]),
         "moe_get_device_status": (ctypes.c_int, [P, ctypes.POINTER(ctypes.c_uint32), P]),
         "moe_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_uint64, P, P]),
         "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -187,6 +201,29 @@ def _ptr(t: Optional[torch.Tensor]):
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _rows(t: torch.Tensor):
+    """Pointer and row stride of a [rows, columns] CUDA tensor whose rows are
+    contiguous (the stride between rows is free)."""
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("expected a 2D tensor with contiguous rows")
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _dtype(*tensors) -> int:
+    """The library's code of the tensors' common 16-bit type."""
+    if any(t.dtype != tensors[0].dtype for t in tensors) or tensors[0].dtype not in _DTYPES:
+        raise ValueError("expected bf16 or fp16 tensors of one type")
+    return _DTYPES[tensors[0].dtype]
+
+
+def _expect(t: Optional[torch.Tensor], name: str, dtype, shape) -> None:
+    """The C side sees only a pointer: what it reads there is checked here."""
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
 def _stream(stream) -> ctypes.c_void_p:
@@ -518,6 +555,92 @@ def moe_layer_bwd(cfg, weights: MoeWeights, wbwd: MoeWeightsBwd, x, dout, ws, gr
                                 _ptr(x), _ptr(dout), _ptr(ws), ws.numel() * ws.element_size(),
                                 _ptr(gu_saved), gu_bytes, ctypes.byref(g), _ptr(bws),
                                 bws.numel() * bws.element_size(), _stream(stream)))
+
+
+# ------------------------------------------- products on ragged groups ----
+def moe_grouped_gemm(x, w, offsets, y, row_scale=None, w_transposed: bool = False, status=None,
+                     stream=None) -> None:
+    """y[r] = row_scale[r] * x[r] W[e]^T for the rows offsets[e] <= r < offsets[e + 1]
+    of every group; x [R, K], w [E, N, K] (or [E, K, N], ``w_transposed``: x[r] W[e]),
+    y [R, N], all bf16 or all fp16, rows of x and y at any stride."""
+    (R, K), (E, a, b) = x.shape, w.shape
+    N = b if w_transposed else a
+    _expect(w, "w", x.dtype, (E, K, N) if w_transposed else (E, N, K))
+    _expect(y, "y", x.dtype, (R, N))
+    _expect(offsets, "offsets", torch.int32, (E + 1,))
+    _expect(row_scale, "row_scale", torch.float32, (R,))
+    (px, ldx), (py, ldy) = _rows(x), _rows(y)
+    _check(load().moe_grouped_gemm(_dtype(x), R, N, K, E, px, ldx, _ptr(w), int(w_transposed),
+                                   _ptr(offsets), _ptr(row_scale), py, ldy, _ptr(status),
+                                   _stream(stream)))
+
+
+def moe_grouped_wgrad(a, b, offsets, out, status=None, stream=None) -> None:
+    """out[e] = sum over group e's rows of a[r]^T b[r]: a [R, M], b [R, N],
+    out [E, M, N], all bf16 or all fp16."""
+    (R, M), N, E = a.shape, b.shape[1], out.shape[0]
+    _expect(b, "b", a.dtype, (R, N))
+    _expect(out, "out", a.dtype, (E, M, N))
+    _expect(offsets, "offsets", torch.int32, (E + 1,))
+    (pa, lda), (pb, ldb) = _rows(a), _rows(b)
+    _check(load().moe_grouped_wgrad(_dtype(a), R, M, N, E, pa, lda, pb, ldb, _ptr(offsets),
+                                    _ptr(out), _ptr(status), _stream(stream)))
+
+
+def moe_fp4_scale_stride(fmt: int, K: int) -> int:
+    """Bytes of one row's block scales (0 for an invalid format or K)."""
+    return int(load().moe_fp4_scale_stride(fmt, K))
+
+
+def moe_quantize_fp4(fmt: int, x, codes, scales, tensor_scale=None, src=None, src_div: int = 1,
+                     swiglu: bool = False, stream=None) -> None:
+    """codes [rows, K / 2] and scales [rows, moe_fp4_scale_stride(fmt, K)] (uint8) of the
+    rows of x (bf16 or fp16), or of x[src // src_div]; with ``swiglu`` of silu(gate) * up
+    of x's 2 K columns, interleaved per 128."""
+    rows, K = codes.shape[0], codes.shape[1] * 2
+    _expect(codes, "codes", torch.uint8, (rows, K // 2))
+    _expect(scales, "scales", torch.uint8, (rows, moe_fp4_scale_stride(fmt, K)))
+    _expect(src, "src", torch.int32, (rows,))
+    _expect(tensor_scale, "tensor_scale", torch.float32, (1,))
+    _expect(x, "x", x.dtype, (x.shape[0], 2 * K if swiglu else K))
+    px, ldx = _rows(x)
+    _check(load().moe_quantize_fp4(fmt, _dtype(x), rows, K, px, x.shape[0], ldx, _ptr(src),
+                                   src_div, int(swiglu), _ptr(tensor_scale), _ptr(codes),
+                                   _ptr(scales), _stream(stream)))
+
+
+def moe_dequantize_fp4(fmt: int, codes, scales, out, tensor_scale=None, stream=None) -> None:
+    """out [rows, K] (bf16 or fp16) = the values of 4-bit rows."""
+    rows, K = out.shape
+    _expect(codes, "codes", torch.uint8, (rows, K // 2))
+    _expect(scales, "scales", torch.uint8, (rows, moe_fp4_scale_stride(fmt, K)))
+    _expect(tensor_scale, "tensor_scale", torch.float32, (1,))
+    po, ldo = _rows(out)
+    _check(load().moe_dequantize_fp4(fmt, _dtype(out), rows, K, _ptr(codes), _ptr(scales),
+                                     _ptr(tensor_scale), po, ldo, _stream(stream)))
+
+
+def moe_grouped_gemm_fp4(fmt: int, x_codes, x_scales, w_codes, w_scales, offsets, y, x_scale=None,
+                         w_scale=None, row_scale=None, status=None, stream=None) -> None:
+    """y[r] = row_scale[r] * x_scale * w_scale[e] * x[r] W[e]^T on 4-bit rows x [R, K] and
+    weights [E, N, K] (codes [.., K / 2] and scales [.., stride], uint8); y bf16 [R, N]."""
+    R, K = x_codes.shape[0], x_codes.shape[1] * 2
+    E, N = w_codes.shape[:2]
+    stride = moe_fp4_scale_stride(fmt, K)
+    _expect(x_codes, "x_codes", torch.uint8, (R, K // 2))
+    _expect(x_scales, "x_scales", torch.uint8, (R, stride))
+    _expect(w_codes, "w_codes", torch.uint8, (E, N, K // 2))
+    _expect(w_scales, "w_scales", torch.uint8, (E, N, stride))
+    _expect(y, "y", torch.bfloat16, (R, N))
+    _expect(offsets, "offsets", torch.int32, (E + 1,))
+    _expect(x_scale, "x_scale", torch.float32, (1,))
+    _expect(w_scale, "w_scale", torch.float32, (E,))
+    _expect(row_scale, "row_scale", torch.float32, (R,))
+    py, ldy = _rows(y)
+    _check(load().moe_grouped_gemm_fp4(fmt, R, N, K, E, _ptr(x_codes), _ptr(x_scales),
+                                       _ptr(w_codes), _ptr(w_scales), _ptr(offsets), _ptr(x_scale),
+                                       _ptr(w_scale), _ptr(row_scale), py, ldy, _ptr(status),
+                                       _stream(stream)))
 
 
 def moe_get_device_status(ws, stream=None) -> int:
