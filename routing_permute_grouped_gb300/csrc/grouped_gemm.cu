@@ -1484,6 +1484,24 @@ bool make_tensor_map_2d(void* tmap, const void* ptr, int64_t rows, int64_t cols,
     return r == CUDA_SUCCESS;
 }
 
+bool make_tensor_map(void* tmap, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box, int dtype) {
+    PFN_encodeTiled enc = encode_fn();
+    if (!enc || rank < 2 || rank > 5) return false;
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], estr[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        estr[i] = 1;
+        if (i) st[i - 1] = strides[i - 1];
+    }
+    return enc(static_cast<CUtensorMap*>(tmap), static_cast<CUtensorMapDataType>(dtype),
+               static_cast<cuuint32_t>(rank), const_cast<void*>(ptr), d, st, b, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // K-major operand [rows, K]: {64, box_rows} boxes.
 static bool make_tmap(CUtensorMap* tm, const void* ptr, int64_t rows, int64_t K, int box_rows) {
     return make_tmap_box(tm, ptr, rows, K, BK, box_rows);

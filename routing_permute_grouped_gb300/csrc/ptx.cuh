@@ -176,6 +176,20 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr) {
     return d;
 }
 
+// Shared-memory descriptor of an MN-major operand in the 128-byte swizzle:
+// rows of 128 bytes (64 16-bit elements along M or N) per k, 8-row groups 1024
+// bytes apart (stride byte offset), 64-column chunks `chunk_bytes` apart
+// (leading byte offset).
+__device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t chunk_bytes) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>((chunk_bytes >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
 // Instruction descriptor of tcgen05.mma kind::f16 with bf16 A and B, fp32
 // accumulator, both operands K-major, no negation / sparsity:
 //   [4,6) D format 1 = f32   [7,10) A format 1 = bf16   [10,13) B format 1 =
@@ -401,6 +415,14 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint16_t mask) {
 
 
 
+// 3D tiled store of a shared-memory box to global memory (bulk async group).
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, const void* smem_src, int32_t x0, int32_t y0,
+                                             int32_t z0) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(tm)),
+                 "r"(x0), "r"(y0), "r"(z0), "r"(smem_u32(smem_src))
+                 : "memory");
+}
 // 2D tiled store of a shared-memory box to global memory (bulk async group).
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, const void* smem_src, int32_t x0,
                                              int32_t y0) {

@@ -39,6 +39,74 @@ __device__ __forceinline__ int2 group_rows(const RaggedArgs& a, int e) {
     return make_int2(lo, hi);
 }
 
+// ------------------------------------------------------------ work list --
+// The products put the weights on the MMA's M side (256 rows of W[e] across a
+// CTA pair) and the token rows on its N side, whose extent is free in steps of
+// 32: a group of any size then costs its own rows rounded up to 32, not a
+// multiple of the tile.  A group of len rows is cut into ceil(len / TN) equal
+// token tiles; a work item is one token tile times one 256-row weight panel.
+struct RaggedTiles {
+    int first[kRaggedMaxGroups + 1];  // a group's first work item
+    int lo[kRaggedMaxGroups], hi[kRaggedMaxGroups];
+};
+
+struct RaggedItem {
+    int e, panel;
+    int row, rows;  // token rows [row, row + rows)
+};
+
+// One warp fills the list from the offsets.
+template <int TN>
+__device__ void ragged_tiles_build(const RaggedArgs& a, RaggedTiles& s, int panels, int lane) {
+    int running = 0;
+    for (int base = 0; base < a.E; base += 32) {
+        const int e = base + lane;
+        int n = 0;
+        if (e < a.E) {
+            const int2 g = group_rows(a, e);
+            s.lo[e] = g.x;
+            s.hi[e] = g.y;
+            n = (g.y - g.x + TN - 1) / TN * panels;
+        }
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (e < a.E) s.first[e] = running + x - n;
+        running += __shfl_sync(0xFFFFFFFFu, x, 31);
+    }
+    if (lane == 0) s.first[a.E] = running;
+}
+
+// Item t: its group by bisection; inside a group, token tiles pass over eight
+// panels at a time, so the items in flight share both operands in L2.
+template <int TN>
+__device__ __forceinline__ RaggedItem ragged_item(const RaggedArgs& a, const RaggedTiles& s, int panels, int t) {
+    int lo = 0, hi = a.E;  // first[lo] <= t < first[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s.first[mid] <= t)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    RaggedItem it;
+    it.e = lo;
+    const int len = s.hi[lo] - s.lo[lo];
+    const int tiles = (len + TN - 1) / TN;
+    const int width = ((len + tiles - 1) / tiles + 31) & ~31;  // <= TN
+    const int i = t - s.first[lo];
+    const int block = i / (tiles * 8), rest = i - block * tiles * 8;
+    const int wide = min(8, panels - block * 8);
+    const int tile = rest / wide;
+    it.panel = block * 8 + rest - tile * wide;
+    it.row = s.lo[lo] + tile * width;
+    it.rows = min(width, s.hi[lo] - it.row);
+    return it;
+}
+
 template <typename T>
 __device__ __forceinline__ float to_float(T v);
 template <>
@@ -51,6 +119,34 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
 template <>
 __device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
+
+__device__ __forceinline__ uint32_t pack2(__nv_bfloat16, float lo, float hi) { return pack_bf16x2(lo, hi); }
+__device__ __forceinline__ uint32_t pack2(__half, float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Epilogue of the products for 32 accumulator columns (tokens row .. row + 31
+// of which `rows` are stored): lane l of the warp holds feature n0 + l of
+// every token.  Neighbouring lanes exchange halves, so that one 4-byte store
+// per lane writes two features of the even or the odd token: each store
+// instruction covers 64 contiguous bytes of two output rows.
+template <typename T>
+__device__ __forceinline__ void store_transposed(const RaggedArgs& a, const uint32_t (&v)[32], int row, int rows,
+                                                 int n0, int lane, float scale) {
+    const int odd = lane & 1;
+    const float gate = a.row_scale && lane < rows ? ld_dep(a.row_scale + row + lane) * scale : scale;
+    T* out = static_cast<T*>(a.out) + (static_cast<int64_t>(row) + odd) * a.ldo + n0 + lane - odd;
+    const bool in = n0 + lane < a.N;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[i] : v[i + 1], 1);
+        const float g = __shfl_sync(0xFFFFFFFFu, gate, i + odd);
+        const float x0 = __uint_as_float(odd ? other : v[i]) * g;
+        const float x1 = __uint_as_float(odd ? v[i + 1] : other) * g;
+        if (in && i + odd < rows) *reinterpret_cast<uint32_t*>(out + i * a.ldo) = pack2(T(), x0, x1);
+    }
+}
 
 // ---------------------------------------------------------- 4-bit values --
 // Two e2m1 codes (low nibble first) -> two floats; every e2m1 value is an f16

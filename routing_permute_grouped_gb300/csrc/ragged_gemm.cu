@@ -2,8 +2,31 @@
 // bf16 or f16: y[r] = row_scale[r] * x[r] W[e]^T (or x[r] W[e]) and the weight
 // gradient dW[e] = sum over e's rows of a[r]^T b[r].
 //
-// Plain tiles: a 16 x 16 thread block computes 64 x 64 outputs, operands
-// staged through shared memory in steps of 16, fp32 accumulators.
+// Both run on CTA pairs (tcgen05 cta_group::2, fp32 accumulators in tensor
+// memory, two of them so that a tile's epilogue overlaps the next tile's MMAs),
+// one persistent pair per two SMs, operands staged by TMA in 64-element steps
+// of the sum.
+//
+// Product.  The operands are swapped: 256 rows of W[e] are the MMA's M (128 per
+// CTA), a token tile of at most 256 rows its N, in steps of 32 -- a ragged
+// group wastes at most 31 columns of one tile, where row tiles on the M side
+// waste up to 255 rows.  The same kernel then serves two rows per expert (the
+// weights stream through the SM once) and thousands.  W is K-major or, for x W
+// and the data gradient, MN-major through the transposing bit of the MMA; no
+// copy is laid out.  Sizes that the tiles do not divide are zero-filled by TMA
+// on loads and cut off by the epilogue.
+//
+// Weight gradient.  The sum runs along the rows, so both operands are MN-major.
+// The last step of a group holds rows of the next one: one warp of each CTA
+// zeroes them in shared memory (both operands: a NaN of another group times
+// zero is not zero) before the step is handed to the MMAs.  An empty group's
+// tiles are written as zeros.
+//
+// Warp roles: warp 0 TMA producer, warp 1 tensor memory and MMA issue (even
+// CTA), warps 2..9 epilogue, warp 10 (weight gradient) the zeroing of tails.
+// Every wait is bounded; on a timeout the CTA flags the status word, lets its
+// copies and MMAs in flight finish and returns.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "../../include/moe.h"
@@ -16,77 +39,550 @@ namespace moe {
 
 namespace {
 
+constexpr int kTN = 256;                // token rows of a tile, at most
+constexpr int kBK = 64;                 // step of the sum
+constexpr int kOpBytes = 128 * kBK * 2; // one operand of one CTA and stage: 16 KB
+constexpr int kStage = 2 * kOpBytes;
+constexpr int kChunk = 64 * kBK * 2;    // a 64 x 64 box of an MN-major operand
+constexpr int kEpiWarps = 8;
+constexpr uint32_t kTimeout = 0x2u;
+constexpr uint32_t kTransA = 1u << 15, kTransB = 1u << 16;
+
 template <typename T>
-struct Strided {  // element (row, k) of a group's operand
-    const T* p;
-    int64_t row, k;
-    __device__ float at(int64_t r, int64_t kk) const { return to_float(p[r * row + kk * k]); }
+struct Elem;
+template <>
+struct Elem<__nv_bfloat16> {
+    static constexpr int map = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    static constexpr uint32_t idesc = idesc_bf16_f32(256, 8) & ~(0x3Fu << 17);
+};
+template <>
+struct Elem<__half> {  // operand formats 0 in bits [7,10) and [10,13)
+    static constexpr int map = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    static constexpr uint32_t idesc = (1u << 4) | ((256u >> 4) << 24);
 };
 
-// The e-th group and 64-row tile of flat tile index t; e = -1 past the last.
-__device__ int3 find_tile(const RaggedArgs& a, int t) {
-    for (int e = 0; e < a.E; ++e) {
-        const int2 g = group_rows(a, e);
-        const int n = (g.y - g.x + 63) / 64;
-        if (t < n) return make_int3(e, g.x + 64 * t, g.y);
-        t -= n;
-    }
-    return make_int3(-1, 0, 0);
-}
+// The barriers of a pipeline of S stages and two accumulators, and what a
+// pair shares; the first 1 KB of shared memory.
+template <int S>
+struct PairBars {
+    uint64_t full[S], empty[S], tail[S], tfull[2], tempty[2], drain;
+    uint32_t tmem, abort;
+};
 
-// 64 x 64 tile of A B^T: rows [m0, m1) of A, [n0, n1) of B, sum over [k0, k1)
-template <typename T, typename Put>
-__device__ void tile_product(const Strided<T>& A, int64_t m0, int64_t m1, const Strided<T>& B, int64_t n0,
-                             int64_t n1, int64_t k0, int64_t k1, Put put) {
-    __shared__ float sa[16][65], sb[16][65];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int64_t k = k0; k < k1; k += 16) {
-        for (int i = threadIdx.x; i < 1024; i += 256) {
-            const int kk = i & 15, r = i >> 4;
-            sa[kk][r] = (m0 + r < m1 && k + kk < k1) ? A.at(m0 + r, k + kk) : 0.0f;
-            sb[kk][r] = (n0 + r < n1 && k + kk < k1) ? B.at(n0 + r, k + kk) : 0.0f;
+struct Ring {  // stage and its parity
+    int s = 0;
+    uint32_t ph = 0;
+    template <int S>
+    __device__ __forceinline__ void next() {
+        if (++s == S) {
+            s = 0;
+            ph ^= 1u;
         }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < 16; ++kk)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += sa[kk][ty + 16 * i] * sb[kk][tx + 16 * j];
-        __syncthreads();
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j)
-            if (m0 + ty + 16 * i < m1 && n0 + tx + 16 * j < n1) put(m0 + ty + 16 * i, n0 + tx + 16 * j, acc[i][j]);
+};
+
+struct Acc {  // accumulator and its parity
+    int i = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        i ^= 1;
+        if (i == 0) ph ^= 1u;
+    }
+};
+
+template <int S>
+__device__ __forceinline__ void pair_start(PairBars<S>& b, uint32_t full_count, int warp) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(b.full + i, full_count);
+            mbar_init(b.empty + i, 1);
+            mbar_init(b.tail + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(b.tfull + i, 1);
+            mbar_init(b.tempty + i, 2 * kEpiWarps);  // every epilogue warp of both CTAs
+        }
+        mbar_init(&b.drain, 1);
+        b.abort = 0;
+        fence_mbar_init();
+    }
+    // tensor memory is taken only once the kernels before this one have
+    // finished (and released theirs)
+    pdl_wait();
+    if (warp == 1) tmem_alloc_pair(&b.tmem, 512);
+}
+
+__device__ __forceinline__ void pair_end(uint32_t tmem_base, int warp) {
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// ---------------------------------------------------------------- product --
+constexpr int kProdStages = 6;
+constexpr int kProdSmem = 1024 + kProdStages * kStage + 1024 + static_cast<int>(sizeof(RaggedTiles));
+
+template <typename T, bool WT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps, 1)
+    k_ragged_product(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tX,
+                     const __grid_constant__ CUtensorMap tX16, const RaggedArgs args) {
+    constexpr int S = kProdStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    PairBars<S>& bars = *reinterpret_cast<PairBars<S>*>(smem + S * kStage);
+    static_assert(sizeof(PairBars<S>) <= 1024, "barriers");
+    RaggedTiles& tiles = *reinterpret_cast<RaggedTiles*>(smem + S * kStage + 1024);
+    volatile uint32_t* abort_flag = &bars.abort;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int panels = (args.N + 255) / 256;
+    const int steps = (args.K + kBK - 1) / kBK;
+    pdl_trigger();
+    pair_start(bars, 1, warp);
+    if (warp == 2) ragged_tiles_build<kTN>(args, tiles, panels, lane);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the peer's barriers are initialised before any remote use
+    tc_fence_after();
+    const uint32_t tmem_base = bars.tmem;
+    const int total = tiles.first[args.E];
+    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    bool timed_out = false;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------ TMA producer
+            Ring r;
+            uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
+            for (int t = first; t < total && !timed_out; t += stride) {
+                const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
+                const int half = ((it.rows + 31) & ~31) / 2;  // token rows of each CTA
+                const int xrow = it.row + half * static_cast<int>(rank);
+                const int wrow = it.panel * 256 + 128 * static_cast<int>(rank);
+                for (int k = 0; k < steps; ++k) {
+                    if (!mbar_wait(bars.empty + r.s, r.ph ^ 1u, abort_flag)) {
+                        timed_out = true;
+                        break;
+                    }
+                    const uint32_t full = mapa_shared(smem_u32(bars.full + r.s), 0);
+                    uint8_t* st = smem + r.s * kStage;
+                    armed &= ~(1u << r.s);
+                    if (leader) mbar_arrive_expect_tx(bars.full + r.s, 2 * (kOpBytes + half * 128));
+                    if constexpr (WT) {
+                        tma_load_3d_pair(st, &tW, wrow, k * kBK, it.e, full);
+                        tma_load_3d_pair(st + kChunk, &tW, wrow + 64, k * kBK, it.e, full);
+                    } else {
+                        tma_load_3d_pair(st, &tW, k * kBK, wrow, it.e, full);
+                    }
+                    if (half == 128) {
+                        tma_load_2d_pair(st + kOpBytes, &tX, k * kBK, xrow, full);
+                    } else {
+                        for (int j = 0; j < half; j += 16)
+                            tma_load_2d_pair(st + kOpBytes + j * 128, &tX16, k * kBK, xrow + j, full);
+                    }
+                    armed |= 1u << r.s;
+                    armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
+                    r.next<S>();
+                }
+            }
+            if ((timed_out || *abort_flag) && leader) {
+                *abort_flag = 1;
+                for (int i = 0; i < S; ++i)
+                    if (armed & (1u << i)) {
+                        volatile uint32_t never = 0;
+                        (void)mbar_wait(bars.full + i, (armed_par >> i) & 1u, &never);
+                    }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            // ------------------------------------------------- MMA issuer
+            Ring r;
+            Acc acc;
+            bool issued = false;
+            for (int t = first; t < total && !timed_out; t += stride) {
+                const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
+                const uint32_t n = (it.rows + 31) & ~31;
+                const uint32_t idesc = Elem<T>::idesc | ((n >> 3) << 17) | (WT ? kTransA : 0u);
+                if (!mbar_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
+                    timed_out = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem_base + static_cast<uint32_t>(acc.i * kTN);
+                for (int k = 0; k < steps; ++k) {
+                    if (!mbar_wait(bars.full + r.s, r.ph, abort_flag)) {
+                        timed_out = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t wa = smem_u32(smem + r.s * kStage), xa = wa + kOpBytes;
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        mma_bf16_pair(d, WT ? sdesc_sw128_mn(wa + kk * 2048, kChunk) : sdesc_sw128(wa + kk * 32),
+                                      sdesc_sw128(xa + kk * 32), idesc, (k | kk) != 0 ? 1u : 0u);
+                    issued = true;
+                    mma_commit_pair(bars.empty + r.s, 0x3);
+                    r.next<S>();
+                }
+                if (timed_out) break;
+                mma_commit_pair(bars.tfull + acc.i, 0x3);
+                acc.next();
+            }
+            if ((timed_out || *abort_flag) && issued) {
+                *abort_flag = 1;
+                mma_commit_pair(&bars.drain, 0x1);
+                volatile uint32_t never = 0;
+                (void)mbar_wait(&bars.drain, 0, &never);
+            }
+        }
+    } else {
+        // ------------------------------------------------------ epilogue
+        // A warp owns 32 of the CTA's 128 features (its tensor-memory lane
+        // quarter) and every other 32-token chunk.
+        const int q = warp & 3, odd = (warp - 2) >> 2;
+        Acc acc;
+        for (int t = first; t < total; t += stride) {
+            const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars.tfull + acc.i, acc.ph, abort_flag))) {
+                timed_out = true;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t taddr =
+                tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc.i * kTN);
+            const int n0 = it.panel * 256 + static_cast<int>(rank) * 128 + q * 32;
+#pragma unroll 1
+            for (int c = odd * 32; c < it.rows; c += 64) {
+                uint32_t v[32];
+                tmem_ld32(taddr + c, v);
+                tmem_ld_wait();
+                store_transposed<T>(args, v, it.row + c, it.rows - c, n0, lane, 1.0f);
+            }
+            // the reads are complete: the MMA side reads nothing stored here
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), 0));
+            acc.next();
+        }
+        if (timed_out) *abort_flag = 1;
+    }
+    if (timed_out && args.status) atomicOr(args.status, kTimeout);
+    pair_end(tmem_base, warp);
+}
+
+// -------------------------------------------------------- weight gradient --
+constexpr int kGradStages = 5;
+constexpr int kOutStage = kEpiWarps * 2 * 4096;  // epilogue warps x 2 buffers x (32 rows x 128 bytes)
+constexpr int kGradSmem = 1024 + kGradStages * kStage + kOutStage + 1024;
+
+struct GradTile {
+    int e, m, n;     // group, first row and column of the 256 x 256 output tile
+    int row, rows;   // the group's rows
+};
+
+__device__ __forceinline__ GradTile grad_tile(const RaggedArgs& a, int t) {
+    const int nt = (a.N + 255) / 256, mt = (a.K + 255) / 256;
+    GradTile g;
+    g.e = t / (mt * nt);
+    const int r = t - g.e * mt * nt;
+    g.m = r / nt * 256;
+    g.n = r % nt * 256;
+    const int2 rows = group_rows(a, g.e);
+    g.row = rows.x;
+    g.rows = rows.y - rows.x;
+    return g;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) k_ragged_product(RaggedArgs a, const T* x, int64_t ldx, const T* w,
-                                                        bool w_transposed) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps, 1)
+    k_ragged_wgrad(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB,
+                   const __grid_constant__ CUtensorMap tOut, const RaggedArgs args) {
+    constexpr int S = kGradStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* sOut = smem + S * kStage;
+    PairBars<S>& bars = *reinterpret_cast<PairBars<S>*>(sOut + kOutStage);
+    volatile uint32_t* abort_flag = &bars.abort;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
     pdl_trigger();
-    pdl_wait();
-    const int3 t = find_tile(a, blockIdx.y);
-    if (t.x < 0) return;
-    const Strided<T> X{x, ldx, 1};
-    const Strided<T> W{w + static_cast<int64_t>(t.x) * a.N * a.K, w_transposed ? 1 : a.K, w_transposed ? a.N : 1};
-    T* out = static_cast<T*>(a.out);
-    tile_product(X, t.y, min(t.z, t.y + 64), W, static_cast<int64_t>(blockIdx.x) * 64, a.N, 0, a.K,
-                 [&](int64_t r, int64_t n, float v) {
-                     out[r * a.ldo + n] = from_float<T>(a.row_scale ? v * ld_dep(a.row_scale + r) : v);
-                 });
+    pair_start(bars, 2, warp);  // a stage is full when both CTAs say so (and its bytes have landed)
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = bars.tmem;
+    const int total = args.E * ((args.N + 255) / 256) * ((args.K + 255) / 256);
+    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    bool timed_out = false;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------ TMA producer
+            Ring r;
+            uint32_t armed = 0, armed_par = 0, tails = 0, tail_par = 0, tail_ph = 0;
+            for (int t = first; t < total && !timed_out; t += stride) {
+                const GradTile g = grad_tile(args, t);
+                const int ac = g.m + 128 * static_cast<int>(rank), bc = g.n + 128 * static_cast<int>(rank);
+                for (int k = 0; k < g.rows; k += kBK) {
+                    if (!mbar_wait(bars.empty + r.s, r.ph ^ 1u, abort_flag)) {
+                        timed_out = true;
+                        break;
+                    }
+                    uint8_t* st = smem + r.s * kStage;
+                    const uint32_t bit = 1u << r.s;
+                    armed &= ~bit;
+                    tails &= ~bit;
+                    uint32_t bar;
+                    if (g.rows - k >= kBK) {
+                        bar = mapa_shared(smem_u32(bars.full + r.s), 0);
+                        if (leader)
+                            mbar_arrive_expect_tx(bars.full + r.s, 2 * kStage);
+                        else
+                            mbar_arrive_cluster_relaxed(bar);
+                        armed |= bit;
+                        armed_par = (armed_par & ~bit) | (r.ph << r.s);
+                    } else {  // the zeroing warp hands this stage on
+                        bar = mapa_shared(smem_u32(bars.tail + r.s), rank);
+                        mbar_arrive_expect_tx(bars.tail + r.s, kStage);
+                        tails |= bit;
+                        tail_par = (tail_par & ~bit) | (tail_ph & bit);
+                        tail_ph ^= bit;
+                    }
+                    const int row = g.row + k;
+                    tma_load_2d_pair(st, &tA, ac, row, bar);
+                    tma_load_2d_pair(st + kChunk, &tA, ac + 64, row, bar);
+                    tma_load_2d_pair(st + kOpBytes, &tB, bc, row, bar);
+                    tma_load_2d_pair(st + kOpBytes + kChunk, &tB, bc + 64, row, bar);
+                    r.next<S>();
+                }
+            }
+            if (timed_out || *abort_flag) {
+                *abort_flag = 1;
+                volatile uint32_t never = 0;
+                for (int i = 0; i < S; ++i) {
+                    if (leader && (armed & (1u << i)))
+                        (void)mbar_wait(bars.full + i, (armed_par >> i) & 1u, &never);
+                    if (tails & (1u << i)) (void)mbar_wait(bars.tail + i, (tail_par >> i) & 1u, &never);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            // ------------------------------------------------- MMA issuer
+            constexpr uint32_t idesc = Elem<T>::idesc | ((256u >> 3) << 17) | kTransA | kTransB;
+            Ring r;
+            Acc acc;
+            bool issued = false;
+            for (int t = first; t < total && !timed_out; t += stride) {
+                const GradTile g = grad_tile(args, t);
+                if (g.rows == 0) continue;  // the epilogue writes zeros
+                if (!mbar_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
+                    timed_out = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem_base + static_cast<uint32_t>(acc.i * 256);
+                for (int k = 0; k < g.rows; k += kBK) {
+                    if (!mbar_wait(bars.full + r.s, r.ph, abort_flag)) {
+                        timed_out = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t aa = smem_u32(smem + r.s * kStage), ba = aa + kOpBytes;
+                    const int n16 = min(kBK, g.rows - k + 15) / 16;  // 16 rows per MMA
+                    for (int kk = 0; kk < n16; ++kk)
+                        mma_bf16_pair(d, sdesc_sw128_mn(aa + kk * 2048, kChunk), sdesc_sw128_mn(ba + kk * 2048, kChunk),
+                                      idesc, (k | kk) != 0 ? 1u : 0u);
+                    issued = true;
+                    mma_commit_pair(bars.empty + r.s, 0x3);
+                    r.next<S>();
+                }
+                if (timed_out) break;
+                mma_commit_pair(bars.tfull + acc.i, 0x3);
+                acc.next();
+            }
+            if ((timed_out || *abort_flag) && issued) {
+                *abort_flag = 1;
+                mma_commit_pair(&bars.drain, 0x1);
+                volatile uint32_t never = 0;
+                (void)mbar_wait(&bars.drain, 0, &never);
+            }
+        }
+    } else if (warp == 2 + kEpiWarps) {
+        // ------------------------------------------------- zeroing of tails
+        Ring r;
+        uint32_t tail_ph = 0;
+        for (int t = first; t < total && !timed_out; t += stride) {
+            const GradTile g = grad_tile(args, t);
+            const int steps = (g.rows + kBK - 1) / kBK, rest = g.rows % kBK;
+            for (int k = 0; k + 1 < steps; ++k) r.next<S>();
+            if (steps == 0) continue;
+            if (rest) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars.tail + r.s, (tail_ph >> r.s) & 1u, abort_flag))) {
+                    timed_out = true;
+                    break;
+                }
+                tail_ph ^= 1u << r.s;
+                // rows [rest, next multiple of 16): one 128-byte row in each of
+                // the four 64-column chunks (a row stays in its own 128 bytes
+                // under the swizzle)
+                uint8_t* st = smem + r.s * kStage;
+                const int n = ((rest + 15) & ~15) - rest;
+                for (int i = lane; i < n * 32; i += 32) {
+                    const int row = rest + (i >> 5), c = (i >> 3) & 3;
+                    *reinterpret_cast<uint4*>(st + c * kChunk + row * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(bars.full + r.s), 0));
+            }
+            r.next<S>();
+        }
+    } else {
+        // ------------------------------------------------------ epilogue
+        // Each warp owns 32 rows of M (its tensor-memory lane quarter) and
+        // half of the tile's columns, and stores them through TMA from boxes
+        // of 32 x 64 staged in shared memory (two buffers per warp); TMA cuts
+        // off what lies past M or N.
+        const int q = warp & 3, ew = warp - 2;
+        const int c0 = (ew >> 2) * 128;
+        Acc acc;
+        int buf = 0;
+        uint8_t* stage = sOut + ew * 2 * 4096;
+        for (int t = first; t < total; t += stride) {
+            const GradTile g = grad_tile(args, t);
+            const int m = g.m + 128 * static_cast<int>(rank) + q * 32;
+            uint32_t pk[64];
+            if (g.rows) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars.tfull + acc.i, acc.ph, abort_flag))) {
+                    timed_out = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t taddr =
+                    tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc.i * 256 + c0);
+#pragma unroll
+                for (int c = 0; c < 128; c += 64) {
+                    uint32_t v[2][32];
+                    tmem_ld32(taddr + c, v[0]);
+                    tmem_ld32(taddr + c + 32, v[1]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        pk[c / 2 + i] = pack2(T(), __uint_as_float(v[i >> 4][2 * (i & 15)]),
+                                              __uint_as_float(v[i >> 4][2 * (i & 15) + 1]));
+                }
+                // handed back before the stores; they are not what the MMA
+                // side waits for, so the arrive need not release them
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), 0));
+                acc.next();
+            } else {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) pk[i] = 0u;
+            }
+#pragma unroll
+            for (int c = 0; c < 128; c += 64) {
+                // a box past the edge takes no buffer: the wait below counts
+                // on every turn of a buffer having its store
+                if (m >= args.K || g.n + c0 + c >= args.N) continue;
+                if (lane == 0) bulk_wait_read<1>();  // this buffer's previous store has read it
+                __syncwarp();
+                uint8_t* sb = stage + buf * 4096 + lane * 128;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {  // 16-byte chunks of the 128-byte row
+                    const uint32_t* u = pk + c / 2 + 4 * j;
+                    *reinterpret_cast<uint4*>(sb + ((j ^ (lane & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&tOut, stage + buf * 4096, g.n + c0 + c, m, g.e);
+                    bulk_commit();
+                }
+                buf ^= 1;
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+        if (timed_out) *abort_flag = 1;
+    }
+    if (timed_out && args.status) atomicOr(args.status, kTimeout);
+    pair_end(tmem_base, warp);
+}
+
+// --------------------------------------------------------------- launches --
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, bool (&done)[kMaxDevices]) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (done[dev]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done[dev] = true;
+    return e;
+}
+
+unsigned pair_grid(int64_t items) {
+    const int64_t pairs = num_sms() / 2;
+    return static_cast<unsigned>(2 * (items < pairs ? items : pairs));
+}
+
+template <typename T, bool WT>
+cudaError_t launch_product(const RaggedArgs& a, const void* x, int64_t ldx, const void* w, cudaStream_t st) {
+    static_assert(kProdSmem <= 232448, "shared memory budget");
+    static bool done[kMaxDevices] = {};
+    cudaError_t e = allow_smem(k_ragged_product<T, WT>, kProdSmem, done);
+    if (e != cudaSuccess) return e;
+    const uint64_t N = a.N, K = a.K, R = a.R, E = a.E;
+    CUtensorMap tW, tX, tX16;
+    const uint64_t wd[3] = {WT ? N : K, WT ? K : N, E};
+    const uint64_t ws[2] = {wd[0] * 2, N * K * 2};
+    const uint32_t wb[3] = {64, WT ? 64u : 128u, 1};
+    const uint64_t xd[2] = {K, R}, xs[1] = {static_cast<uint64_t>(ldx) * 2};
+    const uint32_t xb[2] = {64, 128}, xb16[2] = {64, 16};
+    if (!make_tensor_map(&tW, w, 3, wd, ws, wb, Elem<T>::map) || !make_tensor_map(&tX, x, 2, xd, xs, xb, Elem<T>::map) ||
+        !make_tensor_map(&tX16, x, 2, xd, xs, xb16, Elem<T>::map))
+        return cudaErrorInvalidValue;
+    const int64_t items = (R / kTN + (R < E ? R : E)) * ((N + 255) / 256);  // at most
+    return launch_pdl(k_ragged_product<T, WT>, dim3(pair_grid(items)), dim3(64 + 32 * kEpiWarps), kProdSmem, st, tW, tX,
+                      tX16, a);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) k_ragged_wgrad(RaggedArgs a, const T* x, int64_t ldx, const T* y, int64_t ldy) {
-    pdl_trigger();
-    pdl_wait();
-    const int e = blockIdx.z;
-    const int2 g = group_rows(a, e);
-    const Strided<T> X{x, 1, ldx}, Y{y, 1, ldy};
-    T* out = static_cast<T*>(a.out) + static_cast<int64_t>(e) * a.K * a.N;
-    tile_product(X, static_cast<int64_t>(blockIdx.y) * 64, a.K, Y, static_cast<int64_t>(blockIdx.x) * 64, a.N, g.x,
-                 g.y, [&](int64_t m, int64_t n, float v) { out[m * a.N + n] = from_float<T>(v); });
+cudaError_t launch_wgrad_ragged(const RaggedArgs& a, const void* x, int64_t ldx, const void* y, int64_t ldy,
+                                cudaStream_t st) {
+    static_assert(kGradSmem <= 232448, "shared memory budget");
+    static bool done[kMaxDevices] = {};
+    cudaError_t e = allow_smem(k_ragged_wgrad<T>, kGradSmem, done);
+    if (e != cudaSuccess) return e;
+    const uint64_t M = a.K, N = a.N, R = a.R, E = a.E;
+    CUtensorMap tA, tB, tOut;
+    const uint64_t ad[2] = {M, R}, as[1] = {static_cast<uint64_t>(ldx) * 2};
+    const uint64_t bd[2] = {N, R}, bs[1] = {static_cast<uint64_t>(ldy) * 2};
+    const uint64_t od[3] = {N, M, E}, os[2] = {N * 2, M * N * 2};
+    const uint32_t box[2] = {64, 64}, obox[3] = {64, 32, 1};
+    if (!make_tensor_map(&tA, x, 2, ad, as, box, Elem<T>::map) || !make_tensor_map(&tB, y, 2, bd, bs, box, Elem<T>::map) ||
+        !make_tensor_map(&tOut, a.out, 3, od, os, obox, Elem<T>::map))
+        return cudaErrorInvalidValue;
+    const int64_t items = static_cast<int64_t>(E) * ((N + 255) / 256) * ((M + 255) / 256);
+    if (items > INT32_MAX) return cudaErrorInvalidValue;
+    return launch_pdl(k_ragged_wgrad<T>, dim3(pair_grid(items)), dim3(96 + 32 * kEpiWarps), kGradSmem, st, tA, tB, tOut,
+                      a);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -131,15 +627,14 @@ extern "C" moe_status_t moe_grouped_gemm(int32_t dtype, int64_t R, int32_t N, in
     a.out = y;
     a.ldo = ldy;
     a.status = status;
-    const dim3 grid((N + 63) / 64, static_cast<unsigned>(R / 64 + E));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = dtype == MOE_DTYPE_BF16
-                        ? launch_pdl(k_ragged_product<__nv_bfloat16>, grid, dim3(256), 0, st, a,
-                                     static_cast<const __nv_bfloat16*>(x), ldx,
-                                     static_cast<const __nv_bfloat16*>(w), w_transposed != 0)
-                        : launch_pdl(k_ragged_product<__half>, grid, dim3(256), 0, st, a,
-                                     static_cast<const __half*>(x), ldx, static_cast<const __half*>(w),
-                                     w_transposed != 0);
+    cudaError_t e;
+    if (dtype == MOE_DTYPE_BF16)
+        e = w_transposed ? launch_product<__nv_bfloat16, true>(a, x, ldx, w, st)
+                         : launch_product<__nv_bfloat16, false>(a, x, ldx, w, st);
+    else
+        e = w_transposed ? launch_product<__half, true>(a, x, ldx, w, st)
+                         : launch_product<__half, false>(a, x, ldx, w, st);
     return e == cudaSuccess ? MOE_OK
                             : set_last_error(MOE_ERR_CUDA, "grouped product: %s", cudaGetErrorString(e));
 }
@@ -168,12 +663,8 @@ extern "C" moe_status_t moe_grouped_wgrad(int32_t dtype, int64_t R, int32_t M, i
         a.E = E;
         a.out = out;
         a.status = status;
-        const dim3 grid((N + 63) / 64, (M + 63) / 64, E);
-        e = dtype == MOE_DTYPE_BF16
-                ? launch_pdl(k_ragged_wgrad<__nv_bfloat16>, grid, dim3(256), 0, st, a,
-                             static_cast<const __nv_bfloat16*>(a_), lda, static_cast<const __nv_bfloat16*>(b), ldb)
-                : launch_pdl(k_ragged_wgrad<__half>, grid, dim3(256), 0, st, a, static_cast<const __half*>(a_), lda,
-                             static_cast<const __half*>(b), ldb);
+        e = dtype == MOE_DTYPE_BF16 ? launch_wgrad_ragged<__nv_bfloat16>(a, a_, lda, b, ldb, st)
+                                    : launch_wgrad_ragged<__half>(a, a_, lda, b, ldb, st);
     }
     return e == cudaSuccess ? MOE_OK
                             : set_last_error(MOE_ERR_CUDA, "grouped weight gradient: %s", cudaGetErrorString(e));

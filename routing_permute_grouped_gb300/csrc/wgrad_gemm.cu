@@ -47,19 +47,6 @@ constexpr int kThreads = 64 + 32 * kEpiWarps;
 // output staging: epilogue warps x 2 buffers x (32 rows x 128 bytes)
 constexpr int kOutStage = kEpiWarps * 2 * 4096;
 
-// Shared-memory descriptor of an MN-major operand in the 128-byte swizzle:
-// rows of 128 bytes (64 bf16 along M or N) per k, 8-row groups 1024 bytes
-// apart (stride byte offset), 64-column chunks `chunk_bytes` apart (leading
-// byte offset).
-__device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t chunk_bytes) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>((chunk_bytes >> 4) & 0x3FFFu) << 16;
-    d |= static_cast<uint64_t>(1024u >> 4) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(2u) << 61;
-    return d;
-}
 constexpr uint32_t kBadSegment = 0x4u;
 
 struct WTile {
