@@ -1,8 +1,30 @@
 // fp4_gemm.cu -- the grouped product on 4-bit rows and weights with block
 // scales: y[r] = row_scale[r] * gx * gw[e] * sum_k x[r, k] W[e][n, k].
 //
-// Plain tiles: a 16 x 16 thread block computes 64 x 64 outputs; both operands
-// are widened to fp32 (exactly) into shared memory in steps of 32.
+// The schedule of the 16-bit product (ragged_gemm.cu): 256 rows of W[e] are
+// the M of a CTA pair's MMAs, a token tile of at most 192 rows the N, in steps
+// of 32.  The MMAs (tcgen05 kind::mxf4 / kind::mxf4nvf4, K = 64) multiply the
+// e2m1 codes with their block scales as they are, so nothing is widened: a
+// step of 256 elements is 128 bytes of each row.
+//
+// Scales.  The MMA wants them in tensor memory as 32-bit words (four bytes
+// along K), word of row r in lane r % 32 and column r / 32.  In global memory
+// they are row-major.  Two warps of each CTA read 16 bytes of every row of the
+// tile (one warp the weights' rows, one the tokens'), so each lane holds four
+// words of rows i, i + 32, i + 64, i + 96: writing them word by word is the
+// transposition, four 16-byte shared-memory stores of 512 contiguous bytes per
+// 128 rows.  The MMA thread copies each 512-byte piece into four columns of
+// tensor memory (tcgen05.cp, broadcast to the four lane quarters) ahead of the
+// MMAs that use it.  Bytes past K are cleared on the way (they may hold
+// anything), rows past the operand repeat its last row and reach no stored
+// result.
+//
+// Tensor memory: two accumulators of 192 columns, two scale buffers of 48.
+//
+// Warp roles: warp 0 TMA producer, warp 1 tensor memory, scale copies and MMA
+// issue (even CTA), warp 2 weight scales, warp 3 token scales, warps 4..11
+// epilogue.  Every wait is bounded, as in ragged_gemm.cu.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "../../include/moe.h"
@@ -15,70 +37,334 @@ namespace moe {
 
 namespace {
 
-struct Fp4Rows {
-    const uint8_t* codes;   // [rows, K / 2]
-    const uint8_t* scales;  // [rows, stride]
+constexpr int kTN = 192;                  // token rows of a tile, at most
+constexpr int kStep = 256;                // step of the sum: 128 bytes of codes
+constexpr int kWBytes = 128 * 128;        // weight codes of one CTA and stage
+constexpr int kStage = kWBytes + kTN / 2 * 128;
+constexpr int kStages = 6;
+constexpr int kSlots = 4;                 // scale groups (16 bytes of every row) in shared memory
+constexpr int kSlotW = 4 * 512;           // four words of 128 weight rows
+constexpr int kSlot = kSlotW + 2 * 4 * 512;  // and of 256 token rows
+constexpr uint32_t kScaleCol = 2 * kTN;   // first tensor-memory column of the scale buffers
+constexpr uint32_t kScaleCols = 48;       // 4 words x (4 columns of A + 8 of B)
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr int kAhead = 3;                 // scale groups in flight to a scale warp's registers
+
+struct ScaleBars {
+    uint64_t full[kSlots], empty[kSlots], used[2];
+};
+constexpr int kSmem = 1024 + kStages * kStage + kSlots * kSlot + 1024 + static_cast<int>(sizeof(RaggedTiles));
+static_assert(kSmem <= 232448, "shared memory budget");
+static_assert(kStage % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+static_assert(kScaleCol + 2 * kScaleCols <= 512, "tensor memory budget");
+
+// A work item's scale group g (16 bytes of every row), in the order in which
+// the pair takes them.
+struct ScaleCursor {
+    int t, g;
+    RaggedItem it;
 };
 
-template <bool NV>
-__device__ void stage(float (&s)[32][65], const Fp4Rows& x, int64_t r0, int64_t r1, int k, int K, int stride) {
-    for (int i = threadIdx.x; i < 64 * 16; i += 256) {
-        const int r = i >> 4, b = i & 15;
-        float2 v = make_float2(0.0f, 0.0f);
-        if (r0 + r < r1) {
-            const uint32_t code = ld_dep(x.scales + (r0 + r) * stride + (k + 2 * b) / (NV ? 16 : 32));
-            const float sc = NV ? e4m3_to_f32(code) : e8m0_to_f32(code);
-            v = e2m1x2_to_f32x2(ld_dep(x.codes + (r0 + r) * (K / 2) + k / 2 + b));
-            v.x *= sc;
-            v.y *= sc;
+// Reads scale groups of NR * 32 rows ahead of their use and lays them out for
+// the copies into tensor memory.  `base(item)` is the first row, `last(item)`
+// the last row that exists; slot_off the place inside a slot, ATOMS the number
+// of 128-row pieces.
+template <int NR, int ATOMS, typename Base, typename Last>
+__device__ __forceinline__ bool scale_warp(const RaggedArgs& args, const RaggedTiles& tiles, int panels, int total,
+                                           int first, int stride, int groups, int valid_bytes, int pitch,
+                                           const uint8_t* scales, uint8_t* slots, int slot_off, ScaleBars& sb,
+                                           const volatile uint32_t* abort_flag, int lane, Base base, Last last) {
+    uint4 v[kAhead][NR];
+    ScaleCursor ld{first, 0, {}}, st{first, 0, {}};
+    if (first < total) ld.it = ragged_item<kTN>(args, tiles, panels, first);
+    auto fetch = [&](uint4 (&r)[NR]) {
+        if (ld.t >= total) return;
+        const int64_t r0 = base(ld.it), r1 = last(ld.it);
+#pragma unroll
+        for (int c = 0; c < NR; ++c) {
+            const int64_t row = min(r0 + c * 32 + lane, r1);
+            r[c] = __ldcg(reinterpret_cast<const uint4*>(scales + row * pitch + ld.g * 16));
         }
-        s[2 * b][r] = v.x;
-        s[2 * b + 1][r] = v.y;
+        if (++ld.g == groups) {
+            ld.g = 0;
+            ld.t += stride;
+            if (ld.t < total) ld.it = ragged_item<kTN>(args, tiles, panels, ld.t);
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) fetch(v[d]);
+    int slot = 0;
+    uint32_t ph = 0;
+    while (st.t < total) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+            if (st.t >= total) break;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(sb.empty + slot, ph ^ 1u, abort_flag))) return false;
+            uint8_t* dst = slots + slot * kSlot + slot_off + lane * 16;
+            const int left = valid_bytes - st.g * 16;  // bytes of this group inside K
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int b = left - 4 * q;
+                const uint32_t mask = b >= 4 ? 0xFFFFFFFFu : (b <= 0 ? 0u : (1u << (8 * b)) - 1u);
+#pragma unroll
+                for (int a = 0; a < ATOMS; ++a) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int i = a * 4 + c;
+                        w[c] = 0;
+                        if (i < NR) {
+                            const uint4& u = v[d][i < NR ? i : 0];
+                            w[c] = (q == 0 ? u.x : q == 1 ? u.y : q == 2 ? u.z : u.w) & mask;
+                        }
+                    }
+                    *reinterpret_cast<uint4*>(dst + (q * ATOMS + a) * 512) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            fetch(v[d]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(sb.full + slot), 0));
+            if (++slot == kSlots) {
+                slot = 0;
+                ph ^= 1u;
+            }
+            if (++st.g == groups) {
+                st.g = 0;
+                st.t += stride;
+            }
+        }
     }
+    return true;
 }
 
 template <bool NV>
-__global__ void __launch_bounds__(256) k_ragged_product_fp4(RaggedArgs a, Fp4Rows x, Fp4Rows w, int stride) {
-    __shared__ float sa[32][65], sb[32][65];
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    k_ragged_product_fp4(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tX,
+                         const uint8_t* w_scales, const uint8_t* x_scales, const int pitch, const RaggedArgs args) {
+    constexpr int S = kStages;
+    constexpr int kGroup = NV ? 256 : 512;  // elements under 16 scale bytes
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* slots = smem + S * kStage;
+    PairBars<S>& bars = *reinterpret_cast<PairBars<S>*>(slots + kSlots * kSlot);
+    ScaleBars& sb = *reinterpret_cast<ScaleBars*>(&bars + 1);
+    static_assert(sizeof(PairBars<S>) % 8 == 0 && sizeof(PairBars<S>) + sizeof(ScaleBars) <= 1024, "barriers");
+    RaggedTiles& tiles = *reinterpret_cast<RaggedTiles*>(slots + kSlots * kSlot + 1024);
+    volatile uint32_t* abort_flag = &bars.abort;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int panels = (args.N + 255) / 256;
+    const int steps = (args.K + kStep - 1) / kStep;
+    const int groups = (args.K + kGroup - 1) / kGroup;
     pdl_trigger();
-    pdl_wait();
-    int t = blockIdx.y, e = 0, r0 = 0, r1 = 0;
-    for (; e < a.E; ++e) {
-        const int2 g = group_rows(a, e);
-        const int n = (g.y - g.x + 63) / 64;
-        if (t < n) {
-            r0 = g.x + 64 * t;
-            r1 = min(g.y, r0 + 64);
-            break;
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(sb.full + i, 4);  // both scale warps of both CTAs
+            mbar_init(sb.empty + i, 1);
         }
-        t -= n;
+        mbar_init(sb.used, 1);
+        mbar_init(sb.used + 1, 1);
+        fence_mbar_init();
     }
-    if (e == a.E) return;
-    const int64_t n0 = static_cast<int64_t>(e) * a.N + blockIdx.x * 64;
-    const int64_t n1 = static_cast<int64_t>(e + 1) * a.N;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int k = 0; k < a.K; k += 32) {
-        stage<NV>(sa, x, r0, r1, k, a.K, stride);
-        stage<NV>(sb, w, n0, n1, k, a.K, stride);
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < 32; ++kk)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += sa[kk][ty + 16 * i] * sb[kk][tx + 16 * j];
-        __syncthreads();
-    }
-    const float g = (a.x_scale ? ld_dep(a.x_scale) : 1.0f) * (a.w_scale ? ld_dep(a.w_scale + e) : 1.0f);
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t r = r0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (r < r1 && n < n1)
-                out[r * a.ldo + n - static_cast<int64_t>(e) * a.N] =
-                    __float2bfloat16_rn(acc[i][j] * g * (a.row_scale ? ld_dep(a.row_scale + r) : 1.0f));
+    __syncwarp();
+    pair_start(bars, 1, warp);
+    if (warp == 2) ragged_tiles_build<kTN>(args, tiles, panels, lane);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the peer's barriers are initialised before any remote use
+    tc_fence_after();
+    const uint32_t tmem_base = bars.tmem;
+    const int total = tiles.first[args.E];
+    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    bool timed_out = false;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------ TMA producer
+            Ring r;
+            uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
+            for (int t = first; t < total && !timed_out; t += stride) {
+                const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
+                const int half = ((it.rows + 31) & ~31) / 2;  // token rows of each CTA
+                const int xrow = it.row + half * static_cast<int>(rank);
+                const int wrow = it.panel * 256 + 128 * static_cast<int>(rank);
+                for (int k = 0; k < steps; ++k) {
+                    if (!mbar_wait(bars.empty + r.s, r.ph ^ 1u, abort_flag)) {
+                        timed_out = true;
+                        break;
+                    }
+                    const uint32_t full = mapa_shared(smem_u32(bars.full + r.s), 0);
+                    uint8_t* st = smem + r.s * kStage;
+                    armed &= ~(1u << r.s);
+                    if (leader) mbar_arrive_expect_tx(bars.full + r.s, 2 * (kWBytes + half * 128));
+                    tma_load_3d_pair(st, &tW, k * 128, wrow, it.e, full);
+                    for (int j = 0; j < half; j += 16)
+                        tma_load_2d_pair(st + kWBytes + j * 128, &tX, k * 128, xrow + j, full);
+                    armed |= 1u << r.s;
+                    armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
+                    r.next<S>();
+                }
+            }
+            if ((timed_out || *abort_flag) && leader) {
+                *abort_flag = 1;
+                for (int i = 0; i < S; ++i)
+                    if (armed & (1u << i)) {
+                        volatile uint32_t never = 0;
+                        (void)mbar_wait(bars.full + i, (armed_par >> i) & 1u, &never);
+                    }
+            }
         }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            // ------------------------------------- scale copies, MMA issue
+            constexpr uint32_t idesc0 = idesc_e2m1_f32(256, 8, !NV) & ~(0x3Fu << 17);
+            Ring r;
+            Acc acc;
+            int slot = 0, buf = 0;
+            uint32_t slot_ph = 0, buf_ph = 0;
+            bool issued = false;
+            for (int t = first; t < total && !timed_out; t += stride) {
+                const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
+                const uint32_t n = (it.rows + 31) & ~31;
+                const uint32_t idesc = idesc0 | ((n >> 3) << 17);
+                if (!mbar_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
+                    timed_out = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem_base + static_cast<uint32_t>(acc.i * kTN);
+                uint32_t sc = 0;  // columns of this group's scales
+                for (int k = 0; k < steps; ++k) {
+                    if (NV || (k & 1) == 0) {
+                        // the MMAs that last read this buffer are complete
+                        if (!mbar_wait(sb.used + buf, buf_ph ^ 1u, abort_flag) ||
+                            !mbar_wait(sb.full + slot, slot_ph, abort_flag)) {
+                            timed_out = true;
+                            break;
+                        }
+                        tc_fence_after();
+                        sc = tmem_base + kScaleCol + static_cast<uint32_t>(buf) * kScaleCols;
+                        const uint32_t src = smem_u32(slots + slot * kSlot);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            tmem_copy_scales_pair(sc + q * 4, src + q * 512);
+                            tmem_copy_scales_pair(sc + 16 + q * 8, src + kSlotW + q * 1024);
+                            if (n > 128) tmem_copy_scales_pair(sc + 20 + q * 8, src + kSlotW + q * 1024 + 512);
+                        }
+                        issued = true;
+                        mma_commit_pair(sb.empty + slot, 0x3);
+                        if (++slot == kSlots) {
+                            slot = 0;
+                            slot_ph ^= 1u;
+                        }
+                    }
+                    if (!mbar_wait(bars.full + r.s, r.ph, abort_flag)) {
+                        timed_out = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t wa = smem_u32(smem + r.s * kStage), xa = wa + kWBytes;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {  // 4 x 64 elements of each 128-byte row
+                        if (k * kStep + kk * 64 >= args.K) break;
+                        const int word = NV ? kk : (k & 1) * 2 + kk / 2;
+                        const uint32_t byte = NV ? 0u : static_cast<uint32_t>(kk & 1) * 2u;
+                        mma_e2m1_pair<NV>(d, sdesc_sw128(wa + kk * 32), sdesc_sw128(xa + kk * 32),
+                                          idesc | (byte << 4) | (byte << 29), sc + word * 4, sc + 16 + word * 8,
+                                          (k | kk) != 0 ? 1u : 0u);
+                    }
+                    mma_commit_pair(bars.empty + r.s, 0x3);
+                    r.next<S>();
+                    if (NV || (k & 1) || k + 1 == steps) {
+                        mma_commit_pair(sb.used + buf, 0x1);
+                        buf ^= 1;
+                        if (buf == 0) buf_ph ^= 1u;
+                    }
+                }
+                if (timed_out) break;
+                mma_commit_pair(bars.tfull + acc.i, 0x3);
+                acc.next();
+            }
+            if ((timed_out || *abort_flag) && issued) {
+                *abort_flag = 1;
+                mma_commit_pair(&bars.drain, 0x1);
+                volatile uint32_t never = 0;
+                (void)mbar_wait(&bars.drain, 0, &never);
+            }
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------ weights' scales
+        timed_out = !scale_warp<4, 1>(
+            args, tiles, panels, total, first, stride, groups, args.K / (NV ? 16 : 32), pitch, w_scales, slots, 0, sb,
+            abort_flag, lane,
+            [&](const RaggedItem& it) {
+                return static_cast<int64_t>(it.e) * args.N + it.panel * 256 + 128 * static_cast<int>(rank);
+            },
+            [&](const RaggedItem& it) { return static_cast<int64_t>(it.e + 1) * args.N - 1; });
+    } else if (warp == 3) {
+        // ------------------------------------------------- tokens' scales
+        timed_out = !scale_warp<kTN / 32, 2>(
+            args, tiles, panels, total, first, stride, groups, args.K / (NV ? 16 : 32), pitch, x_scales, slots, kSlotW,
+            sb, abort_flag, lane, [&](const RaggedItem& it) { return static_cast<int64_t>(it.row); },
+            [&](const RaggedItem& it) { return static_cast<int64_t>(it.row + it.rows) - 1; });
+    } else {
+        // ------------------------------------------------------ epilogue
+        // A warp owns 32 of the CTA's 128 features (its tensor-memory lane
+        // quarter) and every other 32-token chunk.
+        const int q = warp & 3, odd = (warp - 4) >> 2;
+        const float gx = args.x_scale ? ld_dep(args.x_scale) : 1.0f;
+        Acc acc;
+        for (int t = first; t < total; t += stride) {
+            const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
+            const float scale = gx * (args.w_scale ? ld_dep(args.w_scale + it.e) : 1.0f);
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars.tfull + acc.i, acc.ph, abort_flag))) {
+                timed_out = true;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t taddr =
+                tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc.i * kTN);
+            const int n0 = it.panel * 256 + static_cast<int>(rank) * 128 + q * 32;
+#pragma unroll 1
+            for (int c = odd * 32; c < it.rows; c += 64) {
+                uint32_t v[32];
+                tmem_ld32(taddr + c, v);
+                tmem_ld_wait();
+                store_transposed<__nv_bfloat16>(args, v, it.row + c, it.rows - c, n0, lane, scale);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), 0));
+            acc.next();
+        }
+    }
+    if (timed_out) *abort_flag = 1;
+    if (timed_out && args.status) atomicOr(args.status, kRaggedTimeout);
+    pair_end(tmem_base, warp);
+}
+
+template <bool NV>
+cudaError_t launch_fp4(const RaggedArgs& a, const void* xq, const uint8_t* xs, const void* wq, const uint8_t* ws,
+                       int pitch, cudaStream_t st) {
+    static bool done[kMaxDevices] = {};
+    cudaError_t e = allow_smem(k_ragged_product_fp4<NV>, kSmem, done);
+    if (e != cudaSuccess) return e;
+    const uint64_t N = a.N, KB = a.K / 2, R = a.R, E = a.E;  // KB bytes of codes per row
+    CUtensorMap tW, tX;
+    const uint64_t wd[3] = {KB, N, E}, wst[2] = {KB, N * KB};
+    const uint64_t xd[2] = {KB, R}, xst[1] = {KB};
+    const uint32_t wb[3] = {128, 128, 1}, xb[2] = {128, 16};
+    if (!make_tensor_map(&tW, wq, 3, wd, wst, wb, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
+        !make_tensor_map(&tX, xq, 2, xd, xst, xb, CU_TENSOR_MAP_DATA_TYPE_UINT8))
+        return cudaErrorInvalidValue;
+    const int64_t items = (R / kTN + (R < E ? R : E)) * ((N + 255) / 256);  // at most
+    return launch_pdl(k_ragged_product_fp4<NV>, dim3(pair_grid(items)), dim3(kThreads), kSmem, st, tW, tX, ws, xs, pitch,
+                      a);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -120,12 +406,11 @@ extern "C" moe_status_t moe_grouped_gemm_fp4(int32_t fmt, int64_t R, int32_t N, 
     a.out = y;
     a.ldo = ldy;
     a.status = status;
-    const Fp4Rows x{static_cast<const uint8_t*>(x_codes), static_cast<const uint8_t*>(x_scales)};
-    const Fp4Rows w{static_cast<const uint8_t*>(w_codes), static_cast<const uint8_t*>(w_scales)};
-    const int stride = static_cast<int>(moe_fp4_scale_stride(fmt, K));
-    const dim3 grid((N + 63) / 64, static_cast<unsigned>(R / 64 + E));
+    const uint8_t* xs = static_cast<const uint8_t*>(x_scales);
+    const uint8_t* ws = static_cast<const uint8_t*>(w_scales);
+    const int pitch = static_cast<int>(moe_fp4_scale_stride(fmt, K));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = fmt == MOE_FP4_NV ? launch_pdl(k_ragged_product_fp4<true>, grid, dim3(256), 0, st, a, x, w, stride)
-                                      : launch_pdl(k_ragged_product_fp4<false>, grid, dim3(256), 0, st, a, x, w, stride);
+    const cudaError_t e = fmt == MOE_FP4_NV ? launch_fp4<true>(a, x_codes, xs, w_codes, ws, pitch, st)
+                                            : launch_fp4<false>(a, x_codes, xs, w_codes, ws, pitch, st);
     return e == cudaSuccess ? MOE_OK : set_last_error(MOE_ERR_CUDA, "4-bit grouped product: %s", cudaGetErrorString(e));
 }

@@ -403,6 +403,52 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, u
         : "memory");
 }
 
+// Instruction descriptor of tcgen05.mma kind::mxf4 / kind::mxf4nvf4: e2m1 A and
+// B (K = 64, both K-major) with block scales, fp32 accumulator:
+//   [4,6) B scale byte   [7,10) A format 1 = e2m1   [10,12) B format 1 = e2m1
+//   [17,23) N >> 3   [23] scale type 0 = ue4m3, 1 = ue8m0   [27,29) M >> 7
+//   [29,31) A scale byte
+__host__ __device__ constexpr uint32_t idesc_e2m1_f32(int M, int N, bool ue8m0) {
+    return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (ue8m0 ? 1u << 23 : 0u) |
+           (static_cast<uint32_t>(M >> 7) << 27);
+}
+
+// D[tmem of both CTAs] (+)= (A * scales) (B * scales)^T on 4-bit operands, M =
+// 256 across the pair, K = 64.  Scale words sit in tensor memory: word of row
+// r in lane r % 32, column r / 32 (in all four lane quarters); A's for the
+// CTA's own 128 rows, B's for all N rows in both CTAs.  MX: two power-of-two
+// bytes of the word per MMA, chosen by idesc; NV: four e4m3 bytes.
+template <bool NV>
+__device__ __forceinline__ void mma_e2m1_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t a_scale, uint32_t b_scale, uint32_t accumulate) {
+    if constexpr (NV)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                "r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                "r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
+            : "memory");
+}
+
+// Copies 32 rows of 16 bytes (512 contiguous bytes of shared memory) into four
+// columns of tensor memory, row r to lane r of every lane quarter, in both CTAs
+// of the pair (each from its own shared memory).
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint32_t saddr) {
+    // no swizzle: 8-row groups of 128 bytes
+    const uint64_t desc = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128u >> 4) << 16) |
+                          (static_cast<uint64_t>(128u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46);
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
 // Arrive once on the mbarrier at the same offset in every CTA of `mask` when
 // the pair's MMAs issued so far have completed.
 __device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint16_t mask) {

@@ -10,6 +10,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "internal.h"
 #include "ptx.cuh"
 
 namespace moe {
@@ -146,6 +147,87 @@ __device__ __forceinline__ void store_transposed(const RaggedArgs& a, const uint
         const float x1 = __uint_as_float(odd ? v[i + 1] : other) * g;
         if (in && i + odd < rows) *reinterpret_cast<uint32_t*>(out + i * a.ldo) = pack2(T(), x0, x1);
     }
+}
+
+// ---------------------------------------------------- CTA-pair pipelines --
+constexpr int kEpiWarps = 8;
+constexpr uint32_t kRaggedTimeout = 0x2u;  // MOE_DEVERR_TIMEOUT
+
+// The barriers of a pipeline of S stages and two accumulators, and what a
+// pair shares; the first 1 KB of shared memory.
+template <int S>
+struct PairBars {
+    uint64_t full[S], empty[S], tail[S], tfull[2], tempty[2], drain;
+    uint32_t tmem, abort;
+};
+
+struct Ring {  // stage and its parity
+    int s = 0;
+    uint32_t ph = 0;
+    template <int S>
+    __device__ __forceinline__ void next() {
+        if (++s == S) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
+struct Acc {  // accumulator and its parity
+    int i = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        i ^= 1;
+        if (i == 0) ph ^= 1u;
+    }
+};
+
+template <int S>
+__device__ __forceinline__ void pair_start(PairBars<S>& b, uint32_t full_count, int warp) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(b.full + i, full_count);
+            mbar_init(b.empty + i, 1);
+            mbar_init(b.tail + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(b.tfull + i, 1);
+            mbar_init(b.tempty + i, 2 * kEpiWarps);  // every epilogue warp of both CTAs
+        }
+        mbar_init(&b.drain, 1);
+        b.abort = 0;
+        fence_mbar_init();
+    }
+    // tensor memory is taken only once the kernels before this one have
+    // finished (and released theirs)
+    pdl_wait();
+    if (warp == 1) tmem_alloc_pair(&b.tmem, 512);
+}
+
+__device__ __forceinline__ void pair_end(uint32_t tmem_base, int warp) {
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, bool (&done)[kMaxDevices]) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (done[dev]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done[dev] = true;
+    return e;
+}
+
+inline unsigned pair_grid(int64_t items) {
+    const int64_t pairs = num_sms() / 2;
+    return static_cast<unsigned>(2 * (items < pairs ? items : pairs));
 }
 
 // ---------------------------------------------------------- 4-bit values --

@@ -44,8 +44,6 @@ constexpr int kBK = 64;                 // step of the sum
 constexpr int kOpBytes = 128 * kBK * 2; // one operand of one CTA and stage: 16 KB
 constexpr int kStage = 2 * kOpBytes;
 constexpr int kChunk = 64 * kBK * 2;    // a 64 x 64 box of an MN-major operand
-constexpr int kEpiWarps = 8;
-constexpr uint32_t kTimeout = 0x2u;
 constexpr uint32_t kTransA = 1u << 15, kTransB = 1u << 16;
 
 template <typename T>
@@ -60,67 +58,6 @@ struct Elem<__half> {  // operand formats 0 in bits [7,10) and [10,13)
     static constexpr int map = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     static constexpr uint32_t idesc = (1u << 4) | ((256u >> 4) << 24);
 };
-
-// The barriers of a pipeline of S stages and two accumulators, and what a
-// pair shares; the first 1 KB of shared memory.
-template <int S>
-struct PairBars {
-    uint64_t full[S], empty[S], tail[S], tfull[2], tempty[2], drain;
-    uint32_t tmem, abort;
-};
-
-struct Ring {  // stage and its parity
-    int s = 0;
-    uint32_t ph = 0;
-    template <int S>
-    __device__ __forceinline__ void next() {
-        if (++s == S) {
-            s = 0;
-            ph ^= 1u;
-        }
-    }
-};
-
-struct Acc {  // accumulator and its parity
-    int i = 0;
-    uint32_t ph = 0;
-    __device__ __forceinline__ void next() {
-        i ^= 1;
-        if (i == 0) ph ^= 1u;
-    }
-};
-
-template <int S>
-__device__ __forceinline__ void pair_start(PairBars<S>& b, uint32_t full_count, int warp) {
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < S; ++i) {
-            mbar_init(b.full + i, full_count);
-            mbar_init(b.empty + i, 1);
-            mbar_init(b.tail + i, 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(b.tfull + i, 1);
-            mbar_init(b.tempty + i, 2 * kEpiWarps);  // every epilogue warp of both CTAs
-        }
-        mbar_init(&b.drain, 1);
-        b.abort = 0;
-        fence_mbar_init();
-    }
-    // tensor memory is taken only once the kernels before this one have
-    // finished (and released theirs)
-    pdl_wait();
-    if (warp == 1) tmem_alloc_pair(&b.tmem, 512);
-}
-
-__device__ __forceinline__ void pair_end(uint32_t tmem_base, int warp) {
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc_pair(tmem_base, 512);
-    }
-}
 
 // ---------------------------------------------------------------- product --
 constexpr int kProdStages = 6;
@@ -275,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
         }
         if (timed_out) *abort_flag = 1;
     }
-    if (timed_out && args.status) atomicOr(args.status, kTimeout);
+    if (timed_out && args.status) atomicOr(args.status, kRaggedTimeout);
     pair_end(tmem_base, warp);
 }
 
@@ -521,27 +458,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
         if (lane == 0) bulk_wait_all();
         if (timed_out) *abort_flag = 1;
     }
-    if (timed_out && args.status) atomicOr(args.status, kTimeout);
+    if (timed_out && args.status) atomicOr(args.status, kRaggedTimeout);
     pair_end(tmem_base, warp);
 }
 
 // --------------------------------------------------------------- launches --
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes, bool (&done)[kMaxDevices]) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    if (done[dev]) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done[dev] = true;
-    return e;
-}
-
-unsigned pair_grid(int64_t items) {
-    const int64_t pairs = num_sms() / 2;
-    return static_cast<unsigned>(2 * (items < pairs ? items : pairs));
-}
-
 template <typename T, bool WT>
 cudaError_t launch_product(const RaggedArgs& a, const void* x, int64_t ldx, const void* w, cudaStream_t st) {
     static_assert(kProdSmem <= 232448, "shared memory budget");
