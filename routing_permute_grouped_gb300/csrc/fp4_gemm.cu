@@ -9,20 +9,23 @@
 //
 // Scales.  The MMA wants them in tensor memory as 32-bit words (four bytes
 // along K), word of row r in lane r % 32 and column r / 32.  In global memory
-// they are row-major.  Two warps of each CTA read 16 bytes of every row of the
-// tile (one warp the weights' rows, one the tokens'), so each lane holds four
-// words of rows i, i + 32, i + 64, i + 96: writing them word by word is the
-// transposition, four 16-byte shared-memory stores of 512 contiguous bytes per
-// 128 rows.  The MMA thread copies each 512-byte piece into four columns of
-// tensor memory (tcgen05.cp, broadcast to the four lane quarters) ahead of the
-// MMAs that use it.  Bytes past K are cleared on the way (they may hold
-// anything), rows past the operand repeat its last row and reach no stored
-// result.
+// they are row-major.  One warp of each CTA copies 16 bytes of every row of the
+// tile (a scale group: 512 elements of MX, 256 of NV) into shared memory with
+// cp.async, several groups ahead.  Two warps take the groups in turn: a lane
+// reads the four words of rows i, i + 32, i + 64, i + 96, and writing them word
+// by word is the transposition, 16-byte stores of 512 contiguous bytes.  The
+// MMA thread copies each 512-byte piece into four columns of tensor memory
+// (tcgen05.cp, broadcast to the four lane quarters) ahead of the MMAs that use
+// it.  Loading and laying out are separate warps because the arrive that
+// publishes a group waits for all of its warp's outstanding loads: one warp
+// doing both took 1.4 us per group.  Bytes past K are cleared on the way (they
+// may hold anything), rows past the operand repeat its last row and reach no
+// stored result.
 //
 // Tensor memory: two accumulators of 192 columns, two scale buffers of 48.
 //
 // Warp roles: warp 0 TMA producer, warp 1 tensor memory, scale copies and MMA
-// issue (even CTA), warp 2 weight scales, warp 3 token scales, warps 4..11
+// issue (even CTA), warp 2 scale loads, warps 3 and 4 scale layout, warps 5..12
 // epilogue.  Every wait is bounded, as in ragged_gemm.cu.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -47,111 +50,37 @@ constexpr int kSlotW = 4 * 512;           // four words of 128 weight rows
 constexpr int kSlot = kSlotW + 2 * 4 * 512;  // and of 256 token rows
 constexpr uint32_t kScaleCol = 2 * kTN;   // first tensor-memory column of the scale buffers
 constexpr uint32_t kScaleCols = 48;       // 4 words x (4 columns of A + 8 of B)
-constexpr int kThreads = 128 + 32 * kEpiWarps;
-constexpr int kAhead = 3;                 // scale groups in flight to a scale warp's registers
+constexpr int kRaw = 5;                   // scale groups as loaded, in shared memory
+constexpr int kRawRows = (4 + kTN / 32) * 512;  // 32-row pieces of 512 bytes: weights, tokens
+constexpr int kLayoutWarps = 2;
+constexpr int kThreads = 96 + 32 * (kLayoutWarps + kEpiWarps);
 
 struct ScaleBars {
-    uint64_t full[kSlots], empty[kSlots], used[2];
+    uint64_t raw_full[kRaw], raw_empty[kRaw];  // groups as loaded
+    uint64_t full[kSlots], empty[kSlots];      // groups laid out
+    uint64_t used[2];                          // the MMAs on a tensor-memory buffer are complete
 };
-constexpr int kSmem = 1024 + kStages * kStage + kSlots * kSlot + 1024 + static_cast<int>(sizeof(RaggedTiles));
+constexpr int kSmem = 1024 + kStages * kStage + kSlots * kSlot + kRaw * kRawRows + 1024 +
+                      static_cast<int>(sizeof(RaggedTiles));
 static_assert(kSmem <= 232448, "shared memory budget");
 static_assert(kStage % 1024 == 0, "swizzled tiles need 1024-byte alignment");
 static_assert(kScaleCol + 2 * kScaleCols <= 512, "tensor memory budget");
 
-// A work item's scale group g (16 bytes of every row), in the order in which
-// the pair takes them.
-struct ScaleCursor {
-    int t, g;
-    RaggedItem it;
-};
-
-// Reads scale groups of NR * 32 rows ahead of their use and lays them out for
-// the copies into tensor memory.  `base(item)` is the first row, `last(item)`
-// the last row that exists; slot_off the place inside a slot, ATOMS the number
-// of 128-row pieces.
-template <int NR, int ATOMS, typename Base, typename Last>
-__device__ __forceinline__ bool scale_warp(const RaggedArgs& args, const RaggedTiles& tiles, int panels, int total,
-                                           int first, int stride, int groups, int valid_bytes, int pitch,
-                                           const uint8_t* scales, uint8_t* slots, int slot_off, ScaleBars& sb,
-                                           const volatile uint32_t* abort_flag, int lane, Base base, Last last) {
-    uint4 v[kAhead][NR];
-    ScaleCursor ld{first, 0, {}}, st{first, 0, {}};
-    if (first < total) ld.it = ragged_item<kTN>(args, tiles, panels, first);
-    auto fetch = [&](uint4 (&r)[NR]) {
-        if (ld.t >= total) return;
-        const int64_t r0 = base(ld.it), r1 = last(ld.it);
-#pragma unroll
-        for (int c = 0; c < NR; ++c) {
-            const int64_t row = min(r0 + c * 32 + lane, r1);
-            r[c] = __ldcg(reinterpret_cast<const uint4*>(scales + row * pitch + ld.g * 16));
-        }
-        if (++ld.g == groups) {
-            ld.g = 0;
-            ld.t += stride;
-            if (ld.t < total) ld.it = ragged_item<kTN>(args, tiles, panels, ld.t);
-        }
-    };
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d) fetch(v[d]);
-    int slot = 0;
-    uint32_t ph = 0;
-    while (st.t < total) {
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d) {
-            if (st.t >= total) break;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(sb.empty + slot, ph ^ 1u, abort_flag))) return false;
-            uint8_t* dst = slots + slot * kSlot + slot_off + lane * 16;
-            const int left = valid_bytes - st.g * 16;  // bytes of this group inside K
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int b = left - 4 * q;
-                const uint32_t mask = b >= 4 ? 0xFFFFFFFFu : (b <= 0 ? 0u : (1u << (8 * b)) - 1u);
-#pragma unroll
-                for (int a = 0; a < ATOMS; ++a) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int i = a * 4 + c;
-                        w[c] = 0;
-                        if (i < NR) {
-                            const uint4& u = v[d][i < NR ? i : 0];
-                            w[c] = (q == 0 ? u.x : q == 1 ? u.y : q == 2 ? u.z : u.w) & mask;
-                        }
-                    }
-                    *reinterpret_cast<uint4*>(dst + (q * ATOMS + a) * 512) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
-            fetch(v[d]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(sb.full + slot), 0));
-            if (++slot == kSlots) {
-                slot = 0;
-                ph ^= 1u;
-            }
-            if (++st.g == groups) {
-                st.g = 0;
-                st.t += stride;
-            }
-        }
-    }
-    return true;
-}
-
 template <bool NV>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_ragged_product_fp4(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tX,
-                         const uint8_t* w_scales, const uint8_t* x_scales, const int pitch, const RaggedArgs args) {
+                         const __grid_constant__ CUtensorMap tX16, const uint8_t* w_scales, const uint8_t* x_scales, const int pitch, const RaggedArgs args) {
     constexpr int S = kStages;
     constexpr int kGroup = NV ? 256 : 512;  // elements under 16 scale bytes
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     uint8_t* slots = smem + S * kStage;
-    PairBars<S>& bars = *reinterpret_cast<PairBars<S>*>(slots + kSlots * kSlot);
+    uint8_t* raw = slots + kSlots * kSlot;
+    PairBars<S>& bars = *reinterpret_cast<PairBars<S>*>(raw + kRaw * kRawRows);
     ScaleBars& sb = *reinterpret_cast<ScaleBars*>(&bars + 1);
     static_assert(sizeof(PairBars<S>) % 8 == 0 && sizeof(PairBars<S>) + sizeof(ScaleBars) <= 1024, "barriers");
-    RaggedTiles& tiles = *reinterpret_cast<RaggedTiles*>(slots + kSlots * kSlot + 1024);
+    RaggedTiles& tiles = *reinterpret_cast<RaggedTiles*>(raw + kRaw * kRawRows + 1024);
     volatile uint32_t* abort_flag = &bars.abort;
 
     const int warp = threadIdx.x >> 5;
@@ -164,8 +93,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pdl_trigger();
     if (threadIdx.x == 32) {
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(sb.full + i, 4);  // both scale warps of both CTAs
+            mbar_init(sb.full + i, 2);  // a layout warp of either CTA
             mbar_init(sb.empty + i, 1);
+        }
+        for (int i = 0; i < kRaw; ++i) {
+            mbar_init(sb.raw_full + i, 32);  // every lane's copies
+            mbar_init(sb.raw_empty + i, 1);
         }
         mbar_init(sb.used, 1);
         mbar_init(sb.used + 1, 1);
@@ -203,8 +136,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     armed &= ~(1u << r.s);
                     if (leader) mbar_arrive_expect_tx(bars.full + r.s, 2 * (kWBytes + half * 128));
                     tma_load_3d_pair(st, &tW, k * 128, wrow, it.e, full);
-                    for (int j = 0; j < half; j += 16)
-                        tma_load_2d_pair(st + kWBytes + j * 128, &tX, k * 128, xrow + j, full);
+                    if (half == kTN / 2) {
+                        tma_load_2d_pair(st + kWBytes, &tX, k * 128, xrow, full);
+                    } else {
+                        for (int j = 0; j < half; j += 16)
+                            tma_load_2d_pair(st + kWBytes + j * 128, &tX16, k * 128, xrow + j, full);
+                    }
                     armed |= 1u << r.s;
                     armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
                     r.next<S>();
@@ -298,25 +235,91 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 2) {
-        // ------------------------------------------------ weights' scales
-        timed_out = !scale_warp<4, 1>(
-            args, tiles, panels, total, first, stride, groups, args.K / (NV ? 16 : 32), pitch, w_scales, slots, 0, sb,
-            abort_flag, lane,
-            [&](const RaggedItem& it) {
-                return static_cast<int64_t>(it.e) * args.N + it.panel * 256 + 128 * static_cast<int>(rank);
-            },
-            [&](const RaggedItem& it) { return static_cast<int64_t>(it.e + 1) * args.N - 1; });
-    } else if (warp == 3) {
-        // ------------------------------------------------- tokens' scales
-        timed_out = !scale_warp<kTN / 32, 2>(
-            args, tiles, panels, total, first, stride, groups, args.K / (NV ? 16 : 32), pitch, x_scales, slots, kSlotW,
-            sb, abort_flag, lane, [&](const RaggedItem& it) { return static_cast<int64_t>(it.row); },
-            [&](const RaggedItem& it) { return static_cast<int64_t>(it.row + it.rows) - 1; });
+        // ---------------------------------------------------- scale loads
+        int s = 0;
+        uint32_t ph = 0;
+        for (int t = first; t < total && !timed_out; t += stride) {
+            const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
+            const int64_t w_last = static_cast<int64_t>(it.e + 1) * args.N - 1;
+            const int64_t w0 = static_cast<int64_t>(it.e) * args.N + it.panel * 256 + 128 * static_cast<int>(rank);
+            const uint8_t* wp[4];
+            const uint8_t* xp[kTN / 32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) wp[c] = w_scales + min(w0 + c * 32 + lane, w_last) * pitch;
+#pragma unroll
+            for (int c = 0; c < kTN / 32; ++c)
+                xp[c] = x_scales + static_cast<int64_t>(it.row + min(c * 32 + lane, it.rows - 1)) * pitch;
+            for (int g = 0; g < groups; ++g) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(sb.raw_empty + s, ph ^ 1u, abort_flag))) {
+                    timed_out = true;
+                    break;
+                }
+                const uint32_t dst = smem_u32(raw + s * kRawRows) + lane * 16;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) cp_async_16(dst + c * 512, wp[c] + g * 16, 16);
+#pragma unroll
+                for (int c = 0; c < kTN / 32; ++c)
+                    if (c * 32 < it.rows) cp_async_16(dst + (4 + c) * 512, xp[c] + g * 16, 16);
+                cp_async_arrive(sb.raw_full + s);
+                if (++s == kRaw) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        // nothing of this CTA's shared memory may still be written to at exit
+        cp_async_commit();
+        cp_async_wait<0>();
+    } else if (warp < 3 + kLayoutWarps) {
+        // --------------------------------------------------- scale layout
+        // i counts this CTA's groups; a warp takes every kLayoutWarps-th.
+        int64_t i = 0;
+        const int mine = warp - 3;
+        const int valid = args.K / (NV ? 16 : 32);  // scale bytes of a row
+        for (int t = first; t < total && !timed_out; t += stride) {
+            for (int g = 0; g < groups; ++g, ++i) {
+                if (i % kLayoutWarps != mine) continue;
+                const int rs = static_cast<int>(i % kRaw), sl = static_cast<int>(i % kSlots);
+                const uint32_t rph = static_cast<uint32_t>(i / kRaw) & 1u, sph = static_cast<uint32_t>(i / kSlots) & 1u;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(sb.raw_full + rs, rph, abort_flag) &&
+                                                 mbar_wait(sb.empty + sl, sph ^ 1u, abort_flag))) {
+                    timed_out = true;
+                    break;
+                }
+                const uint4* src = reinterpret_cast<const uint4*>(raw + rs * kRawRows) + lane;
+                uint4 v[4 + kTN / 32];
+#pragma unroll
+                for (int c = 0; c < 4 + kTN / 32; ++c) v[c] = src[c * 32];
+                uint8_t* dst = slots + sl * kSlot + lane * 16;
+                const int left = valid - g * 16;  // bytes of this group inside K
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int b = left - 4 * q;
+                    const uint32_t mask = b >= 4 ? 0xFFFFFFFFu : (b <= 0 ? 0u : (1u << (8 * b)) - 1u);
+                    auto word = [&](int c) {
+                        if (c >= 4 + kTN / 32) return 0u;
+                        const uint4& u = v[c < 4 + kTN / 32 ? c : 0];
+                        return (q == 0 ? u.x : q == 1 ? u.y : q == 2 ? u.z : u.w) & mask;
+                    };
+                    *reinterpret_cast<uint4*>(dst + q * 512) = make_uint4(word(0), word(1), word(2), word(3));
+#pragma unroll
+                    for (int a = 0; a < 2; ++a)
+                        *reinterpret_cast<uint4*>(dst + kSlotW + (2 * q + a) * 512) =
+                            make_uint4(word(4 + 4 * a), word(5 + 4 * a), word(6 + 4 * a), word(7 + 4 * a));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(sb.raw_empty + rs);
+                    mbar_arrive_cluster(mapa_shared(smem_u32(sb.full + sl), 0));
+                }
+            }
+        }
     } else {
         // ------------------------------------------------------ epilogue
         // A warp owns 32 of the CTA's 128 features (its tensor-memory lane
         // quarter) and every other 32-token chunk.
-        const int q = warp & 3, odd = (warp - 4) >> 2;
+        const int q = warp & 3, odd = (warp - 3 - kLayoutWarps) >> 2;
         const float gx = args.x_scale ? ld_dep(args.x_scale) : 1.0f;
         Acc acc;
         for (int t = first; t < total; t += stride) {
@@ -355,16 +358,17 @@ cudaError_t launch_fp4(const RaggedArgs& a, const void* xq, const uint8_t* xs, c
     cudaError_t e = allow_smem(k_ragged_product_fp4<NV>, kSmem, done);
     if (e != cudaSuccess) return e;
     const uint64_t N = a.N, KB = a.K / 2, R = a.R, E = a.E;  // KB bytes of codes per row
-    CUtensorMap tW, tX;
+    CUtensorMap tW, tX, tX16;
     const uint64_t wd[3] = {KB, N, E}, wst[2] = {KB, N * KB};
     const uint64_t xd[2] = {KB, R}, xst[1] = {KB};
-    const uint32_t wb[3] = {128, 128, 1}, xb[2] = {128, 16};
+    const uint32_t wb[3] = {128, 128, 1}, xb[2] = {128, kTN / 2}, xb16[2] = {128, 16};
     if (!make_tensor_map(&tW, wq, 3, wd, wst, wb, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
-        !make_tensor_map(&tX, xq, 2, xd, xst, xb, CU_TENSOR_MAP_DATA_TYPE_UINT8))
+        !make_tensor_map(&tX, xq, 2, xd, xst, xb, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
+        !make_tensor_map(&tX16, xq, 2, xd, xst, xb16, CU_TENSOR_MAP_DATA_TYPE_UINT8))
         return cudaErrorInvalidValue;
     const int64_t items = (R / kTN + (R < E ? R : E)) * ((N + 255) / 256);  // at most
-    return launch_pdl(k_ragged_product_fp4<NV>, dim3(pair_grid(items)), dim3(kThreads), kSmem, st, tW, tX, ws, xs, pitch,
-                      a);
+    return launch_pdl(k_ragged_product_fp4<NV>, dim3(pair_grid(items)), dim3(kThreads), kSmem, st, tW, tX,
+                      tX16, ws, xs, pitch, a);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }

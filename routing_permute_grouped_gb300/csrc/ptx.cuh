@@ -507,6 +507,11 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// One arrival on the mbarrier (counted in its initial count) once this thread's
+// cp.async copies issued so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 // Makes this thread's completed generic-proxy shared-memory writes visible to
 // later async-proxy readers (TMA, tensor core).
 __device__ __forceinline__ void fence_proxy_async_smem() {
