@@ -157,9 +157,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
             // ------------------------------------- scale copies, MMA issue
+            // converged, one lane issuing, as in ragged_gemm.cu
             constexpr uint32_t idesc0 = idesc_e2m1_f32(256, 8, !NV) & ~(0x3Fu << 17);
+            const bool one = elect_one();
+            const uint64_t wd0 = sdesc_sw128(smem_u32(smem)), xd0 = sdesc_sw128(smem_u32(smem + kWBytes));
+            const uint64_t sd0 = sdesc_scales(smem_u32(slots));
             Ring r;
             Acc acc;
             int slot = 0, buf = 0;
@@ -169,7 +173,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
                 const uint32_t n = (it.rows + 31) & ~31;
                 const uint32_t idesc = idesc0 | ((n >> 3) << 17);
-                if (!mbar_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
+                if (!warp_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
                     timed_out = true;
                     break;
                 }
@@ -179,55 +183,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < steps; ++k) {
                     if (NV || (k & 1) == 0) {
                         // the MMAs that last read this buffer are complete
-                        if (!mbar_wait(sb.used + buf, buf_ph ^ 1u, abort_flag) ||
-                            !mbar_wait(sb.full + slot, slot_ph, abort_flag)) {
+                        if (!warp_wait(sb.used + buf, buf_ph ^ 1u, abort_flag) ||
+                            !warp_wait(sb.full + slot, slot_ph, abort_flag)) {
                             timed_out = true;
                             break;
                         }
                         tc_fence_after();
                         sc = tmem_base + kScaleCol + static_cast<uint32_t>(buf) * kScaleCols;
-                        const uint32_t src = smem_u32(slots + slot * kSlot);
+                        const uint64_t src = sd0 + static_cast<uint32_t>(slot) * (kSlot >> 4);
+                        if (one) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            tmem_copy_scales_pair(sc + q * 4, src + q * 512);
-                            tmem_copy_scales_pair(sc + 16 + q * 8, src + kSlotW + q * 1024);
-                            if (n > 128) tmem_copy_scales_pair(sc + 20 + q * 8, src + kSlotW + q * 1024 + 512);
+                            for (int q = 0; q < 4; ++q) {
+                                tmem_copy_scales_pair(sc + q * 4, src + q * (512 >> 4));
+                                tmem_copy_scales_pair(sc + 16 + q * 8, src + ((kSlotW + q * 1024) >> 4));
+                                if (n > 128)
+                                    tmem_copy_scales_pair(sc + 20 + q * 8, src + ((kSlotW + q * 1024 + 512) >> 4));
+                            }
+                            mma_commit_pair(sb.empty + slot, 0x3);
                         }
+                        __syncwarp();
                         issued = true;
-                        mma_commit_pair(sb.empty + slot, 0x3);
                         if (++slot == kSlots) {
                             slot = 0;
                             slot_ph ^= 1u;
                         }
                     }
-                    if (!mbar_wait(bars.full + r.s, r.ph, abort_flag)) {
+                    if (!warp_wait(bars.full + r.s, r.ph, abort_flag)) {
                         timed_out = true;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t wa = smem_u32(smem + r.s * kStage), xa = wa + kWBytes;
+                    const uint32_t at = static_cast<uint32_t>(r.s) * (kStage >> 4);
+                    const uint32_t sk = sc + (NV ? 0 : (k & 1) * 8), sk16 = sc + 16 + (NV ? 0 : (k & 1) * 16);
+                    const bool last = NV || (k & 1) || k + 1 == steps;
+                    if (one) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {  // 4 x 64 elements of each 128-byte row
-                        if (k * kStep + kk * 64 >= args.K) break;
-                        const int word = NV ? kk : (k & 1) * 2 + kk / 2;
-                        const uint32_t byte = NV ? 0u : static_cast<uint32_t>(kk & 1) * 2u;
-                        mma_e2m1_pair<NV>(d, sdesc_sw128(wa + kk * 32), sdesc_sw128(xa + kk * 32),
-                                          idesc | (byte << 4) | (byte << 29), sc + word * 4, sc + 16 + word * 8,
-                                          (k | kk) != 0 ? 1u : 0u);
+                        for (int kk = 0; kk < 4; ++kk) {  // 4 x 64 elements of each 128-byte row
+                            const int word = NV ? kk : kk / 2;
+                            const uint32_t byte = NV ? 0u : static_cast<uint32_t>(kk & 1) * 2u;
+                            if (k * kStep + kk * 64 < args.K)
+                                mma_e2m1_pair<NV>(d, wd0 + (at + kk * 2), xd0 + (at + kk * 2),
+                                                  idesc | (byte << 4) | (byte << 29), sk + word * 4, sk16 + word * 8,
+                                                  (k | kk) != 0 ? 1u : 0u);
+                        }
+                        mma_commit_pair(bars.empty + r.s, 0x3);
+                        if (last) mma_commit_pair(sb.used + buf, 0x1);
                     }
-                    mma_commit_pair(bars.empty + r.s, 0x3);
+                    __syncwarp();
                     r.next<S>();
-                    if (NV || (k & 1) || k + 1 == steps) {
-                        mma_commit_pair(sb.used + buf, 0x1);
+                    if (last) {
                         buf ^= 1;
                         if (buf == 0) buf_ph ^= 1u;
                     }
                 }
                 if (timed_out) break;
-                mma_commit_pair(bars.tfull + acc.i, 0x3);
+                if (one) mma_commit_pair(bars.tfull + acc.i, 0x3);
+                __syncwarp();
                 acc.next();
             }
-            if ((timed_out || *abort_flag) && issued) {
+            if ((timed_out || *abort_flag) && issued && one) {
                 *abort_flag = 1;
                 mma_commit_pair(&bars.drain, 0x1);
                 volatile uint32_t never = 0;

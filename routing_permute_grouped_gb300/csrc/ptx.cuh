@@ -42,6 +42,17 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
     return t;
 }
 
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // ------------------------------------------------------------- mbarrier --
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));
@@ -439,14 +450,16 @@ __device__ __forceinline__ void mma_e2m1_pair(uint32_t d_tmem, uint64_t adesc, u
             : "memory");
 }
 
-// Copies 32 rows of 16 bytes (512 contiguous bytes of shared memory) into four
-// columns of tensor memory, row r to lane r of every lane quarter, in both CTAs
-// of the pair (each from its own shared memory).
-__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint32_t saddr) {
-    // no swizzle: 8-row groups of 128 bytes
-    const uint64_t desc = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128u >> 4) << 16) |
-                          (static_cast<uint64_t>(128u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46);
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+// Shared-memory descriptor of 512 contiguous bytes, 32 rows of 16 (no swizzle,
+// 8-row groups of 128 bytes).
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128u >> 4) << 16) |
+           (static_cast<uint64_t>(128u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46);
+}
+// Copies such rows into four columns of tensor memory, row r to lane r of every
+// lane quarter, in both CTAs of the pair (each from its own shared memory).
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
 // Arrive once on the mbarrier at the same offset in every CTA of `mask` when

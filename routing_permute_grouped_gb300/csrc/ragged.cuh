@@ -161,6 +161,11 @@ struct PairBars {
     uint32_t tmem, abort;
 };
 
+// A bounded wait of a converged warp; the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort));
+}
+
 struct Ring {  // stage and its parity
     int s = 0;
     uint32_t ph = 0;

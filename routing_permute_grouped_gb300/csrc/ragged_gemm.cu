@@ -140,8 +140,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
             // ------------------------------------------------- MMA issuer
+            // The warp stays converged and one lane issues: descriptors and
+            // loop counters are then warp-uniform values, which the MMA takes
+            // as they are.
+            const bool one = elect_one();
+            const uint64_t wd0 = WT ? sdesc_sw128_mn(smem_u32(smem), kChunk) : sdesc_sw128(smem_u32(smem));
+            const uint64_t xd0 = sdesc_sw128(smem_u32(smem + kOpBytes));
+            constexpr uint32_t kWStep = (WT ? 2048 : 32) >> 4;  // 16 elements of the sum
             Ring r;
             Acc acc;
             bool issued = false;
@@ -149,32 +156,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
                 const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
                 const uint32_t n = (it.rows + 31) & ~31;
                 const uint32_t idesc = Elem<T>::idesc | ((n >> 3) << 17) | (WT ? kTransA : 0u);
-                if (!mbar_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
+                if (!warp_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
                     timed_out = true;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(acc.i * kTN);
                 for (int k = 0; k < steps; ++k) {
-                    if (!mbar_wait(bars.full + r.s, r.ph, abort_flag)) {
+                    if (!warp_wait(bars.full + r.s, r.ph, abort_flag)) {
                         timed_out = true;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t wa = smem_u32(smem + r.s * kStage), xa = wa + kOpBytes;
+                    const uint32_t at = static_cast<uint32_t>(r.s) * (kStage >> 4);
+                    if (one) {
 #pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk)
-                        mma_bf16_pair(d, WT ? sdesc_sw128_mn(wa + kk * 2048, kChunk) : sdesc_sw128(wa + kk * 32),
-                                      sdesc_sw128(xa + kk * 32), idesc, (k | kk) != 0 ? 1u : 0u);
+                        for (int kk = 0; kk < kBK / 16; ++kk)
+                            mma_bf16_pair(d, wd0 + (at + kk * kWStep), xd0 + (at + kk * 2), idesc,
+                                          (k | kk) != 0 ? 1u : 0u);
+                        mma_commit_pair(bars.empty + r.s, 0x3);
+                    }
+                    __syncwarp();
                     issued = true;
-                    mma_commit_pair(bars.empty + r.s, 0x3);
                     r.next<S>();
                 }
                 if (timed_out) break;
-                mma_commit_pair(bars.tfull + acc.i, 0x3);
+                if (one) mma_commit_pair(bars.tfull + acc.i, 0x3);
+                __syncwarp();
                 acc.next();
             }
-            if ((timed_out || *abort_flag) && issued) {
+            if ((timed_out || *abort_flag) && issued && one) {
                 *abort_flag = 1;
                 mma_commit_pair(&bars.drain, 0x1);
                 volatile uint32_t never = 0;
@@ -318,41 +329,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
             // ------------------------------------------------- MMA issuer
             constexpr uint32_t idesc = Elem<T>::idesc | ((256u >> 3) << 17) | kTransA | kTransB;
+            const bool one = elect_one();
+            const uint64_t ad0 = sdesc_sw128_mn(smem_u32(smem), kChunk);
+            const uint64_t bd0 = sdesc_sw128_mn(smem_u32(smem + kOpBytes), kChunk);
             Ring r;
             Acc acc;
             bool issued = false;
             for (int t = first; t < total && !timed_out; t += stride) {
                 const GradTile g = grad_tile(args, t);
                 if (g.rows == 0) continue;  // the epilogue writes zeros
-                if (!mbar_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
+                if (!warp_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
                     timed_out = true;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(acc.i * 256);
                 for (int k = 0; k < g.rows; k += kBK) {
-                    if (!mbar_wait(bars.full + r.s, r.ph, abort_flag)) {
+                    if (!warp_wait(bars.full + r.s, r.ph, abort_flag)) {
                         timed_out = true;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t aa = smem_u32(smem + r.s * kStage), ba = aa + kOpBytes;
-                    const int n16 = min(kBK, g.rows - k + 15) / 16;  // 16 rows per MMA
-                    for (int kk = 0; kk < n16; ++kk)
-                        mma_bf16_pair(d, sdesc_sw128_mn(aa + kk * 2048, kChunk), sdesc_sw128_mn(ba + kk * 2048, kChunk),
-                                      idesc, (k | kk) != 0 ? 1u : 0u);
+                    const uint32_t at = static_cast<uint32_t>(r.s) * (kStage >> 4);
+                    const int rest = g.rows - k;
+                    if (one) {
+#pragma unroll
+                        for (int kk = 0; kk < kBK / 16; ++kk)  // 16 rows per MMA
+                            if (kk * 16 < rest)
+                                mma_bf16_pair(d, ad0 + (at + kk * (2048 >> 4)), bd0 + (at + kk * (2048 >> 4)), idesc,
+                                              (k | kk) != 0 ? 1u : 0u);
+                        mma_commit_pair(bars.empty + r.s, 0x3);
+                    }
+                    __syncwarp();
                     issued = true;
-                    mma_commit_pair(bars.empty + r.s, 0x3);
                     r.next<S>();
                 }
                 if (timed_out) break;
-                mma_commit_pair(bars.tfull + acc.i, 0x3);
+                if (one) mma_commit_pair(bars.tfull + acc.i, 0x3);
+                __syncwarp();
                 acc.next();
             }
-            if ((timed_out || *abort_flag) && issued) {
+            if ((timed_out || *abort_flag) && issued && one) {
                 *abort_flag = 1;
                 mma_commit_pair(&bars.drain, 0x1);
                 volatile uint32_t never = 0;
