@@ -8,25 +8,24 @@
 // step of 256 elements is 128 bytes of each row.
 //
 // Scales.  The MMA wants them in tensor memory as 32-bit words (four bytes
-// along K), word of row r in lane r % 32 and column r / 32.  In global memory
-// they are row-major.  One warp of each CTA copies 16 bytes of every row of the
-// tile (a scale group: 512 elements of MX, 256 of NV) into shared memory with
-// cp.async, several groups ahead.  Two warps take the groups in turn: a lane
-// reads the four words of rows i, i + 32, i + 64, i + 96, and writing them word
-// by word is the transposition, 16-byte stores of 512 contiguous bytes.  The
-// MMA thread copies each 512-byte piece into four columns of tensor memory
-// (tcgen05.cp, broadcast to the four lane quarters) ahead of the MMAs that use
-// it.  Loading and laying out are separate warps because the arrive that
-// publishes a group waits for all of its warp's outstanding loads: one warp
-// doing both took 1.4 us per group.  Bytes past K are cleared on the way (they
-// may hold anything), rows past the operand repeat its last row and reach no
-// stored result.
+// along K), word of row r in lane r % 32 and column r / 32, repeated in the
+// four lane quarters.  In global memory they are row-major.  One warp of each
+// CTA copies 16 bytes of every row of the tile (a scale group: 512 elements of
+// MX, 256 of NV) into shared memory with cp.async, several groups ahead.  Four
+// warps, one per lane quarter, read a group back, lane l the four words of rows
+// l, l + 32, l + 64, ..., and store them to tensor memory word by word; the
+// transposition is a renaming of registers.  (Laying the words out in shared
+// memory for tcgen05.cp needs the writes published to the tensor core of both
+// CTAs: that cluster-scope release made a decode step over
+// 256 experts 884 us instead of 507.)
+// Bytes past K are cleared on the way (they may hold anything), rows past the
+// operand repeat its last row and reach no stored result.
 //
 // Tensor memory: two accumulators of 192 columns, two scale buffers of 48.
 //
-// Warp roles: warp 0 TMA producer, warp 1 tensor memory, scale copies and MMA
-// issue (even CTA), warp 2 scale loads, warps 3 and 4 scale layout, warps 5..12
-// epilogue.  Every wait is bounded, as in ragged_gemm.cu.
+// Warp roles: warp 0 TMA producer, warp 1 tensor memory and MMA issue (even
+// CTA), warp 2 scale loads, warps 4..7 scale layout, warps 8..15 epilogue.
+// Every wait is bounded, as in ragged_gemm.cu.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -45,42 +44,37 @@ constexpr int kStep = 256;                // step of the sum: 128 bytes of codes
 constexpr int kWBytes = 128 * 128;        // weight codes of one CTA and stage
 constexpr int kStage = kWBytes + kTN / 2 * 128;
 constexpr int kStages = 6;
-constexpr int kSlots = 4;                 // scale groups (16 bytes of every row) in shared memory
-constexpr int kSlotW = 4 * 512;           // four words of 128 weight rows
-constexpr int kSlot = kSlotW + 2 * 4 * 512;  // and of 256 token rows
 constexpr uint32_t kScaleCol = 2 * kTN;   // first tensor-memory column of the scale buffers
 constexpr uint32_t kScaleCols = 48;       // 4 words x (4 columns of A + 8 of B)
-constexpr int kRaw = 5;                   // scale groups as loaded, in shared memory
+constexpr int kRaw = 7;                   // scale groups in shared memory
 constexpr int kRawRows = (4 + kTN / 32) * 512;  // 32-row pieces of 512 bytes: weights, tokens
-constexpr int kLayoutWarps = 2;
-constexpr int kThreads = 96 + 32 * (kLayoutWarps + kEpiWarps);
+constexpr int kThreads = 256 + 32 * kEpiWarps;
 
 struct ScaleBars {
-    uint64_t raw_full[kRaw], raw_empty[kRaw];  // groups as loaded
-    uint64_t full[kSlots], empty[kSlots];      // groups laid out
-    uint64_t used[2];                          // the MMAs on a tensor-memory buffer are complete
+    uint64_t raw_full[kRaw], raw_empty[kRaw];  // groups in shared memory
+    uint64_t full[2], used[2];                 // tensor-memory buffers written, their MMAs complete
 };
-constexpr int kSmem = 1024 + kStages * kStage + kSlots * kSlot + kRaw * kRawRows + 1024 +
-                      static_cast<int>(sizeof(RaggedTiles));
+constexpr int kSmem =
+    1024 + kStages * kStage + kRaw * kRawRows + kEpiStage + 1024 + static_cast<int>(sizeof(RaggedTiles));
 static_assert(kSmem <= 232448, "shared memory budget");
 static_assert(kStage % 1024 == 0, "swizzled tiles need 1024-byte alignment");
 static_assert(kScaleCol + 2 * kScaleCols <= 512, "tensor memory budget");
 
 template <bool NV>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    k_ragged_product_fp4(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tX,
-                         const __grid_constant__ CUtensorMap tX16, const uint8_t* w_scales, const uint8_t* x_scales, const int pitch, const RaggedArgs args) {
+    k_ragged_product_fp4(const __grid_constant__ CUtensorMap tW, const __grid_constant__ RowMaps tX,
+                         const uint8_t* w_scales, const uint8_t* x_scales, const int pitch, const RaggedArgs args) {
     constexpr int S = kStages;
     constexpr int kGroup = NV ? 256 : 512;  // elements under 16 scale bytes
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint8_t* slots = smem + S * kStage;
-    uint8_t* raw = slots + kSlots * kSlot;
-    PairBars<S>& bars = *reinterpret_cast<PairBars<S>*>(raw + kRaw * kRawRows);
+    uint8_t* raw = smem + S * kStage;
+    uint8_t* sOut = raw + kRaw * kRawRows;
+    PairBars<S>& bars = *reinterpret_cast<PairBars<S>*>(sOut + kEpiStage);
     ScaleBars& sb = *reinterpret_cast<ScaleBars*>(&bars + 1);
     static_assert(sizeof(PairBars<S>) % 8 == 0 && sizeof(PairBars<S>) + sizeof(ScaleBars) <= 1024, "barriers");
-    RaggedTiles& tiles = *reinterpret_cast<RaggedTiles*>(raw + kRaw * kRawRows + 1024);
+    RaggedTiles& tiles = *reinterpret_cast<RaggedTiles*>(sOut + kEpiStage + 1024);
     volatile uint32_t* abort_flag = &bars.abort;
 
     const int warp = threadIdx.x >> 5;
@@ -92,16 +86,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int groups = (args.K + kGroup - 1) / kGroup;
     pdl_trigger();
     if (threadIdx.x == 32) {
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(sb.full + i, 2);  // a layout warp of either CTA
-            mbar_init(sb.empty + i, 1);
-        }
         for (int i = 0; i < kRaw; ++i) {
             mbar_init(sb.raw_full + i, 32);  // every lane's copies
-            mbar_init(sb.raw_empty + i, 1);
+            mbar_init(sb.raw_empty + i, 4);  // every layout warp
         }
-        mbar_init(sb.used, 1);
-        mbar_init(sb.used + 1, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sb.full + i, 8);  // every layout warp of both CTAs
+            mbar_init(sb.used + i, 1);
+        }
         fence_mbar_init();
     }
     __syncwarp();
@@ -136,12 +128,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     armed &= ~(1u << r.s);
                     if (leader) mbar_arrive_expect_tx(bars.full + r.s, 2 * (kWBytes + half * 128));
                     tma_load_3d_pair(st, &tW, k * 128, wrow, it.e, full);
-                    if (half == kTN / 2) {
-                        tma_load_2d_pair(st + kWBytes, &tX, k * 128, xrow, full);
-                    } else {
-                        for (int j = 0; j < half; j += 16)
-                            tma_load_2d_pair(st + kWBytes + j * 128, &tX16, k * 128, xrow + j, full);
-                    }
+                    load_rows(tX, st + kWBytes, k * 128, xrow, half, full);
                     armed |= 1u << r.s;
                     armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
                     r.next<S>();
@@ -158,16 +145,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         if (leader) {
-            // ------------------------------------- scale copies, MMA issue
+            // ------------------------------------------------- MMA issuer
             // converged, one lane issuing, as in ragged_gemm.cu
             constexpr uint32_t idesc0 = idesc_e2m1_f32(256, 8, !NV) & ~(0x3Fu << 17);
             const bool one = elect_one();
             const uint64_t wd0 = sdesc_sw128(smem_u32(smem)), xd0 = sdesc_sw128(smem_u32(smem + kWBytes));
-            const uint64_t sd0 = sdesc_scales(smem_u32(slots));
             Ring r;
             Acc acc;
-            int slot = 0, buf = 0;
-            uint32_t slot_ph = 0, buf_ph = 0;
+            Acc buf;  // scale buffer
             bool issued = false;
             for (int t = first; t < total && !timed_out; t += stride) {
                 const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
@@ -182,31 +167,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 uint32_t sc = 0;  // columns of this group's scales
                 for (int k = 0; k < steps; ++k) {
                     if (NV || (k & 1) == 0) {
-                        // the MMAs that last read this buffer are complete
-                        if (!warp_wait(sb.used + buf, buf_ph ^ 1u, abort_flag) ||
-                            !warp_wait(sb.full + slot, slot_ph, abort_flag)) {
+                        if (!warp_wait(sb.full + buf.i, buf.ph, abort_flag)) {
                             timed_out = true;
                             break;
                         }
-                        tc_fence_after();
-                        sc = tmem_base + kScaleCol + static_cast<uint32_t>(buf) * kScaleCols;
-                        const uint64_t src = sd0 + static_cast<uint32_t>(slot) * (kSlot >> 4);
-                        if (one) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                tmem_copy_scales_pair(sc + q * 4, src + q * (512 >> 4));
-                                tmem_copy_scales_pair(sc + 16 + q * 8, src + ((kSlotW + q * 1024) >> 4));
-                                if (n > 128)
-                                    tmem_copy_scales_pair(sc + 20 + q * 8, src + ((kSlotW + q * 1024 + 512) >> 4));
-                            }
-                            mma_commit_pair(sb.empty + slot, 0x3);
-                        }
-                        __syncwarp();
-                        issued = true;
-                        if (++slot == kSlots) {
-                            slot = 0;
-                            slot_ph ^= 1u;
-                        }
+                        sc = tmem_base + kScaleCol + static_cast<uint32_t>(buf.i) * kScaleCols;
                     }
                     if (!warp_wait(bars.full + r.s, r.ph, abort_flag)) {
                         timed_out = true;
@@ -227,14 +192,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                                   (k | kk) != 0 ? 1u : 0u);
                         }
                         mma_commit_pair(bars.empty + r.s, 0x3);
-                        if (last) mma_commit_pair(sb.used + buf, 0x1);
+                        if (last) mma_commit_pair(sb.used + buf.i, 0x3);
                     }
                     __syncwarp();
                     r.next<S>();
-                    if (last) {
-                        buf ^= 1;
-                        if (buf == 0) buf_ph ^= 1u;
-                    }
+                    issued = true;
+                    if (last) buf.next();
                 }
                 if (timed_out) break;
                 if (one) mma_commit_pair(bars.tfull + acc.i, 0x3);
@@ -284,61 +247,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // nothing of this CTA's shared memory may still be written to at exit
         cp_async_commit();
         cp_async_wait<0>();
-    } else if (warp < 3 + kLayoutWarps) {
+    } else if (warp == 3) {
+        // no part: the layout warps start at a multiple of four
+    } else if (warp < 8) {
         // --------------------------------------------------- scale layout
-        // i counts this CTA's groups; a warp takes every kLayoutWarps-th.
-        int64_t i = 0;
-        const int mine = warp - 3;
+        constexpr int kPieces = 4 + kTN / 32;
         const int valid = args.K / (NV ? 16 : 32);  // scale bytes of a row
+        const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        int s = 0;
+        uint32_t ph = 0;
+        Acc buf;
         for (int t = first; t < total && !timed_out; t += stride) {
-            for (int g = 0; g < groups; ++g, ++i) {
-                if (i % kLayoutWarps != mine) continue;
-                const int rs = static_cast<int>(i % kRaw), sl = static_cast<int>(i % kSlots);
-                const uint32_t rph = static_cast<uint32_t>(i / kRaw) & 1u, sph = static_cast<uint32_t>(i / kSlots) & 1u;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(sb.raw_full + rs, rph, abort_flag) &&
-                                                 mbar_wait(sb.empty + sl, sph ^ 1u, abort_flag))) {
+            for (int g = 0; g < groups; ++g) {
+                if (!warp_wait(sb.raw_full + s, ph, abort_flag)) {
                     timed_out = true;
                     break;
                 }
-                const uint4* src = reinterpret_cast<const uint4*>(raw + rs * kRawRows) + lane;
-                uint4 v[4 + kTN / 32];
+                const uint4* src = reinterpret_cast<const uint4*>(raw + s * kRawRows) + lane;
+                uint4 v[kPieces];
 #pragma unroll
-                for (int c = 0; c < 4 + kTN / 32; ++c) v[c] = src[c * 32];
-                uint8_t* dst = slots + sl * kSlot + lane * 16;
+                for (int c = 0; c < kPieces; ++c) v[c] = src[c * 32];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sb.raw_empty + s);
+                if (++s == kRaw) {
+                    s = 0;
+                    ph ^= 1u;
+                }
                 const int left = valid - g * 16;  // bytes of this group inside K
+                if (left < 16) {
+                    uint32_t m[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int b = left - 4 * q;
+                        m[q] = b >= 4 ? 0xFFFFFFFFu : (b <= 0 ? 0u : (1u << (8 * b)) - 1u);
+                    }
+#pragma unroll
+                    for (int c = 0; c < kPieces; ++c)
+                        v[c] = make_uint4(v[c].x & m[0], v[c].y & m[1], v[c].z & m[2], v[c].w & m[3]);
+                }
+                uint32_t a[16], b[32];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int b = left - 4 * q;
-                    const uint32_t mask = b >= 4 ? 0xFFFFFFFFu : (b <= 0 ? 0u : (1u << (8 * b)) - 1u);
                     auto word = [&](int c) {
-                        if (c >= 4 + kTN / 32) return 0u;
-                        const uint4& u = v[c < 4 + kTN / 32 ? c : 0];
-                        return (q == 0 ? u.x : q == 1 ? u.y : q == 2 ? u.z : u.w) & mask;
+                        const uint4& u = v[c];
+                        return q == 0 ? u.x : q == 1 ? u.y : q == 2 ? u.z : u.w;
                     };
-                    *reinterpret_cast<uint4*>(dst + q * 512) = make_uint4(word(0), word(1), word(2), word(3));
 #pragma unroll
-                    for (int a = 0; a < 2; ++a)
-                        *reinterpret_cast<uint4*>(dst + kSlotW + (2 * q + a) * 512) =
-                            make_uint4(word(4 + 4 * a), word(5 + 4 * a), word(6 + 4 * a), word(7 + 4 * a));
+                    for (int c = 0; c < 4; ++c) a[4 * q + c] = word(c);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) b[8 * q + c] = c < kTN / 32 ? word(4 + (c < kTN / 32 ? c : 0)) : 0u;
                 }
-                fence_proxy_async_smem();
+                // the MMAs that last read this buffer are complete
+                if (!warp_wait(sb.used + buf.i, buf.ph ^ 1u, abort_flag)) {
+                    timed_out = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t dst = tmem_base + quarter + kScaleCol + static_cast<uint32_t>(buf.i) * kScaleCols;
+                tmem_st16(dst, a);
+                tmem_st32(dst + 16, b);
+                tmem_st_wait();
+                // the words are in tensor memory; the MMA side reads nothing
+                // else of this warp's, so the arrive releases nothing
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(sb.raw_empty + rs);
-                    mbar_arrive_cluster(mapa_shared(smem_u32(sb.full + sl), 0));
-                }
+                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(sb.full + buf.i), 0));
+                buf.next();
             }
         }
     } else {
         // ------------------------------------------------------ epilogue
         // A warp owns 32 of the CTA's 128 features (its tensor-memory lane
         // quarter) and every other 32-token chunk.
-        const int q = warp & 3, odd = (warp - 3 - kLayoutWarps) >> 2;
+        const int q = warp & 3, odd = (warp - 8) >> 2;
         const float gx = args.x_scale ? ld_dep(args.x_scale) : 1.0f;
         Acc acc;
         for (int t = first; t < total; t += stride) {
             const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
             const float scale = gx * (args.w_scale ? ld_dep(args.w_scale + it.e) : 1.0f);
+            float gate[kTN / 64];  // the factor of this lane's token of each chunk
+#pragma unroll
+            for (int i = 0; i < kTN / 64; ++i) {
+                const int token = odd * 32 + i * 64 + lane;
+                gate[i] = args.row_scale && token < it.rows ? ld_dep(args.row_scale + it.row + token) * scale : scale;
+            }
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars.tfull + acc.i, acc.ph, abort_flag))) {
                 timed_out = true;
                 break;
@@ -347,12 +339,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t taddr =
                 tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc.i * kTN);
             const int n0 = it.panel * 256 + static_cast<int>(rank) * 128 + q * 32;
-#pragma unroll 1
-            for (int c = odd * 32; c < it.rows; c += 64) {
-                uint32_t v[32];
-                tmem_ld32(taddr + c, v);
-                tmem_ld_wait();
-                store_transposed<__nv_bfloat16>(args, v, it.row + c, it.rows - c, n0, lane, scale);
+#pragma unroll
+            for (int i = 0; i < kTN / 64; ++i) {
+                const int c = odd * 32 + i * 64;
+                if (c < it.rows)
+                    store_transposed<__nv_bfloat16>(args, taddr + c, it.row + c, it.rows - c, n0, lane, gate[i],
+                                                    sOut + (warp - 8) * 2048);
             }
             tc_fence_before();
             __syncwarp();
@@ -372,17 +364,16 @@ cudaError_t launch_fp4(const RaggedArgs& a, const void* xq, const uint8_t* xs, c
     cudaError_t e = allow_smem(k_ragged_product_fp4<NV>, kSmem, done);
     if (e != cudaSuccess) return e;
     const uint64_t N = a.N, KB = a.K / 2, R = a.R, E = a.E;  // KB bytes of codes per row
-    CUtensorMap tW, tX, tX16;
+    CUtensorMap tW;
+    RowMaps tX;
     const uint64_t wd[3] = {KB, N, E}, wst[2] = {KB, N * KB};
-    const uint64_t xd[2] = {KB, R}, xst[1] = {KB};
-    const uint32_t wb[3] = {128, 128, 1}, xb[2] = {128, kTN / 2}, xb16[2] = {128, 16};
+    const uint32_t wb[3] = {128, 128, 1};
     if (!make_tensor_map(&tW, wq, 3, wd, wst, wb, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
-        !make_tensor_map(&tX, xq, 2, xd, xst, xb, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
-        !make_tensor_map(&tX16, xq, 2, xd, xst, xb16, CU_TENSOR_MAP_DATA_TYPE_UINT8))
+        !make_row_maps(&tX, xq, R, KB, KB, 128, CU_TENSOR_MAP_DATA_TYPE_UINT8))
         return cudaErrorInvalidValue;
     const int64_t items = (R / kTN + (R < E ? R : E)) * ((N + 255) / 256);  // at most
     return launch_pdl(k_ragged_product_fp4<NV>, dim3(pair_grid(items)), dim3(kThreads), kSmem, st, tW, tX,
-                      tX16, ws, xs, pitch, a);
+                      ws, xs, pitch, a);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }

@@ -127,30 +127,54 @@ __device__ __forceinline__ uint32_t pack2(__half, float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Epilogue of the products for 32 accumulator columns (tokens row .. row + 31
-// of which `rows` are stored): lane l of the warp holds feature n0 + l of
-// every token.  Neighbouring lanes exchange halves, so that one 4-byte store
-// per lane writes two features of the even or the odd token: each store
-// instruction covers 64 contiguous bytes of two output rows.
+// Epilogue of the products for 32 accumulator columns: tokens row .. row + 31
+// (`rows` of them are stored) times the warp's 32 features n0 .. n0 + 31, one
+// feature per tensor-memory lane.  The accumulator is read in matrix-fragment
+// form, packed to 16 bits and stored transposed through stmatrix into 2 KB of
+// shared memory ([token][64 bytes], 16-byte pieces permuted against bank
+// conflicts), from where each lane stores 16 bytes: an instruction writes 64
+// contiguous bytes of eight output rows.  (Exchanging neighbours' halves by
+// shuffles and storing 4 bytes per lane took 2.4 times the instructions and
+// held short sums up.)  gate is the factor of token row + lane.
 template <typename T>
-__device__ __forceinline__ void store_transposed(const RaggedArgs& a, const uint32_t (&v)[32], int row, int rows,
-                                                 int n0, int lane, float scale) {
-    const int odd = lane & 1;
-    const float gate = a.row_scale && lane < rows ? ld_dep(a.row_scale + row + lane) * scale : scale;
-    T* out = static_cast<T*>(a.out) + (static_cast<int64_t>(row) + odd) * a.ldo + n0 + lane - odd;
-    const bool in = n0 + lane < a.N;
+__device__ __forceinline__ void store_transposed(const RaggedArgs& a, uint32_t taddr, int row, int rows, int n0,
+                                                 int lane, float gate, uint8_t* stage) {
+    uint32_t v[2][16];
+    tmem_ld_frag32(taddr, v[0]);
+    tmem_ld_frag32(taddr + (16u << 16), v[1]);
+    tmem_ld_wait();
+    __syncwarp();  // the previous chunk has left the staging buffer
+    const uint32_t sbase = smem_u32(stage);
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[i] : v[i + 1], 1);
-        const float g = __shfl_sync(0xFFFFFFFFu, gate, i + odd);
-        const float x0 = __uint_as_float(odd ? other : v[i]) * g;
-        const float x1 = __uint_as_float(odd ? v[i + 1] : other) * g;
-        if (in && i + odd < rows) *reinterpret_cast<uint32_t*>(out + i * a.ldo) = pack2(T(), x0, x1);
+    for (int j = 0; j < 4; ++j) {  // 8 tokens
+        const float g0 = __shfl_sync(0xFFFFFFFFu, gate, 8 * j + 2 * (lane & 3));
+        const float g1 = __shfl_sync(0xFFFFFFFFu, gate, 8 * j + 2 * (lane & 3) + 1);
+        uint32_t p[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {  // 8 features
+            const uint32_t* u = v[f >> 1] + 4 * j + 2 * (f & 1);
+            p[f] = pack2(T(), __uint_as_float(u[0]) * g0, __uint_as_float(u[1]) * g1);
+        }
+        const int token = 8 * j + (lane & 7), f = lane >> 3;
+        stmatrix_x4_trans(sbase + token * 64 + ((f ^ ((token >> 1) & 3)) << 4), p[0], p[1], p[2], p[3]);
+    }
+    __syncwarp();
+    const int f = lane & 3;
+    if (n0 + 8 * f < a.N) {
+        T* out = static_cast<T*>(a.out) + static_cast<int64_t>(row) * a.ldo + n0 + 8 * f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int token = 8 * i + (lane >> 2);
+            if (token < rows)
+                *reinterpret_cast<uint4*>(out + token * a.ldo) =
+                    *reinterpret_cast<const uint4*>(stage + token * 64 + ((f ^ ((token >> 1) & 3)) << 4));
+        }
     }
 }
 
 // ---------------------------------------------------- CTA-pair pipelines --
 constexpr int kEpiWarps = 8;
+constexpr int kEpiStage = kEpiWarps * 2048;  // the products' store staging
 constexpr uint32_t kRaggedTimeout = 0x2u;  // MOE_DEVERR_TIMEOUT
 
 // The barriers of a pipeline of S stages and two accumulators, and what a
@@ -207,6 +231,30 @@ __device__ __forceinline__ void pair_start(PairBars<S>& b, uint32_t full_count, 
     // finished (and released theirs)
     pdl_wait();
     if (warp == 1) tmem_alloc_pair(&b.tmem, 512);
+}
+
+// Token rows as TMA boxes of 128, 64, 32 and 16 rows of 128 bytes, so that any
+// multiple of 16 rows takes the fewest loads.
+struct RowMaps {
+    CUtensorMap box[4];
+};
+__device__ __forceinline__ void load_rows(const RowMaps& m, uint8_t* dst, int x, int row, int rows, uint32_t full) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (rows & (128 >> i)) {
+            tma_load_2d_pair(dst, m.box + i, x, row, full);
+            dst += (128 >> i) * 128;
+            row += 128 >> i;
+        }
+}
+inline bool make_row_maps(RowMaps* m, const void* x, uint64_t rows, uint64_t cols, uint64_t stride, uint32_t box_cols,
+                          int dtype) {
+    const uint64_t dims[2] = {cols, rows}, strides[1] = {stride};
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t box[2] = {box_cols, 128u >> i};
+        if (!make_tensor_map(m->box + i, x, 2, dims, strides, box, dtype)) return false;
+    }
+    return true;
 }
 
 __device__ __forceinline__ void pair_end(uint32_t tmem_base, int warp) {

@@ -61,19 +61,20 @@ struct Elem<__half> {  // operand formats 0 in bits [7,10) and [10,13)
 
 // ---------------------------------------------------------------- product --
 constexpr int kProdStages = 6;
-constexpr int kProdSmem = 1024 + kProdStages * kStage + 1024 + static_cast<int>(sizeof(RaggedTiles));
+constexpr int kProdSmem = 1024 + kProdStages * kStage + kEpiStage + 1024 + static_cast<int>(sizeof(RaggedTiles));
 
 template <typename T, bool WT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps, 1)
-    k_ragged_product(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tX,
-                     const __grid_constant__ CUtensorMap tX16, const RaggedArgs args) {
+    k_ragged_product(const __grid_constant__ CUtensorMap tW, const __grid_constant__ RowMaps tX,
+                     const RaggedArgs args) {
     constexpr int S = kProdStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    PairBars<S>& bars = *reinterpret_cast<PairBars<S>*>(smem + S * kStage);
+    uint8_t* sOut = smem + S * kStage;
+    PairBars<S>& bars = *reinterpret_cast<PairBars<S>*>(sOut + kEpiStage);
     static_assert(sizeof(PairBars<S>) <= 1024, "barriers");
-    RaggedTiles& tiles = *reinterpret_cast<RaggedTiles*>(smem + S * kStage + 1024);
+    RaggedTiles& tiles = *reinterpret_cast<RaggedTiles*>(sOut + kEpiStage + 1024);
     volatile uint32_t* abort_flag = &bars.abort;
 
     const int warp = threadIdx.x >> 5;
@@ -119,12 +120,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
                     } else {
                         tma_load_3d_pair(st, &tW, k * kBK, wrow, it.e, full);
                     }
-                    if (half == 128) {
-                        tma_load_2d_pair(st + kOpBytes, &tX, k * kBK, xrow, full);
-                    } else {
-                        for (int j = 0; j < half; j += 16)
-                            tma_load_2d_pair(st + kOpBytes + j * 128, &tX16, k * kBK, xrow + j, full);
-                    }
+                    load_rows(tX, st + kOpBytes, k * kBK, xrow, half, full);
                     armed |= 1u << r.s;
                     armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
                     r.next<S>();
@@ -200,6 +196,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
         Acc acc;
         for (int t = first; t < total; t += stride) {
             const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
+            float gate[kTN / 64];  // this lane's token of each chunk, read while the MMAs run
+#pragma unroll
+            for (int i = 0; i < kTN / 64; ++i) {
+                const int token = odd * 32 + i * 64 + lane;
+                gate[i] = args.row_scale && token < it.rows ? ld_dep(args.row_scale + it.row + token) : 1.0f;
+            }
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars.tfull + acc.i, acc.ph, abort_flag))) {
                 timed_out = true;
                 break;
@@ -208,12 +210,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
             const uint32_t taddr =
                 tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc.i * kTN);
             const int n0 = it.panel * 256 + static_cast<int>(rank) * 128 + q * 32;
-#pragma unroll 1
-            for (int c = odd * 32; c < it.rows; c += 64) {
-                uint32_t v[32];
-                tmem_ld32(taddr + c, v);
-                tmem_ld_wait();
-                store_transposed<T>(args, v, it.row + c, it.rows - c, n0, lane, 1.0f);
+#pragma unroll
+            for (int i = 0; i < kTN / 64; ++i) {
+                const int c = odd * 32 + i * 64;
+                if (c < it.rows)
+                    store_transposed<T>(args, taddr + c, it.row + c, it.rows - c, n0, lane, gate[i],
+                                        sOut + (warp - 2) * 2048);
             }
             // the reads are complete: the MMA side reads nothing stored here
             tc_fence_before();
@@ -490,18 +492,17 @@ cudaError_t launch_product(const RaggedArgs& a, const void* x, int64_t ldx, cons
     cudaError_t e = allow_smem(k_ragged_product<T, WT>, kProdSmem, done);
     if (e != cudaSuccess) return e;
     const uint64_t N = a.N, K = a.K, R = a.R, E = a.E;
-    CUtensorMap tW, tX, tX16;
+    CUtensorMap tW;
+    RowMaps tX;
     const uint64_t wd[3] = {WT ? N : K, WT ? K : N, E};
     const uint64_t ws[2] = {wd[0] * 2, N * K * 2};
     const uint32_t wb[3] = {64, WT ? 64u : 128u, 1};
-    const uint64_t xd[2] = {K, R}, xs[1] = {static_cast<uint64_t>(ldx) * 2};
-    const uint32_t xb[2] = {64, 128}, xb16[2] = {64, 16};
-    if (!make_tensor_map(&tW, w, 3, wd, ws, wb, Elem<T>::map) || !make_tensor_map(&tX, x, 2, xd, xs, xb, Elem<T>::map) ||
-        !make_tensor_map(&tX16, x, 2, xd, xs, xb16, Elem<T>::map))
+    if (!make_tensor_map(&tW, w, 3, wd, ws, wb, Elem<T>::map) ||
+        !make_row_maps(&tX, x, R, K, static_cast<uint64_t>(ldx) * 2, 64, Elem<T>::map))
         return cudaErrorInvalidValue;
     const int64_t items = (R / kTN + (R < E ? R : E)) * ((N + 255) / 256);  // at most
     return launch_pdl(k_ragged_product<T, WT>, dim3(pair_grid(items)), dim3(64 + 32 * kEpiWarps), kProdSmem, st, tW, tX,
-                      tX16, a);
+                      a);
 }
 
 template <typename T>
