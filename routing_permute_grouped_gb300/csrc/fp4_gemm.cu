@@ -60,8 +60,8 @@ static_assert(kSmem <= 232448, "shared memory budget");
 static_assert(kStage % 1024 == 0, "swizzled tiles need 1024-byte alignment");
 static_assert(kScaleCol + 2 * kScaleCols <= 512, "tensor memory budget");
 
-template <bool NV>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <bool NV, int P>
+__global__ void __launch_bounds__(kThreads, 1)
     k_ragged_product_fp4(const __grid_constant__ CUtensorMap tW, const __grid_constant__ RowMaps tX,
                          const uint8_t* w_scales, const uint8_t* x_scales, const int pitch, const RaggedArgs args) {
     constexpr int S = kStages;
@@ -80,8 +80,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const bool leader = rank == 0;
-    const int panels = (args.N + 255) / 256;
+    const bool leader = (rank & 1) == 0;
+    const uint32_t lead = rank & ~1u;  // the pair's even CTA
+    const int panels = (args.N + 255) / 256 / P;  // sets of P
     const int steps = (args.K + kStep - 1) / kStep;
     const int groups = (args.K + kGroup - 1) / kGroup;
     pdl_trigger();
@@ -97,7 +98,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
     __syncwarp();
-    pair_start(bars, 1, warp);
+    pair_start(bars, 1, P, warp);
     if (warp == 2) ragged_tiles_build<kTN>(args, tiles, panels, lane);
     tc_fence_before();
     __syncthreads();
@@ -105,43 +106,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = bars.tmem;
     const int total = tiles.first[args.E];
-    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    const int first = blockIdx.x / (2 * P), stride = gridDim.x / (2 * P);
     bool timed_out = false;
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ------------------------------------------------ TMA producer
-            Ring r;
-            uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
-            for (int t = first; t < total && !timed_out; t += stride) {
-                const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
-                const int half = ((it.rows + 31) & ~31) / 2;  // token rows of each CTA
-                const int xrow = it.row + half * static_cast<int>(rank);
-                const int wrow = it.panel * 256 + 128 * static_cast<int>(rank);
-                for (int k = 0; k < steps; ++k) {
-                    if (!mbar_wait(bars.empty + r.s, r.ph ^ 1u, abort_flag)) {
-                        timed_out = true;
-                        break;
-                    }
-                    const uint32_t full = mapa_shared(smem_u32(bars.full + r.s), 0);
-                    uint8_t* st = smem + r.s * kStage;
-                    armed &= ~(1u << r.s);
+        // ---------------------------------------------------- TMA producer
+        // converged, one lane issuing, as the MMA warp
+        const bool one = elect_one();
+        Ring r;
+        uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
+        for (int t = first; t < total && !timed_out; t += stride) {
+            const RaggedItem it = ragged_item<kTN, P>(args, tiles, panels, t);
+            const int half = ((it.rows + 31) & ~31) / 2;  // token rows of each CTA
+            const int xrow = it.row + half * static_cast<int>(rank & 1);
+            const int wrow = it.panel * 256 + 128 * static_cast<int>(rank);  // the pairs' panels follow each other
+            for (int k = 0; k < steps; ++k) {
+                if (!warp_wait(bars.empty + r.s, r.ph ^ 1u, abort_flag)) {
+                    timed_out = true;
+                    break;
+                }
+                const uint32_t full = mapa_shared(smem_u32(bars.full + r.s), lead);
+                uint8_t* st = smem + r.s * kStage;
+                armed &= ~(1u << r.s);
+                if (one) {
                     if (leader) mbar_arrive_expect_tx(bars.full + r.s, 2 * (kWBytes + half * 128));
                     tma_load_3d_pair(st, &tW, k * 128, wrow, it.e, full);
-                    load_rows(tX, st + kWBytes, k * 128, xrow, half, full);
-                    armed |= 1u << r.s;
-                    armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
-                    r.next<S>();
+                    load_rows<P>(tX, st + kWBytes, k * 128, xrow, half, full, rank);
                 }
+                __syncwarp();
+                armed |= 1u << r.s;
+                armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
+                r.next<S>();
             }
-            if ((timed_out || *abort_flag) && leader) {
-                *abort_flag = 1;
-                for (int i = 0; i < S; ++i)
-                    if (armed & (1u << i)) {
-                        volatile uint32_t never = 0;
-                        (void)mbar_wait(bars.full + i, (armed_par >> i) & 1u, &never);
-                    }
-            }
+        }
+        if ((timed_out || *abort_flag) && leader && lane == 0) {
+            *abort_flag = 1;
+            for (int i = 0; i < S; ++i)
+                if (armed & (1u << i)) {
+                    volatile uint32_t never = 0;
+                    (void)mbar_wait(bars.full + i, (armed_par >> i) & 1u, &never);
+                }
         }
     } else if (warp == 1) {
         if (leader) {
@@ -149,13 +153,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // converged, one lane issuing, as in ragged_gemm.cu
             constexpr uint32_t idesc0 = idesc_e2m1_f32(256, 8, !NV) & ~(0x3Fu << 17);
             const bool one = elect_one();
+            constexpr uint16_t kAll = (1u << (2 * P)) - 1;                   // a stage is read by every pair
+            const uint16_t both = static_cast<uint16_t>(0x3u << lead);      // this pair
             const uint64_t wd0 = sdesc_sw128(smem_u32(smem)), xd0 = sdesc_sw128(smem_u32(smem + kWBytes));
             Ring r;
             Acc acc;
             Acc buf;  // scale buffer
             bool issued = false;
             for (int t = first; t < total && !timed_out; t += stride) {
-                const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
+                const RaggedItem it = ragged_item<kTN, P>(args, tiles, panels, t);
                 const uint32_t n = (it.rows + 31) & ~31;
                 const uint32_t idesc = idesc0 | ((n >> 3) << 17);
                 if (!warp_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
@@ -191,8 +197,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                                   idesc | (byte << 4) | (byte << 29), sk + word * 4, sk16 + word * 8,
                                                   (k | kk) != 0 ? 1u : 0u);
                         }
-                        mma_commit_pair(bars.empty + r.s, 0x3);
-                        if (last) mma_commit_pair(sb.used + buf.i, 0x3);
+                        mma_commit_pair(bars.empty + r.s, kAll);
+                        if (last) mma_commit_pair(sb.used + buf.i, both);
                     }
                     __syncwarp();
                     r.next<S>();
@@ -200,13 +206,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (last) buf.next();
                 }
                 if (timed_out) break;
-                if (one) mma_commit_pair(bars.tfull + acc.i, 0x3);
+                if (one) mma_commit_pair(bars.tfull + acc.i, both);
                 __syncwarp();
                 acc.next();
             }
             if ((timed_out || *abort_flag) && issued && one) {
                 *abort_flag = 1;
-                mma_commit_pair(&bars.drain, 0x1);
+                mma_commit_pair(&bars.drain, static_cast<uint16_t>(1u << rank));
                 volatile uint32_t never = 0;
                 (void)mbar_wait(&bars.drain, 0, &never);
             }
@@ -216,7 +222,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int s = 0;
         uint32_t ph = 0;
         for (int t = first; t < total && !timed_out; t += stride) {
-            const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
+            const RaggedItem it = ragged_item<kTN, P>(args, tiles, panels, t);
             const int64_t w_last = static_cast<int64_t>(it.e + 1) * args.N - 1;
             const int64_t w0 = static_cast<int64_t>(it.e) * args.N + it.panel * 256 + 128 * static_cast<int>(rank);
             const uint8_t* wp[4];
@@ -311,7 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // else of this warp's, so the arrive releases nothing
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(sb.full + buf.i), 0));
+                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(sb.full + buf.i), lead));
                 buf.next();
             }
         }
@@ -323,7 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float gx = args.x_scale ? ld_dep(args.x_scale) : 1.0f;
         Acc acc;
         for (int t = first; t < total; t += stride) {
-            const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
+            const RaggedItem it = ragged_item<kTN, P>(args, tiles, panels, t);
             const float scale = gx * (args.w_scale ? ld_dep(args.w_scale + it.e) : 1.0f);
             float gate[kTN / 64];  // the factor of this lane's token of each chunk
 #pragma unroll
@@ -348,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), 0));
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), lead));
             acc.next();
         }
     }
@@ -357,23 +363,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pair_end(tmem_base, warp);
 }
 
-template <bool NV>
+template <bool NV, int P>
 cudaError_t launch_fp4(const RaggedArgs& a, const void* xq, const uint8_t* xs, const void* wq, const uint8_t* ws,
                        int pitch, cudaStream_t st) {
-    static bool done[kMaxDevices] = {};
-    cudaError_t e = allow_smem(k_ragged_product_fp4<NV>, kSmem, done);
-    if (e != cudaSuccess) return e;
+    static int resident[kMaxDevices] = {};
     const uint64_t N = a.N, KB = a.K / 2, R = a.R, E = a.E;  // KB bytes of codes per row
     CUtensorMap tW;
     RowMaps tX;
     const uint64_t wd[3] = {KB, N, E}, wst[2] = {KB, N * KB};
     const uint32_t wb[3] = {128, 128, 1};
     if (!make_tensor_map(&tW, wq, 3, wd, wst, wb, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
-        !make_row_maps(&tX, xq, R, KB, KB, 128, CU_TENSOR_MAP_DATA_TYPE_UINT8))
+        !make_row_maps<P>(&tX, xq, R, KB, KB, 128, CU_TENSOR_MAP_DATA_TYPE_UINT8))
         return cudaErrorInvalidValue;
-    const int64_t items = (R / kTN + (R < E ? R : E)) * ((N + 255) / 256);  // at most
-    return launch_pdl(k_ragged_product_fp4<NV>, dim3(pair_grid(items)), dim3(kThreads), kSmem, st, tW, tX,
-                      ws, xs, pitch, a);
+    const int64_t items = (R / kTN + (R < E ? R : E)) * ((N + 255) / 256 / P);  // at most
+    return launch_clusters<P>(k_ragged_product_fp4<NV, P>, items, kThreads, kSmem, resident, st, tW, tX, ws, xs, pitch,
+                              a);
+}
+
+// Clusters of two pairs when the panels come in sets of two, as in ragged_gemm.cu.
+template <bool NV>
+cudaError_t product_fp4(const RaggedArgs& a, const void* xq, const uint8_t* xs, const void* wq, const uint8_t* ws,
+                        int pitch, cudaStream_t st) {
+    return ((a.N + 255) / 256) % 2 == 0 ? launch_fp4<NV, 2>(a, xq, xs, wq, ws, pitch, st)
+                                        : launch_fp4<NV, 1>(a, xq, xs, wq, ws, pitch, st);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -419,7 +431,7 @@ extern "C" moe_status_t moe_grouped_gemm_fp4(int32_t fmt, int64_t R, int32_t N, 
     const uint8_t* ws = static_cast<const uint8_t*>(w_scales);
     const int pitch = static_cast<int>(moe_fp4_scale_stride(fmt, K));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = fmt == MOE_FP4_NV ? launch_fp4<true>(a, x_codes, xs, w_codes, ws, pitch, st)
-                                            : launch_fp4<false>(a, x_codes, xs, w_codes, ws, pitch, st);
+    const cudaError_t e = fmt == MOE_FP4_NV ? product_fp4<true>(a, x_codes, xs, w_codes, ws, pitch, st)
+                                            : product_fp4<false>(a, x_codes, xs, w_codes, ws, pitch, st);
     return e == cudaSuccess ? MOE_OK : set_last_error(MOE_ERR_CUDA, "4-bit grouped product: %s", cudaGetErrorString(e));
 }

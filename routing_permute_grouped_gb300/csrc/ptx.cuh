@@ -379,6 +379,18 @@ __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorM
 }
 
 
+// The same load written to the same place of every CTA of the cluster in
+// `mask`; each destination's bytes are counted on the mbarrier of the CTA of its
+// own pair that has the parity of the one given.
+__device__ __forceinline__ void tma_load_2d_pair_multicast(void* smem_dst, const CUtensorMap* tm, int32_t x0,
+                                                           int32_t y0, uint32_t bar_cluster_addr, uint16_t mask) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+        ".cta_group::2 [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x0), "r"(y0), "r"(bar_cluster_addr), "h"(mask)
+        : "memory");
+}
+
 // Gather four rows r0..r3 of a 2D tensor (box {64 columns, 1 row}) into 4
 // consecutive 128-byte rows of shared memory, completing on an mbarrier that
 // may live in the peer CTA of the pair.

@@ -63,8 +63,8 @@ struct Elem<__half> {  // operand formats 0 in bits [7,10) and [10,13)
 constexpr int kProdStages = 6;
 constexpr int kProdSmem = 1024 + kProdStages * kStage + kEpiStage + 1024 + static_cast<int>(sizeof(RaggedTiles));
 
-template <typename T, bool WT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps, 1)
+template <typename T, bool WT, int P>
+__global__ void __launch_bounds__(64 + 32 * kEpiWarps, 1)
     k_ragged_product(const __grid_constant__ CUtensorMap tW, const __grid_constant__ RowMaps tX,
                      const RaggedArgs args) {
     constexpr int S = kProdStages;
@@ -80,11 +80,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const bool leader = rank == 0;
-    const int panels = (args.N + 255) / 256;
+    const bool leader = (rank & 1) == 0;
+    const uint32_t lead = rank & ~1u;  // the pair's even CTA
+    const int panels = (args.N + 255) / 256 / P;  // sets of P
     const int steps = (args.K + kBK - 1) / kBK;
     pdl_trigger();
-    pair_start(bars, 1, warp);
+    pair_start(bars, 1, P, warp);
     if (warp == 2) ragged_tiles_build<kTN>(args, tiles, panels, lane);
     tc_fence_before();
     __syncthreads();
@@ -92,27 +93,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
     tc_fence_after();
     const uint32_t tmem_base = bars.tmem;
     const int total = tiles.first[args.E];
-    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    const int first = blockIdx.x / (2 * P), stride = gridDim.x / (2 * P);
     bool timed_out = false;
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ------------------------------------------------ TMA producer
-            Ring r;
-            uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
-            for (int t = first; t < total && !timed_out; t += stride) {
-                const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
-                const int half = ((it.rows + 31) & ~31) / 2;  // token rows of each CTA
-                const int xrow = it.row + half * static_cast<int>(rank);
-                const int wrow = it.panel * 256 + 128 * static_cast<int>(rank);
-                for (int k = 0; k < steps; ++k) {
-                    if (!mbar_wait(bars.empty + r.s, r.ph ^ 1u, abort_flag)) {
-                        timed_out = true;
-                        break;
-                    }
-                    const uint32_t full = mapa_shared(smem_u32(bars.full + r.s), 0);
-                    uint8_t* st = smem + r.s * kStage;
-                    armed &= ~(1u << r.s);
+        // ---------------------------------------------------- TMA producer
+        // converged, one lane issuing, as the MMA warp
+        const bool one = elect_one();
+        Ring r;
+        uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
+        for (int t = first; t < total && !timed_out; t += stride) {
+            const RaggedItem it = ragged_item<kTN, P>(args, tiles, panels, t);
+            const int half = ((it.rows + 31) & ~31) / 2;  // token rows of each CTA
+            const int xrow = it.row + half * static_cast<int>(rank & 1);
+            const int wrow = it.panel * 256 + 128 * static_cast<int>(rank);  // the pairs' panels follow each other
+            for (int k = 0; k < steps; ++k) {
+                if (!warp_wait(bars.empty + r.s, r.ph ^ 1u, abort_flag)) {
+                    timed_out = true;
+                    break;
+                }
+                const uint32_t full = mapa_shared(smem_u32(bars.full + r.s), lead);
+                uint8_t* st = smem + r.s * kStage;
+                armed &= ~(1u << r.s);
+                if (one) {
                     if (leader) mbar_arrive_expect_tx(bars.full + r.s, 2 * (kOpBytes + half * 128));
                     if constexpr (WT) {
                         tma_load_3d_pair(st, &tW, wrow, k * kBK, it.e, full);
@@ -120,20 +123,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
                     } else {
                         tma_load_3d_pair(st, &tW, k * kBK, wrow, it.e, full);
                     }
-                    load_rows(tX, st + kOpBytes, k * kBK, xrow, half, full);
-                    armed |= 1u << r.s;
-                    armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
-                    r.next<S>();
+                    load_rows<P>(tX, st + kOpBytes, k * kBK, xrow, half, full, rank);
                 }
+                __syncwarp();
+                armed |= 1u << r.s;
+                armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
+                r.next<S>();
             }
-            if ((timed_out || *abort_flag) && leader) {
-                *abort_flag = 1;
-                for (int i = 0; i < S; ++i)
-                    if (armed & (1u << i)) {
-                        volatile uint32_t never = 0;
-                        (void)mbar_wait(bars.full + i, (armed_par >> i) & 1u, &never);
-                    }
-            }
+        }
+        if ((timed_out || *abort_flag) && leader && lane == 0) {
+            *abort_flag = 1;
+            for (int i = 0; i < S; ++i)
+                if (armed & (1u << i)) {
+                    volatile uint32_t never = 0;
+                    (void)mbar_wait(bars.full + i, (armed_par >> i) & 1u, &never);
+                }
         }
     } else if (warp == 1) {
         if (leader) {
@@ -142,6 +146,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
             // loop counters are then warp-uniform values, which the MMA takes
             // as they are.
             const bool one = elect_one();
+            constexpr uint16_t kAll = (1u << (2 * P)) - 1;                   // a stage is read by every pair
+            const uint16_t both = static_cast<uint16_t>(0x3u << lead);      // this pair
             const uint64_t wd0 = WT ? sdesc_sw128_mn(smem_u32(smem), kChunk) : sdesc_sw128(smem_u32(smem));
             const uint64_t xd0 = sdesc_sw128(smem_u32(smem + kOpBytes));
             constexpr uint32_t kWStep = (WT ? 2048 : 32) >> 4;  // 16 elements of the sum
@@ -149,7 +155,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
             Acc acc;
             bool issued = false;
             for (int t = first; t < total && !timed_out; t += stride) {
-                const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
+                const RaggedItem it = ragged_item<kTN, P>(args, tiles, panels, t);
                 const uint32_t n = (it.rows + 31) & ~31;
                 const uint32_t idesc = Elem<T>::idesc | ((n >> 3) << 17) | (WT ? kTransA : 0u);
                 if (!warp_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
@@ -170,20 +176,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
                         for (int kk = 0; kk < kBK / 16; ++kk)
                             mma_bf16_pair(d, wd0 + (at + kk * kWStep), xd0 + (at + kk * 2), idesc,
                                           (k | kk) != 0 ? 1u : 0u);
-                        mma_commit_pair(bars.empty + r.s, 0x3);
+                        mma_commit_pair(bars.empty + r.s, kAll);
                     }
                     __syncwarp();
                     issued = true;
                     r.next<S>();
                 }
                 if (timed_out) break;
-                if (one) mma_commit_pair(bars.tfull + acc.i, 0x3);
+                if (one) mma_commit_pair(bars.tfull + acc.i, both);
                 __syncwarp();
                 acc.next();
             }
             if ((timed_out || *abort_flag) && issued && one) {
                 *abort_flag = 1;
-                mma_commit_pair(&bars.drain, 0x1);
+                mma_commit_pair(&bars.drain, static_cast<uint16_t>(1u << rank));
                 volatile uint32_t never = 0;
                 (void)mbar_wait(&bars.drain, 0, &never);
             }
@@ -195,7 +201,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
         const int q = warp & 3, odd = (warp - 2) >> 2;
         Acc acc;
         for (int t = first; t < total; t += stride) {
-            const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
+            const RaggedItem it = ragged_item<kTN, P>(args, tiles, panels, t);
             float gate[kTN / 64];  // this lane's token of each chunk, read while the MMAs run
 #pragma unroll
             for (int i = 0; i < kTN / 64; ++i) {
@@ -220,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
             // the reads are complete: the MMA side reads nothing stored here
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), 0));
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), lead));
             acc.next();
         }
         if (timed_out) *abort_flag = 1;
@@ -239,21 +245,23 @@ struct GradTile {
     int row, rows;   // the group's rows
 };
 
+// Item t of a cluster of P pairs, which take P neighbouring column tiles.
+template <int P>
 __device__ __forceinline__ GradTile grad_tile(const RaggedArgs& a, int t) {
-    const int nt = (a.N + 255) / 256, mt = (a.K + 255) / 256;
+    const int nt = (a.N + 255) / 256 / P, mt = (a.K + 255) / 256;
     GradTile g;
     g.e = t / (mt * nt);
     const int r = t - g.e * mt * nt;
     g.m = r / nt * 256;
-    g.n = r % nt * 256;
+    g.n = r % nt * 256 * P;
     const int2 rows = group_rows(a, g.e);
     g.row = rows.x;
     g.rows = rows.y - rows.x;
     return g;
 }
 
-template <typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps, 1)
+template <typename T, int P>
+__global__ void __launch_bounds__(96 + 32 * kEpiWarps, 1)
     k_ragged_wgrad(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB,
                    const __grid_constant__ CUtensorMap tOut, const RaggedArgs args) {
     constexpr int S = kGradStages;
@@ -267,67 +275,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const bool leader = rank == 0;
+    const bool leader = (rank & 1) == 0;
+    const uint32_t lead = rank & ~1u;  // the pair's even CTA
     pdl_trigger();
-    pair_start(bars, 2, warp);  // a stage is full when both CTAs say so (and its bytes have landed)
+    pair_start(bars, 2, P, warp);  // a stage is full when both CTAs say so (and its bytes have landed)
     tc_fence_before();
     __syncthreads();
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = bars.tmem;
-    const int total = args.E * ((args.N + 255) / 256) * ((args.K + 255) / 256);
-    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    const int total = args.E * ((args.N + 255) / 256 / P) * ((args.K + 255) / 256);
+    const int first = blockIdx.x / (2 * P), stride = gridDim.x / (2 * P);
     bool timed_out = false;
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ------------------------------------------------ TMA producer
-            Ring r;
-            uint32_t armed = 0, armed_par = 0, tails = 0, tail_par = 0, tail_ph = 0;
-            for (int t = first; t < total && !timed_out; t += stride) {
-                const GradTile g = grad_tile(args, t);
-                const int ac = g.m + 128 * static_cast<int>(rank), bc = g.n + 128 * static_cast<int>(rank);
-                for (int k = 0; k < g.rows; k += kBK) {
-                    if (!mbar_wait(bars.empty + r.s, r.ph ^ 1u, abort_flag)) {
-                        timed_out = true;
-                        break;
-                    }
-                    uint8_t* st = smem + r.s * kStage;
-                    const uint32_t bit = 1u << r.s;
-                    armed &= ~bit;
-                    tails &= ~bit;
-                    uint32_t bar;
-                    if (g.rows - k >= kBK) {
-                        bar = mapa_shared(smem_u32(bars.full + r.s), 0);
-                        if (leader)
-                            mbar_arrive_expect_tx(bars.full + r.s, 2 * kStage);
-                        else
-                            mbar_arrive_cluster_relaxed(bar);
-                        armed |= bit;
-                        armed_par = (armed_par & ~bit) | (r.ph << r.s);
-                    } else {  // the zeroing warp hands this stage on
-                        bar = mapa_shared(smem_u32(bars.tail + r.s), rank);
+        // ---------------------------------------------------- TMA producer
+        const bool one = elect_one();
+        Ring r;
+        uint32_t armed = 0, armed_par = 0, tails = 0, tail_par = 0, tail_ph = 0;
+        for (int t = first; t < total && !timed_out; t += stride) {
+            const GradTile g = grad_tile<P>(args, t);
+            const int ac = g.m + 128 * static_cast<int>(rank & 1), bc = g.n + 128 * static_cast<int>(rank);
+            for (int k = 0; k < g.rows; k += kBK) {
+                if (!warp_wait(bars.empty + r.s, r.ph ^ 1u, abort_flag)) {
+                    timed_out = true;
+                    break;
+                }
+                uint8_t* st = smem + r.s * kStage;
+                const uint32_t bit = 1u << r.s;
+                // a tail's bytes go to the CTA's own barrier: the zeroing warp
+                // hands that stage on
+                const bool tail = g.rows - k < kBK;
+                armed &= ~bit;
+                tails &= ~bit;
+                if (tail) {
+                    tails |= bit;
+                    tail_par = (tail_par & ~bit) | (tail_ph & bit);
+                    tail_ph ^= bit;
+                } else {
+                    armed |= bit;
+                    armed_par = (armed_par & ~bit) | (r.ph << r.s);
+                }
+                const uint32_t bar = tail ? mapa_shared(smem_u32(bars.tail + r.s), rank)
+                                          : mapa_shared(smem_u32(bars.full + r.s), lead);
+                const int row = g.row + k;
+                if (one) {
+                    if (tail)
                         mbar_arrive_expect_tx(bars.tail + r.s, kStage);
-                        tails |= bit;
-                        tail_par = (tail_par & ~bit) | (tail_ph & bit);
-                        tail_ph ^= bit;
+                    else if (leader)
+                        mbar_arrive_expect_tx(bars.full + r.s, 2 * kStage);
+                    else
+                        mbar_arrive_cluster_relaxed(bar);
+                    if constexpr (P > 1) {  // the pairs share A: each loads 64 of the CTA's columns for both
+                        const int c = static_cast<int>(rank >> 1);
+                        tma_load_2d_pair_multicast(st + c * kChunk, &tA, ac + 64 * c, row, bar,
+                                                   static_cast<uint16_t>(0x5u << (rank & 1)));
+                    } else {
+                        tma_load_2d_pair(st, &tA, ac, row, bar);
+                        tma_load_2d_pair(st + kChunk, &tA, ac + 64, row, bar);
                     }
-                    const int row = g.row + k;
-                    tma_load_2d_pair(st, &tA, ac, row, bar);
-                    tma_load_2d_pair(st + kChunk, &tA, ac + 64, row, bar);
                     tma_load_2d_pair(st + kOpBytes, &tB, bc, row, bar);
                     tma_load_2d_pair(st + kOpBytes + kChunk, &tB, bc + 64, row, bar);
-                    r.next<S>();
                 }
+                __syncwarp();
+                r.next<S>();
             }
-            if (timed_out || *abort_flag) {
-                *abort_flag = 1;
-                volatile uint32_t never = 0;
-                for (int i = 0; i < S; ++i) {
-                    if (leader && (armed & (1u << i)))
-                        (void)mbar_wait(bars.full + i, (armed_par >> i) & 1u, &never);
-                    if (tails & (1u << i)) (void)mbar_wait(bars.tail + i, (tail_par >> i) & 1u, &never);
-                }
+        }
+        if ((timed_out || *abort_flag) && lane == 0) {
+            *abort_flag = 1;
+            volatile uint32_t never = 0;
+            for (int i = 0; i < S; ++i) {
+                if (leader && (armed & (1u << i)))
+                    (void)mbar_wait(bars.full + i, (armed_par >> i) & 1u, &never);
+                if (tails & (1u << i)) (void)mbar_wait(bars.tail + i, (tail_par >> i) & 1u, &never);
             }
         }
     } else if (warp == 1) {
@@ -335,13 +355,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
             // ------------------------------------------------- MMA issuer
             constexpr uint32_t idesc = Elem<T>::idesc | ((256u >> 3) << 17) | kTransA | kTransB;
             const bool one = elect_one();
+            constexpr uint16_t kAll = (1u << (2 * P)) - 1;                   // a stage is read by every pair
+            const uint16_t both = static_cast<uint16_t>(0x3u << lead);      // this pair
             const uint64_t ad0 = sdesc_sw128_mn(smem_u32(smem), kChunk);
             const uint64_t bd0 = sdesc_sw128_mn(smem_u32(smem + kOpBytes), kChunk);
             Ring r;
             Acc acc;
             bool issued = false;
             for (int t = first; t < total && !timed_out; t += stride) {
-                const GradTile g = grad_tile(args, t);
+                const GradTile g = grad_tile<P>(args, t);
                 if (g.rows == 0) continue;  // the epilogue writes zeros
                 if (!warp_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
                     timed_out = true;
@@ -363,20 +385,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
                             if (kk * 16 < rest)
                                 mma_bf16_pair(d, ad0 + (at + kk * (2048 >> 4)), bd0 + (at + kk * (2048 >> 4)), idesc,
                                               (k | kk) != 0 ? 1u : 0u);
-                        mma_commit_pair(bars.empty + r.s, 0x3);
+                        mma_commit_pair(bars.empty + r.s, kAll);
                     }
                     __syncwarp();
                     issued = true;
                     r.next<S>();
                 }
                 if (timed_out) break;
-                if (one) mma_commit_pair(bars.tfull + acc.i, 0x3);
+                if (one) mma_commit_pair(bars.tfull + acc.i, both);
                 __syncwarp();
                 acc.next();
             }
             if ((timed_out || *abort_flag) && issued && one) {
                 *abort_flag = 1;
-                mma_commit_pair(&bars.drain, 0x1);
+                mma_commit_pair(&bars.drain, static_cast<uint16_t>(1u << rank));
                 volatile uint32_t never = 0;
                 (void)mbar_wait(&bars.drain, 0, &never);
             }
@@ -386,7 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
         Ring r;
         uint32_t tail_ph = 0;
         for (int t = first; t < total && !timed_out; t += stride) {
-            const GradTile g = grad_tile(args, t);
+            const GradTile g = grad_tile<P>(args, t);
             const int steps = (g.rows + kBK - 1) / kBK, rest = g.rows % kBK;
             for (int k = 0; k + 1 < steps; ++k) r.next<S>();
             if (steps == 0) continue;
@@ -407,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(bars.full + r.s), 0));
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(bars.full + r.s), lead));
             }
             r.next<S>();
         }
@@ -423,8 +445,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
         int buf = 0;
         uint8_t* stage = sOut + ew * 2 * 4096;
         for (int t = first; t < total; t += stride) {
-            const GradTile g = grad_tile(args, t);
-            const int m = g.m + 128 * static_cast<int>(rank) + q * 32;
+            const GradTile g = grad_tile<P>(args, t);
+            const int m = g.m + 128 * static_cast<int>(rank & 1) + q * 32;
+            const int n = g.n + 256 * static_cast<int>(rank >> 1) + c0;
             uint32_t pk[64];
             if (g.rows) {
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars.tfull + acc.i, acc.ph, abort_flag))) {
@@ -449,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
                 // side waits for, so the arrive need not release them
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), 0));
+                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), lead));
                 acc.next();
             } else {
 #pragma unroll
@@ -459,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
             for (int c = 0; c < 128; c += 64) {
                 // a box past the edge takes no buffer: the wait below counts
                 // on every turn of a buffer having its store
-                if (m >= args.K || g.n + c0 + c >= args.N) continue;
+                if (m >= args.K || n + c >= args.N) continue;
                 if (lane == 0) bulk_wait_read<1>();  // this buffer's previous store has read it
                 __syncwarp();
                 uint8_t* sb = stage + buf * 4096 + lane * 128;
@@ -471,7 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    tma_store_3d(&tOut, stage + buf * 4096, g.n + c0 + c, m, g.e);
+                    tma_store_3d(&tOut, stage + buf * 4096, n + c, m, g.e);
                     bulk_commit();
                 }
                 buf ^= 1;
@@ -485,12 +508,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
 }
 
 // --------------------------------------------------------------- launches --
-template <typename T, bool WT>
+// The pairs of a cluster share an operand when the panels (or column tiles)
+// come in sets of two; an odd number runs as single pairs.
+template <typename T, bool WT, int P>
 cudaError_t launch_product(const RaggedArgs& a, const void* x, int64_t ldx, const void* w, cudaStream_t st) {
     static_assert(kProdSmem <= 232448, "shared memory budget");
-    static bool done[kMaxDevices] = {};
-    cudaError_t e = allow_smem(k_ragged_product<T, WT>, kProdSmem, done);
-    if (e != cudaSuccess) return e;
+    static int resident[kMaxDevices] = {};
     const uint64_t N = a.N, K = a.K, R = a.R, E = a.E;
     CUtensorMap tW;
     RowMaps tX;
@@ -498,20 +521,26 @@ cudaError_t launch_product(const RaggedArgs& a, const void* x, int64_t ldx, cons
     const uint64_t ws[2] = {wd[0] * 2, N * K * 2};
     const uint32_t wb[3] = {64, WT ? 64u : 128u, 1};
     if (!make_tensor_map(&tW, w, 3, wd, ws, wb, Elem<T>::map) ||
-        !make_row_maps(&tX, x, R, K, static_cast<uint64_t>(ldx) * 2, 64, Elem<T>::map))
+        !make_row_maps<P>(&tX, x, R, K, static_cast<uint64_t>(ldx) * 2, 64, Elem<T>::map))
         return cudaErrorInvalidValue;
-    const int64_t items = (R / kTN + (R < E ? R : E)) * ((N + 255) / 256);  // at most
-    return launch_pdl(k_ragged_product<T, WT>, dim3(pair_grid(items)), dim3(64 + 32 * kEpiWarps), kProdSmem, st, tW, tX,
-                      a);
+    const int64_t items = (R / kTN + (R < E ? R : E)) * ((N + 255) / 256 / P);  // at most
+    return launch_clusters<P>(k_ragged_product<T, WT, P>, items, 64 + 32 * kEpiWarps, kProdSmem, resident, st, tW, tX,
+                              a);
 }
 
 template <typename T>
+cudaError_t product(const RaggedArgs& a, const void* x, int64_t ldx, const void* w, bool transposed, cudaStream_t st) {
+    const bool two = ((a.N + 255) / 256) % 2 == 0;
+    if (transposed)
+        return two ? launch_product<T, true, 2>(a, x, ldx, w, st) : launch_product<T, true, 1>(a, x, ldx, w, st);
+    return two ? launch_product<T, false, 2>(a, x, ldx, w, st) : launch_product<T, false, 1>(a, x, ldx, w, st);
+}
+
+template <typename T, int P>
 cudaError_t launch_wgrad_ragged(const RaggedArgs& a, const void* x, int64_t ldx, const void* y, int64_t ldy,
                                 cudaStream_t st) {
     static_assert(kGradSmem <= 232448, "shared memory budget");
-    static bool done[kMaxDevices] = {};
-    cudaError_t e = allow_smem(k_ragged_wgrad<T>, kGradSmem, done);
-    if (e != cudaSuccess) return e;
+    static int resident[kMaxDevices] = {};
     const uint64_t M = a.K, N = a.N, R = a.R, E = a.E;
     CUtensorMap tA, tB, tOut;
     const uint64_t ad[2] = {M, R}, as[1] = {static_cast<uint64_t>(ldx) * 2};
@@ -521,10 +550,16 @@ cudaError_t launch_wgrad_ragged(const RaggedArgs& a, const void* x, int64_t ldx,
     if (!make_tensor_map(&tA, x, 2, ad, as, box, Elem<T>::map) || !make_tensor_map(&tB, y, 2, bd, bs, box, Elem<T>::map) ||
         !make_tensor_map(&tOut, a.out, 3, od, os, obox, Elem<T>::map))
         return cudaErrorInvalidValue;
-    const int64_t items = static_cast<int64_t>(E) * ((N + 255) / 256) * ((M + 255) / 256);
+    const int64_t items = static_cast<int64_t>(E) * ((N + 255) / 256 / P) * ((M + 255) / 256);
     if (items > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_pdl(k_ragged_wgrad<T>, dim3(pair_grid(items)), dim3(96 + 32 * kEpiWarps), kGradSmem, st, tA, tB, tOut,
-                      a);
+    return launch_clusters<P>(k_ragged_wgrad<T, P>, items, 96 + 32 * kEpiWarps, kGradSmem, resident, st, tA, tB, tOut,
+                              a);
+}
+
+template <typename T>
+cudaError_t wgrad(const RaggedArgs& a, const void* x, int64_t ldx, const void* y, int64_t ldy, cudaStream_t st) {
+    return ((a.N + 255) / 256) % 2 == 0 ? launch_wgrad_ragged<T, 2>(a, x, ldx, y, ldy, st)
+                                        : launch_wgrad_ragged<T, 1>(a, x, ldx, y, ldy, st);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -570,13 +605,8 @@ extern "C" moe_status_t moe_grouped_gemm(int32_t dtype, int64_t R, int32_t N, in
     a.ldo = ldy;
     a.status = status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (dtype == MOE_DTYPE_BF16)
-        e = w_transposed ? launch_product<__nv_bfloat16, true>(a, x, ldx, w, st)
-                         : launch_product<__nv_bfloat16, false>(a, x, ldx, w, st);
-    else
-        e = w_transposed ? launch_product<__half, true>(a, x, ldx, w, st)
-                         : launch_product<__half, false>(a, x, ldx, w, st);
+    const cudaError_t e = dtype == MOE_DTYPE_BF16 ? product<__nv_bfloat16>(a, x, ldx, w, w_transposed != 0, st)
+                                                  : product<__half>(a, x, ldx, w, w_transposed != 0, st);
     return e == cudaSuccess ? MOE_OK
                             : set_last_error(MOE_ERR_CUDA, "grouped product: %s", cudaGetErrorString(e));
 }
@@ -605,8 +635,8 @@ extern "C" moe_status_t moe_grouped_wgrad(int32_t dtype, int64_t R, int32_t M, i
         a.E = E;
         a.out = out;
         a.status = status;
-        e = dtype == MOE_DTYPE_BF16 ? launch_wgrad_ragged<__nv_bfloat16>(a, a_, lda, b, ldb, st)
-                                    : launch_wgrad_ragged<__half>(a, a_, lda, b, ldb, st);
+        e = dtype == MOE_DTYPE_BF16 ? wgrad<__nv_bfloat16>(a, a_, lda, b, ldb, st)
+                                    : wgrad<__half>(a, a_, lda, b, ldb, st);
     }
     return e == cudaSuccess ? MOE_OK
                             : set_last_error(MOE_ERR_CUDA, "grouped weight gradient: %s", cudaGetErrorString(e));
