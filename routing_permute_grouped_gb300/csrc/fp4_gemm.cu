@@ -21,10 +21,12 @@
 // Bytes past K are cleared on the way (they may hold anything), rows past the
 // operand repeat its last row and reach no stored result.
 //
-// Tensor memory: two accumulators of 192 columns, two scale buffers of 48.
+// Tensor memory: two accumulators of 192 columns, and buffers for the scales of
+// one step of 256 elements (MX five of 24 columns, NV two of 48).  A buffer is
+// written again once its MMAs are complete.
 //
 // Warp roles: warp 0 TMA producer, warp 1 tensor memory and MMA issue (even
-// CTA), warp 2 scale loads, warps 4..7 scale layout, warps 8..15 epilogue.
+// CTA), warp 2 scale loads, warps 4..11 scale layout, warps 12..19 epilogue.
 // Every wait is bounded, as in ragged_gemm.cu.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -45,27 +47,37 @@ constexpr int kWBytes = 128 * 128;        // weight codes of one CTA and stage
 constexpr int kStage = kWBytes + kTN / 2 * 128;
 constexpr int kStages = 6;
 constexpr uint32_t kScaleCol = 2 * kTN;   // first tensor-memory column of the scale buffers
-constexpr uint32_t kScaleCols = 48;       // 4 words x (4 columns of A + 8 of B)
+// A scale buffer holds the words of kUnit = 256 elements: two of MX, four of NV,
+// each 4 columns of A and 8 of B.
+template <bool NV>
+struct Scales {
+    static constexpr int words = NV ? 4 : 2;
+    static constexpr uint32_t cols = words * 12;
+    static constexpr int bufs = NV ? 2 : 5;
+    static_assert(kScaleCol + bufs * cols <= 512, "tensor memory budget");
+};
 constexpr int kRaw = 7;                   // scale groups in shared memory
 constexpr int kRawRows = (4 + kTN / 32) * 512;  // 32-row pieces of 512 bytes: weights, tokens
-constexpr int kThreads = 256 + 32 * kEpiWarps;
+constexpr int kLayoutSets = 2;            // of four warps, one per lane quarter
+constexpr int kEpi0 = 4 + 4 * kLayoutSets;  // first epilogue warp
+constexpr int kThreads = 32 * (kEpi0 + kEpiWarps);
 
 struct ScaleBars {
     uint64_t raw_full[kRaw], raw_empty[kRaw];  // groups in shared memory
-    uint64_t full[2], used[2];                 // tensor-memory buffers written, their MMAs complete
+    uint64_t full[5], used[5];                 // tensor-memory buffers written, their MMAs complete
 };
 constexpr int kSmem =
     1024 + kStages * kStage + kRaw * kRawRows + kEpiStage + 1024 + static_cast<int>(sizeof(RaggedTiles));
 static_assert(kSmem <= 232448, "shared memory budget");
 static_assert(kStage % 1024 == 0, "swizzled tiles need 1024-byte alignment");
-static_assert(kScaleCol + 2 * kScaleCols <= 512, "tensor memory budget");
 
-template <bool NV, int P>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool NV>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_ragged_product_fp4(const __grid_constant__ CUtensorMap tW, const __grid_constant__ RowMaps tX,
                          const uint8_t* w_scales, const uint8_t* x_scales, const int pitch, const RaggedArgs args) {
     constexpr int S = kStages;
     constexpr int kGroup = NV ? 256 : 512;  // elements under 16 scale bytes
+    using SC = Scales<NV>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -77,12 +89,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     RaggedTiles& tiles = *reinterpret_cast<RaggedTiles*>(sOut + kEpiStage + 1024);
     volatile uint32_t* abort_flag = &bars.abort;
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = uniform(static_cast<int>(threadIdx.x >> 5));
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const bool leader = (rank & 1) == 0;
-    const uint32_t lead = rank & ~1u;  // the pair's even CTA
-    const int panels = (args.N + 255) / 256 / P;  // sets of P
+    const bool leader = rank == 0;
+    const int panels = (args.N + 255) / 256;
     const int steps = (args.K + kStep - 1) / kStep;
     const int groups = (args.K + kGroup - 1) / kGroup;
     pdl_trigger();
@@ -91,22 +102,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(sb.raw_full + i, 32);  // every lane's copies
             mbar_init(sb.raw_empty + i, 4);  // every layout warp
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < SC::bufs; ++i) {
             mbar_init(sb.full + i, 8);  // every layout warp of both CTAs
             mbar_init(sb.used + i, 1);
         }
         fence_mbar_init();
     }
     __syncwarp();
-    pair_start(bars, 1, P, warp);
+    pair_start(bars, 1, warp);
     if (warp == 2) ragged_tiles_build<kTN>(args, tiles, panels, lane);
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // the peer's barriers are initialised before any remote use
     tc_fence_after();
-    const uint32_t tmem_base = bars.tmem;
-    const int total = tiles.first[args.E];
-    const int first = blockIdx.x / (2 * P), stride = gridDim.x / (2 * P);
+    const uint32_t tmem_base = uniform(bars.tmem);
+    const int total = uniform(tiles.first[args.E]);
+    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
     bool timed_out = false;
 
     if (warp == 0) {
@@ -116,22 +127,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         Ring r;
         uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
         for (int t = first; t < total && !timed_out; t += stride) {
-            const RaggedItem it = ragged_item<kTN, P>(args, tiles, panels, t);
+            const RaggedItem it = uniform(ragged_item<kTN>(args, tiles, panels, t));
             const int half = ((it.rows + 31) & ~31) / 2;  // token rows of each CTA
-            const int xrow = it.row + half * static_cast<int>(rank & 1);
-            const int wrow = it.panel * 256 + 128 * static_cast<int>(rank);  // the pairs' panels follow each other
+            const int xrow = it.row + half * static_cast<int>(rank);
+            const int wrow = it.panel * 256 + 128 * static_cast<int>(rank);
             for (int k = 0; k < steps; ++k) {
                 if (!warp_wait(bars.empty + r.s, r.ph ^ 1u, abort_flag)) {
                     timed_out = true;
                     break;
                 }
-                const uint32_t full = mapa_shared(smem_u32(bars.full + r.s), lead);
+                const uint32_t full = mapa_shared(smem_u32(bars.full + r.s), 0);
                 uint8_t* st = smem + r.s * kStage;
                 armed &= ~(1u << r.s);
                 if (one) {
                     if (leader) mbar_arrive_expect_tx(bars.full + r.s, 2 * (kWBytes + half * 128));
                     tma_load_3d_pair(st, &tW, k * 128, wrow, it.e, full);
-                    load_rows<P>(tX, st + kWBytes, k * 128, xrow, half, full, rank);
+                    load_rows(tX, st + kWBytes, k * 128, xrow, half, full);
                 }
                 __syncwarp();
                 armed |= 1u << r.s;
@@ -153,66 +164,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             // converged, one lane issuing, as in ragged_gemm.cu
             constexpr uint32_t idesc0 = idesc_e2m1_f32(256, 8, !NV) & ~(0x3Fu << 17);
             const bool one = elect_one();
-            constexpr uint16_t kAll = (1u << (2 * P)) - 1;                   // a stage is read by every pair
-            const uint16_t both = static_cast<uint16_t>(0x3u << lead);      // this pair
             const uint64_t wd0 = sdesc_sw128(smem_u32(smem)), xd0 = sdesc_sw128(smem_u32(smem + kWBytes));
             Ring r;
             Acc acc;
-            Acc buf;  // scale buffer
+            Ring buf;  // scale buffer
             bool issued = false;
             for (int t = first; t < total && !timed_out; t += stride) {
-                const RaggedItem it = ragged_item<kTN, P>(args, tiles, panels, t);
+                const RaggedItem it = uniform(ragged_item<kTN>(args, tiles, panels, t));
                 const uint32_t n = (it.rows + 31) & ~31;
                 const uint32_t idesc = idesc0 | ((n >> 3) << 17);
                 if (!warp_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
                     timed_out = true;
                     break;
                 }
-                tc_fence_after();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(acc.i * kTN);
-                uint32_t sc = 0;  // columns of this group's scales
                 for (int k = 0; k < steps; ++k) {
-                    if (NV || (k & 1) == 0) {
-                        if (!warp_wait(sb.full + buf.i, buf.ph, abort_flag)) {
-                            timed_out = true;
-                            break;
-                        }
-                        sc = tmem_base + kScaleCol + static_cast<uint32_t>(buf.i) * kScaleCols;
-                    }
                     if (!warp_wait(bars.full + r.s, r.ph, abort_flag)) {
                         timed_out = true;
                         break;
                     }
-                    tc_fence_after();
                     const uint32_t at = static_cast<uint32_t>(r.s) * (kStage >> 4);
-                    const uint32_t sk = sc + (NV ? 0 : (k & 1) * 8), sk16 = sc + 16 + (NV ? 0 : (k & 1) * 16);
-                    const bool last = NV || (k & 1) || k + 1 == steps;
+                    const int left = args.K - k * kStep;
+                    if (!warp_wait(sb.full + buf.s, buf.ph, abort_flag)) {
+                        timed_out = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sc = tmem_base + kScaleCol + static_cast<uint32_t>(buf.s) * SC::cols;
                     if (one) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {  // 4 x 64 elements of each 128-byte row
+                        for (int kk = 0; kk < 4; ++kk) {  // 64 elements of each 128-byte row
                             const int word = NV ? kk : kk / 2;
                             const uint32_t byte = NV ? 0u : static_cast<uint32_t>(kk & 1) * 2u;
-                            if (k * kStep + kk * 64 < args.K)
+                            if (kk * 64 < left)
                                 mma_e2m1_pair<NV>(d, wd0 + (at + kk * 2), xd0 + (at + kk * 2),
-                                                  idesc | (byte << 4) | (byte << 29), sk + word * 4, sk16 + word * 8,
-                                                  (k | kk) != 0 ? 1u : 0u);
+                                                  idesc | (byte << 4) | (byte << 29), sc + word * 4,
+                                                  sc + SC::words * 4 + word * 8, (k | kk) != 0 ? 1u : 0u);
                         }
-                        mma_commit_pair(bars.empty + r.s, kAll);
-                        if (last) mma_commit_pair(sb.used + buf.i, both);
+                        mma_commit_pair(sb.used + buf.s, 0x3);
+                        mma_commit_pair(bars.empty + r.s, 0x3);
                     }
                     __syncwarp();
-                    r.next<S>();
                     issued = true;
-                    if (last) buf.next();
+                    buf.next<SC::bufs>();
+                    r.next<S>();
                 }
                 if (timed_out) break;
-                if (one) mma_commit_pair(bars.tfull + acc.i, both);
+                if (one) mma_commit_pair(bars.tfull + acc.i, 0x3);
                 __syncwarp();
                 acc.next();
             }
             if ((timed_out || *abort_flag) && issued && one) {
                 *abort_flag = 1;
-                mma_commit_pair(&bars.drain, static_cast<uint16_t>(1u << rank));
+                mma_commit_pair(&bars.drain, 0x1);
                 volatile uint32_t never = 0;
                 (void)mbar_wait(&bars.drain, 0, &never);
             }
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int s = 0;
         uint32_t ph = 0;
         for (int t = first; t < total && !timed_out; t += stride) {
-            const RaggedItem it = ragged_item<kTN, P>(args, tiles, panels, t);
+            const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
             const int64_t w_last = static_cast<int64_t>(it.e + 1) * args.N - 1;
             const int64_t w0 = static_cast<int64_t>(it.e) * args.N + it.panel * 256 + 128 * static_cast<int>(rank);
             const uint8_t* wp[4];
@@ -255,81 +259,96 @@ __global__ void __launch_bounds__(kThreads, 1)
         cp_async_wait<0>();
     } else if (warp == 3) {
         // no part: the layout warps start at a multiple of four
-    } else if (warp < 8) {
+    } else if (warp < kEpi0) {
         // --------------------------------------------------- scale layout
+        // Two sets of warps take the groups in turn: waiting for a buffer,
+        // storing to it and handing it on is one chain of latencies.
         constexpr int kPieces = 4 + kTN / 32;
+        const int set = (warp - 4) >> 2;
         const int valid = args.K / (NV ? 16 : 32);  // scale bytes of a row
         const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        int s = 0;
+        int s = 0, turn = 0;
         uint32_t ph = 0;
-        Acc buf;
+        Ring buf;
         for (int t = first; t < total && !timed_out; t += stride) {
             for (int g = 0; g < groups; ++g) {
-                if (!warp_wait(sb.raw_full + s, ph, abort_flag)) {
-                    timed_out = true;
-                    break;
-                }
-                const uint4* src = reinterpret_cast<const uint4*>(raw + s * kRawRows) + lane;
+                const int left = valid - g * 16;  // bytes of this group inside K
                 uint4 v[kPieces];
+                const bool mine = turn == set;
+                if (++turn == kLayoutSets) turn = 0;
+                if (mine) {
+                    if (!warp_wait(sb.raw_full + s, ph, abort_flag)) {
+                        timed_out = true;
+                        break;
+                    }
+                    const uint4* src = reinterpret_cast<const uint4*>(raw + s * kRawRows) + lane;
 #pragma unroll
-                for (int c = 0; c < kPieces; ++c) v[c] = src[c * 32];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sb.raw_empty + s);
+                    for (int c = 0; c < kPieces; ++c) v[c] = src[c * 32];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sb.raw_empty + s);
+                    if (left < 16) {
+                        uint32_t m[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int b = left - 4 * q;
+                            m[q] = b >= 4 ? 0xFFFFFFFFu : (b <= 0 ? 0u : (1u << (8 * b)) - 1u);
+                        }
+#pragma unroll
+                        for (int c = 0; c < kPieces; ++c)
+                            v[c] = make_uint4(v[c].x & m[0], v[c].y & m[1], v[c].z & m[2], v[c].w & m[3]);
+                    }
+                }
                 if (++s == kRaw) {
                     s = 0;
                     ph ^= 1u;
                 }
-                const int left = valid - g * 16;  // bytes of this group inside K
-                if (left < 16) {
-                    uint32_t m[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int b = left - 4 * q;
-                        m[q] = b >= 4 ? 0xFFFFFFFFu : (b <= 0 ? 0u : (1u << (8 * b)) - 1u);
+                for (int h = 0; h < 4 / SC::words; ++h) {  // the group's buffers
+                    if (4 * SC::words * h >= left) break;
+                    if (mine) {
+                        // the MMAs that last read this buffer are complete
+                        if (!warp_wait(sb.used + buf.s, buf.ph ^ 1u, abort_flag)) {
+                            timed_out = true;
+                            break;
+                        }
+                        tc_fence_after();
+                        uint32_t a[4 * SC::words], b[8 * SC::words];
+#pragma unroll
+                        for (int q = 0; q < SC::words; ++q) {
+                            auto word = [&](int c) {
+                                const int i = SC::words * h + q;
+                                return i == 0 ? v[c].x : i == 1 ? v[c].y : i == 2 ? v[c].z : v[c].w;
+                            };
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) a[4 * q + c] = word(c);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) b[8 * q + c] = c < kTN / 32 ? word(4 + (c < kTN / 32 ? c : 0)) : 0u;
+                        }
+                        const uint32_t dst = tmem_base + quarter + kScaleCol + static_cast<uint32_t>(buf.s) * SC::cols;
+                        tmem_st(dst, a);
+                        tmem_st(dst + 4 * SC::words, b);
+                        tmem_st_wait();
+                        // the words are in tensor memory; the MMA side reads
+                        // nothing else of this warp's, so the arrive releases
+                        // nothing
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(sb.full + buf.s), 0));
                     }
-#pragma unroll
-                    for (int c = 0; c < kPieces; ++c)
-                        v[c] = make_uint4(v[c].x & m[0], v[c].y & m[1], v[c].z & m[2], v[c].w & m[3]);
+                    buf.next<SC::bufs>();
                 }
-                uint32_t a[16], b[32];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    auto word = [&](int c) {
-                        const uint4& u = v[c];
-                        return q == 0 ? u.x : q == 1 ? u.y : q == 2 ? u.z : u.w;
-                    };
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) a[4 * q + c] = word(c);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) b[8 * q + c] = c < kTN / 32 ? word(4 + (c < kTN / 32 ? c : 0)) : 0u;
-                }
-                // the MMAs that last read this buffer are complete
-                if (!warp_wait(sb.used + buf.i, buf.ph ^ 1u, abort_flag)) {
-                    timed_out = true;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t dst = tmem_base + quarter + kScaleCol + static_cast<uint32_t>(buf.i) * kScaleCols;
-                tmem_st16(dst, a);
-                tmem_st32(dst + 16, b);
-                tmem_st_wait();
-                // the words are in tensor memory; the MMA side reads nothing
-                // else of this warp's, so the arrive releases nothing
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(sb.full + buf.i), lead));
-                buf.next();
+                if (timed_out) break;
             }
         }
     } else {
         // ------------------------------------------------------ epilogue
         // A warp owns 32 of the CTA's 128 features (its tensor-memory lane
         // quarter) and every other 32-token chunk.
-        const int q = warp & 3, odd = (warp - 8) >> 2;
+        const int q = warp & 3, odd = (warp - kEpi0) >> 2;
         const float gx = args.x_scale ? ld_dep(args.x_scale) : 1.0f;
         Acc acc;
         for (int t = first; t < total; t += stride) {
-            const RaggedItem it = ragged_item<kTN, P>(args, tiles, panels, t);
+            const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
             const float scale = gx * (args.w_scale ? ld_dep(args.w_scale + it.e) : 1.0f);
             float gate[kTN / 64];  // the factor of this lane's token of each chunk
 #pragma unroll
@@ -350,11 +369,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int c = odd * 32 + i * 64;
                 if (c < it.rows)
                     store_transposed<__nv_bfloat16>(args, taddr + c, it.row + c, it.rows - c, n0, lane, gate[i],
-                                                    sOut + (warp - 8) * 2048);
+                                                    sOut + (warp - kEpi0) * 2048);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), lead));
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), 0));
             acc.next();
         }
     }
@@ -363,29 +382,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     pair_end(tmem_base, warp);
 }
 
-template <bool NV, int P>
+template <bool NV>
 cudaError_t launch_fp4(const RaggedArgs& a, const void* xq, const uint8_t* xs, const void* wq, const uint8_t* ws,
                        int pitch, cudaStream_t st) {
-    static int resident[kMaxDevices] = {};
+    static bool ready[kMaxDevices] = {};
     const uint64_t N = a.N, KB = a.K / 2, R = a.R, E = a.E;  // KB bytes of codes per row
     CUtensorMap tW;
     RowMaps tX;
     const uint64_t wd[3] = {KB, N, E}, wst[2] = {KB, N * KB};
     const uint32_t wb[3] = {128, 128, 1};
     if (!make_tensor_map(&tW, wq, 3, wd, wst, wb, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
-        !make_row_maps<P>(&tX, xq, R, KB, KB, 128, CU_TENSOR_MAP_DATA_TYPE_UINT8))
+        !make_row_maps(&tX, xq, R, KB, KB, 128, CU_TENSOR_MAP_DATA_TYPE_UINT8))
         return cudaErrorInvalidValue;
-    const int64_t items = (R / kTN + (R < E ? R : E)) * ((N + 255) / 256 / P);  // at most
-    return launch_clusters<P>(k_ragged_product_fp4<NV, P>, items, kThreads, kSmem, resident, st, tW, tX, ws, xs, pitch,
+    const int64_t items = (R / kTN + (R < E ? R : E)) * ((N + 255) / 256);  // at most
+    return launch_pairs(k_ragged_product_fp4<NV>, items, kThreads, kSmem, ready, st, tW, tX, ws, xs, pitch,
                               a);
-}
-
-// Clusters of two pairs when the panels come in sets of two, as in ragged_gemm.cu.
-template <bool NV>
-cudaError_t product_fp4(const RaggedArgs& a, const void* xq, const uint8_t* xs, const void* wq, const uint8_t* ws,
-                        int pitch, cudaStream_t st) {
-    return ((a.N + 255) / 256) % 2 == 0 ? launch_fp4<NV, 2>(a, xq, xs, wq, ws, pitch, st)
-                                        : launch_fp4<NV, 1>(a, xq, xs, wq, ws, pitch, st);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -431,7 +442,7 @@ extern "C" moe_status_t moe_grouped_gemm_fp4(int32_t fmt, int64_t R, int32_t N, 
     const uint8_t* ws = static_cast<const uint8_t*>(w_scales);
     const int pitch = static_cast<int>(moe_fp4_scale_stride(fmt, K));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = fmt == MOE_FP4_NV ? product_fp4<true>(a, x_codes, xs, w_codes, ws, pitch, st)
-                                            : product_fp4<false>(a, x_codes, xs, w_codes, ws, pitch, st);
+    const cudaError_t e = fmt == MOE_FP4_NV ? launch_fp4<true>(a, x_codes, xs, w_codes, ws, pitch, st)
+                                            : launch_fp4<false>(a, x_codes, xs, w_codes, ws, pitch, st);
     return e == cudaSuccess ? MOE_OK : set_last_error(MOE_ERR_CUDA, "4-bit grouped product: %s", cudaGetErrorString(e));
 }

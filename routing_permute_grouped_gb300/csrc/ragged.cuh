@@ -52,7 +52,7 @@ struct RaggedTiles {
 };
 
 struct RaggedItem {
-    int e, panel;   // panel: the first of the cluster's
+    int e, panel;
     int row, rows;  // token rows [row, row + rows)
 };
 
@@ -82,12 +82,9 @@ __device__ void ragged_tiles_build(const RaggedArgs& a, RaggedTiles& s, int pane
 }
 
 // Item t: its group by bisection; inside a group, token tiles pass over eight
-// panels at a time, so the items in flight share both operands in L2.  A
-// cluster of P pairs takes one item of P neighbouring panels (`panels` counts
-// these sets).
-template <int TN, int P>
+// panels at a time, so the items in flight share both operands in L2.
+template <int TN>
 __device__ __forceinline__ RaggedItem ragged_item(const RaggedArgs& a, const RaggedTiles& s, int panels, int t) {
-    constexpr int kWide = 8 / P;
     int lo = 0, hi = a.E;  // first[lo] <= t < first[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -102,10 +99,10 @@ __device__ __forceinline__ RaggedItem ragged_item(const RaggedArgs& a, const Rag
     const int tiles = (len + TN - 1) / TN;
     const int width = ((len + tiles - 1) / tiles + 31) & ~31;  // <= TN
     const int i = t - s.first[lo];
-    const int block = i / (tiles * kWide), rest = i - block * tiles * kWide;
-    const int wide = min(kWide, panels - block * kWide);
+    const int block = i / (tiles * 8), rest = i - block * tiles * 8;
+    const int wide = min(8, panels - block * 8);
     const int tile = rest / wide;
-    it.panel = (block * kWide + rest - tile * wide) * P;
+    it.panel = block * 8 + rest - tile * wide;
     it.row = s.lo[lo] + tile * width;
     it.rows = min(width, s.hi[lo] - it.row);
     return it;
@@ -188,6 +185,20 @@ struct PairBars {
     uint32_t tmem, abort;
 };
 
+// The value of lane 0 of a converged warp.  The compiler cannot see that what
+// comes from memory is the same in every lane; told so, it keeps loop counters,
+// descriptors and addresses of the issuing warps in uniform registers, which
+// is where TMA and the MMAs take them from.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+__device__ __forceinline__ RaggedItem uniform(RaggedItem it) {
+    it.e = uniform(it.e);
+    it.panel = uniform(it.panel);
+    it.row = uniform(it.row);
+    it.rows = uniform(it.rows);
+    return it;
+}
+
 // A bounded wait of a converged warp; the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort) {
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort));
@@ -214,13 +225,12 @@ struct Acc {  // accumulator and its parity
     }
 };
 
-// full_count: arrivals that fill a stage; empty_count: pairs whose MMAs read it
 template <int S>
-__device__ __forceinline__ void pair_start(PairBars<S>& b, uint32_t full_count, uint32_t empty_count, int warp) {
+__device__ __forceinline__ void pair_start(PairBars<S>& b, uint32_t full_count, int warp) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(b.full + i, full_count);
-            mbar_init(b.empty + i, empty_count);
+            mbar_init(b.empty + i, 1);
             mbar_init(b.tail + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -237,40 +247,27 @@ __device__ __forceinline__ void pair_start(PairBars<S>& b, uint32_t full_count, 
     if (warp == 1) tmem_alloc_pair(&b.tmem, 512);
 }
 
-// Token rows as TMA boxes of 128 / P down to 16 / P rows of 128 bytes, so that
-// any multiple of 16 / P rows takes the fewest loads.  In a cluster of P pairs
-// the pairs work on the same token rows: each loads 1 / P of them and TMA
-// delivers them to all (multicast), because these kernels run against the
-// bandwidth from L2 to the SMs (about 12.5 TB/s, with or without the MMAs).
+// Token rows as TMA boxes of 128, 64, 32 and 16 rows of 128 bytes, so that any
+// multiple of 16 rows takes the fewest loads (boxes of 16 alone: 1.22 against
+// 1.17 ms on the data gradient of a 64-expert layer, whose tiles are 200 to 250
+// rows).
 struct RowMaps {
     CUtensorMap box[4];
 };
-template <int P>
-__device__ __forceinline__ void load_rows(const RowMaps& m, uint8_t* dst, int x, int row, int rows, uint32_t full,
-                                          uint32_t rank) {
-    if constexpr (P > 1) {
-        const int part = static_cast<int>(rank >> 1) * (rows / P);
-        dst += part * 128;
-        row += part;
-    }
-    const uint16_t mask = static_cast<uint16_t>(0x5u << (rank & 1));  // P = 2: the pairs' CTAs of this parity
+__device__ __forceinline__ void load_rows(const RowMaps& m, uint8_t* dst, int x, int row, int rows, uint32_t full) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (rows & (128 >> i)) {
-            if constexpr (P > 1)
-                tma_load_2d_pair_multicast(dst, m.box + i, x, row, full, mask);
-            else
-                tma_load_2d_pair(dst, m.box + i, x, row, full);
-            dst += (128 / P >> i) * 128;
-            row += 128 / P >> i;
+            tma_load_2d_pair(dst, m.box + i, x, row, full);
+            dst += (128 >> i) * 128;
+            row += 128 >> i;
         }
 }
-template <int P>
 inline bool make_row_maps(RowMaps* m, const void* x, uint64_t rows, uint64_t cols, uint64_t stride, uint32_t box_cols,
                           int dtype) {
     const uint64_t dims[2] = {cols, rows}, strides[1] = {stride};
     for (int i = 0; i < 4; ++i) {
-        const uint32_t box[2] = {box_cols, 128u / P >> i};
+        const uint32_t box[2] = {box_cols, 128u >> i};
         if (!make_tensor_map(m->box + i, x, 2, dims, strides, box, dtype)) return false;
     }
     return true;
@@ -286,40 +283,22 @@ __device__ __forceinline__ void pair_end(uint32_t tmem_base, int warp) {
     }
 }
 
-// Launches `kernel` on clusters of P pairs, as many as the GPU holds at once
-// but no more than there are items, after the kernels before it may have begun
-// to finish (launch_pdl).
-template <int P, typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kernel)(KArgs...), int64_t items, int threads, int smem, int (&resident)[kMaxDevices],
-                            cudaStream_t stream, Args&&... args) {
+// Launches `kernel` (clusters of two) on as many pairs as the GPU has SMs for,
+// but no more than there are items.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pairs(void (*kernel)(KArgs...), int64_t items, int threads, int smem, bool (&ready)[kMaxDevices],
+                         cudaStream_t stream, Args&&... args) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2 * P;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (!resident[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (!ready[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        int n = 0;
-        cfg.gridDim = dim3(2 * P);
-        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-        if (e != cudaSuccess) return e;
-        if (n <= 0) return cudaErrorInvalidConfiguration;
-        resident[dev] = n;
+        ready[dev] = true;
     }
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * P * (items < resident[dev] ? items : resident[dev])));
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+    const int64_t pairs = num_sms() / 2;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(2 * (items < pairs ? items : pairs))), dim3(threads), smem,
+                      stream, std::forward<Args>(args)...);
 }
 
 // ---------------------------------------------------------- 4-bit values --

@@ -63,8 +63,8 @@ struct Elem<__half> {  // operand formats 0 in bits [7,10) and [10,13)
 constexpr int kProdStages = 6;
 constexpr int kProdSmem = 1024 + kProdStages * kStage + kEpiStage + 1024 + static_cast<int>(sizeof(RaggedTiles));
 
-template <typename T, bool WT, int P>
-__global__ void __launch_bounds__(64 + 32 * kEpiWarps, 1)
+template <typename T, bool WT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps, 1)
     k_ragged_product(const __grid_constant__ CUtensorMap tW, const __grid_constant__ RowMaps tX,
                      const RaggedArgs args) {
     constexpr int S = kProdStages;
@@ -77,23 +77,22 @@ __global__ void __launch_bounds__(64 + 32 * kEpiWarps, 1)
     RaggedTiles& tiles = *reinterpret_cast<RaggedTiles*>(sOut + kEpiStage + 1024);
     volatile uint32_t* abort_flag = &bars.abort;
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = uniform(static_cast<int>(threadIdx.x >> 5));
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const bool leader = (rank & 1) == 0;
-    const uint32_t lead = rank & ~1u;  // the pair's even CTA
-    const int panels = (args.N + 255) / 256 / P;  // sets of P
+    const bool leader = rank == 0;
+    const int panels = (args.N + 255) / 256;
     const int steps = (args.K + kBK - 1) / kBK;
     pdl_trigger();
-    pair_start(bars, 1, P, warp);
+    pair_start(bars, 1, warp);
     if (warp == 2) ragged_tiles_build<kTN>(args, tiles, panels, lane);
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // the peer's barriers are initialised before any remote use
     tc_fence_after();
-    const uint32_t tmem_base = bars.tmem;
-    const int total = tiles.first[args.E];
-    const int first = blockIdx.x / (2 * P), stride = gridDim.x / (2 * P);
+    const uint32_t tmem_base = uniform(bars.tmem);
+    const int total = uniform(tiles.first[args.E]);
+    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
     bool timed_out = false;
 
     if (warp == 0) {
@@ -103,16 +102,16 @@ __global__ void __launch_bounds__(64 + 32 * kEpiWarps, 1)
         Ring r;
         uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
         for (int t = first; t < total && !timed_out; t += stride) {
-            const RaggedItem it = ragged_item<kTN, P>(args, tiles, panels, t);
+            const RaggedItem it = uniform(ragged_item<kTN>(args, tiles, panels, t));
             const int half = ((it.rows + 31) & ~31) / 2;  // token rows of each CTA
-            const int xrow = it.row + half * static_cast<int>(rank & 1);
-            const int wrow = it.panel * 256 + 128 * static_cast<int>(rank);  // the pairs' panels follow each other
+            const int xrow = it.row + half * static_cast<int>(rank);
+            const int wrow = it.panel * 256 + 128 * static_cast<int>(rank);
             for (int k = 0; k < steps; ++k) {
                 if (!warp_wait(bars.empty + r.s, r.ph ^ 1u, abort_flag)) {
                     timed_out = true;
                     break;
                 }
-                const uint32_t full = mapa_shared(smem_u32(bars.full + r.s), lead);
+                const uint32_t full = mapa_shared(smem_u32(bars.full + r.s), 0);
                 uint8_t* st = smem + r.s * kStage;
                 armed &= ~(1u << r.s);
                 if (one) {
@@ -123,7 +122,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpiWarps, 1)
                     } else {
                         tma_load_3d_pair(st, &tW, k * kBK, wrow, it.e, full);
                     }
-                    load_rows<P>(tX, st + kOpBytes, k * kBK, xrow, half, full, rank);
+                    load_rows(tX, st + kOpBytes, k * kBK, xrow, half, full);
                 }
                 __syncwarp();
                 armed |= 1u << r.s;
@@ -146,8 +145,6 @@ __global__ void __launch_bounds__(64 + 32 * kEpiWarps, 1)
             // loop counters are then warp-uniform values, which the MMA takes
             // as they are.
             const bool one = elect_one();
-            constexpr uint16_t kAll = (1u << (2 * P)) - 1;                   // a stage is read by every pair
-            const uint16_t both = static_cast<uint16_t>(0x3u << lead);      // this pair
             const uint64_t wd0 = WT ? sdesc_sw128_mn(smem_u32(smem), kChunk) : sdesc_sw128(smem_u32(smem));
             const uint64_t xd0 = sdesc_sw128(smem_u32(smem + kOpBytes));
             constexpr uint32_t kWStep = (WT ? 2048 : 32) >> 4;  // 16 elements of the sum
@@ -155,7 +152,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpiWarps, 1)
             Acc acc;
             bool issued = false;
             for (int t = first; t < total && !timed_out; t += stride) {
-                const RaggedItem it = ragged_item<kTN, P>(args, tiles, panels, t);
+                const RaggedItem it = uniform(ragged_item<kTN>(args, tiles, panels, t));
                 const uint32_t n = (it.rows + 31) & ~31;
                 const uint32_t idesc = Elem<T>::idesc | ((n >> 3) << 17) | (WT ? kTransA : 0u);
                 if (!warp_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
@@ -176,20 +173,20 @@ __global__ void __launch_bounds__(64 + 32 * kEpiWarps, 1)
                         for (int kk = 0; kk < kBK / 16; ++kk)
                             mma_bf16_pair(d, wd0 + (at + kk * kWStep), xd0 + (at + kk * 2), idesc,
                                           (k | kk) != 0 ? 1u : 0u);
-                        mma_commit_pair(bars.empty + r.s, kAll);
+                        mma_commit_pair(bars.empty + r.s, 0x3);
                     }
                     __syncwarp();
                     issued = true;
                     r.next<S>();
                 }
                 if (timed_out) break;
-                if (one) mma_commit_pair(bars.tfull + acc.i, both);
+                if (one) mma_commit_pair(bars.tfull + acc.i, 0x3);
                 __syncwarp();
                 acc.next();
             }
             if ((timed_out || *abort_flag) && issued && one) {
                 *abort_flag = 1;
-                mma_commit_pair(&bars.drain, static_cast<uint16_t>(1u << rank));
+                mma_commit_pair(&bars.drain, 0x1);
                 volatile uint32_t never = 0;
                 (void)mbar_wait(&bars.drain, 0, &never);
             }
@@ -201,7 +198,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpiWarps, 1)
         const int q = warp & 3, odd = (warp - 2) >> 2;
         Acc acc;
         for (int t = first; t < total; t += stride) {
-            const RaggedItem it = ragged_item<kTN, P>(args, tiles, panels, t);
+            const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
             float gate[kTN / 64];  // this lane's token of each chunk, read while the MMAs run
 #pragma unroll
             for (int i = 0; i < kTN / 64; ++i) {
@@ -226,7 +223,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpiWarps, 1)
             // the reads are complete: the MMA side reads nothing stored here
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), lead));
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), 0));
             acc.next();
         }
         if (timed_out) *abort_flag = 1;
@@ -245,23 +242,22 @@ struct GradTile {
     int row, rows;   // the group's rows
 };
 
-// Item t of a cluster of P pairs, which take P neighbouring column tiles.
-template <int P>
+// Called by converged warps.
 __device__ __forceinline__ GradTile grad_tile(const RaggedArgs& a, int t) {
-    const int nt = (a.N + 255) / 256 / P, mt = (a.K + 255) / 256;
+    const int nt = (a.N + 255) / 256, mt = (a.K + 255) / 256;
     GradTile g;
     g.e = t / (mt * nt);
     const int r = t - g.e * mt * nt;
     g.m = r / nt * 256;
-    g.n = r % nt * 256 * P;
+    g.n = r % nt * 256;
     const int2 rows = group_rows(a, g.e);
-    g.row = rows.x;
-    g.rows = rows.y - rows.x;
+    g.row = uniform(rows.x);
+    g.rows = uniform(rows.y - rows.x);
     return g;
 }
 
-template <typename T, int P>
-__global__ void __launch_bounds__(96 + 32 * kEpiWarps, 1)
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps, 1)
     k_ragged_wgrad(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB,
                    const __grid_constant__ CUtensorMap tOut, const RaggedArgs args) {
     constexpr int S = kGradStages;
@@ -272,20 +268,19 @@ __global__ void __launch_bounds__(96 + 32 * kEpiWarps, 1)
     PairBars<S>& bars = *reinterpret_cast<PairBars<S>*>(sOut + kOutStage);
     volatile uint32_t* abort_flag = &bars.abort;
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = uniform(static_cast<int>(threadIdx.x >> 5));
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const bool leader = (rank & 1) == 0;
-    const uint32_t lead = rank & ~1u;  // the pair's even CTA
+    const bool leader = rank == 0;
     pdl_trigger();
-    pair_start(bars, 2, P, warp);  // a stage is full when both CTAs say so (and its bytes have landed)
+    pair_start(bars, 2, warp);  // a stage is full when both CTAs say so (and its bytes have landed)
     tc_fence_before();
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    const uint32_t tmem_base = bars.tmem;
-    const int total = args.E * ((args.N + 255) / 256 / P) * ((args.K + 255) / 256);
-    const int first = blockIdx.x / (2 * P), stride = gridDim.x / (2 * P);
+    const uint32_t tmem_base = uniform(bars.tmem);
+    const int total = args.E * ((args.N + 255) / 256) * ((args.K + 255) / 256);
+    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
     bool timed_out = false;
 
     if (warp == 0) {
@@ -294,8 +289,8 @@ __global__ void __launch_bounds__(96 + 32 * kEpiWarps, 1)
         Ring r;
         uint32_t armed = 0, armed_par = 0, tails = 0, tail_par = 0, tail_ph = 0;
         for (int t = first; t < total && !timed_out; t += stride) {
-            const GradTile g = grad_tile<P>(args, t);
-            const int ac = g.m + 128 * static_cast<int>(rank & 1), bc = g.n + 128 * static_cast<int>(rank);
+            const GradTile g = grad_tile(args, t);
+            const int ac = g.m + 128 * static_cast<int>(rank), bc = g.n + 128 * static_cast<int>(rank);
             for (int k = 0; k < g.rows; k += kBK) {
                 if (!warp_wait(bars.empty + r.s, r.ph ^ 1u, abort_flag)) {
                     timed_out = true;
@@ -317,7 +312,7 @@ __global__ void __launch_bounds__(96 + 32 * kEpiWarps, 1)
                     armed_par = (armed_par & ~bit) | (r.ph << r.s);
                 }
                 const uint32_t bar = tail ? mapa_shared(smem_u32(bars.tail + r.s), rank)
-                                          : mapa_shared(smem_u32(bars.full + r.s), lead);
+                                          : mapa_shared(smem_u32(bars.full + r.s), 0);
                 const int row = g.row + k;
                 if (one) {
                     if (tail)
@@ -326,14 +321,8 @@ __global__ void __launch_bounds__(96 + 32 * kEpiWarps, 1)
                         mbar_arrive_expect_tx(bars.full + r.s, 2 * kStage);
                     else
                         mbar_arrive_cluster_relaxed(bar);
-                    if constexpr (P > 1) {  // the pairs share A: each loads 64 of the CTA's columns for both
-                        const int c = static_cast<int>(rank >> 1);
-                        tma_load_2d_pair_multicast(st + c * kChunk, &tA, ac + 64 * c, row, bar,
-                                                   static_cast<uint16_t>(0x5u << (rank & 1)));
-                    } else {
-                        tma_load_2d_pair(st, &tA, ac, row, bar);
-                        tma_load_2d_pair(st + kChunk, &tA, ac + 64, row, bar);
-                    }
+                    tma_load_2d_pair(st, &tA, ac, row, bar);
+                    tma_load_2d_pair(st + kChunk, &tA, ac + 64, row, bar);
                     tma_load_2d_pair(st + kOpBytes, &tB, bc, row, bar);
                     tma_load_2d_pair(st + kOpBytes + kChunk, &tB, bc + 64, row, bar);
                 }
@@ -355,15 +344,13 @@ __global__ void __launch_bounds__(96 + 32 * kEpiWarps, 1)
             // ------------------------------------------------- MMA issuer
             constexpr uint32_t idesc = Elem<T>::idesc | ((256u >> 3) << 17) | kTransA | kTransB;
             const bool one = elect_one();
-            constexpr uint16_t kAll = (1u << (2 * P)) - 1;                   // a stage is read by every pair
-            const uint16_t both = static_cast<uint16_t>(0x3u << lead);      // this pair
             const uint64_t ad0 = sdesc_sw128_mn(smem_u32(smem), kChunk);
             const uint64_t bd0 = sdesc_sw128_mn(smem_u32(smem + kOpBytes), kChunk);
             Ring r;
             Acc acc;
             bool issued = false;
             for (int t = first; t < total && !timed_out; t += stride) {
-                const GradTile g = grad_tile<P>(args, t);
+                const GradTile g = grad_tile(args, t);
                 if (g.rows == 0) continue;  // the epilogue writes zeros
                 if (!warp_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
                     timed_out = true;
@@ -385,20 +372,20 @@ __global__ void __launch_bounds__(96 + 32 * kEpiWarps, 1)
                             if (kk * 16 < rest)
                                 mma_bf16_pair(d, ad0 + (at + kk * (2048 >> 4)), bd0 + (at + kk * (2048 >> 4)), idesc,
                                               (k | kk) != 0 ? 1u : 0u);
-                        mma_commit_pair(bars.empty + r.s, kAll);
+                        mma_commit_pair(bars.empty + r.s, 0x3);
                     }
                     __syncwarp();
                     issued = true;
                     r.next<S>();
                 }
                 if (timed_out) break;
-                if (one) mma_commit_pair(bars.tfull + acc.i, both);
+                if (one) mma_commit_pair(bars.tfull + acc.i, 0x3);
                 __syncwarp();
                 acc.next();
             }
             if ((timed_out || *abort_flag) && issued && one) {
                 *abort_flag = 1;
-                mma_commit_pair(&bars.drain, static_cast<uint16_t>(1u << rank));
+                mma_commit_pair(&bars.drain, 0x1);
                 volatile uint32_t never = 0;
                 (void)mbar_wait(&bars.drain, 0, &never);
             }
@@ -408,7 +395,7 @@ __global__ void __launch_bounds__(96 + 32 * kEpiWarps, 1)
         Ring r;
         uint32_t tail_ph = 0;
         for (int t = first; t < total && !timed_out; t += stride) {
-            const GradTile g = grad_tile<P>(args, t);
+            const GradTile g = grad_tile(args, t);
             const int steps = (g.rows + kBK - 1) / kBK, rest = g.rows % kBK;
             for (int k = 0; k + 1 < steps; ++k) r.next<S>();
             if (steps == 0) continue;
@@ -429,7 +416,7 @@ __global__ void __launch_bounds__(96 + 32 * kEpiWarps, 1)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(bars.full + r.s), lead));
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(bars.full + r.s), 0));
             }
             r.next<S>();
         }
@@ -445,9 +432,9 @@ __global__ void __launch_bounds__(96 + 32 * kEpiWarps, 1)
         int buf = 0;
         uint8_t* stage = sOut + ew * 2 * 4096;
         for (int t = first; t < total; t += stride) {
-            const GradTile g = grad_tile<P>(args, t);
-            const int m = g.m + 128 * static_cast<int>(rank & 1) + q * 32;
-            const int n = g.n + 256 * static_cast<int>(rank >> 1) + c0;
+            const GradTile g = grad_tile(args, t);
+            const int m = g.m + 128 * static_cast<int>(rank) + q * 32;
+            const int n = g.n + c0;
             uint32_t pk[64];
             if (g.rows) {
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars.tfull + acc.i, acc.ph, abort_flag))) {
@@ -472,7 +459,7 @@ __global__ void __launch_bounds__(96 + 32 * kEpiWarps, 1)
                 // side waits for, so the arrive need not release them
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), lead));
+                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), 0));
                 acc.next();
             } else {
 #pragma unroll
@@ -508,12 +495,10 @@ __global__ void __launch_bounds__(96 + 32 * kEpiWarps, 1)
 }
 
 // --------------------------------------------------------------- launches --
-// The pairs of a cluster share an operand when the panels (or column tiles)
-// come in sets of two; an odd number runs as single pairs.
-template <typename T, bool WT, int P>
+template <typename T, bool WT>
 cudaError_t launch_product(const RaggedArgs& a, const void* x, int64_t ldx, const void* w, cudaStream_t st) {
     static_assert(kProdSmem <= 232448, "shared memory budget");
-    static int resident[kMaxDevices] = {};
+    static bool ready[kMaxDevices] = {};
     const uint64_t N = a.N, K = a.K, R = a.R, E = a.E;
     CUtensorMap tW;
     RowMaps tX;
@@ -521,26 +506,23 @@ cudaError_t launch_product(const RaggedArgs& a, const void* x, int64_t ldx, cons
     const uint64_t ws[2] = {wd[0] * 2, N * K * 2};
     const uint32_t wb[3] = {64, WT ? 64u : 128u, 1};
     if (!make_tensor_map(&tW, w, 3, wd, ws, wb, Elem<T>::map) ||
-        !make_row_maps<P>(&tX, x, R, K, static_cast<uint64_t>(ldx) * 2, 64, Elem<T>::map))
+        !make_row_maps(&tX, x, R, K, static_cast<uint64_t>(ldx) * 2, 64, Elem<T>::map))
         return cudaErrorInvalidValue;
-    const int64_t items = (R / kTN + (R < E ? R : E)) * ((N + 255) / 256 / P);  // at most
-    return launch_clusters<P>(k_ragged_product<T, WT, P>, items, 64 + 32 * kEpiWarps, kProdSmem, resident, st, tW, tX,
+    const int64_t items = (R / kTN + (R < E ? R : E)) * ((N + 255) / 256);  // at most
+    return launch_pairs(k_ragged_product<T, WT>, items, 64 + 32 * kEpiWarps, kProdSmem, ready, st, tW, tX,
                               a);
 }
 
 template <typename T>
 cudaError_t product(const RaggedArgs& a, const void* x, int64_t ldx, const void* w, bool transposed, cudaStream_t st) {
-    const bool two = ((a.N + 255) / 256) % 2 == 0;
-    if (transposed)
-        return two ? launch_product<T, true, 2>(a, x, ldx, w, st) : launch_product<T, true, 1>(a, x, ldx, w, st);
-    return two ? launch_product<T, false, 2>(a, x, ldx, w, st) : launch_product<T, false, 1>(a, x, ldx, w, st);
+    return transposed ? launch_product<T, true>(a, x, ldx, w, st) : launch_product<T, false>(a, x, ldx, w, st);
 }
 
-template <typename T, int P>
+template <typename T>
 cudaError_t launch_wgrad_ragged(const RaggedArgs& a, const void* x, int64_t ldx, const void* y, int64_t ldy,
                                 cudaStream_t st) {
     static_assert(kGradSmem <= 232448, "shared memory budget");
-    static int resident[kMaxDevices] = {};
+    static bool ready[kMaxDevices] = {};
     const uint64_t M = a.K, N = a.N, R = a.R, E = a.E;
     CUtensorMap tA, tB, tOut;
     const uint64_t ad[2] = {M, R}, as[1] = {static_cast<uint64_t>(ldx) * 2};
@@ -550,16 +532,10 @@ cudaError_t launch_wgrad_ragged(const RaggedArgs& a, const void* x, int64_t ldx,
     if (!make_tensor_map(&tA, x, 2, ad, as, box, Elem<T>::map) || !make_tensor_map(&tB, y, 2, bd, bs, box, Elem<T>::map) ||
         !make_tensor_map(&tOut, a.out, 3, od, os, obox, Elem<T>::map))
         return cudaErrorInvalidValue;
-    const int64_t items = static_cast<int64_t>(E) * ((N + 255) / 256 / P) * ((M + 255) / 256);
+    const int64_t items = static_cast<int64_t>(E) * ((N + 255) / 256) * ((M + 255) / 256);
     if (items > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_clusters<P>(k_ragged_wgrad<T, P>, items, 96 + 32 * kEpiWarps, kGradSmem, resident, st, tA, tB, tOut,
+    return launch_pairs(k_ragged_wgrad<T>, items, 96 + 32 * kEpiWarps, kGradSmem, ready, st, tA, tB, tOut,
                               a);
-}
-
-template <typename T>
-cudaError_t wgrad(const RaggedArgs& a, const void* x, int64_t ldx, const void* y, int64_t ldy, cudaStream_t st) {
-    return ((a.N + 255) / 256) % 2 == 0 ? launch_wgrad_ragged<T, 2>(a, x, ldx, y, ldy, st)
-                                        : launch_wgrad_ragged<T, 1>(a, x, ldx, y, ldy, st);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -635,8 +611,8 @@ extern "C" moe_status_t moe_grouped_wgrad(int32_t dtype, int64_t R, int32_t M, i
         a.E = E;
         a.out = out;
         a.status = status;
-        e = dtype == MOE_DTYPE_BF16 ? wgrad<__nv_bfloat16>(a, a_, lda, b, ldb, st)
-                                    : wgrad<__half>(a, a_, lda, b, ldb, st);
+        e = dtype == MOE_DTYPE_BF16 ? launch_wgrad_ragged<__nv_bfloat16>(a, a_, lda, b, ldb, st)
+                                    : launch_wgrad_ragged<__half>(a, a_, lda, b, ldb, st);
     }
     return e == cudaSuccess ? MOE_OK
                             : set_last_error(MOE_ERR_CUDA, "grouped weight gradient: %s", cudaGetErrorString(e));
