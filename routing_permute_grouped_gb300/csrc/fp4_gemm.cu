@@ -64,7 +64,7 @@ constexpr int kThreads = 32 * (kEpi0 + kEpiWarps);
 
 struct ScaleBars {
     uint64_t raw_full[kRaw], raw_empty[kRaw];  // groups in shared memory
-    uint64_t full[5], used[5];                 // tensor-memory buffers written, their MMAs complete
+    uint64_t full[5];                          // tensor-memory buffers written
 };
 constexpr int kSmem =
     1024 + kStages * kStage + kRaw * kRawRows + kEpiStage + 1024 + static_cast<int>(sizeof(RaggedTiles));
@@ -104,7 +104,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < SC::bufs; ++i) {
             mbar_init(sb.full + i, 8);  // every layout warp of both CTAs
-            mbar_init(sb.used + i, 1);
         }
         fence_mbar_init();
     }
@@ -123,7 +122,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
         // converged, one lane issuing, as the MMA warp
-        const bool one = elect_one();
+        const uint32_t one = elect_one();
         Ring r;
         uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
         for (int t = first; t < total && !timed_out; t += stride) {
@@ -139,12 +138,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t full = mapa_shared(smem_u32(bars.full + r.s), 0);
                 uint8_t* st = smem + r.s * kStage;
                 armed &= ~(1u << r.s);
-                if (one) {
-                    if (leader) mbar_arrive_expect_tx(bars.full + r.s, 2 * (kWBytes + half * 128));
-                    tma_load_3d_pair(st, &tW, k * 128, wrow, it.e, full);
-                    load_rows(tX, st + kWBytes, k * 128, xrow, half, full);
-                }
-                __syncwarp();
+                if (leader) mbar_arrive_expect_tx_if(one, bars.full + r.s, 2 * (kWBytes + half * 128));
+                tma_load_3d_pair_if(one, st, &tW, k * 128, wrow, it.e, full);
+                load_rows(one, tX, st + kWBytes, k * 128, xrow, half, full);
                 armed |= 1u << r.s;
                 armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
                 r.next<S>();
@@ -163,7 +159,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // ------------------------------------------------- MMA issuer
             // converged, one lane issuing, as in ragged_gemm.cu
             constexpr uint32_t idesc0 = idesc_e2m1_f32(256, 8, !NV) & ~(0x3Fu << 17);
-            const bool one = elect_one();
+            const uint32_t one = elect_one();
             const uint64_t wd0 = sdesc_sw128(smem_u32(smem)), xd0 = sdesc_sw128(smem_u32(smem + kWBytes));
             Ring r;
             Acc acc;
@@ -191,27 +187,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     tc_fence_after();
                     const uint32_t sc = tmem_base + kScaleCol + static_cast<uint32_t>(buf.s) * SC::cols;
-                    if (one) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {  // 64 elements of each 128-byte row
-                            const int word = NV ? kk : kk / 2;
-                            const uint32_t byte = NV ? 0u : static_cast<uint32_t>(kk & 1) * 2u;
-                            if (kk * 64 < left)
-                                mma_e2m1_pair<NV>(d, wd0 + (at + kk * 2), xd0 + (at + kk * 2),
-                                                  idesc | (byte << 4) | (byte << 29), sc + word * 4,
-                                                  sc + SC::words * 4 + word * 8, (k | kk) != 0 ? 1u : 0u);
-                        }
-                        mma_commit_pair(sb.used + buf.s, 0x3);
-                        mma_commit_pair(bars.empty + r.s, 0x3);
+                    for (int kk = 0; kk < 4; ++kk) {  // 64 elements of each 128-byte row
+                        const int word = NV ? kk : kk / 2;
+                        const uint32_t byte = NV ? 0u : static_cast<uint32_t>(kk & 1) * 2u;
+                        if (kk * 64 < left)
+                            mma_e2m1_pair_if<NV>(one, d, wd0 + (at + kk * 2), xd0 + (at + kk * 2),
+                                                 idesc | (byte << 4) | (byte << 29), sc + word * 4,
+                                                 sc + SC::words * 4 + word * 8, (k | kk) != 0 ? 1u : 0u);
                     }
-                    __syncwarp();
+                    // read by the scale warps too: a step's scale buffer is free
+                    // with its stage
+                    mma_commit_pair_if(one, bars.empty + r.s, 0x3);
                     issued = true;
                     buf.next<SC::bufs>();
                     r.next<S>();
                 }
                 if (timed_out) break;
-                if (one) mma_commit_pair(bars.tfull + acc.i, 0x3);
-                __syncwarp();
+                mma_commit_pair_if(one, bars.tfull + acc.i, 0x3);
                 acc.next();
             }
             if ((timed_out || *abort_flag) && issued && one) {
@@ -270,6 +263,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int s = 0, turn = 0;
         uint32_t ph = 0;
         Ring buf;
+        // the stage of the step whose buffer is written next, SC::bufs steps ago
+        Ring old;
+        int fresh = SC::bufs;  // buffers not yet written
         for (int t = first; t < total && !timed_out; t += stride) {
             for (int g = 0; g < groups; ++g) {
                 const int left = valid - g * 16;  // bytes of this group inside K
@@ -307,7 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (4 * SC::words * h >= left) break;
                     if (mine) {
                         // the MMAs that last read this buffer are complete
-                        if (!warp_wait(sb.used + buf.s, buf.ph ^ 1u, abort_flag)) {
+                        if (fresh == 0 && !warp_wait(bars.empty + old.s, old.ph, abort_flag)) {
                             timed_out = true;
                             break;
                         }
@@ -336,6 +332,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(sb.full + buf.s), 0));
                     }
                     buf.next<SC::bufs>();
+                    if (fresh)
+                        --fresh;
+                    else
+                        old.next<S>();
                 }
                 if (timed_out) break;
             }

@@ -452,6 +452,58 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, u
         : "memory");
 }
 
+// Forms for a converged warp of which one lane (`one` != 0) acts, by a predicate
+// on the instruction instead of a branch around it: inside a divergent branch
+// the operands cannot stay in uniform registers, and moving them there for
+// every instruction made the issue of four 4-bit MMAs ISSUE cycles.
+__device__ __forceinline__ void mma_bf16_pair_if(uint32_t one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                 uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit_pair_if(uint32_t one, uint64_t* bar, uint16_t mask) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "h"(mask), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx_if(uint32_t one, uint64_t* bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "r"(bytes), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair_if(uint32_t one, void* smem_dst, const CUtensorMap* tm, int32_t x0,
+                                                    int32_t y0, uint32_t bar_cluster_addr) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x0), "r"(y0), "r"(bar_cluster_addr), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair_if(uint32_t one, void* smem_dst, const CUtensorMap* tm, int32_t x0,
+                                                    int32_t y0, int32_t z0, uint32_t bar_cluster_addr) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x0), "r"(y0), "r"(z0), "r"(bar_cluster_addr), "r"(one)
+        : "memory");
+}
+
 // Instruction descriptor of tcgen05.mma kind::mxf4 / kind::mxf4nvf4: e2m1 A and
 // B (K = 64, both K-major) with block scales, fp32 accumulator:
 //   [4,6) B scale byte   [7,10) A format 1 = e2m1   [10,12) B format 1 = e2m1
@@ -468,23 +520,26 @@ __host__ __device__ constexpr uint32_t idesc_e2m1_f32(int M, int N, bool ue8m0) 
 // CTA's own 128 rows, B's for all N rows in both CTAs.  MX: two power-of-two
 // bytes of the word per MMA, chosen by idesc; NV: four e4m3 bytes.
 template <bool NV>
-__device__ __forceinline__ void mma_e2m1_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                              uint32_t a_scale, uint32_t b_scale, uint32_t accumulate) {
+__device__ __forceinline__ void mma_e2m1_pair_if(uint32_t one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                 uint32_t idesc, uint32_t a_scale, uint32_t b_scale,
+                                                 uint32_t accumulate) {
     if constexpr (NV)
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
+            "{\n\t.reg .pred p, q;\n\t"
             "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
-                "r"(d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
+            "setp.ne.b32 q, %7, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], "
+            "p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate), "r"(one)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
+            "{\n\t.reg .pred p, q;\n\t"
             "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
-                "r"(d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
+            "setp.ne.b32 q, %7, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
+            "p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate), "r"(one)
             : "memory");
 }
 

@@ -254,11 +254,12 @@ __device__ __forceinline__ void pair_start(PairBars<S>& b, uint32_t full_count, 
 struct RowMaps {
     CUtensorMap box[4];
 };
-__device__ __forceinline__ void load_rows(const RowMaps& m, uint8_t* dst, int x, int row, int rows, uint32_t full) {
+__device__ __forceinline__ void load_rows(uint32_t one, const RowMaps& m, uint8_t* dst, int x, int row, int rows,
+                                          uint32_t full) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (rows & (128 >> i)) {
-            tma_load_2d_pair(dst, m.box + i, x, row, full);
+            tma_load_2d_pair_if(one, dst, m.box + i, x, row, full);
             dst += (128 >> i) * 128;
             row += 128 >> i;
         }

@@ -98,7 +98,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
         // converged, one lane issuing, as the MMA warp
-        const bool one = elect_one();
+        const uint32_t one = elect_one();
         Ring r;
         uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
         for (int t = first; t < total && !timed_out; t += stride) {
@@ -114,17 +114,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
                 const uint32_t full = mapa_shared(smem_u32(bars.full + r.s), 0);
                 uint8_t* st = smem + r.s * kStage;
                 armed &= ~(1u << r.s);
-                if (one) {
-                    if (leader) mbar_arrive_expect_tx(bars.full + r.s, 2 * (kOpBytes + half * 128));
-                    if constexpr (WT) {
-                        tma_load_3d_pair(st, &tW, wrow, k * kBK, it.e, full);
-                        tma_load_3d_pair(st + kChunk, &tW, wrow + 64, k * kBK, it.e, full);
-                    } else {
-                        tma_load_3d_pair(st, &tW, k * kBK, wrow, it.e, full);
-                    }
-                    load_rows(tX, st + kOpBytes, k * kBK, xrow, half, full);
+                if (leader) mbar_arrive_expect_tx_if(one, bars.full + r.s, 2 * (kOpBytes + half * 128));
+                if constexpr (WT) {
+                    tma_load_3d_pair_if(one, st, &tW, wrow, k * kBK, it.e, full);
+                    tma_load_3d_pair_if(one, st + kChunk, &tW, wrow + 64, k * kBK, it.e, full);
+                } else {
+                    tma_load_3d_pair_if(one, st, &tW, k * kBK, wrow, it.e, full);
                 }
-                __syncwarp();
+                load_rows(one, tX, st + kOpBytes, k * kBK, xrow, half, full);
                 armed |= 1u << r.s;
                 armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
                 r.next<S>();
@@ -144,7 +141,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
             // The warp stays converged and one lane issues: descriptors and
             // loop counters are then warp-uniform values, which the MMA takes
             // as they are.
-            const bool one = elect_one();
+            const uint32_t one = elect_one();
             const uint64_t wd0 = WT ? sdesc_sw128_mn(smem_u32(smem), kChunk) : sdesc_sw128(smem_u32(smem));
             const uint64_t xd0 = sdesc_sw128(smem_u32(smem + kOpBytes));
             constexpr uint32_t kWStep = (WT ? 2048 : 32) >> 4;  // 16 elements of the sum
@@ -168,20 +165,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
                     }
                     tc_fence_after();
                     const uint32_t at = static_cast<uint32_t>(r.s) * (kStage >> 4);
-                    if (one) {
 #pragma unroll
-                        for (int kk = 0; kk < kBK / 16; ++kk)
-                            mma_bf16_pair(d, wd0 + (at + kk * kWStep), xd0 + (at + kk * 2), idesc,
-                                          (k | kk) != 0 ? 1u : 0u);
-                        mma_commit_pair(bars.empty + r.s, 0x3);
-                    }
-                    __syncwarp();
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        mma_bf16_pair_if(one, d, wd0 + (at + kk * kWStep), xd0 + (at + kk * 2), idesc,
+                                         (k | kk) != 0 ? 1u : 0u);
+                    mma_commit_pair_if(one, bars.empty + r.s, 0x3);
                     issued = true;
                     r.next<S>();
                 }
                 if (timed_out) break;
-                if (one) mma_commit_pair(bars.tfull + acc.i, 0x3);
-                __syncwarp();
+                mma_commit_pair_if(one, bars.tfull + acc.i, 0x3);
                 acc.next();
             }
             if ((timed_out || *abort_flag) && issued && one) {
@@ -285,7 +278,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
 
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
-        const bool one = elect_one();
+        const uint32_t one = elect_one();
         Ring r;
         uint32_t armed = 0, armed_par = 0, tails = 0, tail_par = 0, tail_ph = 0;
         for (int t = first; t < total && !timed_out; t += stride) {
@@ -314,19 +307,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
                 const uint32_t bar = tail ? mapa_shared(smem_u32(bars.tail + r.s), rank)
                                           : mapa_shared(smem_u32(bars.full + r.s), 0);
                 const int row = g.row + k;
-                if (one) {
-                    if (tail)
-                        mbar_arrive_expect_tx(bars.tail + r.s, kStage);
-                    else if (leader)
-                        mbar_arrive_expect_tx(bars.full + r.s, 2 * kStage);
-                    else
-                        mbar_arrive_cluster_relaxed(bar);
-                    tma_load_2d_pair(st, &tA, ac, row, bar);
-                    tma_load_2d_pair(st + kChunk, &tA, ac + 64, row, bar);
-                    tma_load_2d_pair(st + kOpBytes, &tB, bc, row, bar);
-                    tma_load_2d_pair(st + kOpBytes + kChunk, &tB, bc + 64, row, bar);
-                }
-                __syncwarp();
+                if (tail)
+                    mbar_arrive_expect_tx_if(one, bars.tail + r.s, kStage);
+                else if (leader)
+                    mbar_arrive_expect_tx_if(one, bars.full + r.s, 2 * kStage);
+                else if (one)
+                    mbar_arrive_cluster_relaxed(bar);
+                tma_load_2d_pair_if(one, st, &tA, ac, row, bar);
+                tma_load_2d_pair_if(one, st + kChunk, &tA, ac + 64, row, bar);
+                tma_load_2d_pair_if(one, st + kOpBytes, &tB, bc, row, bar);
+                tma_load_2d_pair_if(one, st + kOpBytes + kChunk, &tB, bc + 64, row, bar);
                 r.next<S>();
             }
         }
@@ -343,7 +333,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
         if (leader) {
             // ------------------------------------------------- MMA issuer
             constexpr uint32_t idesc = Elem<T>::idesc | ((256u >> 3) << 17) | kTransA | kTransB;
-            const bool one = elect_one();
+            const uint32_t one = elect_one();
             const uint64_t ad0 = sdesc_sw128_mn(smem_u32(smem), kChunk);
             const uint64_t bd0 = sdesc_sw128_mn(smem_u32(smem + kOpBytes), kChunk);
             Ring r;
@@ -366,21 +356,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
                     tc_fence_after();
                     const uint32_t at = static_cast<uint32_t>(r.s) * (kStage >> 4);
                     const int rest = g.rows - k;
-                    if (one) {
 #pragma unroll
-                        for (int kk = 0; kk < kBK / 16; ++kk)  // 16 rows per MMA
-                            if (kk * 16 < rest)
-                                mma_bf16_pair(d, ad0 + (at + kk * (2048 >> 4)), bd0 + (at + kk * (2048 >> 4)), idesc,
-                                              (k | kk) != 0 ? 1u : 0u);
-                        mma_commit_pair(bars.empty + r.s, 0x3);
-                    }
-                    __syncwarp();
+                    for (int kk = 0; kk < kBK / 16; ++kk)  // 16 rows per MMA
+                        if (kk * 16 < rest)
+                            mma_bf16_pair_if(one, d, ad0 + (at + kk * (2048 >> 4)), bd0 + (at + kk * (2048 >> 4)),
+                                             idesc, (k | kk) != 0 ? 1u : 0u);
+                    mma_commit_pair_if(one, bars.empty + r.s, 0x3);
                     issued = true;
                     r.next<S>();
                 }
                 if (timed_out) break;
-                if (one) mma_commit_pair(bars.tfull + acc.i, 0x3);
-                __syncwarp();
+                mma_commit_pair_if(one, bars.tfull + acc.i, 0x3);
                 acc.next();
             }
             if ((timed_out || *abort_flag) && issued && one) {
