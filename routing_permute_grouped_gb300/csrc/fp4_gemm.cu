@@ -64,7 +64,6 @@ constexpr int kThreads = 32 * (kEpi0 + kEpiWarps);
 
 struct ScaleBars {
     uint64_t raw_full[kRaw], raw_empty[kRaw];  // groups in shared memory
-    uint64_t full[5];                          // tensor-memory buffers written
 };
 constexpr int kSmem =
     1024 + kStages * kStage + kRaw * kRawRows + kEpiStage + 1024 + static_cast<int>(sizeof(RaggedTiles));
@@ -102,13 +101,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(sb.raw_full + i, 32);  // every lane's copies
             mbar_init(sb.raw_empty + i, 4);  // every layout warp
         }
-        for (int i = 0; i < SC::bufs; ++i) {
-            mbar_init(sb.full + i, 8);  // every layout warp of both CTAs
-        }
         fence_mbar_init();
     }
     __syncwarp();
-    pair_start(bars, 1, warp);
+    // a step is full when its codes have landed and the four layout warps of
+    // both CTAs have written its scales
+    pair_start(bars, 9, warp);
     if (warp == 2) ragged_tiles_build<kTN>(args, tiles, panels, lane);
     tc_fence_before();
     __syncthreads();
@@ -164,7 +162,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             Ring r;
             Acc acc;
             Ring buf;  // scale buffer
-            bool issued = false;
+            bool issued = false, ready = false;
             for (int t = first; t < total && !timed_out; t += stride) {
                 const RaggedItem it = uniform(ragged_item<kTN>(args, tiles, panels, t));
                 const uint32_t n = (it.rows + 31) & ~31;
@@ -175,33 +173,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 const uint32_t d = tmem_base + static_cast<uint32_t>(acc.i * kTN);
                 for (int k = 0; k < steps; ++k) {
-                    if (!warp_wait(bars.full + r.s, r.ph, abort_flag)) {
-                        timed_out = true;
-                        break;
-                    }
-                    const uint32_t at = static_cast<uint32_t>(r.s) * (kStage >> 4);
-                    const int left = args.K - k * kStep;
-                    if (!warp_wait(sb.full + buf.s, buf.ph, abort_flag)) {
+                    if (!ready && !warp_wait(bars.full + r.s, r.ph, abort_flag)) {
                         timed_out = true;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sc = tmem_base + kScaleCol + static_cast<uint32_t>(buf.s) * SC::cols;
+                    // the next stage is looked at while this one's MMAs are
+                    // issued: the issue, not the tensor pipe, sets the pace
+                    const Ring next = r.after<S>();
+                    const bool peek = mbar_test_wait(bars.full + next.s, next.ph);
+                    const uint32_t at = static_cast<uint32_t>(r.s) * (kStage >> 4);
+                    const uint32_t sa = tmem_base + kScaleCol + static_cast<uint32_t>(buf.s) * SC::cols;
+                    const int left = args.K - k * kStep;
+                    if (one) {
+                        auto mma = [&](int kk) {  // 64 elements of each 128-byte row
+                            const int word = NV ? kk : kk / 2;
+                            const uint32_t byte = NV ? 0u : static_cast<uint32_t>(kk & 1) * 2u;
+                            mma_e2m1_pair<NV>(d, wd0 + (at + kk * 2), xd0 + (at + kk * 2),
+                                              idesc | (byte << 4) | (byte << 29), sa + word * 4,
+                                              sa + SC::words * 4 + word * 8, (k | kk) != 0 ? 1u : 0u);
+                        };
+                        if (left >= kStep) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {  // 64 elements of each 128-byte row
-                        const int word = NV ? kk : kk / 2;
-                        const uint32_t byte = NV ? 0u : static_cast<uint32_t>(kk & 1) * 2u;
-                        if (kk * 64 < left)
-                            mma_e2m1_pair_if<NV>(one, d, wd0 + (at + kk * 2), xd0 + (at + kk * 2),
-                                                 idesc | (byte << 4) | (byte << 29), sc + word * 4,
-                                                 sc + SC::words * 4 + word * 8, (k | kk) != 0 ? 1u : 0u);
+                            for (int kk = 0; kk < 4; ++kk) mma(kk);
+                        } else {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                if (kk * 64 < left) mma(kk);
+                        }
+                        // read by the scale warps too: a step's scale buffer is
+                        // free with its stage
+                        mma_commit_pair(bars.empty + r.s, 0x3);
                     }
-                    // read by the scale warps too: a step's scale buffer is free
-                    // with its stage
-                    mma_commit_pair_if(one, bars.empty + r.s, 0x3);
+                    ready = __all_sync(0xFFFFFFFFu, peek);
                     issued = true;
                     buf.next<SC::bufs>();
-                    r.next<S>();
+                    r = next;
                 }
                 if (timed_out) break;
                 mma_commit_pair_if(one, bars.tfull + acc.i, 0x3);
@@ -264,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t ph = 0;
         Ring buf;
         // the stage of the step whose buffer is written next, SC::bufs steps ago
-        Ring old;
+        Ring old, cur;  // cur: its own
         int fresh = SC::bufs;  // buffers not yet written
         for (int t = first; t < total && !timed_out; t += stride) {
             for (int g = 0; g < groups; ++g) {
@@ -329,9 +336,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         // nothing
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(sb.full + buf.s), 0));
+                        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.full + cur.s), 0));
                     }
                     buf.next<SC::bufs>();
+                    cur.next<S>();
                     if (fresh)
                         --fresh;
                     else

@@ -214,6 +214,12 @@ struct Ring {  // stage and its parity
             ph ^= 1u;
         }
     }
+    template <int S>
+    __device__ __forceinline__ Ring after() const {
+        Ring r = *this;
+        r.next<S>();
+        return r;
+    }
 };
 
 struct Acc {  // accumulator and its parity

@@ -147,7 +147,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
             constexpr uint32_t kWStep = (WT ? 2048 : 32) >> 4;  // 16 elements of the sum
             Ring r;
             Acc acc;
-            bool issued = false;
+            bool issued = false, ready = false;
             for (int t = first; t < total && !timed_out; t += stride) {
                 const RaggedItem it = uniform(ragged_item<kTN>(args, tiles, panels, t));
                 const uint32_t n = (it.rows + 31) & ~31;
@@ -159,19 +159,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
                 tc_fence_after();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(acc.i * kTN);
                 for (int k = 0; k < steps; ++k) {
-                    if (!warp_wait(bars.full + r.s, r.ph, abort_flag)) {
+                    if (!ready && !warp_wait(bars.full + r.s, r.ph, abort_flag)) {
                         timed_out = true;
                         break;
                     }
                     tc_fence_after();
+                    const Ring next = r.after<S>();
+                    const bool peek = mbar_test_wait(bars.full + next.s, next.ph);
                     const uint32_t at = static_cast<uint32_t>(r.s) * (kStage >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
                         mma_bf16_pair_if(one, d, wd0 + (at + kk * kWStep), xd0 + (at + kk * 2), idesc,
                                          (k | kk) != 0 ? 1u : 0u);
                     mma_commit_pair_if(one, bars.empty + r.s, 0x3);
+                    ready = __all_sync(0xFFFFFFFFu, peek);
                     issued = true;
-                    r.next<S>();
+                    r = next;
                 }
                 if (timed_out) break;
                 mma_commit_pair_if(one, bars.tfull + acc.i, 0x3);
@@ -338,7 +341,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
             const uint64_t bd0 = sdesc_sw128_mn(smem_u32(smem + kOpBytes), kChunk);
             Ring r;
             Acc acc;
-            bool issued = false;
+            bool issued = false, ready = false;
             for (int t = first; t < total && !timed_out; t += stride) {
                 const GradTile g = grad_tile(args, t);
                 if (g.rows == 0) continue;  // the epilogue writes zeros
@@ -349,11 +352,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
                 tc_fence_after();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(acc.i * 256);
                 for (int k = 0; k < g.rows; k += kBK) {
-                    if (!warp_wait(bars.full + r.s, r.ph, abort_flag)) {
+                    if (!ready && !warp_wait(bars.full + r.s, r.ph, abort_flag)) {
                         timed_out = true;
                         break;
                     }
                     tc_fence_after();
+                    const Ring next = r.after<S>();
+                    const bool peek = mbar_test_wait(bars.full + next.s, next.ph);
                     const uint32_t at = static_cast<uint32_t>(r.s) * (kStage >> 4);
                     const int rest = g.rows - k;
 #pragma unroll
@@ -362,8 +367,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
                             mma_bf16_pair_if(one, d, ad0 + (at + kk * (2048 >> 4)), bd0 + (at + kk * (2048 >> 4)),
                                              idesc, (k | kk) != 0 ? 1u : 0u);
                     mma_commit_pair_if(one, bars.empty + r.s, 0x3);
+                    ready = __all_sync(0xFFFFFFFFu, peek);
                     issued = true;
-                    r.next<S>();
+                    r = next;
                 }
                 if (timed_out) break;
                 mma_commit_pair_if(one, bars.tfull + acc.i, 0x3);
