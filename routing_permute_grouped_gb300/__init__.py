@@ -203,26 +203,39 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _addr(t: Optional[torch.Tensor]):
+    """_ptr as a plain integer: short calls are bound by the host, and a ctypes
+    object per pointer costs about as much as the checks."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
+
+
 def _rows(t: torch.Tensor):
-    """Pointer and row stride of a [rows, columns] CUDA tensor whose rows are
+    """Address and row stride of a [rows, columns] CUDA tensor whose rows are
     contiguous (the stride between rows is free)."""
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError("expected a 2D tensor with contiguous rows")
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-def _dtype(*tensors) -> int:
-    """The library's code of the tensors' common 16-bit type."""
-    if any(t.dtype != tensors[0].dtype for t in tensors) or tensors[0].dtype not in _DTYPES:
-        raise ValueError("expected bf16 or fp16 tensors of one type")
-    return _DTYPES[tensors[0].dtype]
+def _dtype(t: torch.Tensor) -> int:
+    """The library's code of a 16-bit type."""
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError("expected a bf16 or fp16 tensor")
+    return code
 
 
 def _expect(t: Optional[torch.Tensor], name: str, dtype, shape) -> None:
     """The C side sees only a pointer: what it reads there is checked here."""
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
+    if t is not None and (t.dtype != dtype or t.shape != shape):
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
@@ -570,8 +583,8 @@ def moe_grouped_gemm(x, w, offsets, y, row_scale=None, w_transposed: bool = Fals
     _expect(offsets, "offsets", torch.int32, (E + 1,))
     _expect(row_scale, "row_scale", torch.float32, (R,))
     (px, ldx), (py, ldy) = _rows(x), _rows(y)
-    _check(load().moe_grouped_gemm(_dtype(x), R, N, K, E, px, ldx, _ptr(w), int(w_transposed),
-                                   _ptr(offsets), _ptr(row_scale), py, ldy, _ptr(status),
+    _check(load().moe_grouped_gemm(_dtype(x), R, N, K, E, px, ldx, _addr(w), int(w_transposed),
+                                   _addr(offsets), _addr(row_scale), py, ldy, _addr(status),
                                    _stream(stream)))
 
 
@@ -583,13 +596,15 @@ def moe_grouped_wgrad(a, b, offsets, out, status=None, stream=None) -> None:
     _expect(out, "out", a.dtype, (E, M, N))
     _expect(offsets, "offsets", torch.int32, (E + 1,))
     (pa, lda), (pb, ldb) = _rows(a), _rows(b)
-    _check(load().moe_grouped_wgrad(_dtype(a), R, M, N, E, pa, lda, pb, ldb, _ptr(offsets),
-                                    _ptr(out), _ptr(status), _stream(stream)))
+    _check(load().moe_grouped_wgrad(_dtype(a), R, M, N, E, pa, lda, pb, ldb, _addr(offsets),
+                                    _addr(out), _addr(status), _stream(stream)))
 
 
 def moe_fp4_scale_stride(fmt: int, K: int) -> int:
     """Bytes of one row's block scales (0 for an invalid format or K)."""
-    return int(load().moe_fp4_scale_stride(fmt, K))
+    if fmt not in (FP4_MX, FP4_NV) or K <= 0 or K % 32:
+        return 0
+    return (K // (32 if fmt == FP4_MX else 16) + 15) // 16 * 16
 
 
 def moe_quantize_fp4(fmt: int, x, codes, scales, tensor_scale=None, src=None, src_div: int = 1,
@@ -604,9 +619,9 @@ def moe_quantize_fp4(fmt: int, x, codes, scales, tensor_scale=None, src=None, sr
     _expect(tensor_scale, "tensor_scale", torch.float32, (1,))
     _expect(x, "x", x.dtype, (x.shape[0], 2 * K if swiglu else K))
     px, ldx = _rows(x)
-    _check(load().moe_quantize_fp4(fmt, _dtype(x), rows, K, px, x.shape[0], ldx, _ptr(src),
-                                   src_div, int(swiglu), _ptr(tensor_scale), _ptr(codes),
-                                   _ptr(scales), _stream(stream)))
+    _check(load().moe_quantize_fp4(fmt, _dtype(x), rows, K, px, x.shape[0], ldx, _addr(src),
+                                   src_div, int(swiglu), _addr(tensor_scale), _addr(codes),
+                                   _addr(scales), _stream(stream)))
 
 
 def moe_dequantize_fp4(fmt: int, codes, scales, out, tensor_scale=None, stream=None) -> None:
@@ -616,8 +631,8 @@ def moe_dequantize_fp4(fmt: int, codes, scales, out, tensor_scale=None, stream=N
     _expect(scales, "scales", torch.uint8, (rows, moe_fp4_scale_stride(fmt, K)))
     _expect(tensor_scale, "tensor_scale", torch.float32, (1,))
     po, ldo = _rows(out)
-    _check(load().moe_dequantize_fp4(fmt, _dtype(out), rows, K, _ptr(codes), _ptr(scales),
-                                     _ptr(tensor_scale), po, ldo, _stream(stream)))
+    _check(load().moe_dequantize_fp4(fmt, _dtype(out), rows, K, _addr(codes), _addr(scales),
+                                     _addr(tensor_scale), po, ldo, _stream(stream)))
 
 
 def moe_grouped_gemm_fp4(fmt: int, x_codes, x_scales, w_codes, w_scales, offsets, y, x_scale=None,
@@ -637,9 +652,9 @@ def moe_grouped_gemm_fp4(fmt: int, x_codes, x_scales, w_codes, w_scales, offsets
     _expect(w_scale, "w_scale", torch.float32, (E,))
     _expect(row_scale, "row_scale", torch.float32, (R,))
     py, ldy = _rows(y)
-    _check(load().moe_grouped_gemm_fp4(fmt, R, N, K, E, _ptr(x_codes), _ptr(x_scales),
-                                       _ptr(w_codes), _ptr(w_scales), _ptr(offsets), _ptr(x_scale),
-                                       _ptr(w_scale), _ptr(row_scale), py, ldy, _ptr(status),
+    _check(load().moe_grouped_gemm_fp4(fmt, R, N, K, E, _addr(x_codes), _addr(x_scales),
+                                       _addr(w_codes), _addr(w_scales), _addr(offsets), _addr(x_scale),
+                                       _addr(w_scale), _addr(row_scale), py, ldy, _addr(status),
                                        _stream(stream)))
 
 

@@ -11,8 +11,13 @@
 // fp32 operation with one rounding (the power-of-two steps have none), so the
 // codes are fixed by the inputs alone.
 //
-// One thread quantises one block; amax is taken on the bit patterns, where
-// NaN and infinity order above every number, and marks the block's scale NaN.
+// Both kernels are bound by memory.  A thread takes 8 elements (16 bytes of the
+// 16-bit side, 4 of codes), so that every access of a warp is contiguous; a
+// team of 8 to 256 threads (about a quarter of the row's 8-element pieces)
+// takes a row, without divisions by the row length.  Instructions come next: a
+// block's amax is taken on the 16-bit patterns, two at a time, where NaN and
+// infinity order above every number (they mark the block's scale NaN), over its
+// 4 (MX) or 2 (NV) threads by shuffles, and bf16 rows are scaled in pairs.
 #include <cuda_runtime.h>
 
 #include "../../include/moe.h"
@@ -34,6 +39,7 @@ struct QuantArgs {
     int32_t src_div;
     int32_t K;           // output columns
     int32_t stride;      // scale bytes per row
+    int32_t team;        // threads per row
     const float* tensor_scale;
     uint8_t* codes;
     uint8_t* scales;
@@ -41,128 +47,198 @@ struct QuantArgs {
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
-template <typename T, int N>
-__device__ __forceinline__ void load_values(const T* p, float (&v)[N]) {
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void widen2(__nv_bfloat16, uint32_t u, float& lo, float& hi) {
+    lo = __uint_as_float(u << 16);
+    hi = __uint_as_float(u & 0xFFFF0000u);
+}
+__device__ __forceinline__ void widen2(__half, uint32_t u, float& lo, float& hi) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+    lo = f.x;
+    hi = f.y;
+}
+template <typename T>
+__device__ __forceinline__ void widen8(const uint4& u, float (&v)[8]) {
+    widen2(T(), u.x, v[0], v[1]);
+    widen2(T(), u.y, v[2], v[3]);
+    widen2(T(), u.z, v[4], v[5]);
+    widen2(T(), u.w, v[6], v[7]);
+}
+__device__ __forceinline__ float widen1(__nv_bfloat16, uint32_t bits) { return __uint_as_float(bits << 16); }
+__device__ __forceinline__ float widen1(__half, uint32_t bits) {
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+}
+// Bit pattern of infinity: magnitudes from here on are not numbers
+template <typename T>
+constexpr uint32_t kInf = 0x7F80u;
+template <>
+constexpr uint32_t kInf<__half> = 0x7C00u;
+
+// Eight values times a power of two, as fp32.  bf16 pairs are multiplied as they
+// are: the result is exact or too small to matter (below 2^-126, code 0).
+__device__ __forceinline__ void scale8(__nv_bfloat16, const uint4& u, float inv, float (&v)[8]) {
+    const __nv_bfloat162 f = __float2bfloat162_rn(inv);
+    uint4 r;
+    const uint32_t* a = &u.x;
+    uint32_t* b = &r.x;
 #pragma unroll
-    for (int i = 0; i < N; i += 8) {
-        const uint4 u = __ldcg(reinterpret_cast<const uint4*>(p + i));
-        const T* t = reinterpret_cast<const T*>(&u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i + j] = to_float(t[j]);
+    for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 m = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(a + j), f);
+        b[j] = *reinterpret_cast<const uint32_t*>(&m);
     }
+    widen8<__nv_bfloat16>(r, v);
+}
+__device__ __forceinline__ void scale8(__half, const uint4& u, float inv, float (&v)[8]) {
+    widen8<__half>(u, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= inv;
+}
+
+// Pieces of 8 elements that a thread has in flight
+constexpr int kPieces = 8;
+
+// A team's row and the thread's place in it; false past the last row.
+__device__ __forceinline__ bool team_row(int team, int64_t rows, int64_t& row, int& lane) {
+    const int per = 256 / team;
+    row = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / team;
+    lane = threadIdx.x & (team - 1);
+    return row < rows;
 }
 
 template <typename T, bool NV, bool SWIGLU>
 __global__ void __launch_bounds__(256) k_quantize_fp4(const QuantArgs a) {
-    constexpr int B = NV ? 16 : 32;
+    constexpr int kShare = NV ? 2 : 4;  // threads of a block of elements
     pdl_trigger();
     pdl_wait();
-    const int64_t total = a.rows * a.stride;
-    const int nb = a.K / B;
+    int64_t r;
+    int me;
+    const bool real = team_row(a.team, a.rows, r, me);  // all lanes stay for the shuffles
+    const int pieces = a.K / 8;
     const float g = NV && a.tensor_scale ? ld_dep(a.tensor_scale) : 1.0f;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t r = i / a.stride;
-        const int b = static_cast<int>(i - r * a.stride);
-        if (b >= nb) {  // the padding of a scale row
-            a.scales[i] = 0;
-            continue;
-        }
-        int64_t xr = r;
-        bool have = true;
-        if (a.src) {
-            const int s = ld_dep(a.src + r);
-            xr = s / a.src_div;
-            have = s >= 0 && xr < a.x_rows;
-        }
-        float v[B];
+    int64_t xr = r;
+    bool have = real;
+    if (real && a.src) {
+        const int s = ld_dep(a.src + r);
+        xr = s / a.src_div;
+        have = s >= 0 && xr < a.x_rows;
+    }
+    const T* row = static_cast<const T*>(a.x) + (have ? xr * a.ldx : 0);
+    uint8_t* scales = a.scales + (real ? r * a.stride : 0);
+    uint32_t* codes = reinterpret_cast<uint32_t*>(a.codes + (real ? r * (a.K / 2) : 0));
+    if (real)
+        for (int i = pieces / kShare + me; i < a.stride; i += a.team) scales[i] = 0;  // the padding
+    for (int p0 = 0; p0 < pieces; p0 += kPieces * a.team) {
+        uint4 in[kPieces], up[SWIGLU ? kPieces : 1];
 #pragma unroll
-        for (int j = 0; j < B; ++j) v[j] = 0.0f;
-        if (have) {
-            const T* row = static_cast<const T*>(a.x) + xr * a.ldx;
-            if constexpr (SWIGLU) {  // gate and up columns interleaved per 128
-                const int c = b * B;
-                float u[B];
-                const T* p = row + (c >> 7) * 256 + (c & 127);
-                load_values<T, B>(p, v);
-                load_values<T, B>(p + 128, u);
+        for (int i = 0; i < kPieces; ++i) {
+            const int p = p0 + i * a.team + me;
+            in[i] = make_uint4(0, 0, 0, 0);
+            if constexpr (SWIGLU) up[i] = in[i];
+            if (have && p < pieces) {
+                if constexpr (SWIGLU) {  // gate and up columns interleaved per 128
+                    const T* q = row + (p >> 4) * 256 + (p & 15) * 8;
+                    in[i] = __ldcg(reinterpret_cast<const uint4*>(q));
+                    up[i] = __ldcg(reinterpret_cast<const uint4*>(q + 128));
+                } else {
+                    in[i] = __ldcg(reinterpret_cast<const uint4*>(row) + p);
+                }
+            }
+        }
 #pragma unroll
-                for (int j = 0; j < B; ++j) v[j] = to_float(from_float<T>(silu(v[j]) * u[j]));
+        for (int i = 0; i < kPieces; ++i) {
+            if (p0 + i * a.team >= pieces) break;  // the same for every team
+            const int p = p0 + i * a.team + me;
+            float v[8];
+            if constexpr (SWIGLU) {
+                float u[8];
+                widen8<T>(in[i], v);
+                widen8<T>(up[i], u);
+                uint32_t* h = &in[i].x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    h[j] = pack2(T(), silu(v[2 * j]) * u[2 * j], silu(v[2 * j + 1]) * u[2 * j + 1]);
+            }
+            constexpr uint32_t kAbs = 0x7FFF7FFFu;
+            uint32_t top2 = max_u16x2(max_u16x2(in[i].x & kAbs, in[i].y & kAbs), max_u16x2(in[i].z & kAbs, in[i].w & kAbs));
+#pragma unroll
+            for (int o = 1; o < kShare; o <<= 1) top2 = max_u16x2(top2, __shfl_xor_sync(0xFFFFFFFFu, top2, o));
+            const uint32_t bits = max(top2 & 0xFFFFu, top2 >> 16);
+            uint32_t code, q = 0;
+            if (bits >= kInf<T>) {  // a NaN or infinity: the whole block is NaN
+                code = NV ? 0x7Fu : 0xFFu;
+            } else if constexpr (NV) {
+                code = f32_to_e4m3(fminf(widen1(T(), bits) / (g * 6.0f), 448.0f));
+                const float s = e4m3_to_f32(code) * g;
+                if (s > 0.0f) {
+                    widen8<T>(in[i], v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] /= s;
+                    q = f32x8_to_e2m1(v);
+                }
             } else {
-                load_values<T, B>(row + static_cast<int64_t>(b) * B, v);
+                // amax = 1.m * 2^(e - 127) <= 1.5 * 2^2 * 2^(code - 127)
+                const uint32_t top = __float_as_uint(widen1(T(), bits));
+                const int c = static_cast<int>(top >> 23) - ((top & 0x7FFFFFu) <= 0x400000u ? 2 : 1);
+                code = top ? static_cast<uint32_t>(max(c, 0)) : 127u;
+                scale8(T(), in[i], __uint_as_float((254u - code) << 23), v);  // times 2^(127 - code)
+                q = f32x8_to_e2m1(v);
+            }
+            if (real && p < pieces) {
+                if ((me & (kShare - 1)) == 0) scales[p / kShare] = static_cast<uint8_t>(code);
+                codes[p] = q;
             }
         }
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < B; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-        uint32_t code;
-        uint32_t q[B / 8];
-        if (top >= 0x7F800000u) {  // a NaN or infinity: the whole block is NaN
-            code = NV ? 0x7Fu : 0xFFu;
-#pragma unroll
-            for (int j = 0; j < B / 8; ++j) q[j] = 0;
-        } else if constexpr (NV) {
-            code = f32_to_e4m3(fminf(__uint_as_float(top) / (g * 6.0f), 448.0f));
-            const float s = e4m3_to_f32(code) * g;
-#pragma unroll
-            for (int j = 0; j < B / 8; ++j) {
-                q[j] = 0;
-                if (s > 0.0f)
-#pragma unroll
-                    for (int p = 0; p < 4; ++p)
-                        q[j] |= f32x2_to_e2m1x2(v[8 * j + 2 * p] / s, v[8 * j + 2 * p + 1] / s) << (8 * p);
-            }
-        } else {
-            // amax = 1.m * 2^(e - 127) <= 1.5 * 2^2 * 2^(code - 127)
-            const int e = static_cast<int>(top >> 23);
-            const int c = e - ((top & 0x7FFFFFu) <= 0x400000u ? 2 : 1);
-            code = top ? static_cast<uint32_t>(max(c, 0)) : 127u;
-            const float inv = __uint_as_float((254u - code) << 23);  // 2^(127 - code)
-#pragma unroll
-            for (int j = 0; j < B / 8; ++j) {
-                q[j] = 0;
-#pragma unroll
-                for (int p = 0; p < 4; ++p)
-                    q[j] |= f32x2_to_e2m1x2(v[8 * j + 2 * p] * inv, v[8 * j + 2 * p + 1] * inv) << (8 * p);
-            }
-        }
-        a.scales[i] = static_cast<uint8_t>(code);
-        uint8_t* out = a.codes + r * (a.K / 2) + static_cast<int64_t>(b) * (B / 2);
-        if constexpr (NV)
-            *reinterpret_cast<uint2*>(out) = make_uint2(q[0], q[1]);
-        else
-            *reinterpret_cast<uint4*>(out) = make_uint4(q[0], q[1], q[2], q[3]);
     }
 }
 
-// Sixteen elements per thread: value = e2m1 * scale (* g), one rounding each
+// value = e2m1 * scale (* g), one rounding each
 template <typename T, bool NV>
 __global__ void __launch_bounds__(256)
-    k_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, int stride,
+    k_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, int stride, int team,
                      const float* tensor_scale, T* out, int64_t ldo) {
+    constexpr int kShare = NV ? 2 : 4;
     pdl_trigger();
     pdl_wait();
-    const int per = K / 16;
-    const int64_t total = rows * per;
+    int64_t r;
+    int me;
+    if (!team_row(team, rows, r, me)) return;
+    const int pieces = K / 8;
     const float g = NV && tensor_scale ? ld_dep(tensor_scale) : 1.0f;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t r = i / per;
-        const int c = static_cast<int>(i - r * per) * 16;
-        const uint2 q = __ldcg(reinterpret_cast<const uint2*>(codes + r * (K / 2) + c / 2));
-        const uint32_t code = ld_dep(scales + r * stride + c / (NV ? 16 : 32));
-        const float s = NV ? e4m3_to_f32(code) : e8m0_to_f32(code);
-        T v[16];
+    const uint32_t* row = reinterpret_cast<const uint32_t*>(codes + r * (K / 2));
+    for (int p0 = 0; p0 < pieces; p0 += kPieces * team) {
+        uint32_t q[kPieces], code[kPieces];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float2 f = e2m1x2_to_f32x2(((j < 4 ? q.x : q.y) >> (8 * (j & 3))) & 0xFFu);
-            v[2 * j] = from_float<T>(f.x * s * g);
-            v[2 * j + 1] = from_float<T>(f.y * s * g);
+        for (int i = 0; i < kPieces; ++i) {
+            const int p = p0 + i * team + me;
+            q[i] = p < pieces ? ld_dep(row + p) : 0u;
+            code[i] = p < pieces ? ld_dep(scales + r * stride + p / kShare) : 0u;
         }
-        uint4* o = reinterpret_cast<uint4*>(out + r * ldo + c);
-        o[0] = reinterpret_cast<const uint4*>(v)[0];
-        o[1] = reinterpret_cast<const uint4*>(v)[1];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int p = p0 + i * team + me;
+            if (p >= pieces) break;
+            const float s = NV ? e4m3_to_f32(code[i]) : e8m0_to_f32(code[i]);
+            uint32_t h[4], v[4];
+            e2m1x8_to_f16x2(q[i], h);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(h + j));
+                v[j] = NV ? pack2(T(), f.x * s * g, f.y * s * g) : pack2(T(), f.x * s, f.y * s);
+            }
+            *reinterpret_cast<uint4*>(out + r * ldo + p * 8) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
     }
+}
+
+// Threads per row: an eighth of its pieces, rounded up to a power of two.
+int team_of(int K) {
+    int team = 8;
+    while (team < 256 && team * kPieces < K / 8) team *= 2;
+    return team;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -172,15 +248,11 @@ moe_status_t check_fp4(int32_t fmt, int64_t rows, int32_t K) {
         return set_last_error(MOE_ERR_INVALID_ARG, "format = %d is neither MX (0) nor NV (1)", fmt);
     if (rows < 0 || K <= 0) return set_last_error(MOE_ERR_INVALID_ARG, "rows must be >= 0 and K > 0");
     if (K % 32) return set_last_error(MOE_ERR_UNSUPPORTED, "K = %d is not a multiple of 32", K);
-    if (rows > (1ll << 40) / K) return set_last_error(MOE_ERR_UNSUPPORTED, "tensor too large");
+    if (rows > (1ll << 30)) return set_last_error(MOE_ERR_UNSUPPORTED, "more than 2^30 rows");
     return MOE_OK;
 }
 
-unsigned blocks_for(int64_t threads) {
-    const int64_t b = (threads + 255) / 256;
-    const int64_t most = static_cast<int64_t>(num_sms()) * 64;
-    return static_cast<unsigned>(b < most ? b : most);
-}
+int64_t blocks_for(int64_t rows, int team) { return (rows + 256 / team - 1) / (256 / team); }
 
 }  // namespace
 }  // namespace moe
@@ -225,7 +297,8 @@ extern "C" moe_status_t moe_quantize_fp4(int32_t fmt, int32_t dtype, int64_t row
     a.tensor_scale = tensor_scale;
     a.codes = static_cast<uint8_t*>(codes);
     a.scales = static_cast<uint8_t*>(scales);
-    const dim3 grid(blocks_for(rows * a.stride));
+    a.team = team_of(K);
+    const dim3 grid(static_cast<unsigned>(blocks_for(rows, a.team)));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool nv = fmt == MOE_FP4_NV, bf = dtype == MOE_DTYPE_BF16;
     auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, st, a); };
@@ -254,11 +327,12 @@ extern "C" moe_status_t moe_dequantize_fp4(int32_t fmt, int32_t dtype, int64_t r
     if (ldo < K || ldo % 8)
         return set_last_error(MOE_ERR_INVALID_ARG, "the row stride must cover the row and be a multiple of 8 elements");
     const int stride = static_cast<int>(moe_fp4_scale_stride(fmt, K));
-    const dim3 grid(blocks_for(rows * (K / 16)));
+    const int team = team_of(K);
+    const dim3 grid(static_cast<unsigned>(blocks_for(rows, team)));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     auto go = [&](auto kernel, auto* o) {
         return launch_pdl(kernel, grid, dim3(256), 0, st, static_cast<const uint8_t*>(codes),
-                          static_cast<const uint8_t*>(scales), rows, K, stride, tensor_scale, o, ldo);
+                          static_cast<const uint8_t*>(scales), rows, K, stride, team, tensor_scale, o, ldo);
     };
     const bool nv = fmt == MOE_FP4_NV;
     cudaError_t e;

@@ -309,20 +309,30 @@ cudaError_t launch_pairs(void (*kernel)(KArgs...), int64_t items, int threads, i
 }
 
 // ---------------------------------------------------------- 4-bit values --
-// Two e2m1 codes (low nibble first) -> two floats; every e2m1 value is an f16
-// value.
-__device__ __forceinline__ float2 e2m1x2_to_f32x2(uint32_t byte) {
-    uint32_t h;
-    asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h) : "r"(byte));
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+// Eight e2m1 codes (lowest nibble first) -> four pairs of f16; every e2m1 value
+// is an f16 value.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t q, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(q));
 }
-// The nearest e2m1 codes of two values (v0 in the low nibble), ties to even,
-// saturating at +-6.
-__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float v0, float v1) {
+// The nearest e2m1 codes of eight values (v[0] in the lowest nibble), ties to
+// even, saturating at +-6.
+__device__ __forceinline__ uint32_t f32x8_to_e2m1(const float (&v)[8]) {
     uint32_t r;
-    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
         : "=r"(r)
-        : "f"(v1), "f"(v0));
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return r;
 }
 // Power-of-two block scale 2^(code - 127); code 255 is NaN.

@@ -112,3 +112,6 @@ def test_scale_stride(lib):
     assert [stride(0, k) for k in (32, 512, 544, 7168)] == [16, 16, 32, 224]
     assert [stride(1, k) for k in (32, 256, 544, 7168)] == [16, 16, 48, 448]
     assert stride(0, 40) == 0 and stride(2, 64) == 0 and stride(1, 0) == 0
+    for fmt in (-1, 0, 1, 2):
+        for k in (-32, 0, 31, 32, 96, 160, 512, 544, 2080, 7168):
+            assert stride(fmt, k) == lib.moe_fp4_scale_stride(fmt, k)
