@@ -760,7 +760,8 @@ moe_status_t moe_layer_bwd(const moe_config_t *cfg, const moe_weights_t *w,
  * padded_offsets of moe_build_offsets).  Groups may have any size, none, any
  * start and gaps between them; rows outside every group are left untouched in
  * the output.  A group that does not lie in [0, R] or runs backwards counts as
- * empty and sets MOE_DEVERR_SEGMENT in *status.
+ * empty and sets MOE_DEVERR_SEGMENT in *status.  With E = 1, offsets may be
+ * NULL: one group of all R rows.
  *
  * Shared rules: dtype is MOE_DTYPE_BF16 or MOE_DTYPE_F16 (operands and output
  * alike); R >= 0 rows (at most 2^30), 1 <= E <= 256; matrix dimensions are
@@ -852,6 +853,66 @@ moe_status_t moe_grouped_gemm_fp4(int32_t fmt, int64_t R, int32_t N, int32_t K, 
                                   const float *x_scale, const float *w_scale,
                                   const float *row_scale, void *y, int64_t ldy, uint32_t *status,
                                   void *stream);
+
+/* 4-bit expert weights of the layer (device pointers): moe_quantize_fp4 of the
+ * K-major rows that moe_pack_experts writes (gate and up interleaved per 128
+ * in W13), codes and block scales, with one fp32 tensor scale per expert for
+ * MOE_FP4_NV (NULL: 1).  The router stays bf16. */
+typedef struct {
+    int32_t fmt;         /* MOE_FP4_MX or MOE_FP4_NV */
+    const void *Wg_t;    /* router weight, K-major: bf16 [E, d] */
+    const float *bias;   /* per-expert logit bias fp32 [E], or NULL */
+    const void *W13q, *s13; const float *g13;    /* rows [E * 2*d_e, d]; fp32 [E] or NULL */
+    const void *W2q, *s2; const float *g2;       /* rows [E * d, d_e]; fp32 [E] or NULL */
+    const void *Ws13q, *ss13; const float *gs13; /* shared: rows [2*d_shared, d]; fp32 [1] or NULL */
+    const void *Ws2q, *ss2; const float *gs2;    /* shared: rows [d, d_shared]; fp32 [1] or NULL */
+    const float *x_scale; /* tensor scale of the token rows, fp32 [1] or NULL (1; NV) */
+    const float *h_scale; /* tensor scale of the SwiGLU outputs, fp32 [1] or NULL (1; NV) */
+} moe_weights_fp4_t;
+
+/* Offsets (bytes) of the moe_layer_fwd_fp4 workspace, multiples of 1024.  The
+ * rows are unpadded (A = T*k of them, moe_build_offsets_unpadded); codes are
+ * followed by their scales (rows x moe_fp4_scale_stride). */
+typedef struct {
+    size_t total;
+    size_t status;         /* uint32 device error word + build scratch */
+    size_t topk_idx;       /* int32 [T, k] */
+    size_t topk_w;         /* fp32 [T, k] */
+    size_t counts;         /* int32 [E] */
+    size_t group_offsets;  /* int32 [E + 1] */
+    size_t perm_row;       /* int32 [A] */
+    size_t row_src;        /* int32 [A] */
+    size_t row_gate;       /* fp32 [A] */
+    size_t router_partial; /* as in moe_workspace_layout_t */
+    size_t xq, xs;         /* token rows in expert order: [A, d] */
+    size_t gu;             /* bf16 [A, 2*d_e]: gate/up, interleaved per 128 */
+    size_t hq, hs;         /* SwiGLU outputs: [A, d_e] */
+    size_t y;              /* bf16 [A, d] */
+    size_t sxq, sxs;       /* shared expert (d_shared > 0): [T, d] */
+    size_t sgu;            /* bf16 [T, 2*d_shared] */
+    size_t shq, shs;       /* [T, d_shared] */
+    size_t ys;             /* bf16 [T, d] */
+} moe_workspace_layout_fp4_t;
+
+size_t moe_workspace_size_fp4(const moe_config_t *cfg, int32_t fmt);
+moe_status_t moe_workspace_layout_fp4(const moe_config_t *cfg, int32_t fmt,
+                                      moe_workspace_layout_fp4_t *layout);
+
+/* The layer on 4-bit experts and activations: router and unpadded offsets,
+ * then moe_quantize_fp4 as the permute (row_src), moe_grouped_gemm_fp4 for
+ * gate/up, moe_quantize_fp4 with the SwiGLU, moe_grouped_gemm_fp4 for the down
+ * projection with the routing weights, the shared expert by the same calls on
+ * one dense group, and moe_combine.  pad_multiple only has to be valid; the
+ * rows are not padded.  x, out bf16 [T, d]; ws at least
+ * moe_workspace_size_fp4(cfg, w->fmt) bytes. */
+moe_status_t moe_layer_fwd_fp4(const moe_config_t *cfg, const moe_weights_fp4_t *w, const void *x,
+                               void *out, void *ws, size_t ws_bytes, void *stream);
+
+/* moe_layer_fwd_fp4 for pre-routed input (as moe_layer_fwd_prerouted). */
+moe_status_t moe_layer_fwd_fp4_prerouted(const moe_config_t *cfg, const moe_weights_fp4_t *w,
+                                         const void *x, const int32_t *topk_idx,
+                                         const float *topk_w, void *out, void *ws, size_t ws_bytes,
+                                         void *stream);
 
 /* ---------------------------------------------------------- diagnostics -- */
 

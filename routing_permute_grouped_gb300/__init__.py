@@ -14,6 +14,7 @@ whole layer with one call.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -41,6 +42,8 @@ __all__ = [
     "moe_build_offsets_unpadded", "moe_grouped_gemm_swiglu_unpadded",
     "moe_grouped_gemm", "moe_grouped_wgrad", "FP4_MX", "FP4_NV", "FP4_FORMATS",
     "moe_fp4_scale_stride", "moe_quantize_fp4", "moe_dequantize_fp4", "moe_grouped_gemm_fp4",
+    "MoeWeightsFp4", "moe_workspace_size_fp4", "moe_workspace_layout_fp4", "moe_layer_fwd_fp4",
+    "moe_layer_fwd_fp4_prerouted", "grouped_linear",
 ]
 
 MOE_OK = 0
@@ -73,6 +76,12 @@ class MoeWeightsFp8(ctypes.Structure):
                 ("Wg_t", "bias", "W13q", "s13", "W2q", "s2", "Ws13q", "ss13", "Ws2q", "ss2")]
 
 
+class MoeWeightsFp4(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32)] + [(n, ctypes.c_void_p) for n in (
+        "Wg_t", "bias", "W13q", "s13", "g13", "W2q", "s2", "g2", "Ws13q", "ss13", "gs13", "Ws2q", "ss2",
+        "gs2", "x_scale", "h_scale")]
+
+
 class MoeWeightsBwd(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("W13t", "W2", "WgP", "Ws13t", "Ws2")]
 
@@ -92,6 +101,15 @@ _LAYOUT_FIELDS = ("total", "status", "topk_idx", "topk_w", "counts", "padded_off
 
 class _Layout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in _LAYOUT_FIELDS]
+
+
+_LAYOUT_FP4_FIELDS = ("total", "status", "topk_idx", "topk_w", "counts", "group_offsets", "perm_row",
+                      "row_src", "row_gate", "router_partial", "xq", "xs", "gu", "hq", "hs", "y",
+                      "sxq", "sxs", "sgu", "shq", "shs", "ys")
+
+
+class _LayoutFp4(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in _LAYOUT_FP4_FIELDS]
 
 
 _lib = None
@@ -173,6 +191,11 @@ def load():
                                             P]),
         "moe_dequantize_fp4": (ctypes.c_int, [I32, I32, I64, I32, P, P, P, P, I64, P]),
         "moe_grouped_gemm_fp4": (ctypes.c_int, [I32, I64, I32, I32, I32] + [P] * 9 + [I64, P, P]),
+        "moe_workspace_size_fp4": (SZ, [CP, I32]),
+        "moe_workspace_layout_fp4": (ctypes.c_int, [CP, I32, ctypes.POINTER(_LayoutFp4)]),
+        "moe_layer_fwd_fp4": (ctypes.c_int, [CP, ctypes.POINTER(MoeWeightsFp4), P, P, P, SZ, P]),
+        "moe_layer_fwd_fp4_prerouted": (ctypes.c_int, [CP, ctypes.POINTER(MoeWeightsFp4), P, P, P,
+                                                       P, P, SZ, P]),
         "moe_get_device_status": (ctypes.c_int, [P, ctypes.POINTER(ctypes.c_uint32), P]),
         "moe_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_uint64, P, P]),
         "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -658,6 +681,57 @@ def moe_grouped_gemm_fp4(fmt: int, x_codes, x_scales, w_codes, w_scales, offsets
                                        _stream(stream)))
 
 
+def moe_workspace_size_fp4(cfg: MoeConfig, fmt: int) -> int:
+    return int(load().moe_workspace_size_fp4(ctypes.byref(cfg), fmt))
+
+
+def moe_workspace_layout_fp4(cfg: MoeConfig, fmt: int) -> dict:
+    L = _LayoutFp4()
+    _check(load().moe_workspace_layout_fp4(ctypes.byref(cfg), fmt, ctypes.byref(L)))
+    return {n: int(getattr(L, n)) for n in _LAYOUT_FP4_FIELDS}
+
+
+def moe_layer_fwd_fp4(cfg, weights: MoeWeightsFp4, x, out, ws, stream=None) -> None:
+    _check(load().moe_layer_fwd_fp4(ctypes.byref(cfg), ctypes.byref(weights), _ptr(x), _ptr(out),
+                                    _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_layer_fwd_fp4_prerouted(cfg, weights: MoeWeightsFp4, x, topk_idx, topk_w, out, ws,
+                                stream=None) -> None:
+    _check(load().moe_layer_fwd_fp4_prerouted(
+        ctypes.byref(cfg), ctypes.byref(weights), _ptr(x), _ptr(topk_idx), _ptr(topk_w), _ptr(out),
+        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+class _GroupedLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets):
+        ctx.save_for_backward(x, w, offsets)
+        y = x.new_zeros((x.shape[0], w.shape[1]))  # rows outside every group stay zero
+        moe_grouped_gemm(x, w, offsets, y)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, offsets = ctx.saved_tensors
+        dy = dy if dy.stride(-1) == 1 and dy.stride(0) % 8 == 0 and dy.data_ptr() % 16 == 0 else dy.contiguous()
+        dx = dw = None
+        if ctx.needs_input_grad[0]:
+            dx = x.new_zeros(x.shape)
+            moe_grouped_gemm(dy, w, offsets, dx, w_transposed=True)
+        if ctx.needs_input_grad[1]:
+            dw = torch.empty_like(w)
+            moe_grouped_wgrad(dy, x, offsets, dw)
+        return dx, dw, None
+
+
+def grouped_linear(x, w, offsets):
+    """y[r] = x[r] W[e]^T for the rows of every group e, differentiable in x and w: x [R, K],
+    w [E, N, K] (bf16 or fp16), offsets int32 [E + 1].  Rows outside every group are zero, in y
+    and in the gradient of x."""
+    return _GroupedLinear.apply(x, w, offsets)
+
+
 def moe_get_device_status(ws, stream=None) -> int:
     """Synchronises the stream and returns (and clears) the device error bits."""
     bits = ctypes.c_uint32(0)
@@ -686,14 +760,24 @@ class MoeLayer:
     W2 [E, d_e, d], shared Ws1/Ws3 [d, d_s], Ws2 [d_s, d]; all bf16 CUDA
     tensors; bias fp32 [E] or None.  ``fp8=True`` packs the routed and shared
     expert weights as e4m3 codes with per-output-channel scales
-    (``moe_pack_experts_fp8``) and runs ``moe_layer_fwd_fp8``.
+    (``moe_pack_experts_fp8``) and runs ``moe_layer_fwd_fp8``.  ``fp4="mx"`` or
+    ``"nv"`` quantises the routed and shared expert weights to 4-bit codes with
+    block scales (``moe_quantize_fp4``; for ``"nv"`` with one fp32 scale per
+    expert) and runs ``moe_layer_fwd_fp4``, which quantises the activations
+    too; ``fp4_scales`` are the tensor scales of the token rows and of the
+    SwiGLU outputs for ``"nv"`` (fp32 [1] CUDA tensors, e.g. the calibrated
+    largest magnitude / 2688; None = 1).
     """
 
     def __init__(self, cfg: MoeConfig, W1, W3, W2, Wg=None, bias=None, Ws1=None, Ws3=None, Ws2=None,
-                 stream=None, fp8: bool = False, keep_gate_up: bool = False):
+                 stream=None, fp8: bool = False, keep_gate_up: bool = False,
+                 fp4: Optional[str] = None, fp4_scales=(None, None)):
         moe_check_config(cfg)
+        if fp4 is not None and (fp8 or keep_gate_up or fp4 not in FP4_FORMATS):
+            raise ValueError('fp4 is "mx" or "nv", without fp8 and keep_gate_up')
         self.cfg = cfg
         self.fp8 = fp8
+        self.fp4 = fp4
         # keep_gate_up: every forward saves the gate/up values (moe_layer_fwd_save)
         # and the backward reads them instead of recomputing them
         self.keep_gate_up = keep_gate_up and not fp8
@@ -705,6 +789,9 @@ class MoeLayer:
         E, d, de = W1.shape
         if fp8:
             self._init_fp8(cfg, W1, W3, W2, Wg, bias, Ws1, Ws3, Ws2, stream)
+            return
+        if fp4:
+            self._init_fp4(cfg, W1, W3, W2, Wg, bias, Ws1, Ws3, Ws2, fp4_scales, stream)
             return
         # the caller's weights, kept by reference for the backward packs
         self._user = dict(W1=W1, W3=W3, W2=W2, Wg=Wg, Ws1=Ws1, Ws3=Ws3, Ws2=Ws2)
@@ -733,7 +820,10 @@ class MoeLayer:
         self._init_ws(cfg, dev)
 
     def _init_ws(self, cfg, dev):
-        self.layout = moe_workspace_layout_fp8(cfg) if self.fp8 else moe_workspace_layout(cfg)
+        if self.fp4:
+            self.layout = moe_workspace_layout_fp4(cfg, FP4_FORMATS[self.fp4])
+        else:
+            self.layout = moe_workspace_layout_fp8(cfg) if self.fp8 else moe_workspace_layout(cfg)
         self.ws = torch.empty(self.layout["total"], dtype=torch.uint8, device=dev)
         self.ws[:256].zero_()
 
@@ -770,10 +860,67 @@ class MoeLayer:
             Ws2q=p(self.Ws2q), ss2=p(self.ss2))
         self._init_ws(cfg, dev)
 
+    def _init_fp4(self, cfg, W1, W3, W2, Wg, bias, Ws1, Ws3, Ws2, fp4_scales, stream):
+        dev = W1.device
+        E, d, de = W1.shape
+        fmt = FP4_FORMATS[self.fp4]
+
+        def quantize(w):
+            """Rows [n, rows, K] of n experts: codes, scales, tensor scales (NV)."""
+            n, rows, K = w.shape
+            q = torch.empty((n, rows, K // 2), dtype=torch.uint8, device=dev)
+            s = torch.empty((n, rows, moe_fp4_scale_stride(fmt, K)), dtype=torch.uint8, device=dev)
+            g = torch.ones((n,), dtype=torch.float32, device=dev) if fmt == FP4_NV else None
+            for e in range(n):
+                if g is not None:  # the largest block scale becomes e4m3's largest value
+                    top = w[e].abs().amax().float() / (6 * 448)
+                    g[e] = torch.where(top > 0, top, 1.0)
+                moe_quantize_fp4(fmt, w[e], q[e], s[e],
+                                 tensor_scale=None if g is None else g[e:e + 1], stream=stream)
+            return q, s, g
+
+        def pack(w1, w3, w2, n, width):
+            w13 = torch.empty((n, 2 * width, d), dtype=torch.bfloat16, device=dev)
+            w2t = torch.empty((n, d, width), dtype=torch.bfloat16, device=dev)
+            moe_pack_experts(w1, w3, w2, w13, w2t, stream)
+            return (*quantize(w13), *quantize(w2t))
+
+        ctx = torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext()
+        with ctx:
+            self.packed = pack(W1, W3, W2, E, de)
+            self.Wg_t = None
+            if Wg is not None:
+                self.Wg_t = torch.empty((E, d), dtype=torch.bfloat16, device=dev)
+                moe_pack_router(Wg, self.Wg_t, stream)
+            self.bias = None if bias is None else bias.to(device=dev, dtype=torch.float32).contiguous()
+            self.shared_packed = (None,) * 6
+            if cfg.d_shared:
+                self.shared_packed = pack(Ws1.unsqueeze(0).contiguous(), Ws3.unsqueeze(0).contiguous(),
+                                          Ws2.unsqueeze(0).contiguous(), 1, cfg.d_shared)
+            self._init_ws(cfg, dev)
+        self.fp4_scales = tuple(fp4_scales)
+        for name, t in zip(("x_scale", "h_scale"), self.fp4_scales):
+            _expect(t, name, torch.float32, (1,))
+
+        def p(t):
+            return None if t is None else t.data_ptr()
+
+        names = ("W13q", "s13", "g13", "W2q", "s2", "g2", "Ws13q", "ss13", "gs13", "Ws2q", "ss2", "gs2",
+                 "x_scale", "h_scale")
+        tensors = (*self.packed, *self.shared_packed, *self.fp4_scales)
+        self.weights = MoeWeightsFp4(fmt=fmt, Wg_t=p(self.Wg_t), bias=p(self.bias),
+                                     **{n: p(t) for n, t in zip(names, tensors)})
+
     def forward(self, x, out=None, topk_idx=None, topk_w=None, stream=None):
         if out is None:
             out = torch.empty_like(x)
-        if self.fp8:
+        if self.fp4:
+            if topk_idx is None:
+                moe_layer_fwd_fp4(self.cfg, self.weights, x, out, self.ws, stream)
+            else:
+                moe_layer_fwd_fp4_prerouted(self.cfg, self.weights, x, topk_idx, topk_w, out,
+                                            self.ws, stream)
+        elif self.fp8:
             if topk_idx is None:
                 moe_layer_fwd_fp8(self.cfg, self.weights, x, out, self.ws, stream)
             else:
@@ -823,7 +970,7 @@ class MoeLayer:
         dW1, dW3, dW2, the shared dWs1/dWs3/dWs2 and, for a routed forward,
         dWg and dbias (``moe_layer_bwd``).  ``prerouted`` marks a forward that
         was given its routing (no router term)."""
-        if self.fp8:
+        if self.fp8 or self.fp4:
             raise NotImplementedError("the backward runs on bf16 expert weights")
         if self.wbwd is None:
             self._init_bwd(stream)

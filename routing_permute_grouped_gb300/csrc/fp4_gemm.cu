@@ -428,7 +428,7 @@ extern "C" moe_status_t moe_grouped_gemm_fp4(int32_t fmt, int64_t R, int32_t N, 
     if (E > kRaggedMaxGroups) return set_last_error(MOE_ERR_UNSUPPORTED, "E = %d > 256", E);
     if (R > (1ll << 30)) return set_last_error(MOE_ERR_UNSUPPORTED, "too many rows for 32-bit row indices");
     if (R == 0) return MOE_OK;
-    if (!x_codes || !x_scales || !w_codes || !w_scales || !offsets || !y)
+    if (!x_codes || !x_scales || !w_codes || !w_scales || (!offsets && E != 1) || !y)
         return set_last_error(MOE_ERR_INVALID_ARG, "null pointer");
     if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(y))
         return set_last_error(MOE_ERR_INVALID_ARG, "codes, scales and y must be 16-byte aligned");

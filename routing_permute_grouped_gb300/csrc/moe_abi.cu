@@ -747,6 +747,122 @@ static moe_status_t layer_fp8(const moe_config_t* cfg, const moe_weights_fp8_t* 
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "combine");
 }
 
+static moe_workspace_layout_fp4_t layout_fp4_of(const moe_config_t& c, int32_t fmt) {
+    const size_t A = static_cast<size_t>(sizes_of(c).A), T = c.T, d = c.d, de = c.d_e;
+    const size_t ds = c.d_shared ? static_cast<size_t>(c.d_shared) : 0, Ts = ds ? T : 0;
+    moe_workspace_layout_fp4_t L{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = align_up(off + bytes, 1024);
+        return o;
+    };
+    auto scales = [&](size_t K) { return K ? moe_fp4_scale_stride(fmt, static_cast<int32_t>(K)) : 0; };
+    L.status = take(offsets_ws_bytes(c));
+    L.topk_idx = take(A * 4);
+    L.topk_w = take(A * 4);
+    L.counts = take(static_cast<size_t>(c.E) * 4);
+    L.group_offsets = take(static_cast<size_t>(c.E + 1) * 4);
+    L.perm_row = take(A * 4);
+    L.row_src = take(A * 4);
+    L.row_gate = take(A * 4);
+    const int S = router_splits(c);
+    L.router_partial = take(S > 1 && !router_uses_cluster(c) ? static_cast<size_t>(S) * T * c.E * 4 : 0);
+    L.xq = take(A * d / 2);
+    L.xs = take(A * scales(d));
+    L.gu = take(A * 2 * de * 2);
+    L.hq = take(A * de / 2);
+    L.hs = take(A * scales(de));
+    L.y = take(A * d * 2);
+    L.sxq = take(Ts * d / 2);
+    L.sxs = take(Ts * scales(d));
+    L.sgu = take(Ts * 2 * ds * 2);
+    L.shq = take(Ts * ds / 2);
+    L.shs = take(Ts * scales(ds));
+    L.ys = take(Ts * d * 2);
+    L.total = off;
+    return L;
+}
+
+// One expert MLP on 4-bit operands: rows of x (gathered by src / src_div) ->
+// gate/up -> SwiGLU -> down.  The rows of E experts, or of the shared one.
+struct MlpFp4 {
+    int64_t rows;
+    int32_t E, width;            // experts, their inner width
+    const int32_t *offsets, *src;
+    const float* gate;
+    const void *W13, *s13, *W2, *s2;
+    const float *g13, *g2;
+    void *xq, *xs, *gu, *hq, *hs, *y;
+};
+
+static moe_status_t mlp_fp4(const moe_config_t& c, const moe_weights_fp4_t& w, const void* x, const MlpFp4& m,
+                            uint32_t* status, cudaStream_t st) {
+    moe_status_t r = moe_quantize_fp4(w.fmt, MOE_DTYPE_BF16, m.rows, c.d, x, c.T, c.d, m.src, c.k, 0, w.x_scale, m.xq,
+                                      m.xs, st);
+    if (r == MOE_OK)
+        r = moe_grouped_gemm_fp4(w.fmt, m.rows, 2 * m.width, c.d, m.E, m.xq, m.xs, m.W13, m.s13, m.offsets, w.x_scale,
+                                 m.g13, nullptr, m.gu, 2 * m.width, status, st);
+    if (r == MOE_OK)
+        r = moe_quantize_fp4(w.fmt, MOE_DTYPE_BF16, m.rows, m.width, m.gu, m.rows, 2 * m.width, nullptr, 1, 1, w.h_scale,
+                             m.hq, m.hs, st);
+    if (r == MOE_OK)
+        r = moe_grouped_gemm_fp4(w.fmt, m.rows, c.d, m.width, m.E, m.hq, m.hs, m.W2, m.s2, m.offsets, w.h_scale, m.g2,
+                                 m.gate, m.y, c.d, status, st);
+    return r;
+}
+
+static moe_status_t layer_fp4(const moe_config_t* cfg, const moe_weights_fp4_t* w, const void* x,
+                              const int32_t* pre_idx, const float* pre_w, void* out, void* ws, size_t ws_bytes,
+                              cudaStream_t st) {
+    if (!w) return fail(MOE_ERR_INVALID_ARG, "null weights");
+    moe_status_t r = check_cfg(cfg, pre_idx == nullptr);
+    if (r != MOE_OK) return r;
+    const moe_config_t& c = *cfg;
+    if (w->fmt != MOE_FP4_MX && w->fmt != MOE_FP4_NV)
+        return fail(MOE_ERR_INVALID_ARG, "format = %d is neither MX (0) nor NV (1)", w->fmt);
+    if (c.T > 0 && (!x || !out)) return fail(MOE_ERR_INVALID_ARG, "null x or out");
+    if (!pre_idx && !w->Wg_t) return fail(MOE_ERR_INVALID_ARG, "null router weight");
+    if (pre_idx && !pre_w && c.T > 0) return fail(MOE_ERR_INVALID_ARG, "null pre-routed gates");
+    if (!w->W13q || !w->s13 || !w->W2q || !w->s2)
+        return fail(MOE_ERR_INVALID_ARG, "null routed expert codes or scales");
+    if (c.d_shared && (!w->Ws13q || !w->ss13 || !w->Ws2q || !w->ss2))
+        return fail(MOE_ERR_INVALID_ARG, "d_shared > 0 but null shared expert codes or scales");
+    const moe_workspace_layout_fp4_t L = layout_fp4_of(c, w->fmt);
+    if (!ws || ws_bytes < L.total)
+        return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, L.total);
+    if (c.T == 0) return MOE_OK;
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    auto at = [&](size_t off) { return static_cast<void*>(base + off); };
+    auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(base + off); };
+    auto f32 = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
+    uint32_t* status = reinterpret_cast<uint32_t*>(base + L.status);
+    if (!pre_idx) {
+        r = do_route_layer(c, x, w->Wg_t, w->bias, i32(L.topk_idx), f32(L.topk_w), f32(L.router_partial), st, status);
+        if (r != MOE_OK) return r;
+        pre_idx = i32(L.topk_idx);
+        pre_w = f32(L.topk_w);
+    }
+    const int64_t A = sizes_of(c).A;
+    cudaError_t e = launch_offsets(pre_idx, pre_w, A, c.E, 1, A, i32(L.counts), i32(L.group_offsets), nullptr, nullptr,
+                                   i32(L.perm_row), i32(L.row_src), f32(L.row_gate), status, i32(L.status + 256), st);
+    if (e != cudaSuccess) return cuda_fail(e, "offsets kernels (unpadded)");
+    if (c.d_shared) {
+        const MlpFp4 shared{c.T,     1,       c.d_shared, nullptr, nullptr,  nullptr,   w->Ws13q,  w->ss13,
+                            w->Ws2q, w->ss2,  w->gs13,    w->gs2,  at(L.sxq), at(L.sxs), at(L.sgu), at(L.shq),
+                            at(L.shs), at(L.ys)};
+        r = mlp_fp4(c, *w, x, shared, status, st);
+        if (r != MOE_OK) return r;
+    }
+    const MlpFp4 routed{A,       c.E,    c.d_e, i32(L.group_offsets), i32(L.row_src), f32(L.row_gate), w->W13q, w->s13,
+                        w->W2q,  w->s2,  w->g13, w->g2,               at(L.xq),       at(L.xs),        at(L.gu), at(L.hq),
+                        at(L.hs), at(L.y)};
+    r = mlp_fp4(c, *w, x, routed, status, st);
+    if (r != MOE_OK) return r;
+    e = launch_combine(at(L.y), i32(L.perm_row), c.d_shared ? at(L.ys) : nullptr, out, c.T, c.d, c.k, st);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "combine");
+}
+
 // ------------------------------------------------------------ backward --
 
 struct BwdLayout {
@@ -1453,6 +1569,33 @@ moe_status_t moe_layer_fwd_fp8_prerouted(const moe_config_t* cfg, const moe_weig
     if (!topk_idx) return fail(MOE_ERR_INVALID_ARG, "null pre-routed indices");
     return layer_fp8(cfg, w, x, topk_idx, topk_w, out, ws, ws_bytes,
                      static_cast<cudaStream_t>(stream));
+}
+
+size_t moe_workspace_size_fp4(const moe_config_t* cfg, int32_t fmt) {
+    moe_workspace_layout_fp4_t L;
+    return moe_workspace_layout_fp4(cfg, fmt, &L) == MOE_OK ? L.total : 0;
+}
+
+moe_status_t moe_workspace_layout_fp4(const moe_config_t* cfg, int32_t fmt, moe_workspace_layout_fp4_t* layout) {
+    const moe_status_t r = check_cfg(cfg, false);
+    if (r != MOE_OK) return r;
+    if (fmt != MOE_FP4_MX && fmt != MOE_FP4_NV)
+        return fail(MOE_ERR_INVALID_ARG, "format = %d is neither MX (0) nor NV (1)", fmt);
+    if (!layout) return fail(MOE_ERR_INVALID_ARG, "layout is NULL");
+    *layout = layout_fp4_of(*cfg, fmt);
+    return MOE_OK;
+}
+
+moe_status_t moe_layer_fwd_fp4(const moe_config_t* cfg, const moe_weights_fp4_t* w, const void* x, void* out, void* ws,
+                               size_t ws_bytes, void* stream) {
+    return layer_fp4(cfg, w, x, nullptr, nullptr, out, ws, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+moe_status_t moe_layer_fwd_fp4_prerouted(const moe_config_t* cfg, const moe_weights_fp4_t* w, const void* x,
+                                         const int32_t* topk_idx, const float* topk_w, void* out, void* ws,
+                                         size_t ws_bytes, void* stream) {
+    if (!topk_idx) return fail(MOE_ERR_INVALID_ARG, "null pre-routed indices");
+    return layer_fp4(cfg, w, x, topk_idx, topk_w, out, ws, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
 moe_status_t moe_pack_experts_bwd(int32_t E, int32_t d, int32_t de, const void* W1, const void* W3,

@@ -19,7 +19,7 @@ constexpr int kRaggedMaxGroups = 256;
 constexpr uint32_t kRaggedBadGroup = 0x4u;  // MOE_DEVERR_SEGMENT
 
 struct RaggedArgs {
-    const int32_t* offsets;  // [E + 1]
+    const int32_t* offsets;  // [E + 1], or null: one group of all rows
     int32_t R, N, K, E;      // rows, output columns, sum length (wgrad: M is K here), groups
     const float* row_scale;  // [R] or null
     const float* x_scale;    // [1] or null: 4-bit rows' tensor scale
@@ -31,6 +31,7 @@ struct RaggedArgs {
 
 // Rows [x, y) of group e; empty and flagged when they do not lie in [0, R].
 __device__ __forceinline__ int2 group_rows(const RaggedArgs& a, int e) {
+    if (!a.offsets) return make_int2(0, a.R);
     const int lo = ld_dep(a.offsets + e);
     const int hi = ld_dep(a.offsets + e + 1);
     if (lo < 0 || hi < lo || hi > a.R) {

@@ -556,7 +556,7 @@ extern "C" moe_status_t moe_grouped_gemm(int32_t dtype, int64_t R, int32_t N, in
     const moe_status_t s = check_ragged(dtype, R, N, K, E);
     if (s != MOE_OK) return s;
     if (R == 0) return MOE_OK;
-    if (!x || !w || !offsets || !y) return set_last_error(MOE_ERR_INVALID_ARG, "null pointer");
+    if (!x || !w || (!offsets && E != 1) || !y) return set_last_error(MOE_ERR_INVALID_ARG, "null pointer");
     if (!aligned16(x) || !aligned16(w) || !aligned16(y))
         return set_last_error(MOE_ERR_INVALID_ARG, "x, w and y must be 16-byte aligned");
     if (ldx < K || ldx % 8 || ldy < N || ldy % 8)
@@ -584,7 +584,7 @@ extern "C" moe_status_t moe_grouped_wgrad(int32_t dtype, int64_t R, int32_t M, i
                                           uint32_t* status, void* stream) {
     const moe_status_t s = check_ragged(dtype, R, M, N, E);
     if (s != MOE_OK) return s;
-    if (!out || (R > 0 && (!a_ || !b || !offsets))) return set_last_error(MOE_ERR_INVALID_ARG, "null pointer");
+    if (!out || (R > 0 && (!a_ || !b || (!offsets && E != 1)))) return set_last_error(MOE_ERR_INVALID_ARG, "null pointer");
     if (!aligned16(out) || (R > 0 && (!aligned16(a_) || !aligned16(b))))
         return set_last_error(MOE_ERR_INVALID_ARG, "a, b and out must be 16-byte aligned");
     if (R > 0 && (lda < M || lda % 8 || ldb < N || ldb % 8))

@@ -115,3 +115,65 @@ def test_scale_stride(lib):
     for fmt in (-1, 0, 1, 2):
         for k in (-32, 0, 31, 32, 96, 160, 512, 544, 2080, 7168):
             assert stride(fmt, k) == lib.moe_fp4_scale_stride(fmt, k)
+
+
+def _cfg(**kw):
+    return moe.config_of(**{**dict(T=64, d=512, d_e=256, E=8, k=2), **kw})
+
+
+W4 = dict(fmt=0, Wg_t=0x1000, W13q=0x1000, s13=0x1000, W2q=0x1000, s2=0x1000)
+
+
+@pytest.mark.parametrize("cfg,weights,kw,status", [
+    ({}, {}, dict(short=1), 3), ({}, dict(fmt=2), {}, INVALID), ({}, dict(s13=None), {}, INVALID),
+    ({}, dict(W2q=None), {}, INVALID), ({}, dict(Wg_t=None), {}, INVALID), ({}, {}, dict(x=None), INVALID),
+    ({}, {}, dict(out=None), INVALID), (dict(d_shared=128), {}, {}, INVALID), (dict(d=500), {}, {}, UNSUPPORTED),
+    (dict(k=9, E=16), {}, {}, UNSUPPORTED), (dict(k=5, E=4), {}, {}, INVALID),
+])
+def test_layer_fp4_refuses(lib, cfg, weights, kw, status):
+    c = _cfg(**cfg)
+    w = moe.MoeWeightsFp4(**{**W4, **weights})
+    need = moe.moe_workspace_size_fp4(c, 0)
+    args = {**dict(x=P, out=P, ws=P), **kw}
+    assert lib.moe_layer_fwd_fp4(ctypes.byref(c), ctypes.byref(w), args["x"], args["out"], args["ws"],
+                                 need - kw.get("short", 0), None) == status
+    assert lib.moe_last_error()
+
+
+def test_layer_fp4_prerouted_refuses_and_empty_batch(lib):
+    c, w = _cfg(), moe.MoeWeightsFp4(**W4)
+    need = moe.moe_workspace_size_fp4(c, 0)
+    pre = lib.moe_layer_fwd_fp4_prerouted
+    assert pre(ctypes.byref(c), ctypes.byref(w), P, None, P, P, P, need, None) == INVALID
+    assert pre(ctypes.byref(c), ctypes.byref(w), P, P, None, P, P, need, None) == INVALID
+    none = _cfg(T=0)
+    assert lib.moe_layer_fwd_fp4(ctypes.byref(none), ctypes.byref(w), None, None, P, need, None) == 0
+
+
+def test_workspace_layout_fp4(lib):
+    for fmt in (0, 1):
+        c = _cfg(d_shared=128)
+        L = moe.moe_workspace_layout_fp4(c, fmt)
+        order = list(L)[1:]
+        assert [L[n] for n in order] == sorted(L[n] for n in order) and all(L[n] % 1024 == 0 for n in order)
+        assert L["total"] == moe.moe_workspace_size_fp4(c, fmt)
+        assert L["xs"] - L["xq"] >= 128 * 256 and L["gu"] - L["xs"] >= 128 * moe.moe_fp4_scale_stride(fmt, 512)
+    assert moe.moe_workspace_size_fp4(_cfg(), 2) == 0
+
+
+def test_binding_refuses_what_c_cannot_see():
+    import torch
+
+    cpu = torch.zeros((4, 64), dtype=torch.bfloat16)
+    off = torch.zeros(3, dtype=torch.int32)
+    w = torch.zeros((2, 64, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):  # host tensors
+        moe.moe_grouped_gemm(cpu, w, off, cpu.clone())
+    with pytest.raises(ValueError):  # another type of weights
+        moe.moe_grouped_gemm(cpu, w.half(), off, cpu.clone())
+    with pytest.raises(ValueError):  # offsets of another length
+        moe.moe_grouped_gemm(cpu, w, off[:2], cpu.clone())
+    with pytest.raises(ValueError):
+        moe.moe_grouped_wgrad(cpu, cpu, off, torch.zeros((2, 64, 32), dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        moe.moe_quantize_fp4(0, cpu, torch.zeros((4, 32), dtype=torch.uint8), torch.zeros((4, 2), dtype=torch.uint8))
