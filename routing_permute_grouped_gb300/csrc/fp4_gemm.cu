@@ -58,7 +58,7 @@ struct Scales {
 };
 constexpr int kRaw = 7;                   // scale groups in shared memory
 constexpr int kRawRows = (4 + kTN / 32) * 512;  // 32-row pieces of 512 bytes: weights, tokens
-constexpr int kLayoutSets = 2;            // of four warps, one per lane quarter
+constexpr int kLayoutSets = 1;            // of four warps, one per lane quarter
 constexpr int kEpi0 = 4 + 4 * kLayoutSets;  // first epilogue warp
 constexpr int kThreads = 32 * (kEpi0 + kEpiWarps);
 
@@ -123,8 +123,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t one = elect_one();
         Ring r;
         uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
+        int e = 0;
         for (int t = first; t < total && !timed_out; t += stride) {
-            const RaggedItem it = uniform(ragged_item<kTN>(args, tiles, panels, t));
+            const RaggedItem it = uniform(ragged_item(tiles, panels, t, e));
             const int half = ((it.rows + 31) & ~31) / 2;  // token rows of each CTA
             const int xrow = it.row + half * static_cast<int>(rank);
             const int wrow = it.panel * 256 + 128 * static_cast<int>(rank);
@@ -163,8 +164,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             Acc acc;
             Ring buf;  // scale buffer
             bool issued = false, ready = false;
+            int e = 0;
             for (int t = first; t < total && !timed_out; t += stride) {
-                const RaggedItem it = uniform(ragged_item<kTN>(args, tiles, panels, t));
+                const RaggedItem it = uniform(ragged_item(tiles, panels, t, e));
                 const uint32_t n = (it.rows + 31) & ~31;
                 const uint32_t idesc = idesc0 | ((n >> 3) << 17);
                 if (!warp_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
@@ -225,8 +227,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---------------------------------------------------- scale loads
         int s = 0;
         uint32_t ph = 0;
+        int e = 0;
         for (int t = first; t < total && !timed_out; t += stride) {
-            const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
+            const RaggedItem it = ragged_item(tiles, panels, t, e);
             const int64_t w_last = static_cast<int64_t>(it.e + 1) * args.N - 1;
             const int64_t w0 = static_cast<int64_t>(it.e) * args.N + it.panel * 256 + 128 * static_cast<int>(rank);
             const uint8_t* wp[4];
@@ -350,40 +353,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else {
         // ------------------------------------------------------ epilogue
-        // A warp owns 32 of the CTA's 128 features (its tensor-memory lane
-        // quarter) and every other 32-token chunk.
-        const int q = warp & 3, odd = (warp - kEpi0) >> 2;
         const float gx = args.x_scale ? ld_dep(args.x_scale) : 1.0f;
-        Acc acc;
-        for (int t = first; t < total; t += stride) {
-            const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
-            const float scale = gx * (args.w_scale ? ld_dep(args.w_scale + it.e) : 1.0f);
-            float gate[kTN / 64];  // the factor of this lane's token of each chunk
-#pragma unroll
-            for (int i = 0; i < kTN / 64; ++i) {
-                const int token = odd * 32 + i * 64 + lane;
-                gate[i] = args.row_scale && token < it.rows ? ld_dep(args.row_scale + it.row + token) * scale : scale;
-            }
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars.tfull + acc.i, acc.ph, abort_flag))) {
-                timed_out = true;
-                break;
-            }
-            tc_fence_after();
-            const uint32_t taddr =
-                tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc.i * kTN);
-            const int n0 = it.panel * 256 + static_cast<int>(rank) * 128 + q * 32;
-#pragma unroll
-            for (int i = 0; i < kTN / 64; ++i) {
-                const int c = odd * 32 + i * 64;
-                if (c < it.rows)
-                    store_transposed<__nv_bfloat16>(args, taddr + c, it.row + c, it.rows - c, n0, lane, gate[i],
-                                                    sOut + (warp - kEpi0) * 2048);
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), 0));
-            acc.next();
-        }
+        if (!product_epilogue<__nv_bfloat16, kTN>(
+                args, tiles, bars, panels, total, first, stride, tmem_base, warp - kEpi0, lane, rank,
+                sOut + (warp - kEpi0) * 2048, gx,
+                [&](int e) { return args.w_scale ? ld_dep(args.w_scale + e) : 1.0f; }))
+            timed_out = true;
     }
     if (timed_out) *abort_flag = 1;
     if (timed_out && args.status) atomicOr(args.status, kRaggedTimeout);

@@ -50,6 +50,8 @@ __device__ __forceinline__ int2 group_rows(const RaggedArgs& a, int e) {
 struct RaggedTiles {
     int first[kRaggedMaxGroups + 1];  // a group's first work item
     int lo[kRaggedMaxGroups], hi[kRaggedMaxGroups];
+    int tiles[kRaggedMaxGroups];      // its token tiles
+    int width[kRaggedMaxGroups];      // their rows, a multiple of 32 (<= TN)
 };
 
 struct RaggedItem {
@@ -68,7 +70,10 @@ __device__ void ragged_tiles_build(const RaggedArgs& a, RaggedTiles& s, int pane
             const int2 g = group_rows(a, e);
             s.lo[e] = g.x;
             s.hi[e] = g.y;
-            n = (g.y - g.x + TN - 1) / TN * panels;
+            const int len = g.y - g.x, tiles = (len + TN - 1) / TN;
+            s.tiles[e] = tiles;
+            s.width[e] = tiles ? ((len + tiles - 1) / tiles + 31) & ~31 : 0;
+            n = tiles * panels;
         }
         int x = n;
 #pragma unroll
@@ -82,30 +87,21 @@ __device__ void ragged_tiles_build(const RaggedArgs& a, RaggedTiles& s, int pane
     if (lane == 0) s.first[a.E] = running;
 }
 
-// Item t: its group by bisection; inside a group, token tiles pass over eight
-// panels at a time, so the items in flight share both operands in L2.
-template <int TN>
-__device__ __forceinline__ RaggedItem ragged_item(const RaggedArgs& a, const RaggedTiles& s, int panels, int t) {
-    int lo = 0, hi = a.E;  // first[lo] <= t < first[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s.first[mid] <= t)
-            lo = mid;
-        else
-            hi = mid;
-    }
+// Item t; e is the group of the caller's last item (0 at first), from which the
+// search goes on.  Inside a group, token tiles pass over eight panels at a time,
+// so the items in flight share both operands in L2.
+__device__ __forceinline__ RaggedItem ragged_item(const RaggedTiles& s, int panels, int t, int& e) {
+    while (s.first[e + 1] <= t) ++e;
     RaggedItem it;
-    it.e = lo;
-    const int len = s.hi[lo] - s.lo[lo];
-    const int tiles = (len + TN - 1) / TN;
-    const int width = ((len + tiles - 1) / tiles + 31) & ~31;  // <= TN
-    const int i = t - s.first[lo];
-    const int block = i / (tiles * 8), rest = i - block * tiles * 8;
-    const int wide = min(8, panels - block * 8);
-    const int tile = rest / wide;
+    it.e = e;
+    const unsigned tiles = s.tiles[e], width = s.width[e];
+    const unsigned i = t - s.first[e];
+    const unsigned block = i / (tiles * 8), rest = i - block * tiles * 8;
+    const unsigned wide = min(8u, panels - block * 8);
+    const unsigned tile = wide == 8 ? rest >> 3 : rest / wide;
     it.panel = block * 8 + rest - tile * wide;
-    it.row = s.lo[lo] + tile * width;
-    it.rows = min(width, s.hi[lo] - it.row);
+    it.row = s.lo[e] + tile * width;
+    it.rows = min(static_cast<int>(width), s.hi[e] - it.row);
     return it;
 }
 
@@ -131,19 +127,15 @@ __device__ __forceinline__ uint32_t pack2(__half, float lo, float hi) {
 // Epilogue of the products for 32 accumulator columns: tokens row .. row + 31
 // (`rows` of them are stored) times the warp's 32 features n0 .. n0 + 31, one
 // feature per tensor-memory lane.  The accumulator is read in matrix-fragment
-// form, packed to 16 bits and stored transposed through stmatrix into 2 KB of
-// shared memory ([token][64 bytes], 16-byte pieces permuted against bank
+// form (v), packed to 16 bits and stored transposed through stmatrix into 2 KB
+// of shared memory ([token][64 bytes], 16-byte pieces permuted against bank
 // conflicts), from where each lane stores 16 bytes: an instruction writes 64
 // contiguous bytes of eight output rows.  (Exchanging neighbours' halves by
 // shuffles and storing 4 bytes per lane took 2.4 times the instructions and
 // held short sums up.)  gate is the factor of token row + lane.
 template <typename T>
-__device__ __forceinline__ void store_transposed(const RaggedArgs& a, uint32_t taddr, int row, int rows, int n0,
-                                                 int lane, float gate, uint8_t* stage) {
-    uint32_t v[2][16];
-    tmem_ld_frag32(taddr, v[0]);
-    tmem_ld_frag32(taddr + (16u << 16), v[1]);
-    tmem_ld_wait();
+__device__ __forceinline__ void store_transposed(const RaggedArgs& a, const uint32_t (&v)[2][16], int row, int rows,
+                                                 int n0, int lane, float gate, uint8_t* stage) {
     __syncwarp();  // the previous chunk has left the staging buffer
     const uint32_t sbase = smem_u32(stage);
 #pragma unroll
@@ -289,6 +281,74 @@ __device__ __forceinline__ void pair_end(uint32_t tmem_base, int warp) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, 512);
     }
+}
+
+// The epilogue warps of the products (`ew` of kEpiWarps): a warp owns 32 of the
+// CTA's 128 features (its tensor-memory lane quarter) and every other 32-token
+// chunk of a tile.  Short sums leave little time per tile, so nothing waits in
+// line: the next item and its routing weights are fetched while a tile is
+// stored, a chunk is read from tensor memory while the one before it is
+// stored, and the accumulator goes back before the last chunk's stores.
+template <typename T, int TN, int S, typename Scale>
+__device__ __forceinline__ bool product_epilogue(const RaggedArgs& args, const RaggedTiles& tiles, PairBars<S>& bars,
+                                                 int panels, int total, int first, int stride, uint32_t tmem_base,
+                                                 int ew, int lane, uint32_t rank, uint8_t* stage, float common,
+                                                 Scale scale_of) {
+    constexpr int kChunks = TN / 64;
+    const int q = (threadIdx.x >> 5) & 3, odd = ew >> 2;
+    const volatile uint32_t* abort_flag = &bars.abort;
+    int e = 0;
+    RaggedItem it{};
+    float gate[kChunks], scale = 1.0f;
+    // item t, its scale and the routing weight of this lane's token of each
+    // chunk; nothing is computed with them before they are needed
+    auto fetch = [&](int t) {
+        if (t >= total) return;
+        it = ragged_item(tiles, panels, t, e);
+        scale = scale_of(it.e);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int token = odd * 32 + i * 64 + lane;
+            gate[i] = args.row_scale && token < it.rows ? ld_dep(args.row_scale + it.row + token) : 1.0f;
+        }
+    };
+    fetch(first);
+    Acc acc;
+    for (int t = first; t < total; t += stride) {
+        if (!warp_wait(bars.tfull + acc.i, acc.ph, abort_flag)) return false;
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc.i * TN);
+        uint32_t v[2][2][16];
+        auto load = [&](int i) {
+            tmem_ld_frag32(taddr + odd * 32 + i * 64, v[i & 1][0]);
+            tmem_ld_frag32(taddr + odd * 32 + i * 64 + (16u << 16), v[i & 1][1]);
+        };
+        const RaggedItem now = it;
+        float g[kChunks];
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) g[i] = gate[i] * scale * common;
+        const int n0 = now.panel * 256 + static_cast<int>(rank) * 128 + q * 32;
+        if (odd * 32 < now.rows) load(0);
+        fetch(t + stride);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int c = odd * 32 + i * 64;
+            tmem_ld_wait();
+            if (c + 64 < now.rows && i + 1 < kChunks) {
+                load(i + 1);
+            } else if (c < now.rows || i == 0) {
+                // the last read is complete; the MMA side reads nothing that
+                // this warp stores, so the arrive need not release it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), 0));
+            }
+            if (c >= now.rows) break;
+            store_transposed<T>(args, v[i & 1], now.row + c, now.rows - c, n0, lane, g[i], stage);
+        }
+        acc.next();
+    }
+    return true;
 }
 
 // Launches `kernel` (clusters of two) on as many pairs as the GPU has SMs for,

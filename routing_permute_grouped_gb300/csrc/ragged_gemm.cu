@@ -101,8 +101,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
         const uint32_t one = elect_one();
         Ring r;
         uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
+        int e = 0;
         for (int t = first; t < total && !timed_out; t += stride) {
-            const RaggedItem it = uniform(ragged_item<kTN>(args, tiles, panels, t));
+            const RaggedItem it = uniform(ragged_item(tiles, panels, t, e));
             const int half = ((it.rows + 31) & ~31) / 2;  // token rows of each CTA
             const int xrow = it.row + half * static_cast<int>(rank);
             const int wrow = it.panel * 256 + 128 * static_cast<int>(rank);
@@ -148,8 +149,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
             Ring r;
             Acc acc;
             bool issued = false, ready = false;
+            int e = 0;
             for (int t = first; t < total && !timed_out; t += stride) {
-                const RaggedItem it = uniform(ragged_item<kTN>(args, tiles, panels, t));
+                const RaggedItem it = uniform(ragged_item(tiles, panels, t, e));
                 const uint32_t n = (it.rows + 31) & ~31;
                 const uint32_t idesc = Elem<T>::idesc | ((n >> 3) << 17) | (WT ? kTransA : 0u);
                 if (!warp_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
@@ -189,39 +191,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
         }
     } else {
         // ------------------------------------------------------ epilogue
-        // A warp owns 32 of the CTA's 128 features (its tensor-memory lane
-        // quarter) and every other 32-token chunk.
-        const int q = warp & 3, odd = (warp - 2) >> 2;
-        Acc acc;
-        for (int t = first; t < total; t += stride) {
-            const RaggedItem it = ragged_item<kTN>(args, tiles, panels, t);
-            float gate[kTN / 64];  // this lane's token of each chunk, read while the MMAs run
-#pragma unroll
-            for (int i = 0; i < kTN / 64; ++i) {
-                const int token = odd * 32 + i * 64 + lane;
-                gate[i] = args.row_scale && token < it.rows ? ld_dep(args.row_scale + it.row + token) : 1.0f;
-            }
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars.tfull + acc.i, acc.ph, abort_flag))) {
-                timed_out = true;
-                break;
-            }
-            tc_fence_after();
-            const uint32_t taddr =
-                tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc.i * kTN);
-            const int n0 = it.panel * 256 + static_cast<int>(rank) * 128 + q * 32;
-#pragma unroll
-            for (int i = 0; i < kTN / 64; ++i) {
-                const int c = odd * 32 + i * 64;
-                if (c < it.rows)
-                    store_transposed<T>(args, taddr + c, it.row + c, it.rows - c, n0, lane, gate[i],
-                                        sOut + (warp - 2) * 2048);
-            }
-            // the reads are complete: the MMA side reads nothing stored here
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), 0));
-            acc.next();
-        }
+        if (!product_epilogue<T, kTN>(args, tiles, bars, panels, total, first, stride, tmem_base, warp - 2, lane, rank,
+                                      sOut + (warp - 2) * 2048, 1.0f, [](int) { return 1.0f; }))
+            timed_out = true;
         if (timed_out) *abort_flag = 1;
     }
     if (timed_out && args.status) atomicOr(args.status, kRaggedTimeout);
