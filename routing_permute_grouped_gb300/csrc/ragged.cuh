@@ -246,31 +246,25 @@ __device__ __forceinline__ void pair_start(PairBars<S>& b, uint32_t full_count, 
     if (warp == 1) tmem_alloc_pair(&b.tmem, 512);
 }
 
-// Token rows as TMA boxes of 128, 64, 32 and 16 rows of 128 bytes, so that any
-// multiple of 16 rows takes the fewest loads (boxes of 16 alone: 1.22 against
-// 1.17 ms on the data gradient of a 64-expert layer, whose tiles are 200 to 250
-// rows).
+// Token rows as TMA boxes of 64 and 16 rows of 128 bytes.  (Boxes of 16 alone:
+// 1.22 against 1.17 ms on the data gradient of a 64-expert layer, whose tiles
+// are 200 to 250 rows; a map for every power of two saves loads that do not
+// bound the kernels, and costs short calls the time to encode it.)
 struct RowMaps {
-    CUtensorMap box[4];
+    CUtensorMap box64, box16;
 };
 __device__ __forceinline__ void load_rows(uint32_t one, const RowMaps& m, uint8_t* dst, int x, int row, int rows,
                                           uint32_t full) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (rows & (128 >> i)) {
-            tma_load_2d_pair_if(one, dst, m.box + i, x, row, full);
-            dst += (128 >> i) * 128;
-            row += 128 >> i;
-        }
+    int i = 0;
+    for (; i + 64 <= rows; i += 64) tma_load_2d_pair_if(one, dst + i * 128, &m.box64, x, row + i, full);
+    for (; i < rows; i += 16) tma_load_2d_pair_if(one, dst + i * 128, &m.box16, x, row + i, full);
 }
 inline bool make_row_maps(RowMaps* m, const void* x, uint64_t rows, uint64_t cols, uint64_t stride, uint32_t box_cols,
                           int dtype) {
     const uint64_t dims[2] = {cols, rows}, strides[1] = {stride};
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t box[2] = {box_cols, 128u >> i};
-        if (!make_tensor_map(m->box + i, x, 2, dims, strides, box, dtype)) return false;
-    }
-    return true;
+    const uint32_t box64[2] = {box_cols, 64}, box16[2] = {box_cols, 16};
+    return make_tensor_map(&m->box64, x, 2, dims, strides, box64, dtype) &&
+           make_tensor_map(&m->box16, x, 2, dims, strides, box16, dtype);
 }
 
 __device__ __forceinline__ void pair_end(uint32_t tmem_base, int warp) {
