@@ -11,13 +11,16 @@
 // fp32 operation with one rounding (the power-of-two steps have none), so the
 // codes are fixed by the inputs alone.
 //
-// Both kernels are bound by memory.  A thread takes 8 elements (16 bytes of the
-// 16-bit side, 4 of codes), so that every access of a warp is contiguous; a
-// team of 8 to 256 threads (about a quarter of the row's 8-element pieces)
-// takes a row, without divisions by the row length.  Instructions come next: a
-// block's amax is taken on the 16-bit patterns, two at a time, where NaN and
-// infinity order above every number (they mark the block's scale NaN), over its
-// 4 (MX) or 2 (NV) threads by shuffles, and bf16 rows are scaled in pairs.
+// Dequantising is bound by memory: a thread takes 8 elements (4 bytes of codes,
+// 16 of output), so that every access of a warp is contiguous (6.1 TB/s at the
+// default batch).  Quantising is bound by integer and conversion instructions
+// (8 elements per thread: 100 against 72 us at the default batch), so a thread takes 16, a whole NV block or half an MX one:
+// what is done once per block is then done by one or two threads.  The rows are
+// read with 32-byte loads where they are aligned to 32 bytes, else with two of
+// 16; amax is taken on the 16-bit patterns, two at a time, where NaN and
+// infinity order above every number (they mark the block's scale NaN); bf16 rows
+// are scaled in pairs.  A team of threads takes a row, without divisions by the
+// row length.
 #include <cuda_runtime.h>
 
 #include "../../include/moe.h"
@@ -98,8 +101,8 @@ __device__ __forceinline__ void scale8(__half, const uint4& u, float inv, float 
     for (int j = 0; j < 8; ++j) v[j] *= inv;
 }
 
-// Pieces of 8 elements that a thread has in flight
-constexpr int kPieces = 8;
+// Pieces of 16 elements that a thread has in flight (dequantising: 8 of 8)
+constexpr int kPieces = 2;
 
 // A team's row and the thread's place in it; false past the last row.
 __device__ __forceinline__ bool team_row(int team, int64_t rows, int64_t& row, int& lane) {
@@ -109,15 +112,51 @@ __device__ __forceinline__ bool team_row(int team, int64_t rows, int64_t& row, i
     return row < rows;
 }
 
-template <typename T, bool NV, bool SWIGLU>
+struct Piece {  // 16 elements
+    uint4 a, b;
+};
+// WIDE: p is aligned to 32 bytes
+template <bool WIDE>
+__device__ __forceinline__ Piece load_piece(const void* p) {
+    Piece r;
+    if constexpr (WIDE) {
+        asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r.a.x), "=r"(r.a.y), "=r"(r.a.z), "=r"(r.a.w), "=r"(r.b.x), "=r"(r.b.y), "=r"(r.b.z),
+                       "=r"(r.b.w)
+                     : "l"(p)
+                     : "memory");
+    } else {
+        r.a = __ldcg(static_cast<const uint4*>(p));
+        r.b = __ldcg(static_cast<const uint4*>(p) + 1);
+    }
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 swiglu8(const uint4& gate, const uint4& up) {
+    float g[8], u[8];
+    widen8<T>(gate, g);
+    widen8<T>(up, u);
+    uint4 r;
+    uint32_t* h = &r.x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = pack2(T(), silu(g[2 * j]) * u[2 * j], silu(g[2 * j + 1]) * u[2 * j + 1]);
+    return r;
+}
+
+constexpr uint32_t kAbs = 0x7FFF7FFFu;
+__device__ __forceinline__ uint32_t top_of(const uint4& u) {
+    return max_u16x2(max_u16x2(u.x & kAbs, u.y & kAbs), max_u16x2(u.z & kAbs, u.w & kAbs));
+}
+
+template <typename T, bool NV, bool SWIGLU, bool WIDE>
 __global__ void __launch_bounds__(256) k_quantize_fp4(const QuantArgs a) {
-    constexpr int kShare = NV ? 2 : 4;  // threads of a block of elements
     pdl_trigger();
     pdl_wait();
     int64_t r;
     int me;
     const bool real = team_row(a.team, a.rows, r, me);  // all lanes stay for the shuffles
-    const int pieces = a.K / 8;
+    const int pieces = a.K / 16, blocks = NV ? pieces : pieces / 2;
     const float g = NV && a.tensor_scale ? ld_dep(a.tensor_scale) : 1.0f;
     int64_t xr = r;
     bool have = real;
@@ -128,23 +167,23 @@ __global__ void __launch_bounds__(256) k_quantize_fp4(const QuantArgs a) {
     }
     const T* row = static_cast<const T*>(a.x) + (have ? xr * a.ldx : 0);
     uint8_t* scales = a.scales + (real ? r * a.stride : 0);
-    uint32_t* codes = reinterpret_cast<uint32_t*>(a.codes + (real ? r * (a.K / 2) : 0));
+    uint2* codes = reinterpret_cast<uint2*>(a.codes + (real ? r * (a.K / 2) : 0));
     if (real)
-        for (int i = pieces / kShare + me; i < a.stride; i += a.team) scales[i] = 0;  // the padding
+        for (int i = blocks + me; i < a.stride; i += a.team) scales[i] = 0;  // the padding
     for (int p0 = 0; p0 < pieces; p0 += kPieces * a.team) {
-        uint4 in[kPieces], up[SWIGLU ? kPieces : 1];
+        Piece in[kPieces], up[SWIGLU ? kPieces : 1];
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const int p = p0 + i * a.team + me;
-            in[i] = make_uint4(0, 0, 0, 0);
+            in[i].a = in[i].b = make_uint4(0, 0, 0, 0);
             if constexpr (SWIGLU) up[i] = in[i];
             if (have && p < pieces) {
                 if constexpr (SWIGLU) {  // gate and up columns interleaved per 128
-                    const T* q = row + (p >> 4) * 256 + (p & 15) * 8;
-                    in[i] = __ldcg(reinterpret_cast<const uint4*>(q));
-                    up[i] = __ldcg(reinterpret_cast<const uint4*>(q + 128));
+                    const T* q = row + (p >> 3) * 256 + (p & 7) * 16;
+                    in[i] = load_piece<WIDE>(q);
+                    up[i] = load_piece<WIDE>(q + 128);
                 } else {
-                    in[i] = __ldcg(reinterpret_cast<const uint4*>(row) + p);
+                    in[i] = load_piece<WIDE>(row + p * 16);
                 }
             }
         }
@@ -152,43 +191,45 @@ __global__ void __launch_bounds__(256) k_quantize_fp4(const QuantArgs a) {
         for (int i = 0; i < kPieces; ++i) {
             if (p0 + i * a.team >= pieces) break;  // the same for every team
             const int p = p0 + i * a.team + me;
-            float v[8];
             if constexpr (SWIGLU) {
-                float u[8];
-                widen8<T>(in[i], v);
-                widen8<T>(up[i], u);
-                uint32_t* h = &in[i].x;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    h[j] = pack2(T(), silu(v[2 * j]) * u[2 * j], silu(v[2 * j + 1]) * u[2 * j + 1]);
+                in[i].a = swiglu8<T>(in[i].a, up[i].a);
+                in[i].b = swiglu8<T>(in[i].b, up[i].b);
             }
-            constexpr uint32_t kAbs = 0x7FFF7FFFu;
-            uint32_t top2 = max_u16x2(max_u16x2(in[i].x & kAbs, in[i].y & kAbs), max_u16x2(in[i].z & kAbs, in[i].w & kAbs));
-#pragma unroll
-            for (int o = 1; o < kShare; o <<= 1) top2 = max_u16x2(top2, __shfl_xor_sync(0xFFFFFFFFu, top2, o));
+            uint32_t top2 = max_u16x2(top_of(in[i].a), top_of(in[i].b));
+            if constexpr (!NV) top2 = max_u16x2(top2, __shfl_xor_sync(0xFFFFFFFFu, top2, 1));
             const uint32_t bits = max(top2 & 0xFFFFu, top2 >> 16);
-            uint32_t code, q = 0;
-            if (bits >= kInf<T>) {  // a NaN or infinity: the whole block is NaN
-                code = NV ? 0x7Fu : 0xFFu;
-            } else if constexpr (NV) {
+            const bool bad = bits >= kInf<T>;  // a NaN or infinity: the whole block is NaN
+            uint32_t code;
+            float v[8];
+            uint2 q = make_uint2(0, 0);
+            if constexpr (NV) {
                 code = f32_to_e4m3(fminf(widen1(T(), bits) / (g * 6.0f), 448.0f));
                 const float s = e4m3_to_f32(code) * g;
-                if (s > 0.0f) {
-                    widen8<T>(in[i], v);
+                if (s > 0.0f && !bad) {
+                    widen8<T>(in[i].a, v);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] /= s;
-                    q = f32x8_to_e2m1(v);
+                    q.x = f32x8_to_e2m1(v);
+                    widen8<T>(in[i].b, v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] /= s;
+                    q.y = f32x8_to_e2m1(v);
                 }
+                code = bad ? 0x7Fu : code;
             } else {
                 // amax = 1.m * 2^(e - 127) <= 1.5 * 2^2 * 2^(code - 127)
                 const uint32_t top = __float_as_uint(widen1(T(), bits));
                 const int c = static_cast<int>(top >> 23) - ((top & 0x7FFFFFu) <= 0x400000u ? 2 : 1);
                 code = top ? static_cast<uint32_t>(max(c, 0)) : 127u;
-                scale8(T(), in[i], __uint_as_float((254u - code) << 23), v);  // times 2^(127 - code)
-                q = f32x8_to_e2m1(v);
+                const float inv = bad ? 0.0f : __uint_as_float((254u - code) << 23);  // 2^(127 - code)
+                scale8(T(), in[i].a, inv, v);
+                q.x = f32x8_to_e2m1(v);
+                scale8(T(), in[i].b, inv, v);
+                q.y = f32x8_to_e2m1(v);
+                code = bad ? 0xFFu : code;
             }
             if (real && p < pieces) {
-                if ((me & (kShare - 1)) == 0) scales[p / kShare] = static_cast<uint8_t>(code);
+                if (NV || (me & 1) == 0) scales[NV ? p : p >> 1] = static_cast<uint8_t>(code);
                 codes[p] = q;
             }
         }
@@ -209,16 +250,16 @@ __global__ void __launch_bounds__(256)
     const int pieces = K / 8;
     const float g = NV && tensor_scale ? ld_dep(tensor_scale) : 1.0f;
     const uint32_t* row = reinterpret_cast<const uint32_t*>(codes + r * (K / 2));
-    for (int p0 = 0; p0 < pieces; p0 += kPieces * team) {
-        uint32_t q[kPieces], code[kPieces];
+    for (int p0 = 0; p0 < pieces; p0 += 8 * team) {
+        uint32_t q[8], code[8];
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
+        for (int i = 0; i < 8; ++i) {
             const int p = p0 + i * team + me;
             q[i] = p < pieces ? ld_dep(row + p) : 0u;
             code[i] = p < pieces ? ld_dep(scales + r * stride + p / kShare) : 0u;
         }
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
+        for (int i = 0; i < 8; ++i) {
             const int p = p0 + i * team + me;
             if (p >= pieces) break;
             const float s = NV ? e4m3_to_f32(code[i]) : e8m0_to_f32(code[i]);
@@ -235,9 +276,9 @@ __global__ void __launch_bounds__(256)
 }
 
 // Threads per row: an eighth of its pieces, rounded up to a power of two.
-int team_of(int K) {
+int team_of(int pieces) {
     int team = 8;
-    while (team < 256 && team * kPieces < K / 8) team *= 2;
+    while (team < 256 && team * 8 < pieces) team *= 2;
     return team;
 }
 
@@ -297,19 +338,20 @@ extern "C" moe_status_t moe_quantize_fp4(int32_t fmt, int32_t dtype, int64_t row
     a.tensor_scale = tensor_scale;
     a.codes = static_cast<uint8_t*>(codes);
     a.scales = static_cast<uint8_t*>(scales);
-    a.team = team_of(K);
+    a.team = team_of(K / 16);
     const dim3 grid(static_cast<unsigned>(blocks_for(rows, a.team)));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool nv = fmt == MOE_FP4_NV, bf = dtype == MOE_DTYPE_BF16;
+    const bool nv = fmt == MOE_FP4_NV, wide = (reinterpret_cast<uintptr_t>(x) & 31) == 0 && ldx % 16 == 0;
     auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, st, a); };
-    cudaError_t e;
-    if (bf)
-        e = nv ? (swiglu ? go(k_quantize_fp4<__nv_bfloat16, true, true>) : go(k_quantize_fp4<__nv_bfloat16, true, false>))
-               : (swiglu ? go(k_quantize_fp4<__nv_bfloat16, false, true>)
-                         : go(k_quantize_fp4<__nv_bfloat16, false, false>));
-    else
-        e = nv ? (swiglu ? go(k_quantize_fp4<__half, true, true>) : go(k_quantize_fp4<__half, true, false>))
-               : (swiglu ? go(k_quantize_fp4<__half, false, true>) : go(k_quantize_fp4<__half, false, false>));
+    auto pick = [&](auto t) {
+        using T = decltype(t);
+        if (nv)
+            return swiglu ? (wide ? go(k_quantize_fp4<T, true, true, true>) : go(k_quantize_fp4<T, true, true, false>))
+                          : (wide ? go(k_quantize_fp4<T, true, false, true>) : go(k_quantize_fp4<T, true, false, false>));
+        return swiglu ? (wide ? go(k_quantize_fp4<T, false, true, true>) : go(k_quantize_fp4<T, false, true, false>))
+                      : (wide ? go(k_quantize_fp4<T, false, false, true>) : go(k_quantize_fp4<T, false, false, false>));
+    };
+    const cudaError_t e = dtype == MOE_DTYPE_BF16 ? pick(__nv_bfloat16()) : pick(__half());
     return e == cudaSuccess ? MOE_OK : set_last_error(MOE_ERR_CUDA, "4-bit quantisation: %s", cudaGetErrorString(e));
 }
 
@@ -327,7 +369,7 @@ extern "C" moe_status_t moe_dequantize_fp4(int32_t fmt, int32_t dtype, int64_t r
     if (ldo < K || ldo % 8)
         return set_last_error(MOE_ERR_INVALID_ARG, "the row stride must cover the row and be a multiple of 8 elements");
     const int stride = static_cast<int>(moe_fp4_scale_stride(fmt, K));
-    const int team = team_of(K);
+    const int team = team_of(K / 8);
     const dim3 grid(static_cast<unsigned>(blocks_for(rows, team)));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     auto go = [&](auto kernel, auto* o) {
