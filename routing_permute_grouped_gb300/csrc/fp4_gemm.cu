@@ -123,9 +123,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t one = elect_one();
         Ring r;
         uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
-        int e = 0;
+        RaggedFeed feed;
         for (int t = first; t < total && !timed_out; t += stride) {
-            const RaggedItem it = uniform(ragged_item(tiles, panels, t, e));
+            const RaggedItem it = feed.next(tiles, args.E, panels, total, t, stride, lane);
             const int half = ((it.rows + 31) & ~31) / 2;  // token rows of each CTA
             const int xrow = it.row + half * static_cast<int>(rank);
             const int wrow = it.panel * 256 + 128 * static_cast<int>(rank);
@@ -164,9 +164,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             Acc acc;
             Ring buf;  // scale buffer
             bool issued = false, ready = false;
-            int e = 0;
+            RaggedFeed feed;
             for (int t = first; t < total && !timed_out; t += stride) {
-                const RaggedItem it = uniform(ragged_item(tiles, panels, t, e));
+                const RaggedItem it = feed.next(tiles, args.E, panels, total, t, stride, lane);
                 const uint32_t n = (it.rows + 31) & ~31;
                 const uint32_t idesc = idesc0 | ((n >> 3) << 17);
                 if (!warp_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
@@ -227,9 +227,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---------------------------------------------------- scale loads
         int s = 0;
         uint32_t ph = 0;
-        int e = 0;
+        RaggedFeed feed;
         for (int t = first; t < total && !timed_out; t += stride) {
-            const RaggedItem it = ragged_item(tiles, panels, t, e);
+            const RaggedItem it = feed.next(tiles, args.E, panels, total, t, stride, lane);
             const int64_t w_last = static_cast<int64_t>(it.e + 1) * args.N - 1;
             const int64_t w0 = static_cast<int64_t>(it.e) * args.N + it.panel * 256 + 128 * static_cast<int>(rank);
             const uint8_t* wp[4];

@@ -87,23 +87,53 @@ __device__ void ragged_tiles_build(const RaggedArgs& a, RaggedTiles& s, int pane
     if (lane == 0) s.first[a.E] = running;
 }
 
-// Item t; e is the group of the caller's last item (0 at first), from which the
-// search goes on.  Inside a group, token tiles pass over eight panels at a time,
-// so the items in flight share both operands in L2.
-__device__ __forceinline__ RaggedItem ragged_item(const RaggedTiles& s, int panels, int t, int& e) {
-    while (s.first[e + 1] <= t) ++e;
+// Item t: its group by bisection; inside a group, token tiles pass over eight
+// panels at a time, so the items in flight share both operands in L2.
+__device__ __forceinline__ RaggedItem ragged_item(const RaggedTiles& s, int n_groups, int panels, int t) {
+    int e = 0, end = n_groups;  // first[e] <= t < first[end]
+    while (end - e > 1) {
+        const int mid = (e + end) >> 1;
+        if (s.first[mid] <= t)
+            e = mid;
+        else
+            end = mid;
+    }
     RaggedItem it;
     it.e = e;
     const unsigned tiles = s.tiles[e], width = s.width[e];
     const unsigned i = t - s.first[e];
     const unsigned block = i / (tiles * 8), rest = i - block * tiles * 8;
     const unsigned wide = min(8u, panels - block * 8);
-    const unsigned tile = wide == 8 ? rest >> 3 : rest / wide;
+    const unsigned tile = rest / wide;
     it.panel = block * 8 + rest - tile * wide;
     it.row = s.lo[e] + tile * width;
     it.rows = min(static_cast<int>(width), s.hi[e] - it.row);
     return it;
 }
+
+// A warp's items first, first + stride, ...: the lanes find 32 of them at a time,
+// and each is then four shuffles, which also make it warp-uniform.  Finding an
+// item alone takes some 500 cycles, which every role of the pipeline would
+// spend at every tile.
+struct RaggedFeed {
+    RaggedItem mine;
+    int k = 32;
+    __device__ __forceinline__ RaggedItem next(const RaggedTiles& s, int n_groups, int panels, int total, int t,
+                                               int stride, int lane) {
+        if (k == 32) {
+            k = 0;
+            const int64_t at = t + static_cast<int64_t>(lane) * stride;
+            if (at < total) mine = ragged_item(s, n_groups, panels, static_cast<int>(at));
+        }
+        RaggedItem it;
+        it.e = __shfl_sync(0xFFFFFFFFu, mine.e, k);
+        it.panel = __shfl_sync(0xFFFFFFFFu, mine.panel, k);
+        it.row = __shfl_sync(0xFFFFFFFFu, mine.row, k);
+        it.rows = __shfl_sync(0xFFFFFFFFu, mine.rows, k);
+        ++k;
+        return it;
+    }
+};
 
 template <typename T>
 __device__ __forceinline__ float to_float(T v);
@@ -184,13 +214,6 @@ struct PairBars {
 // is where TMA and the MMAs take them from.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
-__device__ __forceinline__ RaggedItem uniform(RaggedItem it) {
-    it.e = uniform(it.e);
-    it.panel = uniform(it.panel);
-    it.row = uniform(it.row);
-    it.rows = uniform(it.rows);
-    return it;
-}
 
 // A bounded wait of a converged warp; the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort) {
@@ -291,14 +314,14 @@ __device__ __forceinline__ bool product_epilogue(const RaggedArgs& args, const R
     constexpr int kChunks = TN / 64;
     const int q = (threadIdx.x >> 5) & 3, odd = ew >> 2;
     const volatile uint32_t* abort_flag = &bars.abort;
-    int e = 0;
+    RaggedFeed feed;
     RaggedItem it{};
     float gate[kChunks], scale = 1.0f;
     // item t, its scale and the routing weight of this lane's token of each
     // chunk; nothing is computed with them before they are needed
     auto fetch = [&](int t) {
         if (t >= total) return;
-        it = ragged_item(tiles, panels, t, e);
+        it = feed.next(tiles, args.E, panels, total, t, stride, lane);
         scale = scale_of(it.e);
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {

@@ -101,9 +101,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
         const uint32_t one = elect_one();
         Ring r;
         uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
-        int e = 0;
+        RaggedFeed feed;
         for (int t = first; t < total && !timed_out; t += stride) {
-            const RaggedItem it = uniform(ragged_item(tiles, panels, t, e));
+            const RaggedItem it = feed.next(tiles, args.E, panels, total, t, stride, lane);
             const int half = ((it.rows + 31) & ~31) / 2;  // token rows of each CTA
             const int xrow = it.row + half * static_cast<int>(rank);
             const int wrow = it.panel * 256 + 128 * static_cast<int>(rank);
@@ -149,9 +149,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
             Ring r;
             Acc acc;
             bool issued = false, ready = false;
-            int e = 0;
+            RaggedFeed feed;
             for (int t = first; t < total && !timed_out; t += stride) {
-                const RaggedItem it = uniform(ragged_item(tiles, panels, t, e));
+                const RaggedItem it = feed.next(tiles, args.E, panels, total, t, stride, lane);
                 const uint32_t n = (it.rows + 31) & ~31;
                 const uint32_t idesc = Elem<T>::idesc | ((n >> 3) << 17) | (WT ? kTransA : 0u);
                 if (!warp_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
@@ -210,7 +210,6 @@ struct GradTile {
     int row, rows;   // the group's rows
 };
 
-// Called by converged warps.
 __device__ __forceinline__ GradTile grad_tile(const RaggedArgs& a, int t) {
     const int nt = (a.N + 255) / 256, mt = (a.K + 255) / 256;
     GradTile g;
@@ -219,10 +218,31 @@ __device__ __forceinline__ GradTile grad_tile(const RaggedArgs& a, int t) {
     g.m = r / nt * 256;
     g.n = r % nt * 256;
     const int2 rows = group_rows(a, g.e);
-    g.row = uniform(rows.x);
-    g.rows = uniform(rows.y - rows.x);
+    g.row = rows.x;
+    g.rows = rows.y - rows.x;
     return g;
 }
+
+// A warp's tiles, found 32 at a time (see RaggedFeed).
+struct GradFeed {
+    GradTile mine;
+    int k = 32;
+    __device__ __forceinline__ GradTile next(const RaggedArgs& a, int total, int t, int stride, int lane) {
+        if (k == 32) {
+            k = 0;
+            const int64_t at = t + static_cast<int64_t>(lane) * stride;
+            if (at < total) mine = grad_tile(a, static_cast<int>(at));
+        }
+        GradTile g;
+        g.e = __shfl_sync(0xFFFFFFFFu, mine.e, k);
+        g.m = __shfl_sync(0xFFFFFFFFu, mine.m, k);
+        g.n = __shfl_sync(0xFFFFFFFFu, mine.n, k);
+        g.row = __shfl_sync(0xFFFFFFFFu, mine.row, k);
+        g.rows = __shfl_sync(0xFFFFFFFFu, mine.rows, k);
+        ++k;
+        return g;
+    }
+};
 
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps, 1)
@@ -256,8 +276,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
         const uint32_t one = elect_one();
         Ring r;
         uint32_t armed = 0, armed_par = 0, tails = 0, tail_par = 0, tail_ph = 0;
+        GradFeed feed;
         for (int t = first; t < total && !timed_out; t += stride) {
-            const GradTile g = grad_tile(args, t);
+            const GradTile g = feed.next(args, total, t, stride, lane);
             const int ac = g.m + 128 * static_cast<int>(rank), bc = g.n + 128 * static_cast<int>(rank);
             for (int k = 0; k < g.rows; k += kBK) {
                 if (!warp_wait(bars.empty + r.s, r.ph ^ 1u, abort_flag)) {
@@ -314,8 +335,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
             Ring r;
             Acc acc;
             bool issued = false, ready = false;
+            GradFeed feed;
             for (int t = first; t < total && !timed_out; t += stride) {
-                const GradTile g = grad_tile(args, t);
+                const GradTile g = feed.next(args, total, t, stride, lane);
                 if (g.rows == 0) continue;  // the epilogue writes zeros
                 if (!warp_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
                     timed_out = true;
@@ -358,8 +380,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
         // ------------------------------------------------- zeroing of tails
         Ring r;
         uint32_t tail_ph = 0;
+        GradFeed feed;
         for (int t = first; t < total && !timed_out; t += stride) {
-            const GradTile g = grad_tile(args, t);
+            const GradTile g = feed.next(args, total, t, stride, lane);
             const int steps = (g.rows + kBK - 1) / kBK, rest = g.rows % kBK;
             for (int k = 0; k + 1 < steps; ++k) r.next<S>();
             if (steps == 0) continue;
@@ -395,8 +418,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
         Acc acc;
         int buf = 0;
         uint8_t* stage = sOut + ew * 2 * 4096;
+        GradFeed feed;
         for (int t = first; t < total; t += stride) {
-            const GradTile g = grad_tile(args, t);
+            const GradTile g = feed.next(args, total, t, stride, lane);
             const int m = g.m + 128 * static_cast<int>(rank) + q * 32;
             const int n = g.n + c0;
             uint32_t pk[64];
