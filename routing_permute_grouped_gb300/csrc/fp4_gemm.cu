@@ -2,8 +2,8 @@
 // scales: y[r] = row_scale[r] * gx * gw[e] * sum_k x[r, k] W[e][n, k].
 //
 // The schedule of the 16-bit product (ragged_gemm.cu): 256 rows of W[e] are
-// the M of a CTA pair's MMAs, a token tile of at most 192 rows the N, in steps
-// of 32.  The MMAs (tcgen05 kind::mxf4 / kind::mxf4nvf4, K = 64) multiply the
+// the M of a CTA pair's MMAs, a token tile of at most 224 (MX) or 192 (NV) rows
+// the N, in steps of 32.  The MMAs (tcgen05 kind::mxf4 / kind::mxf4nvf4, K = 64) multiply the
 // e2m1 codes with their block scales as they are, so nothing is widened: a
 // step of 256 elements is 128 bytes of each row.
 //
@@ -16,17 +16,24 @@
 // l, l + 32, l + 64, ..., and store them to tensor memory word by word; the
 // transposition is a renaming of registers.  (Laying the words out in shared
 // memory for tcgen05.cp needs the writes published to the tensor core of both
-// CTAs: that cluster-scope release made a decode step over
-// 256 experts 884 us instead of 507.)
-// Bytes past K are cleared on the way (they may hold anything), rows past the
-// operand repeat its last row and reach no stored result.
+// CTAs: that cluster-scope release made a decode step over 256 experts 884 us
+// instead of 507.)  Bytes past K are cleared on the way (they may hold
+// anything), rows past the operand repeat its last row and reach no stored
+// result.  A step's barrier is full when its codes have landed and its scales
+// are written: one wait per step, because a wait costs the MMA warp some 100
+// cycles even when there is nothing to wait for (445 against 405 us with two).
 //
-// Tensor memory: two accumulators of 192 columns, and buffers for the scales of
-// one step of 256 elements (MX five of 24 columns, NV two of 48).  A buffer is
-// written again once its MMAs are complete.
+// What bounds it (default gate/up product of 8 experts, 32768 rows, 7168 ->
+// 4096, MX: 324 us, 5.9 PFLOP/s): the issue of the MMAs, whose operands and
+// scale addresses make it about 90 cycles each against 112 of execution, with
+// the waits on top; loads alone take 250 us, the launch without scales 290.
+// Decode (two rows for each of 256 experts) runs at the weights' bytes over HBM.
+// Short sums (K = 1024) are bound by the epilogue.
+//
+// A scale buffer in tensor memory is written again once its MMAs are complete.
 //
 // Warp roles: warp 0 TMA producer, warp 1 tensor memory and MMA issue (even
-// CTA), warp 2 scale loads, warps 4..11 scale layout, warps 12..19 epilogue.
+// CTA), warp 2 scale loads, warps 4..7 scale layout, warps 8..15 epilogue.
 // Every wait is bounded, as in ragged_gemm.cu.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -41,50 +48,55 @@ namespace moe {
 
 namespace {
 
-constexpr int kTN = 192;                  // token rows of a tile, at most
 constexpr int kStep = 256;                // step of the sum: 128 bytes of codes
 constexpr int kWBytes = 128 * 128;        // weight codes of one CTA and stage
-constexpr int kStage = kWBytes + kTN / 2 * 128;
-constexpr int kStages = 6;
-constexpr uint32_t kScaleCol = 2 * kTN;   // first tensor-memory column of the scale buffers
-// A scale buffer holds the words of kUnit = 256 elements: two of MX, four of NV,
-// each 4 columns of A and 8 of B.
-template <bool NV>
-struct Scales {
-    static constexpr int words = NV ? 4 : 2;
-    static constexpr uint32_t cols = words * 12;
-    static constexpr int bufs = NV ? 2 : 5;
-    static_assert(kScaleCol + bufs * cols <= 512, "tensor memory budget");
-};
-constexpr int kRaw = 7;                   // scale groups in shared memory
-constexpr int kRawRows = (4 + kTN / 32) * 512;  // 32-row pieces of 512 bytes: weights, tokens
-constexpr int kLayoutSets = 1;            // of four warps, one per lane quarter
-constexpr int kEpi0 = 4 + 4 * kLayoutSets;  // first epilogue warp
+constexpr int kEpi0 = 8;                  // first epilogue warp
 constexpr int kThreads = 32 * (kEpi0 + kEpiWarps);
 
-struct ScaleBars {
-    uint64_t raw_full[kRaw], raw_empty[kRaw];  // groups in shared memory
+// Issuing a step's four MMAs takes about 450 cycles whatever their N, and an MMA
+// runs N / 2 cycles, so the widest tile is the fastest.  Two accumulators and
+// two scale buffers (the words of one step, two of MX and four of NV, each 4
+// columns of A and 8 of B) must fit 512 columns of tensor memory: 224 token rows
+// for MX, 192 for NV (MX with 192: 342 against 324 us).
+template <bool NV>
+struct Cfg {
+    static constexpr int TN = NV ? 192 : 224;  // token rows of a tile, at most
+    static constexpr int pieces = 4 + TN / 32;  // 32-row pieces of a tile's scales: weights, tokens
+    static constexpr int stage = kWBytes + TN / 2 * 128;
+    static constexpr int stages = NV ? 6 : 5;
+    static constexpr int raw = 7;               // scale groups in shared memory
+    static constexpr int raw_bytes = pieces * 512;
+    static constexpr int words = NV ? 4 : 2;    // of a step's scales
+    static constexpr int bufs = 2;              // scale buffers
+    static constexpr uint32_t cols = words * 12;
+    static constexpr uint32_t scale_col = 2 * TN;  // the first one's tensor-memory column
+    static constexpr int smem =
+        1024 + stages * stage + raw * raw_bytes + kEpiStage + 1024 + static_cast<int>(sizeof(RaggedTiles));
+    static_assert(scale_col + bufs * cols <= 512, "tensor memory budget");
+    static_assert(smem <= 232448, "shared memory budget");
+    static_assert(stage % 1024 == 0, "swizzled tiles need 1024-byte alignment");
 };
-constexpr int kSmem =
-    1024 + kStages * kStage + kRaw * kRawRows + kEpiStage + 1024 + static_cast<int>(sizeof(RaggedTiles));
-static_assert(kSmem <= 232448, "shared memory budget");
-static_assert(kStage % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+
+template <int RAW>
+struct ScaleBars {
+    uint64_t raw_full[RAW], raw_empty[RAW];  // groups in shared memory
+};
 
 template <bool NV>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_ragged_product_fp4(const __grid_constant__ CUtensorMap tW, const __grid_constant__ RowMaps tX,
                          const uint8_t* w_scales, const uint8_t* x_scales, const int pitch, const RaggedArgs args) {
-    constexpr int S = kStages;
+    using C = Cfg<NV>;
+    constexpr int S = C::stages;
     constexpr int kGroup = NV ? 256 : 512;  // elements under 16 scale bytes
-    using SC = Scales<NV>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint8_t* raw = smem + S * kStage;
-    uint8_t* sOut = raw + kRaw * kRawRows;
+    uint8_t* raw = smem + S * C::stage;
+    uint8_t* sOut = raw + C::raw * C::raw_bytes;
     PairBars<S>& bars = *reinterpret_cast<PairBars<S>*>(sOut + kEpiStage);
-    ScaleBars& sb = *reinterpret_cast<ScaleBars*>(&bars + 1);
-    static_assert(sizeof(PairBars<S>) % 8 == 0 && sizeof(PairBars<S>) + sizeof(ScaleBars) <= 1024, "barriers");
+    ScaleBars<C::raw>& sb = *reinterpret_cast<ScaleBars<C::raw>*>(&bars + 1);
+    static_assert(sizeof(PairBars<S>) % 8 == 0 && sizeof(PairBars<S>) + sizeof(ScaleBars<C::raw>) <= 1024, "barriers");
     RaggedTiles& tiles = *reinterpret_cast<RaggedTiles*>(sOut + kEpiStage + 1024);
     volatile uint32_t* abort_flag = &bars.abort;
 
@@ -97,7 +109,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int groups = (args.K + kGroup - 1) / kGroup;
     pdl_trigger();
     if (threadIdx.x == 32) {
-        for (int i = 0; i < kRaw; ++i) {
+        for (int i = 0; i < C::raw; ++i) {
             mbar_init(sb.raw_full + i, 32);  // every lane's copies
             mbar_init(sb.raw_empty + i, 4);  // every layout warp
         }
@@ -107,7 +119,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // a step is full when its codes have landed and the four layout warps of
     // both CTAs have written its scales
     pair_start(bars, 9, warp);
-    if (warp == 2) ragged_tiles_build<kTN>(args, tiles, panels, lane);
+    if (warp == 2) ragged_tiles_build<C::TN>(args, tiles, panels, lane);
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // the peer's barriers are initialised before any remote use
@@ -135,7 +147,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     break;
                 }
                 const uint32_t full = mapa_shared(smem_u32(bars.full + r.s), 0);
-                uint8_t* st = smem + r.s * kStage;
+                uint8_t* st = smem + r.s * C::stage;
                 armed &= ~(1u << r.s);
                 if (leader) mbar_arrive_expect_tx_if(one, bars.full + r.s, 2 * (kWBytes + half * 128));
                 tma_load_3d_pair_if(one, st, &tW, k * 128, wrow, it.e, full);
@@ -173,7 +185,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     timed_out = true;
                     break;
                 }
-                const uint32_t d = tmem_base + static_cast<uint32_t>(acc.i * kTN);
+                const uint32_t d = tmem_base + static_cast<uint32_t>(acc.i * C::TN);
                 for (int k = 0; k < steps; ++k) {
                     if (!ready && !warp_wait(bars.full + r.s, r.ph, abort_flag)) {
                         timed_out = true;
@@ -184,8 +196,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     // issued: the issue, not the tensor pipe, sets the pace
                     const Ring next = r.after<S>();
                     const bool peek = mbar_test_wait(bars.full + next.s, next.ph);
-                    const uint32_t at = static_cast<uint32_t>(r.s) * (kStage >> 4);
-                    const uint32_t sa = tmem_base + kScaleCol + static_cast<uint32_t>(buf.s) * SC::cols;
+                    const uint32_t at = static_cast<uint32_t>(r.s) * (C::stage >> 4);
+                    const uint32_t sa = tmem_base + C::scale_col + static_cast<uint32_t>(buf.s) * C::cols;
                     const int left = args.K - k * kStep;
                     if (one) {
                         auto mma = [&](int kk) {  // 64 elements of each 128-byte row
@@ -193,7 +205,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             const uint32_t byte = NV ? 0u : static_cast<uint32_t>(kk & 1) * 2u;
                             mma_e2m1_pair<NV>(d, wd0 + (at + kk * 2), xd0 + (at + kk * 2),
                                               idesc | (byte << 4) | (byte << 29), sa + word * 4,
-                                              sa + SC::words * 4 + word * 8, (k | kk) != 0 ? 1u : 0u);
+                                              sa + C::words * 4 + word * 8, (k | kk) != 0 ? 1u : 0u);
                         };
                         if (left >= kStep) {
 #pragma unroll
@@ -209,7 +221,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     ready = __all_sync(0xFFFFFFFFu, peek);
                     issued = true;
-                    buf.next<SC::bufs>();
+                    buf.next<C::bufs>();
                     r = next;
                 }
                 if (timed_out) break;
@@ -233,25 +245,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int64_t w_last = static_cast<int64_t>(it.e + 1) * args.N - 1;
             const int64_t w0 = static_cast<int64_t>(it.e) * args.N + it.panel * 256 + 128 * static_cast<int>(rank);
             const uint8_t* wp[4];
-            const uint8_t* xp[kTN / 32];
+            const uint8_t* xp[C::TN / 32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) wp[c] = w_scales + min(w0 + c * 32 + lane, w_last) * pitch;
 #pragma unroll
-            for (int c = 0; c < kTN / 32; ++c)
+            for (int c = 0; c < C::TN / 32; ++c)
                 xp[c] = x_scales + static_cast<int64_t>(it.row + min(c * 32 + lane, it.rows - 1)) * pitch;
             for (int g = 0; g < groups; ++g) {
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(sb.raw_empty + s, ph ^ 1u, abort_flag))) {
                     timed_out = true;
                     break;
                 }
-                const uint32_t dst = smem_u32(raw + s * kRawRows) + lane * 16;
+                const uint32_t dst = smem_u32(raw + s * C::raw_bytes) + lane * 16;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) cp_async_16(dst + c * 512, wp[c] + g * 16, 16);
 #pragma unroll
-                for (int c = 0; c < kTN / 32; ++c)
+                for (int c = 0; c < C::TN / 32; ++c)
                     if (c * 32 < it.rows) cp_async_16(dst + (4 + c) * 512, xp[c] + g * 16, 16);
                 cp_async_arrive(sb.raw_full + s);
-                if (++s == kRaw) {
+                if (++s == C::raw) {
                     s = 0;
                     ph ^= 1u;
                 }
@@ -264,84 +276,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // no part: the layout warps start at a multiple of four
     } else if (warp < kEpi0) {
         // --------------------------------------------------- scale layout
-        // Two sets of warps take the groups in turn: waiting for a buffer,
-        // storing to it and handing it on is one chain of latencies.
-        constexpr int kPieces = 4 + kTN / 32;
-        const int set = (warp - 4) >> 2;
         const int valid = args.K / (NV ? 16 : 32);  // scale bytes of a row
         const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        int s = 0, turn = 0;
+        int s = 0;
         uint32_t ph = 0;
         Ring buf;
-        // the stage of the step whose buffer is written next, SC::bufs steps ago
+        // the stage of the step whose buffer is written next, C::bufs steps ago
         Ring old, cur;  // cur: its own
-        int fresh = SC::bufs;  // buffers not yet written
+        int fresh = C::bufs;  // buffers not yet written
         for (int t = first; t < total && !timed_out; t += stride) {
             for (int g = 0; g < groups; ++g) {
                 const int left = valid - g * 16;  // bytes of this group inside K
-                uint4 v[kPieces];
-                const bool mine = turn == set;
-                if (++turn == kLayoutSets) turn = 0;
-                if (mine) {
-                    if (!warp_wait(sb.raw_full + s, ph, abort_flag)) {
-                        timed_out = true;
-                        break;
-                    }
-                    const uint4* src = reinterpret_cast<const uint4*>(raw + s * kRawRows) + lane;
-#pragma unroll
-                    for (int c = 0; c < kPieces; ++c) v[c] = src[c * 32];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sb.raw_empty + s);
-                    if (left < 16) {
-                        uint32_t m[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int b = left - 4 * q;
-                            m[q] = b >= 4 ? 0xFFFFFFFFu : (b <= 0 ? 0u : (1u << (8 * b)) - 1u);
-                        }
-#pragma unroll
-                        for (int c = 0; c < kPieces; ++c)
-                            v[c] = make_uint4(v[c].x & m[0], v[c].y & m[1], v[c].z & m[2], v[c].w & m[3]);
-                    }
+                uint4 v[C::pieces];
+                if (!warp_wait(sb.raw_full + s, ph, abort_flag)) {
+                    timed_out = true;
+                    break;
                 }
-                if (++s == kRaw) {
+                const uint4* src = reinterpret_cast<const uint4*>(raw + s * C::raw_bytes) + lane;
+#pragma unroll
+                for (int c = 0; c < C::pieces; ++c) v[c] = src[c * 32];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sb.raw_empty + s);
+                if (left < 16) {
+                    uint32_t m[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int b = left - 4 * q;
+                        m[q] = b >= 4 ? 0xFFFFFFFFu : (b <= 0 ? 0u : (1u << (8 * b)) - 1u);
+                    }
+#pragma unroll
+                    for (int c = 0; c < C::pieces; ++c)
+                        v[c] = make_uint4(v[c].x & m[0], v[c].y & m[1], v[c].z & m[2], v[c].w & m[3]);
+                }
+                if (++s == C::raw) {
                     s = 0;
                     ph ^= 1u;
                 }
 #pragma unroll
-                for (int h = 0; h < 4 / SC::words; ++h) {  // the group's buffers
-                    if (4 * SC::words * h >= left) break;
-                    if (mine) {
-                        // the MMAs that last read this buffer are complete
-                        if (fresh == 0 && !warp_wait(bars.empty + old.s, old.ph, abort_flag)) {
-                            timed_out = true;
-                            break;
-                        }
-                        tc_fence_after();
-                        uint32_t a[4 * SC::words], b[8 * SC::words];
-#pragma unroll
-                        for (int q = 0; q < SC::words; ++q) {
-                            auto word = [&](int c) {
-                                const int i = SC::words * h + q;
-                                return i == 0 ? v[c].x : i == 1 ? v[c].y : i == 2 ? v[c].z : v[c].w;
-                            };
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) a[4 * q + c] = word(c);
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) b[8 * q + c] = c < kTN / 32 ? word(4 + (c < kTN / 32 ? c : 0)) : 0u;
-                        }
-                        const uint32_t dst = tmem_base + quarter + kScaleCol + static_cast<uint32_t>(buf.s) * SC::cols;
-                        tmem_st(dst, a);
-                        tmem_st(dst + 4 * SC::words, b);
-                        tmem_st_wait();
-                        // the words are in tensor memory; the MMA side reads
-                        // nothing else of this warp's, so the arrive releases
-                        // nothing
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.full + cur.s), 0));
+                for (int h = 0; h < 4 / C::words; ++h) {  // the group's buffers
+                    if (4 * C::words * h >= left) break;
+                    // the MMAs that last read this buffer are complete
+                    if (fresh == 0 && !warp_wait(bars.empty + old.s, old.ph, abort_flag)) {
+                        timed_out = true;
+                        break;
                     }
-                    buf.next<SC::bufs>();
+                    tc_fence_after();
+                    uint32_t a[4 * C::words], b[8 * C::words];
+#pragma unroll
+                    for (int q = 0; q < C::words; ++q) {
+                        auto word = [&](int c) {
+                            const int i = C::words * h + q;
+                            return i == 0 ? v[c].x : i == 1 ? v[c].y : i == 2 ? v[c].z : v[c].w;
+                        };
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) a[4 * q + c] = word(c);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) b[8 * q + c] = c < C::TN / 32 ? word(4 + (c < C::TN / 32 ? c : 0)) : 0u;
+                    }
+                    const uint32_t dst = tmem_base + quarter + C::scale_col + static_cast<uint32_t>(buf.s) * C::cols;
+                    tmem_st(dst, a);
+                    tmem_st(dst + 4 * C::words, b);
+                    tmem_st_wait();
+                    // the words are in tensor memory; the MMA side reads
+                    // nothing else of this warp's, so the arrive releases
+                    // nothing
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.full + cur.s), 0));
+                    buf.next<C::bufs>();
                     cur.next<S>();
                     if (fresh)
                         --fresh;
@@ -354,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else {
         // ------------------------------------------------------ epilogue
         const float gx = args.x_scale ? ld_dep(args.x_scale) : 1.0f;
-        if (!product_epilogue<__nv_bfloat16, kTN>(
+        if (!product_epilogue<__nv_bfloat16, C::TN>(
                 args, tiles, bars, panels, total, first, stride, tmem_base, warp - kEpi0, lane, rank,
                 sOut + (warp - kEpi0) * 2048, gx,
                 [&](int e) { return args.w_scale ? ld_dep(args.w_scale + e) : 1.0f; }))
@@ -368,6 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 template <bool NV>
 cudaError_t launch_fp4(const RaggedArgs& a, const void* xq, const uint8_t* xs, const void* wq, const uint8_t* ws,
                        int pitch, cudaStream_t st) {
+    using C = Cfg<NV>;
     static bool ready[kMaxDevices] = {};
     const uint64_t N = a.N, KB = a.K / 2, R = a.R, E = a.E;  // KB bytes of codes per row
     CUtensorMap tW;
@@ -377,8 +380,8 @@ cudaError_t launch_fp4(const RaggedArgs& a, const void* xq, const uint8_t* xs, c
     if (!make_tensor_map(&tW, wq, 3, wd, wst, wb, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
         !make_row_maps(&tX, xq, R, KB, KB, 128, CU_TENSOR_MAP_DATA_TYPE_UINT8))
         return cudaErrorInvalidValue;
-    const int64_t items = (R / kTN + (R < E ? R : E)) * ((N + 255) / 256);  // at most
-    return launch_pairs(k_ragged_product_fp4<NV>, items, kThreads, kSmem, ready, st, tW, tX, ws, xs, pitch,
+    const int64_t items = (R / C::TN + (R < E ? R : E)) * ((N + 255) / 256);  // at most
+    return launch_pairs(k_ragged_product_fp4<NV>, items, kThreads, C::smem, ready, st, tW, tX, ws, xs, pitch,
                               a);
 }
 

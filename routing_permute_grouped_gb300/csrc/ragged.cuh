@@ -311,7 +311,7 @@ __device__ __forceinline__ bool product_epilogue(const RaggedArgs& args, const R
                                                  int panels, int total, int first, int stride, uint32_t tmem_base,
                                                  int ew, int lane, uint32_t rank, uint8_t* stage, float common,
                                                  Scale scale_of) {
-    constexpr int kChunks = TN / 64;
+    constexpr int kChunks = (TN + 32) / 64;
     const int q = (threadIdx.x >> 5) & 3, odd = ew >> 2;
     const volatile uint32_t* abort_flag = &bars.abort;
     RaggedFeed feed;

@@ -201,8 +201,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
 }
 
 // -------------------------------------------------------- weight gradient --
-constexpr int kGradStages = 5;
-constexpr int kOutStage = kEpiWarps * 2 * 4096;  // epilogue warps x 2 buffers x (32 rows x 128 bytes)
+constexpr int kGradStages = 6;
+// One staging buffer (32 rows x 128 bytes) per epilogue warp and a sixth stage:
+// 1.067 against 1.094 ms with two buffers and five stages on the 64-expert
+// layer's gradient, and as fast where the stores bound it (64 experts, 8 rows
+// each: 6.3 TB/s).
+constexpr int kOutStage = kEpiWarps * 4096;
 constexpr int kGradSmem = 1024 + kGradStages * kStage + kOutStage + 1024;
 
 struct GradTile {
@@ -411,13 +415,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
         // ------------------------------------------------------ epilogue
         // Each warp owns 32 rows of M (its tensor-memory lane quarter) and
         // half of the tile's columns, and stores them through TMA from boxes
-        // of 32 x 64 staged in shared memory (two buffers per warp); TMA cuts
+        // of 32 x 64 staged in shared memory; TMA cuts
         // off what lies past M or N.
         const int q = warp & 3, ew = warp - 2;
         const int c0 = (ew >> 2) * 128;
         Acc acc;
-        int buf = 0;
-        uint8_t* stage = sOut + ew * 2 * 4096;
+        uint8_t* stage = sOut + ew * 4096;
         GradFeed feed;
         for (int t = first; t < total; t += stride) {
             const GradTile g = feed.next(args, total, t, stride, lane);
@@ -455,12 +458,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
             }
 #pragma unroll
             for (int c = 0; c < 128; c += 64) {
-                // a box past the edge takes no buffer: the wait below counts
-                // on every turn of a buffer having its store
                 if (m >= args.K || n + c >= args.N) continue;
-                if (lane == 0) bulk_wait_read<1>();  // this buffer's previous store has read it
+                if (lane == 0) bulk_wait_read<0>();  // the previous store has read the buffer
                 __syncwarp();
-                uint8_t* sb = stage + buf * 4096 + lane * 128;
+                uint8_t* sb = stage + lane * 128;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {  // 16-byte chunks of the 128-byte row
                     const uint32_t* u = pk + c / 2 + 4 * j;
@@ -469,10 +470,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    tma_store_3d(&tOut, stage + buf * 4096, n + c, m, g.e);
+                    tma_store_3d(&tOut, stage, n + c, m, g.e);
                     bulk_commit();
                 }
-                buf ^= 1;
             }
         }
         if (lane == 0) bulk_wait_all();
