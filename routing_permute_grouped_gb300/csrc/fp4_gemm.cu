@@ -3,9 +3,9 @@
 //
 // The schedule of the 16-bit product (ragged_gemm.cu): 256 rows of W[e] are
 // the M of a CTA pair's MMAs, a token tile of at most 224 (MX) or 192 (NV) rows
-// the N, in steps of 32.  The MMAs (tcgen05 kind::mxf4 / kind::mxf4nvf4, K = 64) multiply the
-// e2m1 codes with their block scales as they are, so nothing is widened: a
-// step of 256 elements is 128 bytes of each row.
+// the N, in steps of 32.  The MMAs (tcgen05 kind::mxf4 / kind::mxf4nvf4, K = 64)
+// multiply the e2m1 codes with their block scales as they are, so nothing is
+// widened: a step of 256 elements is 128 bytes of each row.
 //
 // Scales.  The MMA wants them in tensor memory as 32-bit words (four bytes
 // along K), word of row r in lane r % 32 and column r / 32, repeated in the
@@ -26,7 +26,7 @@
 // What bounds it (default gate/up product of 8 experts, 32768 rows, 7168 ->
 // 4096, MX: 324 us, 5.9 PFLOP/s): the issue of the MMAs, whose operands and
 // scale addresses make it about 90 cycles each against 112 of execution, with
-// the waits on top; loads alone take 250 us, the launch without scales 290.
+// the waits on top.  The loads alone took 252 us.
 // Decode (two rows for each of 256 experts) runs at the weights' bytes over HBM.
 // Short sums (K = 1024) are bound by the epilogue.
 //
