@@ -23,10 +23,10 @@
 // tiles are written as zeros.
 //
 // What bounds them: at the default layer's gate/up size (32768 rows, 8 experts,
-// 7168 -> 4096) a launch by itself takes 1.00 ms, 1920 TFLOP/s, with the tensor
-// pipe 93 % busy at 1.65 GHz, the board's power limit; back to back 1.15 to 1.19
-// ms.  The data gradient of a 64-expert layer (98304 rows, 2048 -> 4096): 0.89 ms
-// alone, 92 % busy.  The weight gradient: 0.97 ms, 74 % busy, waiting for loads
+// 7168 -> 4096) a launch by itself takes 1.02 ms, 1890 TFLOP/s, with the tensor
+// pipe 93 % busy at 1.63 GHz, the board's power limit; back to back 1.15 to 1.19
+// ms.  The data gradient of a 64-expert layer (98304 rows, 2048 -> 4096): 0.90 ms
+// alone, 92 % busy.  The weight gradient: 0.93 ms, 81 % busy, waiting for loads
 // (two 64-column boxes per operand and step).  Two rows for each of 256 experts:
 // the weights' bytes over HBM.  Clusters of two pairs that share one operand by
 // TMA multicast gained nothing (default 1.169 against 1.187 ms, data gradient
