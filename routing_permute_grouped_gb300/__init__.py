@@ -226,26 +226,39 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _addr(t: Optional[torch.Tensor]):
-    """_ptr as a plain integer: short calls are bound by the host, and a ctypes
-    object per pointer costs about as much as the checks."""
+# The arguments of the grouped products and of the 4-bit rows.  The C side sees
+# only addresses, so type, shape and layout are checked here; short calls are
+# bound by the host, so each tensor is looked at once, and addresses go as plain
+# integers (a ctypes object per pointer costs about as much as the checks).
+def _bad(t, name, dtype, shape):
+    raise ValueError(f"{name}: expected a CUDA tensor, {dtype} {tuple(shape)}, with contiguous "
+                     f"{'rows' if t.dim() == 2 else 'elements'}; got {t.dtype} {tuple(t.shape)}, "
+                     f"strides {t.stride()}, on {t.device}")
+
+
+def _arg(t: Optional[torch.Tensor], name: str, dtype, shape):
+    """Address of a contiguous CUDA tensor of this type and shape, None for None."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    if not t.is_contiguous():
-        raise ValueError("expected a contiguous tensor")
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _bad(t, name, dtype, shape)
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor):
+def _rows(t: torch.Tensor, name: str, dtype, shape):
     """Address and row stride of a [rows, columns] CUDA tensor whose rows are
     contiguous (the stride between rows is free)."""
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("expected a 2D tensor with contiguous rows")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
+        _bad(t, name, dtype, shape)
+    s0, s1 = t.stride()
+    if s1 != 1 and shape[1] > 1:
+        _bad(t, name, dtype, shape)
+    return t.data_ptr(), s0 if shape[0] > 1 else shape[1]
+
+
+def _status(t: Optional[torch.Tensor]):
+    """Address of the device error word: the first 4 bytes of any CUDA tensor."""
+    return None if t is None else _ptr(t).value
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -256,23 +269,17 @@ def _dtype(t: torch.Tensor) -> int:
     return code
 
 
-def _expect(t: Optional[torch.Tensor], name: str, dtype, shape) -> None:
-    """The C side sees only a pointer: what it reads there is checked here."""
-    if t is not None and (t.dtype != dtype or t.shape != shape):
-        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-
-
 # torch's own raw-handle query: building a torch.cuda.Stream object per call takes
 # 2.9 us, as long as the whole C call of a short product
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
     if stream is None:
         if _raw_stream is not None:
-            return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def config_of(shape=None, **kw) -> MoeConfig:
@@ -605,29 +612,27 @@ def moe_grouped_gemm(x, w, offsets, y, row_scale=None, w_transposed: bool = Fals
                      stream=None) -> None:
     """y[r] = row_scale[r] * x[r] W[e]^T for the rows offsets[e] <= r < offsets[e + 1]
     of every group; x [R, K], w [E, N, K] (or [E, K, N], ``w_transposed``: x[r] W[e]),
-    y [R, N], all bf16 or all fp16, rows of x and y at any stride."""
-    (R, K), (E, a, b) = x.shape, w.shape
+    y [R, N], all bf16 or all fp16, rows of x and y at any stride.  ``offsets`` int32
+    [E + 1], or None with E = 1: one group of all rows."""
+    dtype, (R, K), (E, a, b) = x.dtype, x.shape, w.shape
     N = b if w_transposed else a
-    _expect(w, "w", x.dtype, (E, K, N) if w_transposed else (E, N, K))
-    _expect(y, "y", x.dtype, (R, N))
-    _expect(offsets, "offsets", torch.int32, (E + 1,))
-    _expect(row_scale, "row_scale", torch.float32, (R,))
-    (px, ldx), (py, ldy) = _rows(x), _rows(y)
-    _check(load().moe_grouped_gemm(_dtype(x), R, N, K, E, px, ldx, _addr(w), int(w_transposed),
-                                   _addr(offsets), _addr(row_scale), py, ldy, _addr(status),
-                                   _stream(stream)))
+    px, ldx = _rows(x, "x", dtype, (R, K))
+    py, ldy = _rows(y, "y", dtype, (R, N))
+    _check((_lib or load()).moe_grouped_gemm(
+        _dtype(x), R, N, K, E, px, ldx, _arg(w, "w", dtype, (E, K, N) if w_transposed else (E, N, K)),
+        int(w_transposed), _arg(offsets, "offsets", torch.int32, (E + 1,)),
+        _arg(row_scale, "row_scale", torch.float32, (R,)), py, ldy, _status(status), _stream(stream)))
 
 
 def moe_grouped_wgrad(a, b, offsets, out, status=None, stream=None) -> None:
     """out[e] = sum over group e's rows of a[r]^T b[r]: a [R, M], b [R, N],
     out [E, M, N], all bf16 or all fp16."""
-    (R, M), N, E = a.shape, b.shape[1], out.shape[0]
-    _expect(b, "b", a.dtype, (R, N))
-    _expect(out, "out", a.dtype, (E, M, N))
-    _expect(offsets, "offsets", torch.int32, (E + 1,))
-    (pa, lda), (pb, ldb) = _rows(a), _rows(b)
-    _check(load().moe_grouped_wgrad(_dtype(a), R, M, N, E, pa, lda, pb, ldb, _addr(offsets),
-                                    _addr(out), _addr(status), _stream(stream)))
+    dtype, (R, M), N, E = a.dtype, a.shape, b.shape[1], out.shape[0]
+    pa, lda = _rows(a, "a", dtype, (R, M))
+    pb, ldb = _rows(b, "b", dtype, (R, N))
+    _check((_lib or load()).moe_grouped_wgrad(
+        _dtype(a), R, M, N, E, pa, lda, pb, ldb, _arg(offsets, "offsets", torch.int32, (E + 1,)),
+        _arg(out, "out", dtype, (E, M, N)), _status(status), _stream(stream)))
 
 
 def moe_fp4_scale_stride(fmt: int, K: int) -> int:
@@ -642,50 +647,41 @@ def moe_quantize_fp4(fmt: int, x, codes, scales, tensor_scale=None, src=None, sr
     """codes [rows, K / 2] and scales [rows, moe_fp4_scale_stride(fmt, K)] (uint8) of the
     rows of x (bf16 or fp16), or of x[src // src_div]; with ``swiglu`` of silu(gate) * up
     of x's 2 K columns, interleaved per 128."""
-    rows, K = codes.shape[0], codes.shape[1] * 2
-    _expect(codes, "codes", torch.uint8, (rows, K // 2))
-    _expect(scales, "scales", torch.uint8, (rows, moe_fp4_scale_stride(fmt, K)))
-    _expect(src, "src", torch.int32, (rows,))
-    _expect(tensor_scale, "tensor_scale", torch.float32, (1,))
-    _expect(x, "x", x.dtype, (x.shape[0], 2 * K if swiglu else K))
-    px, ldx = _rows(x)
-    _check(load().moe_quantize_fp4(fmt, _dtype(x), rows, K, px, x.shape[0], ldx, _addr(src),
-                                   src_div, int(swiglu), _addr(tensor_scale), _addr(codes),
-                                   _addr(scales), _stream(stream)))
+    rows, half = codes.shape
+    K, x_rows, u8 = 2 * half, x.shape[0], torch.uint8
+    px, ldx = _rows(x, "x", x.dtype, (x_rows, 2 * K if swiglu else K))
+    _check((_lib or load()).moe_quantize_fp4(
+        fmt, _dtype(x), rows, K, px, x_rows, ldx, _arg(src, "src", torch.int32, (rows,)), src_div,
+        int(swiglu), _arg(tensor_scale, "tensor_scale", torch.float32, (1,)),
+        _arg(codes, "codes", u8, (rows, half)),
+        _arg(scales, "scales", u8, (rows, moe_fp4_scale_stride(fmt, K))), _stream(stream)))
 
 
 def moe_dequantize_fp4(fmt: int, codes, scales, out, tensor_scale=None, stream=None) -> None:
     """out [rows, K] (bf16 or fp16) = the values of 4-bit rows."""
     rows, K = out.shape
-    _expect(codes, "codes", torch.uint8, (rows, K // 2))
-    _expect(scales, "scales", torch.uint8, (rows, moe_fp4_scale_stride(fmt, K)))
-    _expect(tensor_scale, "tensor_scale", torch.float32, (1,))
-    po, ldo = _rows(out)
-    _check(load().moe_dequantize_fp4(fmt, _dtype(out), rows, K, _addr(codes), _addr(scales),
-                                     _addr(tensor_scale), po, ldo, _stream(stream)))
+    po, ldo = _rows(out, "out", out.dtype, (rows, K))
+    _check((_lib or load()).moe_dequantize_fp4(
+        fmt, _dtype(out), rows, K, _arg(codes, "codes", torch.uint8, (rows, K // 2)),
+        _arg(scales, "scales", torch.uint8, (rows, moe_fp4_scale_stride(fmt, K))),
+        _arg(tensor_scale, "tensor_scale", torch.float32, (1,)), po, ldo, _stream(stream)))
 
 
 def moe_grouped_gemm_fp4(fmt: int, x_codes, x_scales, w_codes, w_scales, offsets, y, x_scale=None,
                          w_scale=None, row_scale=None, status=None, stream=None) -> None:
     """y[r] = row_scale[r] * x_scale * w_scale[e] * x[r] W[e]^T on 4-bit rows x [R, K] and
     weights [E, N, K] (codes [.., K / 2] and scales [.., stride], uint8); y bf16 [R, N]."""
-    R, K = x_codes.shape[0], x_codes.shape[1] * 2
-    E, N = w_codes.shape[:2]
-    stride = moe_fp4_scale_stride(fmt, K)
-    _expect(x_codes, "x_codes", torch.uint8, (R, K // 2))
-    _expect(x_scales, "x_scales", torch.uint8, (R, stride))
-    _expect(w_codes, "w_codes", torch.uint8, (E, N, K // 2))
-    _expect(w_scales, "w_scales", torch.uint8, (E, N, stride))
-    _expect(y, "y", torch.bfloat16, (R, N))
-    _expect(offsets, "offsets", torch.int32, (E + 1,))
-    _expect(x_scale, "x_scale", torch.float32, (1,))
-    _expect(w_scale, "w_scale", torch.float32, (E,))
-    _expect(row_scale, "row_scale", torch.float32, (R,))
-    py, ldy = _rows(y)
-    _check(load().moe_grouped_gemm_fp4(fmt, R, N, K, E, _addr(x_codes), _addr(x_scales),
-                                       _addr(w_codes), _addr(w_scales), _addr(offsets), _addr(x_scale),
-                                       _addr(w_scale), _addr(row_scale), py, ldy, _addr(status),
-                                       _stream(stream)))
+    (R, half), (E, N, _), u8, f32 = x_codes.shape, w_codes.shape, torch.uint8, torch.float32
+    K = 2 * half
+    pitch = moe_fp4_scale_stride(fmt, K)
+    py, ldy = _rows(y, "y", torch.bfloat16, (R, N))
+    _check((_lib or load()).moe_grouped_gemm_fp4(
+        fmt, R, N, K, E, _arg(x_codes, "x_codes", u8, (R, half)),
+        _arg(x_scales, "x_scales", u8, (R, pitch)), _arg(w_codes, "w_codes", u8, (E, N, half)),
+        _arg(w_scales, "w_scales", u8, (E, N, pitch)),
+        _arg(offsets, "offsets", torch.int32, (E + 1,)), _arg(x_scale, "x_scale", f32, (1,)),
+        _arg(w_scale, "w_scale", f32, (E,)), _arg(row_scale, "row_scale", f32, (R,)), py, ldy,
+        _status(status), _stream(stream)))
 
 
 def moe_workspace_size_fp4(cfg: MoeConfig, fmt: int) -> int:
@@ -907,7 +903,7 @@ class MoeLayer:
             self._init_ws(cfg, dev)
         self.fp4_scales = tuple(fp4_scales)
         for name, t in zip(("x_scale", "h_scale"), self.fp4_scales):
-            _expect(t, name, torch.float32, (1,))
+            _arg(t, name, torch.float32, (1,))
 
         def p(t):
             return None if t is None else t.data_ptr()
