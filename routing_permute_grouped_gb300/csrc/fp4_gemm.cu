@@ -85,7 +85,8 @@ struct ScaleBars {
 template <bool NV>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_ragged_product_fp4(const __grid_constant__ CUtensorMap tW, const __grid_constant__ RowMaps tX,
-                         const uint8_t* w_scales, const uint8_t* x_scales, const int pitch, const RaggedArgs args) {
+                         const __grid_constant__ CUtensorMap tY, const uint8_t* w_scales, const uint8_t* x_scales,
+                         const int pitch, const RaggedArgs args) {
     using C = Cfg<NV>;
     constexpr int S = C::stages;
     constexpr int kGroup = NV ? 256 : 512;  // elements under 16 scale bytes
@@ -357,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------ epilogue
         const float gx = args.x_scale ? ld_dep(args.x_scale) : 1.0f;
         if (!product_epilogue<__nv_bfloat16, C::TN>(
-                args, tiles, bars, panels, total, first, stride, tmem_base, warp - kEpi0, lane, rank,
+                args, tY, tiles, bars, panels, total, first, stride, tmem_base, warp - kEpi0, lane, rank,
                 sOut + (warp - kEpi0) * 2048, gx,
                 [&](int e) { return args.w_scale ? ld_dep(args.w_scale + e) : 1.0f; }))
             timed_out = true;
@@ -373,15 +374,16 @@ cudaError_t launch_fp4(const RaggedArgs& a, const void* xq, const uint8_t* xs, c
     using C = Cfg<NV>;
     static bool ready[kMaxDevices] = {};
     const uint64_t N = a.N, KB = a.K / 2, R = a.R, E = a.E;  // KB bytes of codes per row
-    CUtensorMap tW;
+    CUtensorMap tW, tY;
     RowMaps tX;
     const uint64_t wd[3] = {KB, N, E}, wst[2] = {KB, N * KB};
     const uint32_t wb[3] = {128, 128, 1};
     if (!make_tensor_map(&tW, wq, 3, wd, wst, wb, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
-        !make_row_maps(&tX, xq, R, KB, KB, 128, CU_TENSOR_MAP_DATA_TYPE_UINT8))
+        !make_row_maps(&tX, xq, R, KB, KB, 128, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
+        !make_out_map(&tY, a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16))
         return cudaErrorInvalidValue;
     const int64_t items = (R / C::TN + (R < E ? R : E)) * ((N + 255) / 256);  // at most
-    return launch_pairs(k_ragged_product_fp4<NV>, items, kThreads, C::smem, ready, st, tW, tX, ws, xs, pitch,
+    return launch_pairs(k_ragged_product_fp4<NV>, items, kThreads, C::smem, ready, st, tW, tX, tY, ws, xs, pitch,
                               a);
 }
 

@@ -1485,7 +1485,7 @@ bool make_tensor_map_2d(void* tmap, const void* ptr, int64_t rows, int64_t cols,
 }
 
 bool make_tensor_map(void* tmap, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
-                     const uint32_t* box, int dtype) {
+                     const uint32_t* box, int dtype, int swizzle_bytes) {
     PFN_encodeTiled enc = encode_fn();
     if (!enc || rank < 2 || rank > 5) return false;
     cuuint64_t d[5], st[4];
@@ -1498,8 +1498,9 @@ bool make_tensor_map(void* tmap, const void* ptr, int rank, const uint64_t* dims
     }
     return enc(static_cast<CUtensorMap*>(tmap), static_cast<CUtensorMapDataType>(dtype),
                static_cast<cuuint32_t>(rank), const_cast<void*>(ptr), d, st, b, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // K-major operand [rows, K]: {64, box_rows} boxes.

@@ -214,10 +214,10 @@ bool make_tensor_map_2d(void* tmap, const void* ptr, int64_t rows, int64_t cols,
                         int dtype, int box_cols, int box_rows, int swizzle_bytes);
 
 // Tensor map of any rank from 2 to 5 (dims from the innermost, strides in bytes
-// of every dimension but that one) with the 128-byte swizzle; out-of-range
-// elements read as zero and are not written.
+// of every dimension but that one) with the 128-byte or 64-byte swizzle;
+// out-of-range elements read as zero and are not written.
 bool make_tensor_map(void* tmap, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
-                     const uint32_t* box, int dtype);
+                     const uint32_t* box, int dtype, int swizzle_bytes = 128);
 
 // e4m3 packing: per-output-channel scales of W [batch][rows][cols] (column c
 // = output channel c), written to scale[b * scale_bstride + packed_row(c,

@@ -158,15 +158,15 @@ __device__ __forceinline__ uint32_t pack2(__half, float lo, float hi) {
 // (`rows` of them are stored) times the warp's 32 features n0 .. n0 + 31, one
 // feature per tensor-memory lane.  The accumulator is read in matrix-fragment
 // form (v), packed to 16 bits and stored transposed through stmatrix into 2 KB
-// of shared memory ([token][64 bytes], 16-byte pieces permuted against bank
-// conflicts), from where each lane stores 16 bytes: an instruction writes 64
-// contiguous bytes of eight output rows.  (Exchanging neighbours' halves by
-// shuffles and storing 4 bytes per lane took 2.4 times the instructions and
-// held short sums up.)  gate is the factor of token row + lane.
+// of shared memory, [token][64 bytes] in the 64-byte swizzle, from where TMA
+// stores it and cuts off the features past N.  The chunk that a group's last
+// token cuts is copied by the lanes: the rows after it are another group's.
+// gate is the factor of token row + lane.
 template <typename T>
-__device__ __forceinline__ void store_transposed(const RaggedArgs& a, const uint32_t (&v)[2][16], int row, int rows,
-                                                 int n0, int lane, float gate, uint8_t* stage) {
-    __syncwarp();  // the previous chunk has left the staging buffer
+__device__ __forceinline__ void store_transposed(const RaggedArgs& a, const CUtensorMap& tY, const uint32_t (&v)[2][16],
+                                                 int row, int rows, int n0, int lane, float gate, uint8_t* stage) {
+    if (lane == 0) bulk_wait_read<0>();  // the previous chunk has left the buffer
+    __syncwarp();
     const uint32_t sbase = smem_u32(stage);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {  // 8 tokens
@@ -180,6 +180,15 @@ __device__ __forceinline__ void store_transposed(const RaggedArgs& a, const uint
         }
         const int token = 8 * j + (lane & 7), f = lane >> 3;
         stmatrix_x4_trans(sbase + token * 64 + ((f ^ ((token >> 1) & 3)) << 4), p[0], p[1], p[2], p[3]);
+    }
+    if (rows >= 32) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && n0 < a.N) {
+            tma_store_2d(&tY, stage, n0, row);
+            bulk_commit();
+        }
+        return;
     }
     __syncwarp();
     const int f = lane & 3;
@@ -307,7 +316,8 @@ __device__ __forceinline__ void pair_end(uint32_t tmem_base, int warp) {
 // stored, a chunk is read from tensor memory while the one before it is
 // stored, and the accumulator goes back before the last chunk's stores.
 template <typename T, int TN, int S, typename Scale>
-__device__ __forceinline__ bool product_epilogue(const RaggedArgs& args, const RaggedTiles& tiles, PairBars<S>& bars,
+__device__ __forceinline__ bool product_epilogue(const RaggedArgs& args, const CUtensorMap& tY,
+                                                 const RaggedTiles& tiles, PairBars<S>& bars,
                                                  int panels, int total, int first, int stride, uint32_t tmem_base,
                                                  int ew, int lane, uint32_t rank, uint8_t* stage, float common,
                                                  Scale scale_of) {
@@ -332,7 +342,10 @@ __device__ __forceinline__ bool product_epilogue(const RaggedArgs& args, const R
     fetch(first);
     Acc acc;
     for (int t = first; t < total; t += stride) {
-        if (!warp_wait(bars.tfull + acc.i, acc.ph, abort_flag)) return false;
+        if (!warp_wait(bars.tfull + acc.i, acc.ph, abort_flag)) {
+            if (lane == 0) bulk_wait_all();
+            return false;
+        }
         tc_fence_after();
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc.i * TN);
         uint32_t v[2][2][16];
@@ -361,11 +374,20 @@ __device__ __forceinline__ bool product_epilogue(const RaggedArgs& args, const R
                 if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), 0));
             }
             if (c >= now.rows) break;
-            store_transposed<T>(args, v[i & 1], now.row + c, now.rows - c, n0, lane, g[i], stage);
+            store_transposed<T>(args, tY, v[i & 1], now.row + c, now.rows - c, n0, lane, g[i], stage);
         }
         acc.next();
     }
+    if (lane == 0) bulk_wait_all();
     return true;
+}
+
+// Tensor map of the products' output: boxes of 32 features x 32 tokens.
+inline bool make_out_map(CUtensorMap* m, const RaggedArgs& a, int dtype) {
+    const uint64_t dims[2] = {static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.R)};
+    const uint64_t strides[1] = {static_cast<uint64_t>(a.ldo) * 2};
+    const uint32_t box[2] = {32, 32};
+    return make_tensor_map(m, a.out, 2, dims, strides, box, dtype, 64);
 }
 
 // Launches `kernel` (clusters of two) on as many pairs as the GPU has SMs for,

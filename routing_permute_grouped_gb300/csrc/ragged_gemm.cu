@@ -76,7 +76,7 @@ constexpr int kProdSmem = 1024 + kProdStages * kStage + kEpiStage + 1024 + stati
 template <typename T, bool WT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps, 1)
     k_ragged_product(const __grid_constant__ CUtensorMap tW, const __grid_constant__ RowMaps tX,
-                     const RaggedArgs args) {
+                     const __grid_constant__ CUtensorMap tY, const RaggedArgs args) {
     constexpr int S = kProdStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -201,7 +201,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
         }
     } else {
         // ------------------------------------------------------ epilogue
-        if (!product_epilogue<T, kTN>(args, tiles, bars, panels, total, first, stride, tmem_base, warp - 2, lane, rank,
+        if (!product_epilogue<T, kTN>(args, tY, tiles, bars, panels, total, first, stride, tmem_base, warp - 2, lane, rank,
                                       sOut + (warp - 2) * 2048, 1.0f, [](int) { return 1.0f; }))
             timed_out = true;
         if (timed_out) *abort_flag = 1;
@@ -498,17 +498,17 @@ cudaError_t launch_product(const RaggedArgs& a, const void* x, int64_t ldx, cons
     static_assert(kProdSmem <= 232448, "shared memory budget");
     static bool ready[kMaxDevices] = {};
     const uint64_t N = a.N, K = a.K, R = a.R, E = a.E;
-    CUtensorMap tW;
+    CUtensorMap tW, tY;
     RowMaps tX;
     const uint64_t wd[3] = {WT ? N : K, WT ? K : N, E};
     const uint64_t ws[2] = {wd[0] * 2, N * K * 2};
     const uint32_t wb[3] = {64, WT ? 64u : 128u, 1};
     if (!make_tensor_map(&tW, w, 3, wd, ws, wb, Elem<T>::map) ||
-        !make_row_maps(&tX, x, R, K, static_cast<uint64_t>(ldx) * 2, 64, Elem<T>::map))
+        !make_row_maps(&tX, x, R, K, static_cast<uint64_t>(ldx) * 2, 64, Elem<T>::map) ||
+        !make_out_map(&tY, a, Elem<T>::map))
         return cudaErrorInvalidValue;
     const int64_t items = (R / kTN + (R < E ? R : E)) * ((N + 255) / 256);  // at most
-    return launch_pairs(k_ragged_product<T, WT>, items, 64 + 32 * kEpiWarps, kProdSmem, ready, st, tW, tX,
-                              a);
+    return launch_pairs(k_ragged_product<T, WT>, items, 64 + 32 * kEpiWarps, kProdSmem, ready, st, tW, tX, tY, a);
 }
 
 template <typename T>
