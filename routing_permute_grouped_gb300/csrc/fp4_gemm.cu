@@ -24,7 +24,7 @@
 // cycles even when there is nothing to wait for (445 against 405 us with two).
 //
 // What bounds it (default gate/up product of 8 experts, 32768 rows, 7168 ->
-// 4096, MX: 324 us, 5.9 PFLOP/s): the issue of the MMAs, whose operands and
+// 4096, MX: 320 to 330 us, 6 PFLOP/s): the issue of the MMAs, whose operands and
 // scale addresses make it about 90 cycles each against 112 of execution, with
 // the waits on top.  The loads alone took 252 us.
 // Decode (two rows for each of 256 experts) runs at the weights' bytes over HBM.
@@ -357,7 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else {
         // ------------------------------------------------------ epilogue
         const float gx = args.x_scale ? ld_dep(args.x_scale) : 1.0f;
-        if (!product_epilogue<__nv_bfloat16, C::TN>(
+        if (!product_epilogue<__nv_bfloat16, C::TN, 1>(
                 args, tY, tiles, bars, panels, total, first, stride, tmem_base, warp - kEpi0, lane, rank,
                 sOut + (warp - kEpi0) * 2048, gx,
                 [&](int e) { return args.w_scale ? ld_dep(args.w_scale + e) : 1.0f; }))

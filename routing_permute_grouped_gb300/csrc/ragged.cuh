@@ -216,7 +216,7 @@ constexpr uint32_t kRaggedTimeout = 0x2u;  // MOE_DEVERR_TIMEOUT
 // pair shares; the first 1 KB of shared memory.
 template <int S>
 struct PairBars {
-    uint64_t full[S], empty[S], tail[S], tfull[2], tempty[2], drain;
+    uint64_t full[S], empty[S], tail[S], tfull[2], tempty[2], join_full[kEpiWarps], join_free[kEpiWarps], drain;
     uint32_t tmem, abort;
 };
 
@@ -260,7 +260,7 @@ struct Acc {  // accumulator and its parity
 };
 
 template <int S>
-__device__ __forceinline__ void pair_start(PairBars<S>& b, uint32_t full_count, int warp) {
+__device__ __forceinline__ void pair_start(PairBars<S>& b, uint32_t full_count, int warp, uint32_t joins = 1) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(b.full + i, full_count);
@@ -270,6 +270,10 @@ __device__ __forceinline__ void pair_start(PairBars<S>& b, uint32_t full_count, 
         for (int i = 0; i < 2; ++i) {
             mbar_init(b.tfull + i, 1);
             mbar_init(b.tempty + i, 2 * kEpiWarps);  // every epilogue warp of both CTAs
+        }
+        for (int i = 0; i < kEpiWarps; ++i) {
+            mbar_init(b.join_full + i, joins);  // the cluster's other pairs
+            mbar_init(b.join_free + i, 1);
         }
         mbar_init(&b.drain, 1);
         b.abort = 0;
@@ -318,16 +322,21 @@ __device__ __forceinline__ void pair_end(uint32_t tmem_base, int warp) {
 // line: the next item and its routing weights are fetched while a tile is
 // stored, a chunk is read from tensor memory while the one before it is
 // stored, and the accumulator goes back before the last chunk's stores.
-template <typename T, int TN, int S, typename Scale>
+//
+// With SP > 1 pairs in the cluster, each holds its part of the same sums: the
+// others' warps write theirs (fp32, 4 KB per warp) into the first pair's shared
+// memory (`join`), whose warps add them in the pairs' order and store.
+template <typename T, int TN, int SP, int S, typename Scale>
 __device__ __forceinline__ bool product_epilogue(const RaggedArgs& args, const CUtensorMap& tY,
                                                  const RaggedTiles& tiles, PairBars<S>& bars,
                                                  int panels, int total, int first, int stride, uint32_t tmem_base,
                                                  int ew, int lane, uint32_t rank, uint8_t* stage, float common,
-                                                 Scale scale_of) {
+                                                 Scale scale_of, uint8_t* join = nullptr) {
     constexpr int kChunks = (TN + 32) / 64;
     const int q = (threadIdx.x >> 5) & 3, odd = ew >> 2;
     const volatile uint32_t* abort_flag = &bars.abort;
     RaggedFeed feed;
+    uint32_t join_ph = 0;
     RaggedItem it{};
     float gate[kChunks], scale = 1.0f;
     // item t, its scale and the routing weight of this lane's token of each
@@ -360,7 +369,7 @@ __device__ __forceinline__ bool product_epilogue(const RaggedArgs& args, const C
         float g[kChunks];
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) g[i] = gate[i] * scale * common;
-        const int n0 = now.panel * 256 + static_cast<int>(rank) * 128 + q * 32;
+        const int n0 = now.panel * 256 + static_cast<int>(rank & 1) * 128 + q * 32;
         if (odd * 32 < now.rows) load(0);
         fetch(t + stride);
 #pragma unroll
@@ -374,9 +383,54 @@ __device__ __forceinline__ bool product_epilogue(const RaggedArgs& args, const C
                 // this warp stores, so the arrive need not release it
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), 0));
+                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), rank & ~1u));
             }
             if (c >= now.rows) break;
+            if constexpr (SP > 1) {
+                static_assert(kChunks == 1, "one chunk per warp and tile");
+                uint32_t* f = &v[0][0][0];
+                const uint32_t pair = rank >> 1;
+                if (pair > 0) {
+                    // the first pair has read this warp's part of the last tile
+                    bool ok = warp_wait(bars.join_free + ew, join_ph ^ 1u, abort_flag);
+                    join_ph ^= 1u;
+                    if (!ok) return false;
+                    fence_cluster();
+                    const uint32_t dst =
+                        mapa_shared(smem_u32(join + ((pair - 1) * kEpiWarps + ew) * 4096), rank & 1u) + lane * 16;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        st_cluster_v4(dst + k * 512, __uint_as_float(f[4 * k]), __uint_as_float(f[4 * k + 1]),
+                                      __uint_as_float(f[4 * k + 2]), __uint_as_float(f[4 * k + 3]));
+                    fence_cluster();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(bars.join_full + ew), rank & 1u));
+                    break;
+                }
+                bool ok = warp_wait(bars.join_full + ew, join_ph, abort_flag);
+                join_ph ^= 1u;
+                if (!ok) {
+                    if (lane == 0) bulk_wait_all();
+                    return false;
+                }
+                fence_cluster();
+#pragma unroll
+                for (int o = 0; o < SP - 1; ++o) {
+                    const float4* src = reinterpret_cast<const float4*>(join + (o * kEpiWarps + ew) * 4096) + lane;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float4 w = src[k * 32];
+                        f[4 * k] = __float_as_uint(__uint_as_float(f[4 * k]) + w.x);
+                        f[4 * k + 1] = __float_as_uint(__uint_as_float(f[4 * k + 1]) + w.y);
+                        f[4 * k + 2] = __float_as_uint(__uint_as_float(f[4 * k + 2]) + w.z);
+                        f[4 * k + 3] = __float_as_uint(__uint_as_float(f[4 * k + 3]) + w.w);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0)
+                    for (int o = 1; o < SP; ++o)
+                        mbar_arrive_cluster(mapa_shared(smem_u32(bars.join_free + ew), rank + 2 * o));
+            }
             store_transposed<T>(args, tY, v[i & 1], now.row + c, now.rows - c, n0, lane, g[i], stage);
         }
         acc.next();
@@ -393,9 +447,9 @@ inline bool make_out_map(CUtensorMap* m, const RaggedArgs& a, int dtype) {
     return make_tensor_map(m, a.out, 2, dims, strides, box, dtype, 64);
 }
 
-// Launches `kernel` (clusters of two) on as many pairs as the GPU has SMs for,
-// but no more than there are items.
-template <typename... KArgs, typename... Args>
+// Launches `kernel` (clusters of SP pairs) on as many clusters as the GPU has
+// SMs for, but no more than there are items.
+template <int SP = 1, typename... KArgs, typename... Args>
 cudaError_t launch_pairs(void (*kernel)(KArgs...), int64_t items, int threads, int smem, bool (&ready)[kMaxDevices],
                          cudaStream_t stream, Args&&... args) {
     int dev = 0;
@@ -406,8 +460,8 @@ cudaError_t launch_pairs(void (*kernel)(KArgs...), int64_t items, int threads, i
         if (e != cudaSuccess) return e;
         ready[dev] = true;
     }
-    const int64_t pairs = num_sms() / 2;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(2 * (items < pairs ? items : pairs))), dim3(threads), smem,
+    const int64_t most = num_sms() / (2 * SP);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(2 * SP * (items < most ? items : most))), dim3(threads), smem,
                       stream, std::forward<Args>(args)...);
 }
 

@@ -49,7 +49,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kTN = 256;                // token rows of a tile, at most
 constexpr int kBK = 64;                 // step of the sum
 constexpr int kOpBytes = 128 * kBK * 2; // one operand of one CTA and stage: 16 KB
 constexpr int kStage = 2 * kOpBytes;
@@ -70,39 +69,55 @@ struct Elem<__half> {  // operand formats 0 in bits [7,10) and [10,13)
 };
 
 // ---------------------------------------------------------------- product --
-constexpr int kProdStages = 6;
-constexpr int kProdSmem = 1024 + kProdStages * kStage + kEpiStage + 1024 + static_cast<int>(sizeof(RaggedTiles));
+// SP > 1 pairs (a cluster of 2 SP CTAs) share an item, each with its part of the
+// sum: for calls with fewer items than pairs and long sums, like one expert's
+// decode batch, whose time is the length of one item's chain of steps.
+template <int SP>
+struct Prod {
+    static constexpr int TN = SP == 1 ? 256 : 64;  // token rows of a tile, at most
+    static constexpr int stages = SP == 1 ? 6 : 5;
+    static constexpr int stage = kOpBytes + TN / 2 * 128;
+    static constexpr int join = (SP - 1) * kEpiWarps * 4096;
+    static constexpr int smem = 1024 + stages * stage + kEpiStage + join + 1024 + static_cast<int>(sizeof(RaggedTiles));
+    static_assert(smem <= 232448, "shared memory budget");
+    static_assert(stage % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+};
 
-template <typename T, bool WT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps, 1)
+template <typename T, bool WT, int SP>
+__global__ void __cluster_dims__(2 * SP, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps, 1)
     k_ragged_product(const __grid_constant__ CUtensorMap tW, const __grid_constant__ RowMaps tX,
                      const __grid_constant__ CUtensorMap tY, const RaggedArgs args) {
-    constexpr int S = kProdStages;
+    using C = Prod<SP>;
+    constexpr int S = C::stages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint8_t* sOut = smem + S * kStage;
-    PairBars<S>& bars = *reinterpret_cast<PairBars<S>*>(sOut + kEpiStage);
+    uint8_t* sOut = smem + S * C::stage;
+    uint8_t* join = sOut + kEpiStage;
+    PairBars<S>& bars = *reinterpret_cast<PairBars<S>*>(join + C::join);
     static_assert(sizeof(PairBars<S>) <= 1024, "barriers");
-    RaggedTiles& tiles = *reinterpret_cast<RaggedTiles*>(sOut + kEpiStage + 1024);
+    RaggedTiles& tiles = *reinterpret_cast<RaggedTiles*>(join + C::join + 1024);
     volatile uint32_t* abort_flag = &bars.abort;
 
     const int warp = uniform(static_cast<int>(threadIdx.x >> 5));
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const bool leader = rank == 0;
+    const uint32_t cta = rank & 1, lead = SP == 1 ? 0 : rank & ~1u;  // of the pair
+    const bool leader = cta == 0;
+    const uint16_t both = static_cast<uint16_t>(0x3u << lead);
     const int panels = (args.N + 255) / 256;
-    const int steps = (args.K + kBK - 1) / kBK;
+    const int all = (args.K + kBK - 1) / kBK, pair = static_cast<int>(rank >> 1);
+    const int k0 = SP == 1 ? 0 : pair * all / SP, k1 = SP == 1 ? all : (pair + 1) * all / SP;  // this pair's steps
     pdl_trigger();
-    pair_start(bars, 1, warp);
-    if (warp == 2) ragged_tiles_build<kTN>(args, tiles, panels, lane);
+    pair_start(bars, 1, warp, SP > 1 ? SP - 1 : 1);
+    if (warp == 2) ragged_tiles_build<C::TN>(args, tiles, panels, lane);
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // the peer's barriers are initialised before any remote use
     tc_fence_after();
     const uint32_t tmem_base = uniform(bars.tmem);
     const int total = uniform(tiles.first[args.E]);
-    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    const int first = blockIdx.x / (2 * SP), stride = gridDim.x / (2 * SP);
     bool timed_out = false;
 
     if (warp == 0) {
@@ -115,15 +130,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
         for (int t = first; t < total && !timed_out; t += stride) {
             const RaggedItem it = feed.next(tiles, args.E, panels, total, t, stride, lane);
             const int half = ((it.rows + 31) & ~31) / 2;  // token rows of each CTA
-            const int xrow = it.row + half * static_cast<int>(rank);
-            const int wrow = it.panel * 256 + 128 * static_cast<int>(rank);
-            for (int k = 0; k < steps; ++k) {
+            const int xrow = it.row + half * static_cast<int>(cta);
+            const int wrow = it.panel * 256 + 128 * static_cast<int>(cta);
+            for (int k = k0; k < k1; ++k) {
                 if (!warp_wait(bars.empty + r.s, r.ph ^ 1u, abort_flag)) {
                     timed_out = true;
                     break;
                 }
-                const uint32_t full = mapa_shared(smem_u32(bars.full + r.s), 0);
-                uint8_t* st = smem + r.s * kStage;
+                const uint32_t full = mapa_shared(smem_u32(bars.full + r.s), lead);
+                uint8_t* st = smem + r.s * C::stage;
                 armed &= ~(1u << r.s);
                 if (leader) mbar_arrive_expect_tx_if(one, bars.full + r.s, 2 * (kOpBytes + half * 128));
                 if constexpr (WT) {
@@ -169,8 +184,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = tmem_base + static_cast<uint32_t>(acc.i * kTN);
-                for (int k = 0; k < steps; ++k) {
+                const uint32_t d = tmem_base + static_cast<uint32_t>(acc.i * C::TN);
+                for (int k = k0; k < k1; ++k) {
                     if (!ready && !warp_wait(bars.full + r.s, r.ph, abort_flag)) {
                         timed_out = true;
                         break;
@@ -178,31 +193,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps,
                     tc_fence_after();
                     const Ring next = r.after<S>();
                     const bool peek = mbar_test_wait(bars.full + next.s, next.ph);
-                    const uint32_t at = static_cast<uint32_t>(r.s) * (kStage >> 4);
+                    const uint32_t at = static_cast<uint32_t>(r.s) * (C::stage >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
                         mma_bf16_pair_if(one, d, wd0 + (at + kk * kWStep), xd0 + (at + kk * 2), idesc,
-                                         (k | kk) != 0 ? 1u : 0u);
-                    mma_commit_pair_if(one, bars.empty + r.s, 0x3);
+                                         ((k - k0) | kk) != 0 ? 1u : 0u);
+                    mma_commit_pair_if(one, bars.empty + r.s, both);
                     ready = __all_sync(0xFFFFFFFFu, peek);
                     issued = true;
                     r = next;
                 }
                 if (timed_out) break;
-                mma_commit_pair_if(one, bars.tfull + acc.i, 0x3);
+                mma_commit_pair_if(one, bars.tfull + acc.i, both);
                 acc.next();
             }
             if ((timed_out || *abort_flag) && issued && one) {
                 *abort_flag = 1;
-                mma_commit_pair(&bars.drain, 0x1);
+                mma_commit_pair(&bars.drain, static_cast<uint16_t>(1u << rank));
                 volatile uint32_t never = 0;
                 (void)mbar_wait(&bars.drain, 0, &never);
             }
         }
     } else {
         // ------------------------------------------------------ epilogue
-        if (!product_epilogue<T, kTN>(args, tY, tiles, bars, panels, total, first, stride, tmem_base, warp - 2, lane, rank,
-                                      sOut + (warp - 2) * 2048, 1.0f, [](int) { return 1.0f; }))
+        if (!product_epilogue<T, C::TN, SP>(args, tY, tiles, bars, panels, total, first, stride, tmem_base, warp - 2, lane,
+                                          rank, sOut + (warp - 2) * 2048, 1.0f, [](int) { return 1.0f; }, join))
             timed_out = true;
         if (timed_out) *abort_flag = 1;
     }
@@ -493,9 +508,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
 }
 
 // --------------------------------------------------------------- launches --
-template <typename T, bool WT>
+// Items of tiles of tn token rows, at most: every group with rows may round up.
+int64_t most_items(const RaggedArgs& a, int tn) {
+    const int64_t groups = a.R < a.E ? a.R : a.E;
+    return (a.R + (tn - 1) * groups) / tn * ((a.N + 255) / 256);
+}
+
+template <typename T, bool WT, int SP>
 cudaError_t launch_product(const RaggedArgs& a, const void* x, int64_t ldx, const void* w, cudaStream_t st) {
-    static_assert(kProdSmem <= 232448, "shared memory budget");
+    using C = Prod<SP>;
     static bool ready[kMaxDevices] = {};
     const uint64_t N = a.N, K = a.K, R = a.R, E = a.E;
     CUtensorMap tW, tY;
@@ -507,13 +528,57 @@ cudaError_t launch_product(const RaggedArgs& a, const void* x, int64_t ldx, cons
         !make_row_maps(&tX, x, R, K, static_cast<uint64_t>(ldx) * 2, 64, Elem<T>::map) ||
         !make_out_map(&tY, a, Elem<T>::map))
         return cudaErrorInvalidValue;
-    const int64_t items = (R / kTN + (R < E ? R : E)) * ((N + 255) / 256);  // at most
-    return launch_pairs(k_ragged_product<T, WT>, items, 64 + 32 * kEpiWarps, kProdSmem, ready, st, tW, tX, tY, a);
+    const int64_t items = most_items(a, C::TN);
+    return launch_pairs<SP>(k_ragged_product<T, WT, SP>, items, 64 + 32 * kEpiWarps, C::smem, ready, st, tW, tX, tY, a);
 }
 
-template <typename T>
-cudaError_t product(const RaggedArgs& a, const void* x, int64_t ldx, const void* w, bool transposed, cudaStream_t st) {
-    return transposed ? launch_product<T, true>(a, x, ldx, w, st) : launch_product<T, false>(a, x, ldx, w, st);
+// Clusters of SP pairs of this kernel that the GPU holds at once (a cluster stays
+// inside one graphics processing cluster, so fewer than its SMs give); 0 if the
+// query fails.
+template <typename T, bool WT, int SP>
+int64_t resident_clusters() {
+    static int found[kMaxDevices] = {};  // + 1
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= kMaxDevices) return 0;
+    if (!found[dev]) {
+        auto kernel = k_ragged_product<T, WT, SP>;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2 * SP;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * SP);
+        cfg.blockDim = dim3(64 + 32 * kEpiWarps);
+        cfg.dynamicSmemBytes = Prod<SP>::smem;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Prod<SP>::smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 0) {
+            (void)cudaGetLastError();
+            n = 0;
+        }
+        found[dev] = n + 1;
+    }
+    return found[dev] - 1;
+}
+
+// Few items and a long sum: the sum is split over the pairs of a cluster, four
+// or two, as many as let every item run at once.  One expert, 16 rows, 7168 ->
+// 2048: 13.7 us with four pairs, 24.8 without; 200 rows: 18.6 against 31.4 with
+// two; 64 rows, 7168 -> 4096: 20.3 against 26.1 with two, 30.9 with four, of
+// which not all 16 clusters fit; 64 rows, 2048 -> 7168: 12.0 against 11.1 with
+// two, so two pairs want the longer sum.
+template <typename T, bool WT>
+cudaError_t product(const RaggedArgs& a, const void* x, int64_t ldx, const void* w, cudaStream_t st) {
+    const int64_t items = most_items(a, Prod<2>::TN);
+    if (a.K >= 16 * kBK && items <= num_sms() / 4) {
+        if (items <= resident_clusters<T, WT, 4>()) return launch_product<T, WT, 4>(a, x, ldx, w, st);
+        if (a.K >= 50 * kBK && items <= resident_clusters<T, WT, 2>())
+            return launch_product<T, WT, 2>(a, x, ldx, w, st);
+    }
+    return launch_product<T, WT, 1>(a, x, ldx, w, st);
 }
 
 template <typename T>
@@ -579,8 +644,11 @@ extern "C" moe_status_t moe_grouped_gemm(int32_t dtype, int64_t R, int32_t N, in
     a.ldo = ldy;
     a.status = status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == MOE_DTYPE_BF16 ? product<__nv_bfloat16>(a, x, ldx, w, w_transposed != 0, st)
-                                                  : product<__half>(a, x, ldx, w, w_transposed != 0, st);
+    cudaError_t e;
+    if (dtype == MOE_DTYPE_BF16)
+        e = w_transposed ? product<__nv_bfloat16, true>(a, x, ldx, w, st) : product<__nv_bfloat16, false>(a, x, ldx, w, st);
+    else
+        e = w_transposed ? product<__half, true>(a, x, ldx, w, st) : product<__half, false>(a, x, ldx, w, st);
     return e == cudaSuccess ? MOE_OK
                             : set_last_error(MOE_ERR_CUDA, "grouped product: %s", cudaGetErrorString(e));
 }

@@ -90,6 +90,34 @@ def test_product(dtype, transposed, case):
     _check(y, *_product_ref(x, w, off, transposed, gate), K, dtype, (sizes, N, K))
 
 
+LONG = [  # few rows and long sums: the sum is split over the pairs of a cluster
+    ([1], 8, 1024), ([64], 512, 7168), ([0, 33, 2], 264, 4096), ([100], 2048, 2056), ([31, 32, 33], 1000, 1032),
+    ([65, 0, 1, 64], 256, 3000), ([7] * 5, 1280, 1544), ([130], 4096, 1096),
+    ([64], 4096, 7168), ([128], 4096, 4104), ([50, 0, 63], 4096, 3592),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_product_long_sums(dtype, transposed, case):
+    sizes, N, K = LONG[case]
+    offsets, off = _offsets(sizes, start=case)
+    R, E = off[-1], len(sizes)
+    x = _rand((R, K), 1 + case, dtype)
+    w = _rand((E, K, N) if transposed else (E, N, K), 100 + case, dtype, K ** -0.5)
+    gate = torch.rand((R,), generator=_gen(7), device="cuda") if case % 2 else None
+    ref, mag = _product_ref(x, w, off, transposed, gate)
+    inside = slice(off[0], off[-1])
+    first = None
+    for _ in range(3):  # and the same bits every time
+        y = torch.full((R, N), float("nan"), dtype=dtype, device="cuda")
+        moe.moe_grouped_gemm(x, w, offsets, y, row_scale=gate, w_transposed=transposed)
+        _check(y[inside], ref[inside], mag[inside], K, dtype, (sizes, N, K))
+        assert first is None or torch.equal(y[inside], first)
+        first = y[inside]
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("case", range(len(SHAPES)))
 def test_wgrad(dtype, case):
