@@ -260,7 +260,8 @@ struct Acc {  // accumulator and its parity
 };
 
 template <int S>
-__device__ __forceinline__ void pair_start(PairBars<S>& b, uint32_t full_count, int warp, uint32_t joins = 1) {
+__device__ __forceinline__ void pair_start(PairBars<S>& b, uint32_t full_count, int warp, uint32_t joins = 1,
+                                           uint32_t frees = 1) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(b.full + i, full_count);
@@ -273,7 +274,7 @@ __device__ __forceinline__ void pair_start(PairBars<S>& b, uint32_t full_count, 
         }
         for (int i = 0; i < kEpiWarps; ++i) {
             mbar_init(b.join_full + i, joins);  // the cluster's other pairs
-            mbar_init(b.join_free + i, 1);
+            mbar_init(b.join_free + i, frees);
         }
         mbar_init(&b.drain, 1);
         b.abort = 0;
@@ -463,6 +464,36 @@ cudaError_t launch_pairs(void (*kernel)(KArgs...), int64_t items, int threads, i
     const int64_t most = num_sms() / (2 * SP);
     return launch_pdl(kernel, dim3(static_cast<unsigned>(2 * SP * (items < most ? items : most))), dim3(threads), smem,
                       stream, std::forward<Args>(args)...);
+}
+
+// Clusters of SP pairs of `kernel` that the GPU holds at once (a cluster stays
+// inside one graphics processing cluster, so fewer than its SMs give); 0 if the
+// query fails.  found: the answers per device, plus one.
+template <int SP, typename K>
+int64_t resident_clusters(K kernel, int threads, int smem, int (&found)[kMaxDevices]) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= kMaxDevices) return 0;
+    if (!found[dev]) {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2 * SP;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * SP);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 0) {
+            (void)cudaGetLastError();
+            n = 0;
+        }
+        found[dev] = n + 1;
+    }
+    return found[dev] - 1;
 }
 
 // ---------------------------------------------------------- 4-bit values --

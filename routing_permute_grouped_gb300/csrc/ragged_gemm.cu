@@ -226,17 +226,19 @@ __global__ void __cluster_dims__(2 * SP, 1, 1) __launch_bounds__(64 + 32 * kEpiW
 }
 
 // -------------------------------------------------------- weight gradient --
-constexpr int kGradStages = 6;
 // One staging buffer (32 rows x 128 bytes) per epilogue warp and a sixth stage:
 // 1.067 against 1.094 ms with two buffers and five stages on the 64-expert
 // layer's gradient, and as fast where the stores bound it (64 experts, 8 rows
 // each: 6.3 TB/s).
+constexpr int kGradStages = 6;
 constexpr int kOutStage = kEpiWarps * 4096;
 constexpr int kGradSmem = 1024 + kGradStages * kStage + kOutStage + 1024;
+static_assert(kGradSmem <= 232448, "shared memory budget");
 
 struct GradTile {
     int e, m, n;     // group, first row and column of the 256 x 256 output tile
-    int row, rows;   // the group's rows
+    int row, rows;   // the group's rows; with several pairs, this pair's part
+    int whole;       // the group's rows
 };
 
 __device__ __forceinline__ GradTile grad_tile(const RaggedArgs& a, int t) {
@@ -253,10 +255,11 @@ __device__ __forceinline__ GradTile grad_tile(const RaggedArgs& a, int t) {
 }
 
 // A warp's tiles, found 32 at a time (see RaggedFeed).
+template <int SP>
 struct GradFeed {
     GradTile mine;
     int k = 32;
-    __device__ __forceinline__ GradTile next(const RaggedArgs& a, int total, int t, int stride, int lane) {
+    __device__ __forceinline__ GradTile next(const RaggedArgs& a, int total, int t, int stride, int lane, int pair) {
         if (k == 32) {
             k = 0;
             const int64_t at = t + static_cast<int64_t>(lane) * stride;
@@ -267,17 +270,94 @@ struct GradFeed {
         g.m = __shfl_sync(0xFFFFFFFFu, mine.m, k);
         g.n = __shfl_sync(0xFFFFFFFFu, mine.n, k);
         g.row = __shfl_sync(0xFFFFFFFFu, mine.row, k);
-        g.rows = __shfl_sync(0xFFFFFFFFu, mine.rows, k);
+        g.rows = g.whole = __shfl_sync(0xFFFFFFFFu, mine.rows, k);
         ++k;
+        if constexpr (SP > 1) {  // whole steps of 64 rows
+            const int steps = (g.whole + kBK - 1) / kBK;
+            const int s0 = pair * steps / SP, s1 = (pair + 1) * steps / SP;
+            g.row += s0 * kBK;
+            g.rows = min(g.whole - s0 * kBK, (s1 - s0) * kBK);
+        }
         return g;
     }
 };
 
-template <typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps, 1)
+// The pairs of a cluster hold sums over parts of a group's rows.  Of the 128
+// columns of an epilogue warp, pair p finishes the p-th 128 / SP: the warps send
+// one another those columns in fp32 and add what they receive to their own, the
+// other pairs' in ascending order.  What is sent lands in the receiver's pipeline
+// stages: a cluster has one tile, so they are free once its sum is complete, which
+// join_free says.  has: this pair had rows, and its accumulator is at taddr.
+// False on a timeout.
+template <int SP>
+__device__ __forceinline__ bool exchange_parts(PairBars<kGradStages>& bars, float (&f)[128 / SP], uint8_t* stages,
+                                               uint32_t taddr, bool has, int ew, int lane, uint32_t rank) {
+    constexpr int kPart = 128 / SP;
+    constexpr int kBytes = kPart * 128;  // of a warp: 32 lanes x kPart fp32
+    static_assert((SP - 1) * kEpiWarps * kBytes <= kGradStages * kStage, "the parts fit the stages");
+    const volatile uint32_t* abort_flag = &bars.abort;
+    const int pair = static_cast<int>(rank >> 1), cta = static_cast<int>(rank & 1);
+    if (lane == 0)
+        for (int o = 0; o < SP; ++o)
+            if (o != pair) mbar_arrive_cluster(mapa_shared(smem_u32(bars.join_free + ew), 2 * o + cta));
+    if (!warp_wait(bars.join_free + ew, 0, abort_flag)) return false;
+    fence_cluster();
+#pragma unroll 1
+    for (int i = 1; i < SP; ++i) {
+        const int to = (pair + i) % SP;  // not all at once to the same pair
+        const int slot = pair < to ? pair : pair - 1;
+        const uint32_t dst = mapa_shared(smem_u32(stages + (slot * kEpiWarps + ew) * kBytes), 2 * to + cta) + lane * 16;
+#pragma unroll
+        for (int c = 0; c < kPart; c += 32) {
+            uint32_t v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0u;
+            if (has) {
+                tmem_ld32(taddr + to * kPart + c, v);
+                tmem_ld_wait();
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                st_cluster_v4(dst + (c / 4 + j) * 512, __uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                              __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+        }
+        fence_cluster();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(bars.join_full + ew), 2 * to + cta));
+    }
+    if (has) {
+#pragma unroll
+        for (int c = 0; c < kPart; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(taddr + pair * kPart + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[c + j] = __uint_as_float(v[j]);
+        }
+    }
+    if (!warp_wait(bars.join_full + ew, 0, abort_flag)) return false;
+    fence_cluster();
+#pragma unroll 1
+    for (int o = 0; o < SP - 1; ++o) {
+        const float4* src = reinterpret_cast<const float4*>(stages + (o * kEpiWarps + ew) * kBytes) + lane;
+#pragma unroll
+        for (int j = 0; j < kPart / 4; ++j) {
+            const float4 w = src[j * 32];
+            f[4 * j] += w.x;
+            f[4 * j + 1] += w.y;
+            f[4 * j + 2] += w.z;
+            f[4 * j + 3] += w.w;
+        }
+    }
+    return true;
+}
+
+template <typename T, int SP>
+__global__ void __cluster_dims__(2 * SP, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps, 1)
     k_ragged_wgrad(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB,
                    const __grid_constant__ CUtensorMap tOut, const RaggedArgs args) {
     constexpr int S = kGradStages;
+    constexpr int kPart = 128 / SP;  // columns of a warp's 128 that this pair finishes
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -288,16 +368,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
     const int warp = uniform(static_cast<int>(threadIdx.x >> 5));
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const bool leader = rank == 0;
+    const uint32_t cta = rank & 1, lead = SP == 1 ? 0 : rank & ~1u;  // of the pair
+    const bool leader = cta == 0;
+    const uint16_t both = static_cast<uint16_t>(0x3u << lead);
+    const int pair = static_cast<int>(rank >> 1);
     pdl_trigger();
-    pair_start(bars, 2, warp);  // a stage is full when both CTAs say so (and its bytes have landed)
+    // a stage is full when both CTAs say so (and its bytes have landed)
+    pair_start(bars, 2, warp, SP > 1 ? SP - 1 : 1, SP > 1 ? SP - 1 : 1);
     tc_fence_before();
     __syncthreads();
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = uniform(bars.tmem);
     const int total = args.E * ((args.N + 255) / 256) * ((args.K + 255) / 256);
-    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    const int first = blockIdx.x / (2 * SP), stride = gridDim.x / (2 * SP);
     bool timed_out = false;
 
     if (warp == 0) {
@@ -305,10 +389,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
         const uint32_t one = elect_one();
         Ring r;
         uint32_t armed = 0, armed_par = 0, tails = 0, tail_par = 0, tail_ph = 0;
-        GradFeed feed;
+        GradFeed<SP> feed;
         for (int t = first; t < total && !timed_out; t += stride) {
-            const GradTile g = feed.next(args, total, t, stride, lane);
-            const int ac = g.m + 128 * static_cast<int>(rank), bc = g.n + 128 * static_cast<int>(rank);
+            const GradTile g = feed.next(args, total, t, stride, lane, pair);
+            const int ac = g.m + 128 * static_cast<int>(cta), bc = g.n + 128 * static_cast<int>(cta);
             for (int k = 0; k < g.rows; k += kBK) {
                 if (!warp_wait(bars.empty + r.s, r.ph ^ 1u, abort_flag)) {
                     timed_out = true;
@@ -330,7 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
                     armed_par = (armed_par & ~bit) | (r.ph << r.s);
                 }
                 const uint32_t bar = tail ? mapa_shared(smem_u32(bars.tail + r.s), rank)
-                                          : mapa_shared(smem_u32(bars.full + r.s), 0);
+                                          : mapa_shared(smem_u32(bars.full + r.s), lead);
                 const int row = g.row + k;
                 if (tail)
                     mbar_arrive_expect_tx_if(one, bars.tail + r.s, kStage);
@@ -364,9 +448,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
             Ring r;
             Acc acc;
             bool issued = false, ready = false;
-            GradFeed feed;
+            GradFeed<SP> feed;
             for (int t = first; t < total && !timed_out; t += stride) {
-                const GradTile g = feed.next(args, total, t, stride, lane);
+                const GradTile g = feed.next(args, total, t, stride, lane, pair);
                 if (g.rows == 0) continue;  // the epilogue writes zeros
                 if (!warp_wait(bars.tempty + acc.i, acc.ph ^ 1u, abort_flag)) {
                     timed_out = true;
@@ -389,18 +473,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
                         if (kk * 16 < rest)
                             mma_bf16_pair_if(one, d, ad0 + (at + kk * (2048 >> 4)), bd0 + (at + kk * (2048 >> 4)),
                                              idesc, (k | kk) != 0 ? 1u : 0u);
-                    mma_commit_pair_if(one, bars.empty + r.s, 0x3);
+                    mma_commit_pair_if(one, bars.empty + r.s, both);
                     ready = __all_sync(0xFFFFFFFFu, peek);
                     issued = true;
                     r = next;
                 }
                 if (timed_out) break;
-                mma_commit_pair_if(one, bars.tfull + acc.i, 0x3);
+                mma_commit_pair_if(one, bars.tfull + acc.i, both);
                 acc.next();
             }
             if ((timed_out || *abort_flag) && issued && one) {
                 *abort_flag = 1;
-                mma_commit_pair(&bars.drain, 0x1);
+                mma_commit_pair(&bars.drain, static_cast<uint16_t>(1u << rank));
                 volatile uint32_t never = 0;
                 (void)mbar_wait(&bars.drain, 0, &never);
             }
@@ -409,9 +493,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
         // ------------------------------------------------- zeroing of tails
         Ring r;
         uint32_t tail_ph = 0;
-        GradFeed feed;
+        GradFeed<SP> feed;
         for (int t = first; t < total && !timed_out; t += stride) {
-            const GradTile g = feed.next(args, total, t, stride, lane);
+            const GradTile g = feed.next(args, total, t, stride, lane, pair);
             const int steps = (g.rows + kBK - 1) / kBK, rest = g.rows % kBK;
             for (int k = 0; k + 1 < steps; ++k) r.next<S>();
             if (steps == 0) continue;
@@ -432,70 +516,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(96 + 32 * kEpiWarps,
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(bars.full + r.s), 0));
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(bars.full + r.s), lead));
             }
             r.next<S>();
         }
     } else {
         // ------------------------------------------------------ epilogue
         // Each warp owns 32 rows of M (its tensor-memory lane quarter) and
-        // half of the tile's columns, and stores them through TMA from boxes
-        // of 32 x 64 staged in shared memory; TMA cuts
-        // off what lies past M or N.
+        // half of the tile's columns (with several pairs, finishes its part of
+        // them), and stores them through TMA from boxes of 32 x 64 (four pairs:
+        // 32 x 32) staged in shared memory; TMA cuts off what lies past M or N.
         const int q = warp & 3, ew = warp - 2;
         const int c0 = (ew >> 2) * 128;
         Acc acc;
         uint8_t* stage = sOut + ew * 4096;
-        GradFeed feed;
+        GradFeed<SP> feed;
         for (int t = first; t < total; t += stride) {
-            const GradTile g = feed.next(args, total, t, stride, lane);
-            const int m = g.m + 128 * static_cast<int>(rank) + q * 32;
+            const GradTile g = feed.next(args, total, t, stride, lane, pair);
+            const int m = g.m + 128 * static_cast<int>(cta) + q * 32;
             const int n = g.n + c0;
-            uint32_t pk[64];
+            uint32_t pk[kPart / 2];
+            uint32_t taddr = 0;
             if (g.rows) {
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars.tfull + acc.i, acc.ph, abort_flag))) {
+                if (!warp_wait(bars.tfull + acc.i, acc.ph, abort_flag)) {
                     timed_out = true;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t taddr =
-                    tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc.i * 256 + c0);
+                taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc.i * 256 + c0);
+            }
+            if constexpr (SP == 1) {
+                if (g.rows) {
 #pragma unroll
-                for (int c = 0; c < 128; c += 64) {
-                    uint32_t v[2][32];
-                    tmem_ld32(taddr + c, v[0]);
-                    tmem_ld32(taddr + c + 32, v[1]);
-                    tmem_ld_wait();
+                    for (int c = 0; c < 128; c += 64) {
+                        uint32_t v[2][32];
+                        tmem_ld32(taddr + c, v[0]);
+                        tmem_ld32(taddr + c + 32, v[1]);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        pk[c / 2 + i] = pack2(T(), __uint_as_float(v[i >> 4][2 * (i & 15)]),
-                                              __uint_as_float(v[i >> 4][2 * (i & 15) + 1]));
+                        for (int i = 0; i < 32; ++i)
+                            pk[c / 2 + i] = pack2(T(), __uint_as_float(v[i >> 4][2 * (i & 15)]),
+                                                  __uint_as_float(v[i >> 4][2 * (i & 15) + 1]));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) pk[i] = 0u;
                 }
+            } else {
+                float f[kPart];
+#pragma unroll
+                for (int i = 0; i < kPart; ++i) f[i] = 0.f;
+                if (g.whole && !exchange_parts<SP>(bars, f, smem, taddr, g.rows != 0, ew, lane, rank)) {
+                    timed_out = true;
+                    break;
+                }
+#pragma unroll
+                for (int i = 0; i < kPart / 2; ++i) pk[i] = pack2(T(), f[2 * i], f[2 * i + 1]);
+            }
+            if (g.rows) {
                 // handed back before the stores; they are not what the MMA
                 // side waits for, so the arrive need not release them
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), 0));
+                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(bars.tempty + acc.i), lead));
                 acc.next();
-            } else {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) pk[i] = 0u;
             }
+            constexpr int kBox = kPart < 64 ? kPart : 64;  // columns per box
 #pragma unroll
-            for (int c = 0; c < 128; c += 64) {
-                if (m >= args.K || n + c >= args.N) continue;
+            for (int c = 0; c < kPart; c += kBox) {
+                const int nc = n + pair * kPart + c;
+                if (m >= args.K || nc >= args.N) continue;
                 if (lane == 0) bulk_wait_read<0>();  // the previous store has read the buffer
                 __syncwarp();
-                uint8_t* sb = stage + lane * 128;
+                uint8_t* sb = stage + lane * kBox * 2;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {  // 16-byte chunks of the 128-byte row
+                for (int j = 0; j < kBox / 8; ++j) {  // 16-byte chunks of a row of 128 or 64 bytes
                     const uint32_t* u = pk + c / 2 + 4 * j;
-                    *reinterpret_cast<uint4*>(sb + ((j ^ (lane & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+                    const int at = kBox == 64 ? j ^ (lane & 7) : j ^ ((lane >> 1) & 3);
+                    *reinterpret_cast<uint4*>(sb + (at << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    tma_store_3d(&tOut, stage, n + c, m, g.e);
+                    tma_store_3d(&tOut, stage, nc, m, g.e);
                     bulk_commit();
                 }
             }
@@ -532,38 +635,6 @@ cudaError_t launch_product(const RaggedArgs& a, const void* x, int64_t ldx, cons
     return launch_pairs<SP>(k_ragged_product<T, WT, SP>, items, 64 + 32 * kEpiWarps, C::smem, ready, st, tW, tX, tY, a);
 }
 
-// Clusters of SP pairs of this kernel that the GPU holds at once (a cluster stays
-// inside one graphics processing cluster, so fewer than its SMs give); 0 if the
-// query fails.
-template <typename T, bool WT, int SP>
-int64_t resident_clusters() {
-    static int found[kMaxDevices] = {};  // + 1
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= kMaxDevices) return 0;
-    if (!found[dev]) {
-        auto kernel = k_ragged_product<T, WT, SP>;
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = 2 * SP;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * SP);
-        cfg.blockDim = dim3(64 + 32 * kEpiWarps);
-        cfg.dynamicSmemBytes = Prod<SP>::smem;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Prod<SP>::smem) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 0) {
-            (void)cudaGetLastError();
-            n = 0;
-        }
-        found[dev] = n + 1;
-    }
-    return found[dev] - 1;
-}
-
 // Few items and a long sum: the sum is split over the pairs of a cluster, four
 // or two, as many as let every item run at once.  One expert, 16 rows, 7168 ->
 // 2048: 13.7 us with four pairs, 24.8 without; 200 rows: 18.6 against 31.4 with
@@ -572,33 +643,57 @@ int64_t resident_clusters() {
 // two, so two pairs want the longer sum.
 template <typename T, bool WT>
 cudaError_t product(const RaggedArgs& a, const void* x, int64_t ldx, const void* w, cudaStream_t st) {
+    static int four[kMaxDevices] = {}, two[kMaxDevices] = {};
+    constexpr int kThreads = 64 + 32 * kEpiWarps;
     const int64_t items = most_items(a, Prod<2>::TN);
     if (a.K >= 16 * kBK && items <= num_sms() / 4) {
-        if (items <= resident_clusters<T, WT, 4>()) return launch_product<T, WT, 4>(a, x, ldx, w, st);
-        if (a.K >= 50 * kBK && items <= resident_clusters<T, WT, 2>())
+        if (items <= resident_clusters<4>(k_ragged_product<T, WT, 4>, kThreads, Prod<4>::smem, four))
+            return launch_product<T, WT, 4>(a, x, ldx, w, st);
+        if (a.K >= 50 * kBK &&
+            items <= resident_clusters<2>(k_ragged_product<T, WT, 2>, kThreads, Prod<2>::smem, two))
             return launch_product<T, WT, 2>(a, x, ldx, w, st);
     }
     return launch_product<T, WT, 1>(a, x, ldx, w, st);
 }
 
-template <typename T>
-cudaError_t launch_wgrad_ragged(const RaggedArgs& a, const void* x, int64_t ldx, const void* y, int64_t ldy,
-                                cudaStream_t st) {
-    static_assert(kGradSmem <= 232448, "shared memory budget");
+template <typename T, int SP>
+cudaError_t launch_wgrad(const RaggedArgs& a, const void* x, int64_t ldx, const void* y, int64_t ldy,
+                         cudaStream_t st) {
     static bool ready[kMaxDevices] = {};
     const uint64_t M = a.K, N = a.N, R = a.R, E = a.E;
     CUtensorMap tA, tB, tOut;
     const uint64_t ad[2] = {M, R}, as[1] = {static_cast<uint64_t>(ldx) * 2};
     const uint64_t bd[2] = {N, R}, bs[1] = {static_cast<uint64_t>(ldy) * 2};
     const uint64_t od[3] = {N, M, E}, os[2] = {N * 2, M * N * 2};
-    const uint32_t box[2] = {64, 64}, obox[3] = {64, 32, 1};
+    const uint32_t box[2] = {64, 64}, obox[3] = {SP == 4 ? 32u : 64u, 32, 1};
     if (!make_tensor_map(&tA, x, 2, ad, as, box, Elem<T>::map) || !make_tensor_map(&tB, y, 2, bd, bs, box, Elem<T>::map) ||
-        !make_tensor_map(&tOut, a.out, 3, od, os, obox, Elem<T>::map))
+        !make_tensor_map(&tOut, a.out, 3, od, os, obox, Elem<T>::map, SP == 4 ? 64 : 128))
         return cudaErrorInvalidValue;
     const int64_t items = static_cast<int64_t>(E) * ((N + 255) / 256) * ((M + 255) / 256);
-    if (items > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_pairs(k_ragged_wgrad<T>, items, 96 + 32 * kEpiWarps, kGradSmem, ready, st, tA, tB, tOut,
-                              a);
+    // split sums: one tile per cluster
+    if (items > (SP > 1 ? num_sms() / (2 * SP) : INT32_MAX)) return cudaErrorInvalidValue;
+    return launch_pairs<SP>(k_ragged_wgrad<T, SP>, items, 96 + 32 * kEpiWarps, kGradSmem, ready, st, tA, tB, tOut, a);
+}
+
+// Few tiles and many rows (a router's or an adapter's gradient, few small
+// experts): the rows are split over the pairs of a cluster, four or two, as many
+// as let every tile run at once.  bf16, one group, without and with: 8192 rows,
+// 2048 x 512: 39.3 and 25.6 us (two pairs); 7168 x 256: 40.3 and 29.1 (two); 4096
+// rows, 512 x 512: 21.9 and 14.0 (four; 16.1 with two); 2048 rows: 13.5 and 11.8;
+// 1024 rows: 9.2 and 10.7.  Eight groups of 2048 rows: 14.6 and 14.8.  So it starts
+// at 2048 rows per group; the average is what the host knows of them.
+template <typename T>
+cudaError_t wgrad(const RaggedArgs& a, const void* x, int64_t ldx, const void* y, int64_t ldy, cudaStream_t st) {
+    static int four[kMaxDevices] = {}, two[kMaxDevices] = {};
+    constexpr int kThreads = 96 + 32 * kEpiWarps;
+    const int64_t items = static_cast<int64_t>(a.E) * ((a.N + 255) / 256) * ((a.K + 255) / 256);
+    if (a.R / a.E >= 32 * kBK && items <= num_sms() / 4) {
+        if (items <= resident_clusters<4>(k_ragged_wgrad<T, 4>, kThreads, kGradSmem, four))
+            return launch_wgrad<T, 4>(a, x, ldx, y, ldy, st);
+        if (items <= resident_clusters<2>(k_ragged_wgrad<T, 2>, kThreads, kGradSmem, two))
+            return launch_wgrad<T, 2>(a, x, ldx, y, ldy, st);
+    }
+    return launch_wgrad<T, 1>(a, x, ldx, y, ldy, st);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -677,8 +772,8 @@ extern "C" moe_status_t moe_grouped_wgrad(int32_t dtype, int64_t R, int32_t M, i
         a.E = E;
         a.out = out;
         a.status = status;
-        e = dtype == MOE_DTYPE_BF16 ? launch_wgrad_ragged<__nv_bfloat16>(a, a_, lda, b, ldb, st)
-                                    : launch_wgrad_ragged<__half>(a, a_, lda, b, ldb, st);
+        e = dtype == MOE_DTYPE_BF16 ? wgrad<__nv_bfloat16>(a, a_, lda, b, ldb, st)
+                                    : wgrad<__half>(a, a_, lda, b, ldb, st);
     }
     return e == cudaSuccess ? MOE_OK
                             : set_last_error(MOE_ERR_CUDA, "grouped weight gradient: %s", cudaGetErrorString(e));

@@ -133,6 +133,36 @@ def test_wgrad(dtype, case):
         _check(out[e], A.T @ B, A.abs().T @ B.abs(), hi - lo, dtype, (sizes, e))
 
 
+MANY = [  # many rows and few outputs: the rows are split over the pairs of a cluster
+    ([1024], 8, 8), ([1025], 264, 72), ([4100, 0], 128, 512), ([0, 0, 4300, 1], 96, 520), ([1087, 1089], 1000, 264),
+    ([2048, 50, 63, 65, 4000, 127, 0, 2000], 256, 256), ([9000], 1032, 1544), ([3001], 2048, 1024),
+    ([2048], 8, 8), ([2049], 264, 72), ([4300, 0, 1, 4400], 96, 520),
+    ([7000, 0, 1, 63, 65, 129, 9100, 200], 256, 256), ([0, 5000, 129], 1000, 776),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_wgrad_many_rows(dtype, case):
+    sizes, M, N = MANY[case]
+    offsets, off = _offsets(sizes, start=3 * case)
+    R, E = off[-1] + case, len(sizes)
+    a, b = _rand((R, M), 3 + case, dtype), _rand((R, N), 200 + case, dtype)
+    for t in (a, b):  # rows of no group
+        t[:off[0]] = float("nan")
+        t[off[-1]:] = float("nan")
+    first = None
+    for _ in range(3):  # and the same bits every time
+        out = torch.full((E, M, N), float("nan"), dtype=dtype, device="cuda")
+        moe.moe_grouped_wgrad(a, b, offsets, out)
+        for e in range(E):
+            lo, hi = off[e], off[e + 1]
+            A, B = a[lo:hi].double(), b[lo:hi].double()
+            _check(out[e], A.T @ B, A.abs().T @ B.abs(), hi - lo, dtype, (sizes, e))
+        assert first is None or torch.equal(out, first)
+        first = out
+
+
 def test_groups_that_start_late_and_rows_outside():
     """Rows before the first and past the last group are neither read into a
     result nor written, whatever they hold."""
