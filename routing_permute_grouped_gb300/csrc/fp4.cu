@@ -14,13 +14,13 @@
 // Dequantising is bound by memory: a thread takes 8 elements (4 bytes of codes,
 // 16 of output), so that every access of a warp is contiguous (6.1 TB/s at the
 // default batch).  Quantising is bound by integer and conversion instructions
-// (8 elements per thread: 100 against 72 us at the default batch), so a thread takes 16, a whole NV block or half an MX one:
-// what is done once per block is then done by one or two threads.  The rows are
-// read with 32-byte loads where they are aligned to 32 bytes, else with two of
-// 16; amax is taken on the 16-bit patterns, two at a time, where NaN and
-// infinity order above every number (they mark the block's scale NaN); bf16 rows
-// are scaled in pairs.  A team of threads takes a row, without divisions by the
-// row length.
+// (8 elements per thread: 100 against 72 us at the default batch), so a thread
+// takes 16, a whole NV block or half an MX one: what is done once per block is
+// then done by one or two threads.  The rows are read with 32-byte loads where
+// they are aligned to 32 bytes, else with two of 16; amax is taken on the 16-bit
+// patterns, two at a time, where NaN and infinity order above every number (they
+// mark the block's scale NaN); bf16 rows are scaled in pairs.  A team of threads
+// takes a row, without divisions by the row length.
 #include <cuda_runtime.h>
 
 #include "../../include/moe.h"

@@ -22,6 +22,10 @@
 // zero is not zero) before the step is handed to the MMAs.  An empty group's
 // tiles are written as zeros.
 //
+// Where a call has fewer tiles than the GPU has pairs and a long sum, two or four
+// pairs of a cluster split the sum (SP) and join their fp32 parts through each
+// other's shared memory, in an order that does not depend on timing.
+//
 // What bounds them: at the default layer's gate/up size (32768 rows, 8 experts,
 // 7168 -> 4096) a launch by itself takes 1.02 ms, 1890 TFLOP/s, with the tensor
 // pipe 93 % busy at 1.63 GHz, the board's power limit; back to back 1.15 to 1.19
