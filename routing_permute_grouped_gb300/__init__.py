@@ -706,9 +706,20 @@ def moe_layer_fwd_fp4_prerouted(cfg, weights: MoeWeightsFp4, x, topk_idx, topk_w
         _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
 
 
+def _row_major(t: torch.Tensor) -> torch.Tensor:
+    """t [rows, columns], or a copy where the products cannot read its layout: torch hands over
+    expanded (a sum's gradient), transposed and oddly placed tensors (a part of a concatenated
+    vector, which .contiguous() would leave where it is)."""
+    rows, cols = t.stride()
+    if cols == 1 and (rows >= t.shape[1] and rows % 8 == 0 or t.shape[0] <= 1) and t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 class _GroupedLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, offsets):
+        x = _row_major(x)
         ctx.save_for_backward(x, w, offsets)
         y = x.new_zeros((x.shape[0], w.shape[1]))  # rows outside every group stay zero
         moe_grouped_gemm(x, w, offsets, y)
@@ -717,7 +728,7 @@ class _GroupedLinear(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
-        dy = dy if dy.stride(-1) == 1 and dy.stride(0) % 8 == 0 and dy.data_ptr() % 16 == 0 else dy.contiguous()
+        dy = _row_major(dy)
         dx = dw = None
         if ctx.needs_input_grad[0]:
             dx = x.new_zeros(x.shape)
@@ -731,7 +742,8 @@ class _GroupedLinear(torch.autograd.Function):
 def grouped_linear(x, w, offsets):
     """y[r] = x[r] W[e]^T for the rows of every group e, differentiable in x and w: x [R, K],
     w [E, N, K] (bf16 or fp16), offsets int32 [E + 1].  Rows outside every group are zero, in y
-    and in the gradient of x."""
+    and in the gradient of x.  x and the gradient of y may have any strides; those that the
+    products cannot read are copied."""
     return _GroupedLinear.apply(x, w, offsets)
 
 
