@@ -20,6 +20,7 @@ import os
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import build as _build
 
@@ -726,6 +727,7 @@ class _GroupedLinear(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
         dy = _row_major(dy)
@@ -743,7 +745,7 @@ def grouped_linear(x, w, offsets):
     """y[r] = x[r] W[e]^T for the rows of every group e, differentiable in x and w: x [R, K],
     w [E, N, K] (bf16 or fp16), offsets int32 [E + 1].  Rows outside every group are zero, in y
     and in the gradient of x.  x and the gradient of y may have any strides; those that the
-    products cannot read are copied."""
+    products cannot read are copied.  A second derivative raises an error."""
     return _GroupedLinear.apply(x, w, offsets)
 
 

@@ -86,3 +86,20 @@ def test_any_input_layout(plain_calls):
         (dx,) = torch.autograd.grad(y.square().sum(), x)
         (want,) = torch.autograd.grad(_reference(x, w).square().sum(), x)
         assert torch.allclose(dx, want, rtol=1e-5, atol=1e-4)
+
+
+def test_second_derivatives_are_refused(plain_calls):
+    """The gradients carry no graph of their own: asking for one raises instead of
+    leaving a gradient penalty's term out."""
+    g = torch.Generator().manual_seed(3)
+    offsets = torch.tensor(OFF, dtype=torch.int32)
+    x = torch.randn((21, 16), generator=g).requires_grad_()
+    w = torch.randn((3, 24, 16), generator=g).requires_grad_()
+    y = moe.grouped_linear(x, w, offsets)
+    dx, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (y.sum() + dx.square().sum()).backward()
+    # first derivatives in the same graph are what they were
+    dx, dw = torch.autograd.grad(moe.grouped_linear(x, w, offsets).square().sum(), (x, w))
+    want = torch.autograd.grad(_reference(x, w).square().sum(), (x, w))
+    assert torch.allclose(dx, want[0], rtol=1e-5, atol=1e-4) and torch.allclose(dw, want[1], rtol=1e-5, atol=1e-4)
