@@ -228,38 +228,53 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 # The arguments of the grouped products and of the 4-bit rows.  The C side sees
-# only addresses, so type, shape and layout are checked here; short calls are
-# bound by the host, so each tensor is looked at once, and addresses go as plain
-# integers (a ctypes object per pointer costs about as much as the checks).
-def _bad(t, name, dtype, shape):
-    raise ValueError(f"{name}: expected a CUDA tensor, {dtype} {tuple(shape)}, with contiguous "
+# only addresses, so device, type, shape and layout are checked here; short calls
+# are bound by the host, so each tensor is looked at once, and addresses go as
+# plain integers (a ctypes object per pointer costs about as much as the checks).
+def _device(t: torch.Tensor) -> int:
+    """The index of a call's device: that of its first tensor, which has to be the
+    current one, where the kernels are launched."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("expected a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _bad(t, name, dtype, shape, dev):
+    raise ValueError(f"{name}: expected a tensor on cuda:{dev}, {dtype} {tuple(shape)}, with contiguous "
                      f"{'rows' if t.dim() == 2 else 'elements'}; got {t.dtype} {tuple(t.shape)}, "
                      f"strides {t.stride()}, on {t.device}")
 
 
-def _arg(t: Optional[torch.Tensor], name: str, dtype, shape):
-    """Address of a contiguous CUDA tensor of this type and shape, None for None."""
+def _arg(t: Optional[torch.Tensor], name: str, dtype, shape, dev: int):
+    """Address of a contiguous tensor of this type and shape on GPU dev, None for None."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        _bad(t, name, dtype, shape)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _bad(t, name, dtype, shape, dev)
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, name: str, dtype, shape):
-    """Address and row stride of a [rows, columns] CUDA tensor whose rows are
+def _rows(t: torch.Tensor, name: str, dtype, shape, dev: int):
+    """Address and row stride of a [rows, columns] tensor on GPU dev whose rows are
     contiguous (the stride between rows is free)."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
-        _bad(t, name, dtype, shape)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _bad(t, name, dtype, shape, dev)
     s0, s1 = t.stride()
     if s1 != 1 and shape[1] > 1:
-        _bad(t, name, dtype, shape)
+        _bad(t, name, dtype, shape, dev)
     return t.data_ptr(), s0 if shape[0] > 1 else shape[1]
 
 
-def _status(t: Optional[torch.Tensor]):
-    """Address of the device error word: the first 4 bytes of any CUDA tensor."""
-    return None if t is None else _ptr(t).value
+def _status(t: Optional[torch.Tensor], dev: int):
+    """Address of the device error word: the first 4 bytes of any tensor on GPU dev."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"status: expected a tensor on cuda:{dev}")
+    return _ptr(t).value
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -275,10 +290,11 @@ def _dtype(t: torch.Tensor) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> int:
+def _stream(stream, dev: Optional[int] = None) -> int:
+    """The raw handle of a stream; None is the current one (of GPU dev, if the caller knows it)."""
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if dev is None else dev)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -615,25 +631,27 @@ def moe_grouped_gemm(x, w, offsets, y, row_scale=None, w_transposed: bool = Fals
     of every group; x [R, K], w [E, N, K] (or [E, K, N], ``w_transposed``: x[r] W[e]),
     y [R, N], all bf16 or all fp16, rows of x and y at any stride.  ``offsets`` int32
     [E + 1], or None with E = 1: one group of all rows."""
-    dtype, (R, K), (E, a, b) = x.dtype, x.shape, w.shape
+    dev, dtype, (R, K), (E, a, b) = _device(x), x.dtype, x.shape, w.shape
     N = b if w_transposed else a
-    px, ldx = _rows(x, "x", dtype, (R, K))
-    py, ldy = _rows(y, "y", dtype, (R, N))
+    px, ldx = _rows(x, "x", dtype, (R, K), dev)
+    py, ldy = _rows(y, "y", dtype, (R, N), dev)
     _check((_lib or load()).moe_grouped_gemm(
-        _dtype(x), R, N, K, E, px, ldx, _arg(w, "w", dtype, (E, K, N) if w_transposed else (E, N, K)),
-        int(w_transposed), _arg(offsets, "offsets", torch.int32, (E + 1,)),
-        _arg(row_scale, "row_scale", torch.float32, (R,)), py, ldy, _status(status), _stream(stream)))
+        _dtype(x), R, N, K, E, px, ldx,
+        _arg(w, "w", dtype, (E, K, N) if w_transposed else (E, N, K), dev),
+        int(w_transposed), _arg(offsets, "offsets", torch.int32, (E + 1,), dev),
+        _arg(row_scale, "row_scale", torch.float32, (R,), dev), py, ldy,
+        _status(status, dev), _stream(stream, dev)))
 
 
 def moe_grouped_wgrad(a, b, offsets, out, status=None, stream=None) -> None:
     """out[e] = sum over group e's rows of a[r]^T b[r]: a [R, M], b [R, N],
     out [E, M, N], all bf16 or all fp16."""
-    dtype, (R, M), N, E = a.dtype, a.shape, b.shape[1], out.shape[0]
-    pa, lda = _rows(a, "a", dtype, (R, M))
-    pb, ldb = _rows(b, "b", dtype, (R, N))
+    dev, dtype, (R, M), N, E = _device(a), a.dtype, a.shape, b.shape[1], out.shape[0]
+    pa, lda = _rows(a, "a", dtype, (R, M), dev)
+    pb, ldb = _rows(b, "b", dtype, (R, N), dev)
     _check((_lib or load()).moe_grouped_wgrad(
-        _dtype(a), R, M, N, E, pa, lda, pb, ldb, _arg(offsets, "offsets", torch.int32, (E + 1,)),
-        _arg(out, "out", dtype, (E, M, N)), _status(status), _stream(stream)))
+        _dtype(a), R, M, N, E, pa, lda, pb, ldb, _arg(offsets, "offsets", torch.int32, (E + 1,), dev),
+        _arg(out, "out", dtype, (E, M, N), dev), _status(status, dev), _stream(stream, dev)))
 
 
 def moe_fp4_scale_stride(fmt: int, K: int) -> int:
@@ -648,41 +666,41 @@ def moe_quantize_fp4(fmt: int, x, codes, scales, tensor_scale=None, src=None, sr
     """codes [rows, K / 2] and scales [rows, moe_fp4_scale_stride(fmt, K)] (uint8) of the
     rows of x (bf16 or fp16), or of x[src // src_div]; with ``swiglu`` of silu(gate) * up
     of x's 2 K columns, interleaved per 128."""
-    rows, half = codes.shape
+    dev, (rows, half) = _device(x), codes.shape
     K, x_rows, u8 = 2 * half, x.shape[0], torch.uint8
-    px, ldx = _rows(x, "x", x.dtype, (x_rows, 2 * K if swiglu else K))
+    px, ldx = _rows(x, "x", x.dtype, (x_rows, 2 * K if swiglu else K), dev)
     _check((_lib or load()).moe_quantize_fp4(
-        fmt, _dtype(x), rows, K, px, x_rows, ldx, _arg(src, "src", torch.int32, (rows,)), src_div,
-        int(swiglu), _arg(tensor_scale, "tensor_scale", torch.float32, (1,)),
-        _arg(codes, "codes", u8, (rows, half)),
-        _arg(scales, "scales", u8, (rows, moe_fp4_scale_stride(fmt, K))), _stream(stream)))
+        fmt, _dtype(x), rows, K, px, x_rows, ldx, _arg(src, "src", torch.int32, (rows,), dev), src_div,
+        int(swiglu), _arg(tensor_scale, "tensor_scale", torch.float32, (1,), dev),
+        _arg(codes, "codes", u8, (rows, half), dev),
+        _arg(scales, "scales", u8, (rows, moe_fp4_scale_stride(fmt, K)), dev), _stream(stream, dev)))
 
 
 def moe_dequantize_fp4(fmt: int, codes, scales, out, tensor_scale=None, stream=None) -> None:
     """out [rows, K] (bf16 or fp16) = the values of 4-bit rows."""
-    rows, K = out.shape
-    po, ldo = _rows(out, "out", out.dtype, (rows, K))
+    dev, (rows, K) = _device(out), out.shape
+    po, ldo = _rows(out, "out", out.dtype, (rows, K), dev)
     _check((_lib or load()).moe_dequantize_fp4(
-        fmt, _dtype(out), rows, K, _arg(codes, "codes", torch.uint8, (rows, K // 2)),
-        _arg(scales, "scales", torch.uint8, (rows, moe_fp4_scale_stride(fmt, K))),
-        _arg(tensor_scale, "tensor_scale", torch.float32, (1,)), po, ldo, _stream(stream)))
+        fmt, _dtype(out), rows, K, _arg(codes, "codes", torch.uint8, (rows, K // 2), dev),
+        _arg(scales, "scales", torch.uint8, (rows, moe_fp4_scale_stride(fmt, K)), dev),
+        _arg(tensor_scale, "tensor_scale", torch.float32, (1,), dev), po, ldo, _stream(stream, dev)))
 
 
 def moe_grouped_gemm_fp4(fmt: int, x_codes, x_scales, w_codes, w_scales, offsets, y, x_scale=None,
                          w_scale=None, row_scale=None, status=None, stream=None) -> None:
     """y[r] = row_scale[r] * x_scale * w_scale[e] * x[r] W[e]^T on 4-bit rows x [R, K] and
     weights [E, N, K] (codes [.., K / 2] and scales [.., stride], uint8); y bf16 [R, N]."""
-    (R, half), (E, N, _), u8, f32 = x_codes.shape, w_codes.shape, torch.uint8, torch.float32
-    K = 2 * half
+    dev, (R, half), (E, N, _) = _device(x_codes), x_codes.shape, w_codes.shape
+    K, u8, f32 = 2 * half, torch.uint8, torch.float32
     pitch = moe_fp4_scale_stride(fmt, K)
-    py, ldy = _rows(y, "y", torch.bfloat16, (R, N))
+    py, ldy = _rows(y, "y", torch.bfloat16, (R, N), dev)
     _check((_lib or load()).moe_grouped_gemm_fp4(
-        fmt, R, N, K, E, _arg(x_codes, "x_codes", u8, (R, half)),
-        _arg(x_scales, "x_scales", u8, (R, pitch)), _arg(w_codes, "w_codes", u8, (E, N, half)),
-        _arg(w_scales, "w_scales", u8, (E, N, pitch)),
-        _arg(offsets, "offsets", torch.int32, (E + 1,)), _arg(x_scale, "x_scale", f32, (1,)),
-        _arg(w_scale, "w_scale", f32, (E,)), _arg(row_scale, "row_scale", f32, (R,)), py, ldy,
-        _status(status), _stream(stream)))
+        fmt, R, N, K, E, _arg(x_codes, "x_codes", u8, (R, half), dev),
+        _arg(x_scales, "x_scales", u8, (R, pitch), dev), _arg(w_codes, "w_codes", u8, (E, N, half), dev),
+        _arg(w_scales, "w_scales", u8, (E, N, pitch), dev),
+        _arg(offsets, "offsets", torch.int32, (E + 1,), dev), _arg(x_scale, "x_scale", f32, (1,), dev),
+        _arg(w_scale, "w_scale", f32, (E,), dev), _arg(row_scale, "row_scale", f32, (R,), dev), py, ldy,
+        _status(status, dev), _stream(stream, dev)))
 
 
 def moe_workspace_size_fp4(cfg: MoeConfig, fmt: int) -> int:
@@ -917,7 +935,7 @@ class MoeLayer:
             self._init_ws(cfg, dev)
         self.fp4_scales = tuple(fp4_scales)
         for name, t in zip(("x_scale", "h_scale"), self.fp4_scales):
-            _arg(t, name, torch.float32, (1,))
+            _arg(t, name, torch.float32, (1,), dev.index)
 
         def p(t):
             return None if t is None else t.data_ptr()
