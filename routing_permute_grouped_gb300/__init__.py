@@ -268,6 +268,16 @@ def _rows(t: torch.Tensor, name: str, dtype, shape, dev: int):
     return t.data_ptr(), s0 if shape[0] > 1 else shape[1]
 
 
+def _whole(t: Optional[torch.Tensor], name: str, dtype, count: int, dev: int):
+    """Address of a contiguous tensor of this type on GPU dev with at least count
+    elements, in whatever shape; None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or t.numel() < count:
+        _bad(t, name, dtype, (count,), dev)
+    return t.data_ptr()
+
+
 def _status(t: Optional[torch.Tensor], dev: int):
     """Address of the device error word: the first 4 bytes of any tensor on GPU dev."""
     if t is None:
@@ -713,16 +723,28 @@ def moe_workspace_layout_fp4(cfg: MoeConfig, fmt: int) -> dict:
     return {n: int(getattr(L, n)) for n in _LAYOUT_FP4_FIELDS}
 
 
+def _layer_fp4(cfg, x, out, ws):
+    """Device and addresses of the 4-bit layer's x, out and workspace."""
+    dev, n = _device(ws), cfg.T * cfg.d
+    return dev, (_whole(x, "x", torch.bfloat16, n, dev), _whole(out, "out", torch.bfloat16, n, dev),
+                 _whole(ws, "ws", ws.dtype, 0, dev), ws.numel() * ws.element_size())
+
+
 def moe_layer_fwd_fp4(cfg, weights: MoeWeightsFp4, x, out, ws, stream=None) -> None:
-    _check(load().moe_layer_fwd_fp4(ctypes.byref(cfg), ctypes.byref(weights), _ptr(x), _ptr(out),
-                                    _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    """x, out bf16, T * d elements of contiguous tensors of any shape."""
+    dev, (px, pout, pws, ws_bytes) = _layer_fp4(cfg, x, out, ws)
+    _check((_lib or load()).moe_layer_fwd_fp4(ctypes.byref(cfg), ctypes.byref(weights), px, pout, pws, ws_bytes,
+                                              _stream(stream, dev)))
 
 
 def moe_layer_fwd_fp4_prerouted(cfg, weights: MoeWeightsFp4, x, topk_idx, topk_w, out, ws,
                                 stream=None) -> None:
-    _check(load().moe_layer_fwd_fp4_prerouted(
-        ctypes.byref(cfg), ctypes.byref(weights), _ptr(x), _ptr(topk_idx), _ptr(topk_w), _ptr(out),
-        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    """x and out as for moe_layer_fwd_fp4; topk_idx int32 and topk_w fp32, T * k elements."""
+    dev, (px, pout, pws, ws_bytes) = _layer_fp4(cfg, x, out, ws)
+    A = cfg.T * cfg.k
+    _check((_lib or load()).moe_layer_fwd_fp4_prerouted(
+        ctypes.byref(cfg), ctypes.byref(weights), px, _whole(topk_idx, "topk_idx", torch.int32, A, dev),
+        _whole(topk_w, "topk_w", torch.float32, A, dev), pout, pws, ws_bytes, _stream(stream, dev)))
 
 
 def _row_major(t: torch.Tensor) -> torch.Tensor:

@@ -107,3 +107,39 @@ def test_tensors_of_another_device_than_the_current_are_refused(lib, name):
     with pytest.raises(ValueError):
         _call(name, lib, **{n: Fake(*v, device=1) for n, v in CALLS[name][0].items()})
     assert not lib.calls
+
+
+# the 4-bit layer of T = 6 tokens to 2 experts each, d = 128
+LAYER = dict(x=(BF, 6, 128), out=(BF, 6, 128), ws=(U8, 4096), topk_idx=(I32, 6, 2), topk_w=(F32, 6, 2))
+
+
+def _layer(prerouted, **other):
+    cfg = moe.config_of(T=6, d=128, d_e=128, E=4, k=2)
+    args = {n: Fake(*v) for n, v in LAYER.items() if prerouted or not n.startswith("topk")}
+    args.update(other)
+    call = moe.moe_layer_fwd_fp4_prerouted if prerouted else moe.moe_layer_fwd_fp4
+    call(cfg, moe.MoeWeightsFp4(), **args)
+
+
+@pytest.mark.parametrize("prerouted", [False, True])
+def test_layer_fp4_takes_whole_tensors_of_any_shape(lib, prerouted):
+    _layer(prerouted)
+    _layer(prerouted, x=Fake(BF, 2, 3, 128), out=Fake(BF, 7, 128))  # larger buffers too
+    assert len(lib.calls) == 2
+
+
+@pytest.mark.parametrize("name,other", [
+    (n, dict(device=1)) for n in LAYER] + [(n, dict(device=-1)) for n in LAYER] + [
+    ("x", dict(shape=(5, 128))), ("out", dict(shape=(6, 120))), ("topk_idx", dict(shape=(6, 1))),
+    ("topk_w", dict(shape=(11,))), ("x", dict(dtype=torch.float16)), ("out", dict(dtype=F32)),
+    ("topk_idx", dict(dtype=torch.int64)), ("topk_w", dict(dtype=BF)), ("x", dict(strides=(256, 1))),
+    ("topk_idx", dict(strides=(1, 6)))])
+def test_layer_fp4_refuses_other_tensors(lib, name, other):
+    dtype, *shape = LAYER[name]
+    bad = Fake(other.pop("dtype", dtype), *other.pop("shape", shape), **other)
+    with pytest.raises(ValueError):
+        _layer(True, **{name: bad})
+    if not name.startswith("topk"):
+        with pytest.raises(ValueError):
+            _layer(False, **{name: bad})
+    assert not lib.calls
