@@ -279,12 +279,15 @@ def _whole(t: Optional[torch.Tensor], name: str, dtype, count: int, dev: int):
 
 
 def _status(t: Optional[torch.Tensor], dev: int):
-    """Address of the device error word: the first 4 bytes of any tensor on GPU dev."""
+    """Address of the device error word: the first 4 bytes of a contiguous tensor on GPU dev,
+    which the kernels update as one 32-bit word."""
     if t is None:
         return None
-    if t.get_device() != dev:
-        raise ValueError(f"status: expected a tensor on cuda:{dev}")
-    return _ptr(t).value
+    at = t.data_ptr()
+    if t.get_device() != dev or not t.is_contiguous() or at % 4 or t.numel() * t.element_size() < 4:
+        raise ValueError(f"status: expected 4 aligned bytes or more on cuda:{dev}; got {t.dtype} "
+                         f"{tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+    return at
 
 
 def _dtype(t: torch.Tensor) -> int:

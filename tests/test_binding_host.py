@@ -143,3 +143,13 @@ def test_layer_fp4_refuses_other_tensors(lib, name, other):
         with pytest.raises(ValueError):
             _layer(False, **{name: bad})
     assert not lib.calls
+
+
+@pytest.mark.parametrize("name", [n for n, (tensors, _) in CALLS.items() if "status" in tensors])
+def test_status_is_a_whole_aligned_word(lib, name):
+    _call(name, lib, status=Fake(U8, 4))
+    _call(name, lib, status=Fake(torch.int64, 1))
+    for bad in (Fake(U8, 3), Fake(I32, 0, address=0), Fake(U8, 8, address=(1 << 20) + 2), Fake(I32, 4, 2, strides=(1, 4))):
+        with pytest.raises(ValueError):
+            _call(name, lib, status=bad)
+    assert len(lib.calls) == 2
