@@ -765,7 +765,7 @@ moe_status_t moe_layer_bwd(const moe_config_t *cfg, const moe_weights_t *w,
  *
  * Shared rules: dtype is MOE_DTYPE_BF16 or MOE_DTYPE_F16 (operands and output
  * alike); R >= 0 rows (at most 2^30), 1 <= E <= 256; matrix dimensions are
- * multiples of 8; matrices are row-major and 16-byte aligned with row strides
+ * multiples of 8, at most 2^30; matrices are row-major and 16-byte aligned with row strides
  * (in elements) that are multiples of 8.  Sums are kept in fp32 and rounded
  * once.  status: uint32 [1] device error word, or NULL. */
 #define MOE_DTYPE_BF16 0
@@ -804,7 +804,7 @@ moe_status_t moe_grouped_wgrad(int32_t dtype, int64_t R, int32_t M, int32_t N, i
  *               fp32 scale for the whole tensor
  * codes uint8 [rows, K / 2]; scales uint8 [rows, moe_fp4_scale_stride(fmt, K)]:
  * a row's K / 32 or K / 16 bytes, padded to a multiple of 16.  K is a multiple
- * of 32; codes and scales are 16-byte aligned. */
+ * of 32, at most 2^30; codes and scales are 16-byte aligned. */
 #define MOE_FP4_MX 0
 #define MOE_FP4_NV 1
 

@@ -242,6 +242,9 @@ def _device(t: torch.Tensor) -> int:
     return dev
 
 
+_MAX_DIM = 1 << 30  # of a matrix; C takes dimensions as 32-bit integers
+
+
 def _bad(t, name, dtype, shape, dev):
     raise ValueError(f"{name}: expected a tensor on cuda:{dev}, {dtype} {tuple(shape)}, with contiguous "
                      f"{'rows' if t.dim() == 2 else 'elements'}; got {t.dtype} {tuple(t.shape)}, "
@@ -262,6 +265,8 @@ def _rows(t: torch.Tensor, name: str, dtype, shape, dev: int):
     contiguous (the stride between rows is free)."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _bad(t, name, dtype, shape, dev)
+    if shape[1] > _MAX_DIM:
+        raise ValueError(f"{name}: more than 2^30 columns")
     s0, s1 = t.stride()
     if s1 != 1 and shape[1] > 1:
         _bad(t, name, dtype, shape, dev)
@@ -669,7 +674,7 @@ def moe_grouped_wgrad(a, b, offsets, out, status=None, stream=None) -> None:
 
 def moe_fp4_scale_stride(fmt: int, K: int) -> int:
     """Bytes of one row's block scales (0 for an invalid format or K)."""
-    if fmt not in (FP4_MX, FP4_NV) or K <= 0 or K % 32:
+    if fmt not in (FP4_MX, FP4_NV) or K <= 0 or K % 32 or K > _MAX_DIM:
         return 0
     return (K // (32 if fmt == FP4_MX else 16) + 15) // 16 * 16
 
@@ -705,6 +710,8 @@ def moe_grouped_gemm_fp4(fmt: int, x_codes, x_scales, w_codes, w_scales, offsets
     weights [E, N, K] (codes [.., K / 2] and scales [.., stride], uint8); y bf16 [R, N]."""
     dev, (R, half), (E, N, _) = _device(x_codes), x_codes.shape, w_codes.shape
     K, u8, f32 = 2 * half, torch.uint8, torch.float32
+    if K > _MAX_DIM:
+        raise ValueError("x_codes: more than 2^30 columns")
     pitch = moe_fp4_scale_stride(fmt, K)
     py, ldy = _rows(y, "y", torch.bfloat16, (R, N), dev)
     _check((_lib or load()).moe_grouped_gemm_fp4(

@@ -289,6 +289,7 @@ moe_status_t check_fp4(int32_t fmt, int64_t rows, int32_t K) {
         return set_last_error(MOE_ERR_INVALID_ARG, "format = %d is neither MX (0) nor NV (1)", fmt);
     if (rows < 0 || K <= 0) return set_last_error(MOE_ERR_INVALID_ARG, "rows must be >= 0 and K > 0");
     if (K % 32) return set_last_error(MOE_ERR_UNSUPPORTED, "K = %d is not a multiple of 32", K);
+    if (K > kRaggedMaxDim) return set_last_error(MOE_ERR_UNSUPPORTED, "K = %d is more than 2^30", K);
     if (rows > (1ll << 30)) return set_last_error(MOE_ERR_UNSUPPORTED, "more than 2^30 rows");
     return MOE_OK;
 }
@@ -301,7 +302,7 @@ int64_t blocks_for(int64_t rows, int team) { return (rows + 256 / team - 1) / (2
 using namespace moe;
 
 extern "C" size_t moe_fp4_scale_stride(int32_t fmt, int32_t K) {
-    if ((fmt != MOE_FP4_MX && fmt != MOE_FP4_NV) || K <= 0 || K % 32) return 0;
+    if ((fmt != MOE_FP4_MX && fmt != MOE_FP4_NV) || K <= 0 || K % 32 || K > kRaggedMaxDim) return 0;
     const size_t n = static_cast<size_t>(K) / (fmt == MOE_FP4_MX ? 32 : 16);
     return (n + 15) / 16 * 16;
 }

@@ -405,6 +405,8 @@ extern "C" moe_status_t moe_grouped_gemm_fp4(int32_t fmt, int64_t R, int32_t N, 
         return set_last_error(MOE_ERR_INVALID_ARG, "rows must be >= 0, dimensions and groups > 0");
     if (K % 32 || N % 8)
         return set_last_error(MOE_ERR_UNSUPPORTED, "K = %d must be a multiple of 32 and N = %d of 8", K, N);
+    if (K > kRaggedMaxDim || N > kRaggedMaxDim)
+        return set_last_error(MOE_ERR_UNSUPPORTED, "K = %d and N = %d must be at most 2^30", K, N);
     if (E > kRaggedMaxGroups) return set_last_error(MOE_ERR_UNSUPPORTED, "E = %d > 256", E);
     if (R > (1ll << 30)) return set_last_error(MOE_ERR_UNSUPPORTED, "too many rows for 32-bit row indices");
     if (R == 0) return MOE_OK;

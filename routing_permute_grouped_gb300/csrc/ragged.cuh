@@ -16,6 +16,7 @@
 namespace moe {
 
 constexpr int kRaggedMaxGroups = 256;
+constexpr int kRaggedMaxDim = 1 << 30;  // of a matrix: (K + 255) / 256, 2 K and the like stay within 32 bits
 constexpr uint32_t kRaggedBadGroup = 0x4u;  // MOE_DEVERR_SEGMENT
 
 struct RaggedArgs {

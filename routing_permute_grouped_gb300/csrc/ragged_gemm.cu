@@ -709,6 +709,8 @@ moe_status_t check_ragged(int32_t dtype, int64_t R, int32_t A, int32_t B, int32_
         return set_last_error(MOE_ERR_INVALID_ARG, "rows must be >= 0, dimensions and groups > 0");
     if (A % 8 || B % 8)
         return set_last_error(MOE_ERR_UNSUPPORTED, "dimensions %d and %d must be multiples of 8", A, B);
+    if (A > kRaggedMaxDim || B > kRaggedMaxDim)
+        return set_last_error(MOE_ERR_UNSUPPORTED, "dimensions %d and %d must be at most 2^30", A, B);
     if (E > kRaggedMaxGroups) return set_last_error(MOE_ERR_UNSUPPORTED, "E = %d > 256", E);
     if (R > (1ll << 30)) return set_last_error(MOE_ERR_UNSUPPORTED, "too many rows for 32-bit row indices");
     return MOE_OK;
