@@ -952,7 +952,12 @@ class MoeLayer:
             moe_pack_experts(w1, w3, w2, w13, w2t, stream)
             return (*quantize(w13), *quantize(w2t))
 
-        ctx = torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext()
+        # torch's part of the set-up (the tensor scales, the reuse of w13 and w2t) goes to the
+        # stream of the library's part, in whatever form it was given
+        ctx = contextlib.nullcontext()
+        if stream is not None:
+            own = isinstance(stream, torch.cuda.Stream)
+            ctx = torch.cuda.stream(stream if own else torch.cuda.ExternalStream(_stream(stream), device=dev))
         with ctx:
             self.packed = pack(W1, W3, W2, E, de)
             self.Wg_t = None
