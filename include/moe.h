@@ -856,8 +856,8 @@ moe_status_t moe_grouped_gemm_fp4(int32_t fmt, int64_t R, int32_t N, int32_t K, 
 
 /* 4-bit expert weights of the layer (device pointers): moe_quantize_fp4 of the
  * K-major rows that moe_pack_experts writes (gate and up interleaved per 128
- * in W13), codes and block scales, with one fp32 tensor scale per expert for
- * MOE_FP4_NV (NULL: 1).  The router stays bf16. */
+ * in W13), codes and block scales, with one fp32 tensor scale per expert (NULL:
+ * 1; the products multiply by it in either format).  The router stays bf16. */
 typedef struct {
     int32_t fmt;         /* MOE_FP4_MX or MOE_FP4_NV */
     const void *Wg_t;    /* router weight, K-major: bf16 [E, d] */
@@ -866,8 +866,8 @@ typedef struct {
     const void *W2q, *s2; const float *g2;       /* rows [E * d, d_e]; fp32 [E] or NULL */
     const void *Ws13q, *ss13; const float *gs13; /* shared: rows [2*d_shared, d]; fp32 [1] or NULL */
     const void *Ws2q, *ss2; const float *gs2;    /* shared: rows [d, d_shared]; fp32 [1] or NULL */
-    const float *x_scale; /* tensor scale of the token rows, fp32 [1] or NULL (1; NV) */
-    const float *h_scale; /* tensor scale of the SwiGLU outputs, fp32 [1] or NULL (1; NV) */
+    const float *x_scale; /* tensor scale of the token rows, fp32 [1] or NULL (1); MX ignores it */
+    const float *h_scale; /* tensor scale of the SwiGLU outputs, fp32 [1] or NULL (1); MX ignores it */
 } moe_weights_fp4_t;
 
 /* Offsets (bytes) of the moe_layer_fwd_fp4 workspace, multiples of 1024.  The

@@ -833,7 +833,7 @@ class MoeLayer:
     expert) and runs ``moe_layer_fwd_fp4``, which quantises the activations
     too; ``fp4_scales`` are the tensor scales of the token rows and of the
     SwiGLU outputs for ``"nv"`` (fp32 [1] CUDA tensors, e.g. the calibrated
-    largest magnitude / 2688; None = 1).
+    largest magnitude / 2688; None = 1); ``"mx"`` ignores them.
     """
 
     def __init__(self, cfg: MoeConfig, W1, W3, W2, Wg=None, bias=None, Ws1=None, Ws3=None, Ws2=None,

@@ -798,16 +798,19 @@ struct MlpFp4 {
 
 static moe_status_t mlp_fp4(const moe_config_t& c, const moe_weights_fp4_t& w, const void* x, const MlpFp4& m,
                             uint32_t* status, cudaStream_t st) {
-    moe_status_t r = moe_quantize_fp4(w.fmt, MOE_DTYPE_BF16, m.rows, c.d, x, c.T, c.d, m.src, c.k, 0, w.x_scale, m.xq,
+    // MX rows have no tensor scale: neither the quantiser nor the product takes one
+    const float* x_scale = w.fmt == MOE_FP4_NV ? w.x_scale : nullptr;
+    const float* h_scale = w.fmt == MOE_FP4_NV ? w.h_scale : nullptr;
+    moe_status_t r = moe_quantize_fp4(w.fmt, MOE_DTYPE_BF16, m.rows, c.d, x, c.T, c.d, m.src, c.k, 0, x_scale, m.xq,
                                       m.xs, st);
     if (r == MOE_OK)
-        r = moe_grouped_gemm_fp4(w.fmt, m.rows, 2 * m.width, c.d, m.E, m.xq, m.xs, m.W13, m.s13, m.offsets, w.x_scale,
+        r = moe_grouped_gemm_fp4(w.fmt, m.rows, 2 * m.width, c.d, m.E, m.xq, m.xs, m.W13, m.s13, m.offsets, x_scale,
                                  m.g13, nullptr, m.gu, 2 * m.width, status, st);
     if (r == MOE_OK)
-        r = moe_quantize_fp4(w.fmt, MOE_DTYPE_BF16, m.rows, m.width, m.gu, m.rows, 2 * m.width, nullptr, 1, 1, w.h_scale,
+        r = moe_quantize_fp4(w.fmt, MOE_DTYPE_BF16, m.rows, m.width, m.gu, m.rows, 2 * m.width, nullptr, 1, 1, h_scale,
                              m.hq, m.hs, st);
     if (r == MOE_OK)
-        r = moe_grouped_gemm_fp4(w.fmt, m.rows, c.d, m.width, m.E, m.hq, m.hs, m.W2, m.s2, m.offsets, w.h_scale, m.g2,
+        r = moe_grouped_gemm_fp4(w.fmt, m.rows, c.d, m.width, m.E, m.hq, m.hs, m.W2, m.s2, m.offsets, h_scale, m.g2,
                                  m.gate, m.y, c.d, status, st);
     return r;
 }

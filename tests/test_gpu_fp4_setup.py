@@ -1,4 +1,4 @@
-"""GPU tests of the 4-bit layer's set-up: streams in any form."""
+"""GPU tests of the 4-bit layer's set-up: streams in any form, tensor scales of the MX format."""
 import pytest
 import torch
 
@@ -29,3 +29,13 @@ def test_setup_on_a_raw_handle(name):
         for a, b in zip((*layer.packed, *layer.shared_packed), (*want.packed, *want.shared_packed)):
             assert (a is None and b is None) or torch.equal(a, b)
         assert torch.equal(layer(x), want(x))
+
+
+@pytest.mark.parametrize("scale", [0.5, 3.0, 0.0, float("nan")])
+def test_mx_rows_have_no_tensor_scale(scale):
+    """The MX quantiser ignores tensor scales, so the products of the layer's own
+    activations do too: the same bits with and without."""
+    want, x = _layer("mx")
+    g = tuple(torch.tensor([s], device="cuda") for s in (scale, 2 * scale))
+    layer, _ = _layer("mx", scales=g)
+    assert torch.equal(layer(x), want(x))
