@@ -760,8 +760,10 @@ moe_status_t moe_layer_bwd(const moe_config_t *cfg, const moe_weights_t *w,
  * padded_offsets of moe_build_offsets).  Groups may have any size, none, any
  * start and gaps between them; rows outside every group are left untouched in
  * the output.  A group that does not lie in [0, R] or runs backwards counts as
- * empty and sets MOE_DEVERR_SEGMENT in *status.  With E = 1, offsets may be
- * NULL: one group of all R rows.
+ * empty and sets MOE_DEVERR_SEGMENT in *status; of the groups after it the
+ * products leave out the rows that lie before the end of an earlier group, so
+ * that no row is two groups' (the weight gradient sums each group's own rows).
+ * With E = 1, offsets may be NULL: one group of all R rows.
  *
  * Shared rules: dtype is MOE_DTYPE_BF16 or MOE_DTYPE_F16 (operands and output
  * alike); R >= 0 rows (at most 2^30), 1 <= E <= 256; matrix dimensions are

@@ -31,12 +31,13 @@ struct RaggedArgs {
 };
 
 // Rows [x, y) of group e; empty and flagged when they do not lie in [0, R].
-__device__ __forceinline__ int2 group_rows(const RaggedArgs& a, int e) {
+__device__ __forceinline__ int2 group_rows(const RaggedArgs& a, int e, bool* bad = nullptr) {
     if (!a.offsets) return make_int2(0, a.R);
     const int lo = ld_dep(a.offsets + e);
     const int hi = ld_dep(a.offsets + e + 1);
     if (lo < 0 || hi < lo || hi > a.R) {
         if (a.status) atomicOr(a.status, kRaggedBadGroup);
+        if (bad) *bad = true;
         return make_int2(0, 0);
     }
     return make_int2(lo, hi);
@@ -63,12 +64,27 @@ struct RaggedItem {
 // One warp fills the list from the offsets.
 template <int TN>
 __device__ void ragged_tiles_build(const RaggedArgs& a, RaggedTiles& s, int panels, int lane) {
-    int running = 0;
+    int running = 0, end = 0;  // work items, and the end of the rows of the groups so far
+    bool skipped = false;
     for (int base = 0; base < a.E; base += 32) {
         const int e = base + lane;
         int n = 0;
+        bool bad = false;
+        int2 g = make_int2(0, 0);
+        if (e < a.E) g = group_rows(a, e, &bad);
+        skipped |= __any_sync(0xFFFFFFFFu, bad);
+        if (skipped) {  // only then can groups overlap: each starts past the ends of those before it
+            int top = g.y;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xFFFFFFFFu, top, o);
+                if (lane >= o) top = max(top, y);
+            }
+            top = __shfl_up_sync(0xFFFFFFFFu, top, 1);
+            g.x = min(max(g.x, lane ? max(top, end) : end), g.y);
+        }
+        end = max(end, __reduce_max_sync(0xFFFFFFFFu, g.y));
         if (e < a.E) {
-            const int2 g = group_rows(a, e);
             s.lo[e] = g.x;
             s.hi[e] = g.y;
             const int len = g.y - g.x, tiles = (len + TN - 1) / TN;
