@@ -757,9 +757,11 @@ moe_status_t moe_layer_bwd(const moe_config_t *cfg, const moe_weights_t *w,
  * layer's SwiGLU pair, for adapters, and for training them: token rows sorted
  * by group, group e owning rows [offsets[e], offsets[e + 1]) (int32 [E + 1],
  * device; e.g. the group_offsets of moe_build_offsets_unpadded or the
- * padded_offsets of moe_build_offsets).  Groups may have any size, none, any
- * start and gaps between them; rows outside every group are left untouched in
- * the output.  A group that does not lie in [0, R] or runs backwards counts as
+ * padded_offsets of moe_build_offsets, whose padding rows then belong to their
+ * groups: the weight gradient sums them, so they must hold zeros in one operand
+ * and numbers in the other).  Groups may have any size or none; the first may
+ * start late and the last end early, and those rows outside every group are
+ * left untouched in the output.  A group that does not lie in [0, R] or runs backwards counts as
  * empty and sets MOE_DEVERR_SEGMENT in *status; of the groups after it the
  * products leave out the rows that lie before the end of an earlier group, so
  * that no row is two groups' (the weight gradient sums each group's own rows).

@@ -2,9 +2,9 @@
 // launch description and the reading of the group offsets.
 //
 // Token rows are sorted by group (expert): group e owns rows
-// [offsets[e], offsets[e + 1]) of the row-major operands, with any sizes,
-// starts and gaps.  The offsets live on the device, so nothing of the launch
-// depends on them.
+// [offsets[e], offsets[e + 1]) of the row-major operands, of any size; rows
+// before the first group and past the last belong to none.  The offsets live on
+// the device, so nothing of the launch depends on them.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
