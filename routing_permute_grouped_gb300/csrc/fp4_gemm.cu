@@ -358,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------ epilogue
         const float gx = args.x_scale ? ld_dep(args.x_scale) : 1.0f;
         if (!product_epilogue<__nv_bfloat16, C::TN, 1>(
-                args, tY, tiles, bars, panels, total, first, stride, tmem_base, warp - kEpi0, lane, rank,
+                args, tY, tiles, bars, panels, total, first, stride, steps, tmem_base, warp - kEpi0, lane, rank,
                 sOut + (warp - kEpi0) * 2048, gx,
                 [&](int e) { return args.w_scale ? ld_dep(args.w_scale + e) : 1.0f; }))
             timed_out = true;

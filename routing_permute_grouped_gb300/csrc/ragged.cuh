@@ -245,8 +245,15 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, 
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
 // A bounded wait of a converged warp; the same answer in every lane.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort,
+                                          uint64_t limit_ns = kWaitLimitNs) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, limit_ns));
+}
+// The limit of a wait for a whole sum of that many steps, which may take longer
+// than kWaitLimitNs: 2^30 rows of one group's weight gradient run for 4.4 s.  A
+// step takes 0.26 us where its loads bound it.
+__device__ __forceinline__ uint64_t sum_limit_ns(int64_t steps) {
+    return kWaitLimitNs + static_cast<uint64_t>(steps) * 2000u;
 }
 
 struct Ring {  // stage and its parity
@@ -347,8 +354,8 @@ __device__ __forceinline__ void pair_end(uint32_t tmem_base, int warp) {
 template <typename T, int TN, int SP, int S, typename Scale>
 __device__ __forceinline__ bool product_epilogue(const RaggedArgs& args, const CUtensorMap& tY,
                                                  const RaggedTiles& tiles, PairBars<S>& bars,
-                                                 int panels, int total, int first, int stride, uint32_t tmem_base,
-                                                 int ew, int lane, uint32_t rank, uint8_t* stage, float common,
+                                                 int panels, int total, int first, int stride, int steps,
+                                                 uint32_t tmem_base, int ew, int lane, uint32_t rank, uint8_t* stage, float common,
                                                  Scale scale_of, uint8_t* join = nullptr) {
     constexpr int kChunks = (TN + 32) / 64;
     const int q = (threadIdx.x >> 5) & 3, odd = ew >> 2;
@@ -372,7 +379,7 @@ __device__ __forceinline__ bool product_epilogue(const RaggedArgs& args, const C
     fetch(first);
     Acc acc;
     for (int t = first; t < total; t += stride) {
-        if (!warp_wait(bars.tfull + acc.i, acc.ph, abort_flag)) {
+        if (!warp_wait(bars.tfull + acc.i, acc.ph, abort_flag, sum_limit_ns(steps))) {
             if (lane == 0) bulk_wait_all();
             return false;
         }
@@ -410,7 +417,7 @@ __device__ __forceinline__ bool product_epilogue(const RaggedArgs& args, const C
                 const uint32_t pair = rank >> 1;
                 if (pair > 0) {
                     // the first pair has read this warp's part of the last tile
-                    bool ok = warp_wait(bars.join_free + ew, join_ph ^ 1u, abort_flag);
+                    bool ok = warp_wait(bars.join_free + ew, join_ph ^ 1u, abort_flag, sum_limit_ns(steps));
                     join_ph ^= 1u;
                     if (!ok) return false;
                     fence_cluster();
@@ -425,7 +432,7 @@ __device__ __forceinline__ bool product_epilogue(const RaggedArgs& args, const C
                     if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(bars.join_full + ew), rank & 1u));
                     break;
                 }
-                bool ok = warp_wait(bars.join_full + ew, join_ph, abort_flag);
+                bool ok = warp_wait(bars.join_full + ew, join_ph, abort_flag, sum_limit_ns(steps));
                 join_ph ^= 1u;
                 if (!ok) {
                     if (lane == 0) bulk_wait_all();

@@ -220,8 +220,8 @@ __global__ void __cluster_dims__(2 * SP, 1, 1) __launch_bounds__(64 + 32 * kEpiW
         }
     } else {
         // ------------------------------------------------------ epilogue
-        if (!product_epilogue<T, C::TN, SP>(args, tY, tiles, bars, panels, total, first, stride, tmem_base, warp - 2, lane,
-                                          rank, sOut + (warp - 2) * 2048, 1.0f, [](int) { return 1.0f; }, join))
+        if (!product_epilogue<T, C::TN, SP>(args, tY, tiles, bars, panels, total, first, stride, k1 - k0, tmem_base, warp - 2,
+                                            lane, rank, sOut + (warp - 2) * 2048, 1.0f, [](int) { return 1.0f; }, join))
             timed_out = true;
         if (timed_out) *abort_flag = 1;
     }
@@ -291,11 +291,12 @@ struct GradFeed {
 // one another those columns in fp32 and add what they receive to their own, the
 // other pairs' in ascending order.  What is sent lands in the receiver's pipeline
 // stages: a cluster has one tile, so they are free once its sum is complete, which
-// join_free says.  has: this pair had rows, and its accumulator is at taddr.
-// False on a timeout.
+// join_free says.  has: this pair had rows, and its accumulator is at taddr;
+// limit: of each wait, in ns.  False on a timeout.
 template <int SP>
 __device__ __forceinline__ bool exchange_parts(PairBars<kGradStages>& bars, float (&f)[128 / SP], uint8_t* stages,
-                                               uint32_t taddr, bool has, int ew, int lane, uint32_t rank) {
+                                               uint32_t taddr, bool has, int ew, int lane, uint32_t rank,
+                                               uint64_t limit) {
     constexpr int kPart = 128 / SP;
     constexpr int kBytes = kPart * 128;  // of a warp: 32 lanes x kPart fp32
     static_assert((SP - 1) * kEpiWarps * kBytes <= kGradStages * kStage, "the parts fit the stages");
@@ -304,7 +305,7 @@ __device__ __forceinline__ bool exchange_parts(PairBars<kGradStages>& bars, floa
     if (lane == 0)
         for (int o = 0; o < SP; ++o)
             if (o != pair) mbar_arrive_cluster(mapa_shared(smem_u32(bars.join_free + ew), 2 * o + cta));
-    if (!warp_wait(bars.join_free + ew, 0, abort_flag)) return false;
+    if (!warp_wait(bars.join_free + ew, 0, abort_flag, limit)) return false;
     fence_cluster();
 #pragma unroll 1
     for (int i = 1; i < SP; ++i) {
@@ -339,7 +340,7 @@ __device__ __forceinline__ bool exchange_parts(PairBars<kGradStages>& bars, floa
             for (int j = 0; j < 32; ++j) f[c + j] = __uint_as_float(v[j]);
         }
     }
-    if (!warp_wait(bars.join_full + ew, 0, abort_flag)) return false;
+    if (!warp_wait(bars.join_full + ew, 0, abort_flag, limit)) return false;
     fence_cluster();
 #pragma unroll 1
     for (int o = 0; o < SP - 1; ++o) {
@@ -497,17 +498,20 @@ __global__ void __cluster_dims__(2 * SP, 1, 1) __launch_bounds__(96 + 32 * kEpiW
         // ------------------------------------------------- zeroing of tails
         Ring r;
         uint32_t tail_ph = 0;
+        int64_t ahead = 0;  // steps from the last tail to the next
         GradFeed<SP> feed;
         for (int t = first; t < total && !timed_out; t += stride) {
             const GradTile g = feed.next(args, total, t, stride, lane, pair);
             const int steps = (g.rows + kBK - 1) / kBK, rest = g.rows % kBK;
             for (int k = 0; k + 1 < steps; ++k) r.next<S>();
             if (steps == 0) continue;
+            ahead += steps;
             if (rest) {
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars.tail + r.s, (tail_ph >> r.s) & 1u, abort_flag))) {
+                if (!warp_wait(bars.tail + r.s, (tail_ph >> r.s) & 1u, abort_flag, sum_limit_ns(ahead))) {
                     timed_out = true;
                     break;
                 }
+                ahead = 0;
                 tail_ph ^= 1u << r.s;
                 // rows [rest, next multiple of 16): one 128-byte row in each of
                 // the four 64-column chunks (a row stays in its own 128 bytes
@@ -541,8 +545,9 @@ __global__ void __cluster_dims__(2 * SP, 1, 1) __launch_bounds__(96 + 32 * kEpiW
             const int n = g.n + c0;
             uint32_t pk[kPart / 2];
             uint32_t taddr = 0;
+            const uint64_t limit = sum_limit_ns(g.whole / kBK + 1);
             if (g.rows) {
-                if (!warp_wait(bars.tfull + acc.i, acc.ph, abort_flag)) {
+                if (!warp_wait(bars.tfull + acc.i, acc.ph, abort_flag, limit)) {
                     timed_out = true;
                     break;
                 }
@@ -570,7 +575,7 @@ __global__ void __cluster_dims__(2 * SP, 1, 1) __launch_bounds__(96 + 32 * kEpiW
                 float f[kPart];
 #pragma unroll
                 for (int i = 0; i < kPart; ++i) f[i] = 0.f;
-                if (g.whole && !exchange_parts<SP>(bars, f, smem, taddr, g.rows != 0, ew, lane, rank)) {
+                if (g.whole && !exchange_parts<SP>(bars, f, smem, taddr, g.rows != 0, ew, lane, rank, limit)) {
                     timed_out = true;
                     break;
                 }
