@@ -802,8 +802,8 @@ moe_status_t moe_grouped_wgrad(int32_t dtype, int64_t R, int32_t M, int32_t N, i
 /* Rows of 4-bit codes with block scales: e2m1 values (0, 0.5, 1, 1.5, 2, 3,
  * 4, 6 and their negatives), two to a byte, the even element in the low
  * nibble, and one scale byte for each block of consecutive elements of a row:
- *   MOE_FP4_MX  blocks of 32, scale 2^(byte - 127) (OCP MX: e2m1 with e8m0;
- *               byte 255 is NaN)
+ *   MOE_FP4_MX  blocks of 32, scale 2^(byte - 127) (the format of OCP MX, e2m1
+ *               with e8m0; byte 255 is NaN)
  *   MOE_FP4_NV  blocks of 16, scale an e4m3 value (byte 127 is NaN) times one
  *               fp32 scale for the whole tensor
  * codes uint8 [rows, K / 2]; scales uint8 [rows, moe_fp4_scale_stride(fmt, K)]:
@@ -822,7 +822,10 @@ size_t moe_fp4_scale_stride(int32_t fmt, int32_t K);
  * interleaved per 128 (the column order of the packed W13; K a multiple of
  * 128), and the element quantised is silu(gate) * up rounded to x's type.
  *   MX: scale = the smallest power of two with max|block| <= 6 * scale (1 for
- *       a block of zeros);
+ *       a block of zeros), so that nothing saturates.  This is not the
+ *       conversion of OCP's text, 2^(floor(log2 max|block|) - 2), which is half
+ *       of it where the significand of max|block| is above 1.5: the codes of
+ *       such blocks differ from those of a quantiser that follows the text;
  *   NV: scale = e4m3(min(448, max|block| / (6 g))) * g with g = *tensor_scale
  *       (1 if NULL; MX ignores it), nearest, ties to even;
  * code = the e2m1 value nearest to x / scale, ties to even, saturating at 6

@@ -4,7 +4,9 @@
 // e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two to a byte,
 // the even element in the low nibble:
 //   MX  32 elements, scale 2^(byte - 127), the smallest power of two with
-//       amax <= 6 * scale (no element saturates)
+//       amax <= 6 * scale (no element saturates; the conversion that OCP's text
+//       gives takes 2^(floor(log2 amax) - 2) and lets the top of a block saturate,
+//       half this scale where amax's significand is above 1.5)
 //   NV  16 elements, scale e4m3(min(448, amax / (6 g))) * g, g the tensor's
 //       fp32 scale
 // code = the e2m1 value nearest to x / scale, ties to even.  Every step is an
@@ -12,9 +14,11 @@
 // codes are fixed by the inputs alone.
 //
 // Dequantising is bound by memory: a thread takes 8 elements (4 bytes of codes,
-// 16 of output), so that every access of a warp is contiguous (6.1 TB/s at the
-// default batch).  Quantising is bound by integer and conversion instructions
-// (8 elements per thread: 100 against 72 us at the default batch), so a thread
+// 16 of output), so that every access of a warp is contiguous (32768 x 7168: MX
+// 88 us, 6.8 TB/s; NV 98).  Quantising is bound by integer and conversion
+// instructions (8192 tokens to 4 experts each, K = 7168: MX 70 us, of which the
+// bytes need 36, NV with a division per element 141; with the SwiGLU, 32768 x
+// 2048, 79 and 103).  MX with 8 elements per thread took 100 us, so a thread
 // takes 16, a whole NV block or half an MX one: what is done once per block is
 // then done by one or two threads.  The rows are read with 32-byte loads where
 // they are aligned to 32 bytes, else with two of 16; amax is taken on the 16-bit

@@ -24,11 +24,20 @@
 // cycles even when there is nothing to wait for (445 against 405 us with two).
 //
 // What bounds it (default gate/up product of 8 experts, 32768 rows, 7168 ->
-// 4096, MX: 320 to 330 us, 6 PFLOP/s): the issue of the MMAs, whose operands and
-// scale addresses make it about 90 cycles each against 112 of execution, with
-// the waits on top.  The loads alone took 252 us.
+// 4096, MX: 293 to 330 us, 5.8 to 6.6 PFLOP/s): the turn of the two scale
+// buffers.  A step's scales can be stored once the MMAs of two steps before are
+// complete, and its own MMAs start only after the store, its hand-over and the
+// issue.  Counted in the kernel at that size, of 627 cycles per step, of which
+// its four MMAs run 432 (tensor pipe 70 % busy): the MMA warp waits 260 for a
+// step's codes and scales (ready at once in 2 % of the steps), issues the MMAs
+// in 130 and commits in 44; a layout warp waits 270 for a free buffer and 70 for
+// a group of scales, stores and hands on in 115 and reads and rearranges the
+// rest; the TMA warp is busy for 510.  The loads alone took 252 us.
 // Decode (two rows for each of 256 experts) runs at the weights' bytes over HBM.
-// Short sums (K = 1024) are bound by the epilogue.
+// Short sums (K = 1024: 216 to 232 us for 98304 rows of 64 experts, N = 4096) are
+// bound by the epilogue: the MMAs of a tile run 40 % of its time.
+// NV has twice the scale words and tiles of 192 rows: 391 to 396 us where MX
+// takes 293 to 297, 259 where it takes 216.
 //
 // A scale buffer in tensor memory is written again once its MMAs are complete.
 //
@@ -53,11 +62,11 @@ constexpr int kWBytes = 128 * 128;        // weight codes of one CTA and stage
 constexpr int kEpi0 = 8;                  // first epilogue warp
 constexpr int kThreads = 32 * (kEpi0 + kEpiWarps);
 
-// Issuing a step's four MMAs takes about 450 cycles whatever their N, and an MMA
-// runs N / 2 cycles, so the widest tile is the fastest.  Two accumulators and
-// two scale buffers (the words of one step, two of MX and four of NV, each 4
-// columns of A and 8 of B) must fit 512 columns of tensor memory: 224 token rows
-// for MX, 192 for NV (MX with 192: 342 against 324 us).
+// A step's cost outside its MMAs is the same for every tile, and an MMA runs N / 2
+// cycles, so the widest tile is the fastest.  Two accumulators and two scale
+// buffers (the words of one step, two of MX and four of NV, each 4 columns of A
+// and 8 of B) must fit 512 columns of tensor memory: 224 token rows for MX, 192
+// for NV (MX with 192: 342 against 324 us).
 template <bool NV>
 struct Cfg {
     static constexpr int TN = NV ? 192 : 224;  // token rows of a tile, at most
@@ -194,7 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     tc_fence_after();
                     // the next stage is looked at while this one's MMAs are
-                    // issued: the issue, not the tensor pipe, sets the pace
+                    // issued: a wait costs even when there is nothing to wait for
                     const Ring next = r.after<S>();
                     const bool peek = mbar_test_wait(bars.full + next.s, next.ph);
                     const uint32_t at = static_cast<uint32_t>(r.s) * (C::stage >> 4);

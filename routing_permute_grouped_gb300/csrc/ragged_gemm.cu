@@ -27,14 +27,15 @@
 // other's shared memory, in an order that does not depend on timing.
 //
 // What bounds them: at the default layer's gate/up size (32768 rows, 8 experts,
-// 7168 -> 4096) a launch by itself takes 1.02 ms, 1890 TFLOP/s, with the tensor
-// pipe 93 % busy at 1.63 GHz, the board's power limit; back to back 1.15 to 1.19
-// ms.  The data gradient of a 64-expert layer (98304 rows, 2048 -> 4096): 0.90 ms
-// alone, 92 % busy.  The weight gradient: 0.93 ms, 81 % busy, waiting for loads
-// (two 64-column boxes per operand and step).  Two rows for each of 256 experts:
-// the weights' bytes over HBM.  Clusters of two pairs that share one operand by
-// TMA multicast gained nothing (default 1.169 against 1.187 ms, data gradient
-// 1.069 against 1.062): fewer SMs hold clusters of four.
+// 7168 -> 4096) a launch by itself takes 1.02 to 1.04 ms, 1850 to 1890 TFLOP/s,
+// with the tensor pipe 92 to 93 % busy at 1.62 GHz, the board's power limit; back
+// to back 1.14 to 1.19 ms.  The data gradient of a 64-expert layer (98304 rows,
+// 2048 -> 4096): 0.90 to 0.91 ms alone, 91 % busy.  The weight gradient: 0.93 ms,
+// 81 % busy, waiting for loads (two 64-column boxes per operand and step).  Two
+// rows for each of 256 experts: the weights' bytes over HBM.  Clusters of two
+// pairs that share one operand by TMA multicast gained nothing (default 1.169
+// against 1.187 ms, data gradient 1.069 against 1.062): fewer SMs hold clusters
+// of four.
 //
 // Warp roles: warp 0 TMA producer, warp 1 tensor memory and MMA issue (even
 // CTA), warps 2..9 epilogue, warp 10 (weight gradient) the zeroing of tails.
