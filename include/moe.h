@@ -921,6 +921,141 @@ moe_status_t moe_layer_fwd_fp4_prerouted(const moe_config_t *cfg, const moe_weig
                                          const float *topk_w, void *out, void *ws, size_t ws_bytes,
                                          void *stream);
 
+/* --------------------------------------------------- routing by scores -- */
+
+/* The choice of experts for routers other than moe_route's, from logits that
+ * the caller has (a product of its own, a noisy or a learned gate), with the
+ * gradient and the losses that training such a router takes.  Per token:
+ *   s     MOE_SCORE_SOFTMAX: the softmax of its logits over all E experts;
+ *         MOE_SCORE_SIGMOID: their sigmoids
+ *   key   s + bias[e] with a bias (for balance: it moves the choice, not the
+ *         weights); without one the experts have the order of their logits
+ *   choice  n_groups > 0: the topk_groups groups of E / n_groups neighbouring
+ *         experts with the best scores are kept, a group's score being its
+ *         largest key (group_top 1) or the sum of its two largest (2, on
+ *         scores even without a bias; its one key where it has no second);
+ *         then the k experts with the largest keys, in descending order.
+ *         Ties go to the lower index
+ *   topk_w  scale * s of the chosen, with renormalize divided by their sum
+ * The choice is that of exact keys (fp64 where fp32 cannot separate two), the
+ * weights are fp32.  A logit of -infinity or NaN has score 0 and is chosen only
+ * when nothing else is left (weight 0); +infinity counts as the largest finite
+ * number.  Biases of -infinity and NaN keep their experts from being chosen in
+ * the same way; +infinity is the largest finite number.
+ *
+ * Limits as for moe_route: 1 <= E <= 256, 1 <= k <= min(8, E), n_groups <= 32
+ * and dividing E, topk_groups * (E / n_groups) >= k, T * k <= 2^30; scale
+ * finite.  Logits are MOE_DTYPE_BF16, MOE_DTYPE_F16 or MOE_DTYPE_F32, rows at
+ * any stride >= E (aligned rows are read faster).  The outputs are what
+ * moe_build_offsets and the pre-routed layer take. */
+#define MOE_DTYPE_F32 2
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+
+typedef struct {
+    int32_t E, k;
+    int32_t score;       /* MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID */
+    int32_t n_groups;    /* 0 = no groups */
+    int32_t topk_groups;
+    int32_t group_top;   /* 1 or 2 (read when n_groups > 0) */
+    int32_t renormalize;
+    float scale;
+} moe_score_rule_t;
+
+/* Bytes of the workspace that loads and losses need; 0 if rule or T is invalid. */
+size_t moe_route_scores_workspace_size(const moe_score_rule_t *rule, int64_t T);
+
+/* The choice and, if asked for, the loads and losses of a training step:
+ *   counts[e]  choices of expert e
+ *   losses[0]  balance: E / (k T) * sum_e counts[e] * mean_t p[t, e], with p
+ *              the scores of a token divided by their sum; 1 when all is even
+ *   losses[1]  z: mean_t (log sum_e exp(logit))^2
+ * A token without a finite logit adds nothing to either.  With T = 0 the counts
+ * and losses are zero and nothing else is touched.
+ *   logits    [T, E], row stride ld            device, read
+ *   bias      fp32 [E] or NULL                 device, read
+ *   topk_idx  int32 [T, k], topk_w fp32 [T, k] device, written
+ *   counts    int32 [E], losses fp32 [2], or both NULL  device, written
+ *   ws        device scratch, 16-byte aligned, any contents; NULL without
+ *             losses.  Calls that may overlap need one each. */
+moe_status_t moe_route_scores(const moe_score_rule_t *rule, int32_t dtype, int64_t T,
+                              const void *logits, int64_t ld, const float *bias, int32_t *topk_idx,
+                              float *topk_w, int32_t *counts, float *losses, void *ws,
+                              size_t ws_bytes, void *stream);
+
+/* dlogits (the type of the logits, row stride ldd) for a gradient dw of topk_w
+ * and dlosses of the losses; the choice and the counts are constants.  The rule
+ * is the forward's (its groups are not read).  Every element is written.
+ *   topk_idx  int32 [T, k], dw fp32 [T, k]: or dw NULL (no such gradient).  An
+ *             index outside [0, E) is left out; one that repeats counts each
+ *             time
+ *   counts    int32 [E], dlosses fp32 [2]: or both NULL
+ *   all device, read but for dlogits. */
+moe_status_t moe_route_scores_bwd(const moe_score_rule_t *rule, int32_t dtype, int64_t T,
+                                  const void *logits, int64_t ld, const int32_t *topk_idx,
+                                  const float *dw, const int32_t *counts, const float *dlosses,
+                                  void *dlogits, int64_t ldd, void *stream);
+
+/* --------------------------------- 4-bit weights under 16-bit activations -- */
+
+/* Rows of unsigned 4-bit codes with a scale, and if asked for a zero point, for
+ * each `group` (32, 64 or 128) of consecutive elements; a row's last group may
+ * be short.  value = (code - zero) * scale with the scale in the rows' own
+ * 16-bit type (MOE_DTYPE_BF16 or MOE_DTYPE_F16) and zero an integer 0 .. 15, 8
+ * where there are no zero points.
+ *   codes   uint8 [rows, K / 2]: eight elements to a little-endian 32-bit word,
+ *           element 2 i in bits 4 i .. 4 i + 3, element 2 i + 1 in bits 16 + 4 i
+ *           .. 19 + 4 i; 16-byte aligned
+ *   scales  dtype [rows, ceil(K / group)]
+ *   zeros   uint8 [rows, ceil(K / group)], or NULL
+ * K is a multiple of 32, at most 2^30; at most 2^30 rows. */
+
+/* Quantises rows: with T() rounding to the rows' type and [] to the nearest
+ * integer, ties to even,
+ *   zeros NULL: scale = T(max|x| / 7), code = 8 + [x / scale] cut to -8 .. 7
+ *   else:       lo = min(0, least x), hi = max(0, largest x),
+ *               scale = T((hi - lo) / 15), zero = [-lo / scale] cut to 0 .. 15,
+ *               code = [x / scale] + zero cut to 0 .. 15
+ * A scale of 0 (a group of zeros, or too small for the type) has codes of value
+ * 0.  A NaN or infinity makes its group's scale, and so its values, NaN.
+ *   x  dtype [rows, K], row stride ldx (a multiple of 8), 16-byte aligned
+ *   all device; x read, the rest written. */
+moe_status_t moe_quantize_int4(int32_t group, int32_t dtype, int64_t rows, int32_t K, const void *x,
+                               int64_t ldx, void *codes, void *scales, void *zeros, void *stream);
+
+/* out[r] = the values of row r (dtype, row stride ldo, a multiple of 8, 16-byte
+ * aligned), rounded once.  With many rows per group, the values and
+ * moe_grouped_gemm are the faster product. */
+moe_status_t moe_dequantize_int4(int32_t group, int32_t dtype, int64_t rows, int32_t K,
+                                 const void *codes, const void *scales, const void *zeros,
+                                 void *out, int64_t ldo, void *stream);
+
+/* The grouped product of 16-bit rows, as they are, with 4-bit weights:
+ *   y[r] = row_scale[r] * x[src[r] / src_div] W[e]^T
+ * on the groups of moe_grouped_gemm (same rules on offsets, E and status), or
+ * with x[r] where src is NULL.  With the row_src and k of
+ * moe_build_offsets_unpadded that is the permute into expert order; negative
+ * entries of src and those past x's rows give rows of zeros.  With swiglu, W has
+ * 2 N rows per group, gate and up interleaved per 128 (the order of the packed
+ * W13; N a multiple of 128), and
+ *   y[r] = row_scale[r] * silu(gate) * up.
+ * Differences of code and zero are multiplied exactly and summed in fp32, each
+ * group's sum is scaled in fp32, and the result is rounded once.  Made for few
+ * rows per group (decoding), where the weights' bytes set the pace.
+ *   x          dtype [x_rows, K], row stride ldx (a multiple of 8)  device, read
+ *   src        int32 [R] or NULL                device, read
+ *   w_codes, w_scales, w_zeros (or NULL)  rows [E * N or E * 2 N, K]  device, read
+ *   offsets    int32 [E + 1], or NULL with E = 1        device, read
+ *   row_scale  fp32 [R] or NULL (1)             device, read
+ *   y          dtype [R, N], row stride ldy (a multiple of 8)  device, written
+ * x, w_codes and y are 16-byte aligned, N is a multiple of 8 and at most 2^29. */
+moe_status_t moe_grouped_gemm_int4(int32_t group, int32_t dtype, int64_t R, int32_t N, int32_t K,
+                                   int32_t E, const void *x, int64_t x_rows, int64_t ldx,
+                                   const int32_t *src, int32_t src_div, const void *w_codes,
+                                   const void *w_scales, const void *w_zeros,
+                                   const int32_t *offsets, const float *row_scale, int32_t swiglu,
+                                   void *y, int64_t ldy, uint32_t *status, void *stream);
+
 /* ---------------------------------------------------------- diagnostics -- */
 
 /* Synchronises `stream`, reads the uint32 device error word at the start of

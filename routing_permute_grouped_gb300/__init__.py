@@ -45,6 +45,9 @@ __all__ = [
     "moe_fp4_scale_stride", "moe_quantize_fp4", "moe_dequantize_fp4", "moe_grouped_gemm_fp4",
     "MoeWeightsFp4", "moe_workspace_size_fp4", "moe_workspace_layout_fp4", "moe_layer_fwd_fp4",
     "moe_layer_fwd_fp4_prerouted", "grouped_linear",
+    "ScoreRule", "score_rule", "moe_route_scores_workspace_size", "moe_route_scores",
+    "moe_route_scores_bwd", "route_scores",
+    "moe_quantize_int4", "moe_dequantize_int4", "moe_grouped_gemm_int4",
 ]
 
 MOE_OK = 0
@@ -53,7 +56,9 @@ DEVERR_TIMEOUT = 0x2
 DEVERR_SEGMENT = 0x4
 FP4_MX, FP4_NV = 0, 1
 FP4_FORMATS = {"mx": FP4_MX, "nv": FP4_NV}
+SCORES = {"softmax": 0, "sigmoid": 1}
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+_LOGIT_DTYPES = {**_DTYPES, torch.float32: 2}
 
 
 class MoeError(RuntimeError):
@@ -111,6 +116,13 @@ _LAYOUT_FP4_FIELDS = ("total", "status", "topk_idx", "topk_w", "counts", "group_
 
 class _LayoutFp4(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in _LAYOUT_FP4_FIELDS]
+
+
+class ScoreRule(ctypes.Structure):
+    """How moe_route_scores chooses and weighs experts (see score_rule)."""
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("E", "k", "score", "n_groups", "topk_groups", "group_top", "renormalize")] + [
+                    ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -197,6 +209,15 @@ def load():
         "moe_layer_fwd_fp4": (ctypes.c_int, [CP, ctypes.POINTER(MoeWeightsFp4), P, P, P, SZ, P]),
         "moe_layer_fwd_fp4_prerouted": (ctypes.c_int, [CP, ctypes.POINTER(MoeWeightsFp4), P, P, P,
                                                        P, P, SZ, P]),
+        "moe_route_scores_workspace_size": (SZ, [ctypes.POINTER(ScoreRule), I64]),
+        "moe_route_scores": (ctypes.c_int, [ctypes.POINTER(ScoreRule), I32, I64, P, I64, P, P, P, P,
+                                            P, P, SZ, P]),
+        "moe_route_scores_bwd": (ctypes.c_int, [ctypes.POINTER(ScoreRule), I32, I64, P, I64, P, P,
+                                                P, P, P, I64, P]),
+        "moe_quantize_int4": (ctypes.c_int, [I32, I32, I64, I32, P, I64, P, P, P, P]),
+        "moe_dequantize_int4": (ctypes.c_int, [I32, I32, I64, I32, P, P, P, P, I64, P]),
+        "moe_grouped_gemm_int4": (ctypes.c_int, [I32, I32, I64, I32, I32, I32, P, I64, I64, P, I32, P,
+                                                 P, P, P, P, I32, P, I64, P, P]),
         "moe_get_device_status": (ctypes.c_int, [P, ctypes.POINTER(ctypes.c_uint32), P]),
         "moe_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_uint64, P, P]),
         "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -797,6 +818,142 @@ def grouped_linear(x, w, offsets):
     and in the gradient of x.  x and the gradient of y may have any strides; those that the
     products cannot read are copied.  A second derivative raises an error."""
     return _GroupedLinear.apply(x, w, offsets)
+
+
+# ---------------------------------------------------- routing by scores ----
+def score_rule(E: int, k: int, score: str = "softmax", n_groups: int = 0, topk_groups: int = 0,
+               group_top: int = 1, renormalize: bool = True, scale: float = 1.0) -> ScoreRule:
+    """The rule of moe_route_scores: the k of E experts, ``score`` "softmax" or "sigmoid",
+    the limit to ``topk_groups`` of ``n_groups`` groups by their largest key (``group_top``
+    1) or the sum of their two largest (2), weights renormalised and scaled."""
+    if score not in SCORES:
+        raise ValueError('score is "softmax" or "sigmoid"')
+    return ScoreRule(E, k, SCORES[score], n_groups, topk_groups, group_top, int(renormalize), scale)
+
+
+def _logits(t: torch.Tensor, name: str, dtype, shape, dev: int):
+    """Address and row stride of a [T, E] tensor whose rows are contiguous."""
+    if t.dim() != 2 or dtype not in _LOGIT_DTYPES:
+        raise ValueError(f"{name}: expected a [T, E] tensor of bf16, fp16 or fp32; got {t.dtype} {tuple(t.shape)}")
+    return _rows(t, name, dtype, shape, dev)
+
+
+def moe_route_scores_workspace_size(rule: ScoreRule, T: int) -> int:
+    return int((_lib or load()).moe_route_scores_workspace_size(ctypes.byref(rule), T))
+
+
+def moe_route_scores(rule: ScoreRule, logits, topk_idx, topk_w, bias=None, counts=None, losses=None,
+                     ws=None, stream=None) -> None:
+    """topk_idx int32 [T, k] and topk_w fp32 [T, k] of logits [T, E] (bf16, fp16 or fp32, rows
+    at any stride), ``bias`` fp32 [E]; for training also counts int32 [E] and losses fp32 [2]
+    (balance, z), with a workspace of moe_route_scores_workspace_size(rule, T) bytes."""
+    dev, T, E, k, f32 = _device(logits), logits.shape[0], rule.E, rule.k, torch.float32
+    px, ld = _logits(logits, "logits", logits.dtype, (T, E), dev)
+    _check((_lib or load()).moe_route_scores(
+        ctypes.byref(rule), _LOGIT_DTYPES[logits.dtype], T, px, ld, _arg(bias, "bias", f32, (E,), dev),
+        _arg(topk_idx, "topk_idx", torch.int32, (T, k), dev), _arg(topk_w, "topk_w", f32, (T, k), dev),
+        _arg(counts, "counts", torch.int32, (E,), dev), _arg(losses, "losses", f32, (2,), dev),
+        None if ws is None else _whole(ws, "ws", ws.dtype, 0, dev),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream, dev)))
+
+
+def moe_route_scores_bwd(rule: ScoreRule, logits, topk_idx, dlogits, dw=None, counts=None, dlosses=None,
+                         stream=None) -> None:
+    """dlogits [T, E] (the logits' type) for the gradient ``dw`` fp32 [T, k] of topk_w and, with
+    ``counts``, ``dlosses`` fp32 [2] of the losses; topk_idx may be None without dw."""
+    dev, T, E, k, f32 = _device(logits), logits.shape[0], rule.E, rule.k, torch.float32
+    px, ld = _logits(logits, "logits", logits.dtype, (T, E), dev)
+    po, ldd = _logits(dlogits, "dlogits", logits.dtype, (T, E), dev)
+    _check((_lib or load()).moe_route_scores_bwd(
+        ctypes.byref(rule), _LOGIT_DTYPES[logits.dtype], T, px, ld,
+        _arg(topk_idx, "topk_idx", torch.int32, (T, k), dev), _arg(dw, "dw", f32, (T, k), dev),
+        _arg(counts, "counts", torch.int32, (E,), dev), _arg(dlosses, "dlosses", f32, (2,), dev), po, ldd,
+        _stream(stream, dev)))
+
+
+class _RouteScores(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, rule, bias, losses):
+        T, dev = logits.shape[0], logits.device
+        if logits.stride(1) != 1 and rule.E > 1 or logits.stride(0) < rule.E and T > 1:
+            logits = logits.clone(memory_format=torch.contiguous_format)
+        idx = torch.empty((T, rule.k), dtype=torch.int32, device=dev)
+        w = torch.empty((T, rule.k), dtype=torch.float32, device=dev)
+        counts = both = ws = None
+        if losses:
+            counts = torch.empty((rule.E,), dtype=torch.int32, device=dev)
+            both = torch.empty((2,), dtype=torch.float32, device=dev)
+            ws = torch.empty((moe_route_scores_workspace_size(rule, T),), dtype=torch.uint8, device=dev)
+        moe_route_scores(rule, logits, idx, w, bias, counts, both, ws)
+        ctx.rule = rule
+        ctx.save_for_backward(logits, idx, counts)
+        ctx.mark_non_differentiable(idx, *([counts] if losses else []))
+        return (w, idx, both, counts) if losses else (w, idx)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dw, _, dlosses=None, __=None):
+        logits, idx, counts = ctx.saved_tensors
+        dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
+        moe_route_scores_bwd(ctx.rule, logits, idx, dlogits, dw=dw.contiguous(), counts=counts,
+                             dlosses=None if counts is None else dlosses.contiguous())
+        return dlogits, None, None, None
+
+
+def route_scores(logits, rule: ScoreRule, bias=None, losses: bool = False):
+    """moe_route_scores, differentiable in the logits: topk_w and topk_idx of logits [T, E], and
+    with ``losses`` also the losses fp32 [2] (balance, z) and the counts int32 [E].  The choice
+    is a constant, so the bias has no gradient.  A second derivative raises an error."""
+    return _RouteScores.apply(logits, rule, bias, losses)
+
+
+# ------------------------------------ 4-bit weights under 16-bit rows ----
+def _groups(group: int, K: int) -> int:
+    if group <= 0 or K > _MAX_DIM:
+        raise ValueError("expected a group of 32, 64 or 128 and at most 2^30 columns")
+    return -(-K // group)
+
+
+def moe_quantize_int4(group: int, x, codes, scales, zeros=None, stream=None) -> None:
+    """codes uint8 [rows, K / 2] and scales [rows, ceil(K / group)] (x's type) of the rows of x
+    (bf16 or fp16); with ``zeros`` uint8 [rows, ceil(K / group)] each group gets a zero point."""
+    dev, (rows, K) = _device(x), x.shape
+    px, ldx = _rows(x, "x", x.dtype, (rows, K), dev)
+    n = _groups(group, K)
+    _check((_lib or load()).moe_quantize_int4(
+        group, _dtype(x), rows, K, px, ldx, _arg(codes, "codes", torch.uint8, (rows, K // 2), dev),
+        _arg(scales, "scales", x.dtype, (rows, n), dev), _arg(zeros, "zeros", torch.uint8, (rows, n), dev),
+        _stream(stream, dev)))
+
+
+def moe_dequantize_int4(group: int, codes, scales, out, zeros=None, stream=None) -> None:
+    """out [rows, K] (bf16 or fp16, the scales' type) = the values of 4-bit rows."""
+    dev, (rows, K) = _device(out), out.shape
+    po, ldo = _rows(out, "out", out.dtype, (rows, K), dev)
+    n = _groups(group, K)
+    _check((_lib or load()).moe_dequantize_int4(
+        group, _dtype(out), rows, K, _arg(codes, "codes", torch.uint8, (rows, K // 2), dev),
+        _arg(scales, "scales", out.dtype, (rows, n), dev), _arg(zeros, "zeros", torch.uint8, (rows, n), dev),
+        po, ldo, _stream(stream, dev)))
+
+
+def moe_grouped_gemm_int4(group: int, x, w_codes, w_scales, offsets, y, w_zeros=None, src=None,
+                          src_div: int = 1, row_scale=None, swiglu: bool = False, status=None,
+                          stream=None) -> None:
+    """y[r] = row_scale[r] * x[src[r] // src_div] W[e]^T (x[r] without ``src``) for the rows of
+    every group: x [x_rows, K] and y [R, N] bf16 or fp16, w_codes uint8 [E, N, K / 2], w_scales
+    [E, N, ceil(K / group)] of x's type, w_zeros uint8 likewise.  With ``swiglu`` W has 2 N rows,
+    gate and up interleaved per 128, and y = silu(gate) * up * row_scale."""
+    dev, dtype, (x_rows, K), (R, N), E = _device(x), x.dtype, x.shape, y.shape, w_codes.shape[0]
+    px, ldx = _rows(x, "x", dtype, (x_rows, K), dev)
+    py, ldy = _rows(y, "y", dtype, (R, N), dev)
+    n, rows, u8, i32 = _groups(group, K), 2 * N if swiglu else N, torch.uint8, torch.int32
+    _check((_lib or load()).moe_grouped_gemm_int4(
+        group, _dtype(x), R, N, K, E, px, x_rows, ldx, _arg(src, "src", i32, (R,), dev), src_div,
+        _arg(w_codes, "w_codes", u8, (E, rows, K // 2), dev), _arg(w_scales, "w_scales", dtype, (E, rows, n), dev),
+        _arg(w_zeros, "w_zeros", u8, (E, rows, n), dev), _arg(offsets, "offsets", i32, (E + 1,), dev),
+        _arg(row_scale, "row_scale", torch.float32, (R,), dev), int(swiglu), py, ldy, _status(status, dev),
+        _stream(stream, dev)))
 
 
 def moe_get_device_status(ws, stream=None) -> int:

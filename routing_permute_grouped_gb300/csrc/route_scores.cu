@@ -1,0 +1,888 @@
+// route_scores.cu -- from a token's router scores to its k experts, and back.
+//
+//   s    softmax of the token's logits over all experts, or their sigmoids
+//   key  s + bias[e]; without a bias the experts keep the order of the logits
+//   choice  the groups of experts with the best scores stay (a group's score is
+//        its largest key or the sum of its two largest), and of their experts
+//        the k with the largest keys, ties to the lower index
+//   w_j  scale * s_j, divided by the sum over the chosen if renormalised
+//   losses  balance = E / (k T) sum_e count_e mean_t p[t, e] with p the scores
+//        divided by their sum, and z = mean_t (log sum_e exp(logit))^2
+//
+// One warp takes a token; lane l holds the V = 1, 2, 4 or 8 experts from l V on,
+// so that a token is read with vector loads and the lower lane has the lower
+// index.  The largest key of a warp is one redux.sync on keys mapped to unsigned
+// integers of the same order.
+//
+// The choice is that of exact keys.  Those of fp32 are off by a few units of the
+// last place, so where two that matter (neighbours among the k + 1 largest, the
+// last kept group and the first dropped) are closer than their error allows, the
+// token is chosen again with keys of fp64.  Experts of the same logit and the
+// same bias have the same key in either and need no second look.
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <cmath>
+
+#include "../../include/moe.h"
+#include "internal.h"
+#include "ragged.cuh"
+
+namespace moe {
+
+#define set_last_error(status, ...) static_cast<moe_status_t>(record_error(status, __VA_ARGS__))
+
+namespace {
+
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr int kMaxChoices = 8;
+constexpr int kWarps = 8;          // per block
+constexpr int kLossWarps = 16;     // per block where loads and losses are summed
+constexpr int kLossBlocks = 320;   // at most
+constexpr int kLossColumns = 8;    // experts per block of the second kernel
+
+struct ScoreArgs {
+    const void* logits;
+    int64_t ld, T;
+    int32_t E, k, n_groups, topk_groups, group_top;
+    int32_t sigmoid, renormalize;
+    float scale;
+    int32_t wide;         // rows of logits may be read V elements at a time
+    const float* bias;    // [E] or null
+    int32_t* idx;         // [T, k]
+    float* w;             // [T, k]
+    // loads and losses
+    float* share;         // [blocks, E] sums of p
+    int32_t* load;        // [blocks, E]
+    float* z;             // [blocks]
+    uint32_t* ticket;     // [1], cleared by the first kernel
+    float* part;          // [E / 8] balance sums of the second kernel's blocks
+    int32_t* counts;      // [E]
+    float* losses;        // [2]
+    int32_t blocks;
+    // gradient
+    const float* dw;      // [T, k] or null
+    const float* dlosses; // [2] or null
+    void* dlogits;
+    int64_t ldd;
+    int32_t wide_out;
+};
+
+
+// ------------------------------------------------------------------- keys --
+// Unsigned integers in the order of the keys: 0 for what may not be chosen, 1
+// for -infinity (chosen only when nothing else is left), then the numbers.
+constexpr uint32_t kDead = 1;
+__device__ __forceinline__ uint32_t key_of(float f) {
+    const uint32_t b = __float_as_uint(f + 0.0f);  // -0 and 0 are one key
+    return f > -INFINITY ? (b >> 31 ? ~b : b | 0x80000000u) : kDead;
+}
+__device__ __forceinline__ uint64_t key_of(double f) {
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(f + 0.0));
+    return f > -INFINITY ? (b >> 63 ? ~b : b | 0x8000000000000000ull) : kDead;
+}
+__device__ __forceinline__ float number_of(uint32_t u) {
+    return __uint_as_float(u >> 31 ? u ^ 0x80000000u : ~u);
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kAll, v); }
+__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
+    const uint32_t hi = __reduce_max_sync(kAll, static_cast<uint32_t>(v >> 32));
+    const uint32_t lo = __reduce_max_sync(kAll, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+    return static_cast<uint64_t>(hi) << 32 | lo;
+}
+__device__ __forceinline__ float warp_maxf(float v) {  // -infinity for a warp without numbers
+    const uint32_t u = warp_max(key_of(v));
+    return u == kDead ? -INFINITY : number_of(u);
+}
+template <typename F>
+__device__ __forceinline__ F warp_sum(F v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+__device__ __forceinline__ float sum8(float v) {  // of lanes 0 .. 7, in them
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+
+// ---------------------------------------------------------------- logits --
+template <typename T>
+__device__ __forceinline__ float as_float(T v) { return to_float<T>(v); }
+template <>
+__device__ __forceinline__ float as_float(float v) { return v; }
+
+template <int BYTES>
+__device__ __forceinline__ void load_bytes(const void* p, uint32_t (&r)[(BYTES + 3) / 4]) {
+    if constexpr (BYTES == 32) {
+        asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "l"(p)
+                     : "memory");
+    } else if constexpr (BYTES == 16) {
+        const uint4 v = ld_dep(static_cast<const uint4*>(p));
+        r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+    } else if constexpr (BYTES == 8) {
+        const uint2 v = ld_dep(static_cast<const uint2*>(p));
+        r[0] = v.x, r[1] = v.y;
+    } else if constexpr (BYTES == 4) {
+        r[0] = ld_dep(static_cast<const uint32_t*>(p));
+    } else {
+        r[0] = ld_dep(static_cast<const uint16_t*>(p));
+    }
+}
+template <int BYTES>
+__device__ __forceinline__ void store_bytes(void* p, const uint32_t (&r)[(BYTES + 3) / 4]) {
+    if constexpr (BYTES == 32) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                     "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    } else if constexpr (BYTES == 16) {
+        *static_cast<uint4*>(p) = make_uint4(r[0], r[1], r[2], r[3]);
+    } else if constexpr (BYTES == 8) {
+        *static_cast<uint2*>(p) = make_uint2(r[0], r[1]);
+    } else if constexpr (BYTES == 4) {
+        *static_cast<uint32_t*>(p) = r[0];
+    } else {
+        *static_cast<uint16_t*>(p) = static_cast<uint16_t>(r[0]);
+    }
+}
+
+// The lane's V logits of token t: -infinity for NaN, for -infinity and past E,
+// +infinity as the largest finite number.
+template <typename T, int V>
+__device__ __forceinline__ void load_logits(const ScoreArgs& a, int64_t t, int lane, float (&l)[V], bool wide) {
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld + lane * V;
+    T v[V];
+    if (wide) {
+        uint32_t r[(V * sizeof(T) + 3) / 4];
+        if (lane * V < a.E) {
+            load_bytes<V * sizeof(T)>(row, r);
+            memcpy(v, r, sizeof v);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (lane * V + i < a.E) v[i] = ld_dep(row + i);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float f = lane * V + i < a.E ? as_float<T>(v[i]) : -INFINITY;
+        l[i] = f > -INFINITY ? fminf(f, FLT_MAX) : -INFINITY;
+    }
+}
+// Biases as keys take them: NaN as -infinity, +infinity as the largest number.
+__device__ __forceinline__ float tame(float b) { return b > -INFINITY ? fminf(b, FLT_MAX) : -INFINITY; }
+
+// Value i of the lane that has expert e = lane * V + i, in a lane that asks for e.
+template <int V>
+__device__ __forceinline__ float value_of(const float (&l)[V], int e) {
+    float r = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float v = __shfl_sync(kAll, l[i], e / V);
+        r = e % V == i ? v : r;
+    }
+    return r;
+}
+
+// ---------------------------------------------------------------- choice --
+// Which groups stay, as a bit mask, from the experts' keys; *close: the last kept
+// score and the first dropped are within tol of one another.  buf holds a warp's
+// 32 V keys.
+template <int V, typename F>
+__device__ __forceinline__ uint32_t kept_groups(const ScoreArgs& a, int gsz, int lane, const F (&key)[V], F* buf, F tol,
+                                                bool* close) {
+    F b1 = -INFINITY, b2 = -INFINITY;  // of group `lane`
+    const int q = gsz / V;
+    if (q > 0 && q * V == gsz && (q & (q - 1)) == 0) {  // a group is q whole lanes
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            b2 = max(b2, min(b1, key[i]));
+            b1 = max(b1, key[i]);
+        }
+        for (int o = 1; o < q; o <<= 1) {
+            const F o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
+            b2 = max(min(b1, o1), max(b2, o2));
+            b1 = max(b1, o1);
+        }
+        b1 = __shfl_sync(kAll, b1, lane * q);  // past the last group: unused
+        b2 = __shfl_sync(kAll, b2, lane * q);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) buf[lane * V + i] = key[i];
+        __syncwarp();
+        if (lane < a.n_groups)
+            for (int e = lane * gsz; e < (lane + 1) * gsz; ++e) {
+                b2 = max(b2, min(b1, buf[e]));
+                b1 = max(b1, buf[e]);
+            }
+        __syncwarp();
+    }
+    const F score = a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+    auto u = lane < a.n_groups ? key_of(score) : 0;
+    uint32_t kept = 0;
+    F last = 0, first = 0;
+    bool both = true;
+    for (int r = 0; r <= a.topk_groups; ++r) {
+        const auto m = warp_max(u);
+        const uint32_t at = __ballot_sync(kAll, u == m);
+        const int g = __ffs(at) - 1;
+        if (r + 1 >= a.topk_groups) {  // the last kept, the first dropped
+            both = both && m > kDead;
+            const F s = __shfl_sync(kAll, score, g);
+            if (r < a.topk_groups)
+                last = s;
+            else
+                first = s;
+        }
+        if (r < a.topk_groups) {
+            kept |= 1u << g;
+            if (lane == g) u = 0;
+        }
+    }
+    *close = both && last - first <= tol;
+    return kept;
+}
+
+// The k + 1 largest keys of the experts that may be chosen: lane r gets the r-th
+// and its expert (key 0 where there is none).
+template <int V, typename U>
+__device__ __forceinline__ void largest(int k, int lane, U (&u)[V], U& my_key, int& my_expert) {
+    my_key = 0;
+    my_expert = 0;
+    for (int r = 0; r <= k; ++r) {
+        U best = 0;
+        int slot = 0;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+            if (u[i] >= best) {
+                best = u[i];
+                slot = i;
+            }
+        const U m = warp_max(best);
+        const int owner = __ffs(__ballot_sync(kAll, best == m)) - 1;
+        const int e = __shfl_sync(kAll, slot, owner) + owner * V;
+        if (lane == r) {
+            my_key = m;
+            my_expert = e;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (lane == owner && slot == i) u[i] = 0;
+    }
+}
+
+// Whether two experts have equal keys in any precision.
+__device__ __forceinline__ bool same_key(const ScoreArgs& a, float l0, int e0, float l1, int e1) {
+    return l0 == l1 && (!a.bias || tame(ld_dep(a.bias + e0)) == tame(ld_dep(a.bias + e1)));
+}
+
+// The choice of token t with keys of fp64; lane r gets the r-th expert.
+template <typename T, int V>
+__device__ __noinline__ int choose_exact(const ScoreArgs& a, int64_t t, double* buf) {
+    const int lane = threadIdx.x & 31;
+    float l[V];
+    load_logits<T, V>(a, t, lane, l, false);
+    double key[V], pick[V];
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
+    top = warp_maxf(top);
+    double sum = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const double x = l[i];
+        key[i] = !(l[i] > -INFINITY) ? 0.0 : a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top);
+        sum += key[i];
+    }
+    sum = warp_sum(sum);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = lane * V + i;
+        if (!a.sigmoid) key[i] /= sum;
+        if (a.bias && e < a.E) key[i] += static_cast<double>(tame(ld_dep(a.bias + e)));
+        if (!(l[i] > -INFINITY)) key[i] = -INFINITY;
+        pick[i] = a.bias ? key[i] : static_cast<double>(l[i]);
+    }
+    uint32_t kept = kAll;
+    const int gsz = a.n_groups ? a.E / a.n_groups : a.E;
+    if (a.n_groups) {
+        bool close;
+        if (a.group_top == 1)
+            kept = kept_groups<V, double>(a, gsz, lane, pick, buf, 0.0, &close);
+        else
+            kept = kept_groups<V, double>(a, gsz, lane, key, buf, 0.0, &close);
+    }
+    uint64_t u[V], my_key;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = lane * V + i;
+        u[i] = e < a.E && (kept >> (e / gsz) & 1u) ? key_of(pick[i]) : 0;
+    }
+    int expert;
+    largest<V, uint64_t>(a.k, lane, u, my_key, expert);
+    return expert;
+}
+
+// 1 / (1 + exp(-x)) = pos or neg by the sign, from e = exp(-|x|): the score and
+// one minus the score without cancellation.
+struct Sigmoid {
+    float s, rest;
+};
+__device__ __forceinline__ Sigmoid sigmoid(float x) {
+    const float e = expf(-fabsf(x)), d = 1.0f / (1.0f + e), ed = e * d;
+    return x >= 0.0f ? Sigmoid{d, ed} : Sigmoid{ed, d};
+}
+// Scores of one token over their sum: sigmoids times exp(-m), m = min(0, largest
+// logit), so that none of a token's underflow together.
+__device__ __forceinline__ float shifted_sigmoid(float x, float m) {
+    if (!(x > -INFINITY)) return 0.0f;
+    return x >= 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x - m) / (1.0f + expf(x));
+}
+// The part of expert j (lanes j < k; lx its logit, -infinity where it has none) in
+// the scores of the chosen.
+__device__ __forceinline__ float chosen_share(const ScoreArgs& a, int lane, float lx) {
+    const float top = warp_maxf(lane < a.k ? lx : -INFINITY);
+    float v = 0.0f;
+    if (lane < a.k && lx > -INFINITY) v = a.sigmoid ? shifted_sigmoid(lx, fminf(top, 0.0f)) : expf(lx - top);
+    const float sum = sum8(v);
+    return v > 0.0f ? v / sum : 0.0f;
+}
+
+template <typename T, int V, bool LOSS>
+__global__ void __launch_bounds__(32 * (LOSS ? kLossWarps : kWarps)) k_route_scores(const __grid_constant__ ScoreArgs a) {
+    constexpr int W = LOSS ? kLossWarps : kWarps;
+    __shared__ double s_buf[W][32 * V];
+    __shared__ int s_load[LOSS ? 32 * V : 1];
+    pdl_trigger();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int gsz = a.n_groups ? a.E / a.n_groups : a.E;
+    const bool grouped = a.n_groups > 0;
+    const bool by_score = a.bias || (grouped && a.group_top == 2);  // keys need scores
+    const bool all = LOSS || by_score || (!a.sigmoid && !a.renormalize);
+    float bias[V], share[LOSS ? V : 1], z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        bias[i] = a.bias && lane * V + i < a.E ? tame(ld_dep(a.bias + lane * V + i)) : 0.0f;
+        if constexpr (LOSS) share[i] = 0.0f;
+    }
+    if constexpr (LOSS) {
+        for (int e = threadIdx.x; e < 32 * V; e += 32 * W) s_load[e] = 0;
+        if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+        __syncthreads();
+    }
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * W + warp; t < a.T; t += static_cast<int64_t>(gridDim.x) * W) {
+        float l[V];
+        load_logits<T, V>(a, t, lane, l, a.wide);
+        float s[V], top = -INFINITY, inv = 0.0f, scores_top = 1.0f;
+        if (all) {
+            if (!a.sigmoid || LOSS) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
+                top = warp_maxf(top);
+            }
+            if (!a.sigmoid || LOSS) {  // softmax, and the z loss of either
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    s[i] = l[i] > -INFINITY ? expf(l[i] - top) : 0.0f;
+                    sum += s[i];
+                }
+                sum = warp_sum(sum);
+                inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+                if (sum > 0.0f) {
+                    const float lse = top + logf(sum);
+                    z = fmaf(lse, lse, z);
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) s[i] *= inv;
+                scores_top = inv;
+            }
+            if constexpr (LOSS) {
+                if (!a.sigmoid) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) share[i] += s[i];
+                } else {
+                    const float m = fminf(top, 0.0f);
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        s[i] = shifted_sigmoid(l[i], m);
+                        sum += s[i];
+                    }
+                    sum = warp_sum(sum);
+                    const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) share[i] = fmaf(s[i], f, share[i]);
+                }
+            }
+            if (a.sigmoid && by_score) {
+                scores_top = 1.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) s[i] = sigmoid(l[i]).s;
+            }
+        }
+        // keys: with a bias or a group's two best they are scores, else logits
+        float key[V];
+        const bool biased = a.bias != nullptr;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            key[i] = by_score ? s[i] + bias[i] : l[i];
+            if (!(l[i] > -INFINITY)) key[i] = -INFINITY;
+        }
+        // twice what the fp32 keys of two experts may be off by: a score by 24
+        // roundings of the largest score (exp, the sum, the division), the sum
+        // with the bias by one of its own
+        const float off = 0x1p-18f * scores_top;
+        bool close = false;
+        uint32_t kept = kAll;
+        if (grouped) {
+            float most = 0.0f;
+            if (by_score) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) most = fmaxf(most, key[i] > -INFINITY ? fabsf(key[i]) : 0.0f);
+                most = warp_maxf(most);
+            }
+            bool near_;
+            kept = kept_groups<V, float>(a, gsz, lane, key, reinterpret_cast<float*>(s_buf[warp]),
+                                         2.0f * off + 0x1p-20f * most, &near_);
+            close = by_score && near_;
+        }
+        uint32_t u[V], my_key;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane * V + i;
+            const bool may = e < a.E && (!grouped || (kept >> (e / gsz) & 1u));
+            u[i] = may ? key_of(biased ? key[i] : l[i]) : 0;
+        }
+        int expert;
+        largest<V, uint32_t>(a.k, lane, u, my_key, expert);
+        if (biased) {
+            const uint32_t next_key = __shfl_down_sync(kAll, my_key, 1);
+            const float f0 = number_of(my_key), f1 = number_of(next_key);
+            const bool near_ = lane < a.k && next_key > kDead && f0 - f1 <= off + 0x1p-22f * fmaxf(fabsf(f0), fabsf(f1));
+            if (__any_sync(kAll, near_)) {
+                const float lx = value_of<V>(l, expert);
+                const float ly = __shfl_down_sync(kAll, lx, 1);
+                const int ey = __shfl_down_sync(kAll, expert, 1);
+                close |= __any_sync(kAll, near_ && !same_key(a, lx, expert, ly, ey));
+            }
+        }
+        if (close) expert = choose_exact<T, V>(a, t, s_buf[warp]);
+        const float lx = value_of<V>(l, expert);
+        float w;
+        if (a.renormalize) {
+            w = chosen_share(a, lane, lx);
+        } else {
+            w = !(lx > -INFINITY) ? 0.0f : a.sigmoid ? sigmoid(lx).s : expf(lx - top) * inv;
+        }
+        if (lane < a.k) {
+            a.idx[t * a.k + lane] = expert;
+            a.w[t * a.k + lane] = w * a.scale;
+            if constexpr (LOSS) atomicAdd(&s_load[expert], 1);
+        }
+    }
+    if constexpr (LOSS) {
+        // the block's sums, its warps' in their order
+        float* part = reinterpret_cast<float*>(s_buf[warp]);
+        float* zs = reinterpret_cast<float*>(s_buf[0]) + 32 * V;  // past the first warp's sums, in its own buffer
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V; ++i) part[lane * V + i] = share[i];
+        if (lane == 0) zs[warp] = z;
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.E; e += 32 * W) {
+            float sum = 0.0f;
+            for (int j = 0; j < W; ++j) sum += reinterpret_cast<const float*>(s_buf[j])[e];
+            a.share[static_cast<int64_t>(blockIdx.x) * a.E + e] = sum;
+            a.load[static_cast<int64_t>(blockIdx.x) * a.E + e] = s_load[e];
+        }
+        if (threadIdx.x == 0) {
+            float sum = 0.0f;
+            for (int j = 0; j < W; ++j) sum += zs[j];
+            a.z[blockIdx.x] = sum;
+        }
+    }
+}
+
+// The blocks' sums to the loads and losses.  A block takes eight experts; the one
+// that ends last adds up what the others left, in their order.
+__global__ void __launch_bounds__(256) k_route_losses(const __grid_constant__ ScoreArgs a) {
+    __shared__ float s_share[32][kLossColumns];
+    __shared__ int s_load[32][kLossColumns];
+    __shared__ float s_sum[8];
+    __shared__ bool s_last;
+    pdl_trigger();
+    pdl_wait();
+    const int c = threadIdx.x % kLossColumns, r = threadIdx.x / kLossColumns, e = blockIdx.x * kLossColumns + c;
+    float share = 0.0f;
+    int load = 0;
+    if (e < a.E)
+        for (int b = r; b < a.blocks; b += 32) {
+            share += ld_dep(a.share + static_cast<int64_t>(b) * a.E + e);
+            load += ld_dep(a.load + static_cast<int64_t>(b) * a.E + e);
+        }
+    s_share[r][c] = share;
+    s_load[r][c] = load;
+    __syncthreads();
+    if (threadIdx.x < kLossColumns) {
+        share = 0.0f;
+        load = 0;
+        for (int i = 0; i < 32; ++i) {
+            share += s_share[i][c];
+            load += s_load[i][c];
+        }
+        if (e < a.E) a.counts[e] = load;
+        // count / (k T) times the mean share
+        float v = e < a.E ? static_cast<float>(load) / (static_cast<float>(a.k) * static_cast<float>(a.T)) * share : 0.0f;
+#pragma unroll
+        for (int o = kLossColumns / 2; o > 0; o >>= 1) v += __shfl_xor_sync((1u << kLossColumns) - 1, v, o);
+        if (threadIdx.x == 0) {
+            a.part[blockIdx.x] = v;
+            __threadfence();
+            s_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+        }
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    float z = 0.0f;
+    for (int b = threadIdx.x; b < a.blocks; b += 256) z += ld_dep(a.z + b);
+    z = warp_sum(z);
+    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = z;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float balance = 0.0f;
+        for (int b = 0; b < static_cast<int>(gridDim.x); ++b) balance += ld_dep(a.part + b);
+        z = 0.0f;
+        for (int i = 0; i < 8; ++i) z += s_sum[i];
+        const float T = static_cast<float>(a.T);
+        a.losses[0] = balance * static_cast<float>(a.E) / T;
+        a.losses[1] = z / T;
+    }
+}
+
+// -------------------------------------------------------------- gradient --
+// With r the chosen experts' parts of the sum of their scores, d the mean of dw
+// under r, p the softmax and D = scale sum_j p_j dw_j:
+//   renormalised     dlogit_j  = scale r_j (dw_j - d), times 1 - s_j for sigmoids
+//   softmax          dlogit_e  = p_e (scale dw_e - D)
+//   sigmoid          dlogit_j  = scale dw_j s_j (1 - s_j)
+//   balance          dlogit_e += p_e (c_e - sum p c), times 1 - s_e for sigmoids,
+//                    c_e = dbalance E count_e / (k T^2), p the scores over their sum
+//   z                dlogit_e += dz (2 / T) lse softmax_e
+template <typename T, int V, bool LOSS>
+__global__ void __launch_bounds__(32 * kWarps) k_route_scores_bwd(const __grid_constant__ ScoreArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float c[LOSS ? V : 1], dz = 0.0f;
+    if constexpr (LOSS) {
+        const double per = static_cast<double>(a.E) / (static_cast<double>(a.k) * static_cast<double>(a.T) * a.T);
+        const float f = static_cast<float>(per) * ld_dep(a.dlosses);
+        dz = ld_dep(a.dlosses + 1) * 2.0f / static_cast<float>(a.T);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            c[i] = lane * V + i < a.E ? f * static_cast<float>(ld_dep(a.counts + lane * V + i)) : 0.0f;
+    }
+    const bool soft = LOSS || (!a.sigmoid && !a.renormalize);
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < a.T;
+         t += static_cast<int64_t>(gridDim.x) * kWarps) {
+        float l[V], g[V];
+        int expert = -1;
+        float dw = 0.0f;
+        if (a.dw && lane < a.k) {
+            expert = ld_dep(a.idx + t * a.k + lane);
+            dw = ld_dep(a.dw + t * a.k + lane);
+        }
+        load_logits<T, V>(a, t, lane, l, a.wide);
+        const bool known = expert >= 0 && expert < a.E;
+        expert = known ? expert : 0;
+        float lx = value_of<V>(l, expert);
+        lx = known ? lx : -INFINITY;
+        dw = lx > -INFINITY ? dw : 0.0f;  // a masked expert has no weight
+        float top = -INFINITY, inv = 0.0f, lse = 0.0f, p[V];
+        if (soft) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
+            top = warp_maxf(top);
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                p[i] = l[i] > -INFINITY ? expf(l[i] - top) : 0.0f;
+                sum += p[i];
+            }
+            sum = warp_sum(sum);
+            inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+            lse = sum > 0.0f ? top + logf(sum) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) p[i] *= inv;
+        }
+        // what goes to the chosen experts alone, and to all by their softmax
+        float mine, all = 0.0f;
+        if (a.renormalize) {
+            const float r = chosen_share(a, lane, lx);
+            const float mean = sum8(r * dw);
+            mine = a.scale * r * (dw - mean);
+            if (a.sigmoid) mine *= sigmoid(lx).rest;
+        } else if (a.sigmoid) {
+            const Sigmoid s = sigmoid(lx);
+            mine = a.scale * dw * s.s * s.rest;
+        } else {
+            mine = lx > -INFINITY ? a.scale * dw * (expf(lx - top) * inv) : 0.0f;
+            all = -__shfl_sync(kAll, sum8(mine), 0);
+        }
+        if constexpr (LOSS) {
+            all = fmaf(dz, lse, all);
+            if (!a.sigmoid) {
+                float mean = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) mean = fmaf(p[i], c[i], mean);
+                mean = warp_sum(mean);
+#pragma unroll
+                for (int i = 0; i < V; ++i) g[i] = p[i] * (c[i] - mean + all);
+            } else {
+                const float m = fminf(top, 0.0f);
+                float s[V], sum = 0.0f, mean = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    s[i] = shifted_sigmoid(l[i], m);
+                    sum += s[i];
+                    mean = fmaf(s[i], c[i], mean);
+                }
+                sum = warp_sum(sum);
+                mean = warp_sum(mean);
+                const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
+                mean *= f;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    g[i] = fmaf(s[i] * f * sigmoid(l[i]).rest, c[i] - mean, p[i] * all);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) g[i] = soft ? p[i] * all : 0.0f;
+        }
+        for (int j = 0; j < a.k; ++j) {
+            const int e = __shfl_sync(kAll, expert, j);
+            const float v = __shfl_sync(kAll, mine, j);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (e == lane * V + i) g[i] += v;
+        }
+        T* row = static_cast<T*>(a.dlogits) + t * a.ldd + lane * V;
+        T o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if constexpr (sizeof(T) == 4)
+                o[i] = g[i];
+            else
+                o[i] = from_float<T>(g[i]);
+        }
+        if (a.wide_out) {
+            if (lane * V < a.E) {
+                uint32_t r[(V * sizeof(T) + 3) / 4];
+                memcpy(r, o, sizeof o);
+                store_bytes<V * sizeof(T)>(row, r);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (lane * V + i < a.E) row[i] = o[i];
+        }
+    }
+}
+
+// ------------------------------------------------------------------ calls --
+int elem_bytes(int32_t dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+int per_lane(int E) { return E > 128 ? 8 : E > 64 ? 4 : E > 32 ? 2 : 1; }
+
+moe_status_t check_rule(const moe_score_rule_t* r) {
+    if (!r) return set_last_error(MOE_ERR_INVALID_ARG, "rule is NULL");
+    if (r->E <= 0 || r->k <= 0) return set_last_error(MOE_ERR_INVALID_ARG, "E and k must be > 0");
+    if (r->E > 256) return set_last_error(MOE_ERR_UNSUPPORTED, "E = %d > 256", r->E);
+    if (r->k > kMaxChoices) return set_last_error(MOE_ERR_UNSUPPORTED, "k = %d > 8", r->k);
+    if (r->k > r->E) return set_last_error(MOE_ERR_INVALID_ARG, "k = %d > E = %d", r->k, r->E);
+    if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID)
+        return set_last_error(MOE_ERR_INVALID_ARG, "score = %d is neither softmax (0) nor sigmoid (1)", r->score);
+    if (!std::isfinite(r->scale)) return set_last_error(MOE_ERR_INVALID_ARG, "scale is not finite");
+    if (r->n_groups < 0) return set_last_error(MOE_ERR_INVALID_ARG, "n_groups < 0");
+    if (r->n_groups > 0) {
+        if (r->n_groups > 32 || r->E % r->n_groups)
+            return set_last_error(MOE_ERR_INVALID_ARG, "n_groups = %d must divide E and be <= 32", r->n_groups);
+        if (r->topk_groups <= 0 || r->topk_groups > r->n_groups)
+            return set_last_error(MOE_ERR_INVALID_ARG, "topk_groups = %d outside [1, n_groups]", r->topk_groups);
+        if (r->topk_groups * (r->E / r->n_groups) < r->k)
+            return set_last_error(MOE_ERR_INVALID_ARG, "topk_groups * (E / n_groups) < k");
+        if (r->group_top != 1 && r->group_top != 2)
+            return set_last_error(MOE_ERR_INVALID_ARG, "group_top = %d is neither 1 nor 2", r->group_top);
+    }
+    return MOE_OK;
+}
+
+moe_status_t check_tokens(const moe_score_rule_t* r, int32_t dtype, int64_t T) {
+    const moe_status_t s = check_rule(r);
+    if (s != MOE_OK) return s;
+    if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F16 && dtype != MOE_DTYPE_F32)
+        return set_last_error(MOE_ERR_INVALID_ARG, "dtype = %d is none of bf16 (0), f16 (1), f32 (2)", dtype);
+    if (T < 0) return set_last_error(MOE_ERR_INVALID_ARG, "T < 0");
+    if (T * r->k > (1ll << 30) || T > (1ll << 30))
+        return set_last_error(MOE_ERR_UNSUPPORTED, "T*k too large for 32-bit row indices");
+    return MOE_OK;
+}
+
+bool aligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+moe_status_t check_rows(const void* p, int64_t ld, int32_t dtype, const moe_score_rule_t* r) {
+    if (!aligned(p, elem_bytes(dtype)))
+        return set_last_error(MOE_ERR_INVALID_ARG, "logits and dlogits must be aligned to their elements");
+    if (ld < r->E) return set_last_error(MOE_ERR_INVALID_ARG, "the row stride must cover the row");
+    return MOE_OK;
+}
+
+// Rows that can be read V elements at a time
+bool wide_rows(const void* p, int64_t ld, int32_t dtype, int E) {
+    const int V = per_lane(E), bytes = V * elem_bytes(dtype);
+    return E % V == 0 && aligned(p, bytes) && ld % V == 0;
+}
+
+ScoreArgs args_of(const moe_score_rule_t* r, int64_t T) {
+    ScoreArgs a{};
+    a.T = T;
+    a.E = r->E;
+    a.k = r->k;
+    a.n_groups = r->n_groups;
+    a.topk_groups = r->topk_groups;
+    a.group_top = r->group_top;
+    a.sigmoid = r->score == MOE_SCORE_SIGMOID;
+    a.renormalize = r->renormalize != 0;
+    a.scale = r->scale;
+    return a;
+}
+
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+
+// Blocks of the first kernel where loads and losses are summed: two per SM, and at
+// most as many as the workspace, whose size no GPU decides, holds sums of
+int most_blocks(int64_t T) {
+    const int64_t need = (T + kLossWarps - 1) / kLossWarps;
+    return static_cast<int>(need < kLossBlocks ? need : kLossBlocks);
+}
+int loss_blocks(int64_t T) {
+    const int most = most_blocks(T);
+    return 2 * num_sms() < most ? 2 * num_sms() : most;
+}
+
+template <typename F>
+cudaError_t by_type(int32_t dtype, int E, F&& go) {
+    auto lanes = [&](auto t) {
+        switch (per_lane(E)) {
+            case 1: return go(t, std::integral_constant<int, 1>());
+            case 2: return go(t, std::integral_constant<int, 2>());
+            case 4: return go(t, std::integral_constant<int, 4>());
+            default: return go(t, std::integral_constant<int, 8>());
+        }
+    };
+    if (dtype == MOE_DTYPE_F32) return lanes(float());
+    return dtype == MOE_DTYPE_BF16 ? lanes(__nv_bfloat16()) : lanes(__half());
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_route_scores_workspace_size(const moe_score_rule_t* rule, int64_t T) {
+    if (check_tokens(rule, MOE_DTYPE_F32, T) != MOE_OK) return 0;
+    const size_t blocks = most_blocks(T);
+    return 2 * up(blocks * rule->E * 4) + up(blocks * 4) + 256;
+}
+
+extern "C" moe_status_t moe_route_scores(const moe_score_rule_t* rule, int32_t dtype, int64_t T, const void* logits,
+                                         int64_t ld, const float* bias, int32_t* topk_idx, float* topk_w,
+                                         int32_t* counts, float* losses, void* ws, size_t ws_bytes, void* stream) {
+    moe_status_t s = check_tokens(rule, dtype, T);
+    if (s != MOE_OK) return s;
+    if (!counts != !losses) return set_last_error(MOE_ERR_INVALID_ARG, "counts and losses come together");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (T == 0) {
+        if (counts) {
+            e = cudaMemsetAsync(counts, 0, static_cast<size_t>(rule->E) * 4, st);
+            if (e == cudaSuccess) e = cudaMemsetAsync(losses, 0, 8, st);
+        }
+        return e == cudaSuccess ? MOE_OK : set_last_error(MOE_ERR_CUDA, "routing by scores: %s", cudaGetErrorString(e));
+    }
+    if (!logits || !topk_idx || !topk_w) return set_last_error(MOE_ERR_INVALID_ARG, "null pointer");
+    s = check_rows(logits, ld, dtype, rule);
+    if (s != MOE_OK) return s;
+    ScoreArgs a = args_of(rule, T);
+    a.logits = logits;
+    a.ld = ld;
+    a.wide = wide_rows(logits, ld, dtype, rule->E);
+    a.bias = bias;
+    a.idx = topk_idx;
+    a.w = topk_w;
+    if (counts) {
+        const size_t need = moe_route_scores_workspace_size(rule, T);
+        if (!ws || ws_bytes < need || !aligned(ws, 16))
+            return set_last_error(MOE_ERR_WORKSPACE, "loads and losses need a 16-byte aligned workspace of %zu bytes", need);
+        char* at = static_cast<char*>(ws);
+        const size_t blocks = most_blocks(T), sums = up(blocks * rule->E * 4);
+        a.share = reinterpret_cast<float*>(at);
+        a.load = reinterpret_cast<int32_t*>(at + sums);
+        a.z = reinterpret_cast<float*>(at + 2 * sums);
+        a.part = reinterpret_cast<float*>(at + 2 * sums + up(blocks * 4));
+        a.ticket = reinterpret_cast<uint32_t*>(a.part + 32);
+        a.counts = counts;
+        a.losses = losses;
+        a.blocks = loss_blocks(T);
+    }
+    e = by_type(dtype, rule->E, [&](auto t, auto v) {
+        using E_ = decltype(t);
+        constexpr int V = decltype(v)::value;
+        if (counts)
+            return launch_pdl(k_route_scores<E_, V, true>, dim3(a.blocks), dim3(32 * kLossWarps), 0, st, a);
+        const int64_t need = (T + kWarps - 1) / kWarps, most = 16ll * num_sms();
+        return launch_pdl(k_route_scores<E_, V, false>, dim3(static_cast<unsigned>(need < most ? need : most)),
+                          dim3(32 * kWarps), 0, st, a);
+    });
+    if (e == cudaSuccess && counts)
+        e = launch_pdl(k_route_losses, dim3((rule->E + kLossColumns - 1) / kLossColumns), dim3(256), 0, st, a);
+    return e == cudaSuccess ? MOE_OK : set_last_error(MOE_ERR_CUDA, "routing by scores: %s", cudaGetErrorString(e));
+}
+
+extern "C" moe_status_t moe_route_scores_bwd(const moe_score_rule_t* rule, int32_t dtype, int64_t T, const void* logits,
+                                             int64_t ld, const int32_t* topk_idx, const float* dw, const int32_t* counts,
+                                             const float* dlosses, void* dlogits, int64_t ldd, void* stream) {
+    moe_status_t s = check_tokens(rule, dtype, T);
+    if (s != MOE_OK) return s;
+    if (!counts != !dlosses) return set_last_error(MOE_ERR_INVALID_ARG, "counts and dlosses come together");
+    if (T == 0) return MOE_OK;
+    if (!logits || !dlogits || (dw && !topk_idx)) return set_last_error(MOE_ERR_INVALID_ARG, "null pointer");
+    s = check_rows(logits, ld, dtype, rule);
+    if (s == MOE_OK) s = check_rows(dlogits, ldd, dtype, rule);
+    if (s != MOE_OK) return s;
+    ScoreArgs a = args_of(rule, T);
+    a.logits = logits;
+    a.ld = ld;
+    a.wide = wide_rows(logits, ld, dtype, rule->E);
+    a.idx = const_cast<int32_t*>(topk_idx);
+    a.dw = dw;
+    a.counts = const_cast<int32_t*>(counts);
+    a.dlosses = dlosses;
+    a.dlogits = dlogits;
+    a.ldd = ldd;
+    a.wide_out = wide_rows(dlogits, ldd, dtype, rule->E);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int64_t need = (T + kWarps - 1) / kWarps, most = 16ll * num_sms();
+    const dim3 grid(static_cast<unsigned>(need < most ? need : most));
+    const cudaError_t e = by_type(dtype, rule->E, [&](auto t, auto v) {
+        using E_ = decltype(t);
+        constexpr int V = decltype(v)::value;
+        return counts ? launch_pdl(k_route_scores_bwd<E_, V, true>, grid, dim3(32 * kWarps), 0, st, a)
+                      : launch_pdl(k_route_scores_bwd<E_, V, false>, grid, dim3(32 * kWarps), 0, st, a);
+    });
+    return e == cudaSuccess ? MOE_OK : set_last_error(MOE_ERR_CUDA, "gradient of the scores: %s", cudaGetErrorString(e));
+}
