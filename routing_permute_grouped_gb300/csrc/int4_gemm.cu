@@ -2,9 +2,30 @@
 //
 //   y[r] = row_scale[r] * x[src[r] / div] W[e]^T   for the rows r of group e
 // with W[e][n][k] = (code - zero) * scale, scale and zero per row n and group of
-// k.  code - zero is a small integer, exact in 16 bits, so a group's products
-// are summed as they are and scaled once, in fp32.
+// k.  code - zero is a small integer, exact in 16 bits, so the tensor cores sum a
+// group's products as they are, and each group's sum is scaled once, in fp32.
+//
+// The weights are the MMA's M side: 128 rows of W[e], widened in registers and
+// written to tensor memory, from where tcgen05.mma takes its A operand; the token
+// rows are its N side (16 to 64 of them, a multiple of 16), staged by TMA.  A work
+// item is such a panel of weight rows times a tile of token rows; the sum runs
+// over chunks of 128 elements.  One CTA of 16 warps per SM:
+//   warp 0       TMA of the codes (12 chunks of 8 KB in flight)
+//   warp 1       TMA of the token rows (gather4 where src picks them)
+//   warp 2       issues the MMAs
+//   warp 3       scales and zero points, a few chunks ahead, into shared memory
+//   warps 4-7    take a chunk's sums (one per group) out of tensor memory, scale
+//                and add them in registers, one weight row per thread; the epilogue
+//   warps 8-15   widen codes, the two halves taking the chunks in turn
+// A code becomes a 16-bit number by or-ing it into the mantissa of 128 (bf16) or
+// 1024 (f16), from which 128 + zero or 1024 + zero is then subtracted exactly.
+//
+// Few items and a long sum: the CTAs of a cluster split the sum; each hands its
+// part of every column to the CTA that stores it, which adds the parts in the
+// CTAs' order.
 #include <cuda_runtime.h>
+
+#include <cmath>
 
 #include "../../include/moe.h"
 #include "int4.h"
@@ -17,69 +38,737 @@ namespace moe {
 
 namespace {
 
-struct Int4Product {
-    RaggedArgs r;          // N: weight rows per group
-    const void* x;
-    int64_t ldx, x_rows;
-    const int32_t* src;    // [R] or null
-    int32_t src_div;
-    const uint32_t* codes; // [E, N, K / 8]
-    const void* scales;    // [E, N, groups]
-    const uint8_t* zeros;  // the same, or null
-    int32_t groups, shift; // groups per weight row, log2 of their words
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr int kChunk = 128;            // elements of the sum per step
+constexpr int kCodeBytes = 128 * 64;   // of a chunk of a panel
+constexpr int kCodeStages = 12;
+constexpr int kRowStages = 4;
+constexpr int kABufs = 4;              // widened chunks in tensor memory, 64 columns each
+constexpr int kParams = 8;             // chunks of scales and zero points in shared memory
+constexpr int kAhead = 4;              // of them loaded at once
+constexpr int kThreads = 512;
+constexpr int kMaxSplit = 8;           // CTAs of a cluster
+
+template <int G>
+struct Cfg {
+    static constexpr int parts = kChunk / G;             // groups of a chunk
+    static constexpr int TN = G == 32 ? 32 : 64;         // token rows of a tile, at most
+    static constexpr int d_cols = parts * TN;            // a chunk's sums
+    static constexpr int d_bufs = 256 / d_cols;
+    static constexpr uint32_t a_col = 256;               // the first widened chunk's column
+    static constexpr int row_stage = TN * 256;
+    static constexpr int param_bytes = parts * 128 * 3;  // scales, then zero points
+    static constexpr int join = TN * 512;                // fp32 parts of the columns this CTA stores
+    static constexpr int smem = 1024 + kCodeStages * kCodeBytes + kRowStages * row_stage + join + kParams * param_bytes +
+                                1024 + 4 * 260 * 4;
+    static_assert(smem <= 232448, "shared memory budget");
+    static_assert(kABufs * 64 + d_bufs * d_cols <= 512, "tensor memory budget");
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
+struct Int4Product {
+    RaggedArgs r;          // N: weight rows per group
+    int32_t x_rows;
+    int32_t columns;       // of y
+    int32_t swiglu;
+    const int32_t* src;    // [R] or null
+    int32_t src_div;
+    const void* scales;    // [E, N, groups]
+    const uint8_t* zeros;  // the same, or null
+    int32_t groups;        // per weight row
+    int32_t whole;         // scales and zero points of a chunk can be read at once
+};
+
+struct Bars {
+    uint64_t code_full[kCodeStages], code_empty[kCodeStages];
+    uint64_t row_full[kRowStages], row_empty[kRowStages];
+    uint64_t a_full[kABufs], a_empty[kABufs];
+    uint64_t d_full[4], d_empty[4];
+    uint64_t p_full[kParams], p_empty[kParams];
+    uint64_t join_full, join_free, drain;
+    uint32_t tmem, abort;
+};
+static_assert(sizeof(Bars) <= 1024, "barriers");
+
+// Rows [lo, hi) of every group, its token tiles' width and its first work item
+struct Lists {
+    int first[260], lo[260], hi[260], width[260];
+};
+
+struct Item {
+    int e, panel;
+    int row, rows;  // token rows
+};
+
+// All threads: thread e takes group e.  Where a group is bad, groups may overlap:
+// each then starts past the ends of those before it.
+template <int TN>
+__device__ __forceinline__ int build_lists(const RaggedArgs& a, Lists& s, int panels) {
+    __shared__ int sums[8];
+    const int e = threadIdx.x, lane = e & 31;
+    bool bad = false;
+    if (e < a.E) {
+        const int2 g = group_rows(a, e, &bad);
+        s.lo[e] = g.x;
+        s.hi[e] = g.y;
+    }
+    if (__syncthreads_or(bad)) {
+        if (e == 0)
+            for (int i = 0, end = 0; i < a.E; ++i) {
+                s.lo[i] = min(max(s.lo[i], end), s.hi[i]);
+                end = max(end, s.hi[i]);
+            }
+        __syncthreads();
+    }
+    int n = 0, x = 0;
+    if (e < 256) {
+        if (e < a.E) {
+            const int len = s.hi[e] - s.lo[e], tiles = (len + TN - 1) / TN;
+            s.width[e] = tiles ? ((len + tiles - 1) / tiles + 15) & ~15 : 16;
+            n = tiles * panels;
+        }
+        x = n;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kAll, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) sums[e >> 5] = x;
+    }
+    __syncthreads();
+    int total = 0, before = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (i == e >> 5) before = total;
+        total += sums[i];
+    }
+    if (e < a.E) s.first[e] = before + x - n;
+    if (e == 0) s.first[a.E] = total;
+    return total;
 }
 
-// One warp per output column: its lanes take the words of the weight row in turn.
-template <typename T, bool SWIGLU>
-__global__ void __launch_bounds__(256) k_int4_product(const __grid_constant__ Int4Product p) {
-    __shared__ RaggedTiles tiles;
+// Item t: its group by bisection; the token tiles of a panel follow one another,
+// so that the CTAs that take them find its codes in L2.
+__device__ __forceinline__ Item item_at(const Lists& s, int n_groups, int panels, int t) {
+    int e = 0, end = n_groups;  // first[e] <= t < first[end]
+    while (end - e > 1) {
+        const int mid = (e + end) >> 1;
+        if (s.first[mid] <= t)
+            e = mid;
+        else
+            end = mid;
+    }
+    Item it;
+    it.e = uniform(e);
+    const unsigned i = t - s.first[e], tiles = static_cast<unsigned>(s.first[e + 1] - s.first[e]) / panels;
+    const unsigned panel = i / tiles;
+    const int width = s.width[e];
+    it.panel = uniform(static_cast<int>(panel));
+    it.row = uniform(s.lo[e] + static_cast<int>(i - panel * tiles) * width);
+    it.rows = uniform(min(width, s.hi[e] - it.row));
+    return it;
+}
+
+// First weight rows of a panel's two halves of 64.  With SwiGLU the halves are
+// gate and up of the same 64 columns (interleaved per 128 in W).
+struct Halves {
+    int a, b;
+};
+__device__ __forceinline__ Halves halves_of(int panel, bool swiglu) {
+    if (swiglu) {
+        const int gate = (panel >> 1) * 256 + (panel & 1) * 64;
+        return {gate, gate + 128};
+    }
+    return {panel * 128, panel * 128 + 64};
+}
+
+template <typename T>
+struct Wide;
+template <>
+struct Wide<__nv_bfloat16> {
+    static constexpr uint32_t magic = 0x43004300u;  // 128
+    static constexpr uint32_t format = 1;
+    static constexpr int map = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    __device__ static __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
+        const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+};
+template <>
+struct Wide<__half> {
+    static constexpr uint32_t magic = 0x64006400u;  // 1024
+    static constexpr uint32_t format = 0;
+    static constexpr int map = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    __device__ static __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
+        const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+};
+// Eight codes to four pairs of numbers; zero is magic + zero point in both halves.
+template <typename T>
+__device__ __forceinline__ void widen(uint32_t w, uint32_t zero, uint32_t* v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = Wide<T>::sub((w >> (4 * i) & 0x000F000Fu) | Wide<T>::magic, zero);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, M = 128, K = 16, where `one` is set.
+__device__ __forceinline__ void mma_tmem_if(uint32_t one, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "setp.ne.b32 q, %4, 0;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t one, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* tm, int x, int r0, int r1, int r2, int r3,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// The token row that src picks for row r of y; false where it picks none.
+__device__ __forceinline__ bool picked(const Int4Product& p, int r, int& from) {
+    const int s = ld_dep(p.src + r);
+    from = s / p.src_div;
+    return s >= 0 && from < p.x_rows;
+}
+
+template <typename T, int G>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_int4_product(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tX,
+                   const __grid_constant__ Int4Product p) {
+    using C = Cfg<G>;
+    constexpr int TN = C::TN;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* s_rows = smem + kCodeStages * kCodeBytes;
+    uint8_t* s_join = s_rows + kRowStages * C::row_stage;
+    uint8_t* s_params = s_join + C::join;
+    Bars& bars = *reinterpret_cast<Bars*>(s_params + kParams * C::param_bytes);
+    Lists& lists = *reinterpret_cast<Lists*>(reinterpret_cast<uint8_t*>(&bars) + 1024);
+    volatile uint32_t* abort_flag = &bars.abort;
+
+    const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    uint32_t split_;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(split_));
+    const int split = static_cast<int>(split_);
+    const bool swiglu = p.swiglu != 0;
+    const int panels = swiglu ? p.columns / 64 : (p.r.N + 127) / 128;
+    const int chunks = (p.r.K + kChunk - 1) / kChunk, per = (chunks + split - 1) / split;
+    const int c0 = min(rank * per, chunks), c1 = min(c0 + per, chunks);
     pdl_trigger();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kCodeStages; ++i) {
+            mbar_init(bars.code_full + i, 1);
+            mbar_init(bars.code_empty + i, 4);  // the warps that widen the chunk
+        }
+        for (int i = 0; i < kRowStages; ++i) {
+            mbar_init(bars.row_full + i, 1);
+            mbar_init(bars.row_empty + i, 1);
+        }
+        for (int i = 0; i < kABufs; ++i) {
+            mbar_init(bars.a_full + i, 4);
+            mbar_init(bars.a_empty + i, 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bars.d_full + i, 1);
+            mbar_init(bars.d_empty + i, 4);
+        }
+        for (int i = 0; i < kParams; ++i) {
+            mbar_init(bars.p_full + i, 1);
+            mbar_init(bars.p_empty + i, 8);  // the widening and the summing warps
+        }
+        mbar_init(&bars.join_full, 4 * split);  // every summing warp of the cluster
+        mbar_init(&bars.join_free, 4 * split);
+        mbar_init(&bars.drain, 1);
+        bars.abort = 0;
+        fence_mbar_init();
+    }
+    // tensor memory is taken only once the kernels before this one have finished
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp == 0) ragged_tiles_build<32>(p.r, tiles, 1, lane);
+    if (warp == 3) tmem_alloc(&bars.tmem, 512);
+    const int total = uniform(build_lists<TN>(p.r, lists, panels));
+    tc_fence_before();
     __syncthreads();
-    const int e = blockIdx.y, n = blockIdx.x * 8 + warp, columns = SWIGLU ? p.r.N / 2 : p.r.N;
-    if (n >= columns) return;
-    const int words = p.r.K / 8;
-    for (int row = tiles.lo[e]; row < tiles.hi[e]; ++row) {
-        int64_t xr = row;
-        bool have = true;
-        if (p.src) {
-            const int s = ld_dep(p.src + row);
-            xr = s / p.src_div;
-            have = s >= 0 && xr < p.x_rows;
-        }
-        float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int h = 0; h < (SWIGLU ? 2 : 1); ++h) {
-            const int64_t w = static_cast<int64_t>(e) * p.r.N + (SWIGLU ? (n >> 7) * 256 + (n & 127) + 128 * h : n);
-            for (int k = lane; have && k < words; k += 32) {
-                const uint32_t q = ld_dep(p.codes + w * words + k);
-                const int64_t g = w * p.groups + (k >> p.shift);
-                const float s = to_float<T>(static_cast<const T*>(p.scales)[g]);
-                const int zero = p.zeros ? p.zeros[g] : 8;
-                const T* x = static_cast<const T*>(p.x) + xr * p.ldx + 8 * k;
-                float part = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    part = fmaf(to_float<T>(x[i]), static_cast<float>(static_cast<int>(q >> (4 * (i >> 1) + 16 * (i & 1)) & 15u) - zero), part);
-                sum[h] = fmaf(part, s, sum[h]);
+    cluster_sync();  // the peers' barriers are initialised before any remote use
+    tc_fence_after();
+    const uint32_t tmem = uniform(bars.tmem);
+    const int first = blockIdx.x / split, stride = gridDim.x / split;
+    bool timed_out = false;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ codes
+        Ring r;
+        uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
+        for (int t = first; t < total && !timed_out; t += stride) {
+            const Item it = item_at(lists, p.r.E, panels, t);
+            const Halves h = halves_of(it.panel, swiglu);
+            for (int c = c0; c < c1; ++c) {
+                if (!warp_wait(bars.code_empty + r.s, r.ph ^ 1u, abort_flag)) {
+                    timed_out = true;
+                    break;
+                }
+                if (lane == 0) {
+                    uint64_t* bar = bars.code_full + r.s;
+                    const uint32_t dst = smem_u32(smem + r.s * kCodeBytes);
+                    mbar_arrive_expect_tx(bar, kCodeBytes);
+                    tma_load_3d(dst, &tW, c * 64, h.a, it.e, bar);
+                    tma_load_3d(dst + kCodeBytes / 2, &tW, c * 64, h.b, it.e, bar);
+                }
+                armed |= 1u << r.s;
+                armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
+                r.next<kCodeStages>();
             }
-            sum[h] = warp_sum(sum[h]);
         }
-        if (lane == 0) {
-            float y = sum[0];
-            if constexpr (SWIGLU) y = y / (1.0f + expf(-y)) * sum[1];
-            if (p.r.row_scale) y *= ld_dep(p.r.row_scale + row);
-            static_cast<T*>(p.r.out)[row * p.r.ldo + n] = from_float<T>(y);
+        if ((timed_out || *abort_flag) && lane == 0) {
+            *abort_flag = 1;
+            for (int i = 0; i < kCodeStages; ++i)
+                if (armed & (1u << i)) {
+                    volatile uint32_t never = 0;
+                    (void)mbar_wait(bars.code_full + i, (armed_par >> i) & 1u, &never);
+                }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------- token rows
+        Ring r;
+        uint32_t armed = 0, armed_par = 0;
+        for (int t = first; t < total && !timed_out; t += stride) {
+            const Item it = item_at(lists, p.r.E, panels, t);
+            const int wide = (it.rows + 15) & ~15;
+            // lane: 16 rows of one half, or 4 rows that src picks, of a stage
+            const int boxes = p.src ? wide / 4 : wide / 16;
+            const int half = lane >= 16 ? 1 : 0, box = lane & 15;
+            int from[4] = {0, 0, 0, 0};
+            if (p.src && box < boxes) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    // rows that are not stored, or stored as zeros, may be any
+                    if (4 * box + j < it.rows && !picked(p, it.row + 4 * box + j, from[j])) from[j] = 0;
+            }
+            for (int c = c0; c < c1; ++c) {
+                if (!warp_wait(bars.row_empty + r.s, r.ph ^ 1u, abort_flag)) {
+                    timed_out = true;
+                    break;
+                }
+                uint64_t* bar = bars.row_full + r.s;
+                if (lane == 0) mbar_arrive_expect_tx(bar, wide * 256);
+                __syncwarp();
+                if (box < boxes) {
+                    const uint32_t dst = smem_u32(s_rows + r.s * C::row_stage + half * (C::row_stage / 2));
+                    const int x0 = c * kChunk + half * 64;
+                    if (p.src)
+                        tma_gather4(dst + box * 512, &tX, x0, from[0], from[1], from[2], from[3], bar);
+                    else
+                        tma_load_2d(s_rows + r.s * C::row_stage + half * (C::row_stage / 2) + box * 2048, &tX, x0,
+                                    it.row + box * 16, bar);
+                }
+                armed |= 1u << r.s;
+                armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
+                r.next<kRowStages>();
+            }
+        }
+        __syncwarp();
+        if ((timed_out || *abort_flag) && lane == 0) {
+            *abort_flag = 1;
+            for (int i = 0; i < kRowStages; ++i)
+                if (armed & (1u << i)) {
+                    volatile uint32_t never = 0;
+                    (void)mbar_wait(bars.row_full + i, (armed_par >> i) & 1u, &never);
+                }
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------- MMAs
+        const uint32_t one = elect_one();
+        const uint64_t b0 = sdesc_sw128(smem_u32(s_rows));
+        Ring r, a, d;
+        bool issued = false;
+        for (int t = first; t < total && !timed_out; t += stride) {
+            const Item it = item_at(lists, p.r.E, panels, t);
+            const uint32_t idesc = (1u << 4) | (Wide<T>::format << 7) | (Wide<T>::format << 10) |
+                                   (static_cast<uint32_t>((it.rows + 15) >> 4) << 18) | (8u << 24);
+            for (int c = c0; c < c1; ++c) {
+                if (!warp_wait(bars.d_empty + d.s, d.ph ^ 1u, abort_flag) ||
+                    !warp_wait(bars.row_full + r.s, r.ph, abort_flag) || !warp_wait(bars.a_full + a.s, a.ph, abort_flag)) {
+                    timed_out = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t dcol = tmem + static_cast<uint32_t>(d.s * C::d_cols);
+                const uint32_t acol = tmem + C::a_col + static_cast<uint32_t>(a.s * 64);
+                const uint64_t b = b0 + static_cast<uint32_t>(r.s * (C::row_stage >> 4));
+#pragma unroll
+                for (int k = 0; k < kChunk / 16; ++k)
+                    mma_tmem_if(one, dcol + (k * 16 / G) * TN, acol + k * 8,
+                                b + (k >> 2) * (C::row_stage / 2 >> 4) + (k & 3) * 2, idesc, k % (G / 16) != 0);
+                commit_if(one, bars.row_empty + r.s);
+                commit_if(one, bars.a_empty + a.s);
+                commit_if(one, bars.d_full + d.s);
+                issued = true;
+                r.next<kRowStages>();
+                a.next<kABufs>();
+                d.next<C::d_bufs>();
+            }
+        }
+        if ((timed_out || *abort_flag) && issued && one) {
+            *abort_flag = 1;
+            mma_commit(&bars.drain);
+            volatile uint32_t never = 0;
+            (void)mbar_wait(&bars.drain, 0, &never);
+        }
+    } else if (warp == 3) {
+        // ------------------------------------------- scales and zero points
+        // rows lane, lane + 32, .. of the panel; kAhead chunks' loads are issued
+        // before the first is used
+        Ring r;
+        for (int t = first; t < total && !timed_out; t += stride) {
+            const Item it = item_at(lists, p.r.E, panels, t);
+            const Halves h = halves_of(it.panel, swiglu);
+            int64_t at[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int n = (i < 2 ? h.a : h.b) + (i & 1) * 32 + lane;
+                at[i] = (static_cast<int64_t>(it.e) * p.r.N + min(n, p.r.N - 1)) * p.groups;
+            }
+            const uint16_t* scales = static_cast<const uint16_t*>(p.scales);
+            constexpr int kBatch = kAhead / C::parts;  // chunks whose loads fit the registers
+            for (int cb = c0; cb < c1 && !timed_out; cb += kBatch) {
+                uint16_t s[kBatch][4][C::parts];
+                uint8_t z[kBatch][4][C::parts];
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int g = (cb + b) * C::parts;
+                        if (p.whole && C::parts > 1) {
+                            uint64_t sv = 0;
+                            uint32_t zv = 0x08080808u;
+                            if (cb + b < c1) {
+                                if constexpr (C::parts == 4) {
+                                    sv = *reinterpret_cast<const uint64_t*>(scales + at[i] + g);
+                                    if (p.zeros) zv = *reinterpret_cast<const uint32_t*>(p.zeros + at[i] + g);
+                                } else if constexpr (C::parts == 2) {
+                                    sv = *reinterpret_cast<const uint32_t*>(scales + at[i] + g);
+                                    if (p.zeros) zv = *reinterpret_cast<const uint16_t*>(p.zeros + at[i] + g);
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < C::parts; ++j) {
+                                s[b][i][j] = static_cast<uint16_t>(sv >> (16 * j));
+                                z[b][i][j] = static_cast<uint8_t>(zv >> (8 * j));
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < C::parts; ++j) {
+                                const bool in = cb + b < c1 && g + j < p.groups;
+                                // a group past the row's end has sum 0 and scale 0
+                                s[b][i][j] = in ? scales[at[i] + g + j] : static_cast<uint16_t>(0);
+                                z[b][i][j] = in && p.zeros ? p.zeros[at[i] + g + j] : static_cast<uint8_t>(8);
+                            }
+                        }
+                    }
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    if (cb + b >= c1) break;
+                    if (!warp_wait(bars.p_empty + r.s, r.ph ^ 1u, abort_flag)) {
+                        timed_out = true;
+                        break;
+                    }
+                    uint16_t* ps = reinterpret_cast<uint16_t*>(s_params + r.s * C::param_bytes);
+                    uint8_t* pz = reinterpret_cast<uint8_t*>(ps + C::parts * 128);
+#pragma unroll
+                    for (int j = 0; j < C::parts; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            ps[j * 128 + i * 32 + lane] = s[b][i][j];
+                            pz[j * 128 + i * 32 + lane] = z[b][i][j];
+                        }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars.p_full + r.s);
+                    r.next<kParams>();
+                }
+            }
+        }
+    } else if (warp < 8) {
+        // ------------------------------------------------- sums and epilogue
+        const int q = warp & 3, me = q * 32 + lane;  // weight row of the panel
+        const uint32_t quarter = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        Ring d, pr;
+        uint32_t join_ph = 0;
+        for (int t = first; t < total && !timed_out; t += stride) {
+            const Item it = item_at(lists, p.r.E, panels, t);
+            const int wide = (it.rows + 15) & ~15;
+            float acc[TN];
+#pragma unroll
+            for (int n = 0; n < TN; ++n) acc[n] = 0.0f;
+            for (int c = c0; c < c1; ++c) {
+                if (!warp_wait(bars.p_full + pr.s, pr.ph, abort_flag)) {
+                    timed_out = true;
+                    break;
+                }
+                float s[C::parts];
+                const T* ps = reinterpret_cast<const T*>(s_params + pr.s * C::param_bytes);
+#pragma unroll
+                for (int j = 0; j < C::parts; ++j) s[j] = to_float<T>(ps[j * 128 + me]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars.p_empty + pr.s);
+                pr.next<kParams>();
+                if (!warp_wait(bars.d_full + d.s, d.ph, abort_flag)) {
+                    timed_out = true;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < C::parts; ++j) {
+                    const uint32_t col = quarter + static_cast<uint32_t>(d.s * C::d_cols + j * TN);
+#pragma unroll
+                    for (int n0 = 0; n0 < TN; n0 += 32) {
+                        if (n0 >= wide) break;
+                        uint32_t v[32];
+                        if (wide - n0 > 16) {
+                            tmem_ld32(col + n0, v);
+                        } else {
+                            uint32_t u[16];
+                            tmem_ld16(col + n0, u);
+#pragma unroll
+                            for (int n = 0; n < 32; ++n) v[n] = n < 16 ? u[n & 15] : 0u;
+                        }
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int n = 0; n < 16; ++n) acc[n0 + n] = fmaf(__uint_as_float(v[n]), s[j], acc[n0 + n]);
+                        if (wide - n0 > 16) {
+#pragma unroll
+                            for (int n = 16; n < 32; ++n) acc[n0 + n] = fmaf(__uint_as_float(v[n]), s[j], acc[n0 + n]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars.d_empty + d.s);
+                d.next<C::d_bufs>();
+            }
+            if (timed_out) break;
+            // every CTA of the cluster stores wide / split columns: parts to them
+            const int share = wide / split;
+            if (!warp_wait(&bars.join_free, join_ph ^ 1u, abort_flag, sum_limit_ns(per))) {
+                timed_out = true;
+                break;
+            }
+            fence_cluster();
+            {
+                int to = 0, left = share;
+                uint32_t dst = mapa_shared(smem_u32(s_join) + static_cast<uint32_t>(rank * share * 512 + me * 4), 0);
+#pragma unroll
+                for (int n = 0; n < TN; ++n) {
+                    if (n >= wide) break;
+                    if (left == 0) {
+                        left = share;
+                        ++to;
+                        dst = mapa_shared(smem_u32(s_join) + static_cast<uint32_t>(rank * share * 512 + me * 4),
+                                          static_cast<uint32_t>(to));
+                    }
+                    st_cluster_f32(dst, acc[n]);
+                    dst += 512;
+                    --left;
+                }
+            }
+            fence_cluster();
+            __syncwarp();
+            if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.join_full), static_cast<uint32_t>(lane)));
+            if (!warp_wait(&bars.join_full, join_ph, abort_flag, sum_limit_ns(per))) {
+                timed_out = true;
+                break;
+            }
+            join_ph ^= 1u;
+            fence_cluster();
+            // a warp takes every fourth column (with SwiGLU, every fourth two): a
+            // token, whose features lie along the lanes, four to each
+            const float* join = reinterpret_cast<const float*>(s_join);
+            T* out = static_cast<T*>(p.r.out);
+            auto sum4 = [&](int c, int f) {
+                float4 v = *reinterpret_cast<const float4*>(join + c * 128 + f);
+                for (int o = 1; o < split; ++o) {
+                    const float4 w = *reinterpret_cast<const float4*>(join + (o * share + c) * 128 + f);
+                    v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+                }
+                return v;
+            };
+            const int each = swiglu ? 2 : 1;
+            for (int cb = q * each; cb < share; cb += 4 * each) {
+                const int c = cb + (swiglu ? lane >> 4 : 0), token = rank * share + c;
+                const int f = swiglu ? 4 * (lane & 15) : 4 * lane, n = it.panel * (swiglu ? 64 : 128) + f;
+                if (c >= share || token >= it.rows || n >= p.columns) continue;
+                const int row = it.row + token;
+                float4 v = sum4(c, f);
+                if (swiglu) {
+                    const float4 u = sum4(c, 64 + f);
+                    v.x = v.x / (1.0f + expf(-v.x)) * u.x;
+                    v.y = v.y / (1.0f + expf(-v.y)) * u.y;
+                    v.z = v.z / (1.0f + expf(-v.z)) * u.z;
+                    v.w = v.w / (1.0f + expf(-v.w)) * u.w;
+                }
+                const float g = p.r.row_scale ? ld_dep(p.r.row_scale + row) : 1.0f;
+                v.x *= g, v.y *= g, v.z *= g, v.w *= g;
+                int from;
+                if (p.src && !picked(p, row, from)) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                *reinterpret_cast<uint2*>(out + row * p.r.ldo + n) = make_uint2(pack2(T(), v.x, v.y), pack2(T(), v.z, v.w));
+            }
+            __syncwarp();
+            if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.join_free), static_cast<uint32_t>(lane)));
+        }
+    } else {
+        // ---------------------------------------------------------- widening
+        const int mine = (warp - 8) >> 2, q = warp & 3, me = q * 32 + lane;
+        const uint32_t quarter = tmem + (static_cast<uint32_t>(q * 32) << 16) + C::a_col;
+        // 16-byte piece i of row `me` in the 64-byte swizzle
+        const int turn = (me >> 1) & 3;
+        Ring s, a, pr;
+        int turns = 0;
+        for (int t = first; t < total && !timed_out; t += stride) {
+            for (int c = c0; c < c1; ++c) {
+                if ((turns++ & 1) == mine) {
+                    if (!warp_wait(bars.p_full + pr.s, pr.ph, abort_flag)) {
+                        timed_out = true;
+                        break;
+                    }
+                    const uint8_t* pz = s_params + pr.s * C::param_bytes + C::parts * 256;
+                    uint32_t zero[C::parts];
+#pragma unroll
+                    for (int j = 0; j < C::parts; ++j) zero[j] = Wide<T>::magic + pz[j * 128 + me] * 0x00010001u;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars.p_empty + pr.s);
+                    if (!warp_wait(bars.code_full + s.s, s.ph, abort_flag)) {
+                        timed_out = true;
+                        break;
+                    }
+                    const uint4* row = reinterpret_cast<const uint4*>(smem + s.s * kCodeBytes + me * 64);
+                    uint4 w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = row[i ^ turn];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars.code_empty + s.s);
+                    if (!warp_wait(bars.a_empty + a.s, a.ph ^ 1u, abort_flag)) {
+                        timed_out = true;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // 64 elements, 32 columns
+                        uint32_t v[32];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint4 u = w[2 * h + i];
+                            const uint32_t z = zero[(2 * h + i) * 32 / G];
+                            widen<T>(u.x, z, v + 16 * i);
+                            widen<T>(u.y, z, v + 16 * i + 4);
+                            widen<T>(u.z, z, v + 16 * i + 8);
+                            widen<T>(u.w, z, v + 16 * i + 12);
+                        }
+                        tmem_st(quarter + static_cast<uint32_t>(a.s * 64 + h * 32), v);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars.a_full + a.s);
+                }
+                s.next<kCodeStages>();
+                a.next<kABufs>();
+                pr.next<kParams>();
+            }
         }
     }
+    if (timed_out) *abort_flag = 1;
+    if (timed_out && p.r.status) atomicOr(p.r.status, kRaggedTimeout);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // no peer still writes to this CTA's shared memory
+    if (warp == 3) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// CTAs that split a sum.  More items than SMs need no split.
+int split_of(int64_t items, int chunks) {
+    int split = 1;
+    while (split < kMaxSplit && items * split < 2 * num_sms() && chunks >= 4 * split) split *= 2;
+    return split;
+}
+
+template <typename T, int G>
+cudaError_t launch(const Int4Product& p, const void* x, int64_t ldx, const void* codes, cudaStream_t st) {
+    using C = Cfg<G>;
+    static int found[kMaxDevices][4] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    CUtensorMap tW, tX;
+    const uint64_t K = p.r.K, N = p.r.N, E = p.r.E;
+    const uint64_t wd[3] = {K / 2, N, E}, ws[2] = {K / 2, N * (K / 2)};
+    const uint32_t wb[3] = {64, 64, 1};
+    const uint64_t xd[2] = {K, static_cast<uint64_t>(p.x_rows)}, xs[1] = {static_cast<uint64_t>(ldx) * 2};
+    const uint32_t xb[2] = {64, p.src ? 1u : 16u};
+    if (!make_tensor_map(&tW, codes, 3, wd, ws, wb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 64) ||
+        !make_tensor_map(&tX, x, 2, xd, xs, xb, Wide<T>::map))
+        return cudaErrorInvalidValue;
+    const int64_t panels = p.swiglu ? p.columns / 64 : (p.r.N + 127) / 128;
+    const int64_t items = panels * (p.r.R / C::TN + (p.r.R < p.r.E ? p.r.R : p.r.E));  // at most
+    const int split = split_of(items, static_cast<int>((K + kChunk - 1) / kChunk));
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(split);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    int& n = found[dev][split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3];  // clusters at once
+    if (!n) {
+        cudaError_t e = cudaFuncSetAttribute(k_int4_product<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+        if (e != cudaSuccess) return e;
+        int most = num_sms();
+        if (split > 1) {
+            e = cudaOccupancyMaxActiveClusters(&most, k_int4_product<T, G>, &cfg);
+            if (e != cudaSuccess) return e;
+        }
+        n = most > 0 ? most : 1;
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>(split * (items < n ? items : n)));
+    return cudaLaunchKernelEx(&cfg, k_int4_product<T, G>, tW, tX, p);
+}
+
+template <typename T>
+cudaError_t product(int group, const Int4Product& p, const void* x, int64_t ldx, const void* codes, cudaStream_t st) {
+    if (group == 32) return launch<T, 32>(p, x, ldx, codes, st);
+    return group == 64 ? launch<T, 64>(p, x, ldx, codes, st) : launch<T, 128>(p, x, ldx, codes, st);
 }
 
 bool aligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -124,21 +813,18 @@ extern "C" moe_status_t moe_grouped_gemm_int4(int32_t group, int32_t dtype, int6
     p.r.out = y;
     p.r.ldo = ldy;
     p.r.status = status;
-    p.x = x;
-    p.ldx = ldx;
-    p.x_rows = x_rows;
+    p.x_rows = static_cast<int32_t>(x_rows < INT32_MAX ? x_rows : INT32_MAX);
+    p.columns = N;
+    p.swiglu = swiglu != 0;
     p.src = src;
     p.src_div = src_div;
-    p.codes = static_cast<const uint32_t*>(w_codes);
     p.scales = w_scales;
     p.zeros = static_cast<const uint8_t*>(w_zeros);
     p.groups = (K + group - 1) / group;
-    p.shift = group == 32 ? 2 : group == 64 ? 3 : 4;
+    const int parts = kChunk / group;  // groups of a chunk
+    p.whole = p.groups % parts == 0 && aligned(w_scales, 2 * parts) && aligned(w_zeros, parts);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const dim3 grid((N + 7) / 8, E);
-    auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, st, p); };
-    const cudaError_t e = dtype == MOE_DTYPE_BF16
-                              ? (swiglu ? go(k_int4_product<__nv_bfloat16, true>) : go(k_int4_product<__nv_bfloat16, false>))
-                              : (swiglu ? go(k_int4_product<__half, true>) : go(k_int4_product<__half, false>));
+    const cudaError_t e = dtype == MOE_DTYPE_BF16 ? product<__nv_bfloat16>(group, p, x, ldx, w_codes, st)
+                                                  : product<__half>(group, p, x, ldx, w_codes, st);
     return e == cudaSuccess ? MOE_OK : set_last_error(MOE_ERR_CUDA, "4-bit weight product: %s", cudaGetErrorString(e));
 }
