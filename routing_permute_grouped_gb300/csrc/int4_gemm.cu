@@ -25,7 +25,7 @@
 // CTAs' order.
 #include <cuda_runtime.h>
 
-#include <cmath>
+#include <type_traits>
 
 #include "../../include/moe.h"
 #include "int4.h"
@@ -39,34 +39,36 @@ namespace moe {
 namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr int kChunk = 128;            // elements of the sum per step
-constexpr int kCodeBytes = 128 * 64;   // of a chunk of a panel
-constexpr int kCodeStages = 12;
-constexpr int kRowStages = 4;
-constexpr int kABufs = 4;              // widened chunks in tensor memory, 64 columns each
-constexpr int kParams = 8;             // chunks of scales and zero points in shared memory
-constexpr int kAhead = 4;              // of them loaded at once
+constexpr int kCodeBytes = 96 * 1024;  // of the codes in flight
+constexpr int kRowStages = 5;          // of token rows, 128 elements each
+constexpr int kRowLag = 3;             // of them under way before the oldest is waited for
 constexpr int kThreads = 512;
 constexpr int kMaxSplit = 8;           // CTAs of a cluster
 
+// A chunk's sums are one column per group and token; two chunks' of them and two
+// widened chunks (half a column per element) share tensor memory.
 template <int G>
 struct Cfg {
-    static constexpr int parts = kChunk / G;             // groups of a chunk
+    static constexpr int chunk = G == 128 ? 256 : 128;   // elements of the sum per step
+    static constexpr int parts = chunk / G;              // groups of a chunk
     static constexpr int TN = G == 32 ? 32 : 64;         // token rows of a tile, at most
     static constexpr int d_cols = parts * TN;            // a chunk's sums
     static constexpr int d_bufs = 256 / d_cols;
     static constexpr uint32_t a_col = 256;               // the first widened chunk's column
+    static constexpr int a_bufs = 512 / chunk;
+    static constexpr int code_stage = 128 * chunk / 2;
+    static constexpr int code_stages = kCodeBytes / code_stage;
     static constexpr int row_stage = TN * 256;
-    static constexpr int param_bytes = parts * 128 * 3;  // scales, then zero points
-    static constexpr int join = TN * 512;                // fp32 parts of the columns this CTA stores
-    static constexpr int smem = 1024 + kCodeStages * kCodeBytes + kRowStages * row_stage + join + kParams * param_bytes +
-                                1024 + 4 * 260 * 4;
+    static constexpr int join = TN * 512;                // fp32 sums of the columns this CTA stores
+    static constexpr int smem = 1024 + kCodeBytes + kRowStages * row_stage + join + 1024 + 4 * 260 * 4;
     static_assert(smem <= 232448, "shared memory budget");
-    static_assert(kABufs * 64 + d_bufs * d_cols <= 512, "tensor memory budget");
+    static_assert(d_bufs * d_cols <= 256 && a_bufs * chunk / 2 <= 256, "tensor memory budget");
 };
 
 struct Int4Product {
     RaggedArgs r;          // N: weight rows per group
+    const void* x;
+    int64_t ldx;
     int32_t x_rows;
     int32_t columns;       // of y
     int32_t swiglu;
@@ -75,15 +77,14 @@ struct Int4Product {
     const void* scales;    // [E, N, groups]
     const uint8_t* zeros;  // the same, or null
     int32_t groups;        // per weight row
-    int32_t whole;         // scales and zero points of a chunk can be read at once
+    int32_t whole;         // scales and zero points can be read eight groups at a time
 };
 
 struct Bars {
-    uint64_t code_full[kCodeStages], code_empty[kCodeStages];
+    uint64_t code_full[12], code_empty[12];
     uint64_t row_full[kRowStages], row_empty[kRowStages];
-    uint64_t a_full[kABufs], a_empty[kABufs];
+    uint64_t a_full[4], a_empty[4];
     uint64_t d_full[4], d_empty[4];
-    uint64_t p_full[kParams], p_empty[kParams];
     uint64_t join_full, join_free, drain;
     uint32_t tmem, abort;
 };
@@ -181,13 +182,18 @@ __device__ __forceinline__ Halves halves_of(int panel, bool swiglu) {
     return {panel * 128, panel * 128 + 64};
 }
 
+// Row `me` of the panel among the weight rows; past the last one, the last.
+__device__ __forceinline__ int64_t weight_row(const Int4Product& p, int e, const Halves& h, int me) {
+    const int n = me < 64 ? h.a + me : h.b + me - 64;
+    return static_cast<int64_t>(e) * p.r.N + min(n, p.r.N - 1);
+}
+
 template <typename T>
 struct Wide;
 template <>
 struct Wide<__nv_bfloat16> {
     static constexpr uint32_t magic = 0x43004300u;  // 128
     static constexpr uint32_t format = 1;
-    static constexpr int map = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     __device__ static __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
         const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
         return *reinterpret_cast<const uint32_t*>(&r);
@@ -197,7 +203,6 @@ template <>
 struct Wide<__half> {
     static constexpr uint32_t magic = 0x64006400u;  // 1024
     static constexpr uint32_t format = 0;
-    static constexpr int map = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     __device__ static __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
         const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
         return *reinterpret_cast<const uint32_t*>(&r);
@@ -236,38 +241,90 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm,
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* tm, int x, int r0, int r1, int r2, int r3,
-                                            uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar))
-        : "memory");
-}
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// The token row that src picks for row r of y; false where it picks none.
-__device__ __forceinline__ bool picked(const Int4Product& p, int r, int& from) {
-    const int s = ld_dep(p.src + r);
-    from = s / p.src_div;
-    return s >= 0 && from < p.x_rows;
+// The token row of row r of y; -1 where src picks none.
+__device__ __forceinline__ int token_row(const Int4Product& p, int r) {
+    if (!p.src) return r;
+    const int s = ld_dep(p.src + r), from = s / p.src_div;
+    return s >= 0 && from < p.x_rows ? from : -1;
 }
+
+// Eight scales (16 bits each) or zero points (8) of a weight row, by the chunk:
+// a row's are read eight groups at a time, one read ahead, where they are aligned
+// for it, else each by itself, a chunk ahead.
+template <int PARTS, typename E>
+struct Stream {
+    using Eight = std::conditional_t<sizeof(E) == 2, uint4, uint2>;
+    const E* at;
+    int groups, whole;
+    uint32_t absent;
+    Eight now, ahead;
+    uint32_t one[PARTS];
+    __device__ __forceinline__ Eight eight(int g) const {
+        Eight v{};
+        if (g < groups) v = *reinterpret_cast<const Eight*>(at + g);
+        return v;
+    }
+    __device__ __forceinline__ void single(int c) {
+#pragma unroll
+        for (int j = 0; j < PARTS; ++j) one[j] = c * PARTS + j < groups ? at[c * PARTS + j] : absent;
+    }
+    __device__ __forceinline__ void start(const E* row, int n, int aligned, uint32_t none, int c) {
+        at = row;
+        groups = n;
+        whole = aligned;
+        absent = none;
+        if (!row) return;
+        if (whole) {
+            now = eight(c * PARTS & ~7);
+            ahead = eight((c * PARTS & ~7) + 8);
+        } else {
+            single(c);
+        }
+    }
+    // Those of chunk c; the chunks follow one another.
+    __device__ __forceinline__ void take(int c, uint32_t (&v)[PARTS]) {
+        if (!at) {
+#pragma unroll
+            for (int j = 0; j < PARTS; ++j) v[j] = absent;
+        } else if (whole) {
+            const uint32_t* w = &now.x;
+#pragma unroll
+            for (int j = 0; j < PARTS; ++j) {
+                const int g = (c * PARTS + j) & 7;
+                if constexpr (sizeof(E) == 2) {
+                    const uint32_t u = g & 4 ? (g & 2 ? w[3] : w[2]) : (g & 2 ? w[1] : w[0]);
+                    v[j] = g & 1 ? u >> 16 : u & 0xFFFFu;
+                } else {
+                    v[j] = (g & 4 ? w[1] : w[0]) >> (8 * (g & 3)) & 0xFFu;
+                }
+            }
+            if (((c + 1) * PARTS & 7) == 0) {
+                now = ahead;
+                ahead = eight((c + 1) * PARTS + 8);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < PARTS; ++j) v[j] = one[j];
+            single(c + 1);
+        }
+    }
+};
 
 template <typename T, int G>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_int4_product(const __grid_constant__ CUtensorMap tW, const __grid_constant__ CUtensorMap tX,
-                   const __grid_constant__ Int4Product p) {
+    k_int4_product(const __grid_constant__ CUtensorMap tW, const __grid_constant__ Int4Product p) {
     using C = Cfg<G>;
     constexpr int TN = C::TN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint8_t* s_rows = smem + kCodeStages * kCodeBytes;
+    uint8_t* s_rows = smem + kCodeBytes;
     uint8_t* s_join = s_rows + kRowStages * C::row_stage;
-    uint8_t* s_params = s_join + C::join;
-    Bars& bars = *reinterpret_cast<Bars*>(s_params + kParams * C::param_bytes);
+    Bars& bars = *reinterpret_cast<Bars*>(s_join + C::join);
     Lists& lists = *reinterpret_cast<Lists*>(reinterpret_cast<uint8_t*>(&bars) + 1024);
     volatile uint32_t* abort_flag = &bars.abort;
 
@@ -278,29 +335,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int split = static_cast<int>(split_);
     const bool swiglu = p.swiglu != 0;
     const int panels = swiglu ? p.columns / 64 : (p.r.N + 127) / 128;
-    const int chunks = (p.r.K + kChunk - 1) / kChunk, per = (chunks + split - 1) / split;
+    const int chunks = (p.r.K + C::chunk - 1) / C::chunk, per = (chunks + split - 1) / split;
     const int c0 = min(rank * per, chunks), c1 = min(c0 + per, chunks);
     pdl_trigger();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kCodeStages; ++i) {
+        for (int i = 0; i < C::code_stages; ++i) {
             mbar_init(bars.code_full + i, 1);
             mbar_init(bars.code_empty + i, 4);  // the warps that widen the chunk
         }
         for (int i = 0; i < kRowStages; ++i) {
-            mbar_init(bars.row_full + i, 1);
+            mbar_init(bars.row_full + i, 2);  // both loading warps
             mbar_init(bars.row_empty + i, 1);
         }
-        for (int i = 0; i < kABufs; ++i) {
+        for (int i = 0; i < C::a_bufs; ++i) {
             mbar_init(bars.a_full + i, 4);
             mbar_init(bars.a_empty + i, 1);
         }
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < C::d_bufs; ++i) {
             mbar_init(bars.d_full + i, 1);
             mbar_init(bars.d_empty + i, 4);
-        }
-        for (int i = 0; i < kParams; ++i) {
-            mbar_init(bars.p_full + i, 1);
-            mbar_init(bars.p_empty + i, 8);  // the widening and the summing warps
         }
         mbar_init(&bars.join_full, 4 * split);  // every summing warp of the cluster
         mbar_init(&bars.join_free, 4 * split);
@@ -334,72 +387,72 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) {
                     uint64_t* bar = bars.code_full + r.s;
-                    const uint32_t dst = smem_u32(smem + r.s * kCodeBytes);
-                    mbar_arrive_expect_tx(bar, kCodeBytes);
-                    tma_load_3d(dst, &tW, c * 64, h.a, it.e, bar);
-                    tma_load_3d(dst + kCodeBytes / 2, &tW, c * 64, h.b, it.e, bar);
+                    const uint32_t dst = smem_u32(smem + r.s * C::code_stage);
+                    mbar_arrive_expect_tx(bar, C::code_stage);
+                    tma_load_3d(dst, &tW, c * (C::chunk / 2), h.a, it.e, bar);
+                    tma_load_3d(dst + C::code_stage / 2, &tW, c * (C::chunk / 2), h.b, it.e, bar);
                 }
                 armed |= 1u << r.s;
                 armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
-                r.next<kCodeStages>();
+                r.next<C::code_stages>();
             }
         }
         if ((timed_out || *abort_flag) && lane == 0) {
             *abort_flag = 1;
-            for (int i = 0; i < kCodeStages; ++i)
+            for (int i = 0; i < C::code_stages; ++i)
                 if (armed & (1u << i)) {
                     volatile uint32_t never = 0;
                     (void)mbar_wait(bars.code_full + i, (armed_par >> i) & 1u, &never);
                 }
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 3) {
         // ------------------------------------------------------- token rows
-        Ring r;
-        uint32_t armed = 0, armed_par = 0;
+        // each of the two warps takes 64 of a stage's 128 elements; a lane 16 bytes
+        // of every fourth row, into the 128-byte swizzle
+        const int half = warp >> 1, sub = lane >> 3, piece = lane & 7;
+        const uint32_t even = sub * 128 + ((piece ^ sub) << 4), odd = (sub + 4) * 128 + ((piece ^ (sub + 4)) << 4);
+        const uint8_t* base = static_cast<const uint8_t*>(p.x);
+        const uint32_t dst0 = smem_u32(s_rows + half * (C::row_stage / 2));
+        Ring r, done;
+        int under_way = 0;
+        auto landed = [&]() {  // the oldest stage, once its copies are seen to be complete
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.row_full + done.s);
+            done.next<kRowStages>();
+            --under_way;
+        };
         for (int t = first; t < total && !timed_out; t += stride) {
             const Item it = item_at(lists, p.r.E, panels, t);
             const int wide = (it.rows + 15) & ~15;
-            // lane: 16 rows of one half, or 4 rows that src picks, of a stage
-            const int boxes = p.src ? wide / 4 : wide / 16;
-            const int half = lane >= 16 ? 1 : 0, box = lane & 15;
-            int from[4] = {0, 0, 0, 0};
-            if (p.src && box < boxes) {
+            int from[TN / 4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    // rows that are not stored, or stored as zeros, may be any
-                    if (4 * box + j < it.rows && !picked(p, it.row + 4 * box + j, from[j])) from[j] = 0;
-            }
-            for (int c = c0; c < c1; ++c) {
+            for (int i = 0; i < TN / 4; ++i)
+                from[i] = 4 * i + sub < it.rows ? token_row(p, it.row + 4 * i + sub) : -1;
+            for (int k0 = c0 * C::chunk; k0 < c1 * C::chunk; k0 += 128) {
                 if (!warp_wait(bars.row_empty + r.s, r.ph ^ 1u, abort_flag)) {
                     timed_out = true;
                     break;
                 }
-                uint64_t* bar = bars.row_full + r.s;
-                if (lane == 0) mbar_arrive_expect_tx(bar, wide * 256);
-                __syncwarp();
-                if (box < boxes) {
-                    const uint32_t dst = smem_u32(s_rows + r.s * C::row_stage + half * (C::row_stage / 2));
-                    const int x0 = c * kChunk + half * 64;
-                    if (p.src)
-                        tma_gather4(dst + box * 512, &tX, x0, from[0], from[1], from[2], from[3], bar);
-                    else
-                        tma_load_2d(s_rows + r.s * C::row_stage + half * (C::row_stage / 2) + box * 2048, &tX, x0,
-                                    it.row + box * 16, bar);
+                const int k = k0 + half * 64 + piece * 8;
+                const uint32_t dst = dst0 + r.s * C::row_stage;
+#pragma unroll
+                for (int i = 0; i < TN / 4; ++i) {
+                    if (4 * i >= wide) break;
+                    const bool in = from[i] >= 0 && k < p.r.K;
+                    cp_async_16(dst + (i >> 1) * 1024 + (i & 1 ? odd : even),
+                                in ? base + (from[i] * p.ldx + k) * 2 : base, in ? 16 : 0);
                 }
-                armed |= 1u << r.s;
-                armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
+                cp_async_commit();
                 r.next<kRowStages>();
+                if (++under_way > kRowLag) {
+                    cp_async_wait<kRowLag>();
+                    landed();
+                }
             }
         }
-        __syncwarp();
-        if ((timed_out || *abort_flag) && lane == 0) {
-            *abort_flag = 1;
-            for (int i = 0; i < kRowStages; ++i)
-                if (armed & (1u << i)) {
-                    volatile uint32_t never = 0;
-                    (void)mbar_wait(bars.row_full + i, (armed_par >> i) & 1u, &never);
-                }
-        }
+        cp_async_wait<0>();
+        while (under_way > 0) landed();
     } else if (warp == 2) {
         // ------------------------------------------------------------- MMAs
         const uint32_t one = elect_one();
@@ -410,26 +463,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Item it = item_at(lists, p.r.E, panels, t);
             const uint32_t idesc = (1u << 4) | (Wide<T>::format << 7) | (Wide<T>::format << 10) |
                                    (static_cast<uint32_t>((it.rows + 15) >> 4) << 18) | (8u << 24);
-            for (int c = c0; c < c1; ++c) {
-                if (!warp_wait(bars.d_empty + d.s, d.ph ^ 1u, abort_flag) ||
-                    !warp_wait(bars.row_full + r.s, r.ph, abort_flag) || !warp_wait(bars.a_full + a.s, a.ph, abort_flag)) {
+            for (int c = c0; c < c1 && !timed_out; ++c) {
+                if (!warp_wait(bars.d_empty + d.s, d.ph ^ 1u, abort_flag) || !warp_wait(bars.a_full + a.s, a.ph, abort_flag)) {
                     timed_out = true;
                     break;
                 }
-                tc_fence_after();
                 const uint32_t dcol = tmem + static_cast<uint32_t>(d.s * C::d_cols);
-                const uint32_t acol = tmem + C::a_col + static_cast<uint32_t>(a.s * 64);
-                const uint64_t b = b0 + static_cast<uint32_t>(r.s * (C::row_stage >> 4));
+                const uint32_t acol = tmem + C::a_col + static_cast<uint32_t>(a.s * (C::chunk / 2));
 #pragma unroll
-                for (int k = 0; k < kChunk / 16; ++k)
-                    mma_tmem_if(one, dcol + (k * 16 / G) * TN, acol + k * 8,
-                                b + (k >> 2) * (C::row_stage / 2 >> 4) + (k & 3) * 2, idesc, k % (G / 16) != 0);
-                commit_if(one, bars.row_empty + r.s);
+                for (int u = 0; u < C::chunk / 128; ++u) {
+                    if (!warp_wait(bars.row_full + r.s, r.ph, abort_flag)) {
+                        timed_out = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t b = b0 + static_cast<uint32_t>(r.s * (C::row_stage >> 4));
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_tmem_if(one, dcol + ((u * 128 + k * 16) / G) * TN, acol + (u * 8 + k) * 8,
+                                    b + (k >> 2) * (C::row_stage / 2 >> 4) + (k & 3) * 2, idesc, k % (G / 16) != 0);
+                    commit_if(one, bars.row_empty + r.s);
+                    issued = true;
+                    r.next<kRowStages>();
+                }
+                if (timed_out) break;
                 commit_if(one, bars.a_empty + a.s);
                 commit_if(one, bars.d_full + d.s);
-                issued = true;
-                r.next<kRowStages>();
-                a.next<kABufs>();
+                a.next<C::a_bufs>();
                 d.next<C::d_bufs>();
             }
         }
@@ -439,103 +499,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             volatile uint32_t never = 0;
             (void)mbar_wait(&bars.drain, 0, &never);
         }
-    } else if (warp == 3) {
-        // ------------------------------------------- scales and zero points
-        // rows lane, lane + 32, .. of the panel; kAhead chunks' loads are issued
-        // before the first is used
-        Ring r;
-        for (int t = first; t < total && !timed_out; t += stride) {
-            const Item it = item_at(lists, p.r.E, panels, t);
-            const Halves h = halves_of(it.panel, swiglu);
-            int64_t at[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = (i < 2 ? h.a : h.b) + (i & 1) * 32 + lane;
-                at[i] = (static_cast<int64_t>(it.e) * p.r.N + min(n, p.r.N - 1)) * p.groups;
-            }
-            const uint16_t* scales = static_cast<const uint16_t*>(p.scales);
-            constexpr int kBatch = kAhead / C::parts;  // chunks whose loads fit the registers
-            for (int cb = c0; cb < c1 && !timed_out; cb += kBatch) {
-                uint16_t s[kBatch][4][C::parts];
-                uint8_t z[kBatch][4][C::parts];
-#pragma unroll
-                for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int g = (cb + b) * C::parts;
-                        if (p.whole && C::parts > 1) {
-                            uint64_t sv = 0;
-                            uint32_t zv = 0x08080808u;
-                            if (cb + b < c1) {
-                                if constexpr (C::parts == 4) {
-                                    sv = *reinterpret_cast<const uint64_t*>(scales + at[i] + g);
-                                    if (p.zeros) zv = *reinterpret_cast<const uint32_t*>(p.zeros + at[i] + g);
-                                } else if constexpr (C::parts == 2) {
-                                    sv = *reinterpret_cast<const uint32_t*>(scales + at[i] + g);
-                                    if (p.zeros) zv = *reinterpret_cast<const uint16_t*>(p.zeros + at[i] + g);
-                                }
-                            }
-#pragma unroll
-                            for (int j = 0; j < C::parts; ++j) {
-                                s[b][i][j] = static_cast<uint16_t>(sv >> (16 * j));
-                                z[b][i][j] = static_cast<uint8_t>(zv >> (8 * j));
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < C::parts; ++j) {
-                                const bool in = cb + b < c1 && g + j < p.groups;
-                                // a group past the row's end has sum 0 and scale 0
-                                s[b][i][j] = in ? scales[at[i] + g + j] : static_cast<uint16_t>(0);
-                                z[b][i][j] = in && p.zeros ? p.zeros[at[i] + g + j] : static_cast<uint8_t>(8);
-                            }
-                        }
-                    }
-#pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    if (cb + b >= c1) break;
-                    if (!warp_wait(bars.p_empty + r.s, r.ph ^ 1u, abort_flag)) {
-                        timed_out = true;
-                        break;
-                    }
-                    uint16_t* ps = reinterpret_cast<uint16_t*>(s_params + r.s * C::param_bytes);
-                    uint8_t* pz = reinterpret_cast<uint8_t*>(ps + C::parts * 128);
-#pragma unroll
-                    for (int j = 0; j < C::parts; ++j)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            ps[j * 128 + i * 32 + lane] = s[b][i][j];
-                            pz[j * 128 + i * 32 + lane] = z[b][i][j];
-                        }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars.p_full + r.s);
-                    r.next<kParams>();
-                }
-            }
-        }
     } else if (warp < 8) {
         // ------------------------------------------------- sums and epilogue
         const int q = warp & 3, me = q * 32 + lane;  // weight row of the panel
         const uint32_t quarter = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        Ring d, pr;
+        Ring d;
         uint32_t join_ph = 0;
         for (int t = first; t < total && !timed_out; t += stride) {
             const Item it = item_at(lists, p.r.E, panels, t);
+            const Halves hv = halves_of(it.panel, swiglu);
             const int wide = (it.rows + 15) & ~15;
+            Stream<C::parts, uint16_t> scales;
+            scales.start(static_cast<const uint16_t*>(p.scales) + weight_row(p, it.e, hv, me) * p.groups, p.groups, p.whole,
+                         0u, c0);
             float acc[TN];
 #pragma unroll
             for (int n = 0; n < TN; ++n) acc[n] = 0.0f;
             for (int c = c0; c < c1; ++c) {
-                if (!warp_wait(bars.p_full + pr.s, pr.ph, abort_flag)) {
-                    timed_out = true;
-                    break;
-                }
-                float s[C::parts];
-                const T* ps = reinterpret_cast<const T*>(s_params + pr.s * C::param_bytes);
-#pragma unroll
-                for (int j = 0; j < C::parts; ++j) s[j] = to_float<T>(ps[j * 128 + me]);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars.p_empty + pr.s);
-                pr.next<kParams>();
+                // a group past the row's end has sum 0, and scale 0
+                uint32_t sbits[C::parts];
+                scales.take(c, sbits);
                 if (!warp_wait(bars.d_full + d.s, d.ph, abort_flag)) {
                     timed_out = true;
                     break;
@@ -544,25 +527,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < C::parts; ++j) {
                     const uint32_t col = quarter + static_cast<uint32_t>(d.s * C::d_cols + j * TN);
+                    const float s = to_float<T>(__builtin_bit_cast(T, static_cast<uint16_t>(sbits[j])));
 #pragma unroll
-                    for (int n0 = 0; n0 < TN; n0 += 32) {
+                    for (int n0 = 0; n0 < TN; n0 += 16) {
                         if (n0 >= wide) break;
-                        uint32_t v[32];
-                        if (wide - n0 > 16) {
-                            tmem_ld32(col + n0, v);
-                        } else {
-                            uint32_t u[16];
-                            tmem_ld16(col + n0, u);
-#pragma unroll
-                            for (int n = 0; n < 32; ++n) v[n] = n < 16 ? u[n & 15] : 0u;
-                        }
+                        uint32_t v[16];
+                        tmem_ld16(col + n0, v);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int n = 0; n < 16; ++n) acc[n0 + n] = fmaf(__uint_as_float(v[n]), s[j], acc[n0 + n]);
-                        if (wide - n0 > 16) {
-#pragma unroll
-                            for (int n = 16; n < 32; ++n) acc[n0 + n] = fmaf(__uint_as_float(v[n]), s[j], acc[n0 + n]);
-                        }
+                        for (int n = 0; n < 16; ++n) acc[n0 + n] = fmaf(__uint_as_float(v[n]), s, acc[n0 + n]);
                     }
                 }
                 tc_fence_before();
@@ -574,36 +547,44 @@ __global__ void __launch_bounds__(kThreads, 1)
             // every CTA of the cluster stores wide / split columns: parts to them
             const int share = wide / split;
             if (!warp_wait(&bars.join_free, join_ph ^ 1u, abort_flag, sum_limit_ns(per))) {
-                timed_out = true;
+                timed_out = true;  // the columns of the item before have not been read
                 break;
             }
-            fence_cluster();
-            {
+            if (split == 1) {
+                float* dst = reinterpret_cast<float*>(s_join) + me;
+#pragma unroll
+                for (int n = 0; n < TN; ++n) {
+                    if (n >= wide) break;
+                    dst[n * 128] = acc[n];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.join_full);
+            } else {
+                fence_cluster();
+                const uint32_t mine = smem_u32(s_join) + static_cast<uint32_t>(rank * share * 512 + me * 4);
                 int to = 0, left = share;
-                uint32_t dst = mapa_shared(smem_u32(s_join) + static_cast<uint32_t>(rank * share * 512 + me * 4), 0);
+                uint32_t dst = mapa_shared(mine, 0);
 #pragma unroll
                 for (int n = 0; n < TN; ++n) {
                     if (n >= wide) break;
                     if (left == 0) {
                         left = share;
-                        ++to;
-                        dst = mapa_shared(smem_u32(s_join) + static_cast<uint32_t>(rank * share * 512 + me * 4),
-                                          static_cast<uint32_t>(to));
+                        dst = mapa_shared(mine, static_cast<uint32_t>(++to));
                     }
                     st_cluster_f32(dst, acc[n]);
                     dst += 512;
                     --left;
                 }
+                fence_cluster();
+                __syncwarp();
+                if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.join_full), static_cast<uint32_t>(lane)));
             }
-            fence_cluster();
-            __syncwarp();
-            if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.join_full), static_cast<uint32_t>(lane)));
             if (!warp_wait(&bars.join_full, join_ph, abort_flag, sum_limit_ns(per))) {
                 timed_out = true;
                 break;
             }
+            if (split > 1) fence_cluster();
             join_ph ^= 1u;
-            fence_cluster();
             // a warp takes every fourth column (with SwiGLU, every fourth two): a
             // token, whose features lie along the lanes, four to each
             const float* join = reinterpret_cast<const float*>(s_join);
@@ -617,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return v;
             };
             const int each = swiglu ? 2 : 1;
-            for (int cb = q * each; cb < share; cb += 4 * each) {
+            for (int cb = q * each; cb < min(share, it.rows - rank * share); cb += 4 * each) {
                 const int c = cb + (swiglu ? lane >> 4 : 0), token = rank * share + c;
                 const int f = swiglu ? 4 * (lane & 15) : 4 * lane, n = it.panel * (swiglu ? 64 : 128) + f;
                 if (c >= share || token >= it.rows || n >= p.columns) continue;
@@ -632,71 +613,63 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float g = p.r.row_scale ? ld_dep(p.r.row_scale + row) : 1.0f;
                 v.x *= g, v.y *= g, v.z *= g, v.w *= g;
-                int from;
-                if (p.src && !picked(p, row, from)) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (p.src && token_row(p, row) < 0) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 *reinterpret_cast<uint2*>(out + row * p.r.ldo + n) = make_uint2(pack2(T(), v.x, v.y), pack2(T(), v.z, v.w));
             }
             __syncwarp();
-            if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.join_free), static_cast<uint32_t>(lane)));
+            if (split == 1) {
+                if (lane == 0) mbar_arrive(&bars.join_free);
+            } else if (lane < split) {
+                mbar_arrive_cluster(mapa_shared(smem_u32(&bars.join_free), static_cast<uint32_t>(lane)));
+            }
         }
     } else {
         // ---------------------------------------------------------- widening
         const int mine = (warp - 8) >> 2, q = warp & 3, me = q * 32 + lane;
         const uint32_t quarter = tmem + (static_cast<uint32_t>(q * 32) << 16) + C::a_col;
-        // 16-byte piece i of row `me` in the 64-byte swizzle
-        const int turn = (me >> 1) & 3;
-        Ring s, a, pr;
+        // 16-byte piece i of row `me` in the 128-byte or 64-byte swizzle
+        const int turn = C::chunk == 256 ? me & 7 : (me >> 1) & 3;
+        Ring s, a;
         int turns = 0;
         for (int t = first; t < total && !timed_out; t += stride) {
+            const Item it = item_at(lists, p.r.E, panels, t);
+            Stream<C::parts, uint8_t> zeros;
+            zeros.start(p.zeros ? p.zeros + weight_row(p, it.e, halves_of(it.panel, swiglu), me) * p.groups : nullptr,
+                        p.groups, p.whole, 8u, c0);
             for (int c = c0; c < c1; ++c) {
+                uint32_t zero[C::parts];
+                zeros.take(c, zero);
                 if ((turns++ & 1) == mine) {
-                    if (!warp_wait(bars.p_full + pr.s, pr.ph, abort_flag)) {
-                        timed_out = true;
-                        break;
-                    }
-                    const uint8_t* pz = s_params + pr.s * C::param_bytes + C::parts * 256;
-                    uint32_t zero[C::parts];
-#pragma unroll
-                    for (int j = 0; j < C::parts; ++j) zero[j] = Wide<T>::magic + pz[j * 128 + me] * 0x00010001u;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars.p_empty + pr.s);
-                    if (!warp_wait(bars.code_full + s.s, s.ph, abort_flag)) {
-                        timed_out = true;
-                        break;
-                    }
-                    const uint4* row = reinterpret_cast<const uint4*>(smem + s.s * kCodeBytes + me * 64);
-                    uint4 w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = row[i ^ turn];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars.code_empty + s.s);
-                    if (!warp_wait(bars.a_empty + a.s, a.ph ^ 1u, abort_flag)) {
+                    if (!warp_wait(bars.code_full + s.s, s.ph, abort_flag) ||
+                        !warp_wait(bars.a_empty + a.s, a.ph ^ 1u, abort_flag)) {
                         timed_out = true;
                         break;
                     }
                     tc_fence_after();
+                    const uint4* row = reinterpret_cast<const uint4*>(smem + s.s * C::code_stage + me * (C::chunk / 2));
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {  // 64 elements, 32 columns
+                    for (int h = 0; h < C::chunk / 64; ++h) {  // 64 elements, 32 columns
                         uint32_t v[32];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const uint4 u = w[2 * h + i];
-                            const uint32_t z = zero[(2 * h + i) * 32 / G];
+                            const uint4 u = row[(2 * h + i) ^ turn];
+                            const uint32_t z = Wide<T>::magic + zero[(2 * h + i) * 32 / G] * 0x00010001u;
                             widen<T>(u.x, z, v + 16 * i);
                             widen<T>(u.y, z, v + 16 * i + 4);
                             widen<T>(u.z, z, v + 16 * i + 8);
                             widen<T>(u.w, z, v + 16 * i + 12);
                         }
-                        tmem_st(quarter + static_cast<uint32_t>(a.s * 64 + h * 32), v);
+                        tmem_st(quarter + static_cast<uint32_t>(a.s * (C::chunk / 2) + h * 32), v);
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars.code_empty + s.s);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bars.a_full + a.s);
                 }
-                s.next<kCodeStages>();
-                a.next<kABufs>();
-                pr.next<kParams>();
+                s.next<C::code_stages>();
+                a.next<C::a_bufs>();
             }
         }
     }
@@ -719,24 +692,20 @@ int split_of(int64_t items, int chunks) {
 }
 
 template <typename T, int G>
-cudaError_t launch(const Int4Product& p, const void* x, int64_t ldx, const void* codes, cudaStream_t st) {
+cudaError_t launch(const Int4Product& p, const void* codes, cudaStream_t st) {
     using C = Cfg<G>;
     static int found[kMaxDevices][4] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    CUtensorMap tW, tX;
+    CUtensorMap tW;
     const uint64_t K = p.r.K, N = p.r.N, E = p.r.E;
     const uint64_t wd[3] = {K / 2, N, E}, ws[2] = {K / 2, N * (K / 2)};
-    const uint32_t wb[3] = {64, 64, 1};
-    const uint64_t xd[2] = {K, static_cast<uint64_t>(p.x_rows)}, xs[1] = {static_cast<uint64_t>(ldx) * 2};
-    const uint32_t xb[2] = {64, p.src ? 1u : 16u};
-    if (!make_tensor_map(&tW, codes, 3, wd, ws, wb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 64) ||
-        !make_tensor_map(&tX, x, 2, xd, xs, xb, Wide<T>::map))
-        return cudaErrorInvalidValue;
+    const uint32_t wb[3] = {C::chunk / 2, 64, 1};
+    if (!make_tensor_map(&tW, codes, 3, wd, ws, wb, CU_TENSOR_MAP_DATA_TYPE_UINT8, C::chunk / 2)) return cudaErrorInvalidValue;
     const int64_t panels = p.swiglu ? p.columns / 64 : (p.r.N + 127) / 128;
     const int64_t items = panels * (p.r.R / C::TN + (p.r.R < p.r.E ? p.r.R : p.r.E));  // at most
-    const int split = split_of(items, static_cast<int>((K + kChunk - 1) / kChunk));
+    const int split = split_of(items, static_cast<int>((K + C::chunk - 1) / C::chunk));
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -762,13 +731,13 @@ cudaError_t launch(const Int4Product& p, const void* x, int64_t ldx, const void*
         n = most > 0 ? most : 1;
     }
     cfg.gridDim = dim3(static_cast<unsigned>(split * (items < n ? items : n)));
-    return cudaLaunchKernelEx(&cfg, k_int4_product<T, G>, tW, tX, p);
+    return cudaLaunchKernelEx(&cfg, k_int4_product<T, G>, tW, p);
 }
 
 template <typename T>
-cudaError_t product(int group, const Int4Product& p, const void* x, int64_t ldx, const void* codes, cudaStream_t st) {
-    if (group == 32) return launch<T, 32>(p, x, ldx, codes, st);
-    return group == 64 ? launch<T, 64>(p, x, ldx, codes, st) : launch<T, 128>(p, x, ldx, codes, st);
+cudaError_t product(int group, const Int4Product& p, const void* codes, cudaStream_t st) {
+    if (group == 32) return launch<T, 32>(p, codes, st);
+    return group == 64 ? launch<T, 64>(p, codes, st) : launch<T, 128>(p, codes, st);
 }
 
 bool aligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -813,6 +782,8 @@ extern "C" moe_status_t moe_grouped_gemm_int4(int32_t group, int32_t dtype, int6
     p.r.out = y;
     p.r.ldo = ldy;
     p.r.status = status;
+    p.x = x;
+    p.ldx = ldx;
     p.x_rows = static_cast<int32_t>(x_rows < INT32_MAX ? x_rows : INT32_MAX);
     p.columns = N;
     p.swiglu = swiglu != 0;
@@ -821,10 +792,9 @@ extern "C" moe_status_t moe_grouped_gemm_int4(int32_t group, int32_t dtype, int6
     p.scales = w_scales;
     p.zeros = static_cast<const uint8_t*>(w_zeros);
     p.groups = (K + group - 1) / group;
-    const int parts = kChunk / group;  // groups of a chunk
-    p.whole = p.groups % parts == 0 && aligned(w_scales, 2 * parts) && aligned(w_zeros, parts);
+    p.whole = p.groups % 8 == 0 && aligned(w_scales, 16) && aligned(w_zeros, 8);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == MOE_DTYPE_BF16 ? product<__nv_bfloat16>(group, p, x, ldx, w_codes, st)
-                                                  : product<__half>(group, p, x, ldx, w_codes, st);
+    const cudaError_t e = dtype == MOE_DTYPE_BF16 ? product<__nv_bfloat16>(group, p, w_codes, st)
+                                                  : product<__half>(group, p, w_codes, st);
     return e == cudaSuccess ? MOE_OK : set_last_error(MOE_ERR_CUDA, "4-bit weight product: %s", cudaGetErrorString(e));
 }
