@@ -40,9 +40,12 @@ namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kCodeBytes = 96 * 1024;  // of the codes in flight
-constexpr int kRowStages = 5;          // of token rows, 128 elements each
-constexpr int kRowLag = 3;             // of them under way before the oldest is waited for
-constexpr int kThreads = 512;
+constexpr int kRowBytes = 80 * 1024;   // of the token rows in flight
+constexpr int kRowStages = 16;         // of 128 elements each, at most
+constexpr int kThreads = 640;
+// Registers per thread of the roles; together no more than the launch's 96 each
+constexpr int kIssueRegs = 56, kSumRegs = 120, kWidenRegs = 88;
+static_assert(kIssueRegs + 2 * kSumRegs + 2 * kWidenRegs <= 5 * 96, "register split");
 constexpr int kMaxSplit = 8;           // CTAs of a cluster
 
 // A chunk's sums are one column per group and token; two chunks' of them and two
@@ -58,9 +61,8 @@ struct Cfg {
     static constexpr int a_bufs = 512 / chunk;
     static constexpr int code_stage = 128 * chunk / 2;
     static constexpr int code_stages = kCodeBytes / code_stage;
-    static constexpr int row_stage = TN * 256;
     static constexpr int join = TN * 512;                // fp32 sums of the columns this CTA stores
-    static constexpr int smem = 1024 + kCodeBytes + kRowStages * row_stage + join + 1024 + 4 * 260 * 4;
+    static constexpr int smem = 1024 + kCodeBytes + kRowBytes + join + 1024 + 4 * 260 * 4;
     static_assert(smem <= 232448, "shared memory budget");
     static_assert(d_bufs * d_cols <= 256 && a_bufs * chunk / 2 <= 256, "tensor memory budget");
 };
@@ -85,7 +87,7 @@ struct Bars {
     uint64_t row_full[kRowStages], row_empty[kRowStages];
     uint64_t a_full[4], a_empty[4];
     uint64_t d_full[4], d_empty[4];
-    uint64_t join_full, join_free, drain;
+    uint64_t join_full[2], join_free[2], summed[2], drain;
     uint32_t tmem, abort;
 };
 static_assert(sizeof(Bars) <= 1024, "barriers");
@@ -159,15 +161,38 @@ __device__ __forceinline__ Item item_at(const Lists& s, int n_groups, int panels
             end = mid;
     }
     Item it;
-    it.e = uniform(e);
+    it.e = e;
     const unsigned i = t - s.first[e], tiles = static_cast<unsigned>(s.first[e + 1] - s.first[e]) / panels;
     const unsigned panel = i / tiles;
     const int width = s.width[e];
-    it.panel = uniform(static_cast<int>(panel));
-    it.row = uniform(s.lo[e] + static_cast<int>(i - panel * tiles) * width);
-    it.rows = uniform(min(width, s.hi[e] - it.row));
+    it.panel = static_cast<int>(panel);
+    it.row = s.lo[e] + static_cast<int>(i - panel * tiles) * width;
+    it.rows = min(width, s.hi[e] - it.row);
     return it;
 }
+
+// A warp's items first, first + stride, ..: the lanes find 32 of them at a time.
+struct Feed {
+    Item mine;
+    int k = 32;
+    __device__ __forceinline__ Item next(const Lists& s, int n_groups, int panels, int total, int t, int stride, int lane) {
+        if (k == 32) {
+            k = 0;
+            const int64_t at = t + static_cast<int64_t>(lane) * stride;
+            if (at < total) mine = item_at(s, n_groups, panels, static_cast<int>(at));
+        }
+        Item it;
+        it.e = __shfl_sync(kAll, mine.e, k);
+        it.panel = __shfl_sync(kAll, mine.panel, k);
+        it.row = __shfl_sync(kAll, mine.row, k);
+        it.rows = __shfl_sync(kAll, mine.rows, k);
+        ++k;
+        return it;
+    }
+};
+
+// Stages of token rows that fit beside one another, for tiles of `wide` rows
+__device__ __forceinline__ int row_stages(int wide) { return min(kRowStages, kRowBytes / (wide * 256)); }
 
 // First weight rows of a panel's two halves of 64.  With SwiGLU the halves are
 // gate and up of the same 64 columns (interleaved per 128 in W).
@@ -243,6 +268,41 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm,
 }
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// A bounded wait of a converged warp.  Many warps wait at a time here, so that the
+// hardware is told to suspend them for longer than it would by itself: polling took
+// half of the issued instructions.
+__device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort,
+                                          uint64_t limit_ns = kWaitLimitNs) {
+    const uint32_t at = smem_u32(bar);
+    auto once = [&]() {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(at), "r"(parity), "r"(20000u)
+            : "memory");
+        return __all_sync(kAll, ok != 0);
+    };
+    if (once()) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!once()) {
+        if (__any_sync(kAll, *abort != 0)) return false;
+        if (__any_sync(kAll, globaltimer_ns() - t0 > limit_ns)) return false;
+    }
+    return true;
+}
+
+template <int N>
+__device__ __forceinline__ void give_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void take_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // The token row of row r of y; -1 where src picks none.
@@ -323,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     uint8_t* s_rows = smem + kCodeBytes;
-    uint8_t* s_join = s_rows + kRowStages * C::row_stage;
+    uint8_t* s_join = s_rows + kRowBytes;
     Bars& bars = *reinterpret_cast<Bars*>(s_join + C::join);
     Lists& lists = *reinterpret_cast<Lists*>(reinterpret_cast<uint8_t*>(&bars) + 1024);
     volatile uint32_t* abort_flag = &bars.abort;
@@ -344,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bars.code_empty + i, 4);  // the warps that widen the chunk
         }
         for (int i = 0; i < kRowStages; ++i) {
-            mbar_init(bars.row_full + i, 2);  // both loading warps
+            mbar_init(bars.row_full + i, 64);  // every lane of both loading warps
             mbar_init(bars.row_empty + i, 1);
         }
         for (int i = 0; i < C::a_bufs; ++i) {
@@ -355,8 +415,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bars.d_full + i, 1);
             mbar_init(bars.d_empty + i, 4);
         }
-        mbar_init(&bars.join_full, 4 * split);  // every summing warp of the cluster
-        mbar_init(&bars.join_free, 4 * split);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bars.join_full + i, 4 * split);  // a summing warpgroup of every CTA of the cluster
+            mbar_init(bars.join_free + i, 4 * split);
+            mbar_init(bars.summed + i, 4);
+        }
         mbar_init(&bars.drain, 1);
         bars.abort = 0;
         fence_mbar_init();
@@ -372,141 +435,168 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = uniform(bars.tmem);
     const int first = blockIdx.x / split, stride = gridDim.x / split;
     bool timed_out = false;
-
-    if (warp == 0) {
-        // ------------------------------------------------------------ codes
-        Ring r;
-        uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
-        for (int t = first; t < total && !timed_out; t += stride) {
-            const Item it = item_at(lists, p.r.E, panels, t);
-            const Halves h = halves_of(it.panel, swiglu);
-            for (int c = c0; c < c1; ++c) {
-                if (!warp_wait(bars.code_empty + r.s, r.ph ^ 1u, abort_flag)) {
-                    timed_out = true;
-                    break;
-                }
-                if (lane == 0) {
-                    uint64_t* bar = bars.code_full + r.s;
-                    const uint32_t dst = smem_u32(smem + r.s * C::code_stage);
-                    mbar_arrive_expect_tx(bar, C::code_stage);
-                    tma_load_3d(dst, &tW, c * (C::chunk / 2), h.a, it.e, bar);
-                    tma_load_3d(dst + C::code_stage / 2, &tW, c * (C::chunk / 2), h.b, it.e, bar);
-                }
-                armed |= 1u << r.s;
-                armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
-                r.next<C::code_stages>();
-            }
-        }
-        if ((timed_out || *abort_flag) && lane == 0) {
-            *abort_flag = 1;
-            for (int i = 0; i < C::code_stages; ++i)
-                if (armed & (1u << i)) {
-                    volatile uint32_t never = 0;
-                    (void)mbar_wait(bars.code_full + i, (armed_par >> i) & 1u, &never);
-                }
-        }
-    } else if (warp == 1 || warp == 3) {
-        // ------------------------------------------------------- token rows
-        // each of the two warps takes 64 of a stage's 128 elements; a lane 16 bytes
-        // of every fourth row, into the 128-byte swizzle
-        const int half = warp >> 1, sub = lane >> 3, piece = lane & 7;
-        const uint32_t even = sub * 128 + ((piece ^ sub) << 4), odd = (sub + 4) * 128 + ((piece ^ (sub + 4)) << 4);
-        const uint8_t* base = static_cast<const uint8_t*>(p.x);
-        const uint32_t dst0 = smem_u32(s_rows + half * (C::row_stage / 2));
-        Ring r, done;
-        int under_way = 0;
-        auto landed = [&]() {  // the oldest stage, once its copies are seen to be complete
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars.row_full + done.s);
-            done.next<kRowStages>();
-            --under_way;
-        };
-        for (int t = first; t < total && !timed_out; t += stride) {
-            const Item it = item_at(lists, p.r.E, panels, t);
-            const int wide = (it.rows + 15) & ~15;
-            int from[TN / 4];
-#pragma unroll
-            for (int i = 0; i < TN / 4; ++i)
-                from[i] = 4 * i + sub < it.rows ? token_row(p, it.row + 4 * i + sub) : -1;
-            for (int k0 = c0 * C::chunk; k0 < c1 * C::chunk; k0 += 128) {
-                if (!warp_wait(bars.row_empty + r.s, r.ph ^ 1u, abort_flag)) {
-                    timed_out = true;
-                    break;
-                }
-                const int k = k0 + half * 64 + piece * 8;
-                const uint32_t dst = dst0 + r.s * C::row_stage;
-#pragma unroll
-                for (int i = 0; i < TN / 4; ++i) {
-                    if (4 * i >= wide) break;
-                    const bool in = from[i] >= 0 && k < p.r.K;
-                    cp_async_16(dst + (i >> 1) * 1024 + (i & 1 ? odd : even),
-                                in ? base + (from[i] * p.ldx + k) * 2 : base, in ? 16 : 0);
-                }
-                cp_async_commit();
-                r.next<kRowStages>();
-                if (++under_way > kRowLag) {
-                    cp_async_wait<kRowLag>();
-                    landed();
-                }
-            }
-        }
-        cp_async_wait<0>();
-        while (under_way > 0) landed();
-    } else if (warp == 2) {
-        // ------------------------------------------------------------- MMAs
-        const uint32_t one = elect_one();
-        const uint64_t b0 = sdesc_sw128(smem_u32(s_rows));
-        Ring r, a, d;
-        bool issued = false;
-        for (int t = first; t < total && !timed_out; t += stride) {
-            const Item it = item_at(lists, p.r.E, panels, t);
-            const uint32_t idesc = (1u << 4) | (Wide<T>::format << 7) | (Wide<T>::format << 10) |
-                                   (static_cast<uint32_t>((it.rows + 15) >> 4) << 18) | (8u << 24);
-            for (int c = c0; c < c1 && !timed_out; ++c) {
-                if (!warp_wait(bars.d_empty + d.s, d.ph ^ 1u, abort_flag) || !warp_wait(bars.a_full + a.s, a.ph, abort_flag)) {
-                    timed_out = true;
-                    break;
-                }
-                const uint32_t dcol = tmem + static_cast<uint32_t>(d.s * C::d_cols);
-                const uint32_t acol = tmem + C::a_col + static_cast<uint32_t>(a.s * (C::chunk / 2));
-#pragma unroll
-                for (int u = 0; u < C::chunk / 128; ++u) {
-                    if (!warp_wait(bars.row_full + r.s, r.ph, abort_flag)) {
+    // a warpgroup takes its registers with one instruction
+    if (warp < 4) {
+        give_registers<kIssueRegs>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ codes
+            Feed feed;
+            Ring r;
+            uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
+            for (int t = first; t < total && !timed_out; t += stride) {
+                const Item it = feed.next(lists, p.r.E, panels, total, t, stride, lane);
+                const Halves h = halves_of(it.panel, swiglu);
+                for (int c = c0; c < c1; ++c) {
+                    if (!role_wait(bars.code_empty + r.s, r.ph ^ 1u, abort_flag)) {
                         timed_out = true;
                         break;
                     }
-                    tc_fence_after();
-                    const uint64_t b = b0 + static_cast<uint32_t>(r.s * (C::row_stage >> 4));
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_tmem_if(one, dcol + ((u * 128 + k * 16) / G) * TN, acol + (u * 8 + k) * 8,
-                                    b + (k >> 2) * (C::row_stage / 2 >> 4) + (k & 3) * 2, idesc, k % (G / 16) != 0);
-                    commit_if(one, bars.row_empty + r.s);
-                    issued = true;
-                    r.next<kRowStages>();
+                    if (lane == 0) {
+                        uint64_t* bar = bars.code_full + r.s;
+                        const uint32_t dst = smem_u32(smem + r.s * C::code_stage);
+                        mbar_arrive_expect_tx(bar, C::code_stage);
+                        tma_load_3d(dst, &tW, c * (C::chunk / 2), h.a, it.e, bar);
+                        tma_load_3d(dst + C::code_stage / 2, &tW, c * (C::chunk / 2), h.b, it.e, bar);
+                    }
+                    armed |= 1u << r.s;
+                    armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
+                    r.next<C::code_stages>();
                 }
-                if (timed_out) break;
-                commit_if(one, bars.a_empty + a.s);
-                commit_if(one, bars.d_full + d.s);
-                a.next<C::a_bufs>();
-                d.next<C::d_bufs>();
+            }
+            if ((timed_out || *abort_flag) && lane == 0) {
+                *abort_flag = 1;
+                for (int i = 0; i < C::code_stages; ++i)
+                    if (armed & (1u << i)) {
+                        volatile uint32_t never = 0;
+                        (void)mbar_wait(bars.code_full + i, (armed_par >> i) & 1u, &never);
+                    }
+            }
+        } else if (warp == 1 || warp == 3) {
+            // ------------------------------------------------------- token rows
+            // each of the two warps takes 64 of a stage's 128 elements; a lane 16 bytes
+            // of every fourth row, into the 128-byte swizzle, whose 8-row atoms of the
+            // two halves alternate.  As many stages as tiles of this width leave room
+            // for; where the width changes, they are all waited for first.
+            Feed feed;
+            const int half = warp >> 1, sub = lane >> 3, piece = lane & 7;
+            const uint32_t even = sub * 128 + ((piece ^ sub) << 4), odd = (sub + 4) * 128 + ((piece ^ (sub + 4)) << 4);
+            const uint8_t* base = static_cast<const uint8_t*>(p.x);
+            const uint32_t dst0 = smem_u32(s_rows) + half * 1024;
+            int n_stages = 0, s = 0;
+            uint32_t used = 0;  // parity of each stage's uses
+            for (int t = first; t < total && !timed_out; t += stride) {
+                const Item it = feed.next(lists, p.r.E, panels, total, t, stride, lane);
+                const int wide = (it.rows + 15) & ~15;
+                if (row_stages(wide) != n_stages) {
+                    for (int i = 0; i < n_stages && !timed_out; ++i)
+                        timed_out = !role_wait(bars.row_empty + i, (used >> i & 1u) ^ 1u, abort_flag);
+                    n_stages = row_stages(wide);
+                    s = 0;
+                }
+                int from[TN / 4];
+#pragma unroll
+                for (int i = 0; i < TN / 4; ++i)
+                    from[i] = 4 * i + sub < it.rows ? token_row(p, it.row + 4 * i + sub) : -1;
+                for (int k0 = c0 * C::chunk; k0 < c1 * C::chunk && !timed_out; k0 += 128) {
+                    if (!role_wait(bars.row_empty + s, (used >> s & 1u) ^ 1u, abort_flag)) {
+                        timed_out = true;
+                        break;
+                    }
+                    const int k = k0 + half * 64 + piece * 8;
+                    const uint32_t dst = dst0 + s * wide * 256;
+#pragma unroll
+                    for (int i = 0; i < TN / 4; ++i) {
+                        if (4 * i >= wide) break;
+                        const bool in = from[i] >= 0 && k < p.r.K;
+                        cp_async_16(dst + (i >> 1) * 2048 + (i & 1 ? odd : even),
+                                    in ? base + (from[i] * p.ldx + k) * 2 : base, in ? 16 : 0);
+                    }
+                    cp_async_arrive(bars.row_full + s);
+                    used ^= 1u << s;
+                    if (++s == n_stages) s = 0;
+                }
+            }
+            // nothing of this CTA's shared memory may still be written to at exit
+            cp_async_commit();
+            cp_async_wait<0>();
+        } else if (warp == 2) {
+            // ------------------------------------------------------------- MMAs
+            Feed feed;
+            const uint32_t one = elect_one();
+            // 8-row atoms 2048 bytes apart: those of the two halves alternate
+            const uint64_t b0 = sdesc_sw128(smem_u32(s_rows)) + (static_cast<uint64_t>(1024u >> 4) << 32);
+            Ring a, d;
+            int n_stages = 0, s = 0;
+            uint32_t used = 0;
+            bool issued = false;
+            for (int t = first; t < total && !timed_out; t += stride) {
+                const Item it = feed.next(lists, p.r.E, panels, total, t, stride, lane);
+                const int wide = (it.rows + 15) & ~15;
+                if (row_stages(wide) != n_stages) {
+                    n_stages = row_stages(wide);
+                    s = 0;
+                }
+                const uint32_t idesc = (1u << 4) | (Wide<T>::format << 7) | (Wide<T>::format << 10) |
+                                       (static_cast<uint32_t>(wide >> 3) << 17) | (8u << 24);
+                for (int c = c0; c < c1 && !timed_out; ++c) {
+                    if (!role_wait(bars.d_empty + d.s, d.ph ^ 1u, abort_flag) || !role_wait(bars.a_full + a.s, a.ph, abort_flag)) {
+                        timed_out = true;
+                        break;
+                    }
+                    const uint32_t dcol = tmem + static_cast<uint32_t>(d.s * C::d_cols);
+                    const uint32_t acol = tmem + C::a_col + static_cast<uint32_t>(a.s * (C::chunk / 2));
+#pragma unroll
+                    for (int u = 0; u < C::chunk / 128; ++u) {
+                        if (!role_wait(bars.row_full + s, used >> s & 1u, abort_flag)) {
+                            timed_out = true;
+                            break;
+                        }
+                        fence_proxy_async_smem();  // the rows came through the generic proxy
+                        tc_fence_after();
+                        const uint64_t b = b0 + static_cast<uint32_t>(s * wide * 16);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_tmem_if(one, dcol + ((u * 128 + k * 16) / G) * TN, acol + (u * 8 + k) * 8,
+                                        b + (k >> 2) * 64 + (k & 3) * 2, idesc, k % (G / 16) != 0);
+                        commit_if(one, bars.row_empty + s);
+                        issued = true;
+                        used ^= 1u << s;
+                        if (++s == n_stages) s = 0;
+                    }
+                    if (timed_out) break;
+                    commit_if(one, bars.a_empty + a.s);
+                    commit_if(one, bars.d_full + d.s);
+                    a.next<C::a_bufs>();
+                    d.next<C::d_bufs>();
+                }
+            }
+            if ((timed_out || *abort_flag) && issued && one) {
+                *abort_flag = 1;
+                mma_commit(&bars.drain);
+                volatile uint32_t never = 0;
+                (void)mbar_wait(&bars.drain, 0, &never);
             }
         }
-        if ((timed_out || *abort_flag) && issued && one) {
-            *abort_flag = 1;
-            mma_commit(&bars.drain);
-            volatile uint32_t never = 0;
-            (void)mbar_wait(&bars.drain, 0, &never);
-        }
-    } else if (warp < 8) {
+    } else if (warp < 12) {
+        take_registers<kSumRegs>();
         // ------------------------------------------------- sums and epilogue
         const int q = warp & 3, me = q * 32 + lane;  // weight row of the panel
         const uint32_t quarter = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        Feed feed;
         Ring d;
-        uint32_t join_ph = 0;
-        for (int t = first; t < total && !timed_out; t += stride) {
-            const Item it = item_at(lists, p.r.E, panels, t);
+        // The two warpgroups take the items in turn: one's epilogue runs beside the
+        // other's sums.  Each item's barriers are those of its warpgroup, so that a
+        // phase is waited for only once the phase before it has been: a parity says
+        // no more than that.
+        const int w = warp >> 3;
+        int turn = 0;
+        for (int t = first; t < total && !timed_out; t += stride, ++turn) {
+            const Item it = feed.next(lists, p.r.E, panels, total, t, stride, lane);
+            if ((turn & 1) != w) {
+                for (int c = c0; c < c1; ++c) d.next<C::d_bufs>();
+                continue;
+            }
+            const uint32_t ph = turn >> 1 & 1, other_ph = w ? ph : ph ^ 1u;  // of the item before: none, at first
             const Halves hv = halves_of(it.panel, swiglu);
             const int wide = (it.rows + 15) & ~15;
             Stream<C::parts, uint16_t> scales;
@@ -515,11 +605,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             float acc[TN];
 #pragma unroll
             for (int n = 0; n < TN; ++n) acc[n] = 0.0f;
+            // the sums of the item before have been taken
+            if (!role_wait(bars.summed + (w ^ 1), other_ph, abort_flag, sum_limit_ns(per))) {
+                timed_out = true;
+                break;
+            }
             for (int c = c0; c < c1; ++c) {
                 // a group past the row's end has sum 0, and scale 0
                 uint32_t sbits[C::parts];
                 scales.take(c, sbits);
-                if (!warp_wait(bars.d_full + d.s, d.ph, abort_flag)) {
+                if (!role_wait(bars.d_full + d.s, d.ph, abort_flag)) {
                     timed_out = true;
                     break;
                 }
@@ -544,9 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 d.next<C::d_bufs>();
             }
             if (timed_out) break;
+            if (lane == 0) mbar_arrive(bars.summed + w);
             // every CTA of the cluster stores wide / split columns: parts to them
             const int share = wide / split;
-            if (!warp_wait(&bars.join_free, join_ph ^ 1u, abort_flag, sum_limit_ns(per))) {
+            if (!role_wait(bars.join_free + (w ^ 1), other_ph, abort_flag, sum_limit_ns(per))) {
                 timed_out = true;  // the columns of the item before have not been read
                 break;
             }
@@ -558,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     dst[n * 128] = acc[n];
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.join_full);
+                if (lane == 0) mbar_arrive(bars.join_full + w);
             } else {
                 fence_cluster();
                 const uint32_t mine = smem_u32(s_join) + static_cast<uint32_t>(rank * share * 512 + me * 4);
@@ -577,14 +673,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fence_cluster();
                 __syncwarp();
-                if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.join_full), static_cast<uint32_t>(lane)));
+                if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(bars.join_full + w), static_cast<uint32_t>(lane)));
             }
-            if (!warp_wait(&bars.join_full, join_ph, abort_flag, sum_limit_ns(per))) {
+            if (!role_wait(bars.join_full + w, ph, abort_flag, sum_limit_ns(per))) {
                 timed_out = true;
                 break;
             }
             if (split > 1) fence_cluster();
-            join_ph ^= 1u;
             // a warp takes every fourth column (with SwiGLU, every fourth two): a
             // token, whose features lie along the lanes, four to each
             const float* join = reinterpret_cast<const float*>(s_join);
@@ -618,21 +713,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (split == 1) {
-                if (lane == 0) mbar_arrive(&bars.join_free);
+                if (lane == 0) mbar_arrive(bars.join_free + w);
             } else if (lane < split) {
-                mbar_arrive_cluster(mapa_shared(smem_u32(&bars.join_free), static_cast<uint32_t>(lane)));
+                mbar_arrive_cluster(mapa_shared(smem_u32(bars.join_free + w), static_cast<uint32_t>(lane)));
             }
         }
     } else {
         // ---------------------------------------------------------- widening
-        const int mine = (warp - 8) >> 2, q = warp & 3, me = q * 32 + lane;
+        give_registers<kWidenRegs>();
+        Feed feed;
+        const int mine = (warp - 12) >> 2, q = warp & 3, me = q * 32 + lane;
         const uint32_t quarter = tmem + (static_cast<uint32_t>(q * 32) << 16) + C::a_col;
         // 16-byte piece i of row `me` in the 128-byte or 64-byte swizzle
         const int turn = C::chunk == 256 ? me & 7 : (me >> 1) & 3;
         Ring s, a;
         int turns = 0;
         for (int t = first; t < total && !timed_out; t += stride) {
-            const Item it = item_at(lists, p.r.E, panels, t);
+            const Item it = feed.next(lists, p.r.E, panels, total, t, stride, lane);
             Stream<C::parts, uint8_t> zeros;
             zeros.start(p.zeros ? p.zeros + weight_row(p, it.e, halves_of(it.panel, swiglu), me) * p.groups : nullptr,
                         p.groups, p.whole, 8u, c0);
@@ -640,8 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t zero[C::parts];
                 zeros.take(c, zero);
                 if ((turns++ & 1) == mine) {
-                    if (!warp_wait(bars.code_full + s.s, s.ph, abort_flag) ||
-                        !warp_wait(bars.a_empty + a.s, a.ph ^ 1u, abort_flag)) {
+                    if (!role_wait(bars.code_full + s.s, s.ph, abort_flag) ||
+                        !role_wait(bars.a_empty + a.s, a.ph ^ 1u, abort_flag)) {
                         timed_out = true;
                         break;
                     }
