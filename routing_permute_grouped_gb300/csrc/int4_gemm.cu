@@ -5,24 +5,25 @@
 // k.  code - zero is a small integer, exact in 16 bits, so the tensor cores sum a
 // group's products as they are, and each group's sum is scaled once, in fp32.
 //
-// The weights are the MMA's M side: 128 rows of W[e], widened in registers and
-// written to tensor memory, from where tcgen05.mma takes its A operand; the token
-// rows are its N side (16 to 64 of them, a multiple of 16), staged by TMA.  A work
-// item is such a panel of weight rows times a tile of token rows; the sum runs
-// over chunks of 128 elements.  One CTA of 16 warps per SM:
-//   warp 0       TMA of the codes (12 chunks of 8 KB in flight)
-//   warp 1       TMA of the token rows (gather4 where src picks them)
-//   warp 2       issues the MMAs
-//   warp 3       scales and zero points, a few chunks ahead, into shared memory
-//   warps 4-7    take a chunk's sums (one per group) out of tensor memory, scale
-//                and add them in registers, one weight row per thread; the epilogue
-//   warps 8-15   widen codes, the two halves taking the chunks in turn
+// Few token rows: the weights' bytes set the pace, and what has to keep up with
+// them is the widening of the codes, 11 instructions for 8 codes.  So nothing is
+// handed from warp to warp: a warp streams 32 weight rows (with SwiGLU 16 of gate
+// and the same 16 of up) straight into registers in the layout of the A operand of
+// mma.m16n8k16, a few chunks of 128 elements ahead, widens them in place and
+// multiplies them by 8 or 16 token rows, which it reads as the B operand through
+// L1.  (The same product with the widened weights written to tensor memory for
+// tcgen05.mma spends as much again on barriers, tensor-memory stores and sums read
+// back per group: 195 us where this takes FIXME.)
+//
+// The order of k inside a group is free as long as both operands share it: a lane
+// takes whole 32-bit words, and one word's eight elements are its part of two
+// steps of 16.  All of a step's elements lie in one group of scales, so a lane's
+// load is 4, 2 or 1 words for groups of 128, 64 or 32.
+//
 // A code becomes a 16-bit number by or-ing it into the mantissa of 128 (bf16) or
 // 1024 (f16), from which 128 + zero or 1024 + zero is then subtracted exactly.
 //
-// Few items and a long sum: the CTAs of a cluster split the sum; each hands its
-// part of every column to the CTA that stores it, which adds the parts in the
-// CTAs' order.
+// Few items: the warps of a CTA split the sum and add their parts in order.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -39,33 +40,12 @@ namespace moe {
 namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr int kCodeBytes = 96 * 1024;  // of the codes in flight
-constexpr int kRowBytes = 80 * 1024;   // of the token rows in flight
-constexpr int kRowStages = 16;         // of 128 elements each, at most
-constexpr int kThreads = 640;
-// Registers per thread of the roles; together no more than the launch's 96 each
-constexpr int kIssueRegs = 56, kSumRegs = 120, kWidenRegs = 88;
-static_assert(kIssueRegs + 2 * kSumRegs + 2 * kWidenRegs <= 5 * 96, "register split");
-constexpr int kMaxSplit = 8;           // CTAs of a cluster
-
-// A chunk's sums are one column per group and token; two chunks' of them and two
-// widened chunks (half a column per element) share tensor memory.
-template <int G>
-struct Cfg {
-    static constexpr int chunk = G == 128 ? 256 : 128;   // elements of the sum per step
-    static constexpr int parts = chunk / G;              // groups of a chunk
-    static constexpr int TN = G == 32 ? 32 : 64;         // token rows of a tile, at most
-    static constexpr int d_cols = parts * TN;            // a chunk's sums
-    static constexpr int d_bufs = 256 / d_cols;
-    static constexpr uint32_t a_col = 256;               // the first widened chunk's column
-    static constexpr int a_bufs = 512 / chunk;
-    static constexpr int code_stage = 128 * chunk / 2;
-    static constexpr int code_stages = kCodeBytes / code_stage;
-    static constexpr int join = TN * 512;                // fp32 sums of the columns this CTA stores
-    static constexpr int smem = 1024 + kCodeBytes + kRowBytes + join + 1024 + 4 * 260 * 4;
-    static_assert(smem <= 232448, "shared memory budget");
-    static_assert(d_bufs * d_cols <= 256 && a_bufs * chunk / 2 <= 256, "tensor memory budget");
-};
+constexpr int kChunk = 128;   // elements of the sum per step
+constexpr int kWarps = 8;     // of a CTA, two CTAs to an SM
+constexpr int kTile = 16;     // token rows of an item, at most
+constexpr int kStages = 4;    // chunks of a warp in shared memory
+constexpr int kStageBytes = 32 * 64;
+constexpr int kSmem = kWarps * kStages * kStageBytes;
 
 struct Int4Product {
     RaggedArgs r;          // N: weight rows per group
@@ -76,21 +56,13 @@ struct Int4Product {
     int32_t swiglu;
     const int32_t* src;    // [R] or null
     int32_t src_div;
+    const uint8_t* codes;  // [E, N, K / 2]
     const void* scales;    // [E, N, groups]
     const uint8_t* zeros;  // the same, or null
     int32_t groups;        // per weight row
-    int32_t whole;         // scales and zero points can be read eight groups at a time
+    int32_t whole;         // a chunk's scales and zero points can be read at once
+    int32_t split;         // warps that share a sum: 1, 2, 4 or 8
 };
-
-struct Bars {
-    uint64_t code_full[12], code_empty[12];
-    uint64_t row_full[kRowStages], row_empty[kRowStages];
-    uint64_t a_full[4], a_empty[4];
-    uint64_t d_full[4], d_empty[4];
-    uint64_t join_full[2], join_free[2], summed[2], drain;
-    uint32_t tmem, abort;
-};
-static_assert(sizeof(Bars) <= 1024, "barriers");
 
 // Rows [lo, hi) of every group, its token tiles' width and its first work item
 struct Lists {
@@ -104,7 +76,6 @@ struct Item {
 
 // All threads: thread e takes group e.  Where a group is bad, groups may overlap:
 // each then starts past the ends of those before it.
-template <int TN>
 __device__ __forceinline__ int build_lists(const RaggedArgs& a, Lists& s, int panels) {
     __shared__ int sums[8];
     const int e = threadIdx.x, lane = e & 31;
@@ -122,21 +93,19 @@ __device__ __forceinline__ int build_lists(const RaggedArgs& a, Lists& s, int pa
             }
         __syncthreads();
     }
-    int n = 0, x = 0;
-    if (e < 256) {
-        if (e < a.E) {
-            const int len = s.hi[e] - s.lo[e], tiles = (len + TN - 1) / TN;
-            s.width[e] = tiles ? ((len + tiles - 1) / tiles + 15) & ~15 : 16;
-            n = tiles * panels;
-        }
-        x = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kAll, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) sums[e >> 5] = x;
+    int n = 0;
+    if (e < a.E) {
+        const int len = s.hi[e] - s.lo[e], tiles = (len + kTile - 1) / kTile;
+        s.width[e] = tiles ? ((len + tiles - 1) / tiles + 7) & ~7 : 8;
+        n = tiles * panels;
     }
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kAll, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[e >> 5] = x;
     __syncthreads();
     int total = 0, before = 0;
 #pragma unroll
@@ -146,6 +115,7 @@ __device__ __forceinline__ int build_lists(const RaggedArgs& a, Lists& s, int pa
     }
     if (e < a.E) s.first[e] = before + x - n;
     if (e == 0) s.first[a.E] = total;
+    __syncthreads();
     return total;
 }
 
@@ -171,138 +141,38 @@ __device__ __forceinline__ Item item_at(const Lists& s, int n_groups, int panels
     return it;
 }
 
-// A warp's items first, first + stride, ..: the lanes find 32 of them at a time.
-struct Feed {
-    Item mine;
-    int k = 32;
-    __device__ __forceinline__ Item next(const Lists& s, int n_groups, int panels, int total, int t, int stride, int lane) {
-        if (k == 32) {
-            k = 0;
-            const int64_t at = t + static_cast<int64_t>(lane) * stride;
-            if (at < total) mine = item_at(s, n_groups, panels, static_cast<int>(at));
-        }
-        Item it;
-        it.e = __shfl_sync(kAll, mine.e, k);
-        it.panel = __shfl_sync(kAll, mine.panel, k);
-        it.row = __shfl_sync(kAll, mine.row, k);
-        it.rows = __shfl_sync(kAll, mine.rows, k);
-        ++k;
-        return it;
-    }
-};
-
-// Stages of token rows that fit beside one another, for tiles of `wide` rows
-__device__ __forceinline__ int row_stages(int wide) { return min(kRowStages, kRowBytes / (wide * 256)); }
-
-// First weight rows of a panel's two halves of 64.  With SwiGLU the halves are
-// gate and up of the same 64 columns (interleaved per 128 in W).
-struct Halves {
-    int a, b;
-};
-__device__ __forceinline__ Halves halves_of(int panel, bool swiglu) {
-    if (swiglu) {
-        const int gate = (panel >> 1) * 256 + (panel & 1) * 64;
-        return {gate, gate + 128};
-    }
-    return {panel * 128, panel * 128 + 64};
-}
-
-// Row `me` of the panel among the weight rows; past the last one, the last.
-__device__ __forceinline__ int64_t weight_row(const Int4Product& p, int e, const Halves& h, int me) {
-    const int n = me < 64 ? h.a + me : h.b + me - 64;
-    return static_cast<int64_t>(e) * p.r.N + min(n, p.r.N - 1);
-}
-
 template <typename T>
 struct Wide;
 template <>
 struct Wide<__nv_bfloat16> {
     static constexpr uint32_t magic = 0x43004300u;  // 128
-    static constexpr uint32_t format = 1;
     __device__ static __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
         const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
         return *reinterpret_cast<const uint32_t*>(&r);
+    }
+    __device__ static __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
 };
 template <>
 struct Wide<__half> {
     static constexpr uint32_t magic = 0x64006400u;  // 1024
-    static constexpr uint32_t format = 0;
     __device__ static __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
         const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
         return *reinterpret_cast<const uint32_t*>(&r);
     }
-};
-// Eight codes to four pairs of numbers; zero is magic + zero point in both halves.
-template <typename T>
-__device__ __forceinline__ void widen(uint32_t w, uint32_t zero, uint32_t* v) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = Wide<T>::sub((w >> (4 * i) & 0x000F000Fu) | Wide<T>::magic, zero);
-}
-
-// D[tmem] (+)= A[tmem] * B[smem]^T, M = 128, K = 16, where `one` is set.
-__device__ __forceinline__ void mma_tmem_if(uint32_t one, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "setp.ne.b32 q, %4, 0;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t}" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
-        : "memory");
-}
-__device__ __forceinline__ void commit_if(uint32_t one, uint64_t* bar) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %1, 0;\n\t"
-        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-        "r"(one)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
-            "r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
-// A bounded wait of a converged warp.  Many warps wait at a time here, so that the
-// hardware is told to suspend them for longer than it would by itself: polling took
-// half of the issued instructions.
-__device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort,
-                                          uint64_t limit_ns = kWaitLimitNs) {
-    const uint32_t at = smem_u32(bar);
-    auto once = [&]() {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(at), "r"(parity), "r"(20000u)
-            : "memory");
-        return __all_sync(kAll, ok != 0);
-    };
-    if (once()) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!once()) {
-        if (__any_sync(kAll, *abort != 0)) return false;
-        if (__any_sync(kAll, globaltimer_ns() - t0 > limit_ns)) return false;
+    __device__ static __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
-    return true;
-}
-
-template <int N>
-__device__ __forceinline__ void give_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void take_registers() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+};
+// Pair i of a word's eight codes as numbers; zero is magic + zero point in both halves.
+template <typename T>
+__device__ __forceinline__ uint32_t widen(uint32_t w, int i, uint32_t zero) {
+    return Wide<T>::sub((w >> (4 * i) & 0x000F000Fu) | Wide<T>::magic, zero);
 }
 
 // The token row of row r of y; -1 where src picks none.
@@ -312,529 +182,269 @@ __device__ __forceinline__ int token_row(const Int4Product& p, int r) {
     return s >= 0 && from < p.x_rows ? from : -1;
 }
 
-// Eight scales (16 bits each) or zero points (8) of a weight row, by the chunk:
-// a row's are read eight groups at a time, one read ahead, where they are aligned
-// for it, else each by itself, a chunk ahead.
-template <int PARTS, typename E>
-struct Stream {
-    using Eight = std::conditional_t<sizeof(E) == 2, uint4, uint2>;
-    const E* at;
-    int groups, whole;
-    uint32_t absent;
-    Eight now, ahead;
-    uint32_t one[PARTS];
-    __device__ __forceinline__ Eight eight(int g) const {
-        Eight v{};
-        if (g < groups) v = *reinterpret_cast<const Eight*>(at + g);
-        return v;
+template <typename T, int G>
+struct Warp {
+    static constexpr int parts = kChunk / G, words = 4 / parts;  // groups of a chunk, words of a lane in each
+    const Int4Product& p;
+    const uint8_t* codes;    // this lane's 16 bytes of a chunk of its first weight row
+    int64_t to[3];           // from there to its other three
+    int64_t par_row;         // the weight row whose scales this lane reads, times the groups of a row
+    uint32_t ring;           // the warp's stages in shared memory
+    int lane, t4, last;      // lane % 4, last chunk
+
+    // 32 rows x 64 bytes; a row's 16-byte pieces in an order that its number gives,
+    // so that reading one piece of eight rows meets no bank twice.  Past the end of
+    // a row any of its codes will do: they meet token rows that read as zero.
+    __device__ __forceinline__ void load(int stage, int c) const {
+        const int at = min(c * 64, p.r.K / 2 - 16 - t4 * 16);
+        const int g = lane >> 2;
+        const uint32_t dst = ring + stage * kStageBytes + g * 64 + ((t4 ^ (g >> 1 & 3)) << 4);
+        const uint8_t* q = codes + at;
+        cp_async_16(dst, q, 16);
+        cp_async_16(dst + 512, q + to[0], 16);
+        cp_async_16(dst + 1024, q + to[1], 16);
+        cp_async_16(dst + 1536, q + to[2], 16);
     }
-    __device__ __forceinline__ void single(int c) {
+    // Word w (of four) of the lane in row lane / 4 + 8 i.
+    __device__ __forceinline__ void codes_of(int stage, int j, uint32_t (&q)[4][words]) const {
+        const int g = lane >> 2, piece = words == 4 ? t4 : words == 2 ? 2 * j + (t4 >> 1) : j;
+        const uint32_t at = ring + stage * kStageBytes + g * 64 + ((piece ^ (g >> 1 & 3)) << 4) +
+                            (words == 4 ? 0 : words == 2 ? (t4 & 1) * 8 : t4 * 4);
 #pragma unroll
-        for (int j = 0; j < PARTS; ++j) one[j] = c * PARTS + j < groups ? at[c * PARTS + j] : absent;
-    }
-    __device__ __forceinline__ void start(const E* row, int n, int aligned, uint32_t none, int c) {
-        at = row;
-        groups = n;
-        whole = aligned;
-        absent = none;
-        if (!row) return;
-        if (whole) {
-            now = eight(c * PARTS & ~7);
-            ahead = eight((c * PARTS & ~7) + 8);
-        } else {
-            single(c);
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (words == 4)
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(q[i][0]), "=r"(q[i][1]), "=r"(q[i][2]), "=r"(q[i][3])
+                             : "r"(at + 512 * i)
+                             : "memory");
+            else if constexpr (words == 2)
+                asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(q[i][0]), "=r"(q[i][1]) : "r"(at + 512 * i) : "memory");
+            else
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(q[i][0]) : "r"(at + 512 * i) : "memory");
         }
     }
-    // Those of chunk c; the chunks follow one another.
-    __device__ __forceinline__ void take(int c, uint32_t (&v)[PARTS]) {
-        if (!at) {
+    // Scales, zero points << 16; past the last group the last one's, for sums of 0.
+    __device__ __forceinline__ void params(int c, uint32_t (&par)[parts]) const {
+        c = min(c, last);
+        const uint16_t* sc = static_cast<const uint16_t*>(p.scales) + par_row;
+        const uint8_t* z = p.zeros + par_row;
+        if (parts == 1 || !p.whole) {
 #pragma unroll
-            for (int j = 0; j < PARTS; ++j) v[j] = absent;
-        } else if (whole) {
-            const uint32_t* w = &now.x;
-#pragma unroll
-            for (int j = 0; j < PARTS; ++j) {
-                const int g = (c * PARTS + j) & 7;
-                if constexpr (sizeof(E) == 2) {
-                    const uint32_t u = g & 4 ? (g & 2 ? w[3] : w[2]) : (g & 2 ? w[1] : w[0]);
-                    v[j] = g & 1 ? u >> 16 : u & 0xFFFFu;
-                } else {
-                    v[j] = (g & 4 ? w[1] : w[0]) >> (8 * (g & 3)) & 0xFFu;
-                }
+            for (int j = 0; j < parts; ++j) {
+                const int at = min(c * parts + j, p.groups - 1);
+                par[j] = sc[at] | (p.zeros ? z[at] : 8u) << 16;
             }
-            if (((c + 1) * PARTS & 7) == 0) {
-                now = ahead;
-                ahead = eight((c + 1) * PARTS + 8);
-            }
-        } else {
+        } else if constexpr (parts == 2) {
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(sc + c * parts);
+            const uint32_t w = p.zeros ? *reinterpret_cast<const uint16_t*>(z + c * parts) : 0x0808u;
+            par[0] = (v & 0xFFFFu) | (w & 0xFFu) << 16;
+            par[1] = v >> 16 | (w >> 8) << 16;
+        } else if constexpr (parts == 4) {
+            const uint2 v = *reinterpret_cast<const uint2*>(sc + c * parts);
+            const uint32_t w = p.zeros ? *reinterpret_cast<const uint32_t*>(z + c * parts) : 0x08080808u;
+            par[0] = (v.x & 0xFFFFu) | (w & 0xFFu) << 16;
+            par[1] = v.x >> 16 | (w >> 8 & 0xFFu) << 16;
+            par[2] = (v.y & 0xFFFFu) | (w >> 16 & 0xFFu) << 16;
+            par[3] = v.y >> 16 | (w >> 24) << 16;
+        }
+    }
+
+    // sum[m][n]: 16 weight rows m by 8 token rows n; x[n]: this lane's token row, or null
+    template <int NT>
+    __device__ __forceinline__ void chunk(int stage, int c, const uint32_t (&par)[parts], const T* const (&x)[NT],
+                                          float (&sum)[2][NT][4]) const {
+        uint4 b[2][NT];  // of this word and the next
+        auto fetch = [&](int w) {
 #pragma unroll
-            for (int j = 0; j < PARTS; ++j) v[j] = one[j];
-            single(c + 1);
+            for (int n = 0; n < NT; ++n) {
+                const int k = c * kChunk + ((w / words * 4 + t4) * words + w % words) * 8;
+                b[w & 1][n] = make_uint4(0, 0, 0, 0);
+                if (x[n] && k < p.r.K) b[w & 1][n] = *reinterpret_cast<const uint4*>(x[n] + k);
+            }
+        };
+        fetch(0);
+#pragma unroll
+        for (int j = 0; j < parts; ++j) {
+            float scale[4];
+            uint32_t zero[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t v = __shfl_sync(kAll, par[j], (lane & ~3) | i);
+                scale[i] = to_float<T>(__builtin_bit_cast(T, static_cast<uint16_t>(v)));
+                zero[i] = Wide<T>::magic + (v >> 16) * 0x00010001u;
+            }
+            uint32_t q[4][words];
+            codes_of(stage, j, q);
+            float part[2][NT][4] = {};
+#pragma unroll
+            for (int u = 0; u < words; ++u) {
+                const int w = j * words + u;
+                if (w < 3) fetch(w + 1);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        uint32_t a[4];
+                        a[0] = widen<T>(q[2 * m][u], 2 * h, zero[2 * m]);
+                        a[1] = widen<T>(q[2 * m + 1][u], 2 * h, zero[2 * m + 1]);
+                        a[2] = widen<T>(q[2 * m][u], 2 * h + 1, zero[2 * m]);
+                        a[3] = widen<T>(q[2 * m + 1][u], 2 * h + 1, zero[2 * m + 1]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            Wide<T>::mma(part[m][n], a, h ? b[w & 1][n].z : b[w & 1][n].x, h ? b[w & 1][n].w : b[w & 1][n].y);
+                    }
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum[m][n][i] = fmaf(part[m][n][i], scale[2 * m + (i >> 1)], sum[m][n][i]);
         }
     }
 };
 
-template <typename T, int G>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_int4_product(const __grid_constant__ CUtensorMap tW, const __grid_constant__ Int4Product p) {
-    using C = Cfg<G>;
-    constexpr int TN = C::TN;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                               ~static_cast<uintptr_t>(1023));
-    uint8_t* s_rows = smem + kCodeBytes;
-    uint8_t* s_join = s_rows + kRowBytes;
-    Bars& bars = *reinterpret_cast<Bars*>(s_join + C::join);
-    Lists& lists = *reinterpret_cast<Lists*>(reinterpret_cast<uint8_t*>(&bars) + 1024);
-    volatile uint32_t* abort_flag = &bars.abort;
-
-    const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(cluster_ctarank());
-    uint32_t split_;
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(split_));
-    const int split = static_cast<int>(split_);
-    const bool swiglu = p.swiglu != 0;
-    const int panels = swiglu ? p.columns / 64 : (p.r.N + 127) / 128;
-    const int chunks = (p.r.K + C::chunk - 1) / C::chunk, per = (chunks + split - 1) / split;
-    const int c0 = min(rank * per, chunks), c1 = min(c0 + per, chunks);
-    pdl_trigger();
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < C::code_stages; ++i) {
-            mbar_init(bars.code_full + i, 1);
-            mbar_init(bars.code_empty + i, 4);  // the warps that widen the chunk
-        }
-        for (int i = 0; i < kRowStages; ++i) {
-            mbar_init(bars.row_full + i, 64);  // every lane of both loading warps
-            mbar_init(bars.row_empty + i, 1);
-        }
-        for (int i = 0; i < C::a_bufs; ++i) {
-            mbar_init(bars.a_full + i, 4);
-            mbar_init(bars.a_empty + i, 1);
-        }
-        for (int i = 0; i < C::d_bufs; ++i) {
-            mbar_init(bars.d_full + i, 1);
-            mbar_init(bars.d_empty + i, 4);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bars.join_full + i, 4 * split);  // a summing warpgroup of every CTA of the cluster
-            mbar_init(bars.join_free + i, 4 * split);
-            mbar_init(bars.summed + i, 4);
-        }
-        mbar_init(&bars.drain, 1);
-        bars.abort = 0;
-        fence_mbar_init();
-    }
-    // tensor memory is taken only once the kernels before this one have finished
-    pdl_wait();
-    if (warp == 3) tmem_alloc(&bars.tmem, 512);
-    const int total = uniform(build_lists<TN>(p.r, lists, panels));
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync();  // the peers' barriers are initialised before any remote use
-    tc_fence_after();
-    const uint32_t tmem = uniform(bars.tmem);
-    const int first = blockIdx.x / split, stride = gridDim.x / split;
-    bool timed_out = false;
-    // a warpgroup takes its registers with one instruction
-    if (warp < 4) {
-        give_registers<kIssueRegs>();
-        if (warp == 0) {
-            // ------------------------------------------------------------ codes
-            Feed feed;
-            Ring r;
-            uint32_t armed = 0, armed_par = 0;  // stages with copies not yet seen landed
-            for (int t = first; t < total && !timed_out; t += stride) {
-                const Item it = feed.next(lists, p.r.E, panels, total, t, stride, lane);
-                const Halves h = halves_of(it.panel, swiglu);
-                for (int c = c0; c < c1; ++c) {
-                    if (!role_wait(bars.code_empty + r.s, r.ph ^ 1u, abort_flag)) {
-                        timed_out = true;
-                        break;
-                    }
-                    if (lane == 0) {
-                        uint64_t* bar = bars.code_full + r.s;
-                        const uint32_t dst = smem_u32(smem + r.s * C::code_stage);
-                        mbar_arrive_expect_tx(bar, C::code_stage);
-                        tma_load_3d(dst, &tW, c * (C::chunk / 2), h.a, it.e, bar);
-                        tma_load_3d(dst + C::code_stage / 2, &tW, c * (C::chunk / 2), h.b, it.e, bar);
-                    }
-                    armed |= 1u << r.s;
-                    armed_par = (armed_par & ~(1u << r.s)) | (r.ph << r.s);
-                    r.next<C::code_stages>();
-                }
-            }
-            if ((timed_out || *abort_flag) && lane == 0) {
-                *abort_flag = 1;
-                for (int i = 0; i < C::code_stages; ++i)
-                    if (armed & (1u << i)) {
-                        volatile uint32_t never = 0;
-                        (void)mbar_wait(bars.code_full + i, (armed_par >> i) & 1u, &never);
-                    }
-            }
-        } else if (warp == 1 || warp == 3) {
-            // ------------------------------------------------------- token rows
-            // each of the two warps takes 64 of a stage's 128 elements; a lane 16 bytes
-            // of every fourth row, into the 128-byte swizzle, whose 8-row atoms of the
-            // two halves alternate.  As many stages as tiles of this width leave room
-            // for; where the width changes, they are all waited for first.
-            Feed feed;
-            const int half = warp >> 1, sub = lane >> 3, piece = lane & 7;
-            const uint32_t even = sub * 128 + ((piece ^ sub) << 4), odd = (sub + 4) * 128 + ((piece ^ (sub + 4)) << 4);
-            const uint8_t* base = static_cast<const uint8_t*>(p.x);
-            const uint32_t dst0 = smem_u32(s_rows) + half * 1024;
-            int n_stages = 0, s = 0;
-            uint32_t used = 0;  // parity of each stage's uses
-            for (int t = first; t < total && !timed_out; t += stride) {
-                const Item it = feed.next(lists, p.r.E, panels, total, t, stride, lane);
-                const int wide = (it.rows + 15) & ~15;
-                if (row_stages(wide) != n_stages) {
-                    for (int i = 0; i < n_stages && !timed_out; ++i)
-                        timed_out = !role_wait(bars.row_empty + i, (used >> i & 1u) ^ 1u, abort_flag);
-                    n_stages = row_stages(wide);
-                    s = 0;
-                }
-                int from[TN / 4];
+template <typename T, int G, int NT>
+__device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, float* join, uint8_t* ring) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const int split = p.split, part = warp % split, block = it.panel * (kWarps / split) + warp / split;
+    // the warp's weight rows: 16 from a on and 16 from b on
+    const int a0 = p.swiglu ? (block >> 3) * 256 + (block & 7) * 16 : block * 32, b0 = a0 + (p.swiglu ? 128 : 16);
+    const bool live = a0 < p.r.N;
+    float sum[2][NT][4] = {};
+    if (live) {
+        using W = Warp<T, G>;
+        const int64_t first = static_cast<int64_t>(it.e) * p.r.N, bytes = p.r.K / 2;
+        // N is a multiple of 8: rows past the last one are read as others, and not stored
+        auto row = [&](int i) {
+            const int r = i < 2 ? a0 + 8 * i : b0 + 8 * (i - 2);
+            return r < p.r.N ? r : a0;
+        };
+        const W w{p, p.codes + (first + a0 + g) * bytes + t4 * 16, {(row(1) - a0) * bytes, (row(2) - a0) * bytes, (row(3) - a0) * bytes},
+                  (first + row(t4) + g) * p.groups, smem_u32(ring + warp * kStages * kStageBytes), lane, t4,
+                  (p.r.K + kChunk - 1) / kChunk - 1};
+        const T* x[NT];
 #pragma unroll
-                for (int i = 0; i < TN / 4; ++i)
-                    from[i] = 4 * i + sub < it.rows ? token_row(p, it.row + 4 * i + sub) : -1;
-                for (int k0 = c0 * C::chunk; k0 < c1 * C::chunk && !timed_out; k0 += 128) {
-                    if (!role_wait(bars.row_empty + s, (used >> s & 1u) ^ 1u, abort_flag)) {
-                        timed_out = true;
-                        break;
-                    }
-                    const int k = k0 + half * 64 + piece * 8;
-                    const uint32_t dst = dst0 + s * wide * 256;
+        for (int n = 0; n < NT; ++n) {
+            const int from = n * 8 + g < it.rows ? token_row(p, it.row + n * 8 + g) : -1;
+            x[n] = from < 0 ? nullptr : static_cast<const T*>(p.x) + from * p.ldx;
+        }
+        uint32_t par[W::parts];
+        w.params(part, par);
 #pragma unroll
-                    for (int i = 0; i < TN / 4; ++i) {
-                        if (4 * i >= wide) break;
-                        const bool in = from[i] >= 0 && k < p.r.K;
-                        cp_async_16(dst + (i >> 1) * 2048 + (i & 1 ? odd : even),
-                                    in ? base + (from[i] * p.ldx + k) * 2 : base, in ? 16 : 0);
-                    }
-                    cp_async_arrive(bars.row_full + s);
-                    used ^= 1u << s;
-                    if (++s == n_stages) s = 0;
-                }
-            }
-            // nothing of this CTA's shared memory may still be written to at exit
+        for (int i = 0; i < kStages - 1; ++i) {
+            if (part + i * split <= w.last) w.load(i, part + i * split);
             cp_async_commit();
-            cp_async_wait<0>();
-        } else if (warp == 2) {
-            // ------------------------------------------------------------- MMAs
-            Feed feed;
-            const uint32_t one = elect_one();
-            // 8-row atoms 2048 bytes apart: those of the two halves alternate
-            const uint64_t b0 = sdesc_sw128(smem_u32(s_rows)) + (static_cast<uint64_t>(1024u >> 4) << 32);
-            Ring a, d;
-            int n_stages = 0, s = 0;
-            uint32_t used = 0;
-            bool issued = false;
-            for (int t = first; t < total && !timed_out; t += stride) {
-                const Item it = feed.next(lists, p.r.E, panels, total, t, stride, lane);
-                const int wide = (it.rows + 15) & ~15;
-                if (row_stages(wide) != n_stages) {
-                    n_stages = row_stages(wide);
-                    s = 0;
-                }
-                const uint32_t idesc = (1u << 4) | (Wide<T>::format << 7) | (Wide<T>::format << 10) |
-                                       (static_cast<uint32_t>(wide >> 3) << 17) | (8u << 24);
-                for (int c = c0; c < c1 && !timed_out; ++c) {
-                    if (!role_wait(bars.d_empty + d.s, d.ph ^ 1u, abort_flag) || !role_wait(bars.a_full + a.s, a.ph, abort_flag)) {
-                        timed_out = true;
-                        break;
-                    }
-                    const uint32_t dcol = tmem + static_cast<uint32_t>(d.s * C::d_cols);
-                    const uint32_t acol = tmem + C::a_col + static_cast<uint32_t>(a.s * (C::chunk / 2));
-#pragma unroll
-                    for (int u = 0; u < C::chunk / 128; ++u) {
-                        if (!role_wait(bars.row_full + s, used >> s & 1u, abort_flag)) {
-                            timed_out = true;
-                            break;
-                        }
-                        fence_proxy_async_smem();  // the rows came through the generic proxy
-                        tc_fence_after();
-                        const uint64_t b = b0 + static_cast<uint32_t>(s * wide * 16);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_tmem_if(one, dcol + ((u * 128 + k * 16) / G) * TN, acol + (u * 8 + k) * 8,
-                                        b + (k >> 2) * 64 + (k & 3) * 2, idesc, k % (G / 16) != 0);
-                        commit_if(one, bars.row_empty + s);
-                        issued = true;
-                        used ^= 1u << s;
-                        if (++s == n_stages) s = 0;
-                    }
-                    if (timed_out) break;
-                    commit_if(one, bars.a_empty + a.s);
-                    commit_if(one, bars.d_full + d.s);
-                    a.next<C::a_bufs>();
-                    d.next<C::d_bufs>();
-                }
-            }
-            if ((timed_out || *abort_flag) && issued && one) {
-                *abort_flag = 1;
-                mma_commit(&bars.drain);
-                volatile uint32_t never = 0;
-                (void)mbar_wait(&bars.drain, 0, &never);
-            }
         }
-    } else if (warp < 12) {
-        take_registers<kSumRegs>();
-        // ------------------------------------------------- sums and epilogue
-        const int q = warp & 3, me = q * 32 + lane;  // weight row of the panel
-        const uint32_t quarter = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        Feed feed;
-        Ring d;
-        // The two warpgroups take the items in turn: one's epilogue runs beside the
-        // other's sums.  Each item's barriers are those of its warpgroup, so that a
-        // phase is waited for only once the phase before it has been: a parity says
-        // no more than that.
-        const int w = warp >> 3;
-        int turn = 0;
-        for (int t = first; t < total && !timed_out; t += stride, ++turn) {
-            const Item it = feed.next(lists, p.r.E, panels, total, t, stride, lane);
-            if ((turn & 1) != w) {
-                for (int c = c0; c < c1; ++c) d.next<C::d_bufs>();
-                continue;
-            }
-            const uint32_t ph = turn >> 1 & 1, other_ph = w ? ph : ph ^ 1u;  // of the item before: none, at first
-            const Halves hv = halves_of(it.panel, swiglu);
-            const int wide = (it.rows + 15) & ~15;
-            Stream<C::parts, uint16_t> scales;
-            scales.start(static_cast<const uint16_t*>(p.scales) + weight_row(p, it.e, hv, me) * p.groups, p.groups, p.whole,
-                         0u, c0);
-            float acc[TN];
+        int stage = 0;
+        for (int c = part; c <= w.last; c += split) {
+            cp_async_wait<kStages - 2>();
+            __syncwarp();  // every lane's copies, and the reads of the stage that is filled next
+            const int next = c + (kStages - 1) * split;
+            if (next <= w.last) w.load(stage == 0 ? kStages - 1 : stage - 1, next);
+            cp_async_commit();
+            uint32_t now[W::parts];
 #pragma unroll
-            for (int n = 0; n < TN; ++n) acc[n] = 0.0f;
-            // the sums of the item before have been taken
-            if (!role_wait(bars.summed + (w ^ 1), other_ph, abort_flag, sum_limit_ns(per))) {
-                timed_out = true;
-                break;
-            }
-            for (int c = c0; c < c1; ++c) {
-                // a group past the row's end has sum 0, and scale 0
-                uint32_t sbits[C::parts];
-                scales.take(c, sbits);
-                if (!role_wait(bars.d_full + d.s, d.ph, abort_flag)) {
-                    timed_out = true;
-                    break;
-                }
-                tc_fence_after();
-#pragma unroll
-                for (int j = 0; j < C::parts; ++j) {
-                    const uint32_t col = quarter + static_cast<uint32_t>(d.s * C::d_cols + j * TN);
-                    const float s = to_float<T>(__builtin_bit_cast(T, static_cast<uint16_t>(sbits[j])));
-#pragma unroll
-                    for (int n0 = 0; n0 < TN; n0 += 16) {
-                        if (n0 >= wide) break;
-                        uint32_t v[16];
-                        tmem_ld16(col + n0, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int n = 0; n < 16; ++n) acc[n0 + n] = fmaf(__uint_as_float(v[n]), s, acc[n0 + n]);
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars.d_empty + d.s);
-                d.next<C::d_bufs>();
-            }
-            if (timed_out) break;
-            if (lane == 0) mbar_arrive(bars.summed + w);
-            // every CTA of the cluster stores wide / split columns: parts to them
-            const int share = wide / split;
-            if (!role_wait(bars.join_free + (w ^ 1), other_ph, abort_flag, sum_limit_ns(per))) {
-                timed_out = true;  // the columns of the item before have not been read
-                break;
-            }
-            if (split == 1) {
-                float* dst = reinterpret_cast<float*>(s_join) + me;
-#pragma unroll
-                for (int n = 0; n < TN; ++n) {
-                    if (n >= wide) break;
-                    dst[n * 128] = acc[n];
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars.join_full + w);
-            } else {
-                fence_cluster();
-                const uint32_t mine = smem_u32(s_join) + static_cast<uint32_t>(rank * share * 512 + me * 4);
-                int to = 0, left = share;
-                uint32_t dst = mapa_shared(mine, 0);
-#pragma unroll
-                for (int n = 0; n < TN; ++n) {
-                    if (n >= wide) break;
-                    if (left == 0) {
-                        left = share;
-                        dst = mapa_shared(mine, static_cast<uint32_t>(++to));
-                    }
-                    st_cluster_f32(dst, acc[n]);
-                    dst += 512;
-                    --left;
-                }
-                fence_cluster();
-                __syncwarp();
-                if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(bars.join_full + w), static_cast<uint32_t>(lane)));
-            }
-            if (!role_wait(bars.join_full + w, ph, abort_flag, sum_limit_ns(per))) {
-                timed_out = true;
-                break;
-            }
-            if (split > 1) fence_cluster();
-            // a warp takes every fourth column (with SwiGLU, every fourth two): a
-            // token, whose features lie along the lanes, four to each
-            const float* join = reinterpret_cast<const float*>(s_join);
-            T* out = static_cast<T*>(p.r.out);
-            auto sum4 = [&](int c, int f) {
-                float4 v = *reinterpret_cast<const float4*>(join + c * 128 + f);
-                for (int o = 1; o < split; ++o) {
-                    const float4 w = *reinterpret_cast<const float4*>(join + (o * share + c) * 128 + f);
-                    v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
-                }
-                return v;
-            };
-            const int each = swiglu ? 2 : 1;
-            for (int cb = q * each; cb < min(share, it.rows - rank * share); cb += 4 * each) {
-                const int c = cb + (swiglu ? lane >> 4 : 0), token = rank * share + c;
-                const int f = swiglu ? 4 * (lane & 15) : 4 * lane, n = it.panel * (swiglu ? 64 : 128) + f;
-                if (c >= share || token >= it.rows || n >= p.columns) continue;
-                const int row = it.row + token;
-                float4 v = sum4(c, f);
-                if (swiglu) {
-                    const float4 u = sum4(c, 64 + f);
-                    v.x = v.x / (1.0f + expf(-v.x)) * u.x;
-                    v.y = v.y / (1.0f + expf(-v.y)) * u.y;
-                    v.z = v.z / (1.0f + expf(-v.z)) * u.z;
-                    v.w = v.w / (1.0f + expf(-v.w)) * u.w;
-                }
-                const float g = p.r.row_scale ? ld_dep(p.r.row_scale + row) : 1.0f;
-                v.x *= g, v.y *= g, v.z *= g, v.w *= g;
-                if (p.src && token_row(p, row) < 0) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                *reinterpret_cast<uint2*>(out + row * p.r.ldo + n) = make_uint2(pack2(T(), v.x, v.y), pack2(T(), v.z, v.w));
-            }
-            __syncwarp();
-            if (split == 1) {
-                if (lane == 0) mbar_arrive(bars.join_free + w);
-            } else if (lane < split) {
-                mbar_arrive_cluster(mapa_shared(smem_u32(bars.join_free + w), static_cast<uint32_t>(lane)));
-            }
+            for (int j = 0; j < W::parts; ++j) now[j] = par[j];
+            w.params(c + split, par);
+            w.template chunk<NT>(stage, c, now, x, sum);
+            stage = stage == kStages - 1 ? 0 : stage + 1;
         }
-    } else {
-        // ---------------------------------------------------------- widening
-        give_registers<kWidenRegs>();
-        Feed feed;
-        const int mine = (warp - 12) >> 2, q = warp & 3, me = q * 32 + lane;
-        const uint32_t quarter = tmem + (static_cast<uint32_t>(q * 32) << 16) + C::a_col;
-        // 16-byte piece i of row `me` in the 128-byte or 64-byte swizzle
-        const int turn = C::chunk == 256 ? me & 7 : (me >> 1) & 3;
-        Ring s, a;
-        int turns = 0;
-        for (int t = first; t < total && !timed_out; t += stride) {
-            const Item it = feed.next(lists, p.r.E, panels, total, t, stride, lane);
-            Stream<C::parts, uint8_t> zeros;
-            zeros.start(p.zeros ? p.zeros + weight_row(p, it.e, halves_of(it.panel, swiglu), me) * p.groups : nullptr,
-                        p.groups, p.whole, 8u, c0);
-            for (int c = c0; c < c1; ++c) {
-                uint32_t zero[C::parts];
-                zeros.take(c, zero);
-                if ((turns++ & 1) == mine) {
-                    if (!role_wait(bars.code_full + s.s, s.ph, abort_flag) ||
-                        !role_wait(bars.a_empty + a.s, a.ph ^ 1u, abort_flag)) {
-                        timed_out = true;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint4* row = reinterpret_cast<const uint4*>(smem + s.s * C::code_stage + me * (C::chunk / 2));
-#pragma unroll
-                    for (int h = 0; h < C::chunk / 64; ++h) {  // 64 elements, 32 columns
-                        uint32_t v[32];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint4 u = row[(2 * h + i) ^ turn];
-                            const uint32_t z = Wide<T>::magic + zero[(2 * h + i) * 32 / G] * 0x00010001u;
-                            widen<T>(u.x, z, v + 16 * i);
-                            widen<T>(u.y, z, v + 16 * i + 4);
-                            widen<T>(u.z, z, v + 16 * i + 8);
-                            widen<T>(u.w, z, v + 16 * i + 12);
-                        }
-                        tmem_st(quarter + static_cast<uint32_t>(a.s * (C::chunk / 2) + h * 32), v);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars.code_empty + s.s);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars.a_full + a.s);
-                }
-                s.next<C::code_stages>();
-                a.next<C::a_bufs>();
-            }
-        }
+        __syncwarp();  // the next item's copies come after these reads
     }
-    if (timed_out) *abort_flag = 1;
-    if (timed_out && p.r.status) atomicOr(p.r.status, kRaggedTimeout);
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync();  // no peer still writes to this CTA's shared memory
-    if (warp == 3) {
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
+    if (split > 1) {  // the parts to the first of the warps, in order
+        __syncthreads();
+        if (part > 0) {
+#pragma unroll
+            for (int v = 0; v < 8 * NT; ++v) join[(warp * 16 + v) * 32 + lane] = (&sum[0][0][0])[v];
+        }
+        __syncthreads();
+        if (part > 0) return;
+        for (int o = 1; o < split; ++o)
+#pragma unroll
+            for (int v = 0; v < 8 * NT; ++v) (&sum[0][0][0])[v] += join[((warp + o) * 16 + v) * 32 + lane];
+    }
+    if (!live) return;
+    // lane: token rows 2 t4 and 2 t4 + 1 of each eight, weight rows g and g + 8 of each 16
+    T* out = static_cast<T*>(p.r.out);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int token = n * 8 + 2 * t4 + j, row = it.row + token;
+            if (token >= it.rows) continue;
+            const float f = p.r.row_scale ? ld_dep(p.r.row_scale + row) : 1.0f;
+            const bool none = p.src && token_row(p, row) < 0;
+            T* y = out + row * p.r.ldo;
+            if (p.swiglu) {
+                const int col = block * 16 + g;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float gate = sum[0][n][2 * h + j];
+                    const float v = gate / (1.0f + expf(-gate)) * sum[1][n][2 * h + j] * f;
+                    y[col + 8 * h] = from_float<T>(none ? 0.0f : v);
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int col = a0 + 16 * m + 8 * h + g;
+                        if (col < p.columns) y[col] = from_float<T>(none ? 0.0f : sum[m][n][2 * h + j] * f);
+                    }
+            }
+        }
+}
+
+template <typename T, int G>
+__global__ void __launch_bounds__(32 * kWarps, 2) k_int4_product(const __grid_constant__ Int4Product p) {
+    __shared__ Lists lists;
+    __shared__ float join[kWarps * 16 * 32];
+    extern __shared__ __align__(16) uint8_t ring[];
+    pdl_trigger();
+    pdl_wait();
+    const int blocks = (p.r.N + 31) / 32, per = kWarps / p.split, panels = (blocks + per - 1) / per;
+    const int total = build_lists(p.r, lists, panels);
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+        const Item it = item_at(lists, p.r.E, panels, t);
+        if (it.rows > 8)
+            run_item<T, G, 2>(p, it, join, ring);
+        else
+            run_item<T, G, 1>(p, it, join, ring);
     }
 }
 
-// CTAs that split a sum.  More items than SMs need no split.
-int split_of(int64_t items, int chunks) {
+// Warps that split a sum: more where the items are few.
+int split_of(int64_t blocks_by_tiles, int chunks) {
     int split = 1;
-    while (split < kMaxSplit && items * split < 2 * num_sms() && chunks >= 4 * split) split *= 2;
+    while (split < kWarps && blocks_by_tiles * split < 4ll * kWarps * 2 * num_sms() && chunks >= 2 * split) split *= 2;
     return split;
 }
 
 template <typename T, int G>
-cudaError_t launch(const Int4Product& p, const void* codes, cudaStream_t st) {
-    using C = Cfg<G>;
-    static int found[kMaxDevices][4] = {};
+cudaError_t launch(const Int4Product& q, cudaStream_t st) {
+    Int4Product p = q;
+    const int64_t blocks = (p.r.N + 31) / 32;
+    const int64_t tiles = p.r.R / kTile + (p.r.R < p.r.E ? p.r.R : p.r.E);  // at most
+    p.split = split_of(blocks * tiles, (p.r.K + kChunk - 1) / kChunk);
+    const int64_t per = kWarps / p.split, items = (blocks + per - 1) / per * tiles, most = 2 * num_sms();
+    static bool ready[kMaxDevices] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    CUtensorMap tW;
-    const uint64_t K = p.r.K, N = p.r.N, E = p.r.E;
-    const uint64_t wd[3] = {K / 2, N, E}, ws[2] = {K / 2, N * (K / 2)};
-    const uint32_t wb[3] = {C::chunk / 2, 64, 1};
-    if (!make_tensor_map(&tW, codes, 3, wd, ws, wb, CU_TENSOR_MAP_DATA_TYPE_UINT8, C::chunk / 2)) return cudaErrorInvalidValue;
-    const int64_t panels = p.swiglu ? p.columns / 64 : (p.r.N + 127) / 128;
-    const int64_t items = panels * (p.r.R / C::TN + (p.r.R < p.r.E ? p.r.R : p.r.E));  // at most
-    const int split = split_of(items, static_cast<int>((K + C::chunk - 1) / C::chunk));
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = split;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(split);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    int& n = found[dev][split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3];  // clusters at once
-    if (!n) {
-        cudaError_t e = cudaFuncSetAttribute(k_int4_product<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+    if (!ready[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(k_int4_product<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
-        int most = num_sms();
-        if (split > 1) {
-            e = cudaOccupancyMaxActiveClusters(&most, k_int4_product<T, G>, &cfg);
-            if (e != cudaSuccess) return e;
-        }
-        n = most > 0 ? most : 1;
+        ready[dev] = true;
     }
-    cfg.gridDim = dim3(static_cast<unsigned>(split * (items < n ? items : n)));
-    return cudaLaunchKernelEx(&cfg, k_int4_product<T, G>, tW, p);
+    return launch_pdl(k_int4_product<T, G>, dim3(static_cast<unsigned>(items < most ? items : most)), dim3(32 * kWarps), kSmem,
+                      st, p);
 }
 
 template <typename T>
-cudaError_t product(int group, const Int4Product& p, const void* codes, cudaStream_t st) {
-    if (group == 32) return launch<T, 32>(p, codes, st);
-    return group == 64 ? launch<T, 64>(p, codes, st) : launch<T, 128>(p, codes, st);
+cudaError_t product(int group, const Int4Product& p, cudaStream_t st) {
+    if (group == 32) return launch<T, 32>(p, st);
+    return group == 64 ? launch<T, 64>(p, st) : launch<T, 128>(p, st);
 }
 
 bool aligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -886,12 +496,14 @@ extern "C" moe_status_t moe_grouped_gemm_int4(int32_t group, int32_t dtype, int6
     p.swiglu = swiglu != 0;
     p.src = src;
     p.src_div = src_div;
+    p.codes = static_cast<const uint8_t*>(w_codes);
     p.scales = w_scales;
     p.zeros = static_cast<const uint8_t*>(w_zeros);
     p.groups = (K + group - 1) / group;
-    p.whole = p.groups % 8 == 0 && aligned(w_scales, 16) && aligned(w_zeros, 8);
+    const int parts = kChunk / group;
+    p.whole = p.groups % parts == 0 && aligned(w_scales, 2 * parts) && aligned(w_zeros, parts);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == MOE_DTYPE_BF16 ? product<__nv_bfloat16>(group, p, w_codes, st)
-                                                  : product<__half>(group, p, w_codes, st);
+    const cudaError_t e = dtype == MOE_DTYPE_BF16 ? product<__nv_bfloat16>(group, p, st)
+                                                  : product<__half>(group, p, st);
     return e == cudaSuccess ? MOE_OK : set_last_error(MOE_ERR_CUDA, "4-bit weight product: %s", cudaGetErrorString(e));
 }
