@@ -43,7 +43,7 @@ constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kChunk = 128;   // elements of the sum per step
 constexpr int kWarps = 8;     // of a CTA, two CTAs to an SM
 constexpr int kTile = 16;     // token rows of an item, at most
-constexpr int kStages = 4;    // chunks of a warp in shared memory
+constexpr int kStages = 4;    // chunks of a warp's codes in shared memory
 constexpr int kStageBytes = 32 * 64;
 constexpr int kSmem = kWarps * kStages * kStageBytes;
 
@@ -186,30 +186,23 @@ template <typename T, int G>
 struct Warp {
     static constexpr int parts = kChunk / G, words = 4 / parts;  // groups of a chunk, words of a lane in each
     const Int4Product& p;
-    const uint8_t* codes;    // this lane's 16 bytes of a chunk of its first weight row
-    int64_t to[3];           // from there to its other three
-    int64_t par_row;         // the weight row whose scales this lane reads, times the groups of a row
-    uint32_t ring;           // the warp's stages in shared memory
-    int lane, t4, last;      // lane % 4, last chunk
+    const uint8_t* codes[4];  // this lane's 16 bytes of the next chunk to load of its four weight rows
+    const uint16_t* scales;   // of the next chunk, of the weight row lane % 4 of the four
+    const uint8_t* zeros;
+    uint32_t put, get;        // this lane's places in the first of the warp's stages
+    int lane, t4;             // lane % 4
 
     // 32 rows x 64 bytes; a row's 16-byte pieces in an order that its number gives,
-    // so that reading one piece of eight rows meets no bank twice.  Past the end of
-    // a row any of its codes will do: they meet token rows that read as zero.
-    __device__ __forceinline__ void load(int stage, int c) const {
-        const int at = min(c * 64, p.r.K / 2 - 16 - t4 * 16);
-        const int g = lane >> 2;
-        const uint32_t dst = ring + stage * kStageBytes + g * 64 + ((t4 ^ (g >> 1 & 3)) << 4);
-        const uint8_t* q = codes + at;
-        cp_async_16(dst, q, 16);
-        cp_async_16(dst + 512, q + to[0], 16);
-        cp_async_16(dst + 1024, q + to[1], 16);
-        cp_async_16(dst + 1536, q + to[2], 16);
+    // so that reading one piece of eight rows meets no bank twice.
+    __device__ __forceinline__ void load(uint32_t stage) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cp_async_16(put + stage + 512 * i, codes[i], 16);
     }
-    // Word w (of four) of the lane in row lane / 4 + 8 i.
-    __device__ __forceinline__ void codes_of(int stage, int j, uint32_t (&q)[4][words]) const {
-        const int g = lane >> 2, piece = words == 4 ? t4 : words == 2 ? 2 * j + (t4 >> 1) : j;
-        const uint32_t at = ring + stage * kStageBytes + g * 64 + ((piece ^ (g >> 1 & 3)) << 4) +
-                            (words == 4 ? 0 : words == 2 ? (t4 & 1) * 8 : t4 * 4);
+    // The lane's words of group j of the chunk, in rows lane / 4 + 8 i.
+    __device__ __forceinline__ void codes_of(uint32_t stage, int j, uint32_t (&q)[4][words]) const {
+        uint32_t at = get + stage;
+        if constexpr (words == 2) at ^= j << 5;
+        if constexpr (words == 1) at ^= j << 4;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (words == 4)
@@ -223,63 +216,64 @@ struct Warp {
                 asm volatile("ld.shared.b32 %0, [%1];" : "=r"(q[i][0]) : "r"(at + 512 * i) : "memory");
         }
     }
-    // Scales, zero points << 16; past the last group the last one's, for sums of 0.
-    __device__ __forceinline__ void params(int c, uint32_t (&par)[parts]) const {
-        c = min(c, last);
-        const uint16_t* sc = static_cast<const uint16_t*>(p.scales) + par_row;
-        const uint8_t* z = p.zeros + par_row;
+    // Scales as fp32, and magic + zero point in both halves, of the next chunk; past
+    // the last group (left: groups from this one on) the last one's, for sums of 0.
+    __device__ __forceinline__ void params(int left, float (&scale)[parts], uint32_t (&zero)[parts]) const {
+        uint32_t s[parts], z[parts];
         if (parts == 1 || !p.whole) {
 #pragma unroll
             for (int j = 0; j < parts; ++j) {
-                const int at = min(c * parts + j, p.groups - 1);
-                par[j] = sc[at] | (p.zeros ? z[at] : 8u) << 16;
+                const int at = min(j, left - 1);
+                s[j] = scales[at];
+                z[j] = p.zeros ? zeros[at] : 8u;
             }
         } else if constexpr (parts == 2) {
-            const uint32_t v = *reinterpret_cast<const uint32_t*>(sc + c * parts);
-            const uint32_t w = p.zeros ? *reinterpret_cast<const uint16_t*>(z + c * parts) : 0x0808u;
-            par[0] = (v & 0xFFFFu) | (w & 0xFFu) << 16;
-            par[1] = v >> 16 | (w >> 8) << 16;
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(scales);
+            const uint32_t w = p.zeros ? *reinterpret_cast<const uint16_t*>(zeros) : 0x0808u;
+            s[0] = v & 0xFFFFu, s[1] = v >> 16;
+            z[0] = w & 0xFFu, z[1] = w >> 8;
         } else if constexpr (parts == 4) {
-            const uint2 v = *reinterpret_cast<const uint2*>(sc + c * parts);
-            const uint32_t w = p.zeros ? *reinterpret_cast<const uint32_t*>(z + c * parts) : 0x08080808u;
-            par[0] = (v.x & 0xFFFFu) | (w & 0xFFu) << 16;
-            par[1] = v.x >> 16 | (w >> 8 & 0xFFu) << 16;
-            par[2] = (v.y & 0xFFFFu) | (w >> 16 & 0xFFu) << 16;
-            par[3] = v.y >> 16 | (w >> 24) << 16;
+            const uint2 v = *reinterpret_cast<const uint2*>(scales);
+            const uint32_t w = p.zeros ? *reinterpret_cast<const uint32_t*>(zeros) : 0x08080808u;
+            s[0] = v.x & 0xFFFFu, s[1] = v.x >> 16, s[2] = v.y & 0xFFFFu, s[3] = v.y >> 16;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[j] = w >> (8 * j) & 0xFFu;
+        }
+#pragma unroll
+        for (int j = 0; j < parts; ++j) {
+            scale[j] = to_float<T>(__builtin_bit_cast(T, static_cast<uint16_t>(s[j])));
+            zero[j] = Wide<T>::magic + z[j] * 0x00010001u;
         }
     }
 
-    // sum[m][n]: 16 weight rows m by 8 token rows n; x[n]: this lane's token row, or null
-    template <int NT>
-    __device__ __forceinline__ void chunk(int stage, int c, const uint32_t (&par)[parts], const T* const (&x)[NT],
-                                          float (&sum)[2][NT][4]) const {
-        uint4 b[2][NT];  // of this word and the next
-        auto fetch = [&](int w) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int k = c * kChunk + ((w / words * 4 + t4) * words + w % words) * 8;
-                b[w & 1][n] = make_uint4(0, 0, 0, 0);
-                if (x[n] && k < p.r.K) b[w & 1][n] = *reinterpret_cast<const uint4*>(x[n] + k);
-            }
-        };
-        fetch(0);
+    // sum[m][n]: 16 weight rows m by 8 token rows n; x: the chunk's first element for
+    // this lane in its token rows, of which `left` are inside the row
+    template <int NT, bool ALL>
+    __device__ __forceinline__ void chunk(uint32_t stage, const T* const (&x)[NT], int left, const float (&scales_)[parts],
+                                          const uint32_t (&zeros_)[parts], float (&sum)[2][NT][4]) const {
 #pragma unroll
         for (int j = 0; j < parts; ++j) {
             float scale[4];
             uint32_t zero[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t v = __shfl_sync(kAll, par[j], (lane & ~3) | i);
-                scale[i] = to_float<T>(__builtin_bit_cast(T, static_cast<uint16_t>(v)));
-                zero[i] = Wide<T>::magic + (v >> 16) * 0x00010001u;
+                scale[i] = __shfl_sync(kAll, scales_[j], (lane & ~3) | i);
+                zero[i] = __shfl_sync(kAll, zeros_[j], (lane & ~3) | i);
             }
             uint32_t q[4][words];
             codes_of(stage, j, q);
             float part[2][NT][4] = {};
 #pragma unroll
             for (int u = 0; u < words; ++u) {
-                const int w = j * words + u;
-                if (w < 3) fetch(w + 1);
+                const int k = (j * 4 * words + u) * 8;  // from the lane's first element on
+                uint4 b[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (ALL || k < left)
+                        b[n] = *reinterpret_cast<const uint4*>(x[n] + k);
+                    else
+                        b[n] = make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -290,8 +284,7 @@ struct Warp {
                         a[2] = widen<T>(q[2 * m][u], 2 * h + 1, zero[2 * m]);
                         a[3] = widen<T>(q[2 * m + 1][u], 2 * h + 1, zero[2 * m + 1]);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            Wide<T>::mma(part[m][n], a, h ? b[w & 1][n].z : b[w & 1][n].x, h ? b[w & 1][n].w : b[w & 1][n].y);
+                        for (int n = 0; n < NT; ++n) Wide<T>::mma(part[m][n], a, h ? b[n].z : b[n].x, h ? b[n].w : b[n].y);
                     }
             }
 #pragma unroll
@@ -306,49 +299,83 @@ struct Warp {
 
 template <typename T, int G, int NT>
 __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, float* join, uint8_t* ring) {
+    using W = Warp<T, G>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    const int split = p.split, part = warp % split, block = it.panel * (kWarps / split) + warp / split;
+    const int split = p.split, part = warp & (split - 1), block = it.panel * (kWarps / split) + warp / split;
     // the warp's weight rows: 16 from a on and 16 from b on
     const int a0 = p.swiglu ? (block >> 3) * 256 + (block & 7) * 16 : block * 32, b0 = a0 + (p.swiglu ? 128 : 16);
     const bool live = a0 < p.r.N;
     float sum[2][NT][4] = {};
     if (live) {
-        using W = Warp<T, G>;
-        const int64_t first = static_cast<int64_t>(it.e) * p.r.N, bytes = p.r.K / 2;
+        const int64_t first = static_cast<int64_t>(it.e) * p.r.N + g;
         // N is a multiple of 8: rows past the last one are read as others, and not stored
         auto row = [&](int i) {
             const int r = i < 2 ? a0 + 8 * i : b0 + 8 * (i - 2);
-            return r < p.r.N ? r : a0;
+            return first + (r < p.r.N ? r : a0);
         };
-        const W w{p, p.codes + (first + a0 + g) * bytes + t4 * 16, {(row(1) - a0) * bytes, (row(2) - a0) * bytes, (row(3) - a0) * bytes},
-                  (first + row(t4) + g) * p.groups, smem_u32(ring + warp * kStages * kStageBytes), lane, t4,
-                  (p.r.K + kChunk - 1) / kChunk - 1};
+        const int chunks = (p.r.K + kChunk - 1) / kChunk;
+        W w{p};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w.codes[i] = p.codes + row(i) * (p.r.K / 2) + part * 64 + t4 * 16;
+        w.scales = static_cast<const uint16_t*>(p.scales) + row(t4) * p.groups + part * W::parts;
+        w.zeros = p.zeros + row(t4) * p.groups + part * W::parts;
+        const uint32_t mine = smem_u32(ring + warp * kStages * kStageBytes) + g * 64;
+        const int turn = g >> 1 & 3;
+        w.put = mine + ((t4 ^ turn) << 4);
+        w.get = W::words == 4 ? w.put : W::words == 2 ? mine + (((t4 >> 1) ^ turn) << 4) + (t4 & 1) * 8 : mine + (turn << 4) + t4 * 4;
+        w.lane = lane;
+        w.t4 = t4;
+        // columns of the product past the item's rows are not stored: any row will do
         const T* x[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int from = n * 8 + g < it.rows ? token_row(p, it.row + n * 8 + g) : -1;
-            x[n] = from < 0 ? nullptr : static_cast<const T*>(p.x) + from * p.ldx;
+            const int from = token_row(p, it.row + (n * 8 + g < it.rows ? n * 8 + g : 0));
+            x[n] = static_cast<const T*>(p.x) + (from < 0 ? 0 : from) * p.ldx + part * kChunk + t4 * W::words * 8;
         }
-        uint32_t par[W::parts];
-        w.params(part, par);
+        // Past the end of a row any codes will do, with token rows that read as zero.
+        int ahead = part, bytes = p.r.K / 2 - part * 64 - t4 * 16;  // of the next chunk to load
+        auto load = [&](uint32_t stage) {
+            if (ahead < chunks) {
+                if (bytes <= 0) {  // the row's last 16 bytes instead
 #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) {
-            if (part + i * split <= w.last) w.load(i, part + i * split);
+                    for (int i = 0; i < 4; ++i) w.codes[i] += bytes - 16;
+                }
+                w.load(stage);
+            }
             cp_async_commit();
-        }
-        int stage = 0;
-        for (int c = part; c <= w.last; c += split) {
+            ahead += split;
+            bytes -= split * 64;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w.codes[i] += split * 64;
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) load(i * kStageBytes);
+        float scale[W::parts];
+        uint32_t zero[W::parts];
+        int groups = p.groups - part * W::parts;  // from the next chunk's parameters on
+        if (part < chunks) w.params(groups, scale, zero);
+        uint32_t stage = 0;
+        int left = p.r.K - part * kChunk - t4 * W::words * 8;
+        for (int c = part; c < chunks; c += split) {
             cp_async_wait<kStages - 2>();
             __syncwarp();  // every lane's copies, and the reads of the stage that is filled next
-            const int next = c + (kStages - 1) * split;
-            if (next <= w.last) w.load(stage == 0 ? kStages - 1 : stage - 1, next);
-            cp_async_commit();
-            uint32_t now[W::parts];
+            load(stage == 0 ? (kStages - 1) * kStageBytes : stage - kStageBytes);
+            float s[W::parts];
+            uint32_t z[W::parts];
 #pragma unroll
-            for (int j = 0; j < W::parts; ++j) now[j] = par[j];
-            w.params(c + split, par);
-            w.template chunk<NT>(stage, c, now, x, sum);
-            stage = stage == kStages - 1 ? 0 : stage + 1;
+            for (int j = 0; j < W::parts; ++j) s[j] = scale[j], z[j] = zero[j];
+            w.scales += split * W::parts;
+            w.zeros += split * W::parts;
+            groups -= split * W::parts;
+            if (c + split < chunks) w.params(groups, scale, zero);
+            if ((c + 1) * kChunk <= p.r.K)
+                w.template chunk<NT, true>(stage, x, 0, s, z, sum);
+            else
+                w.template chunk<NT, false>(stage, x, left, s, z, sum);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[n] += split * kChunk;
+            left -= split * kChunk;
+            stage = stage == (kStages - 1) * kStageBytes ? 0 : stage + kStageBytes;
         }
         __syncwarp();  // the next item's copies come after these reads
     }
@@ -356,13 +383,13 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, f
         __syncthreads();
         if (part > 0) {
 #pragma unroll
-            for (int v = 0; v < 8 * NT; ++v) join[(warp * 16 + v) * 32 + lane] = (&sum[0][0][0])[v];
+            for (int v = 0; v < 8 * NT; ++v) join[(warp * 8 * NT + v) * 32 + lane] = (&sum[0][0][0])[v];
         }
         __syncthreads();
         if (part > 0) return;
         for (int o = 1; o < split; ++o)
 #pragma unroll
-            for (int v = 0; v < 8 * NT; ++v) (&sum[0][0][0])[v] += join[((warp + o) * 16 + v) * 32 + lane];
+            for (int v = 0; v < 8 * NT; ++v) (&sum[0][0][0])[v] += join[((warp + o) * 8 * NT + v) * 32 + lane];
     }
     if (!live) return;
     // lane: token rows 2 t4 and 2 t4 + 1 of each eight, weight rows g and g + 8 of each 16
@@ -371,11 +398,11 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, f
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int token = n * 8 + 2 * t4 + j, row = it.row + token;
+            const int token = n * 8 + 2 * t4 + j, to = it.row + token;
             if (token >= it.rows) continue;
-            const float f = p.r.row_scale ? ld_dep(p.r.row_scale + row) : 1.0f;
-            const bool none = p.src && token_row(p, row) < 0;
-            T* y = out + row * p.r.ldo;
+            const float f = p.r.row_scale ? ld_dep(p.r.row_scale + to) : 1.0f;
+            const bool none = p.src && token_row(p, to) < 0;
+            T* y = out + to * p.r.ldo;
             if (p.swiglu) {
                 const int col = block * 16 + g;
 #pragma unroll
@@ -399,8 +426,8 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, f
 template <typename T, int G>
 __global__ void __launch_bounds__(32 * kWarps, 2) k_int4_product(const __grid_constant__ Int4Product p) {
     __shared__ Lists lists;
-    __shared__ float join[kWarps * 16 * 32];
-    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float join[kWarps * kTile * 32];
+    extern __shared__ __align__(128) uint8_t ring[];
     pdl_trigger();
     pdl_wait();
     const int blocks = (p.r.N + 31) / 32, per = kWarps / p.split, panels = (blocks + per - 1) / per;
@@ -412,6 +439,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_int4_product(const __grid_co
         else
             run_item<T, G, 1>(p, it, join, ring);
     }
+    cp_async_wait<0>();
 }
 
 // Warps that split a sum: more where the items are few.
