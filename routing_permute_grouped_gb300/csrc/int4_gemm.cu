@@ -172,7 +172,9 @@ struct Wide<__half> {
 // Pair i of a word's eight codes as numbers; zero is magic + zero point in both halves.
 template <typename T>
 __device__ __forceinline__ uint32_t widen(uint32_t w, int i, uint32_t zero) {
-    return Wide<T>::sub((w >> (4 * i) & 0x000F000Fu) | Wide<T>::magic, zero);
+    uint32_t v;  // (w >> 4 i & mask) | magic in one operation besides the shift
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w >> (4 * i)), "r"(0x000F000Fu), "r"(Wide<T>::magic));
+    return Wide<T>::sub(v, zero);
 }
 
 // The token row of row r of y; -1 where src picks none.
