@@ -40,12 +40,10 @@ namespace moe {
 namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr int kChunk = 128;   // elements of the sum per step
+constexpr int kChunk = 128;   // elements of the sum that a lane's four words and its neighbours' make
 constexpr int kWarps = 8;     // of a CTA, two CTAs to an SM
 constexpr int kTile = 16;     // token rows of an item, at most
-constexpr int kStages = 4;    // chunks of a warp's codes in shared memory
-constexpr int kStageBytes = 32 * 64;
-constexpr int kSmem = kWarps * kStages * kStageBytes;
+constexpr int kStages = 3;    // steps of a warp's codes in shared memory
 
 struct Int4Product {
     RaggedArgs r;          // N: weight rows per group
@@ -60,7 +58,7 @@ struct Int4Product {
     const void* scales;    // [E, N, groups]
     const uint8_t* zeros;  // the same, or null
     int32_t groups;        // per weight row
-    int32_t whole;         // a chunk's scales and zero points can be read at once
+    int32_t whole;         // a step's scales and zero points can be read at once
     int32_t split;         // warps that share a sum: 1, 2, 4 or 8
 };
 
@@ -187,18 +185,30 @@ __device__ __forceinline__ int token_row(const Int4Product& p, int r) {
 template <typename T, int G>
 struct Warp {
     static constexpr int parts = kChunk / G, words = 4 / parts;  // groups of a chunk, words of a lane in each
+    static constexpr int halves = G == 128 ? 2 : 1;              // chunks of a step
+    static constexpr int groups = halves * parts, step = halves * kChunk, stage_bytes = halves * 32 * 64;
     const Int4Product& p;
-    const uint8_t* codes[4];  // this lane's 16 bytes of the next chunk to load of its four weight rows
-    const uint16_t* scales;   // of the next chunk, of the weight row lane % 4 of the four
+    const uint8_t* codes[4];  // this lane's 16 bytes of the next step's first chunk, of its four weight rows
+    const uint16_t* scales;   // of the next step, of the weight row lane % 4 of the four
     const uint8_t* zeros;
     uint32_t put, get;        // this lane's places in the first of the warp's stages
     int lane, t4;             // lane % 4
 
-    // 32 rows x 64 bytes; a row's 16-byte pieces in an order that its number gives,
-    // so that reading one piece of eight rows meets no bank twice.
-    __device__ __forceinline__ void load(uint32_t stage) const {
+    // 32 rows x 64 bytes of every chunk; a row's 16-byte pieces in an order that its
+    // number gives, so that reading one piece of eight rows meets no bank twice.
+    // left: bytes of the row from the lane's first on.  Past its end any codes will
+    // do (its last ones), with token rows that read as zero.
+    __device__ __forceinline__ void load(uint32_t stage, int left) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cp_async_16(put + stage + 512 * i, codes[i], 16);
+        for (int h = 0; h < halves; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cp_async_16(put + stage + 2048 * h + 512 * i, codes[i] + min(h * 64, left - 16), 16);
+    }
+    __device__ __forceinline__ void load_whole(uint32_t stage) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int h = 0; h < halves; ++h) cp_async_16(put + stage + 2048 * h + 512 * i, codes[i] + h * 64, 16);
     }
     // The lane's words of group j of the chunk, in rows lane / 4 + 8 i.
     __device__ __forceinline__ void codes_of(uint32_t stage, int j, uint32_t (&q)[4][words]) const {
@@ -218,23 +228,24 @@ struct Warp {
                 asm volatile("ld.shared.b32 %0, [%1];" : "=r"(q[i][0]) : "r"(at + 512 * i) : "memory");
         }
     }
-    // Scales as fp32, and magic + zero point in both halves, of the next chunk; past
-    // the last group (left: groups from this one on) the last one's, for sums of 0.
-    __device__ __forceinline__ void params(int left, float (&scale)[parts], uint32_t (&zero)[parts]) const {
-        uint32_t s[parts], z[parts];
-        if (parts == 1 || !p.whole) {
+    // Scales as fp32, and magic + zero point in both halves, of the next step; past the
+    // last group (left: groups from this one on) the last one's, for sums of 0.
+    __device__ __forceinline__ void params(int left, float (&scale)[groups], uint32_t (&zero)[groups]) const {
+        uint32_t s[groups], z[groups];
+        if (!p.whole) {
 #pragma unroll
-            for (int j = 0; j < parts; ++j) {
+            for (int j = 0; j < groups; ++j) {
                 const int at = min(j, left - 1);
                 s[j] = scales[at];
                 z[j] = p.zeros ? zeros[at] : 8u;
             }
-        } else if constexpr (parts == 2) {
+        } else if constexpr (groups == 2) {
             const uint32_t v = *reinterpret_cast<const uint32_t*>(scales);
             const uint32_t w = p.zeros ? *reinterpret_cast<const uint16_t*>(zeros) : 0x0808u;
             s[0] = v & 0xFFFFu, s[1] = v >> 16;
             z[0] = w & 0xFFu, z[1] = w >> 8;
-        } else if constexpr (parts == 4) {
+        } else {
+            static_assert(groups == 4 || groups == 2, "groups of a step");
             const uint2 v = *reinterpret_cast<const uint2*>(scales);
             const uint32_t w = p.zeros ? *reinterpret_cast<const uint32_t*>(zeros) : 0x08080808u;
             s[0] = v.x & 0xFFFFu, s[1] = v.x >> 16, s[2] = v.y & 0xFFFFu, s[3] = v.y >> 16;
@@ -242,32 +253,33 @@ struct Warp {
             for (int j = 0; j < 4; ++j) z[j] = w >> (8 * j) & 0xFFu;
         }
 #pragma unroll
-        for (int j = 0; j < parts; ++j) {
+        for (int j = 0; j < groups; ++j) {
             scale[j] = to_float<T>(__builtin_bit_cast(T, static_cast<uint16_t>(s[j])));
             zero[j] = Wide<T>::magic + z[j] * 0x00010001u;
         }
     }
 
-    // sum[m][n]: 16 weight rows m by 8 token rows n; x: the chunk's first element for
+    // sum[m][n]: 16 weight rows m by 8 token rows n; x: the step's first element for
     // this lane in its token rows, of which `left` are inside the row
     template <int NT, bool ALL>
-    __device__ __forceinline__ void chunk(uint32_t stage, const T* const (&x)[NT], int left, const float (&scales_)[parts],
-                                          const uint32_t (&zeros_)[parts], float (&sum)[2][NT][4]) const {
+    __device__ __forceinline__ void take(uint32_t stage, const T* const (&x)[NT], int left, const float (&scales_)[groups],
+                                         const uint32_t (&zeros_)[groups], float (&sum)[2][NT][4]) const {
 #pragma unroll
-        for (int j = 0; j < parts; ++j) {
+        for (int hj = 0; hj < groups; ++hj) {
+            const int half = hj / parts, j = hj % parts;
             float scale[4];
             uint32_t zero[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                scale[i] = __shfl_sync(kAll, scales_[j], (lane & ~3) | i);
-                zero[i] = __shfl_sync(kAll, zeros_[j], (lane & ~3) | i);
+                scale[i] = __shfl_sync(kAll, scales_[hj], (lane & ~3) | i);
+                zero[i] = __shfl_sync(kAll, zeros_[hj], (lane & ~3) | i);
             }
             uint32_t q[4][words];
-            codes_of(stage, j, q);
+            codes_of(stage + 2048 * half, j, q);
             float part[2][NT][4] = {};
 #pragma unroll
             for (int u = 0; u < words; ++u) {
-                const int k = (j * 4 * words + u) * 8;  // from the lane's first element on
+                const int k = half * kChunk + (j * 4 * words + u) * 8;  // from the lane's first element on
                 uint4 b[NT];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -300,7 +312,7 @@ struct Warp {
 };
 
 template <typename T, int G, int NT>
-__device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, float* join, uint8_t* ring) {
+__device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, uint8_t* ring) {
     using W = Warp<T, G>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int split = p.split, part = warp & (split - 1), block = it.panel * (kWarps / split) + warp / split;
@@ -315,13 +327,13 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, f
             const int r = i < 2 ? a0 + 8 * i : b0 + 8 * (i - 2);
             return first + (r < p.r.N ? r : a0);
         };
-        const int chunks = (p.r.K + kChunk - 1) / kChunk;
+        const int steps = (p.r.K + W::step - 1) / W::step;
         W w{p};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w.codes[i] = p.codes + row(i) * (p.r.K / 2) + part * 64 + t4 * 16;
-        w.scales = static_cast<const uint16_t*>(p.scales) + row(t4) * p.groups + part * W::parts;
-        w.zeros = p.zeros + row(t4) * p.groups + part * W::parts;
-        const uint32_t mine = smem_u32(ring + warp * kStages * kStageBytes) + g * 64;
+        for (int i = 0; i < 4; ++i) w.codes[i] = p.codes + row(i) * (p.r.K / 2) + part * (W::step / 2) + t4 * 16;
+        w.scales = static_cast<const uint16_t*>(p.scales) + row(t4) * p.groups + part * W::groups;
+        w.zeros = p.zeros + row(t4) * p.groups + part * W::groups;
+        const uint32_t mine = smem_u32(ring + warp * kStages * W::stage_bytes) + g * 64;
         const int turn = g >> 1 & 3;
         w.put = mine + ((t4 ^ turn) << 4);
         w.get = W::words == 4 ? w.put : W::words == 2 ? mine + (((t4 >> 1) ^ turn) << 4) + (t4 & 1) * 8 : mine + (turn << 4) + t4 * 4;
@@ -332,66 +344,63 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, f
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int from = token_row(p, it.row + (n * 8 + g < it.rows ? n * 8 + g : 0));
-            x[n] = static_cast<const T*>(p.x) + (from < 0 ? 0 : from) * p.ldx + part * kChunk + t4 * W::words * 8;
+            x[n] = static_cast<const T*>(p.x) + (from < 0 ? 0 : from) * p.ldx + part * W::step + t4 * W::words * 8;
         }
-        // Past the end of a row any codes will do, with token rows that read as zero.
-        int ahead = part, bytes = p.r.K / 2 - part * 64 - t4 * 16;  // of the next chunk to load
+        int ahead = part;  // the next step to load
         auto load = [&](uint32_t stage) {
-            if (ahead < chunks) {
-                if (bytes <= 0) {  // the row's last 16 bytes instead
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w.codes[i] += bytes - 16;
-                }
-                w.load(stage);
+            if (ahead < steps) {
+                if ((ahead + 1) * W::step <= p.r.K)
+                    w.load_whole(stage);
+                else
+                    w.load(stage, p.r.K / 2 - ahead * (W::step / 2) - t4 * 16);
             }
             cp_async_commit();
             ahead += split;
-            bytes -= split * 64;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w.codes[i] += split * 64;
+            for (int i = 0; i < 4; ++i) w.codes[i] += split * (W::step / 2);
         };
 #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) load(i * kStageBytes);
-        float scale[W::parts];
-        uint32_t zero[W::parts];
-        int groups = p.groups - part * W::parts;  // from the next chunk's parameters on
-        if (part < chunks) w.params(groups, scale, zero);
+        for (int i = 0; i < kStages - 1; ++i) load(i * W::stage_bytes);
+        float scale[W::groups];
+        uint32_t zero[W::groups];
+        if (part < steps) w.params(p.groups - part * W::groups, scale, zero);
         uint32_t stage = 0;
-        int left = p.r.K - part * kChunk - t4 * W::words * 8;
-        for (int c = part; c < chunks; c += split) {
+        for (int c = part; c < steps; c += split) {
             cp_async_wait<kStages - 2>();
             __syncwarp();  // every lane's copies, and the reads of the stage that is filled next
-            load(stage == 0 ? (kStages - 1) * kStageBytes : stage - kStageBytes);
-            float s[W::parts];
-            uint32_t z[W::parts];
+            load(stage == 0 ? (kStages - 1) * W::stage_bytes : stage - W::stage_bytes);
+            float s[W::groups];
+            uint32_t z[W::groups];
 #pragma unroll
-            for (int j = 0; j < W::parts; ++j) s[j] = scale[j], z[j] = zero[j];
-            w.scales += split * W::parts;
-            w.zeros += split * W::parts;
-            groups -= split * W::parts;
-            if (c + split < chunks) w.params(groups, scale, zero);
-            if ((c + 1) * kChunk <= p.r.K)
-                w.template chunk<NT, true>(stage, x, 0, s, z, sum);
+            for (int j = 0; j < W::groups; ++j) s[j] = scale[j], z[j] = zero[j];
+            w.scales += split * W::groups;
+            w.zeros += split * W::groups;
+            if (c + split < steps) w.params(p.groups - (c + split) * W::groups, scale, zero);
+            if ((c + 1) * W::step <= p.r.K)
+                w.template take<NT, true>(stage, x, 0, s, z, sum);
             else
-                w.template chunk<NT, false>(stage, x, left, s, z, sum);
+                w.template take<NT, false>(stage, x, p.r.K - c * W::step - t4 * W::words * 8, s, z, sum);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) x[n] += split * kChunk;
-            left -= split * kChunk;
-            stage = stage == (kStages - 1) * kStageBytes ? 0 : stage + kStageBytes;
+            for (int n = 0; n < NT; ++n) x[n] += split * W::step;
+            stage = stage == (kStages - 1) * W::stage_bytes ? 0 : stage + W::stage_bytes;
         }
         __syncwarp();  // the next item's copies come after these reads
     }
-    if (split > 1) {  // the parts to the first of the warps, in order
+    if (split > 1) {  // the parts to the first of the warps, in order, through the ring's memory
+        float* join = reinterpret_cast<float*>(ring);
+        cp_async_wait<0>();
         __syncthreads();
         if (part > 0) {
 #pragma unroll
             for (int v = 0; v < 8 * NT; ++v) join[(warp * 8 * NT + v) * 32 + lane] = (&sum[0][0][0])[v];
         }
         __syncthreads();
-        if (part > 0) return;
-        for (int o = 1; o < split; ++o)
+        if (part == 0)
+            for (int o = 1; o < split; ++o)
 #pragma unroll
-            for (int v = 0; v < 8 * NT; ++v) (&sum[0][0][0])[v] += join[((warp + o) * 8 * NT + v) * 32 + lane];
+                for (int v = 0; v < 8 * NT; ++v) (&sum[0][0][0])[v] += join[((warp + o) * 8 * NT + v) * 32 + lane];
+        __syncthreads();
+        if (part > 0) return;
     }
     if (!live) return;
     // lane: token rows 2 t4 and 2 t4 + 1 of each eight, weight rows g and g + 8 of each 16
@@ -428,7 +437,6 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, f
 template <typename T, int G>
 __global__ void __launch_bounds__(32 * kWarps, 2) k_int4_product(const __grid_constant__ Int4Product p) {
     __shared__ Lists lists;
-    __shared__ float join[kWarps * kTile * 32];
     extern __shared__ __align__(128) uint8_t ring[];
     pdl_trigger();
     pdl_wait();
@@ -437,9 +445,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_int4_product(const __grid_co
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
         const Item it = item_at(lists, p.r.E, panels, t);
         if (it.rows > 8)
-            run_item<T, G, 2>(p, it, join, ring);
+            run_item<T, G, 2>(p, it, ring);
         else
-            run_item<T, G, 1>(p, it, join, ring);
+            run_item<T, G, 1>(p, it, ring);
     }
     cp_async_wait<0>();
 }
@@ -456,7 +464,11 @@ cudaError_t launch(const Int4Product& q, cudaStream_t st) {
     Int4Product p = q;
     const int64_t blocks = (p.r.N + 31) / 32;
     const int64_t tiles = p.r.R / kTile + (p.r.R < p.r.E ? p.r.R : p.r.E);  // at most
-    p.split = split_of(blocks * tiles, (p.r.K + kChunk - 1) / kChunk);
+    using W = Warp<T, G>;
+    constexpr int kSmem = kWarps * kStages * W::stage_bytes;
+    p.split = split_of(blocks * tiles, (p.r.K + W::step - 1) / W::step);
+    p.whole = p.groups % W::groups == 0 && (reinterpret_cast<uintptr_t>(p.scales) & (2 * W::groups - 1)) == 0 &&
+              (reinterpret_cast<uintptr_t>(p.zeros) & (W::groups - 1)) == 0;
     const int64_t per = kWarps / p.split, items = (blocks + per - 1) / per * tiles, most = 2 * num_sms();
     static bool ready[kMaxDevices] = {};
     int dev = 0;
@@ -530,8 +542,6 @@ extern "C" moe_status_t moe_grouped_gemm_int4(int32_t group, int32_t dtype, int6
     p.scales = w_scales;
     p.zeros = static_cast<const uint8_t*>(w_zeros);
     p.groups = (K + group - 1) / group;
-    const int parts = kChunk / group;
-    p.whole = p.groups % parts == 0 && aligned(w_scales, 2 * parts) && aligned(w_zeros, parts);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = dtype == MOE_DTYPE_BF16 ? product<__nv_bfloat16>(group, p, st)
                                                   : product<__half>(group, p, st);
