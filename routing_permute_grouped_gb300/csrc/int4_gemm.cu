@@ -139,15 +139,20 @@ __device__ __forceinline__ Item item_at(const Lists& s, int n_groups, int panels
     return it;
 }
 
+// Codes to 16-bit numbers.  Bits 0 .. 7 of a half word, with the rest zero, are the
+// number bits * 2^-133 (bf16) or bits * 2^-24 (f16): below 2^-126 and 2^-14, and in the
+// binade above, these types are linear.  So a masked nibble, in bits 0 .. 3 or 4 .. 7
+// as it lies, is multiplied up and has its zero point subtracted in one operation,
+// (code - zero) * 2^-6 or 2^-9 exactly, and two of a half word's four nibbles share a
+// shift.  (Or-ing each shifted nibble into the mantissa of 128 and subtracting takes
+// three shifts, which were what bound the kernel.)
 template <typename T>
 struct Wide;
 template <>
 struct Wide<__nv_bfloat16> {
-    static constexpr uint32_t magic = 0x43004300u;  // 128
-    __device__ static __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
-        const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-        return *reinterpret_cast<const uint32_t*>(&r);
-    }
+    using P = __nv_bfloat162;
+    static constexpr uint32_t low = 0x7F007F00u, high = 0x7D007D00u;  // 2^127, 2^123
+    static constexpr float unit = 0x1p-6f;
     __device__ static __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -156,23 +161,24 @@ struct Wide<__nv_bfloat16> {
 };
 template <>
 struct Wide<__half> {
-    static constexpr uint32_t magic = 0x64006400u;  // 1024
-    __device__ static __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
-        const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-        return *reinterpret_cast<const uint32_t*>(&r);
-    }
+    using P = __half2;
+    static constexpr uint32_t low = 0x78007800u, high = 0x68006800u;  // 2^15, 2^11
+    static constexpr float unit = 0x1p-9f;
     __device__ static __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
 };
-// Pair i of a word's eight codes as numbers; zero is magic + zero point in both halves.
+// Pair i of a word's eight codes, times Wide<T>::unit; zero is -zero point in both
+// halves in the same unit.
 template <typename T>
 __device__ __forceinline__ uint32_t widen(uint32_t w, int i, uint32_t zero) {
-    uint32_t v;  // (w >> 4 i & mask) | magic in one operation besides the shift
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w >> (4 * i)), "r"(0x000F000Fu), "r"(Wide<T>::magic));
-    return Wide<T>::sub(v, zero);
+    using P = typename Wide<T>::P;
+    const uint32_t bits = (i < 2 ? w : w >> 8) & (i & 1 ? 0x00F000F0u : 0x000F000Fu);
+    const uint32_t up = i & 1 ? Wide<T>::high : Wide<T>::low;
+    const P v = __hfma2(*reinterpret_cast<const P*>(&bits), *reinterpret_cast<const P*>(&up), *reinterpret_cast<const P*>(&zero));
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // The token row of row r of y; -1 where src picks none.
@@ -228,7 +234,8 @@ struct Warp {
                 asm volatile("ld.shared.b32 %0, [%1];" : "=r"(q[i][0]) : "r"(at + 512 * i) : "memory");
         }
     }
-    // Scales as fp32, and magic + zero point in both halves, of the next step; past the
+    // Scales over the unit of the codes, and the zero points as widen takes them, of the
+    // next step; past the
     // last group (left: groups from this one on) the last one's, for sums of 0.
     __device__ __forceinline__ void params(int left, float (&scale)[groups], uint32_t (&zero)[groups]) const {
         uint32_t s[groups], z[groups];
@@ -254,8 +261,9 @@ struct Warp {
         }
 #pragma unroll
         for (int j = 0; j < groups; ++j) {
-            scale[j] = to_float<T>(__builtin_bit_cast(T, static_cast<uint16_t>(s[j])));
-            zero[j] = Wide<T>::magic + z[j] * 0x00010001u;
+            scale[j] = to_float<T>(__builtin_bit_cast(T, static_cast<uint16_t>(s[j]))) * (1.0f / Wide<T>::unit);
+            const float back = static_cast<float>(z[j]) * -Wide<T>::unit;
+            zero[j] = pack2(T(), back, back);
         }
     }
 
