@@ -43,7 +43,8 @@ constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kChunk = 128;   // elements of the sum that a lane's four words and its neighbours' make
 constexpr int kWarps = 8;     // of a CTA, two CTAs to an SM
 constexpr int kTile = 16;     // token rows of an item, at most
-constexpr int kStages = 3;    // steps of a warp's codes in shared memory
+constexpr int kStages = 2;    // steps of a warp's codes in shared memory
+constexpr int kRowBytes = 16 * 1024;  // of a block of token rows
 
 struct Int4Product {
     RaggedArgs r;          // N: weight rows per group
@@ -153,6 +154,11 @@ struct Wide<__nv_bfloat16> {
     using P = __nv_bfloat162;
     static constexpr uint32_t low = 0x7F007F00u, high = 0x7D007D00u;  // 2^127, 2^123
     static constexpr float unit = 0x1p-6f;
+    __device__ static __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+    }
     __device__ static __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -164,6 +170,11 @@ struct Wide<__half> {
     using P = __half2;
     static constexpr uint32_t low = 0x78007800u, high = 0x68006800u;  // 2^15, 2^11
     static constexpr float unit = 0x1p-9f;
+    __device__ static __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+    }
     __device__ static __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -186,6 +197,14 @@ __device__ __forceinline__ int token_row(const Int4Product& p, int r) {
     if (!p.src) return r;
     const int s = ld_dep(p.src + r), from = s / p.src_div;
     return s >= 0 && from < p.x_rows ? from : -1;
+}
+
+// Where piece `piece` (16 bytes) of a token row's 256 bytes of a chunk lies: eight
+// lanes that read their B operands together (two rows, four pieces) meet no bank twice.
+template <int WORDS>
+__device__ __forceinline__ int row_place(int row, int piece) {
+    if (WORDS == 4) piece = (piece & 3) << 2 | piece >> 2;
+    return piece ^ (WORDS == 2 ? row & 1 : (row & 1) << 2);
 }
 
 template <typename T, int G>
@@ -267,11 +286,22 @@ struct Warp {
         }
     }
 
-    // sum[m][n]: 16 weight rows m by 8 token rows n; x: the step's first element for
-    // this lane in its token rows, of which `left` are inside the row
-    template <int NT, bool ALL>
-    __device__ __forceinline__ void take(uint32_t stage, const T* const (&x)[NT], int left, const float (&scales_)[groups],
+    // sum[m][n]: 16 weight rows m by 8 token rows n; x: the step's first element of this
+    // lane's token rows in shared memory, 256 bytes for a chunk, pieces placed by row_place
+    template <int NT>
+    __device__ __forceinline__ void take(uint32_t stage, const uint32_t (&x)[NT], int odd, const float (&scales_)[groups],
                                          const uint32_t (&zeros_)[groups], float (&sum)[2][NT][4]) const {
+        uint4 ahead[NT];
+        auto fetch = [&](int w) {  // the lane's word w of the step
+            const int at = w / 4 * 256 + (row_place<words>(0, (w % 4 / words * 4 + t4) * words + w % words) << 4 ^ odd);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(ahead[n].x), "=r"(ahead[n].y), "=r"(ahead[n].z), "=r"(ahead[n].w)
+                             : "r"(x[n] + at)
+                             : "memory");
+        };
+        fetch(0);
 #pragma unroll
         for (int hj = 0; hj < groups; ++hj) {
             const int half = hj / parts, j = hj % parts;
@@ -284,18 +314,13 @@ struct Warp {
             }
             uint32_t q[4][words];
             codes_of(stage + 2048 * half, j, q);
-            float part[2][NT][4] = {};
+            float part[2][NT][4];
 #pragma unroll
             for (int u = 0; u < words; ++u) {
-                const int k = half * kChunk + (j * 4 * words + u) * 8;  // from the lane's first element on
                 uint4 b[NT];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (ALL || k < left)
-                        b[n] = *reinterpret_cast<const uint4*>(x[n] + k);
-                    else
-                        b[n] = make_uint4(0, 0, 0, 0);
-                }
+                for (int n = 0; n < NT; ++n) b[n] = ahead[n];
+                if (hj * words + u + 1 < groups * words) fetch(hj * words + u + 1);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -306,7 +331,12 @@ struct Warp {
                         a[2] = widen<T>(q[2 * m][u], 2 * h + 1, zero[2 * m]);
                         a[3] = widen<T>(q[2 * m + 1][u], 2 * h + 1, zero[2 * m + 1]);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) Wide<T>::mma(part[m][n], a, h ? b[n].z : b[n].x, h ? b[n].w : b[n].y);
+                        for (int n = 0; n < NT; ++n) {
+                            if (u == 0 && h == 0)
+                                Wide<T>::mma0(part[m][n], a, b[n].x, b[n].y);
+                            else
+                                Wide<T>::mma(part[m][n], a, h ? b[n].z : b[n].x, h ? b[n].w : b[n].y);
+                        }
                     }
             }
 #pragma unroll
@@ -319,61 +349,92 @@ struct Warp {
     }
 };
 
+struct Shared {
+    Lists lists;
+    uint64_t full[2], empty[2];  // blocks of token rows
+    uint32_t abort;
+};
+
 template <typename T, int G, int NT>
-__device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, uint8_t* ring) {
+__device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, Shared& sh, uint8_t* ring, uint8_t* s_rows,
+                                         int& blocks_so_far, bool& timed_out) {
     using W = Warp<T, G>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int split = p.split, part = warp & (split - 1), block = it.panel * (kWarps / split) + warp / split;
     // the warp's weight rows: 16 from a on and 16 from b on
     const int a0 = p.swiglu ? (block >> 3) * 256 + (block & 7) * 16 : block * 32, b0 = a0 + (p.swiglu ? 128 : 16);
     const bool live = a0 < p.r.N;
-    float sum[2][NT][4] = {};
-    if (live) {
-        const int64_t first = static_cast<int64_t>(it.e) * p.r.N + g;
-        // N is a multiple of 8: rows past the last one are read as others, and not stored
-        auto row = [&](int i) {
-            const int r = i < 2 ? a0 + 8 * i : b0 + 8 * (i - 2);
-            return first + (r < p.r.N ? r : a0);
-        };
-        const int steps = (p.r.K + W::step - 1) / W::step;
-        W w{p};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w.codes[i] = p.codes + row(i) * (p.r.K / 2) + part * (W::step / 2) + t4 * 16;
-        w.scales = static_cast<const uint16_t*>(p.scales) + row(t4) * p.groups + part * W::groups;
-        w.zeros = p.zeros + row(t4) * p.groups + part * W::groups;
-        const uint32_t mine = smem_u32(ring + warp * kStages * W::stage_bytes) + g * 64;
-        const int turn = g >> 1 & 3;
-        w.put = mine + ((t4 ^ turn) << 4);
-        w.get = W::words == 4 ? w.put : W::words == 2 ? mine + (((t4 >> 1) ^ turn) << 4) + (t4 & 1) * 8 : mine + (turn << 4) + t4 * 4;
-        w.lane = lane;
-        w.t4 = t4;
-        // columns of the product past the item's rows are not stored: any row will do
-        const T* x[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int from = token_row(p, it.row + (n * 8 + g < it.rows ? n * 8 + g : 0));
-            x[n] = static_cast<const T*>(p.x) + (from < 0 ? 0 : from) * p.ldx + part * W::step + t4 * W::words * 8;
-        }
-        int ahead = part;  // the next step to load
-        auto load = [&](uint32_t stage) {
-            if (ahead < steps) {
-                if ((ahead + 1) * W::step <= p.r.K)
-                    w.load_whole(stage);
-                else
-                    w.load(stage, p.r.K / 2 - ahead * (W::step / 2) - t4 * 16);
+    const int64_t first = static_cast<int64_t>(it.e) * p.r.N + g;
+    // N is a multiple of 8: rows past the last one are read as others, and not stored
+    auto row = [&](int i) {
+        const int r = i < 2 ? a0 + 8 * i : b0 + 8 * (i - 2);
+        return first + (r < p.r.N ? r : live ? a0 : 0);
+    };
+    // Token rows, in blocks of `columns` elements, two in shared memory.  Columns of the
+    // product past the item's rows are not stored: any row will do for them.
+    const int held = NT == 2 ? 16 : it.rows > 4 ? 8 : it.rows > 2 ? 4 : it.rows;  // rows with a place
+    const int super = split * W::step, supers = (p.r.K + super - 1) / super;
+    const int each = min(supers, kRowBytes / (held * 2) / super), columns = each * super;
+    const int n_blocks = (supers + each - 1) / each;
+    auto load_rows = [&](int b) {
+        const int use = blocks_so_far + b, buf = use & 1;
+        timed_out = timed_out || !warp_wait(sh.empty + buf, (use >> 1 & 1) ^ 1, &sh.abort);
+        const uint32_t dst = smem_u32(s_rows) + buf * kRowBytes;
+        for (int r = 0; r < it.rows; ++r) {
+            const int from = token_row(p, it.row + r);
+            const T* x = static_cast<const T*>(p.x) + (from < 0 ? 0 : from) * p.ldx + b * columns;
+            for (int q = threadIdx.x; q < columns / 8; q += 32 * kWarps) {
+                const bool in = b * columns + q * 8 < p.r.K;
+                cp_async_16(dst + r * columns * 2 + (q >> 4) * 256 + (row_place<W::words>(r, q & 15) << 4), in ? x + q * 8 : x - b * columns,
+                            in ? 16 : 0);
             }
-            cp_async_commit();
-            ahead += split;
+        }
+        cp_async_arrive(sh.full + buf);
+    };
+    W w{p};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w.codes[i] += split * (W::step / 2);
-        };
+    for (int i = 0; i < 4; ++i) w.codes[i] = p.codes + row(i) * (p.r.K / 2) + part * (W::step / 2) + t4 * 16;
+    w.scales = static_cast<const uint16_t*>(p.scales) + row(t4) * p.groups + part * W::groups;
+    w.zeros = p.zeros + row(t4) * p.groups + part * W::groups;
+    const uint32_t mine = smem_u32(ring + warp * kStages * W::stage_bytes) + g * 64;
+    const int turn = g >> 1 & 3;
+    w.put = mine + ((t4 ^ turn) << 4);
+    w.get = W::words == 4 ? w.put : W::words == 2 ? mine + (((t4 >> 1) ^ turn) << 4) + (t4 & 1) * 8 : mine + (turn << 4) + t4 * 4;
+    w.lane = lane;
+    w.t4 = t4;
+    const int steps = (p.r.K + W::step - 1) / W::step;
+    int ahead = part;  // the next step to load
+    auto load = [&](uint32_t stage) {
+        if (ahead < steps) {
+            if ((ahead + 1) * W::step <= p.r.K)
+                w.load_whole(stage);
+            else
+                w.load(stage, p.r.K / 2 - ahead * (W::step / 2) - t4 * 16);
+        }
+        cp_async_commit();
+        ahead += split;
 #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) load(i * W::stage_bytes);
-        float scale[W::groups];
-        uint32_t zero[W::groups];
-        if (part < steps) w.params(p.groups - part * W::groups, scale, zero);
-        uint32_t stage = 0;
-        for (int c = part; c < steps; c += split) {
+        for (int i = 0; i < 4; ++i) w.codes[i] += split * (W::step / 2);
+    };
+    load_rows(0);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) load(i * W::stage_bytes);
+    float scale[W::groups];
+    uint32_t zero[W::groups];
+    if (part < steps) w.params(p.groups - part * W::groups, scale, zero);
+    float sum[2][NT][4] = {};
+    uint32_t stage = 0;
+    const int mine_of = (NT == 2 ? g : g & (held - 1)), odd = row_place<W::words>(mine_of, 0) << 4;
+    for (int b = 0; b < n_blocks; ++b) {
+        if (b + 1 < n_blocks) load_rows(b + 1);
+        const int use = blocks_so_far + b, buf = use & 1;
+        timed_out = timed_out || !warp_wait(sh.full + buf, use >> 1 & 1, &sh.abort);
+        uint32_t x[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            x[n] = smem_u32(s_rows) + buf * kRowBytes + (n * 8 + mine_of) * columns * 2 + part * (W::step * 2);
+        const int end = min((b + 1) * each * split, steps);
+        for (int c = b * each * split + part; c < end; c += split) {
             cp_async_wait<kStages - 2>();
             __syncwarp();  // every lane's copies, and the reads of the stage that is filled next
             load(stage == 0 ? (kStages - 1) * W::stage_bytes : stage - W::stage_bytes);
@@ -384,16 +445,16 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, u
             w.scales += split * W::groups;
             w.zeros += split * W::groups;
             if (c + split < steps) w.params(p.groups - (c + split) * W::groups, scale, zero);
-            if ((c + 1) * W::step <= p.r.K)
-                w.template take<NT, true>(stage, x, 0, s, z, sum);
-            else
-                w.template take<NT, false>(stage, x, p.r.K - c * W::step - t4 * W::words * 8, s, z, sum);
+            w.template take<NT>(stage, x, odd, s, z, sum);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) x[n] += split * W::step;
+            for (int n = 0; n < NT; ++n) x[n] += super * 2;
             stage = stage == (kStages - 1) * W::stage_bytes ? 0 : stage + W::stage_bytes;
         }
-        __syncwarp();  // the next item's copies come after these reads
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sh.empty + buf);
     }
+    blocks_so_far += n_blocks;
+    __syncwarp();  // the next item's copies come after these reads
     if (split > 1) {  // the parts to the first of the warps, in order, through the ring's memory
         float* join = reinterpret_cast<float*>(ring);
         cp_async_wait<0>();
@@ -444,26 +505,43 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, u
 
 template <typename T, int G>
 __global__ void __launch_bounds__(32 * kWarps, 2) k_int4_product(const __grid_constant__ Int4Product p) {
-    __shared__ Lists lists;
+    __shared__ Shared sh;
     extern __shared__ __align__(128) uint8_t ring[];
     pdl_trigger();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sh.full + i, 32 * kWarps);
+            mbar_init(sh.empty + i, kWarps);
+        }
+        sh.abort = 0;
+        fence_mbar_init();
+    }
     pdl_wait();
     const int blocks = (p.r.N + 31) / 32, per = kWarps / p.split, panels = (blocks + per - 1) / per;
-    const int total = build_lists(p.r, lists, panels);
+    const int total = build_lists(p.r, sh.lists, panels);
+    uint8_t* rows = ring + kWarps * kStages * Warp<T, G>::stage_bytes;
+    int blocks_so_far = 0;  // of token rows
+    bool timed_out = false;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
-        const Item it = item_at(lists, p.r.E, panels, t);
+        const Item it = item_at(sh.lists, p.r.E, panels, t);
         if (it.rows > 8)
-            run_item<T, G, 2>(p, it, ring);
+            run_item<T, G, 2>(p, it, sh, ring, rows, blocks_so_far, timed_out);
         else
-            run_item<T, G, 1>(p, it, ring);
+            run_item<T, G, 1>(p, it, sh, ring, rows, blocks_so_far, timed_out);
     }
-    cp_async_wait<0>();
+    cp_async_commit();
+    cp_async_wait<0>();  // nothing may still be written to shared memory at exit
+    if (timed_out && p.r.status) atomicOr(p.r.status, kRaggedTimeout);
 }
 
-// Warps that split a sum: more where the items are few.
-int split_of(int64_t blocks_by_tiles, int chunks) {
+// Warps that split a sum: more where the items are few, as far as the token rows of
+// their steps fit a block.
+int split_of(int64_t blocks_by_tiles, int64_t rows, int steps, int step) {
+    const int held = rows > 8 ? 16 : rows > 4 ? 8 : rows > 2 ? 4 : static_cast<int>(rows);  // of the longest tile
     int split = 1;
-    while (split < kWarps && blocks_by_tiles * split < 4ll * kWarps * 2 * num_sms() && chunks >= 2 * split) split *= 2;
+    while (split < kWarps && blocks_by_tiles * split < 4ll * kWarps * 2 * num_sms() && steps >= 2 * split &&
+           2 * split * held * step * 2 <= kRowBytes)
+        split *= 2;
     return split;
 }
 
@@ -473,8 +551,8 @@ cudaError_t launch(const Int4Product& q, cudaStream_t st) {
     const int64_t blocks = (p.r.N + 31) / 32;
     const int64_t tiles = p.r.R / kTile + (p.r.R < p.r.E ? p.r.R : p.r.E);  // at most
     using W = Warp<T, G>;
-    constexpr int kSmem = kWarps * kStages * W::stage_bytes;
-    p.split = split_of(blocks * tiles, (p.r.K + W::step - 1) / W::step);
+    constexpr int kSmem = kWarps * kStages * W::stage_bytes + 2 * kRowBytes;
+    p.split = split_of(blocks * tiles, p.r.R, (p.r.K + W::step - 1) / W::step, W::step);
     p.whole = p.groups % W::groups == 0 && (reinterpret_cast<uintptr_t>(p.scales) & (2 * W::groups - 1)) == 0 &&
               (reinterpret_cast<uintptr_t>(p.zeros) & (W::groups - 1)) == 0;
     const int64_t per = kWarps / p.split, items = (blocks + per - 1) / per * tiles, most = 2 * num_sms();
