@@ -44,7 +44,7 @@ constexpr int kChunk = 128;   // elements of the sum that a lane's four words an
 constexpr int kWarps = 8;     // of a CTA, two CTAs to an SM
 constexpr int kTile = 16;     // token rows of an item, at most
 constexpr int kStages = 2;    // steps of a warp's codes in shared memory
-constexpr int kRowBytes = 16 * 1024;  // of a block of token rows
+constexpr int kRowBytes = 18 * 1024;  // of a block of token rows
 
 struct Int4Product {
     RaggedArgs r;          // N: weight rows per group
@@ -59,7 +59,7 @@ struct Int4Product {
     const void* scales;    // [E, N, groups]
     const uint8_t* zeros;  // the same, or null
     int32_t groups;        // per weight row
-    int32_t whole;         // a step's scales and zero points can be read at once
+    int32_t whole;         // scales and zero points can be copied four bytes at a time
     int32_t split;         // warps that share a sum: 1, 2, 4 or 8
 };
 
@@ -211,12 +211,14 @@ template <typename T, int G>
 struct Warp {
     static constexpr int parts = kChunk / G, words = 4 / parts;  // groups of a chunk, words of a lane in each
     static constexpr int halves = G == 128 ? 2 : 1;              // chunks of a step
-    static constexpr int groups = halves * parts, step = halves * kChunk, stage_bytes = halves * 32 * 64;
+    static constexpr int groups = halves * parts, step = halves * kChunk;
+    // of a step: codes, then scales and (four bytes with) zero points of a row per lane
+    static constexpr int code_bytes = halves * 32 * 64, stage_bytes = code_bytes + 32 * (2 * groups + 4);
     const Int4Product& p;
     const uint8_t* codes[4];  // this lane's 16 bytes of the next step's first chunk, of its four weight rows
-    const uint16_t* scales;   // of the next step, of the weight row lane % 4 of the four
+    const uint16_t* scales;   // of the weight row lane % 4 of the four
     const uint8_t* zeros;
-    uint32_t put, get;        // this lane's places in the first of the warp's stages
+    uint32_t put, get, par, par_zero;  // this lane's places in the first of the warp's stages
     int lane, t4;             // lane % 4
 
     // 32 rows x 64 bytes of every chunk; a row's 16-byte pieces in an order that its
@@ -253,34 +255,48 @@ struct Warp {
                 asm volatile("ld.shared.b32 %0, [%1];" : "=r"(q[i][0]) : "r"(at + 512 * i) : "memory");
         }
     }
-    // Scales over the unit of the codes, and the zero points as widen takes them, of the
-    // next step; past the
-    // last group (left: groups from this one on) the last one's, for sums of 0.
-    __device__ __forceinline__ void params(int left, float (&scale)[groups], uint32_t (&zero)[groups]) const {
+    // Scales and zero points of step c come by way of shared memory as well, where they
+    // can be copied four bytes at a time (`whole`); else they are read as they are
+    // needed.  Past the last group the last ones', for sums of 0.
+    __device__ __forceinline__ void load_params(uint32_t stage, int c) const {
+        const int at = min(c * groups, p.groups - groups);
+        const uint32_t dst = par + stage;
+        if constexpr (groups == 4)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(scales + at) : "memory");
+        else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(scales + at) : "memory");
+        if (p.zeros)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(par_zero + stage), "l"(zeros + (at & ~3)) : "memory");
+    }
+    __device__ __forceinline__ void params(uint32_t stage, int c, float (&scale)[groups], uint32_t (&zero)[groups]) const {
         uint32_t s[groups], z[groups];
-        if (!p.whole) {
+        if (p.whole) {
+            const uint32_t at = par + stage;
+            uint32_t v[groups / 2], w = 0x08080808u;
+            if constexpr (groups == 4)
+                asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at) : "memory");
+            else
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(at) : "memory");
+            if (p.zeros) {
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(par_zero + stage) : "memory");
+                if constexpr (groups == 2) w >>= (min(c * groups, p.groups - groups) & 2) * 8;
+            }
 #pragma unroll
             for (int j = 0; j < groups; ++j) {
-                const int at = min(j, left - 1);
+                s[j] = v[j / 2] >> (16 * (j & 1)) & 0xFFFFu;
+                z[j] = w >> (8 * j) & 0xFFu;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < groups; ++j) {
+                const int at = min(c * groups + j, p.groups - 1);
                 s[j] = scales[at];
                 z[j] = p.zeros ? zeros[at] : 8u;
             }
-        } else if constexpr (groups == 2) {
-            const uint32_t v = *reinterpret_cast<const uint32_t*>(scales);
-            const uint32_t w = p.zeros ? *reinterpret_cast<const uint16_t*>(zeros) : 0x0808u;
-            s[0] = v & 0xFFFFu, s[1] = v >> 16;
-            z[0] = w & 0xFFu, z[1] = w >> 8;
-        } else {
-            static_assert(groups == 4 || groups == 2, "groups of a step");
-            const uint2 v = *reinterpret_cast<const uint2*>(scales);
-            const uint32_t w = p.zeros ? *reinterpret_cast<const uint32_t*>(zeros) : 0x08080808u;
-            s[0] = v.x & 0xFFFFu, s[1] = v.x >> 16, s[2] = v.y & 0xFFFFu, s[3] = v.y >> 16;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) z[j] = w >> (8 * j) & 0xFFu;
         }
 #pragma unroll
         for (int j = 0; j < groups; ++j) {
-            scale[j] = to_float<T>(__builtin_bit_cast(T, static_cast<uint16_t>(s[j]))) * (1.0f / Wide<T>::unit);
+            scale[j] = to_float<T>(__builtin_bit_cast(T, static_cast<uint16_t>(s[j])));
             const float back = static_cast<float>(z[j]) * -Wide<T>::unit;
             zero[j] = pack2(T(), back, back);
         }
@@ -394,9 +410,11 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, S
     W w{p};
 #pragma unroll
     for (int i = 0; i < 4; ++i) w.codes[i] = p.codes + row(i) * (p.r.K / 2) + part * (W::step / 2) + t4 * 16;
-    w.scales = static_cast<const uint16_t*>(p.scales) + row(t4) * p.groups + part * W::groups;
-    w.zeros = p.zeros + row(t4) * p.groups + part * W::groups;
-    const uint32_t mine = smem_u32(ring + warp * kStages * W::stage_bytes) + g * 64;
+    w.scales = static_cast<const uint16_t*>(p.scales) + row(t4) * p.groups;
+    w.zeros = p.zeros + row(t4) * p.groups;
+    const uint32_t stages = smem_u32(ring + warp * kStages * W::stage_bytes), mine = stages + g * 64;
+    w.par = stages + W::code_bytes + lane * 2 * W::groups;
+    w.par_zero = stages + W::code_bytes + 64 * W::groups + lane * 4;
     const int turn = g >> 1 & 3;
     w.put = mine + ((t4 ^ turn) << 4);
     w.get = W::words == 4 ? w.put : W::words == 2 ? mine + (((t4 >> 1) ^ turn) << 4) + (t4 & 1) * 8 : mine + (turn << 4) + t4 * 4;
@@ -410,6 +428,7 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, S
                 w.load_whole(stage);
             else
                 w.load(stage, p.r.K / 2 - ahead * (W::step / 2) - t4 * 16);
+            if (p.whole) w.load_params(stage, ahead);
         }
         cp_async_commit();
         ahead += split;
@@ -419,9 +438,6 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, S
     load_rows(0);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) load(i * W::stage_bytes);
-    float scale[W::groups];
-    uint32_t zero[W::groups];
-    if (part < steps) w.params(p.groups - part * W::groups, scale, zero);
     float sum[2][NT][4] = {};
     uint32_t stage = 0;
     const int mine_of = (NT == 2 ? g : g & (held - 1)), odd = row_place<W::words>(mine_of, 0) << 4;
@@ -440,11 +456,7 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, S
             load(stage == 0 ? (kStages - 1) * W::stage_bytes : stage - W::stage_bytes);
             float s[W::groups];
             uint32_t z[W::groups];
-#pragma unroll
-            for (int j = 0; j < W::groups; ++j) s[j] = scale[j], z[j] = zero[j];
-            w.scales += split * W::groups;
-            w.zeros += split * W::groups;
-            if (c + split < steps) w.params(p.groups - (c + split) * W::groups, scale, zero);
+            w.params(stage, c, s, z);
             w.template take<NT>(stage, x, odd, s, z, sum);
 #pragma unroll
             for (int n = 0; n < NT; ++n) x[n] += super * 2;
@@ -454,6 +466,9 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, S
         if (lane == 0) mbar_arrive(sh.empty + buf);
     }
     blocks_so_far += n_blocks;
+    // the codes were widened in units of their own
+#pragma unroll
+    for (int v = 0; v < 8 * NT; ++v) (&sum[0][0][0])[v] *= 1.0f / Wide<T>::unit;
     __syncwarp();  // the next item's copies come after these reads
     if (split > 1) {  // the parts to the first of the warps, in order, through the ring's memory
         float* join = reinterpret_cast<float*>(ring);
@@ -553,8 +568,8 @@ cudaError_t launch(const Int4Product& q, cudaStream_t st) {
     using W = Warp<T, G>;
     constexpr int kSmem = kWarps * kStages * W::stage_bytes + 2 * kRowBytes;
     p.split = split_of(blocks * tiles, p.r.R, (p.r.K + W::step - 1) / W::step, W::step);
-    p.whole = p.groups % W::groups == 0 && (reinterpret_cast<uintptr_t>(p.scales) & (2 * W::groups - 1)) == 0 &&
-              (reinterpret_cast<uintptr_t>(p.zeros) & (W::groups - 1)) == 0;
+    p.whole = p.groups % (p.zeros ? 4 : W::groups) == 0 && (reinterpret_cast<uintptr_t>(p.scales) & (2 * W::groups - 1)) == 0 &&
+              (reinterpret_cast<uintptr_t>(p.zeros) & 3) == 0;
     const int64_t per = kWarps / p.split, items = (blocks + per - 1) / per * tiles, most = 2 * num_sms();
     static bool ready[kMaxDevices] = {};
     int dev = 0;
