@@ -21,7 +21,8 @@ LIB = os.path.join(BUILD, "libmoe_gb300.so")
 SOURCES = ["moe_abi.cu", "grouped_gemm.cu", "offsets.cu", "permute_combine.cu", "pack.cu",
            "offsets_noalloc.cu", "router_reduce.cu", "skinny_gemm.cu",
            "backward.cu", "wgrad_gemm.cu", "ragged_gemm.cu", "fp4.cu", "fp4_gemm.cu",
-           "route_scores.cu", "int4.cu", "int4_gemm.cu"]
+           "route_scores.cu", "int4.cu", "int4_gemm.cu",
+           "int4_wide.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]

@@ -41,162 +41,30 @@ namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kChunk = 128;   // elements of the sum that a lane's four words and its neighbours' make
-constexpr int kWarps = 8;     // of a CTA, two CTAs to an SM
-constexpr int kTile = 16;     // token rows of an item, at most
 constexpr int kStages = 2;    // steps of a warp's codes in shared memory
+
+constexpr int kWarps = 8;     // of a CTA, two CTAs to an SM
+constexpr int kTile = 8;      // token rows of an item, at most
 constexpr int kRowBytes = 18 * 1024;  // of a block of token rows
 
-struct Int4Product {
-    RaggedArgs r;          // N: weight rows per group
-    const void* x;
-    int64_t ldx;
-    int32_t x_rows;
-    int32_t columns;       // of y
-    int32_t swiglu;
-    const int32_t* src;    // [R] or null
-    int32_t src_div;
-    const uint8_t* codes;  // [E, N, K / 2]
-    const void* scales;    // [E, N, groups]
-    const uint8_t* zeros;  // the same, or null
-    int32_t groups;        // per weight row
-    int32_t whole;         // scales and zero points can be copied four bytes at a time
-    int32_t split;         // warps that share a sum: 1, 2, 4 or 8
-};
-
-// Rows [lo, hi) of every group, its token tiles' width and its first work item
-struct Lists {
-    int first[260], lo[260], hi[260], width[260];
-};
-
-struct Item {
-    int e, panel;
-    int row, rows;  // token rows
-};
-
-// All threads: thread e takes group e.  Where a group is bad, groups may overlap:
-// each then starts past the ends of those before it.
-__device__ __forceinline__ int build_lists(const RaggedArgs& a, Lists& s, int panels) {
-    __shared__ int sums[8];
-    const int e = threadIdx.x, lane = e & 31;
-    bool bad = false;
-    if (e < a.E) {
-        const int2 g = group_rows(a, e, &bad);
-        s.lo[e] = g.x;
-        s.hi[e] = g.y;
+// d (+)= a b on 16 weight rows, 8 token rows and 16 elements
+template <typename T, bool FIRST>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+#define MOE_MMA(type)                                                                                                     \
+    if constexpr (FIRST)                                                                                                  \
+        asm("mma.sync.aligned.m16n8k16.row.col.f32." type "." type ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};" \
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                                              \
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));                                   \
+    else                                                                                                                  \
+        asm("mma.sync.aligned.m16n8k16.row.col.f32." type "." type ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};" \
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                                              \
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1))
+    if constexpr (std::is_same_v<T, __half>) {
+        MOE_MMA("f16");
+    } else {
+        MOE_MMA("bf16");
     }
-    if (__syncthreads_or(bad)) {
-        if (e == 0)
-            for (int i = 0, end = 0; i < a.E; ++i) {
-                s.lo[i] = min(max(s.lo[i], end), s.hi[i]);
-                end = max(end, s.hi[i]);
-            }
-        __syncthreads();
-    }
-    int n = 0;
-    if (e < a.E) {
-        const int len = s.hi[e] - s.lo[e], tiles = (len + kTile - 1) / kTile;
-        s.width[e] = tiles ? ((len + tiles - 1) / tiles + 7) & ~7 : 8;
-        n = tiles * panels;
-    }
-    int x = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(kAll, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) sums[e >> 5] = x;
-    __syncthreads();
-    int total = 0, before = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (i == e >> 5) before = total;
-        total += sums[i];
-    }
-    if (e < a.E) s.first[e] = before + x - n;
-    if (e == 0) s.first[a.E] = total;
-    __syncthreads();
-    return total;
-}
-
-// Item t: its group by bisection; the token tiles of a panel follow one another,
-// so that the CTAs that take them find its codes in L2.
-__device__ __forceinline__ Item item_at(const Lists& s, int n_groups, int panels, int t) {
-    int e = 0, end = n_groups;  // first[e] <= t < first[end]
-    while (end - e > 1) {
-        const int mid = (e + end) >> 1;
-        if (s.first[mid] <= t)
-            e = mid;
-        else
-            end = mid;
-    }
-    Item it;
-    it.e = e;
-    const unsigned i = t - s.first[e], tiles = static_cast<unsigned>(s.first[e + 1] - s.first[e]) / panels;
-    const unsigned panel = i / tiles;
-    const int width = s.width[e];
-    it.panel = static_cast<int>(panel);
-    it.row = s.lo[e] + static_cast<int>(i - panel * tiles) * width;
-    it.rows = min(width, s.hi[e] - it.row);
-    return it;
-}
-
-// Codes to 16-bit numbers.  Bits 0 .. 7 of a half word, with the rest zero, are the
-// number bits * 2^-133 (bf16) or bits * 2^-24 (f16): below 2^-126 and 2^-14, and in the
-// binade above, these types are linear.  So a masked nibble, in bits 0 .. 3 or 4 .. 7
-// as it lies, is multiplied up and has its zero point subtracted in one operation,
-// (code - zero) * 2^-6 or 2^-9 exactly, and two of a half word's four nibbles share a
-// shift.  (Or-ing each shifted nibble into the mantissa of 128 and subtracting takes
-// three shifts, which were what bound the kernel.)
-template <typename T>
-struct Wide;
-template <>
-struct Wide<__nv_bfloat16> {
-    using P = __nv_bfloat162;
-    static constexpr uint32_t low = 0x7F007F00u, high = 0x7D007D00u;  // 2^127, 2^123
-    static constexpr float unit = 0x1p-6f;
-    __device__ static __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
-    }
-    __device__ static __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-};
-template <>
-struct Wide<__half> {
-    using P = __half2;
-    static constexpr uint32_t low = 0x78007800u, high = 0x68006800u;  // 2^15, 2^11
-    static constexpr float unit = 0x1p-9f;
-    __device__ static __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
-    }
-    __device__ static __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-};
-// Pair i of a word's eight codes, times Wide<T>::unit; zero is -zero point in both
-// halves in the same unit.
-template <typename T>
-__device__ __forceinline__ uint32_t widen(uint32_t w, int i, uint32_t zero) {
-    using P = typename Wide<T>::P;
-    const uint32_t bits = (i < 2 ? w : w >> 8) & (i & 1 ? 0x00F000F0u : 0x000F000Fu);
-    const uint32_t up = i & 1 ? Wide<T>::high : Wide<T>::low;
-    const P v = __hfma2(*reinterpret_cast<const P*>(&bits), *reinterpret_cast<const P*>(&up), *reinterpret_cast<const P*>(&zero));
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// The token row of row r of y; -1 where src picks none.
-__device__ __forceinline__ int token_row(const Int4Product& p, int r) {
-    if (!p.src) return r;
-    const int s = ld_dep(p.src + r), from = s / p.src_div;
-    return s >= 0 && from < p.x_rows ? from : -1;
+#undef MOE_MMA
 }
 
 // Where piece `piece` (16 bytes) of a token row's 256 bytes of a chunk lies: eight
@@ -297,8 +165,7 @@ struct Warp {
 #pragma unroll
         for (int j = 0; j < groups; ++j) {
             scale[j] = to_float<T>(__builtin_bit_cast(T, static_cast<uint16_t>(s[j])));
-            const float back = static_cast<float>(z[j]) * -Wide<T>::unit;
-            zero[j] = pack2(T(), back, back);
+            zero[j] = int4_zero<T>(z[j]);
         }
     }
 
@@ -342,16 +209,16 @@ struct Warp {
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
                         uint32_t a[4];
-                        a[0] = widen<T>(q[2 * m][u], 2 * h, zero[2 * m]);
-                        a[1] = widen<T>(q[2 * m + 1][u], 2 * h, zero[2 * m + 1]);
-                        a[2] = widen<T>(q[2 * m][u], 2 * h + 1, zero[2 * m]);
-                        a[3] = widen<T>(q[2 * m + 1][u], 2 * h + 1, zero[2 * m + 1]);
+                        a[0] = int4_widen<T>(q[2 * m][u], 2 * h, zero[2 * m]);
+                        a[1] = int4_widen<T>(q[2 * m + 1][u], 2 * h, zero[2 * m + 1]);
+                        a[2] = int4_widen<T>(q[2 * m][u], 2 * h + 1, zero[2 * m]);
+                        a[3] = int4_widen<T>(q[2 * m + 1][u], 2 * h + 1, zero[2 * m + 1]);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             if (u == 0 && h == 0)
-                                Wide<T>::mma0(part[m][n], a, b[n].x, b[n].y);
+                                mma<T, true>(part[m][n], a, b[n].x, b[n].y);
                             else
-                                Wide<T>::mma(part[m][n], a, h ? b[n].z : b[n].x, h ? b[n].w : b[n].y);
+                                mma<T, false>(part[m][n], a, h ? b[n].z : b[n].x, h ? b[n].w : b[n].y);
                         }
                     }
             }
@@ -366,15 +233,17 @@ struct Warp {
 };
 
 struct Shared {
-    Lists lists;
+    Int4Lists lists;
     uint64_t full[2], empty[2];  // blocks of token rows
+    int from[2][kTile];            // an item's token rows
     uint32_t abort;
 };
 
-template <typename T, int G, int NT>
-__device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, Shared& sh, uint8_t* ring, uint8_t* s_rows,
-                                         int& blocks_so_far, bool& timed_out) {
+template <typename T, int G>
+__device__ __forceinline__ void run_item(const Int4Product& p, const Int4Item& it, Shared& sh, uint8_t* ring, uint8_t* s_rows,
+                                         int& blocks_so_far, int& turn_of, bool& timed_out) {
     using W = Warp<T, G>;
+    constexpr int NT = 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int split = p.split, part = warp & (split - 1), block = it.panel * (kWarps / split) + warp / split;
     // the warp's weight rows: 16 from a on and 16 from b on
@@ -386,9 +255,13 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, S
         const int r = i < 2 ? a0 + 8 * i : b0 + 8 * (i - 2);
         return first + (r < p.r.N ? r : live ? a0 : 0);
     };
+    const int* from = sh.from[turn_of & 1];  // of the item before the last one no one reads any more
+    if (threadIdx.x < it.rows) sh.from[turn_of & 1][threadIdx.x] = max(int4_token_row(p, it.row + threadIdx.x), 0);
+    ++turn_of;
+    __syncthreads();
     // Token rows, in blocks of `columns` elements, two in shared memory.  Columns of the
     // product past the item's rows are not stored: any row will do for them.
-    const int held = NT == 2 ? 16 : it.rows > 4 ? 8 : it.rows > 2 ? 4 : it.rows;  // rows with a place
+    const int held = it.rows > 4 ? 8 : it.rows > 2 ? 4 : it.rows;  // rows with a place
     const int super = split * W::step, supers = (p.r.K + super - 1) / super;
     const int each = min(supers, kRowBytes / (held * 2) / super), columns = each * super;
     const int n_blocks = (supers + each - 1) / each;
@@ -396,15 +269,15 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, S
         const int use = blocks_so_far + b, buf = use & 1;
         timed_out = timed_out || !warp_wait(sh.empty + buf, (use >> 1 & 1) ^ 1, &sh.abort);
         const uint32_t dst = smem_u32(s_rows) + buf * kRowBytes;
-        for (int r = 0; r < it.rows; ++r) {
-            const int from = token_row(p, it.row + r);
-            const T* x = static_cast<const T*>(p.x) + (from < 0 ? 0 : from) * p.ldx + b * columns;
-            for (int q = threadIdx.x; q < columns / 8; q += 32 * kWarps) {
-                const bool in = b * columns + q * 8 < p.r.K;
-                cp_async_16(dst + r * columns * 2 + (q >> 4) * 256 + (row_place<W::words>(r, q & 15) << 4), in ? x + q * 8 : x - b * columns,
-                            in ? 16 : 0);
-            }
-        }
+        const int piece = threadIdx.x & 15, slot = threadIdx.x >> 4, chunks = columns / kChunk;
+        auto copy = [&](int r, int c) {  // chunk c of row r
+            const int k = b * columns + c * kChunk + piece * 8;
+            const bool in = k < p.r.K;
+            cp_async_16(dst + (r * chunks + c) * 256 + (row_place<W::words>(r, piece) << 4),
+                        static_cast<const T*>(p.x) + (from[r] * p.ldx + (in ? k : 0)), in ? 16 : 0);
+        };
+        for (int c = slot; c < chunks; c += 2 * kWarps)
+            for (int r = 0; r < it.rows; ++r) copy(r, c);
         cp_async_arrive(sh.full + buf);
     };
     W w{p};
@@ -440,7 +313,7 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, S
     for (int i = 0; i < kStages - 1; ++i) load(i * W::stage_bytes);
     float sum[2][NT][4] = {};
     uint32_t stage = 0;
-    const int mine_of = (NT == 2 ? g : g & (held - 1)), odd = row_place<W::words>(mine_of, 0) << 4;
+    const int mine_of = g & (held - 1), odd = row_place<W::words>(mine_of, 0) << 4;
     for (int b = 0; b < n_blocks; ++b) {
         if (b + 1 < n_blocks) load_rows(b + 1);
         const int use = blocks_so_far + b, buf = use & 1;
@@ -468,7 +341,7 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, S
     blocks_so_far += n_blocks;
     // the codes were widened in units of their own
 #pragma unroll
-    for (int v = 0; v < 8 * NT; ++v) (&sum[0][0][0])[v] *= 1.0f / Wide<T>::unit;
+    for (int v = 0; v < 8 * NT; ++v) (&sum[0][0][0])[v] *= 1.0f / Int4Wide<T>::unit;
     __syncwarp();  // the next item's copies come after these reads
     if (split > 1) {  // the parts to the first of the warps, in order, through the ring's memory
         float* join = reinterpret_cast<float*>(ring);
@@ -496,7 +369,7 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Item& it, S
             const int token = n * 8 + 2 * t4 + j, to = it.row + token;
             if (token >= it.rows) continue;
             const float f = p.r.row_scale ? ld_dep(p.r.row_scale + to) : 1.0f;
-            const bool none = p.src && token_row(p, to) < 0;
+            const bool none = p.src && int4_token_row(p, to) < 0;
             T* y = out + to * p.r.ldo;
             if (p.swiglu) {
                 const int col = block * 16 + g;
@@ -533,16 +406,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_int4_product(const __grid_co
     }
     pdl_wait();
     const int blocks = (p.r.N + 31) / 32, per = kWarps / p.split, panels = (blocks + per - 1) / per;
-    const int total = build_lists(p.r, sh.lists, panels);
+    const int total = int4_lists<kTile, 1>(p.r, sh.lists, panels);
     uint8_t* rows = ring + kWarps * kStages * Warp<T, G>::stage_bytes;
-    int blocks_so_far = 0;  // of token rows
+    int blocks_so_far = 0, turn_of = 0;  // blocks of token rows, items
     bool timed_out = false;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
-        const Item it = item_at(sh.lists, p.r.E, panels, t);
-        if (it.rows > 8)
-            run_item<T, G, 2>(p, it, sh, ring, rows, blocks_so_far, timed_out);
-        else
-            run_item<T, G, 1>(p, it, sh, ring, rows, blocks_so_far, timed_out);
+        const Int4Item it = int4_item(sh.lists, p.r.E, panels, t);
+        run_item<T, G>(p, it, sh, ring, rows, blocks_so_far, turn_of, timed_out);
     }
     cp_async_commit();
     cp_async_wait<0>();  // nothing may still be written to shared memory at exit
@@ -552,7 +422,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_int4_product(const __grid_co
 // Warps that split a sum: more where the items are few, as far as the token rows of
 // their steps fit a block.
 int split_of(int64_t blocks_by_tiles, int64_t rows, int steps, int step) {
-    const int held = rows > 8 ? 16 : rows > 4 ? 8 : rows > 2 ? 4 : static_cast<int>(rows);  // of the longest tile
+    const int held = rows > 4 ? 8 : rows > 2 ? 4 : static_cast<int>(rows);  // of the longest tile
     int split = 1;
     while (split < kWarps && blocks_by_tiles * split < 4ll * kWarps * 2 * num_sms() && steps >= 2 * split &&
            2 * split * held * step * 2 <= kRowBytes)
@@ -562,11 +432,12 @@ int split_of(int64_t blocks_by_tiles, int64_t rows, int steps, int step) {
 
 template <typename T, int G>
 cudaError_t launch(const Int4Product& q, cudaStream_t st) {
+    using W = Warp<T, G>;
+    constexpr int kSmem = kWarps * kStages * W::stage_bytes + 2 * kRowBytes;
+    static_assert(2 * (kSmem + static_cast<int>(sizeof(Shared)) + 1024 + 64) <= 233472, "shared memory budget");
     Int4Product p = q;
     const int64_t blocks = (p.r.N + 31) / 32;
     const int64_t tiles = p.r.R / kTile + (p.r.R < p.r.E ? p.r.R : p.r.E);  // at most
-    using W = Warp<T, G>;
-    constexpr int kSmem = kWarps * kStages * W::stage_bytes + 2 * kRowBytes;
     p.split = split_of(blocks * tiles, p.r.R, (p.r.K + W::step - 1) / W::step, W::step);
     p.whole = p.groups % (p.zeros ? 4 : W::groups) == 0 && (reinterpret_cast<uintptr_t>(p.scales) & (2 * W::groups - 1)) == 0 &&
               (reinterpret_cast<uintptr_t>(p.zeros) & 3) == 0;
@@ -580,12 +451,13 @@ cudaError_t launch(const Int4Product& q, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         ready[dev] = true;
     }
-    return launch_pdl(k_int4_product<T, G>, dim3(static_cast<unsigned>(items < most ? items : most)), dim3(32 * kWarps), kSmem,
-                      st, p);
+    return launch_pdl(k_int4_product<T, G>, dim3(static_cast<unsigned>(items < most ? items : most)), dim3(32 * kWarps),
+                      kSmem, st, p);
 }
 
 template <typename T>
 cudaError_t product(int group, const Int4Product& p, cudaStream_t st) {
+    if (p.r.R > 8ll * p.r.E) return launch_int4_wide<T>(group, p, st);
     if (group == 32) return launch<T, 32>(p, st);
     return group == 64 ? launch<T, 64>(p, st) : launch<T, 128>(p, st);
 }
