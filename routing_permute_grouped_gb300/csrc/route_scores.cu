@@ -37,8 +37,8 @@ namespace {
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kMaxChoices = 8;
 constexpr int kWarps = 8;          // per block
-constexpr int kLossWarps = 16;     // per block where loads and losses are summed
-constexpr int kLossBlocks = 320;   // at most
+constexpr int kPerSm = 3;          // blocks; a warp's set-up is then shared by a dozen tokens of a large batch
+constexpr int kLossBlocks = 512;   // at most, where loads and losses are summed
 constexpr int kLossColumns = 8;    // experts per block of the second kernel
 
 struct ScoreArgs {
@@ -148,29 +148,33 @@ __device__ __forceinline__ void store_bytes(void* p, const uint32_t (&r)[(BYTES 
     }
 }
 
-// The lane's V logits of token t: -infinity for NaN, for -infinity and past E,
-// +infinity as the largest finite number.
+// The lane's V logits of token t as they lie in memory, and as they are taken:
+// -infinity for NaN, for -infinity and past E, +infinity as the largest finite number.
 template <typename T, int V>
-__device__ __forceinline__ void load_logits(const ScoreArgs& a, int64_t t, int lane, float (&l)[V], bool wide) {
-    const T* row = static_cast<const T*>(a.logits) + t * a.ld + lane * V;
-    T v[V];
-    if (wide) {
-        uint32_t r[(V * sizeof(T) + 3) / 4];
-        if (lane * V < a.E) {
-            load_bytes<V * sizeof(T)>(row, r);
-            memcpy(v, r, sizeof v);
+struct Raw {
+    uint32_t r[(V * sizeof(T) + 3) / 4];
+    __device__ __forceinline__ void load(const ScoreArgs& a, int64_t t, int lane, bool wide) {
+        const T* row = static_cast<const T*>(a.logits) + t * a.ld + lane * V;
+        if (wide) {
+            if (lane * V < a.E) load_bytes<V * sizeof(T)>(row, r);
+        } else {
+            T v[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (lane * V + i < a.E) v[i] = ld_dep(row + i);
+            memcpy(r, v, sizeof v);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (lane * V + i < a.E) v[i] = ld_dep(row + i);
     }
+    __device__ __forceinline__ void take(const ScoreArgs& a, int lane, float (&l)[V]) const {
+        T v[V];
+        memcpy(v, r, sizeof v);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float f = lane * V + i < a.E ? as_float<T>(v[i]) : -INFINITY;
-        l[i] = f > -INFINITY ? fminf(f, FLT_MAX) : -INFINITY;
+        for (int i = 0; i < V; ++i) {
+            const float f = lane * V + i < a.E ? as_float<T>(v[i]) : -INFINITY;
+            l[i] = f > -INFINITY ? fminf(f, FLT_MAX) : -INFINITY;
+        }
     }
-}
+};
 // Biases as keys take them: NaN as -infinity, +infinity as the largest number.
 __device__ __forceinline__ float tame(float b) { return b > -INFINITY ? fminf(b, FLT_MAX) : -INFINITY; }
 
@@ -220,28 +224,20 @@ __device__ __forceinline__ uint32_t kept_groups(const ScoreArgs& a, int gsz, int
         __syncwarp();
     }
     const F score = a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
-    auto u = lane < a.n_groups ? key_of(score) : 0;
-    uint32_t kept = 0;
-    F last = 0, first = 0;
-    bool both = true;
-    for (int r = 0; r <= a.topk_groups; ++r) {
-        const auto m = warp_max(u);
-        const uint32_t at = __ballot_sync(kAll, u == m);
-        const int g = __ffs(at) - 1;
-        if (r + 1 >= a.topk_groups) {  // the last kept, the first dropped
-            both = both && m > kDead;
-            const F s = __shfl_sync(kAll, score, g);
-            if (r < a.topk_groups)
-                last = s;
-            else
-                first = s;
-        }
-        if (r < a.topk_groups) {
-            kept |= 1u << g;
-            if (lane == g) u = 0;
-        }
+    const auto u = lane < a.n_groups ? key_of(score) : 0;
+    int rank = 0;  // groups before this one
+    for (int g = 0; g < a.n_groups; ++g) {
+        const auto o = __shfl_sync(kAll, u, g);
+        rank += o > u || (o == u && g < lane);
     }
-    *close = both && last - first <= tol;
+    const uint32_t kept = __ballot_sync(kAll, lane < a.n_groups && rank < a.topk_groups);
+    *close = false;
+    if (a.topk_groups < a.n_groups) {
+        const int last = __ffs(__ballot_sync(kAll, lane < a.n_groups && rank == a.topk_groups - 1)) - 1;
+        const int first = __ffs(__ballot_sync(kAll, lane < a.n_groups && rank == a.topk_groups)) - 1;
+        const F lo = __shfl_sync(kAll, score, first), hi = __shfl_sync(kAll, score, last);
+        *close = lo > -INFINITY && hi - lo <= tol;
+    }
     return kept;
 }
 
@@ -273,6 +269,65 @@ __device__ __forceinline__ void largest(int k, int lane, U (&u)[V], U& my_key, i
     }
 }
 
+// A lane's expert among a token's k + 1 largest keys, and how many come before it; no
+// expert: rank above k.
+struct Pick {
+    int rank, expert;
+    uint32_t key;
+    float logit;
+};
+
+// The same choice in parallel: the (k + 1)-th largest of the lanes' own largest keys is
+// no larger than the (k + 1)-th key of all, so that what is not below it, a dozen
+// experts as a rule, holds all that is looked for; these are dealt to the lanes and
+// count who comes before them.  False where they are more than the lanes (many ties, or
+// few lanes with experts that may be chosen).  list: 96 words of the warp's own.
+template <int V>
+__device__ __forceinline__ bool largest_in_parallel(int k, int lane, const uint32_t (&u)[V], const float (&l)[V],
+                                                    uint32_t* list, Pick& mine) {
+    uint32_t best = u[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) best = max(best, u[i]);
+    uint32_t floor_ = 1;
+    for (int n = 0; n <= k;) {
+        const uint32_t m = warp_max(best);
+        const uint32_t at = __ballot_sync(kAll, best == m);
+        if (m == 0) break;  // every expert that may be chosen is looked at
+        n += __popc(at);
+        floor_ = n > k ? m : 1u;
+        best = best == m ? 0u : best;
+    }
+    // in ascending order of the lane, and in a lane of the slot: of the expert
+    int count = 0, before = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const uint32_t at = __ballot_sync(kAll, u[i] >= floor_);
+        count += __popc(at);
+        before += __popc(at & ((1u << lane) - 1u));
+    }
+    if (count > 32) return false;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (u[i] >= floor_) {
+            list[before] = u[i];
+            list[32 + before] = __float_as_uint(l[i]);
+            list[64 + before] = lane * V + i;
+            ++before;
+        }
+    __syncwarp();
+    mine.key = lane < count ? list[lane] : 0;
+    mine.logit = __uint_as_float(lane < count ? list[32 + lane] : 0xFF800000u);  // -infinity
+    mine.expert = lane < count ? static_cast<int>(list[64 + lane]) : 0;
+    int rank = 0;
+    for (int j = 0; j < count; ++j) {
+        const uint32_t o = __shfl_sync(kAll, mine.key, j);
+        rank += o > mine.key || (o == mine.key && j < lane);
+    }
+    mine.rank = lane < count ? rank : 32;
+    __syncwarp();
+    return true;
+}
+
 // Whether two experts have equal keys in any precision.
 __device__ __forceinline__ bool same_key(const ScoreArgs& a, float l0, int e0, float l1, int e1) {
     return l0 == l1 && (!a.bias || tame(ld_dep(a.bias + e0)) == tame(ld_dep(a.bias + e1)));
@@ -283,7 +338,9 @@ template <typename T, int V>
 __device__ __noinline__ int choose_exact(const ScoreArgs& a, int64_t t, double* buf) {
     const int lane = threadIdx.x & 31;
     float l[V];
-    load_logits<T, V>(a, t, lane, l, false);
+    Raw<T, V> raw;
+    raw.load(a, t, lane, false);
+    raw.take(a, lane, l);
     double key[V], pick[V];
     float top = -INFINITY;
 #pragma unroll
@@ -325,6 +382,15 @@ __device__ __noinline__ int choose_exact(const ScoreArgs& a, int64_t t, double* 
     return expert;
 }
 
+// exp and 1 / x for what is summed or compared, not for the weights that come out:
+// off by 2 and 1 units of the last place, and exp by its rounded argument.
+__device__ __forceinline__ float exp_fast(float x) { return __expf(x); }
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // 1 / (1 + exp(-x)) = pos or neg by the sign, from e = exp(-|x|): the score and
 // one minus the score without cancellation.
 struct Sigmoid {
@@ -334,26 +400,30 @@ __device__ __forceinline__ Sigmoid sigmoid(float x) {
     const float e = expf(-fabsf(x)), d = 1.0f / (1.0f + e), ed = e * d;
     return x >= 0.0f ? Sigmoid{d, ed} : Sigmoid{ed, d};
 }
+__device__ __forceinline__ Sigmoid sigmoid_fast(float x) {
+    const float e = exp_fast(-fabsf(x)), d = rcp_fast(1.0f + e), ed = e * d;
+    return x >= 0.0f ? Sigmoid{d, ed} : Sigmoid{ed, d};
+}
 // Scores of one token over their sum: sigmoids times exp(-m), m = min(0, largest
 // logit), so that none of a token's underflow together.
 __device__ __forceinline__ float shifted_sigmoid(float x, float m) {
     if (!(x > -INFINITY)) return 0.0f;
     return x >= 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x - m) / (1.0f + expf(x));
 }
-// The part of expert j (lanes j < k; lx its logit, -infinity where it has none) in
-// the scores of the chosen.
-__device__ __forceinline__ float chosen_share(const ScoreArgs& a, int lane, float lx) {
-    const float top = warp_maxf(lane < a.k ? lx : -INFINITY);
+// The part of this lane's expert (logit lx; -infinity or not one of the chosen: none) in
+// the scores of the chosen, k lanes of the warp.
+__device__ __forceinline__ float chosen_share(const ScoreArgs& a, float lx) {
+    const float top = warp_maxf(lx);
     float v = 0.0f;
-    if (lane < a.k && lx > -INFINITY) v = a.sigmoid ? shifted_sigmoid(lx, fminf(top, 0.0f)) : expf(lx - top);
-    const float sum = sum8(v);
+    if (lx > -INFINITY) v = a.sigmoid ? shifted_sigmoid(lx, fminf(top, 0.0f)) : expf(lx - top);
+    const float sum = warp_sum(v);
     return v > 0.0f ? v / sum : 0.0f;
 }
 
 template <typename T, int V, bool LOSS>
-__global__ void __launch_bounds__(32 * (LOSS ? kLossWarps : kWarps)) k_route_scores(const __grid_constant__ ScoreArgs a) {
-    constexpr int W = LOSS ? kLossWarps : kWarps;
-    __shared__ double s_buf[W][32 * V];
+__global__ void __launch_bounds__(32 * kWarps, kPerSm) k_route_scores(const __grid_constant__ ScoreArgs a) {
+    constexpr int W = kWarps;
+    __shared__ double s_buf[W][V == 1 ? 48 : 32 * V];  // 32 V keys, or the lists of 32 candidates
     __shared__ int s_load[LOSS ? 32 * V : 1];
     pdl_trigger();
     pdl_wait();
@@ -361,10 +431,12 @@ __global__ void __launch_bounds__(32 * (LOSS ? kLossWarps : kWarps)) k_route_sco
     const int gsz = a.n_groups ? a.E / a.n_groups : a.E;
     const bool grouped = a.n_groups > 0;
     const bool by_score = a.bias || (grouped && a.group_top == 2);  // keys need scores
-    const bool all = LOSS || by_score || (!a.sigmoid && !a.renormalize);
+    const bool soft = LOSS || (!a.sigmoid && (by_score || !a.renormalize));  // the softmax is needed
+    uint32_t group_bit[V];
     float bias[V], share[LOSS ? V : 1], z = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+        group_bit[i] = 1u << ((lane * V + i) / gsz & 31);
         bias[i] = a.bias && lane * V + i < a.E ? tame(ld_dep(a.bias + lane * V + i)) : 0.0f;
         if constexpr (LOSS) share[i] = 0.0f;
     }
@@ -373,55 +445,66 @@ __global__ void __launch_bounds__(32 * (LOSS ? kLossWarps : kWarps)) k_route_sco
         if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
         __syncthreads();
     }
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * W + warp; t < a.T; t += static_cast<int64_t>(gridDim.x) * W) {
+    Raw<T, V> raw;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * W + warp, stride = static_cast<int64_t>(gridDim.x) * W;
+    if (first < a.T) raw.load(a, first, lane, a.wide);
+    for (int64_t t = first; t < a.T; t += stride) {
         float l[V];
-        load_logits<T, V>(a, t, lane, l, a.wide);
+        raw.take(a, lane, l);
+        if (t + stride < a.T) raw.load(a, t + stride, lane, a.wide);  // the next token's come meanwhile
         float s[V], top = -INFINITY, inv = 0.0f, scores_top = 1.0f;
-        if (all) {
-            if (!a.sigmoid || LOSS) {
+        if (soft) {  // softmax, and the z loss of either
 #pragma unroll
-                for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
-                top = warp_maxf(top);
+            for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
+            top = warp_maxf(top);
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                s[i] = l[i] > -INFINITY ? exp_fast(l[i] - top) : 0.0f;
+                sum += s[i];
             }
-            if (!a.sigmoid || LOSS) {  // softmax, and the z loss of either
-                float sum = 0.0f;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    s[i] = l[i] > -INFINITY ? expf(l[i] - top) : 0.0f;
-                    sum += s[i];
-                }
-                sum = warp_sum(sum);
-                inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-                if (sum > 0.0f) {
-                    const float lse = top + logf(sum);
-                    z = fmaf(lse, lse, z);
-                }
-#pragma unroll
-                for (int i = 0; i < V; ++i) s[i] *= inv;
-                scores_top = inv;
+            sum = warp_sum(sum);
+            inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+            if (LOSS && sum > 0.0f) {
+                const float lse = top + logf(sum);
+                z = fmaf(lse, lse, z);
             }
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] *= inv;
+            scores_top = inv;
             if constexpr (LOSS) {
                 if (!a.sigmoid) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) share[i] += s[i];
-                } else {
-                    const float m = fminf(top, 0.0f);
-                    float sum = 0.0f;
+                }
+            }
+        }
+        if (a.sigmoid && (LOSS || by_score)) {
+            scores_top = 1.0f;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                s[i] = sigmoid_fast(l[i]).s;
+                sum += s[i];
+            }
+            if constexpr (LOSS) {
+                if (top >= 0.0f) {
+                    const float f = 1.0f / warp_sum(sum);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) share[i] = fmaf(s[i], f, share[i]);
+                } else {  // small scores, on a common factor
+                    float r[V];
+                    sum = 0.0f;
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        s[i] = shifted_sigmoid(l[i], m);
-                        sum += s[i];
+                        r[i] = shifted_sigmoid(l[i], top);
+                        sum += r[i];
                     }
                     sum = warp_sum(sum);
                     const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) share[i] = fmaf(s[i], f, share[i]);
+                    for (int i = 0; i < V; ++i) share[i] = fmaf(r[i], f, share[i]);
                 }
-            }
-            if (a.sigmoid && by_score) {
-                scores_top = 1.0f;
-#pragma unroll
-                for (int i = 0; i < V; ++i) s[i] = sigmoid(l[i]).s;
             }
         }
         // keys: with a bias or a group's two best they are scores, else logits
@@ -432,10 +515,11 @@ __global__ void __launch_bounds__(32 * (LOSS ? kLossWarps : kWarps)) k_route_sco
             key[i] = by_score ? s[i] + bias[i] : l[i];
             if (!(l[i] > -INFINITY)) key[i] = -INFINITY;
         }
-        // twice what the fp32 keys of two experts may be off by: a score by 24
-        // roundings of the largest score (exp, the sum, the division), the sum
-        // with the bias by one of its own
-        const float off = 0x1p-18f * scores_top;
+        // What the difference of two fp32 keys may be off by.  A sigmoid: its 1 + e, the
+        // reciprocal and an e of at most 1 that is off by 5 units, a quarter of which
+        // counts; 4 units of 2^-24 in all.  A softmax: 24 of the largest score's (exp,
+        // the sum of 256, the quotient).  The sum with the bias adds half a unit of the key.
+        const float off = a.sigmoid ? 0x1p-20f : 0x1p-18f * scores_top;
         bool close = false;
         uint32_t kept = kAll;
         if (grouped) {
@@ -447,41 +531,61 @@ __global__ void __launch_bounds__(32 * (LOSS ? kLossWarps : kWarps)) k_route_sco
             }
             bool near_;
             kept = kept_groups<V, float>(a, gsz, lane, key, reinterpret_cast<float*>(s_buf[warp]),
-                                         2.0f * off + 0x1p-20f * most, &near_);
+                                         2.0f * off + 0x1p-21f * most, &near_);
             close = by_score && near_;
         }
-        uint32_t u[V], my_key;
+        uint32_t u[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int e = lane * V + i;
-            const bool may = e < a.E && (!grouped || (kept >> (e / gsz) & 1u));
+            const bool may = e < a.E && (!grouped || (kept & group_bit[i]));
             u[i] = may ? key_of(biased ? key[i] : l[i]) : 0;
         }
-        int expert;
-        largest<V, uint32_t>(a.k, lane, u, my_key, expert);
-        if (biased) {
-            const uint32_t next_key = __shfl_down_sync(kAll, my_key, 1);
-            const float f0 = number_of(my_key), f1 = number_of(next_key);
-            const bool near_ = lane < a.k && next_key > kDead && f0 - f1 <= off + 0x1p-22f * fmaxf(fabsf(f0), fabsf(f1));
-            if (__any_sync(kAll, near_)) {
-                const float lx = value_of<V>(l, expert);
-                const float ly = __shfl_down_sync(kAll, lx, 1);
-                const int ey = __shfl_down_sync(kAll, expert, 1);
-                close |= __any_sync(kAll, near_ && !same_key(a, lx, expert, ly, ey));
-            }
+        Pick mine;
+        if (!largest_in_parallel<V>(a.k, lane, u, l, reinterpret_cast<uint32_t*>(s_buf[warp]), mine)) {
+            largest<V, uint32_t>(a.k, lane, u, mine.key, mine.expert);
+            mine.rank = lane;
+            mine.logit = value_of<V>(l, mine.expert);
         }
-        if (close) expert = choose_exact<T, V>(a, t, s_buf[warp]);
-        const float lx = value_of<V>(l, expert);
+        if (biased && !close) {
+            // neighbours in the order of the keys
+            uint32_t* order = reinterpret_cast<uint32_t*>(s_buf[warp]);
+            if (lane <= a.k) order[lane] = 0;
+            __syncwarp();
+            if (mine.rank <= a.k) order[mine.rank] = mine.key;
+            __syncwarp();
+            const uint32_t next_key = mine.rank < a.k ? order[mine.rank + 1] : 0;
+            const float f0 = number_of(mine.key), f1 = number_of(next_key);
+            const bool near_ = next_key > kDead && f0 - f1 <= off + 0x1p-23f * fmaxf(fabsf(f0), fabsf(f1));
+            if (__any_sync(kAll, near_)) {
+                // experts of one logit and one bias have one key in any precision
+                uint32_t* lane_of = order + 16;
+                if (mine.rank <= a.k) lane_of[mine.rank] = lane;
+                __syncwarp();
+                const int after = near_ ? static_cast<int>(lane_of[mine.rank + 1]) : lane;
+                const float ly = __shfl_sync(kAll, mine.logit, after);
+                const int ey = __shfl_sync(kAll, mine.expert, after);
+                close = __any_sync(kAll, near_ && !same_key(a, mine.logit, mine.expert, ly, ey));
+            }
+            __syncwarp();
+        }
+        if (close) {
+            mine.expert = choose_exact<T, V>(a, t, s_buf[warp]);
+            mine.rank = lane;
+            mine.logit = value_of<V>(l, mine.expert);
+        }
+        const bool chosen = mine.rank < a.k;
+        const float lx = chosen ? mine.logit : -INFINITY;
         float w;
         if (a.renormalize) {
-            w = chosen_share(a, lane, lx);
+            w = chosen_share(a, lx);
         } else {
             w = !(lx > -INFINITY) ? 0.0f : a.sigmoid ? sigmoid(lx).s : expf(lx - top) * inv;
         }
-        if (lane < a.k) {
-            a.idx[t * a.k + lane] = expert;
-            a.w[t * a.k + lane] = w * a.scale;
-            if constexpr (LOSS) atomicAdd(&s_load[expert], 1);
+        if (chosen) {
+            a.idx[t * a.k + mine.rank] = mine.expert;
+            a.w[t * a.k + mine.rank] = w * a.scale;
+            if constexpr (LOSS) atomicAdd(&s_load[mine.expert], 1);
         }
     }
     if constexpr (LOSS) {
@@ -575,6 +679,7 @@ __global__ void __launch_bounds__(256) k_route_losses(const __grid_constant__ Sc
 //   z                dlogit_e += dz (2 / T) lse softmax_e
 template <typename T, int V, bool LOSS>
 __global__ void __launch_bounds__(32 * kWarps) k_route_scores_bwd(const __grid_constant__ ScoreArgs a) {
+    __shared__ __align__(32) float s_add[kWarps][32 * V];
     pdl_trigger();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -588,16 +693,24 @@ __global__ void __launch_bounds__(32 * kWarps) k_route_scores_bwd(const __grid_c
             c[i] = lane * V + i < a.E ? f * static_cast<float>(ld_dep(a.counts + lane * V + i)) : 0.0f;
     }
     const bool soft = LOSS || (!a.sigmoid && !a.renormalize);
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < a.T;
-         t += static_cast<int64_t>(gridDim.x) * kWarps) {
-        float l[V], g[V];
-        int expert = -1;
-        float dw = 0.0f;
+    Raw<T, V> raw;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kWarps + warp, stride = static_cast<int64_t>(gridDim.x) * kWarps;
+    int next_expert = -1;
+    float next_dw = 0.0f;
+    auto load = [&](int64_t t) {
+        raw.load(a, t, lane, a.wide);
         if (a.dw && lane < a.k) {
-            expert = ld_dep(a.idx + t * a.k + lane);
-            dw = ld_dep(a.dw + t * a.k + lane);
+            next_expert = ld_dep(a.idx + t * a.k + lane);
+            next_dw = ld_dep(a.dw + t * a.k + lane);
         }
-        load_logits<T, V>(a, t, lane, l, a.wide);
+    };
+    if (first < a.T) load(first);
+    for (int64_t t = first; t < a.T; t += stride) {
+        float l[V], g[V];
+        raw.take(a, lane, l);
+        int expert = next_expert;
+        float dw = next_dw;
+        if (t + stride < a.T) load(t + stride);  // the next token's come meanwhile
         const bool known = expert >= 0 && expert < a.E;
         expert = known ? expert : 0;
         float lx = value_of<V>(l, expert);
@@ -611,7 +724,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_route_scores_bwd(const __grid_c
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                p[i] = l[i] > -INFINITY ? expf(l[i] - top) : 0.0f;
+                p[i] = l[i] > -INFINITY ? exp_fast(l[i] - top) : 0.0f;
                 sum += p[i];
             }
             sum = warp_sum(sum);
@@ -623,7 +736,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_route_scores_bwd(const __grid_c
         // what goes to the chosen experts alone, and to all by their softmax
         float mine, all = 0.0f;
         if (a.renormalize) {
-            const float r = chosen_share(a, lane, lx);
+            const float r = chosen_share(a, lane < a.k ? lx : -INFINITY);
             const float mean = sum8(r * dw);
             mine = a.scale * r * (dw - mean);
             if (a.sigmoid) mine *= sigmoid(lx).rest;
@@ -644,11 +757,19 @@ __global__ void __launch_bounds__(32 * kWarps) k_route_scores_bwd(const __grid_c
 #pragma unroll
                 for (int i = 0; i < V; ++i) g[i] = p[i] * (c[i] - mean + all);
             } else {
-                const float m = fminf(top, 0.0f);
-                float s[V], sum = 0.0f, mean = 0.0f;
+                float s[V], rest[V], sum = 0.0f, mean = 0.0f;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    s[i] = shifted_sigmoid(l[i], m);
+                    const Sigmoid v = sigmoid_fast(l[i]);
+                    s[i] = v.s;
+                    rest[i] = v.rest;
+                }
+                if (top < 0.0f) {  // small scores, on a common factor
+#pragma unroll
+                    for (int i = 0; i < V; ++i) s[i] = shifted_sigmoid(l[i], top);
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
                     sum += s[i];
                     mean = fmaf(s[i], c[i], mean);
                 }
@@ -657,19 +778,33 @@ __global__ void __launch_bounds__(32 * kWarps) k_route_scores_bwd(const __grid_c
                 const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
                 mean *= f;
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    g[i] = fmaf(s[i] * f * sigmoid(l[i]).rest, c[i] - mean, p[i] * all);
+                for (int i = 0; i < V; ++i) g[i] = fmaf(s[i] * f * rest[i], c[i] - mean, p[i] * all);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i) g[i] = soft ? p[i] * all : 0.0f;
         }
-        for (int j = 0; j < a.k; ++j) {
-            const int e = __shfl_sync(kAll, expert, j);
-            const float v = __shfl_sync(kAll, mine, j);
+        if (a.dw) {
+            const bool adds = known && mine != 0.0f;
+            const uint32_t same = __match_any_sync(kAll, adds ? expert : -1 - lane);
+            if (__any_sync(kAll, (same & (same - 1)) != 0)) {  // an expert that repeats: one after the other
+                for (int j = 0; j < a.k; ++j) {
+                    const int e = __shfl_sync(kAll, expert, j);
+                    const float v = __shfl_sync(kAll, adds ? mine : 0.0f, j);
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (e == lane * V + i) g[i] += v;
+                    for (int i = 0; i < V; ++i)
+                        if (e == lane * V + i) g[i] += v;
+                }
+            } else {
+                float* buf = s_add[warp];
+#pragma unroll
+                for (int i = 0; i < V; ++i) buf[lane * V + i] = 0.0f;
+                __syncwarp();
+                if (adds) buf[expert] = mine;
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < V; ++i) g[i] += buf[lane * V + i];
+            }
         }
         T* row = static_cast<T*>(a.dlogits) + t * a.ldd + lane * V;
         T o[V];
@@ -763,15 +898,15 @@ ScoreArgs args_of(const moe_score_rule_t* r, int64_t T) {
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
-// Blocks of the first kernel where loads and losses are summed: two per SM, and at
+// Blocks of the first kernel where loads and losses are summed: kPerSm per SM, and at
 // most as many as the workspace, whose size no GPU decides, holds sums of
 int most_blocks(int64_t T) {
-    const int64_t need = (T + kLossWarps - 1) / kLossWarps;
+    const int64_t need = (T + kWarps - 1) / kWarps;
     return static_cast<int>(need < kLossBlocks ? need : kLossBlocks);
 }
 int loss_blocks(int64_t T) {
     const int most = most_blocks(T);
-    return 2 * num_sms() < most ? 2 * num_sms() : most;
+    return kPerSm * num_sms() < most ? kPerSm * num_sms() : most;
 }
 
 template <typename F>
@@ -843,8 +978,8 @@ extern "C" moe_status_t moe_route_scores(const moe_score_rule_t* rule, int32_t d
         using E_ = decltype(t);
         constexpr int V = decltype(v)::value;
         if (counts)
-            return launch_pdl(k_route_scores<E_, V, true>, dim3(a.blocks), dim3(32 * kLossWarps), 0, st, a);
-        const int64_t need = (T + kWarps - 1) / kWarps, most = 16ll * num_sms();
+            return launch_pdl(k_route_scores<E_, V, true>, dim3(a.blocks), dim3(32 * kWarps), 0, st, a);
+        const int64_t need = (T + kWarps - 1) / kWarps, most = static_cast<int64_t>(kPerSm) * num_sms();
         return launch_pdl(k_route_scores<E_, V, false>, dim3(static_cast<unsigned>(need < most ? need : most)),
                           dim3(32 * kWarps), 0, st, a);
     });
@@ -876,7 +1011,7 @@ extern "C" moe_status_t moe_route_scores_bwd(const moe_score_rule_t* rule, int32
     a.ldd = ldd;
     a.wide_out = wide_rows(dlogits, ldd, dtype, rule->E);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t need = (T + kWarps - 1) / kWarps, most = 16ll * num_sms();
+    const int64_t need = (T + kWarps - 1) / kWarps, most = 5ll * num_sms();
     const dim3 grid(static_cast<unsigned>(need < most ? need : most));
     const cudaError_t e = by_type(dtype, rule->E, [&](auto t, auto v) {
         using E_ = decltype(t);
