@@ -70,16 +70,17 @@ struct ScoreArgs {
 
 
 // ------------------------------------------------------------------- keys --
-// Unsigned integers in the order of the keys: 0 for what may not be chosen, 1
-// for -infinity (chosen only when nothing else is left), then the numbers.
-constexpr uint32_t kDead = 1;
+// Unsigned integers in the order of the keys, which are numbers or -infinity; 0 for
+// what may not be chosen.  -infinity, chosen only when nothing else is left, comes
+// just below the numbers.
+constexpr uint32_t kDead = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t key_of(float f) {
-    const uint32_t b = __float_as_uint(f + 0.0f);  // -0 and 0 are one key
-    return f > -INFINITY ? (b >> 31 ? ~b : b | 0x80000000u) : kDead;
+    const int b = __float_as_int(f + 0.0f);  // -0 and 0 are one key
+    return static_cast<uint32_t>(b ^ (b >> 31 | static_cast<int>(0x80000000u)));
 }
 __device__ __forceinline__ uint64_t key_of(double f) {
-    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(f + 0.0));
-    return f > -INFINITY ? (b >> 63 ? ~b : b | 0x8000000000000000ull) : kDead;
+    const long long b = __double_as_longlong(f + 0.0);
+    return static_cast<uint64_t>(b ^ (b >> 63 | static_cast<long long>(0x8000000000000000ull)));
 }
 __device__ __forceinline__ float number_of(uint32_t u) {
     return __uint_as_float(u >> 31 ? u ^ 0x80000000u : ~u);
@@ -91,8 +92,7 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
     return static_cast<uint64_t>(hi) << 32 | lo;
 }
 __device__ __forceinline__ float warp_maxf(float v) {  // -infinity for a warp without numbers
-    const uint32_t u = warp_max(key_of(v));
-    return u == kDead ? -INFINITY : number_of(u);
+    return number_of(warp_max(key_of(v)));
 }
 template <typename F>
 __device__ __forceinline__ F warp_sum(F v) {
@@ -226,10 +226,8 @@ __device__ __forceinline__ uint32_t kept_groups(const ScoreArgs& a, int gsz, int
     const F score = a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
     const auto u = lane < a.n_groups ? key_of(score) : 0;
     int rank = 0;  // groups before this one
-    for (int g = 0; g < a.n_groups; ++g) {
-        const auto o = __shfl_sync(kAll, u, g);
-        rank += o > u || (o == u && g < lane);
-    }
+#pragma unroll 4
+    for (int g = 0; g < a.n_groups; ++g) rank += __shfl_sync(kAll, u, g) + (g < lane) > u;  // ties to the lower group
     const uint32_t kept = __ballot_sync(kAll, lane < a.n_groups && rank < a.topk_groups);
     *close = false;
     if (a.topk_groups < a.n_groups) {
@@ -269,6 +267,34 @@ __device__ __forceinline__ void largest(int k, int lane, U (&u)[V], U& my_key, i
     }
 }
 
+// V words of a lane in shared memory, aligned to them all
+template <int V>
+__device__ __forceinline__ void put_words(uint32_t* p, const uint32_t (&v)[V]) {
+    if constexpr (V == 1) {
+        p[0] = v[0];
+    } else if constexpr (V == 2) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(v[0], v[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) *reinterpret_cast<uint4*>(p + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void get_words(const uint32_t* p, uint32_t (&v)[V]) {
+    if constexpr (V == 1) {
+        v[0] = p[0];
+    } else if constexpr (V == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        v[0] = u.x, v[1] = u.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const uint4 u = *reinterpret_cast<const uint4*>(p + i);
+            v[i] = u.x, v[i + 1] = u.y, v[i + 2] = u.z, v[i + 3] = u.w;
+        }
+    }
+}
+
 // A lane's expert among a token's k + 1 largest keys, and how many come before it; no
 // expert: rank above k.
 struct Pick {
@@ -281,24 +307,28 @@ struct Pick {
 // no larger than the (k + 1)-th key of all, so that what is not below it, a dozen
 // experts as a rule, holds all that is looked for; these are dealt to the lanes and
 // count who comes before them.  False where they are more than the lanes (many ties, or
-// few lanes with experts that may be chosen).  list: 96 words of the warp's own.
+// few lanes with experts that may be chosen).  buf: the warp's 32 V logits, 32 V keys
+// and 32 experts.
 template <int V>
 __device__ __forceinline__ bool largest_in_parallel(int k, int lane, const uint32_t (&u)[V], const float (&l)[V],
-                                                    uint32_t* list, Pick& mine) {
+                                                    uint32_t* buf, Pick& mine) {
     uint32_t best = u[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) best = max(best, u[i]);
     uint32_t floor_ = 1;
     for (int n = 0; n <= k;) {
         const uint32_t m = warp_max(best);
-        const uint32_t at = __ballot_sync(kAll, best == m);
-        if (m == 0) break;  // every expert that may be chosen is looked at
-        n += __popc(at);
-        floor_ = n > k ? m : 1u;
+        if (m == 0) {  // every expert that may be chosen is looked at
+            floor_ = 1;
+            break;
+        }
+        floor_ = m;
+        n += __popc(__ballot_sync(kAll, best == m));
         best = best == m ? 0u : best;
     }
     // in ascending order of the lane, and in a lane of the slot: of the expert
     int count = 0, before = 0;
+    uint8_t* list = reinterpret_cast<uint8_t*>(buf + 64 * V);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const uint32_t at = __ballot_sync(kAll, u[i] >= floor_);
@@ -306,23 +336,21 @@ __device__ __forceinline__ bool largest_in_parallel(int k, int lane, const uint3
         before += __popc(at & ((1u << lane) - 1u));
     }
     if (count > 32) return false;
+    uint32_t bits[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (u[i] >= floor_) {
-            list[before] = u[i];
-            list[32 + before] = __float_as_uint(l[i]);
-            list[64 + before] = lane * V + i;
-            ++before;
-        }
-    __syncwarp();
-    mine.key = lane < count ? list[lane] : 0;
-    mine.logit = __uint_as_float(lane < count ? list[32 + lane] : 0xFF800000u);  // -infinity
-    mine.expert = lane < count ? static_cast<int>(list[64 + lane]) : 0;
-    int rank = 0;
-    for (int j = 0; j < count; ++j) {
-        const uint32_t o = __shfl_sync(kAll, mine.key, j);
-        rank += o > mine.key || (o == mine.key && j < lane);
+    for (int i = 0; i < V; ++i) {
+        bits[i] = __float_as_uint(l[i]);
+        if (u[i] >= floor_) list[before++] = static_cast<uint8_t>(lane * V + i);
     }
+    put_words<V>(buf + lane * V, bits);
+    put_words<V>(buf + 32 * V + lane * V, u);
+    __syncwarp();
+    mine.expert = lane < count ? list[lane] : 0;
+    mine.key = lane < count ? buf[32 * V + mine.expert] : 0u;
+    mine.logit = __uint_as_float(buf[mine.expert]);
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < count; ++j) rank += __shfl_sync(kAll, mine.key, j) + (j < lane) > mine.key;  // ties to the lower expert
     mine.rank = lane < count ? rank : 32;
     __syncwarp();
     return true;
@@ -415,15 +443,26 @@ __device__ __forceinline__ float shifted_sigmoid(float x, float m) {
 __device__ __forceinline__ float chosen_share(const ScoreArgs& a, float lx) {
     const float top = warp_maxf(lx);
     float v = 0.0f;
-    if (lx > -INFINITY) v = a.sigmoid ? shifted_sigmoid(lx, fminf(top, 0.0f)) : expf(lx - top);
+    if (a.sigmoid) {
+        if (top >= 0.0f) {
+            const float e = expf(-fabsf(lx)), d = rcp_fast(1.0f + e);
+            v = lx >= 0.0f ? d : e * d;  // exp(-infinity) = 0
+        } else {
+            v = shifted_sigmoid(lx, top);
+        }
+    } else if (lx > -INFINITY) {
+        v = expf(lx - top);
+    }
     const float sum = warp_sum(v);
-    return v > 0.0f ? v / sum : 0.0f;
+    return sum > 0.0f ? v * rcp_fast(sum) : 0.0f;
 }
 
 template <typename T, int V, bool LOSS>
 __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_route_scores(const __grid_constant__ ScoreArgs a) {
     constexpr int W = kWarps;
-    __shared__ double s_buf[W][V == 1 ? 48 : 32 * V];  // 32 V keys, or the lists of 32 candidates
+    __shared__ __align__(32) double s_buf[W][32 * V + 16];  // 32 V keys of fp64, or logits, keys and 32 candidates
+    __shared__ __align__(32) float s_bias[32 * V];
+    __shared__ __align__(32) uint32_t s_group[32 * V];  // the bit of an expert's group
     __shared__ int s_load[LOSS ? 32 * V : 1];
     pdl_trigger();
     pdl_wait();
@@ -432,19 +471,25 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_route_scores(const __gr
     const bool grouped = a.n_groups > 0;
     const bool by_score = a.bias || (grouped && a.group_top == 2);  // keys need scores
     const bool soft = LOSS || (!a.sigmoid && (by_score || !a.renormalize));  // the softmax is needed
-    uint32_t group_bit[V];
-    float bias[V], share[LOSS ? V : 1], z = 0.0f;
+    float share[LOSS ? V : 1], z = 0.0f;
+    for (int e = threadIdx.x; e < 32 * V; e += 32 * W) {
+        s_bias[e] = a.bias && e < a.E ? tame(ld_dep(a.bias + e)) : 0.0f;
+        const int group = e / gsz;
+        s_group[e] = !grouped || group < a.n_groups ? 1u << (group & 31) : 0u;
+    }
+    if constexpr (LOSS) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        group_bit[i] = 1u << ((lane * V + i) / gsz & 31);
-        bias[i] = a.bias && lane * V + i < a.E ? tame(ld_dep(a.bias + lane * V + i)) : 0.0f;
-        if constexpr (LOSS) share[i] = 0.0f;
+        for (int i = 0; i < V; ++i) share[i] = 0.0f;
     }
     if constexpr (LOSS) {
         for (int e = threadIdx.x; e < 32 * V; e += 32 * W) s_load[e] = 0;
         if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
-        __syncthreads();
     }
+    __syncthreads();
+    float most = 0.0f;  // of a key's magnitude
+#pragma unroll
+    for (int i = 0; i < V; ++i) most = fmaxf(most, s_bias[lane * V + i] > -INFINITY ? fabsf(s_bias[lane * V + i]) : 0.0f);
+    most = 1.0f + warp_maxf(most);
     Raw<T, V> raw;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * W + warp, stride = static_cast<int64_t>(gridDim.x) * W;
     if (first < a.T) raw.load(a, first, lane, a.wide);
@@ -510,11 +555,10 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_route_scores(const __gr
         // keys: with a bias or a group's two best they are scores, else logits
         float key[V];
         const bool biased = a.bias != nullptr;
+        uint32_t words[V];
+        get_words<V>(reinterpret_cast<const uint32_t*>(s_bias) + lane * V, words);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            key[i] = by_score ? s[i] + bias[i] : l[i];
-            if (!(l[i] > -INFINITY)) key[i] = -INFINITY;
-        }
+        for (int i = 0; i < V; ++i) key[i] = by_score && l[i] > -INFINITY ? s[i] + __uint_as_float(words[i]) : l[i];
         // What the difference of two fp32 keys may be off by.  A sigmoid: its 1 + e, the
         // reciprocal and an e of at most 1 that is off by 5 units, a quarter of which
         // counts; 4 units of 2^-24 in all.  A softmax: 24 of the largest score's (exp,
@@ -523,24 +567,16 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_route_scores(const __gr
         bool close = false;
         uint32_t kept = kAll;
         if (grouped) {
-            float most = 0.0f;
-            if (by_score) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) most = fmaxf(most, key[i] > -INFINITY ? fabsf(key[i]) : 0.0f);
-                most = warp_maxf(most);
-            }
             bool near_;
             kept = kept_groups<V, float>(a, gsz, lane, key, reinterpret_cast<float*>(s_buf[warp]),
                                          2.0f * off + 0x1p-21f * most, &near_);
             close = by_score && near_;
         }
+        // slots past the last expert have -infinity and come after all experts that do
         uint32_t u[V];
+        get_words<V>(s_group + lane * V, words);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane * V + i;
-            const bool may = e < a.E && (!grouped || (kept & group_bit[i]));
-            u[i] = may ? key_of(biased ? key[i] : l[i]) : 0;
-        }
+        for (int i = 0; i < V; ++i) u[i] = kept & words[i] ? key_of(biased ? key[i] : l[i]) : 0u;
         Pick mine;
         if (!largest_in_parallel<V>(a.k, lane, u, l, reinterpret_cast<uint32_t*>(s_buf[warp]), mine)) {
             largest<V, uint32_t>(a.k, lane, u, mine.key, mine.expert);
