@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(256) k_route_losses(const __grid_constant__ Sc
 //                    c_e = dbalance E count_e / (k T^2), p the scores over their sum
 //   z                dlogit_e += dz (2 / T) lse softmax_e
 template <typename T, int V, bool LOSS>
-__global__ void __launch_bounds__(32 * kWarps) k_route_scores_bwd(const __grid_constant__ ScoreArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, kPerSm) k_route_scores_bwd(const __grid_constant__ ScoreArgs a) {
     __shared__ __align__(32) float s_add[kWarps][32 * V];
     pdl_trigger();
     pdl_wait();
