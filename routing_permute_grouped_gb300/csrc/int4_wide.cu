@@ -119,14 +119,15 @@ __device__ __forceinline__ int64_t weight_row(const Int4Product& p, int e, const
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, M = 128, K = 16, where `one` is set.
-__device__ __forceinline__ void mma_tmem_if(uint32_t one, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+__device__ __forceinline__ void mma_tmem_if(uint32_t one, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                            bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "setp.ne.b32 q, %4, 0;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t}" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, q;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(one)
         : "memory");
 }
 __device__ __forceinline__ void commit_if(uint32_t one, uint64_t* bar) {
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bars.code_empty + i, 4);  // the warps that widen the chunk
         }
         for (int i = 0; i < kRowStages; ++i) {
-            mbar_init(bars.row_full + i, 2);  // both loading warps
+            mbar_init(bars.row_full + i, 64);  // every lane of both loading warps
             mbar_init(bars.row_empty + i, 1);
         }
         for (int i = 0; i < C::a_bufs; ++i) {
@@ -351,67 +352,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             Feed feed;
             const int half = warp >> 1, sub = lane >> 3, piece = lane & 7;
             const uint32_t even = sub * 128 + ((piece ^ sub) << 4), odd = (sub + 4) * 128 + ((piece ^ (sub + 4)) << 4);
-            const uint8_t* base = static_cast<const uint8_t*>(p.x);
             const uint32_t dst0 = smem_u32(s_rows) + half * 1024;
-            int n_stages = 0, s = 0, oldest = 0, under_way = 0;
+            int n_stages = 0, s = 0;
             uint32_t used = 0;  // parity of each stage's uses
-            auto landed = [&]() {  // the oldest stage's copies, seen to be complete
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars.row_full + oldest);
-                if (++oldest == n_stages) oldest = 0;
-                --under_way;
-            };
             for (int t = first; t < total && !timed_out; t += stride) {
                 const Int4Item it = feed.next(lists, p.r.E, panels, total, t, stride, lane);
                 const int wide = (it.rows + 15) & ~15;
                 if (row_stages(wide) != n_stages) {
-                    cp_async_wait<0>();
-                    while (under_way > 0) landed();
                     for (int i = 0; i < n_stages && !timed_out; ++i)
                         timed_out = !role_wait(bars.row_empty + i, (used >> i & 1u) ^ 1u, abort_flag);
                     n_stages = row_stages(wide);
-                    s = oldest = 0;
+                    s = 0;
                 }
-                int from[TN / 4];
+                // rows that are not stored, or stored as zeros, may be any
+                const uint8_t* from[TN / 4];
 #pragma unroll
-                for (int i = 0; i < TN / 4; ++i)
-                    from[i] = 4 * i + sub < it.rows ? int4_token_row(p, it.row + 4 * i + sub) : -1;
+                for (int i = 0; i < TN / 4; ++i) {
+                    const int row = 4 * i + sub < it.rows ? int4_token_row(p, it.row + 4 * i + sub) : 0;
+                    from[i] = static_cast<const uint8_t*>(p.x) +
+                              (max(row, 0) * p.ldx + c0 * C::chunk + half * 64 + piece * 8) * static_cast<int64_t>(2);
+                }
                 for (int k0 = c0 * C::chunk; k0 < c1 * C::chunk && !timed_out; k0 += 128) {
                     if (!role_wait(bars.row_empty + s, (used >> s & 1u) ^ 1u, abort_flag)) {
                         timed_out = true;
                         break;
                     }
-                    const int k = k0 + half * 64 + piece * 8;
-                    const uint32_t dst = dst0 + s * wide * 256;
+                    const uint32_t dst_even = dst0 + s * wide * 256 + even, dst_odd = dst0 + s * wide * 256 + odd;
+                    if (k0 + 128 <= p.r.K) {
 #pragma unroll
-                    for (int i = 0; i < TN / 4; ++i) {
-                        if (4 * i >= wide) break;
-                        const bool in = from[i] >= 0 && k < p.r.K;
-                        cp_async_16(dst + (i >> 1) * 2048 + (i & 1 ? odd : even),
-                                    in ? base + (from[i] * p.ldx + k) * 2 : base, in ? 16 : 0);
+                        for (int i = 0; i < TN / 4; ++i) {
+                            if (4 * i >= wide) break;
+                            cp_async_16((i & 1 ? dst_odd : dst_even) + (i >> 1) * 2048, from[i], 16);
+                            from[i] += 256;
+                        }
+                    } else {
+                        const bool in = k0 + half * 64 + piece * 8 < p.r.K;
+#pragma unroll
+                        for (int i = 0; i < TN / 4; ++i) {
+                            if (4 * i >= wide) break;
+                            cp_async_16((i & 1 ? dst_odd : dst_even) + (i >> 1) * 2048, in ? from[i] : static_cast<const uint8_t*>(p.x),
+                                        in ? 16 : 0);
+                            from[i] += 256;
+                        }
                     }
-                    cp_async_commit();
+                    // not a wait for the copies and a proxy fence here: the fence waits for all
+                    // that the warp has under way (127 us for 32 rows in each of 32 groups)
+                    cp_async_arrive(bars.row_full + s);
                     used ^= 1u << s;
                     if (++s == n_stages) s = 0;
-                    // two to five stages are handed over ahead of their use, the others under way
-                    if (n_stages == 5 && ++under_way > 3) {
-                        cp_async_wait<3>();
-                        landed();
-                    } else if (n_stages == 6 && ++under_way > 4) {
-                        cp_async_wait<4>();
-                        landed();
-                    } else if (n_stages == 10 && ++under_way > 7) {
-                        cp_async_wait<7>();
-                        landed();
-                    } else if (n_stages == 16 && ++under_way > 11) {
-                        cp_async_wait<11>();
-                        landed();
-                    }
                 }
             }
+            // nothing of this CTA's shared memory may still be written to at exit
+            cp_async_commit();
             cp_async_wait<0>();
-            while (under_way > 0) landed();
         } else if (warp == 2) {
             // ------------------------------------------------------------- MMAs
             Feed feed;
@@ -444,12 +437,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             timed_out = true;
                             break;
                         }
+                        fence_proxy_async_smem();  // the rows came through the generic proxy
                         tc_fence_after();
-                        const uint64_t b = b0 + static_cast<uint32_t>(s * wide * 16);
+                        const uint32_t b = static_cast<uint32_t>(b0) + static_cast<uint32_t>(s * wide * 16);
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             mma_tmem_if(one, dcol + ((u * 128 + k * 16) / G) * TN, acol + (u * 8 + k) * 8,
-                                        b + (k >> 2) * 64 + (k & 3) * 2, idesc, k % (G / 16) != 0);
+                                        b + (k >> 2) * 64 + (k & 3) * 2, static_cast<uint32_t>(b0 >> 32), idesc,
+                                        k % (G / 16) != 0);
                         commit_if(one, bars.row_empty + s);
                         issued = true;
                         used ^= 1u << s;
