@@ -492,6 +492,8 @@ extern "C" moe_status_t moe_grouped_gemm_int4(int32_t group, int32_t dtype, int6
         return set_last_error(MOE_ERR_INVALID_ARG, "x, w_codes and y must be 16-byte aligned, w_scales 2-byte");
     if (ldx < K || ldx % 8 || ldy < N || ldy % 8)
         return set_last_error(MOE_ERR_INVALID_ARG, "row strides must cover the row and be multiples of 8 elements");
+    if (ldx > kRaggedMaxDim || ldy > kRaggedMaxDim)
+        return set_last_error(MOE_ERR_UNSUPPORTED, "a row stride is more than 2^30");
     if (src ? (src_div <= 0 || x_rows <= 0) : x_rows < R)
         return set_last_error(MOE_ERR_INVALID_ARG, "x has too few rows, or src_div <= 0");
     Int4Product p{};

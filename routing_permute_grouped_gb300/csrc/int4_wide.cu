@@ -42,7 +42,7 @@ constexpr int kRowBytes = 80 * 1024;   // of the token rows in flight
 constexpr int kRowStages = 16;         // of 128 elements each, at most
 constexpr int kThreads = 640;
 // Registers per thread of the roles; together no more than the launch's 96 each
-constexpr int kIssueRegs = 56, kSumRegs = 120, kWidenRegs = 88;
+constexpr int kIssueRegs = 80, kSumRegs = 120, kWidenRegs = 80;
 static_assert(kIssueRegs + 2 * kSumRegs + 2 * kWidenRegs <= 5 * 96, "register split");
 constexpr int kMaxSplit = 8;           // CTAs of a cluster
 
@@ -352,9 +352,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             Feed feed;
             const int half = warp >> 1, sub = lane >> 3, piece = lane & 7;
             const uint32_t even = sub * 128 + ((piece ^ sub) << 4), odd = (sub + 4) * 128 + ((piece ^ (sub + 4)) << 4);
-            const uint32_t dst0 = smem_u32(s_rows) + half * 1024;
+            const uint32_t dst0 = smem_u32(s_rows) + half * 1024, pitch = static_cast<uint32_t>(p.ldx * 2);
             int n_stages = 0, s = 0;
             uint32_t used = 0;  // parity of each stage's uses
+            auto load = [&](const Int4Item& it, auto quads) {
+                constexpr int kQuads = decltype(quads)::value, wide = 4 * kQuads;
+                // rows that are not stored, or stored as zeros, may be any; their numbers are
+                // held and not their addresses, which would not fit beside one another
+                uint32_t from[kQuads];
+#pragma unroll
+                for (int i = 0; i < kQuads; ++i)
+                    from[i] = 4 * i + sub < it.rows ? max(int4_token_row(p, it.row + 4 * i + sub), 0) : 0;
+                const uint8_t* at = static_cast<const uint8_t*>(p.x) + (c0 * C::chunk + half * 64 + piece * 8) * static_cast<int64_t>(2);
+                for (int c = c0; c < c1; ++c) {
+#pragma unroll
+                    for (int u = 0; u < C::chunk / 128; ++u) {
+                        if (!role_wait(bars.row_empty + s, (used >> s & 1u) ^ 1u, abort_flag)) {
+                            timed_out = true;
+                            return;
+                        }
+                        const uint32_t to_even = dst0 + s * wide * 256 + even, to_odd = dst0 + s * wide * 256 + odd;
+                        const int k0 = c * C::chunk + u * 128;
+                        if (k0 + 128 <= p.r.K) {
+#pragma unroll
+                            for (int i = 0; i < kQuads; ++i)
+                                cp_async_16((i & 1 ? to_odd : to_even) + (i >> 1) * 2048, at + static_cast<uint64_t>(from[i]) * pitch + u * 256, 16);
+                        } else {
+                            const bool in = k0 + half * 64 + piece * 8 < p.r.K;
+#pragma unroll
+                            for (int i = 0; i < kQuads; ++i)
+                                cp_async_16((i & 1 ? to_odd : to_even) + (i >> 1) * 2048,
+                                            in ? at + static_cast<uint64_t>(from[i]) * pitch + u * 256 : static_cast<const uint8_t*>(p.x), in ? 16 : 0);
+                        }
+                        // not a wait for the copies and a proxy fence here: the fence waits for all
+                        // that the warp has under way (127 us for 32 rows in each of 32 groups)
+                        cp_async_arrive(bars.row_full + s);
+                        used ^= 1u << s;
+                        if (++s == row_stages(wide)) s = 0;
+                    }
+                    at += C::chunk * 2;
+                }
+            };
             for (int t = first; t < total && !timed_out; t += stride) {
                 const Int4Item it = feed.next(lists, p.r.E, panels, total, t, stride, lane);
                 const int wide = (it.rows + 15) & ~15;
@@ -363,43 +401,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         timed_out = !role_wait(bars.row_empty + i, (used >> i & 1u) ^ 1u, abort_flag);
                     n_stages = row_stages(wide);
                     s = 0;
+                    if (timed_out) break;
                 }
-                // rows that are not stored, or stored as zeros, may be any
-                const uint8_t* from[TN / 4];
-#pragma unroll
-                for (int i = 0; i < TN / 4; ++i) {
-                    const int row = 4 * i + sub < it.rows ? int4_token_row(p, it.row + 4 * i + sub) : 0;
-                    from[i] = static_cast<const uint8_t*>(p.x) +
-                              (max(row, 0) * p.ldx + c0 * C::chunk + half * 64 + piece * 8) * static_cast<int64_t>(2);
-                }
-                for (int k0 = c0 * C::chunk; k0 < c1 * C::chunk && !timed_out; k0 += 128) {
-                    if (!role_wait(bars.row_empty + s, (used >> s & 1u) ^ 1u, abort_flag)) {
-                        timed_out = true;
-                        break;
-                    }
-                    const uint32_t dst_even = dst0 + s * wide * 256 + even, dst_odd = dst0 + s * wide * 256 + odd;
-                    if (k0 + 128 <= p.r.K) {
-#pragma unroll
-                        for (int i = 0; i < TN / 4; ++i) {
-                            if (4 * i >= wide) break;
-                            cp_async_16((i & 1 ? dst_odd : dst_even) + (i >> 1) * 2048, from[i], 16);
-                            from[i] += 256;
-                        }
-                    } else {
-                        const bool in = k0 + half * 64 + piece * 8 < p.r.K;
-#pragma unroll
-                        for (int i = 0; i < TN / 4; ++i) {
-                            if (4 * i >= wide) break;
-                            cp_async_16((i & 1 ? dst_odd : dst_even) + (i >> 1) * 2048, in ? from[i] : static_cast<const uint8_t*>(p.x),
-                                        in ? 16 : 0);
-                            from[i] += 256;
-                        }
-                    }
-                    // not a wait for the copies and a proxy fence here: the fence waits for all
-                    // that the warp has under way (127 us for 32 rows in each of 32 groups)
-                    cp_async_arrive(bars.row_full + s);
-                    used ^= 1u << s;
-                    if (++s == n_stages) s = 0;
+                if (wide == 16) load(it, std::integral_constant<int, 4>());
+                else if (wide == 32) load(it, std::integral_constant<int, 8>());
+                else if constexpr (TN == 64) {
+                    if (wide == 48) load(it, std::integral_constant<int, 12>());
+                    else load(it, std::integral_constant<int, 16>());
                 }
             }
             // nothing of this CTA's shared memory may still be written to at exit
