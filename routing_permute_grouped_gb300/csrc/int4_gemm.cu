@@ -419,15 +419,20 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_int4_product(const __grid_co
     if (timed_out && p.r.status) atomicOr(p.r.status, kRaggedTimeout);
 }
 
-// Warps that split a sum: more where the items are few, as far as the token rows of
-// their steps fit a block.
-int split_of(int64_t blocks_by_tiles, int64_t rows, int steps, int step) {
+// Warps that split a sum, as far as the token rows of their steps fit a block: the
+// number that makes the fewest steps of the CTAs that run one after another, an item's
+// start and end counted as kItemSteps.
+constexpr int kItemSteps = 4;
+int split_of(int64_t blocks, int64_t tiles, int64_t rows, int steps, int step) {
     const int held = rows > 4 ? 8 : rows > 2 ? 4 : static_cast<int>(rows);  // of the longest tile
-    int split = 1;
-    while (split < kWarps && blocks_by_tiles * split < 4ll * kWarps * 2 * num_sms() && steps >= 2 * split &&
-           2 * split * held * step * 2 <= kRowBytes)
-        split *= 2;
-    return split;
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int split = 1; split <= kWarps && (split == 1 || split * held * step * 2 <= kRowBytes); split *= 2) {
+        const int64_t items = (blocks * split + kWarps - 1) / kWarps * tiles, ctas = 2 * num_sms();
+        const int64_t cost = (items + ctas - 1) / ctas * ((steps + split - 1) / split + kItemSteps);
+        if (cost < least) least = cost, best = split;
+    }
+    return best;
 }
 
 template <typename T, int G>
@@ -438,7 +443,7 @@ cudaError_t launch(const Int4Product& q, cudaStream_t st) {
     Int4Product p = q;
     const int64_t blocks = (p.r.N + 31) / 32;
     const int64_t tiles = p.r.R / kTile + (p.r.R < p.r.E ? p.r.R : p.r.E);  // at most
-    p.split = split_of(blocks * tiles, p.r.R, (p.r.K + W::step - 1) / W::step, W::step);
+    p.split = split_of(blocks, tiles, p.r.R, (p.r.K + W::step - 1) / W::step, W::step);
     p.whole = p.groups % (p.zeros ? 4 : W::groups) == 0 && (reinterpret_cast<uintptr_t>(p.scales) & (2 * W::groups - 1)) == 0 &&
               (reinterpret_cast<uintptr_t>(p.zeros) & 3) == 0;
     const int64_t per = kWarps / p.split, items = (blocks + per - 1) / per * tiles, most = 2 * num_sms();
