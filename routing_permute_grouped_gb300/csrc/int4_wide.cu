@@ -686,10 +686,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// CTAs that split a sum.  More items than SMs need no split.
+// CTAs that split a sum: as many as leave all items, of groups of equal lengths, to run
+// at once; an item costs its start and its joining whatever is left of its sum.  By split
+// 1, 2, 4 and 8, with groups of 128 elements: 64 rows with 4096 x 4096 weights (32 items)
+// 35, 33, 29 and 37 us, with 1024 x 16384 (8 items) 74, 53, 39 and 31, 16 rows in each of
+// 8 groups of 7168 x 2048 (448 items) 35, 47, 68 and 131.
 int split_of(int64_t items, int chunks) {
     int split = 1;
-    while (split < kMaxSplit && items * split < 2 * num_sms() && chunks >= 4 * split) split *= 2;
+    while (split < kMaxSplit && items * split * 2 <= num_sms() && chunks >= 4 * split) split *= 2;
     return split;
 }
 
@@ -710,7 +714,8 @@ cudaError_t launch(const Int4Product& q, cudaStream_t st) {
     if (!make_tensor_map(&tW, p.codes, 3, wd, ws, wb, CU_TENSOR_MAP_DATA_TYPE_UINT8, C::chunk / 2)) return cudaErrorInvalidValue;
     const int64_t panels = p.swiglu ? p.columns / 64 : (p.r.N + 127) / 128;
     const int64_t items = panels * (p.r.R / C::TN + (p.r.R < p.r.E ? p.r.R : p.r.E));  // at most
-    const int split = split_of(items, static_cast<int>((K + C::chunk - 1) / C::chunk));
+    const int64_t used = p.r.R < p.r.E ? p.r.R : p.r.E, each = (p.r.R + used - 1) / used;  // groups with rows, theirs
+    const int split = split_of(panels * used * ((each + C::TN - 1) / C::TN), static_cast<int>((K + C::chunk - 1) / C::chunk));
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
