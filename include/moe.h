@@ -1048,7 +1048,8 @@ moe_status_t moe_dequantize_int4(int32_t group, int32_t dtype, int64_t rows, int
  *   offsets    int32 [E + 1], or NULL with E = 1        device, read
  *   row_scale  fp32 [R] or NULL (1)             device, read
  *   y          dtype [R, N], row stride ldy (a multiple of 8)  device, written
- * x, w_codes and y are 16-byte aligned, N is a multiple of 8 and at most 2^29. */
+ * x, w_codes and y are 16-byte aligned, N is a multiple of 8 and at most 2^29;
+ * row strides are at most 2^30. */
 moe_status_t moe_grouped_gemm_int4(int32_t group, int32_t dtype, int64_t R, int32_t N, int32_t K,
                                    int32_t E, const void *x, int64_t x_rows, int64_t ldx,
                                    const int32_t *src, int32_t src_div, const void *w_codes,

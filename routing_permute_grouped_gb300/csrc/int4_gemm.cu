@@ -462,7 +462,13 @@ cudaError_t launch(const Int4Product& q, cudaStream_t st) {
 
 template <typename T>
 cudaError_t product(int group, const Int4Product& p, cudaStream_t st) {
-    if (p.r.R > 8ll * p.r.E) return launch_int4_wide<T>(group, p, st);
+    // Wide tiles read a group's weights once for up to 64 rows, but need more rows than a
+    // narrow tile's 8, and enough work: their warps hand every chunk on, 20 us at least.
+    // Narrow and wide, in us: 8 rows in each of 32 groups of 7168 x 2048 59 and 92, 12 rows
+    // 104 and 94, 32 rows 203 and 104; 16 rows in 4 groups of 1024 x 7168 (2^29 products)
+    // 20 and 27, 16 rows in 8 groups of 7168 x 2048 (2^31) 39 and 35, 64 rows of 1024 x 16384
+    // (2^30) 39 and 31.
+    if (p.r.R > 8ll * p.r.E && static_cast<double>(p.r.R) * p.r.N * p.r.K >= 0x1p30) return launch_int4_wide<T>(group, p, st);
     if (group == 32) return launch<T, 32>(p, st);
     return group == 64 ? launch<T, 64>(p, st) : launch<T, 128>(p, st);
 }

@@ -136,7 +136,7 @@ PRODUCT = dict(group=64, dtype=0, R=8, N=128, K=128, E=4, x=P, x_rows=8, ldx=128
     (dict(off=None), INVALID), (dict(y=None), INVALID), (dict(x=ODD), INVALID), (dict(codes=ODD), INVALID),
     (dict(y=ODD), INVALID), (dict(scales=ONE), INVALID), (dict(ldx=120), INVALID), (dict(ldx=132), INVALID),
     (dict(ldy=120), INVALID), (dict(ldy=132), INVALID), (dict(x_rows=7), INVALID), (dict(src=P, div=0), INVALID),
-    (dict(src=P, x_rows=0), INVALID),
+    (dict(src=P, x_rows=0), INVALID), (dict(ldx=(1 << 30) + 8), UNSUPPORTED), (dict(ldy=(1 << 30) + 8), UNSUPPORTED),
 ])
 def test_product_refuses(lib, kw, status):
     assert _call(lib.moe_grouped_gemm_int4, PRODUCT, kw) == status
