@@ -137,7 +137,7 @@ __device__ __forceinline__ void store64(void* p, const uint32_t (&r)[16]) {
 }
 
 template <typename T, bool ZEROS, bool WIDE>
-__global__ void __launch_bounds__(256) k_quantize_int4(const __grid_constant__ Int4Args a) {
+__global__ void __launch_bounds__(256, 5) k_quantize_int4(const __grid_constant__ Int4Args a) {
     pdl_trigger();
     pdl_wait();
     const int me = threadIdx.x & (a.team - 1);

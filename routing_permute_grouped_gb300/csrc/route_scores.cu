@@ -38,6 +38,7 @@ constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kMaxChoices = 8;
 constexpr int kWarps = 8;          // per block
 constexpr int kPerSm = 3;          // blocks; a warp's set-up is then shared by a dozen tokens of a large batch
+constexpr int kPerSmBwd = 4;       // of the gradient, which waits more than it computes (3: 25 us where 4 take 21)
 constexpr int kLossBlocks = 512;   // at most, where loads and losses are summed
 constexpr int kLossColumns = 8;    // experts per block of the second kernel
 
@@ -63,6 +64,7 @@ struct ScoreArgs {
     // gradient
     const float* dw;      // [T, k] or null
     const float* dlosses; // [2] or null
+    float per_count;      // E / (k T^2)
     void* dlogits;
     int64_t ldd;
     int32_t wide_out;
@@ -714,19 +716,23 @@ __global__ void __launch_bounds__(256) k_route_losses(const __grid_constant__ Sc
 //                    c_e = dbalance E count_e / (k T^2), p the scores over their sum
 //   z                dlogit_e += dz (2 / T) lse softmax_e
 template <typename T, int V, bool LOSS>
-__global__ void __launch_bounds__(32 * kWarps, kPerSm) k_route_scores_bwd(const __grid_constant__ ScoreArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, kPerSmBwd) k_route_scores_bwd(const __grid_constant__ ScoreArgs a) {
     __shared__ __align__(32) float s_add[kWarps][32 * V];
+    __shared__ __align__(32) float s_count[LOSS ? 32 * V : 1];  // E / (k T^2) dbalance count
     pdl_trigger();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float c[LOSS ? V : 1], dz = 0.0f;
     if constexpr (LOSS) {
-        const double per = static_cast<double>(a.E) / (static_cast<double>(a.k) * static_cast<double>(a.T) * a.T);
-        const float f = static_cast<float>(per) * ld_dep(a.dlosses);
+        // by way of shared memory: where every warp reads the counts itself, their few lines
+        // are what all wait for (52 us of 32768 x 256 against 33)
+        const float f = a.per_count * ld_dep(a.dlosses);
         dz = ld_dep(a.dlosses + 1) * 2.0f / static_cast<float>(a.T);
+        for (int e = threadIdx.x; e < 32 * V; e += 32 * kWarps)
+            s_count[e] = e < a.E ? f * static_cast<float>(ld_dep(a.counts + e)) : 0.0f;
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            c[i] = lane * V + i < a.E ? f * static_cast<float>(ld_dep(a.counts + lane * V + i)) : 0.0f;
+        for (int i = 0; i < V; ++i) c[i] = s_count[lane * V + i];
     }
     const bool soft = LOSS || (!a.sigmoid && !a.renormalize);
     Raw<T, V> raw;
@@ -1042,12 +1048,13 @@ extern "C" moe_status_t moe_route_scores_bwd(const moe_score_rule_t* rule, int32
     a.idx = const_cast<int32_t*>(topk_idx);
     a.dw = dw;
     a.counts = const_cast<int32_t*>(counts);
+    a.per_count = static_cast<float>(rule->E / (static_cast<double>(rule->k) * static_cast<double>(T) * static_cast<double>(T)));
     a.dlosses = dlosses;
     a.dlogits = dlogits;
     a.ldd = ldd;
     a.wide_out = wide_rows(dlogits, ldd, dtype, rule->E);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t need = (T + kWarps - 1) / kWarps, most = 5ll * num_sms();
+    const int64_t need = (T + kWarps - 1) / kWarps, most = static_cast<int64_t>(kPerSmBwd) * num_sms();
     const dim3 grid(static_cast<unsigned>(need < most ? need : most));
     const cudaError_t e = by_type(dtype, rule->E, [&](auto t, auto v) {
         using E_ = decltype(t);
