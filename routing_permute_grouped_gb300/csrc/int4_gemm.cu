@@ -1,4 +1,4 @@
-// int4_gemm.cu -- products of 16-bit rows with 4-bit weights, by groups of rows.
+// int4_gemm.cu -- products of 16-bit rows with 4-bit weights, few rows to a group.
 //
 //   y[r] = row_scale[r] * x[src[r] / div] W[e]^T   for the rows r of group e
 // with W[e][n][k] = (code - zero) * scale, scale and zero per row n and group of
@@ -6,22 +6,27 @@
 // group's products as they are, and each group's sum is scaled once, in fp32.
 //
 // Few token rows: the weights' bytes set the pace, and what has to keep up with
-// them is the widening of the codes, 11 instructions for 8 codes.  So nothing is
-// handed from warp to warp: a warp streams 32 weight rows (with SwiGLU 16 of gate
-// and the same 16 of up) straight into registers in the layout of the A operand of
-// mma.m16n8k16, a few chunks of 128 elements ahead, widens them in place and
-// multiplies them by 8 or 16 token rows, which it reads as the B operand through
-// L1.  (The same product with the widened weights written to tensor memory for
-// tcgen05.mma spends as much again on barriers, tensor-memory stores and sums read
-// back per group: 195 us where this takes FIXME.)
+// them is the widening of the codes.  So no weight is handed from warp to warp: a
+// warp streams 32 weight rows (with SwiGLU 16 of gate and the same 16 of up), with
+// their scales and zero points, by cp.async into a ring of its own, a step of 128
+// elements (256 for groups of 128) ahead, widens them in registers as the A operand of
+// mma.m16n8k16 and multiplies them by up to 8 token rows, whose B operands it reads
+// from two blocks of token rows that the CTA's 8 warps share.  Two CTAs to an SM.
+// (The same product with the widened weights written to tensor memory for
+// tcgen05.mma, int4_wide.cu, spends as much again on handing chunks on: 2 rows in
+// each of 220 groups of 7168 x 2048 545 us, here 330.)
+//
+// That decode batch reads 1.72 GB at 5.2 TB/s, 78 % of a copy's rate.  Its loads alone
+// take 287 us and its arithmetic alone 291: 298 instructions for 32 x 128 weights, 60 % of
+// the issue slots with the 16 warps that the registers leave.  Measured on the way there:
+// or-ing the codes into a mantissa, three shifts instead of one, 306 instructions;
+// scales and zero points through L1 instead of shared memory 385 us; token rows through
+// L1 420; three CTAs to an SM spill.
 //
 // The order of k inside a group is free as long as both operands share it: a lane
 // takes whole 32-bit words, and one word's eight elements are its part of two
 // steps of 16.  All of a step's elements lie in one group of scales, so a lane's
-// load is 4, 2 or 1 words for groups of 128, 64 or 32.
-//
-// A code becomes a 16-bit number by or-ing it into the mantissa of 128 (bf16) or
-// 1024 (f16), from which 128 + zero or 1024 + zero is then subtracted exactly.
+// part is 4, 2 or 1 words for groups of 128, 64 or 32.
 //
 // Few items: the warps of a CTA split the sum and add their parts in order.
 #include <cuda_runtime.h>
@@ -422,6 +427,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_int4_product(const __grid_co
 // Warps that split a sum, as far as the token rows of their steps fit a block: the
 // number that makes the fewest steps of the CTAs that run one after another, an item's
 // start and end counted as kItemSteps.
+// One token on 8 experts of 4096 x 7168, by split 1, 2 and 4: 47, 43 and 45 us; one row of
+// 1024 x 4096, by 1 and 8: 35 and 12.
 constexpr int kItemSteps = 4;
 int split_of(int64_t blocks, int64_t tiles, int64_t rows, int steps, int step) {
     const int held = rows > 4 ? 8 : rows > 2 ? 4 : static_cast<int>(rows);  // of the longest tile

@@ -7,18 +7,26 @@
 //
 // The weights are the MMA's M side: 128 rows of W[e], widened in registers and
 // written to tensor memory, from where tcgen05.mma takes its A operand; the token
-// rows are its N side (16 to 64 of them, a multiple of 16), staged by TMA.  A work
-// item is such a panel of weight rows times a tile of token rows; the sum runs
-// over chunks of 128 elements.  One CTA of 16 warps per SM:
-//   warp 0       TMA of the codes (12 chunks of 8 KB in flight)
-//   warp 1       TMA of the token rows (gather4 where src picks them)
+// rows are its N side (16 to 64 of them, a multiple of 16).  A work item is such a
+// panel of weight rows times a tile of token rows; the sum runs over chunks of 256
+// elements (128 for groups of 64 and 32).  One CTA of 20 warps per SM:
+//   warp 0       TMA of the codes (6 chunks of 16 KB in flight)
+//   warps 1, 3   the token rows by cp.async, 80 KB of them in flight, whichever src picks
 //   warp 2       issues the MMAs
-//   warp 3       scales and zero points, a few chunks ahead, into shared memory
-//   warps 4-7    take a chunk's sums (one per group) out of tensor memory, scale
-//                and add them in registers, one weight row per thread; the epilogue
-//   warps 8-15   widen codes, the two halves taking the chunks in turn
-// A code becomes a 16-bit number by or-ing it into the mantissa of 128 (bf16) or
-// 1024 (f16), from which 128 + zero or 1024 + zero is then subtracted exactly.
+//   warps 4-11   two warpgroups that take the items in turn: a chunk's sums (one per
+//                group of scales) out of tensor memory, scaled and added in registers,
+//                one weight row per thread; the epilogue beside the other's sums
+//   warps 12-19  widen codes, two warpgroups that take the chunks in turn
+//
+// What bounds it: not one of these.  32 rows in each of 32 groups of 7168 x 2048 take 104
+// us (2.5 TB/s; 39 us of bytes), 64 rows in each of 8 of 4096 x 4096 49 (350 TFLOP/s).
+// With seven of eight MMAs, the widening's arithmetic, the sums' or three quarters of the
+// token rows' loads left out, the first takes 96, 92, 96 or 100: a chunk is handed on four
+// times, and tensor memory holds two of them (512 columns: two widened, two of sums).
+// Measured and slower: chunks of 128, four of them in tensor memory (102 to 109); three
+// widening warpgroups (108); both summing warpgroups on half of every tile's columns
+// (107); sums by packed pairs (110); two issuing warps (115); token rows by 256 elements
+// (123) or gathered by TMA; scales of the rows read before the sums (115).
 //
 // Few items and a long sum: the CTAs of a cluster split the sum; each hands its
 // part of every column to the CTA that stores it, which adds the parts in the
@@ -41,7 +49,8 @@ constexpr int kCodeBytes = 96 * 1024;  // of the codes in flight
 constexpr int kRowBytes = 80 * 1024;   // of the token rows in flight
 constexpr int kRowStages = 16;         // of 128 elements each, at most
 constexpr int kThreads = 640;
-// Registers per thread of the roles; together no more than the launch's 96 each
+// Registers per thread of the roles; together no more than the launch's 96 each.  (56,
+// 120 and 88 spill in the loaders: 115 us where these take 110.)
 constexpr int kIssueRegs = 80, kSumRegs = 120, kWidenRegs = 80;
 static_assert(kIssueRegs + 2 * kSumRegs + 2 * kWidenRegs <= 5 * 96, "register split");
 constexpr int kMaxSplit = 8;           // CTAs of a cluster
