@@ -874,6 +874,8 @@ def moe_route_scores_bwd(rule: ScoreRule, logits, topk_idx, dlogits, dw=None, co
 class _RouteScores(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, rule, bias, losses):
+        if logits.dim() != 2:
+            raise ValueError(f"logits: expected a [T, E] tensor; got {tuple(logits.shape)}")
         T, dev = logits.shape[0], logits.device
         if logits.stride(1) != 1 and rule.E > 1 or logits.stride(0) < rule.E and T > 1:
             logits = logits.clone(memory_format=torch.contiguous_format)
@@ -903,7 +905,10 @@ class _RouteScores(torch.autograd.Function):
 def route_scores(logits, rule: ScoreRule, bias=None, losses: bool = False):
     """moe_route_scores, differentiable in the logits: topk_w and topk_idx of logits [T, E], and
     with ``losses`` also the losses fp32 [2] (balance, z) and the counts int32 [E].  The choice
-    is a constant, so the bias has no gradient.  A second derivative raises an error."""
+    is a constant, so the bias has no gradient.  A second derivative raises an error.  In a CUDA
+    graph the backward pass is captured with its forward, while no result computed outside of
+    the graph from the same leaves is alive (torch accumulates their gradients on the stream of
+    the first)."""
     return _RouteScores.apply(logits, rule, bias, losses)
 
 

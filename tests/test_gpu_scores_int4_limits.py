@@ -225,6 +225,36 @@ def test_calls_on_streams_of_their_own_and_two_graphs():
     same()
 
 
+def test_forward_and_backward_captured_together():
+    rule = moe.score_rule(64, 6, "sigmoid", 8, 4, 2)
+    bias = torch.randn((64,), generator=_gen(2), device="cuda") * 0.01
+    x = torch.randn((500, 64), generator=_gen(3), device="cuda")
+    g = torch.randn((500, 6), generator=_gen(4), device="cuda")
+
+    def loss(leaf):
+        w, _, both, _ = moe.route_scores(leaf, rule, bias, losses=True)
+        return (w * g).sum() + both[0] + 0.1 * both[1]
+
+    leaf = x.clone().requires_grad_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        loss(leaf).backward()
+    torch.cuda.current_stream().wait_stream(side)
+    leaf.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss(leaf).backward()
+    for seed in (5, 6):
+        new = torch.randn((500, 64), generator=_gen(seed), device="cuda")
+        with torch.no_grad():
+            leaf.copy_(new)
+        graph.replay()
+        other = new.clone().requires_grad_()
+        loss(other).backward()
+        assert torch.equal(leaf.grad, other.grad)
+
+
 # -------------------------------------------------- offsets past 32 bits --
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_routing_of_more_than_2_31_logits(score):

@@ -213,3 +213,9 @@ def test_groups_of_no_elements_are_refused(fake_lib):  # noqa: F811
         with pytest.raises(ValueError):
             moe.moe_quantize_int4(group, Fake(BF, 8, 96), Fake(U8, 8, 48), Fake(BF, 8, 2))
     assert not fake_lib.calls
+
+
+def test_scores_of_another_number_of_dimensions_are_refused():
+    for shape in ((16,), (2, 3, 16)):
+        with pytest.raises(ValueError, match="logits"):
+            moe.route_scores(torch.zeros(shape), moe.score_rule(16, 2))
