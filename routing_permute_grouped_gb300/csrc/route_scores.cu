@@ -16,18 +16,17 @@
 //
 // The choice is that of exact keys.  Those of fp32 are off by a few units of the
 // last place, so where two that matter (neighbours among the k + 1 largest, the
-// last kept group and the first dropped) are closer than their error allows, the
-// token is chosen again with keys of fp64.  Experts of the same logit and the
-// same bias have the same key in either and need no second look.
+// last kept group and the first dropped) are closer than their error allows, keys of
+// fp64 decide, of the experts whose fp32 keys leave it open.  Experts of the same logit
+// and the same bias have the same key in either and need no second look.  exp of fp64
+// takes a warp 2000 cycles and a division 1600: 20 to 30 tokens of 32768 have such
+// neighbours, and with the keys of all 256 experts in fp64 each of them held its block for
+// 37 thousand, 15 to 28 us at the end of a batch.
 //
 // What bounds it: instructions, where there are many tokens.  32768 x 256 fp32 logits, 8
-// chosen of 4 of 8 groups by sigmoids with a bias, with losses: 71 us (5 us of bytes),
-// 1280 instructions per token and 71 % of the issue slots; without bias and groups 33.
-// 15 to 28 us of it are the tokens chosen again, 20 to 30 of them: exp of fp64 takes a warp
-// 2000 cycles and a division 1600, and each holds its block for 37 thousand in all.  (fp64
-// keys only for experts near a boundary, or small loops over shared memory instead of
-// unrolled ones, gain 2 us.)
-// The gradient: 33 us with losses, 21 without (10 us of bytes).
+// chosen of 4 of 8 groups by sigmoids with a bias: 49 us (5 us of bytes), with the losses
+// 63, without bias and groups 35.  The gradient: 33 us with losses, 21 without (10 us of
+// bytes).
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -46,10 +45,11 @@ namespace {
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kMaxChoices = 8;
 constexpr int kWarps = 8;          // per block
-constexpr int kPerSm = 3;          // blocks; a warp's set-up is shared by a dozen tokens (4 spill: 87 us where 3 take 74)
+constexpr int kPerSm = 3;          // blocks; a warp's set-up is shared by a dozen tokens (4 spill: 72 us where 3 take 64)
 constexpr int kPerSmBwd = 4;       // of the gradient, which waits more than it computes (3: 25 us where 4 take 21)
 constexpr int kLossBlocks = 512;   // at most, where loads and losses are summed
 constexpr int kLossColumns = 8;    // experts per block of the second kernel
+constexpr int kLossThreads = 1024; // of it (256 take 1 us more)
 
 struct ScoreArgs {
     const void* logits;
@@ -316,17 +316,17 @@ struct Pick {
 
 // The same choice in parallel: the (k + 1)-th largest of the lanes' own largest keys is
 // no larger than the (k + 1)-th key of all, so that what is not below it, a dozen
-// experts as a rule, holds all that is looked for; these are dealt to the lanes and
-// count who comes before them.  False where they are more than the lanes (many ties, or
-// few lanes with experts that may be chosen).  buf: the warp's 32 V logits, 32 V keys
-// and 32 experts.
+// experts as a rule, holds all that is looked for, and all that is within `margin` of it
+// where that is taken off; these are dealt to the lanes and count who comes before them.
+// False where they are more than the lanes (many ties, or few lanes with experts that may
+// be chosen).  buf: the warp's 32 V logits, 32 V keys and 32 experts; floor_: the bound.
 template <int V>
 __device__ __forceinline__ bool largest_in_parallel(int k, int lane, const uint32_t (&u)[V], const float (&l)[V],
-                                                    uint32_t* buf, Pick& mine) {
+                                                    float margin, uint32_t* buf, Pick& mine, uint32_t& floor_) {
     uint32_t best = u[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) best = max(best, u[i]);
-    uint32_t floor_ = 1;
+    floor_ = 1;
     for (int n = 0; n <= k;) {
         const uint32_t m = warp_max(best);
         if (m == 0) {  // every expert that may be chosen is looked at
@@ -337,6 +337,7 @@ __device__ __forceinline__ bool largest_in_parallel(int k, int lane, const uint3
         n += __popc(__ballot_sync(kAll, best == m));
         best = best == m ? 0u : best;
     }
+    if (margin > 0.0f && floor_ > kDead) floor_ = key_of(number_of(floor_) - margin);
     // in ascending order of the lane, and in a lane of the slot: of the expert
     int count = 0, before = 0;
     uint8_t* list = reinterpret_cast<uint8_t*>(buf + 64 * V);
@@ -372,7 +373,8 @@ __device__ __forceinline__ bool same_key(const ScoreArgs& a, float l0, int e0, f
     return l0 == l1 && (!a.bias || tame(ld_dep(a.bias + e0)) == tame(ld_dep(a.bias + e1)));
 }
 
-// The choice of token t with keys of fp64; lane r gets the r-th expert.
+// The choice of token t with keys of fp64 of all experts; lane r gets the r-th.  For
+// softmaxes, whose sum needs all of them, and where more experts than lanes are too close.
 template <typename T, int V>
 __device__ __noinline__ int choose_exact(const ScoreArgs& a, int64_t t, double* buf) {
     const int lane = threadIdx.x & 31;
@@ -419,6 +421,88 @@ __device__ __noinline__ int choose_exact(const ScoreArgs& a, int64_t t, double* 
     int expert;
     largest<V, uint64_t>(a.k, lane, u, my_key, expert);
     return expert;
+}
+
+// The kept groups by keys of fp64, which only the experts have that may be a group's best
+// (or two best): the others' fp32 keys are further below than `margin`, their error.  buf: a
+// warp's 32 slots fp32 keys, its 32 slots logits, a list of experts; top: the largest logit.
+__device__ __noinline__ uint32_t exact_groups(const ScoreArgs& a, uint32_t* buf, int slots, float margin, float top) {
+    const int lane = threadIdx.x & 31, gsz = a.E / a.n_groups;
+    const float* key = reinterpret_cast<const float*>(buf);
+    const float* logit = key + 32 * slots;
+    uint8_t* list = reinterpret_cast<uint8_t*>(buf + 64 * slots);
+    uint64_t* exact = reinterpret_cast<uint64_t*>(buf);  // of the list's experts, over what has been read
+    float f1 = -INFINITY, f2 = -INFINITY;  // of group `lane`
+    if (lane < a.n_groups)
+#pragma unroll 1
+        for (int e = lane * gsz; e < (lane + 1) * gsz; ++e) {
+            f2 = fmaxf(f2, fminf(f1, key[e]));
+            f1 = fmaxf(f1, key[e]);
+        }
+    const float least = (a.group_top == 2 ? f2 : f1) - margin;
+    int count = 0;
+#pragma unroll 1
+    for (int base = 0; base < a.E; base += 32) {
+        const int e = base + lane;
+        const float from = __shfl_sync(kAll, least, e < a.E ? e / gsz : 0);
+        const bool need = e < a.E && key[e] > -INFINITY && key[e] >= from;
+        const uint32_t at = __ballot_sync(kAll, need);
+        if (need) list[count + __popc(at & ((1u << lane) - 1u))] = static_cast<uint8_t>(e);
+        count += __popc(at);
+    }
+    double sum = 0;
+    if (!a.sigmoid) {
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += 32)
+            if (logit[e] > -INFINITY) sum += exp(static_cast<double>(logit[e]) - top);
+        sum = warp_sum(sum);
+    }
+    __syncwarp();
+    // entry c of the list has expert c or a later one, whose logit lies past where
+    // its 32 keys and all before them go
+#pragma unroll 1
+    for (int c0 = 0; c0 < count; c0 += 32) {
+        const int e = list[min(c0 + lane, count - 1)];
+        const double x = logit[e];
+        __syncwarp();
+        const double ex = exp(a.sigmoid ? -x : x - top);
+        double v = (a.sigmoid ? 1.0 : ex) / (a.sigmoid ? 1.0 + ex : sum);
+        if (a.bias) v += static_cast<double>(tame(ld_dep(a.bias + e)));
+        if (c0 + lane < count) exact[c0 + lane] = key_of(v);
+        __syncwarp();
+    }
+    uint64_t b1 = 0, b2 = 0;
+#pragma unroll 1
+    for (int c = 0; c < count; ++c) {
+        const int e = list[c];
+        if (e >= lane * gsz && e < (lane + 1) * gsz) {
+            const uint64_t u = exact[c];
+            b2 = max(b2, min(b1, u));
+            b1 = max(b1, u);
+        }
+    }
+    auto number = [](uint64_t u) { return __longlong_as_double(u >> 63 ? u ^ 0x8000000000000000ull : ~u); };
+    if (a.group_top == 2 && b2) b1 = key_of(number(b1) + number(b2));
+    int rank = 0;  // groups before this one; ties to the lower group
+#pragma unroll 1
+    for (int g = 0; g < a.n_groups; ++g) rank += __shfl_sync(kAll, b1, g) + (g < lane) > b1;
+    __syncwarp();
+    return __ballot_sync(kAll, lane < a.n_groups && rank < a.topk_groups);
+}
+
+// How many of the experts that `need` be compared come before the lane's, by sigmoids of
+// fp64; ties to the lower lane.
+__device__ __noinline__ int exact_rank(float logit, float bias, bool need) {
+    const int lane = threadIdx.x & 31;
+    const double v = 1.0 / (1.0 + exp(-static_cast<double>(logit))) + static_cast<double>(bias);
+    const uint64_t u = need ? key_of(v) : 0;
+    int rank = 0;
+#pragma unroll 1
+    for (uint32_t m = __ballot_sync(kAll, need); m; m &= m - 1) {
+        const int j = __ffs(m) - 1;
+        rank += __shfl_sync(kAll, u, j) + (j < lane) > u;
+    }
+    return rank;
 }
 
 // exp and 1 / x for what is summed or compared, not for the weights that come out:
@@ -471,7 +555,7 @@ __device__ __forceinline__ float chosen_share(const ScoreArgs& a, float lx) {
 template <typename T, int V, bool LOSS>
 __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_route_scores(const __grid_constant__ ScoreArgs a) {
     constexpr int W = kWarps;
-    __shared__ __align__(32) double s_buf[W][32 * V + 16];  // 32 V keys of fp64, or logits, keys and 32 candidates
+    __shared__ __align__(32) double s_buf[W][32 * V + 32];  // 32 V keys of fp64 or logits and keys, and a list of experts
     __shared__ __align__(32) float s_bias[32 * V];
     __shared__ __align__(32) uint32_t s_group[32 * V];  // the bit of an expert's group
     __shared__ int s_load[LOSS ? 32 * V : 1];
@@ -577,11 +661,22 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_route_scores(const __gr
         const float off = a.sigmoid ? 0x1p-20f : 0x1p-18f * scores_top;
         bool close = false;
         uint32_t kept = kAll;
+        const float margin = 2.0f * off + 0x1p-21f * most;
         if (grouped) {
             bool near_;
-            kept = kept_groups<V, float>(a, gsz, lane, key, reinterpret_cast<float*>(s_buf[warp]),
-                                         2.0f * off + 0x1p-21f * most, &near_);
-            close = by_score && near_;
+            kept = kept_groups<V, float>(a, gsz, lane, key, reinterpret_cast<float*>(s_buf[warp]), margin, &near_);
+            if (by_score && near_) {
+                uint32_t* buf = reinterpret_cast<uint32_t*>(s_buf[warp]);
+#pragma unroll
+                for (int i = 0; i < V; ++i) words[i] = __float_as_uint(key[i]);
+                put_words<V>(buf + lane * V, words);
+#pragma unroll
+                for (int i = 0; i < V; ++i) words[i] = __float_as_uint(l[i]);
+                put_words<V>(buf + 32 * V + lane * V, words);
+                __syncwarp();
+                kept = exact_groups(a, buf, V, margin, top);
+                __syncwarp();
+            }
         }
         // slots past the last expert have -infinity and come after all experts that do
         uint32_t u[V];
@@ -589,18 +684,23 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_route_scores(const __gr
 #pragma unroll
         for (int i = 0; i < V; ++i) u[i] = kept & words[i] ? key_of(biased ? key[i] : l[i]) : 0u;
         Pick mine;
-        if (!largest_in_parallel<V>(a.k, lane, u, l, reinterpret_cast<uint32_t*>(s_buf[warp]), mine)) {
+        uint32_t floor_;
+        const bool parallel = largest_in_parallel<V>(a.k, lane, u, l, biased ? margin : 0.0f,
+                                                     reinterpret_cast<uint32_t*>(s_buf[warp]), mine, floor_);
+        if (!parallel) {
             largest<V, uint32_t>(a.k, lane, u, mine.key, mine.expert);
             mine.rank = lane;
             mine.logit = value_of<V>(l, mine.expert);
         }
-        if (biased && !close) {
+        uint32_t last = 0;  // the k-th largest key
+        if (biased) {
             // neighbours in the order of the keys
             uint32_t* order = reinterpret_cast<uint32_t*>(s_buf[warp]);
             if (lane <= a.k) order[lane] = 0;
             __syncwarp();
             if (mine.rank <= a.k) order[mine.rank] = mine.key;
             __syncwarp();
+            last = order[a.k - 1];
             const uint32_t next_key = mine.rank < a.k ? order[mine.rank + 1] : 0;
             const float f0 = number_of(mine.key), f1 = number_of(next_key);
             const bool near_ = next_key > kDead && f0 - f1 <= off + 0x1p-23f * fmaxf(fabsf(f0), fabsf(f1));
@@ -617,9 +717,18 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_route_scores(const __gr
             __syncwarp();
         }
         if (close) {
-            mine.expert = choose_exact<T, V>(a, t, s_buf[warp]);
-            mine.rank = lane;
-            mine.logit = value_of<V>(l, mine.expert);
+            // what may be among the k lies no further below the k-th than the error; where the
+            // lanes have it all, a key of fp64 each
+            const uint32_t from = last > kDead ? key_of(number_of(last) - margin) : 0;
+            if (parallel && a.sigmoid && from >= floor_) {
+                const bool need = mine.rank < 32 && mine.key >= from;
+                const int rank = exact_rank(mine.logit, s_bias[mine.expert], need);
+                mine.rank = need ? rank : 32;
+            } else {
+                mine.expert = choose_exact<T, V>(a, t, s_buf[warp]);
+                mine.rank = lane;
+                mine.logit = value_of<V>(l, mine.expert);
+            }
         }
         const bool chosen = mine.rank < a.k;
         const float lx = chosen ? mine.logit : -INFINITY;
@@ -660,10 +769,11 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_route_scores(const __gr
 
 // The blocks' sums to the loads and losses.  A block takes eight experts; the one
 // that ends last adds up what the others left, in their order.
-__global__ void __launch_bounds__(256) k_route_losses(const __grid_constant__ ScoreArgs a) {
-    __shared__ float s_share[32][kLossColumns];
-    __shared__ int s_load[32][kLossColumns];
-    __shared__ float s_sum[8];
+__global__ void __launch_bounds__(kLossThreads) k_route_losses(const __grid_constant__ ScoreArgs a) {
+    constexpr int kRows = kLossThreads / kLossColumns, W = kLossThreads / 32;
+    __shared__ float s_share[W][kLossColumns];
+    __shared__ int s_load[W][kLossColumns];
+    __shared__ float s_sum[W];
     __shared__ bool s_last;
     pdl_trigger();
     pdl_wait();
@@ -671,17 +781,25 @@ __global__ void __launch_bounds__(256) k_route_losses(const __grid_constant__ Sc
     float share = 0.0f;
     int load = 0;
     if (e < a.E)
-        for (int b = r; b < a.blocks; b += 32) {
+#pragma unroll 4
+        for (int b = r; b < a.blocks; b += kRows) {
             share += ld_dep(a.share + static_cast<int64_t>(b) * a.E + e);
             load += ld_dep(a.load + static_cast<int64_t>(b) * a.E + e);
         }
-    s_share[r][c] = share;
-    s_load[r][c] = load;
+#pragma unroll
+    for (int o = kLossColumns; o < 32; o <<= 1) {
+        share += __shfl_xor_sync(kAll, share, o);
+        load += __shfl_xor_sync(kAll, load, o);
+    }
+    if ((threadIdx.x & 31) < kLossColumns) {
+        s_share[threadIdx.x >> 5][c] = share;
+        s_load[threadIdx.x >> 5][c] = load;
+    }
     __syncthreads();
     if (threadIdx.x < kLossColumns) {
         share = 0.0f;
         load = 0;
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < W; ++i) {
             share += s_share[i][c];
             load += s_load[i][c];
         }
@@ -700,7 +818,7 @@ __global__ void __launch_bounds__(256) k_route_losses(const __grid_constant__ Sc
     if (!s_last) return;
     __threadfence();
     float z = 0.0f;
-    for (int b = threadIdx.x; b < a.blocks; b += 256) z += ld_dep(a.z + b);
+    for (int b = threadIdx.x; b < a.blocks; b += kLossThreads) z += ld_dep(a.z + b);
     z = warp_sum(z);
     if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = z;
     __syncthreads();
@@ -708,7 +826,7 @@ __global__ void __launch_bounds__(256) k_route_losses(const __grid_constant__ Sc
         float balance = 0.0f;
         for (int b = 0; b < static_cast<int>(gridDim.x); ++b) balance += ld_dep(a.part + b);
         z = 0.0f;
-        for (int i = 0; i < 8; ++i) z += s_sum[i];
+        for (int i = 0; i < W; ++i) z += s_sum[i];
         const float T = static_cast<float>(a.T);
         a.losses[0] = balance * static_cast<float>(a.E) / T;
         a.losses[1] = z / T;
@@ -1035,7 +1153,7 @@ extern "C" moe_status_t moe_route_scores(const moe_score_rule_t* rule, int32_t d
                           dim3(32 * kWarps), 0, st, a);
     });
     if (e == cudaSuccess && counts)
-        e = launch_pdl(k_route_losses, dim3((rule->E + kLossColumns - 1) / kLossColumns), dim3(256), 0, st, a);
+        e = launch_pdl(k_route_losses, dim3((rule->E + kLossColumns - 1) / kLossColumns), dim3(kLossThreads), 0, st, a);
     return e == cudaSuccess ? MOE_OK : set_last_error(MOE_ERR_CUDA, "routing by scores: %s", cudaGetErrorString(e));
 }
 

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import routing_permute_grouped_gb300 as moe
+from tests import scores_ref
 from tests.test_gpu_int4 import NAN, TYPES, _gen, _offsets, _product_check, _quantize, _rand, _weights
 
 pytestmark = pytest.mark.gpu
@@ -140,6 +141,42 @@ def test_rows_and_scales_that_are_not_numbers(dtype):
         assert not torch.isfinite(y[1, columns]).any() and torch.isnan(y[R - 1, columns]).all()
         rows = [r for r in range(R) if r not in (1, R - 1)]
         assert torch.isfinite(y[rows][:, columns]).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,kept,top", [(256, 0, 0, 1), (256, 8, 4, 1), (256, 8, 4, 2), (60, 6, 3, 2), (64, 32, 9, 1),
+                                               (256, 2, 1, 2)])
+@pytest.mark.parametrize("bias_of", ["even", "odd", "large"])
+def test_neighbours_at_the_last_place_of_the_choice(score, E, groups, kept, top, bias_of):
+    """A stranger's logit one fp32 step from that of the last expert chosen, and a dropped group
+    whose logits are the last kept one's but for one step: choices of fp64 among few experts."""
+    T, k = 1500, 6
+    rule = moe.score_rule(E, k, score, groups, kept, top)
+    gen = torch.Generator().manual_seed(E + groups + top)
+    logits = torch.randn((T, E), generator=gen) * 1.5
+    bias = {"even": torch.full((E,), 0.25), "odd": (torch.randn((E,), generator=gen) * 3).round() / 64,
+            "large": torch.where(torch.arange(E) % 3 == 0, 100.0, 100.25)}[bias_of]
+    last = scores_ref.choose(logits.cuda(), rule, bias.cuda())[:, k - 1].long()
+    t = torch.arange(T)
+    up = torch.rand((T,), generator=gen) < 0.5
+    step = torch.where(up, torch.inf, -torch.inf)
+    if groups:  # every second token: another group like that of the last expert
+        n = E // groups
+        mine, other = last // n, torch.randint(0, groups, (T,), generator=gen)
+        at = torch.arange(n)[None]
+        copy = logits[t[:, None], mine[:, None] * n + at]
+        big = copy.argmax(1)
+        copy[t, big] = torch.nextafter(copy[t, big], step)
+        rows = (t % 2 == 0) & (mine != other)
+        logits[t[rows, None], (other[:, None] * n + at)[rows]] = copy[rows]
+    odd = t % 2 == 1
+    stranger = torch.randint(0, E, (T,), generator=gen)
+    logits[t[odd], stranger[odd]] = torch.nextafter(logits[t, last], step)[odd]
+    logits, bias = logits.cuda(), bias.cuda()
+    idx = torch.empty((T, k), dtype=torch.int32, device="cuda")
+    w = torch.empty((T, k), device="cuda")
+    moe.moe_route_scores(rule, logits, idx, w, bias)
+    assert torch.equal(idx.cpu(), scores_ref.choose(logits, rule, bias))
 
 
 # ---------------------------------------------- calls beside one another --
