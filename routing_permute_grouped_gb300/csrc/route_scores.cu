@@ -15,10 +15,11 @@
 // integers of the same order.
 //
 // The choice is that of exact keys.  Those of fp32 are off by a few units of the
-// last place, so where two that matter (neighbours among the k + 1 largest, the
-// last kept group and the first dropped) are closer than their error allows, keys of
-// fp64 decide, of the experts whose fp32 keys leave it open.  Experts of the same logit
-// and the same bias have the same key in either and need no second look.  exp of fp64
+// last place, so where two that matter (neighbours among the k + 1 largest, the k-th
+// and any behind it, the last kept group and the first dropped) are closer than their
+// error allows, keys of fp64 decide, of the experts whose fp32 keys leave it open.
+// Experts of the same logit and the same bias have the same key in either and need no
+// second look; what lies behind such a pair at the last place does.  exp of fp64
 // takes a warp 2000 cycles and a division 1600: 20 to 30 tokens of 32768 have such
 // neighbours, and with the keys of all 256 experts in fp64 each of them held its block for
 // 37 thousand, 15 to 28 us at the end of a batch.
@@ -368,6 +369,12 @@ __device__ __forceinline__ bool largest_in_parallel(int k, int lane, const uint3
     return true;
 }
 
+// Whether the error of two fp32 keys, the first no smaller, may hide their order; off: that
+// of their scores' difference.  The sums with the biases add half a unit of each.
+__device__ __forceinline__ bool too_close(float f0, float f1, float off) {
+    return f0 - f1 <= off + 0x1p-23f * fmaxf(fabsf(f0), fabsf(f1));
+}
+
 // Whether two experts have equal keys in any precision.
 __device__ __forceinline__ bool same_key(const ScoreArgs& a, float l0, int e0, float l1, int e1) {
     return l0 == l1 && (!a.bias || tame(ld_dep(a.bias + e0)) == tame(ld_dep(a.bias + e1)));
@@ -691,6 +698,15 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_route_scores(const __gr
             largest<V, uint32_t>(a.k, lane, u, mine.key, mine.expert);
             mine.rank = lane;
             mine.logit = value_of<V>(l, mine.expert);
+            if (biased) {  // the experts behind the k + 1 largest, against the k-th
+                const float fk = number_of(__shfl_sync(kAll, mine.key, a.k - 1)), lk = __shfl_sync(kAll, mine.logit, a.k - 1);
+                const float bk = s_bias[__shfl_sync(kAll, mine.expert, a.k - 1)];
+                bool other = false;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    other |= u[i] > kDead && too_close(fk, number_of(u[i]), off) && !(l[i] == lk && s_bias[lane * V + i] == bk);
+                close = __any_sync(kAll, other);
+            }
         }
         uint32_t last = 0;  // the k-th largest key
         if (biased) {
@@ -702,8 +718,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_route_scores(const __gr
             __syncwarp();
             last = order[a.k - 1];
             const uint32_t next_key = mine.rank < a.k ? order[mine.rank + 1] : 0;
-            const float f0 = number_of(mine.key), f1 = number_of(next_key);
-            const bool near_ = next_key > kDead && f0 - f1 <= off + 0x1p-23f * fmaxf(fabsf(f0), fabsf(f1));
+            const bool near_ = next_key > kDead && too_close(number_of(mine.key), number_of(next_key), off);
             if (__any_sync(kAll, near_)) {
                 // experts of one logit and one bias have one key in any precision
                 uint32_t* lane_of = order + 16;
@@ -712,7 +727,15 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) k_route_scores(const __gr
                 const int after = near_ ? static_cast<int>(lane_of[mine.rank + 1]) : lane;
                 const float ly = __shfl_sync(kAll, mine.logit, after);
                 const int ey = __shfl_sync(kAll, mine.expert, after);
-                close = __any_sync(kAll, near_ && !same_key(a, mine.logit, mine.expert, ly, ey));
+                bool other = near_ && !same_key(a, mine.logit, mine.expert, ly, ey);
+                if (parallel) {  // the k-th may have its like behind it, and another expert behind those
+                    const int at = static_cast<int>(lane_of[a.k - 1]);
+                    const float lk = __shfl_sync(kAll, mine.logit, at);
+                    const int ek = __shfl_sync(kAll, mine.expert, at);
+                    other |= mine.rank > a.k && mine.rank < 32 && mine.key > kDead &&
+                             too_close(number_of(last), number_of(mine.key), off) && !same_key(a, lk, ek, mine.logit, mine.expert);
+                }
+                close |= __any_sync(kAll, other);
             }
             __syncwarp();
         }

@@ -1,0 +1,100 @@
+"""GPU tests of the choice of experts where equal keys, masked experts or keys at the
+end of fp32's range meet the last place, against plain fp64 arithmetic (scores_ref.py).
+
+What is compared are indices: they have to be equal.  The inputs' exact keys are far
+enough apart in fp64 (by 2^-40 of themselves at least, or equal) for its own rounding
+not to matter."""
+import pytest
+import torch
+
+import routing_permute_grouped_gb300 as moe
+from tests import scores_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+def _route(rule, logits, bias=None, losses=False):
+    T = logits.shape[0]
+    idx = torch.full((T, rule.k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, rule.k), float("nan"), device="cuda")
+    kw = {}
+    if losses:
+        kw = dict(counts=torch.empty((rule.E,), dtype=torch.int32, device="cuda"), losses=torch.empty((2,), device="cuda"),
+                  ws=torch.empty((moe.moe_route_scores_workspace_size(rule, T),), dtype=torch.uint8, device="cuda"))
+    moe.moe_route_scores(rule, logits, idx, w, bias=bias, **kw)
+    return idx, w
+
+
+def _check(rule, logits, bias):
+    logits = logits.cuda()
+    bias = None if bias is None else bias.cuda()
+    want = ref.choose(logits, rule, bias)
+    for losses in (False, True):
+        idx, w = _route(rule, logits, bias, losses)
+        off = (idx.cpu() != want).any(1).nonzero().flatten()
+        assert not len(off), (off[0].item(), idx[off[0]].tolist(), want[off[0]].tolist())
+        assert torch.isfinite(w).all()
+
+
+# ------------------------------------------- equal keys at the last place --
+def test_a_larger_exact_key_behind_two_equal_ones():
+    """Sigmoids of 17 and 18, and of 20 and 20.125, are 1 in fp32; 3 and its neighbour are
+    not told apart under a bias of 100."""
+    up = torch.nextafter(torch.tensor(3.0), torch.tensor(4.0)).item()
+    rows = torch.tensor([[17.0, 17.0, 18.0], [20.0, 20.0, 20.125], [18.0, 17.0, 17.0], [17.0, 18.0, 17.0], [3.0, 3.0, up]])
+    for bias in (0.0, 100.0):
+        for k in (1, 2):
+            _check(moe.score_rule(3, k, "sigmoid"), rows, torch.full((3,), bias))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,kept,top", [(16, 0, 0, 1), (64, 0, 0, 1), (256, 0, 0, 1), (64, 8, 4, 1), (64, 8, 4, 2),
+                                               (60, 6, 3, 2), (256, 8, 4, 2)])
+@pytest.mark.parametrize("ties", [2, 3, 7, 40])
+@pytest.mark.parametrize("k", [1, 5, 8])
+def test_equal_keys_over_the_last_place(score, E, groups, kept, top, ties, k):
+    """`ties` experts of one logit hold the last place, one or two others have a key that is
+    larger or smaller but the same, or next to it, in fp32."""
+    if ties > E // 2:
+        ties = E // 2
+    T = 120
+    gen = torch.Generator().manual_seed(E + 10 * ties + k + top)
+    rule = moe.score_rule(E, k, score, groups, kept, top)
+    for kind in ("saturated", "large bias"):
+        if kind == "saturated":  # scores of 1, or of 0, in fp32
+            base = 18.0 if score == "sigmoid" else -30.0
+            rest, step = base - 16.0 + torch.randn((T, E), generator=gen) * 0.3, 0.125
+            bias = torch.zeros(E)
+        else:
+            base = 0.5
+            rest, step = -4.0 + torch.randn((T, E), generator=gen) * 0.3, 2.0 ** -16
+            bias = torch.full((E,), 100.0)
+        logits = rest
+        # k - 1 or fewer clear ones, the ties, and strangers a step away, at random places
+        for t in range(T):
+            order = torch.randperm(E, generator=gen)
+            clear = int(torch.randint(max(0, k - ties), k, (1,), generator=gen))
+            logits[t, order[:clear]] = base + 4.0 + 0.25 * torch.arange(clear)
+            logits[t, order[clear:clear + ties]] = base
+            strangers = order[clear + ties:clear + ties + 1 + t % 2]
+            logits[t, strangers] = base + step * (1 if t % 3 else -1)
+        if score == "softmax" and kind == "saturated":
+            logits[:, 0] = 0.0  # takes all of the softmax
+        _check(rule, logits, bias)
+
+
+def test_equal_logits_under_unequal_biases():
+    """More experts than lanes share a logit; their biases differ by less than fp32 keys can."""
+    E, T = 256, 64
+    gen = torch.Generator().manual_seed(5)
+    logits = torch.zeros((T, E))
+    logits[1::2] = 0.25
+    bias = 1.0 + torch.randint(0, 3, (E,), generator=gen) * 2.0 ** -23
+    logits[:, 7] += 2.0 ** -22
+    for score in ("softmax", "sigmoid"):
+        for k in (1, 8):
+            for groups, kept, top in ((0, 0, 1), (8, 4, 2)):
+                _check(moe.score_rule(E, k, score, groups, kept, top), logits, bias)
+                _check(moe.score_rule(E, k, score, groups, kept, top), torch.zeros((T, E)), torch.full((E,), 0.25))
