@@ -235,7 +235,9 @@ __device__ __forceinline__ uint32_t kept_groups(const ScoreArgs& a, int gsz, int
             }
         __syncwarp();
     }
-    const F score = a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+    // of fp32 keys half the sum, which stays a number
+    const F part = a.group_top == 2 && sizeof(F) == 4 ? 0.5 : 1.0;
+    const F score = a.group_top == 2 && b2 > -INFINITY ? part * b1 + part * b2 : part * b1;
     const auto u = lane < a.n_groups ? key_of(score) : 0;
     int rank = 0;  // groups before this one
 #pragma unroll 4
@@ -246,7 +248,7 @@ __device__ __forceinline__ uint32_t kept_groups(const ScoreArgs& a, int gsz, int
         const int last = __ffs(__ballot_sync(kAll, lane < a.n_groups && rank == a.topk_groups - 1)) - 1;
         const int first = __ffs(__ballot_sync(kAll, lane < a.n_groups && rank == a.topk_groups)) - 1;
         const F lo = __shfl_sync(kAll, score, first), hi = __shfl_sync(kAll, score, last);
-        *close = lo > -INFINITY && hi - lo <= tol;
+        *close = lo > -INFINITY && hi - lo <= part * tol;
     }
     return kept;
 }

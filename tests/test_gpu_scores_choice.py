@@ -98,3 +98,28 @@ def test_equal_logits_under_unequal_biases():
             for groups, kept, top in ((0, 0, 1), (8, 4, 2)):
                 _check(moe.score_rule(E, k, score, groups, kept, top), logits, bias)
                 _check(moe.score_rule(E, k, score, groups, kept, top), torch.zeros((T, E)), torch.full((E,), 0.25))
+
+
+# ---------------------------------------------- masks and the ends of fp32 --
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_sums_of_a_group_that_pass_fp32(score):
+    """Two best keys whose sum is past fp32's largest number, or below its lowest: their
+    order counts all the same, and a group that has them is not one without experts."""
+    half = torch.finfo(torch.float32).max
+    cases = [
+        ([0.0] * 4, [2e38, 2e38, 3e38, 3e38], 2),
+        ([0.0] * 4, [3e38, 3e38, INF, INF], 2),
+        ([0.0] * 4, [INF, 1e38, INF, 2e38], 2),
+        ([0.0] * 4, [-3e38, -3e38, -2e38, -2e38], 2),
+        ([-INF, -INF, 0.0, 0.0], [0.0, 0.0, -3e38, -3e38], 2),
+        ([-INF, -INF, 0.0, 0.0, 0.0, 0.0], [0.0, 0.0, -half, -half, -half, -2e38], 3),
+        ([0.0, -INF, 0.0, 0.0], [-2e38, 0.0, -half, -half], 2),
+        ([0.0, -INF, 0.0, 0.0], [half, 0.0, 1e38, 1e38], 2),
+        ([0.0, -INF, 0.0, 0.0], [2e38, 0.0, half, -half], 2),
+        ([0.0] * 6, [3e38, 3e38, INF, INF, 3.1e38, 3.1e38], 3),
+    ]
+    for logits, bias, groups in cases:
+        for kept in range(1, groups):
+            for k in (1, 2):
+                rule = moe.score_rule(len(logits), k, score, groups, kept, 2)
+                _check(rule, torch.tensor([logits]), torch.tensor(bias))
