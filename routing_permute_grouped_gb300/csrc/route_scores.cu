@@ -500,10 +500,12 @@ __device__ __noinline__ uint32_t exact_groups(const ScoreArgs& a, uint32_t* buf,
 }
 
 // How many of the experts that `need` be compared come before the lane's, by sigmoids of
-// fp64; ties to the lower lane.
+// fp64; ties to the lower lane.  Experts without a score (logit -infinity) are among them
+// where the k-th key is next to the lowest number, and come last as they do in fp32.
 __device__ __noinline__ int exact_rank(float logit, float bias, bool need) {
     const int lane = threadIdx.x & 31;
-    const double v = 1.0 / (1.0 + exp(-static_cast<double>(logit))) + static_cast<double>(bias);
+    double v = 1.0 / (1.0 + exp(-static_cast<double>(logit))) + static_cast<double>(bias);
+    if (!(logit > -INFINITY)) v = -INFINITY;
     const uint64_t u = need ? key_of(v) : 0;
     int rank = 0;
 #pragma unroll 1

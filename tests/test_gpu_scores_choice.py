@@ -123,3 +123,24 @@ def test_sums_of_a_group_that_pass_fp32(score):
             for k in (1, 2):
                 rule = moe.score_rule(len(logits), k, score, groups, kept, 2)
                 _check(rule, torch.tensor([logits]), torch.tensor(bias))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,kept,top", [(0, 0, 1), (4, 3, 1), (4, 3, 2)])
+def test_biases_of_the_lowest_value_and_masked_logits(score, groups, kept, top):
+    """An expert whose bias is the type's lowest number still comes before one without a score."""
+    E, k = 16, 8
+    lowest = torch.finfo(torch.float32).min
+    gen = torch.Generator().manual_seed(3)
+    rows, biases = [], []
+    for _ in range(60):
+        order = torch.randperm(E, generator=gen)
+        live, low = (int(torch.randint(0, 7, (1,), generator=gen)) for _ in range(2))
+        logits, bias = torch.full((E,), -INF), torch.zeros(E)
+        logits[order[:live + low]] = torch.randn(live + low, generator=gen)
+        bias[order[live:live + low]] = lowest
+        bias[order[live + low:]] = torch.randint(-2, 8, (E - live - low,), generator=gen).float()
+        rows.append(logits)
+        biases.append(bias)
+    for logits, bias in zip(rows, biases):
+        _check(moe.score_rule(E, k, score, groups, kept, top), logits[None], bias)
