@@ -243,8 +243,10 @@ __global__ void __launch_bounds__(256, 5) k_quantize_int4(const __grid_constant_
     }
 }
 
-// (code - zero) scale = (128 + code) scale - (128 + zero) scale: both products and
-// their difference are exact in fp32.
+// (code - zero) scale = ((128 + code) - (128 + zero)) scale: the difference is exact, and
+// so is its product with a 16-bit scale in fp32.  (Two products and their difference, one
+// operation less, pass fp32's range from bf16 scales of 2^121 on, which are a group's with
+// elements from 1.7e37.)
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256) k_dequantize_int4(const __grid_constant__ Int4Args a, T* out, int64_t ldo) {
     pdl_trigger();
@@ -257,7 +259,7 @@ __global__ void __launch_bounds__(256) k_dequantize_int4(const __grid_constant__
         const int64_t at = r * a.groups + (p >> a.shift);
         const float s = low_half<T>(ld_dep(static_cast<const uint16_t*>(a.scales) + at));
         const uint32_t z = a.zeros ? ld_dep(a.zeros + at) : 8u;
-        const float back = -__uint_as_float(0x43000000u | z << 16) * s;
+        const float back = -128.0f - static_cast<float>(z);
         const uint32_t word[4] = {q.x, q.y, q.z, q.w};
         uint32_t v[16];
 #pragma unroll
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__(256) k_dequantize_int4(const __grid_constant__
             for (int j = 0; j < 4; ++j) {
                 uint32_t u;  // 128 + code as the upper halves of two fp32 numbers
                 asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(u) : "r"(word[w] >> (4 * j)), "r"(0x000F000Fu), "r"(0x43004300u));
-                v[4 * w + j] = pack2(T(), fmaf(__uint_as_float(u << 16), s, back), fmaf(__uint_as_float(u & 0xFFFF0000u), s, back));
+                v[4 * w + j] = pack2(T(), (__uint_as_float(u << 16) + back) * s, (__uint_as_float(u & 0xFFFF0000u) + back) * s);
             }
         store64<WIDE>(out + r * ldo + p * kPiece, v);
     }
