@@ -130,7 +130,8 @@ struct Warp {
     }
     // Scales and zero points of step c come by way of shared memory as well, where they
     // can be copied four bytes at a time (`whole`); else they are read as they are
-    // needed.  Past the last group the last ones', for sums of 0.
+    // needed, with a scale of 0 past the last group, where the sums are 0 (an infinite
+    // scale of the last one would make them NaN).
     __device__ __forceinline__ void load_params(uint32_t stage, int c) const {
         const int at = min(c * groups, p.groups - groups);
         const uint32_t dst = par + stage;
@@ -162,9 +163,9 @@ struct Warp {
         } else {
 #pragma unroll
             for (int j = 0; j < groups; ++j) {
-                const int at = min(c * groups + j, p.groups - 1);
-                s[j] = scales[at];
-                z[j] = p.zeros ? zeros[at] : 8u;
+                const int at = c * groups + j;
+                s[j] = at < p.groups ? scales[at] : 0u;
+                z[j] = p.zeros && at < p.groups ? zeros[at] : 8u;
             }
         }
 #pragma unroll

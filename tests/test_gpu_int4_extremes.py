@@ -50,3 +50,24 @@ def test_values_of_every_code_and_zero_point(dtype):
                 moe.moe_dequantize_int4(32, codes[:n].contiguous(), scales[:n].contiguous(), out, zeros=zz)
                 want = _values(codes[:n], scales[:n], zz, 32).to(dtype)
                 assert torch.equal(out, want), (s, sign)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("with_zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_an_infinite_scale_gives_infinities(dtype, with_zeros, group):
+    """A sum other than 0 times an infinite scale, in any group of a row and wherever the row
+    ends: an infinity of the sum's sign."""
+    for R, N in ((1, 16), (3, 40), (64, 1032)):
+        for K in (32, 96, 128, 160, 256, 384) if R < 64 else (16384, 16544):
+            n = -(-K // group)
+            codes = torch.full((1, N, K // 2), 0xBB, dtype=torch.uint8, device="cuda")  # 11
+            codes[:, ::2] = 0x33                                                        # 3
+            z = torch.full((1, N, n), 8, dtype=torch.uint8, device="cuda") if with_zeros else None
+            x = torch.ones((R, K), dtype=dtype, device="cuda")
+            for at in {0, n - 1}:
+                scales = torch.full((1, N, n), 2.0 ** -9, dtype=dtype, device="cuda")
+                scales[:, :, at] = INF
+                y = torch.full((R, N), NAN, dtype=dtype, device="cuda")
+                moe.moe_grouped_gemm_int4(group, x, codes, scales, None, y, w_zeros=z)
+                assert (y[:, ::2] == -INF).all() and (y[:, 1::2] == INF).all(), (R, K, at)
