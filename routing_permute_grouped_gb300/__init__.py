@@ -887,7 +887,7 @@ class _RouteScores(torch.autograd.Function):
             both = torch.empty((2,), dtype=torch.float32, device=dev)
             ws = torch.empty((moe_route_scores_workspace_size(rule, T),), dtype=torch.uint8, device=dev)
         moe_route_scores(rule, logits, idx, w, bias, counts, both, ws)
-        ctx.rule = rule
+        ctx.rule = ScoreRule.from_buffer_copy(rule)  # the caller may change its own before the gradient
         ctx.save_for_backward(logits, idx, counts)
         ctx.mark_non_differentiable(idx, *([counts] if losses else []))
         return (w, idx, both, counts) if losses else (w, idx)
