@@ -163,9 +163,9 @@ struct Warp {
         } else {
 #pragma unroll
             for (int j = 0; j < groups; ++j) {
-                const int at = c * groups + j;
-                s[j] = at < p.groups ? scales[at] : 0u;
-                z[j] = p.zeros && at < p.groups ? zeros[at] : 8u;
+                const int at = min(c * groups + j, p.groups - 1);
+                s[j] = at < c * groups + j ? 0u : scales[at];
+                z[j] = p.zeros ? zeros[at] : 8u;
             }
         }
 #pragma unroll
