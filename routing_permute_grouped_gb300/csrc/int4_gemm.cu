@@ -175,20 +175,17 @@ struct Warp {
         }
     }
 
-    // sum[m][n]: 16 weight rows m by 8 token rows n; x: the step's first element of this
-    // lane's token rows in shared memory, 256 bytes for a chunk, pieces placed by row_place
-    template <int NT>
-    __device__ __forceinline__ void take(uint32_t stage, const uint32_t (&x)[NT], int odd, const float (&scales_)[groups],
-                                         const uint32_t (&zeros_)[groups], float (&sum)[2][NT][4]) const {
-        uint4 ahead[NT];
+    // sum[m]: 16 weight rows m by 8 token rows; x: the step's first element of this lane's
+    // token row in shared memory, 256 bytes for a chunk, pieces placed by row_place
+    __device__ __forceinline__ void take(uint32_t stage, uint32_t x, int odd, const float (&scales_)[groups],
+                                         const uint32_t (&zeros_)[groups], float (&sum)[2][4]) const {
+        uint4 ahead;
         auto fetch = [&](int w) {  // the lane's word w of the step
             const int at = w / 4 * 256 + (row_place<words>(0, (w % 4 / words * 4 + t4) * words + w % words) << 4 ^ odd);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(ahead[n].x), "=r"(ahead[n].y), "=r"(ahead[n].z), "=r"(ahead[n].w)
-                             : "r"(x[n] + at)
-                             : "memory");
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(ahead.x), "=r"(ahead.y), "=r"(ahead.z), "=r"(ahead.w)
+                         : "r"(x + at)
+                         : "memory");
         };
         fetch(0);
 #pragma unroll
@@ -203,12 +200,10 @@ struct Warp {
             }
             uint32_t q[4][words];
             codes_of(stage + 2048 * half, j, q);
-            float part[2][NT][4];
+            float part[2][4];
 #pragma unroll
             for (int u = 0; u < words; ++u) {
-                uint4 b[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) b[n] = ahead[n];
+                const uint4 b = ahead;
                 if (hj * words + u + 1 < groups * words) fetch(hj * words + u + 1);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -219,21 +214,16 @@ struct Warp {
                         a[1] = int4_widen<T>(q[2 * m + 1][u], 2 * h, zero[2 * m + 1]);
                         a[2] = int4_widen<T>(q[2 * m][u], 2 * h + 1, zero[2 * m]);
                         a[3] = int4_widen<T>(q[2 * m + 1][u], 2 * h + 1, zero[2 * m + 1]);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            if (u == 0 && h == 0)
-                                mma<T, true>(part[m][n], a, b[n].x, b[n].y);
-                            else
-                                mma<T, false>(part[m][n], a, h ? b[n].z : b[n].x, h ? b[n].w : b[n].y);
-                        }
+                        if (u == 0 && h == 0)
+                            mma<T, true>(part[m], a, b.x, b.y);
+                        else
+                            mma<T, false>(part[m], a, h ? b.z : b.x, h ? b.w : b.y);
                     }
             }
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sum[m][n][i] = fmaf(part[m][n][i], scale[2 * m + (i >> 1)], sum[m][n][i]);
+                for (int i = 0; i < 4; ++i) sum[m][i] = fmaf(part[m][i], scale[2 * m + (i >> 1)], sum[m][i]);
         }
     }
 };
@@ -249,7 +239,6 @@ template <typename T, int G>
 __device__ __forceinline__ void run_item(const Int4Product& p, const Int4Item& it, Shared& sh, uint8_t* ring, uint8_t* s_rows,
                                          int& blocks_so_far, int& turn_of, bool& timed_out) {
     using W = Warp<T, G>;
-    constexpr int NT = 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int split = p.split, part = warp & (split - 1), block = it.panel * (kWarps / split) + warp / split;
     // the warp's weight rows: 16 from a on and 16 from b on
@@ -317,17 +306,14 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Int4Item& i
     load_rows(0);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) load(i * W::stage_bytes);
-    float sum[2][NT][4] = {};
+    float sum[2][4] = {};
     uint32_t stage = 0;
     const int mine_of = g & (held - 1), odd = row_place<W::words>(mine_of, 0) << 4;
     for (int b = 0; b < n_blocks; ++b) {
         if (b + 1 < n_blocks) load_rows(b + 1);
         const int use = blocks_so_far + b, buf = use & 1;
         timed_out = timed_out || !warp_wait(sh.full + buf, use >> 1 & 1, &sh.abort);
-        uint32_t x[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            x[n] = smem_u32(s_rows) + buf * kRowBytes + (n * 8 + mine_of) * columns * 2 + part * (W::step * 2);
+        uint32_t x = smem_u32(s_rows) + buf * kRowBytes + mine_of * columns * 2 + part * (W::step * 2);
         const int end = min((b + 1) * each * split, steps);
         for (int c = b * each * split + part; c < end; c += split) {
             cp_async_wait<kStages - 2>();
@@ -336,9 +322,8 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Int4Item& i
             float s[W::groups];
             uint32_t z[W::groups];
             w.params(stage, c, s, z);
-            w.template take<NT>(stage, x, odd, s, z, sum);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) x[n] += super * 2;
+            w.take(stage, x, odd, s, z, sum);
+            x += super * 2;
             stage = stage == (kStages - 1) * W::stage_bytes ? 0 : stage + W::stage_bytes;
         }
         __syncwarp();
@@ -347,7 +332,7 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Int4Item& i
     blocks_so_far += n_blocks;
     // the codes were widened in units of their own
 #pragma unroll
-    for (int v = 0; v < 8 * NT; ++v) (&sum[0][0][0])[v] *= 1.0f / Int4Wide<T>::unit;
+    for (int v = 0; v < 8; ++v) (&sum[0][0])[v] *= 1.0f / Int4Wide<T>::unit;
     __syncwarp();  // the next item's copies come after these reads
     if (split > 1) {  // the parts to the first of the warps, in order, through the ring's memory
         float* join = reinterpret_cast<float*>(ring);
@@ -355,46 +340,44 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Int4Item& i
         __syncthreads();
         if (part > 0) {
 #pragma unroll
-            for (int v = 0; v < 8 * NT; ++v) join[(warp * 8 * NT + v) * 32 + lane] = (&sum[0][0][0])[v];
+            for (int v = 0; v < 8; ++v) join[(warp * 8 + v) * 32 + lane] = (&sum[0][0])[v];
         }
         __syncthreads();
         if (part == 0)
             for (int o = 1; o < split; ++o)
 #pragma unroll
-                for (int v = 0; v < 8 * NT; ++v) (&sum[0][0][0])[v] += join[((warp + o) * 8 * NT + v) * 32 + lane];
+                for (int v = 0; v < 8; ++v) (&sum[0][0])[v] += join[((warp + o) * 8 + v) * 32 + lane];
         __syncthreads();
         if (part > 0) return;
     }
     if (!live) return;
-    // lane: token rows 2 t4 and 2 t4 + 1 of each eight, weight rows g and g + 8 of each 16
+    // lane: token rows 2 t4 and 2 t4 + 1, weight rows g and g + 8 of each 16
     T* out = static_cast<T*>(p.r.out);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int j = 0; j < 2; ++j) {
+        const int token = 2 * t4 + j, to = it.row + token;
+        if (token >= it.rows) continue;
+        const float f = p.r.row_scale ? ld_dep(p.r.row_scale + to) : 1.0f;
+        const bool none = p.src && int4_token_row(p, to) < 0;
+        T* y = out + to * p.r.ldo;
+        if (p.swiglu) {
+            const int col = block * 16 + g;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int token = n * 8 + 2 * t4 + j, to = it.row + token;
-            if (token >= it.rows) continue;
-            const float f = p.r.row_scale ? ld_dep(p.r.row_scale + to) : 1.0f;
-            const bool none = p.src && int4_token_row(p, to) < 0;
-            T* y = out + to * p.r.ldo;
-            if (p.swiglu) {
-                const int col = block * 16 + g;
+            for (int h = 0; h < 2; ++h) {
+                const float gate = sum[0][2 * h + j];
+                const float v = gate / (1.0f + expf(-gate)) * sum[1][2 * h + j] * f;
+                y[col + 8 * h] = from_float<T>(none ? 0.0f : v);
+            }
+        } else {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float gate = sum[0][n][2 * h + j];
-                    const float v = gate / (1.0f + expf(-gate)) * sum[1][n][2 * h + j] * f;
-                    y[col + 8 * h] = from_float<T>(none ? 0.0f : v);
+                    const int col = a0 + 16 * m + 8 * h + g;
+                    if (col < p.columns) y[col] = from_float<T>(none ? 0.0f : sum[m][2 * h + j] * f);
                 }
-            } else {
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int col = a0 + 16 * m + 8 * h + g;
-                        if (col < p.columns) y[col] = from_float<T>(none ? 0.0f : sum[m][n][2 * h + j] * f);
-                    }
-            }
         }
+    }
 }
 
 template <typename T, int G>
