@@ -240,6 +240,10 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Int4Item& i
                                          int& blocks_so_far, int& turn_of, bool& timed_out) {
     using W = Warp<T, G>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    // Set once a wait of the CTA has run out: the other warps' waits end as well, and no sum is
+    // stored any more.  (Leaving the blocks and items there and then: decode 330 -> 336 us, for
+    // registers.)
+    volatile uint32_t* abort_flag = &sh.abort;
     const int split = p.split, part = warp & (split - 1), block = it.panel * (kWarps / split) + warp / split;
     // the warp's weight rows: 16 from a on and 16 from b on
     const int a0 = p.swiglu ? (block >> 3) * 256 + (block & 7) * 16 : block * 32, b0 = a0 + (p.swiglu ? 128 : 16);
@@ -263,6 +267,7 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Int4Item& i
     auto load_rows = [&](int b) {
         const int use = blocks_so_far + b, buf = use & 1;
         timed_out = timed_out || !warp_wait(sh.empty + buf, (use >> 1 & 1) ^ 1, &sh.abort);
+        if (timed_out) *abort_flag = 1;  // before what comes may lie over rows that others read
         const uint32_t dst = smem_u32(s_rows) + buf * kRowBytes;
         const int piece = threadIdx.x & 15, slot = threadIdx.x >> 4, chunks = columns / kChunk;
         auto copy = [&](int r, int c) {  // chunk c of row r
@@ -313,6 +318,7 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Int4Item& i
         if (b + 1 < n_blocks) load_rows(b + 1);
         const int use = blocks_so_far + b, buf = use & 1;
         timed_out = timed_out || !warp_wait(sh.full + buf, use >> 1 & 1, &sh.abort);
+        if (timed_out) *abort_flag = 1;
         uint32_t x = smem_u32(s_rows) + buf * kRowBytes + mine_of * columns * 2 + part * (W::step * 2);
         const int end = min((b + 1) * each * split, steps);
         for (int c = b * each * split + part; c < end; c += split) {
@@ -350,7 +356,7 @@ __device__ __forceinline__ void run_item(const Int4Product& p, const Int4Item& i
         __syncthreads();
         if (part > 0) return;
     }
-    if (!live) return;
+    if (!live || *abort_flag) return;
     // lane: token rows 2 t4 and 2 t4 + 1, weight rows g and g + 8 of each 16
     T* out = static_cast<T*>(p.r.out);
 #pragma unroll
