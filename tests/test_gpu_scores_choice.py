@@ -144,3 +144,18 @@ def test_biases_of_the_lowest_value_and_masked_logits(score, groups, kept, top):
         biases.append(bias)
     for logits, bias in zip(rows, biases):
         _check(moe.score_rule(E, k, score, groups, kept, top), logits[None], bias)
+
+
+# ----------------------------------------------------------------- weights --
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [8, 64, 256])
+def test_equal_scores_have_equal_weights_to_the_bit(score, E):
+    """2, 4 or 8 chosen experts of one score: their sum is that many times it exactly, and so
+    is the quotient, at any logit."""
+    T = 4000
+    gen = torch.Generator().manual_seed(E)
+    for spread in (1.0, 20.0):
+        logits = (torch.randn((T, 1), generator=gen) * spread).expand(T, E).contiguous().cuda()
+        for k in (2, 4, 8):
+            _, w = _route(moe.score_rule(E, k, score), logits)
+            assert (w == 1.0 / k).all()
