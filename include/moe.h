@@ -1041,7 +1041,10 @@ moe_status_t moe_dequantize_int4(int32_t group, int32_t dtype, int64_t rows, int
  *   y[r] = row_scale[r] * silu(gate) * up.
  * Differences of code and zero are multiplied exactly and summed in fp32, each
  * group's sum is scaled in fp32, and the result is rounded once.  Made for few
- * rows per group (decoding), where the weights' bytes set the pace.
+ * rows per group (decoding), where the weights' bytes set the pace.  The kernel
+ * is chosen by R / E: a few long groups among many empty ones are slower than
+ * the same groups by themselves.  Rows of a call that reports
+ * MOE_DEVERR_TIMEOUT are not all written.
  *   x          dtype [x_rows, K], row stride ldx (a multiple of 8)  device, read
  *   src        int32 [R] or NULL                device, read
  *   w_codes, w_scales, w_zeros (or NULL)  rows [E * N or E * 2 N, K]  device, read

@@ -22,7 +22,8 @@
 // A thread takes 32 elements, so that what is done once for a group of 128 (the
 // exchange of its ends, the scale, the zero point) is done by four threads: with 8
 // elements per thread that was most of the work (262144 x 1024, groups of 128 with zero
-// points: 267 us quantising and 132 back where this takes 148 and 103).  64 bytes of a row
+// points: 267 us quantising and 132 back where this takes 147 and 103, by events around
+// single calls; the kernels by themselves 144 and 97).  64 bytes of a row
 // go as two accesses of 32 where they are aligned to it, else as four of 16 (169 and 134,
 // before the quantiser's registers were held to 48 for five blocks per SM, 160 to 148).
 // Back is bound by HBM (6.6 TB/s); quantising, at 4.6 TB/s, by its instructions, 15 for an

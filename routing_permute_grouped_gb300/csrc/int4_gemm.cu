@@ -417,8 +417,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_int4_product(const __grid_co
 // Warps that split a sum, as far as the token rows of their steps fit a block: the
 // number that makes the fewest steps of the CTAs that run one after another, an item's
 // start and end counted as kItemSteps.
-// One token on 8 experts of 4096 x 7168, by split 1, 2 and 4: 47, 43 and 45 us; one row of
-// 1024 x 4096, by 1 and 8: 35 and 12.
+// One token on 8 experts of 4096 x 7168, by split 1, 2 and 4: 47, 43 and 45 us (events
+// around single calls; 40 back to back); one row of 1024 x 4096, by 1 and 8: 35 and 12.
 constexpr int kItemSteps = 4;
 int split_of(int64_t blocks, int64_t tiles, int64_t rows, int steps, int step) {
     const int held = rows > 4 ? 8 : rows > 2 ? 4 : static_cast<int>(rows);  // of the longest tile
@@ -464,7 +464,9 @@ cudaError_t product(int group, const Int4Product& p, cudaStream_t st) {
     // Narrow and wide, in us: 8 rows in each of 32 groups of 7168 x 2048 59 and 92, 12 rows
     // 104 and 94, 32 rows 203 and 104; 16 rows in 4 groups of 1024 x 7168 (2^29 products)
     // 20 and 27, 16 rows in 8 groups of 7168 x 2048 (2^31) 39 and 35, 64 rows of 1024 x 16384
-    // (2^30) 39 and 31.
+    // (2^30) 39 and 31.  E counts groups without rows, which the host cannot tell: 2000 rows in
+    // 8 groups of 2048 x 4096 take 80 us, the same rows where those are 8 of 256 groups 229, in
+    // narrow tiles, and 2100 rows there 104, in wide ones.
     if (p.r.R > 8ll * p.r.E && static_cast<double>(p.r.R) * p.r.N * p.r.K >= 0x1p30) return launch_int4_wide<T>(group, p, st);
     if (group == 32) return launch<T, 32>(p, st);
     return group == 64 ? launch<T, 64>(p, st) : launch<T, 128>(p, st);

@@ -25,9 +25,11 @@
 // 37 thousand, 15 to 28 us at the end of a batch.
 //
 // What bounds it: instructions, where there are many tokens.  32768 x 256 fp32 logits, 8
-// chosen of 4 of 8 groups by sigmoids with a bias: 49 us (5 us of bytes), with the losses
-// 63, without bias and groups 35.  The gradient: 33 us with losses, 21 without (10 us of
-// bytes).
+// chosen of 4 of 8 groups by sigmoids with a bias: 50 us (5 us of bytes), with the losses
+// 63, without bias and groups 35, tokens of one value 62 (with groups 640: the groups are
+// too close in fp32 and all take fp64).  The gradient: 33 us with losses, 21 without (10 us
+// of bytes).  These are events around a single call, whose launch and end count; calls back
+// to back overlap, 60 us with the losses and 30 for their gradient.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -46,7 +48,7 @@ namespace {
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kMaxChoices = 8;
 constexpr int kWarps = 8;          // per block
-constexpr int kPerSm = 3;          // blocks; a warp's set-up is shared by a dozen tokens (4 spill: 72 us where 3 take 64)
+constexpr int kPerSm = 3;          // blocks; a warp's set-up is shared by a dozen tokens (4 spill: 72 us where 3 take 63)
 constexpr int kPerSmBwd = 4;       // of the gradient, which waits more than it computes (3: 25 us where 4 take 21)
 constexpr int kLossBlocks = 512;   // at most, where loads and losses are summed
 constexpr int kLossColumns = 8;    // experts per block of the second kernel
